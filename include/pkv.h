@@ -51,7 +51,7 @@ extern "C" {
 /* Host-side status codes. */
 #define PKV_OK 0
 #define PKV_ERR_NULL_POINTER (-1)      /* a required pointer is NULL */
-#define PKV_ERR_UNSUPPORTED (-2)       /* head_dim/block_size/head counts outside the supported shape */
+#define PKV_ERR_UNSUPPORTED (-2)       /* head_dim/block_size/head counts outside the call's supported shape */
 #define PKV_ERR_BAD_STRIDE (-3)        /* a row stride smaller than the row */
 #define PKV_ERR_ALIGNMENT (-4)         /* pointer or stride not 16-byte aligned where a kernel needs it */
 #define PKV_ERR_WORKSPACE (-5)         /* workspace NULL or smaller than the *_workspace_bytes query */
@@ -304,6 +304,121 @@ int pkv_decode_noalloc(const void* q, int64_t q_row_stride, const void* k_cache,
                        const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                        int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale,
                        void* out, cudaStream_t stream);
+
+/*
+ * ---- The 4-bit paged cache ----
+ *
+ * The pages keep K and V in the cache as 16-bit rows. These entry points have
+ * no counterpart there: they hold the same paged cache in 4 bits per element
+ * plus a scale and a minimum per 32 elements (5 bits in all), 3.2 times the
+ * tokens in the same memory, with the same slots, block tables and lengths.
+ *
+ * Format. A row (one token, one kv head, 128 dims, of K or of V) is 4 groups
+ * of 32 dims. A group keeps, in fp16, s = (max - min) / 15 and z = min; a dim
+ * keeps the code c = (x - z) / s rounded half to even and clamped to 0..15 (0
+ * where s is 0), and stands for s * c + z. |x| > 65504 counts as 65504. A
+ * group that holds a NaN or an infinity has s = z = NaN: it reads back as NaN
+ * and takes part in attention as NaN.
+ *
+ * Layout. k_cache and v_cache are uint8 [num_blocks, num_kv_heads, 16, 1280],
+ * contiguous and 16-byte aligned: a 256-token block of a head is 16 tiles of
+ * 16 tokens, a tile is 16 x 64 bytes of codes, then 16 x 4 x (s, z) fp16.
+ *   K code row: the 32-bit word at byte 16 t + 4 j holds dims 32 j + 8 t + p in
+ *     bits 4p..4p+3 (p = 0..7; j, t = 0..3).
+ *   V code row: the 8-byte chunk r (0..7) lies at chunk place
+ *     r ^ (token & 4); its 16-bit field j holds dims 32 j + 4 r + p in bits
+ *     4p..4p+3 (p = 0..3).
+ * Slot s is token s % 256 of block s / 256, as in the 16-bit cache. A cache
+ * needs no initialisation: only stored tokens are read (bytes of others may be
+ * fetched, but never reach a result).
+ *
+ * Supported: head_dim 128, block_size 256, any num_kv_heads up to 8192; for
+ * attention 1, 2 or 4 query heads to a kv head (prefill: 16 and 8). The rows
+ * (q, k, v, out) are bf16, or fp16 for the *_f16 names; the cache is the same
+ * for both. Sizes of 0 are no-ops.
+ */
+
+/*
+ * pkv_store_kvcache_q4 -- pkv_store_kvcache into the 4-bit cache: rows
+ * k[i], v[i] are quantised into slot slot_mapping[i] (-1: skipped).
+ *   k, v  [num_tokens, num_kv_heads, 128], heads and dims contiguous, rows
+ *         k_row_stride / v_row_stride elements apart; any 2-byte alignment
+ *         (16-byte vectors where pointers and strides allow it).
+ * A row's bytes belong to that row alone, so tokens of one call may share a
+ * block or a tile. Duplicate slots in one call race. Slots outside the pool set
+ * PKV_DEVERR_BAD_SLOT and are skipped.
+ */
+int pkv_store_kvcache_q4(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride, void* k_cache,
+                         void* v_cache, const int32_t* slot_mapping, int32_t num_tokens, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int32_t num_blocks, cudaStream_t stream);
+int pkv_store_kvcache_q4_f16(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride, void* k_cache,
+                             void* v_cache, const int32_t* slot_mapping, int32_t num_tokens, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t block_size, int32_t num_blocks, cudaStream_t stream);
+
+/*
+ * pkv_load_kvcache_q4 -- reads slots back: k[i], v[i] = the values that slot
+ * slot_mapping[i] stands for, rounded to the element type (fp16: saturated at
+ * 65504). Rows whose slot is -1, or outside the pool (PKV_DEVERR_BAD_SLOT),
+ * are left as they were. Slots may repeat (a shared prefix).
+ *   k, v  [num_tokens, num_kv_heads, 128] contiguous, 16-byte aligned.
+ */
+int pkv_load_kvcache_q4(const void* k_cache, const void* v_cache, const int32_t* slot_mapping, int32_t num_tokens,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, void* k,
+                        void* v, cudaStream_t stream);
+int pkv_load_kvcache_q4_f16(const void* k_cache, const void* v_cache, const int32_t* slot_mapping, int32_t num_tokens,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, void* k,
+                            void* v, cudaStream_t stream);
+
+/*
+ * pkv_decode_q4 -- pkv_decode over the 4-bit cache: attention of one query row
+ * per sequence over the values that its cached tokens stand for (the codes are
+ * used exactly; p times a row's scale is rounded to fp16 for the product with
+ * V's codes, sums and maxima are fp32). Arguments and errors as for pkv_decode
+ * but for the caches, the head counts and the workspace:
+ *   workspace  >= pkv_decode_q4_workspace_bytes(num_seqs, num_heads,
+ *         num_kv_heads, max_context_len) bytes, ZERO-FILLED ONCE before its
+ *         first use and used for these calls only, always with the same
+ *         workspace_bytes; every call leaves it ready for the next one, of any
+ *         sizes and head counts that it is large enough for. Calls that share
+ *         it (two captured graphs, say) must not overlap in time.
+ * How a sequence is split over the GPU follows from the call's context lengths
+ * alone, and the partial results are joined in chunk order, so equal calls give
+ * equal bits.
+ */
+int pkv_decode_q4(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                  const int32_t* block_tables, int32_t block_table_stride, const int32_t* context_lens,
+                  int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                  int32_t max_context_len, float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+int pkv_decode_q4_f16(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
+                      int32_t num_blocks, const int32_t* block_tables, int32_t block_table_stride,
+                      const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale, void* out,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * pkv_store_decode_q4 -- pkv_store_kvcache_q4 of the step's new rows, then
+ * pkv_decode_q4, in one launch, with the same results. As for
+ * pkv_store_decode, slot_mapping[b] is -1 (nothing stored) or the slot of
+ * position context_lens[b] - 1; any other slot is not stored and sets
+ * PKV_DEVERR_BAD_SLOT. k, v 16-byte aligned, row strides multiples of 8.
+ */
+int pkv_store_decode_q4(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                        int64_t v_row_stride, const int32_t* slot_mapping, void* k_cache, void* v_cache,
+                        int32_t num_blocks, const int32_t* block_tables, int32_t block_table_stride,
+                        const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale, void* out,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+int pkv_store_decode_q4_f16(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                            int64_t v_row_stride, const int32_t* slot_mapping, void* k_cache, void* v_cache,
+                            int32_t num_blocks, const int32_t* block_tables, int32_t block_table_stride,
+                            const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale,
+                            void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes pkv_decode_q4, pkv_store_decode_q4 and their _f16 forms need (0 for sizes they refuse). */
+size_t pkv_decode_q4_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t max_context_len);
 
 /*
  * pkv_build_prefill_metadata / pkv_build_decode_metadata -- the per-step index

@@ -11,6 +11,7 @@ Layouts (Qwen3-0.6B attention shape):
   q            [tokens, 16, 128] (row stride may exceed 2048, e.g. fused qkv)
   k, v         [tokens, 8, 128]
   k/v caches   [num_blocks, 256, 8, 128] contiguous
+  4-bit caches [num_blocks, num_kv_heads, 16, 1280] uint8 (the *_q4 names; see q4_cache)
   slot_mapping, cu_seqlens_*, block_tables, context_lens  int32 on the GPU
 Element type: bf16 for the plain names, fp16 for the ``*_f16`` names (one type
 per call for q, k, v, caches and output); the store copies either.
@@ -36,6 +37,7 @@ PKV_DEVERR_TIMEOUT = 0x8
 PKV_ERR_SCRATCH_LIMIT = -9
 PKV_DECODE_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 HEAD_DIM, BLOCK_SIZE, NUM_HEADS, NUM_KV_HEADS = 128, 256, 16, 8
+Q4_TILES, Q4_TILE_BYTES = 16, 1280  # 4-bit cache: tiles of 16 tokens per block, bytes per tile and kv head
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libpkv.so is not built ({LIB_PATH}); run python paged_kv_cache_kvh_gb300/build_lib.py")
@@ -71,7 +73,15 @@ _SIGNATURES = {
                                                   _vp]),
     "pkv_build_decode_metadata": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
     "pkv_selftest_wait_timeout": (ctypes.c_int, [_u64, _vp]),
+    "pkv_decode_q4_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
 }
+for _suffix in ("", "_f16"):
+    _SIGNATURES["pkv_store_kvcache_q4" + _suffix] = (
+        ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp])
+    _SIGNATURES["pkv_load_kvcache_q4" + _suffix] = (
+        ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp])
+    for _op in ("pkv_decode", "pkv_store_decode"):  # the 16-bit calls' arguments
+        _SIGNATURES[_op + "_q4" + _suffix] = _SIGNATURES[_op]
 for _name, (_res, _args) in _SIGNATURES.items():
     _f = getattr(_lib, _name)
     _f.restype = _res
@@ -354,6 +364,168 @@ def pkv_store_decode_f16(q, k, v, slot_mapping, k_cache, v_cache, block_tables, 
     """pkv_store_decode on fp16 tensors; returns fp16."""
     return _store_decode("pkv_store_decode_f16", torch.float16, q, k, v, slot_mapping, k_cache, v_cache,
                          block_tables, context_lens, max_context_len, softmax_scale, workspace, out, stream)
+
+
+# ---- the 4-bit paged cache ----------------------------------------------------------
+
+
+def q4_cache(num_blocks: int, num_kv_heads: int = NUM_KV_HEADS, device="cuda") -> torch.Tensor:
+    """A 4-bit K or V cache, uint8 [num_blocks, num_kv_heads, 16, 1280]: per 256-token
+    block and kv head, 16 tiles of 16 tokens (16 x 64 bytes of codes, then 16 x 4 x
+    (scale, minimum) in fp16); 80 bytes per (token, kv head) instead of 256. The byte
+    order within a tile is written down in include/pkv.h. Needs no initialisation."""
+    return torch.empty((num_blocks, num_kv_heads, Q4_TILES, Q4_TILE_BYTES), dtype=torch.uint8, device=device)
+
+
+def _here(*tensors):
+    """All on the current CUDA device: the library launches there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        _need(t is None or t.get_device() == dev, "tensors must be on the current CUDA device")
+
+
+def _q4_caches(k_cache, v_cache, hkv):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t.dtype == torch.uint8 and t.is_cuda and t.is_contiguous() and t.dim() == 4
+              and tuple(t.shape[1:]) == (hkv, Q4_TILES, Q4_TILE_BYTES),
+              f"{name}: contiguous uint8 CUDA [blocks, {hkv}, 16, 1280] (q4_cache)")
+    _need(k_cache.shape[0] == v_cache.shape[0], "k_cache and v_cache must have the same number of blocks")
+
+
+def _store_q4(entry, dtype, k, v, k_cache, v_cache, slot_mapping, stream):
+    _need(k.dim() == 3 and v.shape == k.shape, "k, v must be [N, num_kv_heads, 128]")
+    N, hkv = k.shape[0], k.shape[1]
+    _rows(k, "k", hkv, dtype)
+    _rows(v, "v", hkv, dtype)
+    _q4_caches(k_cache, v_cache, hkv)
+    _dev_i32(slot_mapping, "slot_mapping")
+    _need(slot_mapping.numel() == N, "slot_mapping must have one entry per token")
+    _here(k, v, k_cache, v_cache, slot_mapping)
+    _check(getattr(_lib, entry)(_ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(slot_mapping), N, hkv, HEAD_DIM, BLOCK_SIZE, k_cache.shape[0], _stream(stream)),
+           entry)
+
+
+def _row_stride(t):
+    """Elements between rows; that of a single row is never used and may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pkv_store_kvcache_q4(k, v, k_cache, v_cache, slot_mapping, stream=None):
+    """store_kvcache into the 4-bit cache: bf16 rows k[i], v[i] quantised into slot
+    slot_mapping[i] (-1: skipped). k, v [N, num_kv_heads, 128], rows may be strided."""
+    _store_q4("pkv_store_kvcache_q4", torch.bfloat16, k, v, k_cache, v_cache, slot_mapping, stream)
+
+
+def pkv_store_kvcache_q4_f16(k, v, k_cache, v_cache, slot_mapping, stream=None):
+    """pkv_store_kvcache_q4 of fp16 rows."""
+    _store_q4("pkv_store_kvcache_q4_f16", torch.float16, k, v, k_cache, v_cache, slot_mapping, stream)
+
+
+def _load_q4(entry, dtype, k_cache, v_cache, slot_mapping, k, v, stream):
+    _need(k_cache.dim() == 4, "k_cache: uint8 [blocks, num_kv_heads, 16, 1280] (q4_cache)")
+    hkv = k_cache.shape[1]
+    _q4_caches(k_cache, v_cache, hkv)
+    _dev_i32(slot_mapping, "slot_mapping")
+    shape = (slot_mapping.numel(), hkv, HEAD_DIM)
+    if k is None:
+        k = torch.zeros(shape, dtype=dtype, device=k_cache.device)
+    if v is None:
+        v = torch.zeros(shape, dtype=dtype, device=k_cache.device)
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t.dtype == dtype and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape,
+              f"{n} must be contiguous {_TYPE_NAME[dtype]} CUDA [N, {hkv}, 128]")
+    _here(k_cache, v_cache, slot_mapping, k, v)
+    _check(getattr(_lib, entry)(_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), shape[0], hkv, HEAD_DIM, BLOCK_SIZE,
+                                k_cache.shape[0], _ptr(k), _ptr(v), _stream(stream)), entry)
+    return k, v
+
+
+def pkv_load_kvcache_q4(k_cache, v_cache, slot_mapping, *, k=None, v=None, stream=None):
+    """Reads slots of the 4-bit cache back into bf16 rows: k[i], v[i] = the values of
+    slot slot_mapping[i]. Rows of slot -1 are left as they were (zeros where the
+    binding allocates k or v). Returns (k, v) [N, num_kv_heads, 128]; contiguous
+    keys for pkv_prefill_varlen, for instance."""
+    return _load_q4("pkv_load_kvcache_q4", torch.bfloat16, k_cache, v_cache, slot_mapping, k, v, stream)
+
+
+def pkv_load_kvcache_q4_f16(k_cache, v_cache, slot_mapping, *, k=None, v=None, stream=None):
+    """pkv_load_kvcache_q4 into fp16 rows (saturated at 65504)."""
+    return _load_q4("pkv_load_kvcache_q4_f16", torch.float16, k_cache, v_cache, slot_mapping, k, v, stream)
+
+
+def pkv_decode_q4_workspace_bytes(num_seqs: int, max_context_len: int, num_heads: int = NUM_HEADS,
+                                  num_kv_heads: int = NUM_KV_HEADS) -> int:
+    return int(_lib.pkv_decode_q4_workspace_bytes(num_seqs, num_heads, num_kv_heads, max_context_len))
+
+
+def decode_q4_workspace(num_seqs: int, max_context_len: int, num_heads: int = NUM_HEADS,
+                        num_kv_heads: int = NUM_KV_HEADS, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for pkv_decode_q4 (allocated by torch, outside the library)."""
+    n = pkv_decode_q4_workspace_bytes(num_seqs, max_context_len, num_heads, num_kv_heads)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _decode_q4(entry, dtype, q, new, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale,
+               workspace, out, stream):
+    _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [B, num_heads, 128], k_cache [blocks, num_kv_heads, 16, 1280]")
+    B, hq, hkv = q.shape[0], q.shape[1], k_cache.shape[1]
+    _rows(q, "q", hq, dtype)
+    _q4_caches(k_cache, v_cache, hkv)
+    _dev_i32(block_tables, "block_tables")
+    _dev_i32(context_lens, "context_lens")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] >= B and context_lens.numel() >= B, "table sizes")
+    if out is None:
+        out = torch.empty((B, hq, HEAD_DIM), dtype=dtype, device=q.device)
+    _need(out.is_cuda and out.is_contiguous() and out.shape == (B, hq, HEAD_DIM) and out.dtype == dtype,
+          f"out must be contiguous {_TYPE_NAME[dtype]} CUDA [B, {hq}, 128]")
+    _need(workspace.dtype == torch.uint8 and workspace.is_cuda and workspace.is_contiguous(),
+          "workspace must be a contiguous uint8 CUDA tensor")
+    _here(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    rows = ()
+    if new is not None:
+        k, v, slot_mapping = new
+        _rows(k, "k", hkv, dtype)
+        _rows(v, "v", hkv, dtype)
+        _dev_i32(slot_mapping, "slot_mapping")
+        _need(k.shape[0] >= B and v.shape[0] >= B and slot_mapping.numel() >= B, "one new row per sequence")
+        _here(k, v, slot_mapping)
+        rows = (_ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(slot_mapping))
+    _check(getattr(_lib, entry)(_ptr(q), _row_stride(q), *rows, _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
+                                _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, hq, hkv, HEAD_DIM,
+                                BLOCK_SIZE, int(max_context_len), float(softmax_scale), _ptr(out), _ptr(workspace),
+                                workspace.numel(), _stream(stream)), entry)
+    return out
+
+
+def pkv_decode_q4(q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace, *,
+                  out=None, stream=None):
+    """pkv_decode over the 4-bit cache. q [B, num_heads, 128] bf16 with 1, 2 or 4 query heads
+    to a kv head of the caches. Returns out [B, num_heads, 128] bf16."""
+    return _decode_q4("pkv_decode_q4", torch.bfloat16, q, None, k_cache, v_cache, block_tables, context_lens,
+                      max_context_len, softmax_scale, workspace, out, stream)
+
+
+def pkv_decode_q4_f16(q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace, *,
+                      out=None, stream=None):
+    """pkv_decode_q4 with fp16 q; returns fp16."""
+    return _decode_q4("pkv_decode_q4_f16", torch.float16, q, None, k_cache, v_cache, block_tables, context_lens,
+                      max_context_len, softmax_scale, workspace, out, stream)
+
+
+def pkv_store_decode_q4(q, k, v, slot_mapping, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                        softmax_scale, workspace, *, out=None, stream=None):
+    """pkv_store_kvcache_q4 of the step's new K/V rows fused into the decode launch.
+    slot_mapping[b] must be -1 or the slot of position context_lens[b]-1."""
+    return _decode_q4("pkv_store_decode_q4", torch.bfloat16, q, (k, v, slot_mapping), k_cache, v_cache, block_tables,
+                      context_lens, max_context_len, softmax_scale, workspace, out, stream)
+
+
+def pkv_store_decode_q4_f16(q, k, v, slot_mapping, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                            softmax_scale, workspace, *, out=None, stream=None):
+    """pkv_store_decode_q4 on fp16 rows; returns fp16."""
+    return _decode_q4("pkv_store_decode_q4_f16", torch.float16, q, (k, v, slot_mapping), k_cache, v_cache,
+                      block_tables, context_lens, max_context_len, softmax_scale, workspace, out, stream)
 
 
 def pkv_build_prefill_metadata(num_cached_tokens, num_scheduled_tokens, block_tables, num_blocks, capacity,

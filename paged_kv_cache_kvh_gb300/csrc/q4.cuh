@@ -1,0 +1,162 @@
+// q4.cuh -- the 4-bit paged KV cache: format, quantiser and reader (sm_103a).
+//
+// One (token, kv head) row of K or of V is 128 dims in 4 groups of 32. A group
+// keeps a scale s = fp16((max - min) / 15) and a minimum z = fp16(min), a dim
+// keeps the code c = clamp(round_half_even((x - z) / s), 0, 15) (0 where s is
+// 0), and stands for s * c + z. |x| above 65504 counts as 65504; a group with
+// a NaN or an infinity has s = z = NaN, so it reads back as NaN.
+//
+// Cache layout, uint8 [num_blocks, num_kv_heads, 16, 1280]: a 256-token block
+// is 16 tiles of 16 tokens per head, a tile is 16 x 64 bytes of codes and then
+// 16 x 4 x (s, z) in fp16. The tokens of one head are contiguous, so any run
+// of whole tiles of a (block, head) is one bulk copy. Within a code row:
+//   K: the 32-bit word at byte 16 t + 4 j holds dims 32 j + 8 t + p, p = 0..7,
+//      code p in bits 4p..4p+3.
+//   V: the 8-byte chunk r sits at chunk place r ^ (4 if token & 4 else 0); its
+//      16-bit field j holds dims 32 j + 4 r + p, p = 0..3.
+// Both orders are what a tensor-core operand fragment of the decode kernel
+// reads with one 16-byte (K) or 8-byte (V) shared-memory load without bank
+// conflicts; the swap of the V halves is for the latter.
+#pragma once
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+constexpr int kQ4Tile = 16;                                   // tokens per tile
+constexpr int kQ4CodeBytes = 64;                              // one row's codes
+constexpr int kQ4ParamBytes = 16;                             // one row's 4 x (s, z)
+constexpr int kQ4TileBytes = kQ4Tile * (kQ4CodeBytes + kQ4ParamBytes);  // 1280
+constexpr int kQ4TileParams = kQ4Tile * kQ4CodeBytes;         // parameters' offset in a tile
+constexpr int kQ4RecordBytes = kBlockSize / kQ4Tile * kQ4TileBytes;     // one (block, head): 20480
+constexpr float kF16Max = 65504.f;
+
+__device__ __forceinline__ float2 h2_to_f2(uint32_t packed) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&packed));
+}
+
+// Packed pair max / min that keep a NaN of either operand.
+template <Elem E>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (E == Elem::kBF16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <Elem E>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (E == Elem::kBF16)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Quantises 8 consecutive dims per lane; the 4 lanes of an aligned lane quad
+// hold one group of 32 (all 32 lanes call this). Returns the 8 codes, dim p in
+// bits 4p..4p+3, and the group's parameters (s low half, z high half).
+//
+// The codes are those of the definition exactly, also next to a border between
+// two codes: the fp32 quotient is off by less than 15 * 2^-21 < 2^-17, so only
+// an element whose quotient lies within 2^-16 of a border is decided again,
+// from the sign of x - z - (k + 1/2) s. There the fp32 difference t = x - z
+// cancels against (k + 1/2) s (16 bits) without rounding, and what t itself
+// was rounded by is added back.
+template <Elem E>
+__device__ __forceinline__ uint32_t quantise8(const uint4 raw, uint32_t& param) {
+  using Ops = ElemOps<E>;
+  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t mx2 = max2_nan<E>(max2_nan<E>(in[0], in[1]), max2_nan<E>(in[2], in[3]));
+  uint32_t mn2 = min2_nan<E>(min2_nan<E>(in[0], in[1]), min2_nan<E>(in[2], in[3]));
+#pragma unroll
+  for (int off = 1; off <= 2; off <<= 1) {
+    mx2 = max2_nan<E>(mx2, __shfl_xor_sync(0xffffffffu, mx2, off));
+    mn2 = min2_nan<E>(mn2, __shfl_xor_sync(0xffffffffu, mn2, off));
+  }
+  mx2 = max2_nan<E>(mx2, __byte_perm(mx2, mx2, 0x1032));
+  mn2 = min2_nan<E>(mn2, __byte_perm(mn2, mn2, 0x1032));
+  float mx = Ops::lo(mx2), mn = Ops::lo(mn2);
+  if (!(fabsf(mx) < INFINITY && fabsf(mn) < INFINITY)) {
+    param = 0x7fff7fffu;
+    return 0u;
+  }
+  mx = fminf(fmaxf(mx, -kF16Max), kF16Max);
+  mn = fminf(fmaxf(mn, -kF16Max), kF16Max);
+  const __half hs = __float2half_rn(__fdiv_rn(mx - mn, 15.f)), hz = __float2half_rn(mn);
+  param = static_cast<uint32_t>(__half_as_ushort(hs)) | (static_cast<uint32_t>(__half_as_ushort(hz)) << 16);
+  const float s = __half2float(hs), z = __half2float(hz);
+  const float rs15 = s > 0.f ? __fdividef(1.f, 15.f * s) : 0.f;
+  float x[8], k[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = Ops::lo(in[i]);
+    x[2 * i + 1] = Ops::hi(in[i]);
+  }
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float u = __saturatef((x[i] - z) * rs15);  // (x - z) / (15 s), clamped to [0, 1]
+    k[i] = fmaf(u, 15.f, kRound) - kRound;
+    far = fmaxf(far, fabsf(fmaf(u, 15.f, -k[i])));
+  }
+  if (far > 0.5f - 1.52587890625e-5f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = x[i] - z;
+      const float d = fmaf(__saturatef(t * rs15), 15.f, -k[i]);
+      if (fabsf(d) > 0.5f - 1.52587890625e-5f) {
+        const float lower = d > 0.f ? k[i] : k[i] - 1.f;
+        const float b = t - x[i];
+        const float lost = (x[i] - (t - b)) + (-z - b);  // x - z == t + lost
+        const float side = fmaf(-(lower + 0.5f), s, t) + lost;
+        const bool odd = (static_cast<int>(lower) & 1) != 0;
+        k[i] = (side > 0.f || (side == 0.f && odd)) ? lower + 1.f : lower;
+      }
+    }
+  }
+  // four codes are one exact integer below 2^16 in fp32
+  const float lo = fmaf(4096.f, k[3], fmaf(256.f, k[2], fmaf(16.f, k[1], k[0])));
+  const float hi = fmaf(4096.f, k[7], fmaf(256.f, k[6], fmaf(16.f, k[5], k[4])));
+  return __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
+}
+
+// The V word of lane (j, t) of a row's 16 lanes (lane 4 j + t): chunk
+// 2 t + (j & 1), fields j & ~1 and j | 1, from every lane's 8 dims 8 (4 j + t)...
+// The same exchange turns such words back into dims.
+__device__ __forceinline__ uint32_t v_exchange(uint32_t own, int j) {
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 4);
+  return (j & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+}
+
+// Byte offsets within a tile, for lane (j, t) of token `tok` of the tile.
+__device__ __forceinline__ int q4_k_word(int tok, int j, int t) { return tok * kQ4CodeBytes + 16 * t + 4 * j; }
+__device__ __forceinline__ int q4_v_word(int tok, int j, int t) {
+  return tok * kQ4CodeBytes + ((2 * t + (j & 1)) ^ (tok & 4)) * 8 + (j >> 1) * 4;
+}
+__device__ __forceinline__ int q4_param(int tok, int j) { return kQ4TileParams + tok * kQ4ParamBytes + 4 * j; }
+
+// 8 codes -> 8 values s * c + z, rounded once to the element type (fp16:
+// saturated, since z + 15 s may pass 65504 by half a step of s).
+template <Elem E>
+__device__ __forceinline__ float q4_value(uint32_t code, float s, float z) {
+  float v = fmaf(static_cast<float>(code), s, z);
+  if (E == Elem::kF16) asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(kF16Max));
+  return v;
+}
+template <Elem E>
+__device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t param) {
+  using Ops = ElemOps<E>;
+  const float2 sz = h2_to_f2(param);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = Ops::pack(q4_value<E>((codes >> (8 * i)) & 15u, sz.x, sz.y),
+                     q4_value<E>((codes >> (8 * i + 4)) & 15u, sz.x, sz.y));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace pkv
