@@ -37,6 +37,8 @@
 // chunks go to the workspace, and the warp that finishes last merges them
 // (ticket, no waiting): up to 16 chunks at once, groups of 16 and then the
 // groups beyond that.
+#include <type_traits>
+
 #include "q4.cuh"
 
 namespace pkv {
@@ -51,16 +53,31 @@ struct FusedStore {
 
 namespace {
 
-constexpr int kUnit = 32;                                    // tokens per stage
+constexpr int kUnit = 64;                                    // tokens per stage
+constexpr int kHalfUnit = 32;                                // the shortest chunk
 constexpr int kUnitTiles = kUnit / kQ4Tile;
-constexpr int kUnitBytes = kUnitTiles * kQ4TileBytes;        // 2560, of K and of V each
-constexpr int kMaxChunk = kBlockSize / kUnit;                // units per item at most
-constexpr int kWarps = 12;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kMaxSeqs = 1024;                               // sequences per launch (item table in shared memory)
-constexpr int kPlanWarps = 152 * kWarps;                     // warps the chunk rule splits a call over
+constexpr int kUnitBytes = kUnitTiles * kQ4TileBytes;        // 5120, of K and of V each
+constexpr int kMaxChunk = 16;                                // units per chunk at most
+constexpr int kMaxSeqs = 768;                                // sequences per launch (item table in shared memory)
+constexpr int kClasses = 8;                                  // sizes that short chunks are sorted into
 constexpr int kFan = 16;                                     // chunks merged at once
+constexpr int kFirst = 1 << 30, kLast = 1 << 29;             // stage header: an item's first and last unit
+constexpr uint32_t kTf32Mask = 0xffffe000u;                  // the bits that a tf32 operand keeps
+constexpr uint32_t kOne = 0x3f800000u;                       // 1.0f
+
+// Warps per CTA (one CTA per SM) for G query heads to a kv head.
+#ifndef PKV_Q4_WARPS
+#define PKV_Q4_WARPS 12
+#endif
+__host__ __device__ constexpr int warps_of(int G) { return G <= 2 ? PKV_Q4_WARPS : 8; }
+
+// A warp's shared memory: two units of K, one of V, the query rows of two items
+// (they arrive with an item's first K), what is known of the two units, barriers.
+struct UnitHeader {
+  int32_t seq, head, tokens, chunks;  // head with kFirst / kLast; chunk | chunks of the sequence << 16
+  int64_t offset;                     // of the unit's first tile in the cache
+  int32_t bytes, pad;
+};
 
 struct Q4DecodeParams {
   const uint16_t* q;
@@ -77,10 +94,10 @@ struct Q4DecodeParams {
   float scale_log2;
   uint16_t* out;
   int32_t* work;     // {next item, warps done}, zero between calls
-  int32_t* tickets;  // one per item, zero between calls
-  float2* ml;        // [item][G] (max in log2 units, sum)
-  float* opart;      // [item][G][128], not normalised
-  int64_t max_items;
+  int32_t* tickets;  // one per slot, zero between calls
+  float2* ml;        // [slot][G] (max in log2 units, sum)
+  float* opart;      // [slot][G][128], not normalised; slot (whole chunks before b + b + chunk) * hkv + head
+  int64_t max_slots;
   // the step's new rows (pkv_store_decode_q4); k_new == nullptr for plain decode
   const uint16_t* k_new;
   const uint16_t* v_new;
@@ -92,14 +109,16 @@ struct Q4DecodeParams {
   unsigned int* err;
 };
 
-// Units per chunk. x is the number of units each planned warp would get: up to
-// kMaxChunk, one chunk each; beyond, as many rounds of equal chunks as keep a
-// chunk within kMaxChunk.
-__host__ __device__ inline int chunk_units(int64_t units_all_heads) {
-  const int64_t x = (units_all_heads + kPlanWarps - 1) / kPlanWarps;
-  if (x <= 1) return 1;
+// Tokens per chunk. Where half units suffice for one chunk to a warp, chunks of
+// 32 tokens (a short call is bound by the time of one chunk). Otherwise whole
+// units: x is the number that each warp would get; up to kMaxChunk, one chunk
+// each; beyond, as many rounds of equal chunks as keep a chunk within kMaxChunk.
+__host__ __device__ inline int chunk_tokens(int64_t half_units, int64_t units, int warps) {
+  const int64_t plan = int64_t{152} * warps;
+  if (half_units <= plan) return kHalfUnit;
+  const int64_t x = (units + plan - 1) / plan;
   const int64_t rounds = (x + kMaxChunk - 1) / kMaxChunk;
-  return static_cast<int>((x + rounds - 1) / rounds);
+  return static_cast<int>((x + rounds - 1) / rounds) * kUnit;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -107,10 +126,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
   return r;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
-  return r;
+// Four 8 x 8 matrices of 16-bit fields, transposed: lane i gives the address of
+// row i % 8 of matrix i / 8; lane (r, t) gets column r of rows 2t, 2t + 1.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&d)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(addr));
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
@@ -118,13 +139,26 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return r;
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ void mma1688_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -184,34 +218,39 @@ __device__ __forceinline__ void merge_slots(const Q4DecodeParams& p, int64_t fir
 }
 
 template <Elem E, int G>
-__global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodeParams p) {
+__global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4DecodeParams p) {
   using Ops = ElemOps<E>;
+  constexpr int kWarps = warps_of(G), kThreads = kWarps * 32;
   constexpr int kNB = (G + 1) / 2;            // B operands: pairs of query heads
   constexpr int kQBytes = G * kHeadDim * 2;   // one item's query rows
-  constexpr int kStageBytes = 2 * kUnitBytes + kQBytes;
+  constexpr int kWarpBytes = 3 * kUnitBytes + 2 * kQBytes;
   extern __shared__ __align__(128) uint8_t smem[];
-  int4* hdr_all = reinterpret_cast<int4*>(smem + kWarps * kStages * kStageBytes);  // [warp][stage]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(hdr_all + kWarps * kStages);        // [warp][stage]
-  int* sF = reinterpret_cast<int*>(bars + kWarps * kStages);                       // [num_seqs + 1] chunks before b
+  UnitHeader* hdr_all = reinterpret_cast<UnitHeader*>(smem + kWarps * kWarpBytes);  // [warp][2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(hdr_all + kWarps * 2);               // [warp][3]: K, K, V
+  int* sF = reinterpret_cast<int*>(bars + kWarps * 3);                              // [num_seqs + 1] whole chunks before b
   int* sCtx = sF + kMaxSeqs + 1;                                                   // [num_seqs]
-  int* red = sCtx + kMaxSeqs;                                                      // [kWarps]
+  int* plist = sCtx + kMaxSeqs;                                                    // sequences with a short last chunk
+  int* red = plist + kMaxSeqs;                                                     // [2][kWarps], then [9][32]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.num_seqs;
   const int n_ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
 
-  // ---- item table: chunks before each sequence ----
-  int chunk;  // units per chunk
+  // ---- item table (every CTA builds the same one) ----
+  // Whole chunks first, in sequence order, then the short last chunks in kClasses
+  // sizes, longest first: the items that end the call are the shortest. A warp
+  // holds sequences i * kThreads + tid, 32 consecutive ones (a group) at a time.
+  int chunk, n_full, n_part = 0;
   {
     constexpr int kPer = (kMaxSeqs + kThreads - 1) / kThreads;
-    const int per = (B + kThreads - 1) / kThreads;  // consecutive sequences per thread
+    static_assert(kPer * kWarps <= 32, "one lane per group below");
     int ctx[kPer];
-    int units = 0;
+    int halves = 0, units = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int b = tid * per + i;
+      const int b = i * kThreads + tid;
       ctx[i] = 0;
-      if (i < per && b < B) {
+      if (b < B) {
         const int c = p.context_lens[b];
         if (c < 0 || c > p.max_ctx || c > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
           if (cta == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
@@ -220,48 +259,88 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
         }
         sCtx[b] = ctx[i];
       }
+      halves += (ctx[i] + kHalfUnit - 1) / kHalfUnit;
       units += (ctx[i] + kUnit - 1) / kUnit;
     }
-    int sum = units;
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) red[warp] = sum;
-    if (lane < kStages) mbar_init(smem_u32(bars + warp * kStages + lane), 1);
+    for (int off = 16; off >= 1; off >>= 1) {
+      halves += __shfl_xor_sync(0xffffffffu, halves, off);
+      units += __shfl_xor_sync(0xffffffffu, units, off);
+    }
+    if (lane == 0) {
+      red[warp] = halves;
+      red[kWarps + warp] = units;
+    }
+    if (lane < 3) mbar_init(smem_u32(bars + warp * 3 + lane), 1);
     mbar_fence_init();
     __syncthreads();
-    int64_t all = 0;
+    int64_t all_halves = 0, all_units = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) all += red[w];
-    chunk = chunk_units(all * p.hkv);
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += ((ctx[i] + kUnit - 1) / kUnit + chunk - 1) / chunk;
-    int scan = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, scan, off);
-      if (lane >= off) scan += y;
+    for (int w = 0; w < kWarps; ++w) {
+      all_halves += red[w];
+      all_units += red[kWarps + w];
     }
-    __syncthreads();  // every thread has read red
-    if (lane == 31) red[warp] = scan;
-    __syncthreads();
-    int before = scan - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (w < warp) before += red[w];
+    chunk = chunk_tokens(all_halves * p.hkv, all_units * p.hkv, kWarps);
+    __syncthreads();  // red is written again
+    int full[kPer], cls[kPer], scan[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int b = tid * per + i;
-      if (i < per && b < B) {
-        sF[b] = before;
-        before += ((ctx[i] + kUnit - 1) / kUnit + chunk - 1) / chunk;
-        if (b == B - 1) sF[B] = before;
+      full[i] = ctx[i] / chunk;
+      const int rest = ctx[i] - full[i] * chunk;
+      cls[i] = rest > 0 ? kClasses - 1 - (rest * kClasses - 1) / chunk : -1;
+      scan[i] = full[i];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, scan[i], off);
+        if (lane >= off) scan[i] += y;
       }
+      int mine = 0;
+#pragma unroll
+      for (int k = 0; k < kClasses; ++k) {
+        const int c = __popc(__ballot_sync(0xffffffffu, cls[i] == k));
+        if (lane == k) mine = c;
+      }
+      const int group = i * kWarps + warp;
+      if (lane < kClasses) red[lane * 32 + group] = mine;
+      if (lane == 31) red[kClasses * 32 + group] = scan[i];
     }
     __syncthreads();
+    // lane = group: what comes before each group
+    constexpr int kGroups = kPer * kWarps;
+    int before[kClasses + 1];
+#pragma unroll
+    for (int k = 0; k <= kClasses; ++k) {
+      const int own = lane < kGroups ? red[k * 32 + lane] : 0;
+      int x = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, x, 31);
+      before[k] = x - own + (k < kClasses ? n_part : 0);
+      if (k < kClasses)
+        n_part += total;
+      else
+        n_full = total;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = i * kThreads + tid, group = i * kWarps + warp;
+      const int f0 = __shfl_sync(0xffffffffu, before[kClasses], group);
+      if (b < B) sF[b] = f0 + scan[i] - full[i];
+#pragma unroll
+      for (int k = 0; k < kClasses; ++k) {
+        const uint32_t same = __ballot_sync(0xffffffffu, cls[i] == k);
+        const int at = __shfl_sync(0xffffffffu, before[k], group);
+        if (cls[i] == k) plist[at + __popc(same & ((1u << lane) - 1u))] = b;
+      }
+    }
+    if (tid == 0) sF[B] = n_full;
+    __syncthreads();
   }
-  const int64_t n_items = static_cast<int64_t>(sF[B]) * p.hkv;
-  if (n_items > p.max_items) {  // cannot happen: the workspace bound covers every table
+  const int64_t n_items = static_cast<int64_t>(n_full + n_part) * p.hkv;
+  if (static_cast<int64_t>(n_full + B) * p.hkv > p.max_slots) {  // cannot happen: the workspace bound covers every table
     if (tid == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
   }
@@ -274,9 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
     }
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
-  const uint32_t full = smem_u32(bars + warp * kStages);
-  int4* hdr = hdr_all + warp * kStages;
+  const uint32_t k_buf = smem_u32(smem) + warp * kWarpBytes, v_buf = k_buf + 2 * kUnitBytes;
+  const uint32_t q_buf = v_buf + kUnitBytes;
+  const uint32_t k_full = smem_u32(bars + warp * 3), v_full = k_full + 16;
+  UnitHeader* hdr = hdr_all + warp * 2;
   const int r = lane >> 2, t = lane & 3;
   const int W = n_ctas * kWarps;
   const bool dynamic = n_items > W;
@@ -285,48 +365,57 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
   int64_t item = static_cast<int64_t>(warp) * n_ctas + cta;
   int next_raw = 0;  // lane 0: the counter's answer for the item after this one
   if (dynamic && lane == 0) next_raw = atomicAdd(p.work, 1);
-  int ib = 0, ihead = 0, ic = 0, inch = 0, iu = 0, iend = 0, ipb = -1, ipblk = -1;
+  int ib = 0, ihead = 0, ic = 0, inch = 0, itok = 0, iend = 0;  // sequence, head, chunk, chunks, next token, chunk's end
+  int ipb = -1;        // block of the unit to fetch; read one unit ahead of its use
+  bool fresh = false;  // ipb has not been checked yet
+  auto look_up = [&]() {
+    ipb = p.block_tables[static_cast<int64_t>(ib) * p.bt_stride + itok / kBlockSize];
+    fresh = true;
+  };
   auto resolve = [&]() {  // item -> sequence, chunk, head (whole warp)
     const int ci = static_cast<int>(item / p.hkv);
     ihead = static_cast<int>(item - static_cast<int64_t>(ci) * p.hkv);
-    // largest b with sF[b] <= ci, 32 probes at a time
-    const int step = (B + 31) / 32;
-    const int probe = lane * step;
-    const int hi = __popc(__ballot_sync(0xffffffffu, probe < B && sF[probe] <= ci)) - 1;
-    const int q0 = hi * step;
-    const int probe2 = q0 + lane;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, lane < step && probe2 < B && sF[probe2] <= ci));
-    ib = q0 + cnt - 1;
-    ic = ci - sF[ib];
+    if (ci < n_full) {
+      // largest b with sF[b] <= ci, 32 probes at a time
+      const int step = (B + 31) / 32;
+      const int probe = lane * step;
+      const int hi = __popc(__ballot_sync(0xffffffffu, probe < B && sF[probe] <= ci)) - 1;
+      const int probe2 = hi * step + lane;
+      const int cnt = __popc(__ballot_sync(0xffffffffu, lane < step && probe2 < B && sF[probe2] <= ci));
+      ib = hi * step + cnt - 1;
+      ic = ci - sF[ib];
+    } else {
+      ib = plist[ci - n_full];
+      ic = sF[ib + 1] - sF[ib];
+    }
+    const int ctx = sCtx[ib];
     inch = sF[ib + 1] - sF[ib];
-    iu = ic * chunk;
-    iend = min(iu + chunk, (sCtx[ib] + kUnit - 1) / kUnit);
-    ipblk = -1;
+    inch += inch * chunk < ctx ? 1 : 0;
+    itok = ic * chunk;
+    iend = min(itok + chunk, ctx);
+    look_up();
   };
   bool more = item < n_items;
   if (more) resolve();
-  int issued = 0;
-  auto issue = [&]() {  // fetches one unit into slot issued % kStages (whole warp)
+  int issued = 0;  // units whose K has been asked for
+  auto issue_k = [&]() {  // fetches the next unit's K (whole warp)
     if (!more) return;
-    const int s = issued % kStages;
-    const int ctx = sCtx[ib];
-    const int tok0 = iu * kUnit;
-    const int ntok = min(kUnit, ctx - tok0);
-    if (ipblk != tok0 / kBlockSize) {
-      ipblk = tok0 / kBlockSize;
-      ipb = p.block_tables[static_cast<int64_t>(ib) * p.bt_stride + ipblk];
+    if (fresh) {
       if (ipb < 0 || ipb >= p.num_blocks) {
         if (lane == 0) flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
         ipb = -1;
       }
+      fresh = false;
     }
+    const int ntok = min(kUnit, iend - itok);
     const int64_t rec = (static_cast<int64_t>(ipb) * p.hkv + ihead) * kQ4RecordBytes;
-    const bool last = iu + 1 == iend;
+    const bool first = itok == ic * chunk, last = itok + ntok == iend;
     if (p.k_new != nullptr && last && ic == inch - 1) {
       // this unit holds the newest position: its row is written before the unit is fetched
       const int64_t slot = p.slot_mapping[ib];
       if (slot != -1) {
-        if (ipb < 0 || slot != static_cast<int64_t>(ipb) * kBlockSize + (ctx - 1) % kBlockSize) {
+        const int in_block = (iend - 1) % kBlockSize, tok = in_block % kQ4Tile;
+        if (ipb < 0 || slot != static_cast<int64_t>(ipb) * kBlockSize + in_block) {
           if (lane == 0 && ihead == 0) flag_error(p.err, PKV_DEVERR_BAD_SLOT);
         } else {
           const int lane16 = lane & 15, j = lane16 >> 2, tt = lane16 & 3;
@@ -336,7 +425,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           uint32_t par;
           uint32_t codes = quantise8<E>(*reinterpret_cast<const uint4*>(src), par);
           const uint32_t vcodes = v_exchange(codes, j);
-          const int in_block = (ctx - 1) % kBlockSize, tok = in_block % kQ4Tile;
           uint8_t* dst = (is_v ? p.v_cache_w : p.k_cache_w) + rec + in_block / kQ4Tile * kQ4TileBytes;
           *reinterpret_cast<uint32_t*>(dst + (is_v ? q4_v_word(tok, j, tt) : q4_k_word(tok, j, tt))) =
               is_v ? vcodes : codes;
@@ -348,23 +436,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
       }
     }
     if (lane == 0) {
-      const uint32_t dst = ring + s * kStageBytes;
-      const bool first = iu == ic * chunk;
+      const int s = issued & 1;
       const uint32_t bytes = ipb < 0 ? 0u : static_cast<uint32_t>((ntok + kQ4Tile - 1) / kQ4Tile) * kQ4TileBytes;
-      hdr[s] = make_int4(ib, ihead | (static_cast<int>(first) << 30) | (static_cast<int>(last) << 29),
-                         ipb < 0 ? 0 : ntok, ic);
-      mbar_arrive_expect_tx(full + 8 * s, 2 * bytes + (first ? kQBytes : 0));
-      if (bytes > 0) {
-        const int64_t off = rec + (tok0 % kBlockSize) / kQ4Tile * kQ4TileBytes;
-        bulk_g2s(dst, p.k_cache + off, bytes, full + 8 * s);
-        bulk_g2s(dst + kUnitBytes, p.v_cache + off, bytes, full + 8 * s);
-      }
+      const int64_t off = rec + (itok % kBlockSize) / kQ4Tile * kQ4TileBytes;
+      UnitHeader u;
+      u.seq = ib;
+      u.head = ihead | (first ? kFirst : 0) | (last ? kLast : 0);
+      u.tokens = ipb < 0 ? 0 : ntok;
+      u.chunks = ic | (inch << 16);
+      u.offset = off;
+      u.bytes = static_cast<int32_t>(bytes);
+      u.pad = 0;
+      hdr[s] = u;
+      mbar_arrive_expect_tx(k_full + 8 * s, bytes + (first ? kQBytes : 0));
+      if (bytes > 0) bulk_g2s(k_buf + s * kUnitBytes, p.k_cache + off, bytes, k_full + 8 * s);
       if (first)
-        bulk_g2s(dst + 2 * kUnitBytes, p.q + static_cast<int64_t>(ib) * p.q_row_stride + ihead * G * kHeadDim, kQBytes,
-                 full + 8 * s);
+        bulk_g2s(q_buf + s * kQBytes, p.q + static_cast<int64_t>(ib) * p.q_row_stride + ihead * G * kHeadDim, kQBytes,
+                 k_full + 8 * s);
     }
     ++issued;
-    ++iu;
+    itok += ntok;
     if (last) {
       more = false;
       if (dynamic) {
@@ -375,323 +466,414 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           resolve();
         }
       }
+    } else if (itok % kBlockSize == 0) {
+      look_up();
     }
   };
-#pragma unroll 1
-  for (int s = 0; s < kStages; ++s) issue();
+  auto issue_v = [&](int n) {  // fetches V of unit n, whose K has been asked for
+    if (n < issued && lane == 0) {
+      const int64_t off = hdr[n & 1].offset;
+      const uint32_t bytes = static_cast<uint32_t>(hdr[n & 1].bytes);
+      mbar_arrive_expect_tx(v_full, bytes);
+      if (bytes > 0) bulk_g2s(v_buf, p.v_cache + off, bytes, v_full);
+    }
+  };
+  issue_k();
+  issue_v(0);
+  issue_k();
 
   // ---- the computing side ----
-  // lane (r, t): K rows (C fragment) of tokens tk, tk + 8 and group t; V columns
-  // of tokens tv, tv ^ 1, tv + 8, (tv ^ 1) + 8 and 16-dim chunk r. Row r of a C
-  // fragment stands for token r ^ (r >> 1 & 1), which makes both loads free of
-  // bank conflicts.
-  const int tk = r ^ ((r >> 1) & 1);
-  const int tv = (2 * t) ^ (t & 1);
-  const uint32_t k_off = tk * kQ4CodeBytes + t * 16;
-  const uint32_t par_off = kQ4TileParams + tk * kQ4ParamBytes + t * 4;
-  const uint32_t va_off = tv * kQ4CodeBytes + ((r ^ (tv & 4)) << 3);
-  const uint32_t vb_off = (tv ^ 1) * kQ4CodeBytes + ((r ^ (tv & 4)) << 3);
-  uint32_t qb[kNB][8][2];           // B fragments of q, one per 16 dims
-  float kc[G + (G & 1)], qs[G + (G & 1)];
+  // Lane (r, t): K rows (and C rows) of tokens r, r + 8, group t. For V, lane i of
+  // a 4-matrix transposing load addresses 16-byte chunk i / 8 of token i % 8; lane
+  // (r, t) then holds, of tokens 2t, 2t + 1, four dims of group r & 3 per chunk.
+  const uint32_t par_off = kQ4TileParams + r * kQ4ParamBytes + t * 4;
+  const uint32_t v_off = (lane & 7) * kQ4CodeBytes + (((lane >> 3) ^ ((lane & 4) >> 1)) << 4);
+  uint32_t qb[kNB][8][2];    // B fragments of q, one per 16 dims
+  uint32_t qs_b[G][2];       // B fragment of sum q over group t: high and low part
+  float kc[kNB][2];          // per head: the power of two taken out of q and the codes, times scale * log2(e)
   float acc[kNB][8][4];
-  float m[G], l[G], zs[G];
+  uint64_t l2[G], z2[G];     // sums of p and of p z, tokens r and r + 8 apart
+  float m[G];                // running maximum, -INFINITY before the first unit
+  float from[G][4];          // minus the maximum that logits are taken relative to (a C fragment)
   float nu = 1.f;
-  int done = 0;
-  for (; done < issued; ++done) {
-    const int s = done % kStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, (done / kStages) & 1, p.err))) break;
-    const int4 hd = hdr[s];
-    const uint32_t st = ring + s * kStageBytes;
-    if (hd.y & (1 << 30)) {
-      // ---- a new item: query fragments ----
+
+  int done = 0;              // units worked through
+  bool pending = false;      // a partial result is written, its ticket not taken yet
+  int pend_b = 0, pend_head = 0, pend_c = 0;  // pend_c: chunk | chunks << 16
+  while (true) {
+    const bool have = done < issued;
+    int seq = 0, head_flags = 0, chunks = 0;
+    if (have) {
+      const int s = done & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(k_full + 8 * s, (done >> 1) & 1, p.err))) break;
+      const uint32_t kst = k_buf + s * kUnitBytes;
+      seq = hdr[s].seq;
+      head_flags = hdr[s].head;
+      chunks = hdr[s].chunks;
+      const int ntok = hdr[s].tokens;
+      if (head_flags & kFirst) {
+        // ---- a new item: query fragments ----
 #pragma unroll
-      for (int nb = 0; nb < kNB; ++nb) {
-        const int h = 2 * nb + (r & 1);  // the column's head; its group is r >> 1
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (h < G) raw = lds128(st + 2 * kUnitBytes + h * kHeadDim * 2 + ((r >> 1) * 32 + t * 8) * 2);
-        float x[8] = {Ops::lo(raw.x), Ops::hi(raw.x), Ops::lo(raw.y), Ops::hi(raw.y),
-                      Ops::lo(raw.z), Ops::hi(raw.z), Ops::lo(raw.w), Ops::hi(raw.w)};
-        float big = 0.f, sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          big = fmaxf(big, fabsf(x[i]));
-          sum += x[i];
-        }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int e = big > 0.f ? max(-100, 13 - exponent_of(big)) : 0;  // the largest |q| goes to [2^13, 2^14)
-        const float f = pow2(min(e, 120));
-        const float f16 = f * 0.0625f;  // for the codes that A holds 16 times too large
-        const uint32_t own[4] = {pack_f16(x[0] * f, x[4] * f), pack_f16(x[1] * f16, x[5] * f16),
-                                 pack_f16(x[2] * f, x[6] * f), pack_f16(x[3] * f16, x[7] * f16)};
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const bool on = (ks >> 1) == (r >> 1);
-          qb[nb][ks][0] = on ? own[(ks & 1) * 2] : 0u;
-          qb[nb][ks][1] = on ? own[(ks & 1) * 2 + 1] : 0u;
-        }
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const float fh = __shfl_sync(0xffffffffu, f, 4 * h2);
-          kc[2 * nb + h2] = __fdividef(16777216.f, fh) * p.scale_log2;  // a power of two times scale * log2(e)
-          qs[2 * nb + h2] = __shfl_sync(0xffffffffu, sum, (2 * t + h2) * 4) * p.scale_log2;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[nb][i][c] = 0.f;
-      }
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        m[h] = -INFINITY;
-        l[h] = zs[h] = 0.f;
-      }
-      nu = 1.f;
-    }
-    const int ntok = hd.z;
-    if (ntok > 0) {
-      // ---- logits ----
-      float lg[kNB][kUnitTiles][4];  // [2 half + head]: token tk + 8 half
-#pragma unroll
-      for (int tile = 0; tile < kUnitTiles; ++tile) {
-        const uint32_t base = st + tile * kQ4TileBytes;
-        const uint4 w0 = lds128(base + k_off), w1 = lds128(base + k_off + 8 * kQ4CodeBytes);
-        const float2 sz0 = h2_to_f2(lds32(base + par_off)), sz1 = h2_to_f2(lds32(base + par_off + 8 * kQ4ParamBytes));
-        float c[kNB][4];
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) c[nb][0] = c[nb][1] = c[nb][2] = c[nb][3] = 0.f;
-        const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, b[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t ah = a[j] >> 8, bh = b[j] >> 8;
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) {
-            mma16816(c[nb], a[j] & 0x000f000fu, b[j] & 0x000f000fu, a[j] & 0x00f000f0u, b[j] & 0x00f000f0u,
-                     qb[nb][2 * j][0], qb[nb][2 * j][1]);
-            mma16816(c[nb], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u,
-                     qb[nb][2 * j + 1][0], qb[nb][2 * j + 1][1]);
-          }
-        }
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            float x0 = fmaf(c[nb][h2], sz0.x * kc[2 * nb + h2], sz0.y * qs[2 * nb + h2]);
-            float x1 = fmaf(c[nb][2 + h2], sz1.x * kc[2 * nb + h2], sz1.y * qs[2 * nb + h2]);
-            x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
-            x1 += __shfl_xor_sync(0xffffffffu, x1, 1);
-            x0 += __shfl_xor_sync(0xffffffffu, x0, 2);
-            x1 += __shfl_xor_sync(0xffffffffu, x1, 2);
-            lg[nb][tile][h2] = x0;
-            lg[nb][tile][2 + h2] = x1;
-          }
-      }
-      // V's scale and minimum of this lane's tokens and group; past the end both are 0
-      float2 vsz[kUnitTiles][2];
-#pragma unroll
-      for (int tile = 0; tile < kUnitTiles; ++tile)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const bool in = tile * kQ4Tile + 8 * half + tk < ntok;
-          const uint32_t w = lds32(st + kUnitBytes + tile * kQ4TileBytes + par_off + half * 8 * kQ4ParamBytes);
-          vsz[tile][half] = h2_to_f2(in ? w : 0u);
-          if (!in) {
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) lg[nb][tile][2 * half] = lg[nb][tile][2 * half + 1] = -INFINITY;
-          }
-        }
-      // ---- running maximum: moves only when a logit passes it by more than 8 (2^8 of headroom) ----
-      float top[G];
-      bool moved = false;
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int tile = 0; tile < kUnitTiles; ++tile)
-          x = fmax3(x, lg[h / 2][tile][h & 1], lg[h / 2][tile][2 + (h & 1)]);
-        top[h] = x;
-        moved |= x > m[h] + 8.f;
-      }
-      moved = __any_sync(0xffffffffu, moved);
-      if (moved) {
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          float x = top[h];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, m[h]);
-          const float sc = ex2_approx(m[h] - (x == -INFINITY ? 0.f : x));
-          m[h] = x;
-          l[h] *= sc;
-          zs[h] *= sc;
+        for (int nb = 0; nb < kNB; ++nb) {
+          const int h = 2 * nb + (r & 1);  // the column's head; its group is r >> 1
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (h < G) raw = lds128(q_buf + s * kQBytes + h * kHeadDim * 2 + ((r >> 1) * 32 + t * 8) * 2);
+          float x[8] = {Ops::lo(raw.x), Ops::hi(raw.x), Ops::lo(raw.y), Ops::hi(raw.y),
+                        Ops::lo(raw.z), Ops::hi(raw.z), Ops::lo(raw.w), Ops::hi(raw.w)};
+          float big = 0.f, sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            acc[h / 2][i][h & 1] *= sc;
-            acc[h / 2][i][2 + (h & 1)] *= sc;
+            big = fmaxf(big, fabsf(x[i]));
+            sum += x[i];
           }
-        }
-      }
-      // ---- p, its sums, and p * s for the product with V's codes ----
-      float w[kNB][kUnitTiles][4];
-      float wmax = 0.f;
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          const int e = big > 0.f ? max(-100, 13 - exponent_of(big)) : 0;  // the largest |q| goes to [2^13, 2^14)
+          const float f = pow2(min(e, 120));
+          const float f16 = f * 0.0625f;  // for the codes that A holds 16 times too large
+          const uint32_t own[4] = {pack_f16(x[0] * f, x[4] * f), pack_f16(x[1] * f16, x[5] * f16),
+                                   pack_f16(x[2] * f, x[6] * f), pack_f16(x[3] * f16, x[7] * f16)};
 #pragma unroll
-      for (int nb = 0; nb < kNB; ++nb)
+          for (int ks = 0; ks < 8; ++ks) {
+            const bool on = (ks >> 1) == (r >> 1);
+            qb[nb][ks][0] = on ? own[(ks & 1) * 2] : 0u;
+            qb[nb][ks][1] = on ? own[(ks & 1) * 2 + 1] : 0u;
+          }
 #pragma unroll
-        for (int tile = 0; tile < kUnitTiles; ++tile)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int h = 2 * nb + (i & 1);
-            w[nb][tile][i] = 0.f;
-            if (h < G) {
-              const float mu = m[h] == -INFINITY ? 0.f : m[h];
-              const float pr = ex2_approx(lg[nb][tile][i] - mu);
-              l[h] += pr;
-              zs[h] = fmaf(pr, vsz[tile][i >> 1].y, zs[h]);
-              w[nb][tile][i] = pr * vsz[tile][i >> 1].x;
-              wmax = fmaxf(wmax, w[nb][tile][i]);
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const float fh = __shfl_sync(0xffffffffu, f, 4 * h2);
+            kc[nb][h2] = __fdividef(16777216.f, fh) * p.scale_log2;
+            const float qs = __shfl_sync(0xffffffffu, sum, (2 * t + h2) * 4) * p.scale_log2;
+            if (2 * nb + h2 < G) {
+              qs_b[(2 * nb + h2) % G][0] = __float_as_uint(qs) & kTf32Mask;
+              qs_b[(2 * nb + h2) % G][1] = __float_as_uint(qs - __uint_as_float(__float_as_uint(qs) & kTf32Mask));
             }
           }
-      if (moved || __any_sync(0xffffffffu, wmax * nu > 16384.f)) {
-        // nu: the power of two that takes the largest p s of this unit to [1, 2)
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
-        const float nu2 = pow2(max(-24, min(24, -exponent_of(wmax))));
-        const float sc = __fdividef(nu2, nu);
-        nu = nu2;
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[nb][i][c] *= sc;
-      }
-      // ---- o += (p s) . V codes ----
-#pragma unroll
-      for (int tile = 0; tile < kUnitTiles; ++tile) {
-        uint32_t pb[kNB][2];
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) {
-          pb[nb][0] = movmatrix(pack_f16(w[nb][tile][0] * nu, w[nb][tile][1] * nu));
-          pb[nb][1] = movmatrix(pack_f16(w[nb][tile][2] * nu, w[nb][tile][3] * nu));
+            for (int c = 0; c < 4; ++c) acc[nb][i][c] = 0.f;
         }
-        const uint32_t base = st + kUnitBytes + tile * kQ4TileBytes;
-        const uint2 a0 = lds64(base + va_off), a1 = lds64(base + vb_off);
-        const uint2 b0 = lds64(base + va_off + 8 * kQ4CodeBytes), b1 = lds64(base + vb_off + 8 * kQ4CodeBytes);
-        const uint32_t lo[4] = {__byte_perm(a0.x, a1.x, 0x5410), __byte_perm(a0.x, a1.x, 0x7632),
-                                __byte_perm(a0.y, a1.y, 0x5410), __byte_perm(a0.y, a1.y, 0x7632)};
-        const uint32_t hi[4] = {__byte_perm(b0.x, b1.x, 0x5410), __byte_perm(b0.x, b1.x, 0x7632),
-                                __byte_perm(b0.y, b1.y, 0x5410), __byte_perm(b0.y, b1.y, 0x7632)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo8 = lo[j] >> 8, hi8 = hi[j] >> 8;
+        for (int h = 0; h < G; ++h) {
+          m[h] = -INFINITY;
+          from[h][0] = from[h][1] = from[h][2] = from[h][3] = 0.f;
+          l2[h] = z2[h] = 0;
+        }
+        nu = 1.f;
+      }
+
+      // ---- logits, less the running maximum: lg[h][tile][half], tokens r + 8 half ----
+      float lg[G][kUnitTiles][2];
+#pragma unroll
+      for (int pair = 0; pair < kUnitTiles / 2; ++pair) {
+        if (pair * kHalfUnit >= ntok) {
+#pragma unroll
+          for (int h = 0; h < G; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lg[h][2 * pair + i / 2][i & 1] = -INFINITY;
+          continue;
+        }
+        float c[2][kNB][4];
+        uint4 w0[2], w1[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t base = kst + (2 * pair + i) * kQ4TileBytes + lane * 16;
+          w0[i] = lds128(base);
+          w1[i] = lds128(base + 8 * kQ4CodeBytes);
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb) c[i][nb][0] = c[i][nb][1] = c[i][nb][2] = c[i][nb][3] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a = j == 0 ? w0[i].x : j == 1 ? w0[i].y : j == 2 ? w0[i].z : w0[i].w;
+            const uint32_t b = j == 0 ? w1[i].x : j == 1 ? w1[i].y : j == 2 ? w1[i].z : w1[i].w;
+            const uint32_t ah = a >> 8, bh = b >> 8;
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) {
+              mma16816(c[i][nb], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qb[nb][2 * j][0],
+                       qb[nb][2 * j][1], c[i][nb]);
+              mma16816(c[i][nb], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u,
+                       qb[nb][2 * j + 1][0], qb[nb][2 * j + 1][1], c[i][nb]);
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t base = kst + (2 * pair + i) * kQ4TileBytes + par_off;
+          const float2 sz0 = h2_to_f2(lds32(base)), sz1 = h2_to_f2(lds32(base + 8 * kQ4ParamBytes));
 #pragma unroll
           for (int nb = 0; nb < kNB; ++nb) {
-            mma16816(acc[nb][2 * j], lo[j] & 0x000f000fu, lo[j] & 0x00f000f0u, hi[j] & 0x000f000fu,
-                     hi[j] & 0x00f000f0u, pb[nb][0], pb[nb][1]);
-            mma16816(acc[nb][2 * j + 1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu,
-                     hi8 & 0x00f000f0u, pb[nb][0], pb[nb][1]);
+            float x[4];  // s_g acc_g of [half][head]
+            f32x2_unpack(f32x2_mul(f32x2_pack(c[i][nb][0], c[i][nb][1]),
+                                   f32x2_pack(sz0.x * kc[nb][0], sz0.x * kc[nb][1])), x[0], x[1]);
+            f32x2_unpack(f32x2_mul(f32x2_pack(c[i][nb][2], c[i][nb][3]),
+                                   f32x2_pack(sz1.x * kc[nb][0], sz1.x * kc[nb][1])), x[2], x[3]);
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const int h = 2 * nb + h2;
+              if (h < G) {
+                // the sum over the groups (the four lanes t) as a product with ones, plus z . sum q
+                float d[4];
+                const uint32_t h0 = __float_as_uint(x[h2]) & kTf32Mask, h1 = __float_as_uint(x[2 + h2]) & kTf32Mask;
+                mma1688_tf32(d, __float_as_uint(sz0.y), __float_as_uint(sz1.y), __float_as_uint(sz0.y),
+                             __float_as_uint(sz1.y), qs_b[h][0], qs_b[h][1], from[h]);
+                mma1688_tf32(d, h0, h1, __float_as_uint(x[h2] - __uint_as_float(h0)),
+                             __float_as_uint(x[2 + h2] - __uint_as_float(h1)), kOne, kOne, d);
+                lg[h][2 * pair + i][0] = d[0];
+                lg[h][2 * pair + i][1] = d[2];
+              }
+            }
           }
         }
       }
-    }
-    __syncwarp();  // every lane has read the slot
-    issue();
-    if (!(hd.y & (1 << 29))) continue;
+      __syncwarp();  // every lane has read K and the header
+      issue_k();
+      if (!__all_sync(0xffffffffu, mbar_wait(v_full, done & 1, p.err))) break;
 
-    // ---- the item's end: dims 32 t + 4 r .. + 3 of every head in this lane ----
-    const int b = hd.x, head = hd.y & 0xffff, c = hd.w;
-    const int first_chunk = sF[b], nch = sF[b + 1] - first_chunk;
-    const int64_t slot = static_cast<int64_t>(first_chunk + c) * p.hkv + head;
-    uint16_t* orow = p.out + (static_cast<int64_t>(b) * p.hkv + head) * G * kHeadDim;
+      if (ntok > 0) {
+        // V's scale and minimum of this lane's tokens and group
+        uint32_t vp[kUnitTiles][2];
+#pragma unroll
+        for (int tile = 0; tile < kUnitTiles; ++tile)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            vp[tile][half] = lds32(v_buf + tile * kQ4TileBytes + par_off + half * 8 * kQ4ParamBytes);
+        if (ntok < kUnit) {
+          // past the end: no weight, and 0 for whatever the bytes there hold
+#pragma unroll
+          for (int tile = 0; tile < kUnitTiles; ++tile)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              if (tile * kQ4Tile + 8 * half + r >= ntok) {
+                vp[tile][half] = 0u;
+#pragma unroll
+                for (int h = 0; h < G; ++h) lg[h][tile][half] = -INFINITY;
+              }
+        }
+        // ---- running maximum: moves only when a logit passes it by more than 8 (2^8 of headroom) ----
+        float top[G];
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          top[h] = fmaxf(lg[h][0][0], lg[h][0][1]);
+#pragma unroll
+          for (int tile = 1; tile < kUnitTiles; ++tile) top[h] = fmax3(top[h], lg[h][tile][0], lg[h][tile][1]);
+          moved |= top[h] > 8.f || m[h] == -INFINITY;
+        }
+        moved = __any_sync(0xffffffffu, moved);
+        if (moved) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            float x = top[h];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            // logits are relative to the old maximum (to 0 if there is none yet)
+            const bool none = m[h] == -INFINITY;
+            const float up = none ? (x == -INFINITY ? 0.f : x) : fmaxf(x, 0.f);
+            const float sc = none ? 0.f : ex2_approx(-up);
+            m[h] = none ? x : m[h] + up;
+            from[h][0] = from[h][1] = from[h][2] = from[h][3] = m[h] == -INFINITY ? 0.f : -m[h];
+#pragma unroll
+            for (int tile = 0; tile < kUnitTiles; ++tile)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) lg[h][tile][half] -= up;
+            l2[h] = f32x2_mul(l2[h], f32x2_pack(sc, sc));
+            z2[h] = f32x2_mul(z2[h], f32x2_pack(sc, sc));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[h / 2][i][h & 1] *= sc;
+              acc[h / 2][i][2 + (h & 1)] *= sc;
+            }
+          }
+        }
+        // ---- p and its sums ----
+        float2 vsz[kUnitTiles][2];
+        float smax = 0.f;
+#pragma unroll
+        for (int tile = 0; tile < kUnitTiles; ++tile) {
+          vsz[tile][0] = h2_to_f2(vp[tile][0]);
+          vsz[tile][1] = h2_to_f2(vp[tile][1]);
+          smax = fmax3(smax, vsz[tile][0].x, vsz[tile][1].x);
+        }
+        uint64_t pr[G][kUnitTiles];
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+#pragma unroll
+          for (int tile = 0; tile < kUnitTiles; ++tile) {
+            pr[h][tile] = f32x2_pack(ex2_approx(lg[h][tile][0]), ex2_approx(lg[h][tile][1]));
+            l2[h] = f32x2_add(l2[h], pr[h][tile]);
+            z2[h] = f32x2_fma(pr[h][tile], f32x2_pack(vsz[tile][0].y, vsz[tile][1].y), z2[h]);
+          }
+        if (moved || __any_sync(0xffffffffu, smax * nu > 64.f)) {
+          // p <= 2^8, so p s nu stays below 2^14 otherwise. nu: the power of two
+          // that takes the largest p s of this unit to [1, 2)
+          float wmax = 0.f;
+#pragma unroll
+          for (int h = 0; h < G; ++h)
+#pragma unroll
+            for (int tile = 0; tile < kUnitTiles; ++tile) {
+              float p0, p1;
+              f32x2_unpack(pr[h][tile], p0, p1);
+              wmax = fmax3(wmax, p0 * vsz[tile][0].x, p1 * vsz[tile][1].x);
+            }
+#pragma unroll
+          for (int off = 16; off >= 1; off >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
+          const float nu2 = pow2(max(-24, min(24, -exponent_of(wmax))));
+          const float sc = __fdividef(nu2, nu);
+          nu = nu2;
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[nb][i][c] *= sc;
+        }
+        // ---- o += (p s) . V codes ----
+#pragma unroll
+        for (int tile = 0; tile < kUnitTiles; ++tile) {
+          if (tile == 2 && ntok <= kHalfUnit) break;
+          const uint64_t s2 = f32x2_pack(vsz[tile][0].x * nu, vsz[tile][1].x * nu);
+          uint32_t pb[kNB][2];
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb) {
+            float a0, a1, b0 = 0.f, b1 = 0.f;
+            f32x2_unpack(f32x2_mul(pr[2 * nb][tile], s2), a0, a1);
+            if (2 * nb + 1 < G) f32x2_unpack(f32x2_mul(pr[(2 * nb + 1) % G][tile], s2), b0, b1);
+            pb[nb][0] = movmatrix(pack_f16(a0, b0));
+            pb[nb][1] = movmatrix(pack_f16(a1, b1));
+          }
+          const uint32_t base = v_buf + tile * kQ4TileBytes + v_off;
+          uint32_t lo[4], hi[4];
+          ldmatrix_x4_trans(base, lo);
+          ldmatrix_x4_trans(base + 8 * kQ4CodeBytes, hi);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t lo8 = lo[q] >> 8, hi8 = hi[q] >> 8;
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) {
+              mma16816(acc[nb][2 * q], lo[q] & 0x000f000fu, lo[q] & 0x00f000f0u, hi[q] & 0x000f000fu,
+                       hi[q] & 0x00f000f0u, pb[nb][0], pb[nb][1], acc[nb][2 * q]);
+              mma16816(acc[nb][2 * q + 1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u,
+                       pb[nb][0], pb[nb][1], acc[nb][2 * q + 1]);
+            }
+          }
+        }
+      }
+      ++done;
+      __syncwarp();  // every lane has read V
+      issue_v(done);
+    }
+
+    // ---- the ticket of the item before: its writes have had a unit's time to land ----
+    if (pending) {
+      pending = false;
+      const int first_chunk = sF[pend_b] + pend_b, nch = pend_c >> 16, c = pend_c & 0xffff;
+      auto arrive = [&](int64_t ticket, int expected) -> bool {
+        __syncwarp();
+        int is_last = 0;
+        if (lane == 0) {
+          __threadfence();
+          is_last = atomicAdd(p.tickets + ticket, 1) == expected - 1;
+          if (is_last) p.tickets[ticket] = 0;  // ready for the next call
+        }
+        is_last = __shfl_sync(0xffffffffu, is_last, 0);
+        if (is_last) __threadfence();
+        return is_last != 0;
+      };
+      const int g0 = c - c % kFan;  // this chunk's group of kFan
+      const int64_t slot_g = static_cast<int64_t>(first_chunk + g0) * p.hkv + pend_head;
+      const int in_group = min(kFan, nch - g0);
+      bool merge = arrive(slot_g, in_group);
+      int64_t at = slot_g, stride = p.hkv;
+      int n = in_group;
+      if (merge && nch > kFan) {
+        // merge the group into its first slot, then the groups
+#pragma unroll 1
+        for (int h = 0; h < G; ++h) {
+          float M, den;
+          float4 a;
+          merge_slots(p, slot_g, p.hkv, in_group, G, h, lane, M, den, a);
+          reinterpret_cast<float4*>(p.opart + (slot_g * G + h) * kHeadDim)[lane] = a;
+          __syncwarp();
+          if (lane == 0) p.ml[slot_g * G + h] = make_float2(M, den);
+        }
+        at = static_cast<int64_t>(first_chunk) * p.hkv + pend_head;
+        stride = static_cast<int64_t>(kFan) * p.hkv;
+        n = (nch + kFan - 1) / kFan;
+        merge = arrive(at + p.hkv, n);  // the ticket of chunk 1, which no group uses
+      }
+      if (merge) {
+        uint16_t* orow = p.out + (static_cast<int64_t>(pend_b) * p.hkv + pend_head) * G * kHeadDim;
+#pragma unroll 1
+        for (int h = 0; h < G; ++h) {
+          float M, den;
+          float4 a;
+          merge_slots(p, at, stride, n, G, h, lane, M, den, a);
+          const float inv = den == 0.f ? 0.f : 1.f / den;
+          uint2 v;
+          v.x = Ops::pack(a.x * inv, a.y * inv);
+          v.y = Ops::pack(a.z * inv, a.w * inv);
+          reinterpret_cast<uint2*>(orow + h * kHeadDim)[lane] = v;
+        }
+      }
+    }
+    if (!have) break;
+    if (!(head_flags & kLast)) continue;
+
+    // ---- the item's end: lanes with t == (r & 3) hold dims 32 t + 8 q + 4 (r >> 2) .. + 3, q = 0..3 ----
+    const int b = seq, head = head_flags & 0xffff, nch = chunks >> 16;
+    const int64_t slot = static_cast<int64_t>(sF[b] + b + (chunks & 0xffff)) * p.hkv + head;
     const float back = __fdividef(16777216.f, nu);
+    const int d0 = 32 * t + 4 * (r >> 2);
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      float sum = l[h], z = zs[h];
+      float s0, s1, z0, z1;
+      f32x2_unpack(l2[h], s0, s1);
+      f32x2_unpack(z2[h], z0, z1);
+      float sum = s0 + s1, z = z0 + z1;
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, off);
         z += __shfl_xor_sync(0xffffffffu, z, off);
       }
-      float o[4];
+      const float inv = nch > 1 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+      const float ka = back * inv, kb = ka * 0.0625f;
+      z *= inv;
+      if (t == (r & 3)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int f = (i >> 1), cc = (i & 1) * 2 + (h & 1);
-        float x = acc[h / 2][f][cc];
-        x = t == 1 ? acc[h / 2][2 + f][cc] : x;
-        x = t == 2 ? acc[h / 2][4 + f][cc] : x;
-        x = t == 3 ? acc[h / 2][6 + f][cc] : x;
-        o[i] = fmaf(x, (i & 1) ? back * 0.0625f : back, z);
+        for (int q = 0; q < 4; ++q) {
+          const float o0 = fmaf(acc[h / 2][2 * q][h & 1], ka, z), o1 = fmaf(acc[h / 2][2 * q][2 + (h & 1)], kb, z);
+          const float o2 = fmaf(acc[h / 2][2 * q + 1][h & 1], ka, z), o3 = fmaf(acc[h / 2][2 * q + 1][2 + (h & 1)], kb, z);
+          if (nch > 1) {
+            *reinterpret_cast<float4*>(p.opart + (slot * G + h) * kHeadDim + d0 + 8 * q) = make_float4(o0, o1, o2, o3);
+          } else {
+            uint16_t* orow = p.out + ((static_cast<int64_t>(b) * p.hkv + head) * G + h) * kHeadDim;
+            uint2 v;
+            v.x = Ops::pack(o0, o1);
+            v.y = Ops::pack(o2, o3);
+            *reinterpret_cast<uint2*>(orow + d0 + 8 * q) = v;
+          }
+        }
       }
-      const int d = 32 * t + 4 * r;
-      if (nch == 1) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint2 v;
-        v.x = Ops::pack(o[0] * inv, o[1] * inv);
-        v.y = Ops::pack(o[2] * inv, o[3] * inv);
-        *reinterpret_cast<uint2*>(orow + h * kHeadDim + d) = v;
-      } else {
-        *reinterpret_cast<float4*>(p.opart + (slot * G + h) * kHeadDim + d) = make_float4(o[0], o[1], o[2], o[3]);
-        if (lane == 0) p.ml[slot * G + h] = make_float2(m[h], sum);
-      }
+      if (nch > 1 && lane == 0) p.ml[slot * G + h] = make_float2(m[h], sum);
     }
-    if (nch == 1) continue;
-
-    // ---- merge by the warp that finishes last ----
-    auto arrive = [&](int64_t at, int expected) -> bool {
-      __threadfence();
-      __syncwarp();
-      int last = 0;
-      if (lane == 0) {
-        last = atomicAdd(p.tickets + at, 1) == expected - 1;
-        if (last) p.tickets[at] = 0;  // ready for the next call
-      }
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (last) __threadfence();
-      return last != 0;
-    };
-    const int g0 = c - c % kFan;  // this chunk's group of kFan
-    const int64_t slot_g = static_cast<int64_t>(first_chunk + g0) * p.hkv + head;
-    const int in_group = min(kFan, nch - g0);
-    if (!arrive(slot_g, in_group)) continue;
-    int64_t from = slot_g, stride = p.hkv;
-    int n = in_group;
-    if (nch > kFan) {
-      // merge the group into its first slot, then the groups
-#pragma unroll 1
-      for (int h = 0; h < G; ++h) {
-        float M, den;
-        float4 a;
-        merge_slots(p, slot_g, p.hkv, in_group, G, h, lane, M, den, a);
-        reinterpret_cast<float4*>(p.opart + (slot_g * G + h) * kHeadDim)[lane] = a;
-        __syncwarp();
-        if (lane == 0) p.ml[slot_g * G + h] = make_float2(M, den);
-      }
-      const int groups = (nch + kFan - 1) / kFan;
-      const int64_t slot_0 = static_cast<int64_t>(first_chunk) * p.hkv + head;
-      if (!arrive(slot_0 + p.hkv, groups)) continue;  // the ticket of chunk 1, which no group uses
-      from = slot_0;
-      stride = static_cast<int64_t>(kFan) * p.hkv;
-      n = groups;
-    }
-#pragma unroll 1
-    for (int h = 0; h < G; ++h) {
-      float M, den;
-      float4 a;
-      merge_slots(p, from, stride, n, G, h, lane, M, den, a);
-      const float inv = den == 0.f ? 0.f : 1.f / den;
-      uint2 v;
-      v.x = Ops::pack(a.x * inv, a.y * inv);
-      v.y = Ops::pack(a.z * inv, a.w * inv);
-      reinterpret_cast<uint2*>(orow + h * kHeadDim)[lane] = v;
-    }
+    pending = nch > 1;
+    pend_b = b;
+    pend_head = head;
+    pend_c = chunks;
   }
   // only after a wait that ran out: never leave a copy in flight into this CTA's shared memory
-  for (; done < issued; ++done) mbar_wait(full + 8 * (done % kStages), (done / kStages) & 1, p.err);
+  if (done < issued) {
+    mbar_wait(v_full, done & 1, p.err);
+    for (; done < issued; ++done) mbar_wait(k_full + 8 * (done & 1), (done >> 1) & 1, p.err);
+  }
 
   if (dynamic && lane == 0) {
     // the last warp to take no more items resets the counters for the next call
@@ -705,10 +887,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
 
 template <int G>
 constexpr size_t smem_bytes() {
-  return static_cast<size_t>(kWarps) * kStages * (2 * kUnitBytes + G * kHeadDim * 2 + sizeof(int4) + sizeof(uint64_t)) +
-         (2 * kMaxSeqs + 1 + kWarps) * sizeof(int);
+  return static_cast<size_t>(warps_of(G)) *
+             (3 * kUnitBytes + 2 * G * kHeadDim * 2 + 2 * sizeof(UnitHeader) + 3 * sizeof(uint64_t)) +
+         (3 * kMaxSeqs + 1 + (kClasses + 1) * 32) * sizeof(int);
 }
-static_assert(smem_bytes<4>() <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
+static_assert(smem_bytes<2>() <= 227 * 1024 && smem_bytes<4>() <= 227 * 1024,
+              "shared memory above the 227 KB a CTA can opt into");
 
 template <Elem E, int G>
 cudaError_t launch_typed(const Q4DecodeParams& p, cudaStream_t stream) {
@@ -722,28 +906,28 @@ cudaError_t launch_typed(const Q4DecodeParams& p, cudaStream_t stream) {
     attr_done[dev] = true;
   }
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
-  q4_decode_kernel<E, G><<<sms, kThreads, smem_bytes<G>(), stream>>>(p);
+  q4_decode_kernel<E, G><<<sms, warps_of(G) * 32, smem_bytes<G>(), stream>>>(p);
   return cudaGetLastError();
 }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Most items that a launch over these sizes can have. chunk_units gives one
-// item per planned warp up to x = kMaxChunk units each, chunks of at least 5
-// units for x <= 64 and of kMaxChunk beyond, plus one short chunk per sequence
-// and head; and never more items than units.
-int64_t max_items(int64_t num_seqs, int64_t hkv, int64_t max_ctx) {
+// Most slots for partial results that a launch over these sizes can use: its
+// whole chunks, one short chunk per sequence, times heads. chunk_tokens makes at
+// most one whole chunk per warp up to x = kMaxChunk, chunks of 9 units or more
+// up to x = 128 and of 15 or more beyond; and none shorter than half a unit.
+int64_t max_slots(int64_t num_seqs, int64_t hkv, int64_t group, int64_t max_ctx) {
   const int64_t units = num_seqs * ((max_ctx + kUnit - 1) / kUnit) * hkv;
-  int64_t chunks = int64_t{64} * kPlanWarps / 5 + 1;
-  if (units / kMaxChunk + 1 > chunks) chunks = units / kMaxChunk + 1;
-  chunks += num_seqs * hkv;
-  return units < chunks ? units : chunks;
+  const int64_t halves = num_seqs * (max_ctx / kHalfUnit) * hkv;
+  int64_t chunks = int64_t{128} * 152 * warps_of(static_cast<int>(group)) / 9 + 1;
+  if (units / 15 + 1 > chunks) chunks = units / 15 + 1;
+  return (halves < chunks ? halves : chunks) + num_seqs * hkv;
 }
 
 }  // namespace
 
-// Workspace: two work counters and a ticket per item (zero between calls), then
-// the items' partial outputs and (m, l). Launches of kMaxSeqs sequences follow
+// Workspace: two work counters and a ticket per slot (zero between calls), then
+// the slots' partial outputs and (m, l). Launches of kMaxSeqs sequences follow
 // one another on the stream and share it. The counters' region depends on the
 // size of the workspace alone, so that calls of other sizes on the same
 // workspace find zeros there: 1/128 of it, which holds the tickets (4 bytes) of
@@ -751,7 +935,7 @@ int64_t max_items(int64_t num_seqs, int64_t hkv, int64_t max_ctx) {
 size_t decode_q4_counter_bytes(size_t workspace_bytes) { return 256 + (workspace_bytes / 128 & ~size_t{255}); }
 
 size_t decode_q4_workspace_bytes(int32_t num_seqs, int32_t hkv, int32_t group, int32_t max_ctx) {
-  const int64_t n = max_items(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv, max_ctx);
+  const int64_t n = max_slots(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv, group, max_ctx);
   const size_t partials = static_cast<size_t>(n) * group * (kHeadDim * sizeof(float) + sizeof(float2));
   return align_up((partials + 512) / 127 * 128 + 512, 256);
 }
@@ -776,14 +960,14 @@ cudaError_t launch_decode_q4(const void* q, int64_t q_row_stride, const void* k_
     p.max_ctx = max_ctx;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = static_cast<uint16_t*>(out) + static_cast<int64_t>(b0) * hkv * group * kHeadDim;
-    const int64_t n = max_items(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv, max_ctx);
+    const int64_t n = max_slots(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv, group, max_ctx);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.work = reinterpret_cast<int32_t*>(ws);
     p.tickets = p.work + 2;
     ws += decode_q4_counter_bytes(workspace_bytes);
     p.opart = reinterpret_cast<float*>(ws);
     p.ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(n) * group * kHeadDim * sizeof(float));
-    p.max_items = n;
+    p.max_slots = n;
     if (fused) {
       p.k_new = static_cast<const uint16_t*>(fused->k) + b0 * fused->k_row_stride;
       p.v_new = static_cast<const uint16_t*>(fused->v) + b0 * fused->v_row_stride;

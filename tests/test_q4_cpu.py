@@ -78,36 +78,36 @@ def test_workspace_sizes(lib):
     for hq in (8, 16, 32):
         sizes = [f(n, hq, 8, c) for n, c in ((1, 32), (4, 511), (256, 4096), (512, 4096), (1024, 4096))]
         assert sizes == sorted(sizes) and sizes[0] >= 8 * (hq // 8) * 520
-    # launches of 1024 sequences share it
-    assert f(5000, 16, 8, 4096) == f(1024, 16, 8, 4096)
+    # launches of 768 sequences share it
+    assert f(5000, 16, 8, 4096) == f(768, 16, 8, 4096)
 
 
-def test_workspace_covers_every_item():
-    """The number of items that the chunk rule makes of any context lengths stays within the workspace's bound
-    (both restated here), and the tickets within their share of the bytes."""
+def test_workspace_covers_every_slot():
+    """The slots for partial results that the chunk rule makes of any context lengths stay within the workspace's
+    bound (both restated here), and the tickets within their share of the bytes."""
     import random
-    warps, unit, most = 152 * 12, 32, 8
+    def chunk(halves, units, plan):
+        if halves <= plan:
+            return 32
+        x = -(-units // plan)
+        return 64 * -(-x // -(-x // 16))
 
-    def chunk(units):
-        x = -(-units // warps)
-        return 1 if x <= 1 else -(-x // -(-x // most))
-
-    def bound(n, hkv, ctx):
-        units = n * -(-ctx // unit) * hkv
-        return min(units, max(64 * warps // 5 + 1, units // most + 1) + n * hkv)
+    def bound(n, hkv, ctx, plan):
+        units, halves = n * -(-ctx // 64) * hkv, n * (ctx // 32) * hkv
+        return min(halves, max(128 * plan // 9 + 1, units // 15 + 1)) + n * hkv
 
     rng = random.Random(1)
-    for _ in range(3000):
-        n, hkv = rng.choice([1, 2, 7, 64, 300, 1024]), rng.choice([1, 2, 5, 8, 40])
+    for _ in range(4000):
+        n, hkv = rng.choice([1, 2, 7, 64, 300, 768]), rng.choice([1, 2, 5, 8, 40])
         ctx = int(2 ** rng.uniform(0, 17))
         lens = [rng.randint(0, ctx) if rng.random() < 0.8 else ctx for _ in range(n)]
-        units = [-(-c // unit) for c in lens]
-        c = chunk(sum(units) * hkv)
-        assert 1 <= c <= most
-        items = sum(-(-u // c) for u in units) * hkv
-        assert items <= bound(n, hkv, ctx)
         for group in (1, 2, 4):
-            m = bound(n, hkv, ctx)
+            plan = 152 * (12 if group <= 2 else 8)
+            c = chunk(sum(-(-x // 32) for x in lens) * hkv, sum(-(-x // 64) for x in lens) * hkv, plan)
+            assert c == 32 or (c % 64 == 0 and c <= 1024)
+            m = bound(n, hkv, ctx, plan)
+            assert sum(x // c for x in lens) * hkv + n * hkv <= m
+            assert max(-(-x // c) for x in lens) < 2 ** 15
             size = ((m * group * 520 + 512) // 127 * 128 + 512 + 255) // 256 * 256
             counters = 256 + (size // 128 & ~255)
             assert 8 + 4 * m <= counters and counters + m * group * 520 <= size
