@@ -333,7 +333,7 @@ int pkv_decode_noalloc(const void* q, int64_t q_row_stride, const void* k_cache,
  * fetched, but never reach a result).
  *
  * Supported: head_dim 128, block_size 256, any num_kv_heads up to 8192; for
- * attention 1, 2 or 4 query heads to a kv head (prefill: 16 and 8). The rows
+ * attention 1, 2 or 4 query heads to a kv head (prefill: 2 or 4). The rows
  * (q, k, v, out) are bf16, or fp16 for the *_f16 names; the cache is the same
  * for both. Sizes of 0 are no-ops.
  */
@@ -415,6 +415,33 @@ int pkv_store_decode_q4_f16(const void* q, int64_t q_row_stride, const void* k, 
                             const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                             int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale,
                             void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * pkv_prefill_varlen_q4 -- pkv_prefill_varlen in prefix-cache mode with every
+ * key and value (cached prefix and new tokens, which the caller stores first
+ * on the same stream) taken from the 4-bit cache. The values are rounded to the
+ * element type as pkv_load_kvcache_q4 rounds them, and the arithmetic is
+ * pkv_prefill_varlen's: the result is that of loading the rows and attending to
+ * them contiguously, without the load. A group of V that reads back as NaN
+ * gives NaN in its 32 dims to the rows that may attend to it, and to no others.
+ * Arguments, errors and the optional tile plan in `workspace` are as for
+ * pkv_prefill_varlen. Rows of q and out that belong to no sequence are left
+ * as they were.
+ */
+int pkv_prefill_varlen_q4(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache,
+                          const void* v_cache, int32_t num_blocks, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                          const int32_t* block_tables, int32_t block_table_stride, int32_t num_seqs,
+                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                          float softmax_scale, void* out, const void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+int pkv_prefill_varlen_q4_f16(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache,
+                          const void* v_cache, int32_t num_blocks, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                          const int32_t* block_tables, int32_t block_table_stride, int32_t num_seqs,
+                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                          float softmax_scale, void* out, const void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
 
 /* Workspace bytes pkv_decode_q4, pkv_store_decode_q4 and their _f16 forms need (0 for sizes they refuse). */
 size_t pkv_decode_q4_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,

@@ -80,6 +80,9 @@ for _suffix in ("", "_f16"):
         ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp])
     _SIGNATURES["pkv_load_kvcache_q4" + _suffix] = (
         ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp])
+    _SIGNATURES["pkv_prefill_varlen_q4" + _suffix] = (
+        ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                       _f32, _vp, _vp, _sz, _vp])
     for _op in ("pkv_decode", "pkv_store_decode"):  # the 16-bit calls' arguments
         _SIGNATURES[_op + "_q4" + _suffix] = _SIGNATURES[_op]
 for _name, (_res, _args) in _SIGNATURES.items():
@@ -526,6 +529,48 @@ def pkv_store_decode_q4_f16(q, k, v, slot_mapping, k_cache, v_cache, block_table
     """pkv_store_decode_q4 on fp16 rows; returns fp16."""
     return _decode_q4("pkv_store_decode_q4_f16", torch.float16, q, (k, v, slot_mapping), k_cache, v_cache,
                       block_tables, context_lens, max_context_len, softmax_scale, workspace, out, stream)
+
+
+def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache,
+                v_cache, block_tables, out, plan, stream):
+    _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [total_q, num_heads, 128], k_cache [blocks, num_kv_heads, 16, 1280]")
+    total_q, hq, hkv = q.shape[0], q.shape[1], k_cache.shape[1]
+    _rows(q, "q", hq, dtype)
+    _q4_caches(k_cache, v_cache, hkv)
+    _dev_i32(cu_seqlens_q, "cu_seqlens_q")
+    _dev_i32(cu_seqlens_k, "cu_seqlens_k")
+    _dev_i32(block_tables, "block_tables")
+    num_seqs = cu_seqlens_q.numel() - 1
+    _need(num_seqs >= 0 and cu_seqlens_k.numel() == num_seqs + 1, "cu_seqlens sizes")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] >= num_seqs, "block_tables [num_seqs, width]")
+    if out is None:
+        out = torch.empty((total_q, hq, HEAD_DIM), dtype=dtype, device=q.device)
+    _need(out.is_cuda and out.is_contiguous() and out.shape == (total_q, hq, HEAD_DIM) and out.dtype == dtype,
+          f"out must be contiguous {_TYPE_NAME[dtype]} CUDA [total_q, {hq}, 128]")
+    plan = _plan_arg(plan, None)
+    _here(q, cu_seqlens_q, cu_seqlens_k, k_cache, v_cache, block_tables, out, plan)
+    _check(getattr(_lib, entry)(
+        _ptr(q), _row_stride(q), total_q, _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(cu_seqlens_q),
+        _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], num_seqs,
+        hq, hkv, HEAD_DIM, BLOCK_SIZE, float(softmax_scale), _ptr(out), _ptr(plan),
+        0 if plan is None else plan.numel() * 4, _stream(stream)), entry)
+    return out
+
+
+def pkv_prefill_varlen_q4(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache, v_cache,
+                          block_tables, *, out=None, plan=None, stream=None):
+    """pkv_prefill_varlen in prefix-cache mode over the 4-bit cache (new tokens stored first).
+    q [total_q, num_heads, 128] bf16, 2 or 4 query heads to a kv head; plan: optional tile plan
+    (pkv_prefill_plan). Returns out [total_q, num_heads, 128] bf16."""
+    return _prefill_q4("pkv_prefill_varlen_q4", torch.bfloat16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                       max_seqlen_k, softmax_scale, k_cache, v_cache, block_tables, out, plan, stream)
+
+
+def pkv_prefill_varlen_q4_f16(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache,
+                              v_cache, block_tables, *, out=None, plan=None, stream=None):
+    """pkv_prefill_varlen_q4 with fp16 q; returns fp16."""
+    return _prefill_q4("pkv_prefill_varlen_q4_f16", torch.float16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                       max_seqlen_k, softmax_scale, k_cache, v_cache, block_tables, out, plan, stream)
 
 
 def pkv_build_prefill_metadata(num_cached_tokens, num_scheduled_tokens, block_tables, num_blocks, capacity,

@@ -139,23 +139,39 @@ __device__ __forceinline__ int q4_v_word(int tok, int j, int t) {
 }
 __device__ __forceinline__ int q4_param(int tok, int j) { return kQ4TileParams + tok * kQ4ParamBytes + 4 * j; }
 
-// 8 codes -> 8 values s * c + z, rounded once to the element type (fp16:
-// saturated, since z + 15 s may pass 65504 by half a step of s).
-template <Elem E>
-__device__ __forceinline__ float q4_value(uint32_t code, float s, float z) {
-  float v = fmaf(static_cast<float>(code), s, z);
-  if (E == Elem::kF16) asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(kF16Max));
-  return v;
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
+
+// 8 codes -> 8 values s * c + z, rounded once in fp32 and then to the element
+// type (fp16: saturated, since z + 15 s may pass 65504 by half a step of s).
+// A nibble becomes a float without a conversion: or-ed into 2^23 at its own
+// place it adds c * 2^(4p); 2^23 is taken off again exactly, and s * 2^(-4p)
+// (exact) undoes the shift.
 template <Elem E>
 __device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t param) {
   using Ops = ElemOps<E>;
   const float2 sz = h2_to_f2(param);
+  const uint32_t high = codes >> 16;
+  const uint64_t z2 = f32x2_pack(sz.y, sz.y), off2 = f32x2_pack(-8388608.f, -8388608.f);
+  float v[8];
+  float s = sz.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // dims i and i + 4
+    const uint32_t mask = 0xfu << (4 * i);
+    const uint64_t c2 = f32x2_add(f32x2_pack(__uint_as_float((codes & mask) | 0x4b000000u),
+                                             __uint_as_float((high & mask) | 0x4b000000u)), off2);
+    f32x2_unpack(f32x2_fma(c2, f32x2_pack(s, s), z2), v[i], v[i + 4]);
+    s *= 0.0625f;
+  }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = Ops::pack(q4_value<E>((codes >> (8 * i)) & 15u, sz.x, sz.y),
-                     q4_value<E>((codes >> (8 * i + 4)) & 15u, sz.x, sz.y));
+  for (int i = 0; i < 4; ++i) {
+    w[i] = Ops::pack(v[2 * i], v[2 * i + 1]);
+    if (E == Elem::kF16) w[i] = min2_nan<E>(w[i], 0x7bff7bffu);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -25,6 +25,12 @@ cudaError_t launch_decode_q4(const void* q, int64_t q_row_stride, const void* k_
                              const int32_t* context_lens, int32_t num_seqs, int32_t hkv, int32_t group,
                              int32_t max_ctx, float scale, void* out, void* workspace, size_t workspace_bytes,
                              unsigned int* err, cudaStream_t stream, const FusedStore* fused, Elem elem);
+cudaError_t launch_prefill_q4(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache,
+                              const void* v_cache, int32_t num_blocks, const int32_t* cu_q, const int32_t* cu_k,
+                              int32_t max_seqlen_q, int32_t max_seqlen_k, const int32_t* block_tables,
+                              int32_t bt_stride, int32_t num_seqs, int32_t hq, int32_t hkv, float scale,
+                              const int32_t* items, int32_t num_items, void* out, unsigned int* err,
+                              cudaStream_t stream, Elem elem);
 }  // namespace pkv
 
 namespace {
@@ -134,6 +140,44 @@ int store_decode_common(const void* q, int64_t q_row_stride, const void* k, int6
                        workspace, workspace_bytes, stream, &fused, elem);
 }
 
+int prefill_common(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache, const void* v_cache,
+                   int32_t num_blocks, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t max_seqlen_q,
+                   int32_t max_seqlen_k, const int32_t* block_tables, int32_t block_table_stride, int32_t num_seqs,
+                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   float softmax_scale, void* out, const void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream, pkv::Elem elem) {
+  int st = check_cache_shape(num_kv_heads, head_dim, block_size);
+  if (st == PKV_OK) st = check_heads(num_heads, num_kv_heads);
+  if (st == PKV_OK && num_heads == num_kv_heads) st = PKV_ERR_UNSUPPORTED;  // a CTA takes two heads of one kv head
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || num_seqs > 65535 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || num_blocks < 0 ||
+      block_table_stride < 0)
+    return PKV_ERR_BAD_SIZE;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+  if (!(softmax_scale > 0.f)) return PKV_ERR_BAD_SIZE;
+  if (!q || !out || !cu_seqlens_q || !cu_seqlens_k || !k_cache || !v_cache || !block_tables)
+    return PKV_ERR_NULL_POINTER;
+  if (num_blocks == 0 || block_table_stride == 0) return PKV_ERR_BAD_SIZE;
+  if (q_row_stride < static_cast<int64_t>(num_heads) * head_dim) return PKV_ERR_BAD_STRIDE;
+  if (!aligned(q, 16) || q_row_stride % 8 != 0 || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return PKV_ERR_ALIGNMENT;
+  const int32_t* items = nullptr;
+  int32_t num_items = 0;
+  if (workspace && workspace_bytes > 0) {  // a tile plan (pkv_prefill_plan)
+    if (workspace_bytes % 4 != 0 || workspace_bytes / 4 > (size_t{1} << 28)) return PKV_ERR_BAD_SIZE;
+    if (!aligned(workspace, 4)) return PKV_ERR_ALIGNMENT;
+    items = static_cast<const int32_t*>(workspace);
+    num_items = static_cast<int32_t>(workspace_bytes / 4);
+  }
+  unsigned int* err = nullptr;
+  st = pkv::device_error_word(&err);
+  if (st != PKV_OK) return st;
+  return launched(pkv::launch_prefill_q4(q, q_row_stride, total_q, k_cache, v_cache, num_blocks, cu_seqlens_q,
+                                         cu_seqlens_k, max_seqlen_q, max_seqlen_k, block_tables, block_table_stride,
+                                         num_seqs, num_heads, num_kv_heads, softmax_scale, items, num_items, out, err,
+                                         stream, elem));
+}
+
 }  // namespace
 
 extern "C" {
@@ -218,6 +262,32 @@ int pkv_store_decode_q4_f16(const void* q, int64_t q_row_stride, const void* k, 
                              num_blocks, block_tables, block_table_stride, context_lens, num_seqs, num_heads,
                              num_kv_heads, head_dim, block_size, max_context_len, softmax_scale, out, workspace,
                              workspace_bytes, stream, pkv::Elem::kF16);
+}
+
+int pkv_prefill_varlen_q4(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache,
+                          const void* v_cache, int32_t num_blocks, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                          const int32_t* block_tables, int32_t block_table_stride, int32_t num_seqs,
+                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                          float softmax_scale, void* out, const void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  return prefill_common(q, q_row_stride, total_q, k_cache, v_cache, num_blocks, cu_seqlens_q, cu_seqlens_k,
+                        max_seqlen_q, max_seqlen_k, block_tables, block_table_stride, num_seqs, num_heads,
+                        num_kv_heads, head_dim, block_size, softmax_scale, out, workspace, workspace_bytes, stream,
+                        pkv::Elem::kBF16);
+}
+
+int pkv_prefill_varlen_q4_f16(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache,
+                          const void* v_cache, int32_t num_blocks, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                          const int32_t* block_tables, int32_t block_table_stride, int32_t num_seqs,
+                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                          float softmax_scale, void* out, const void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  return prefill_common(q, q_row_stride, total_q, k_cache, v_cache, num_blocks, cu_seqlens_q, cu_seqlens_k,
+                        max_seqlen_q, max_seqlen_k, block_tables, block_table_stride, num_seqs, num_heads,
+                        num_kv_heads, head_dim, block_size, softmax_scale, out, workspace, workspace_bytes, stream,
+                        pkv::Elem::kF16);
 }
 
 }  // extern "C"

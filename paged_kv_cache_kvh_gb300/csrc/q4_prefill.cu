@@ -1,0 +1,613 @@
+// q4_prefill.cu -- causal variable-length attention on tcgen05 whose keys and
+// values all sit in the 4-bit paged cache.
+//
+// The operation is that of prefill.cu: query row i of sequence b sits at
+// position Lk_b - Lq_b + i and attends to keys 0..that position. A key or value
+// element is s * c + z (q4.cuh) rounded to the element type, exactly what
+// pkv_load_kvcache_q4 returns, and the products, softmax and roundings are
+// those of prefill.cu in the same order: the output has the bits of loading the
+// rows and attending to them contiguously. What it saves is that round trip:
+// 512 bytes written and read again per (token, kv head), for every sequence
+// that shares a prefix.
+//
+// One CTA computes a 128-row query tile of one sequence for two query heads of
+// one kv head, so a K or V tile is widened once for two products:
+//   warp 0        loads the Q tiles by TMA
+//   warp 1        allocates TMEM, one lane issues every tcgen05.mma
+//   warps 4-7     softmax of the first head   (thread = TMEM lane = query row)
+//   warps 8-11    softmax of the second head
+//   warps 12-15   widen K_n, V_n (128 keys x 128 dims) into the 3-slot ring
+// (warps 2, 3 only make up the warpgroup for the register split.) A widening
+// warp takes 32 keys: four batches of 8 keys, 16 bytes of codes a lane, which
+// are 8 dims of each of the 4 groups. A batch's registers are loaded again for
+// the next tile as soon as it is widened, so a tile's loads are in flight while
+// the other batches are converted and the ring slot is waited for. 21
+// instructions widen 8 codes: about 2.7 k warp instructions per key tile beside
+// the 7 k or so of the softmax, in the two products' shadow. Rows past the
+// sequence are written as zeros. So is a group of V that reads back as NaN: in a
+// product it would reach every query row of the tile, masked or not (0 * NaN).
+// The first such position of each group is kept instead, and rows at or past it
+// get NaN in the epilogue.
+// Registers: 512 threads x 128 at launch; the softmax warpgroups take 192 each,
+// the widening one 88, the first 40 (128 * (192 + 192 + 88 + 40) = 65536).
+// TMEM columns, issue order, the lazily moved maximum and the epilogue are as in
+// prefill.cu.
+#include <cuda.h>
+
+#include <climits>
+
+#include "q4.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBN = 128;
+constexpr int kTileBytes = 128 * kHeadDim * 2;  // 32 KB
+constexpr int kHalfBytes = kTileBytes / 2;      // 16 KB: 128 rows x 64 dims
+constexpr int kKvSlots = 3;
+constexpr int kThreads = 512;
+constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
+
+constexpr int kOffQ = 0;                                 // 2 tiles
+constexpr int kOffP = 2 * kTileBytes;                    // 2 tiles
+constexpr int kOffKV = 4 * kTileBytes;                   // kKvSlots tiles
+constexpr int kOffBar = kOffKV + kKvSlots * kTileBytes;  // barriers
+constexpr int kBarQ = 0;
+constexpr int kBarKvFull = 1;                       // +slot, 4 warps
+constexpr int kBarKvFree = kBarKvFull + kKvSlots;   // +slot
+constexpr int kBarSFull = kBarKvFree + kKvSlots;    // +g
+constexpr int kBarPReady = kBarSFull + 2;           // +g, 4 warps
+constexpr int kBarOFinal = kBarPReady + 2;
+constexpr int kBarDrain = kBarOFinal + 1;
+constexpr int kBarStaged = kBarDrain + 1;           // the 8 softmax warps have staged their O rows
+constexpr int kNumBars = kBarStaged + 1;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;    // tmem address, abort flag, first NaN position of V's 4 groups
+constexpr size_t kSmemBytes = kOffMisc + 32 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
+
+struct Q4PrefillParams {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* block_tables;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  int32_t bt_stride;
+  int32_t num_blocks;
+  int32_t num_seqs;
+  int32_t max_q_tiles;
+  int32_t max_seqlen_q;
+  int32_t max_seqlen_k;
+  int32_t total_q;
+  int32_t hq;
+  int32_t hkv;
+  float scale_log2;
+  const int32_t* items;  // optional tile plan: (qt << 16) | b per item; NULL: all pairs
+  uint16_t* out;
+  unsigned int* err;
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                              unsigned int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      flag_error(err, PKV_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_reg_fence8(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <Elem E>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_q4_kernel(const __grid_constant__ CUtensorMap tm_q, const Q4PrefillParams p) {
+  using Ops = ElemOps<E>;
+  extern __shared__ uint8_t smem_raw[];
+  // 1024-byte alignment for the 128-byte-swizzle atoms.
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw_addr);
+  const uint32_t bar0 = sbase + kOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  int* s_nan = reinterpret_cast<int*>(smem + kOffMisc + 8);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // ---- work item: (query tile, sequence, pair of query heads), longest tiles first ----
+  const int pairs = p.hq / 2;
+  int qt, b, pair;
+  {
+    const int cta = static_cast<int>(blockIdx.x);
+    pair = cta % pairs;
+    if (p.items) {
+      const int code = p.items[cta / pairs];
+      qt = code >> 16;
+      b = code & 0xffff;
+    } else {
+      qt = p.max_q_tiles - 1 - cta / pairs / p.num_seqs;
+      b = cta / pairs % p.num_seqs;
+    }
+  }
+  if (b >= p.num_seqs || qt < 0) {  // a plan for other cu_seqlens: skip the item
+    if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+    return;
+  }
+  const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1];
+  const int Lq = cq1 - cq0, Lk = p.cu_k[b + 1] - p.cu_k[b];
+  if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || cq0 < 0 || cq1 > p.total_q ||
+      Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
+    if (threadIdx.x == 0 && qt == 0 && pair == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+    return;
+  }
+  const int r0 = qt * kBM;
+  if (r0 >= Lq) return;
+  const int rows_valid = min(kBM, Lq - r0);
+  const int pos0 = Lk - Lq + r0;  // position of the tile's first query row
+  const int n_tiles = (pos0 + rows_valid - 1) / kBN + 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i == kBarPReady || i == kBarPReady + 1 || (i >= kBarKvFull && i < kBarKvFull + kKvSlots)) count = 4;
+      if (i == kBarStaged) count = 8;
+      mbar_init(bar(i), count);
+    }
+    *s_abort = 0;
+    for (int i = 0; i < 4; ++i) s_nan[i] = INT_MAX;
+    mbar_fence_init();
+    prefetch_tmap(&tm_q);
+    mbar_arrive_expect_tx(bar(kBarQ), 2 * kTileBytes);
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t dst = sbase + kOffQ + g * kTileBytes;
+      tma_load_3d(dst, &tm_q, 0, 2 * pair + g, cq0 + r0, bar(kBarQ));
+      tma_load_3d(dst + kHalfBytes, &tm_q, 64, 2 * pair + g, cq0 + r0, bar(kBarQ));
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp < 4) {
+    regs_dec<40>();
+    if (warp == 0 && lane == 0) mbar_wait(bar(kBarQ), 0, p.err);  // never leave a copy in flight
+    if (warp == 1 && lane == 0) {
+      // =========================== MMA issuer ===========================
+      constexpr uint32_t idesc_s = idesc_f16kind_f32(kBM, kBN, false, false, Ops::kMmaFormat);
+      constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kHeadDim, false, true, Ops::kMmaFormat);
+      bool ok = wait_or_abort(bar(kBarQ), 0, s_abort, p.err);
+      auto slot_of = [](int i) { return i % kKvSlots; };
+      auto par_of = [](int i) { return static_cast<uint32_t>((i / kKvSlots) & 1); };
+      const uint32_t lo_kmaj = desc_lo(sbase, 16), lo_v = desc_lo(sbase, kHalfBytes);
+      auto issue_s = [&](int g, int n) {
+        const uint32_t qa = lo_kmaj + ((kOffQ + g * kTileBytes) >> 4);
+        const uint32_t kbb = lo_kmaj + (kOffKV >> 4) + slot_of(2 * n) * (kTileBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+          mma_f16kind_lo(tmem + g * 128, qa + off, kbb + off, idesc_s, ks > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int g, int n) {
+        const uint32_t pa = lo_kmaj + ((kOffP + g * kTileBytes) >> 4);
+        const uint32_t vbb = lo_v + (kOffKV >> 4) + slot_of(2 * n + 1) * (kTileBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kBN / 16; ++ks) {
+          const uint32_t aoff = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+          mma_f16kind_lo(tmem + 256 + g * 128, pa + aoff, vbb + ((ks * 16 * 128) >> 4), idesc_pv,
+                         (n > 0 || ks > 0) ? 1u : 0u);
+        }
+      };
+      if (ok) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        mma_commit(bar(kBarSFull + 0));
+        issue_s(1, 0);
+        mma_commit(bar(kBarSFull + 1));
+        mma_commit(bar(kBarKvFree + slot_of(0)));
+      }
+      for (int n = 0; ok && n < n_tiles; ++n) {
+        const int iv = 2 * n + 1;
+        if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(iv)), par_of(iv), s_abort, p.err))) break;
+        if (!(ok = wait_or_abort(bar(kBarPReady + 0), n & 1, s_abort, p.err))) break;
+        tc_fence_after();
+        issue_pv(0, n);
+        const bool more = n + 1 < n_tiles;
+        if (more) {
+          if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(2 * n + 2)), par_of(2 * n + 2), s_abort, p.err))) break;
+          tc_fence_after();
+          issue_s(0, n + 1);
+          mma_commit(bar(kBarSFull + 0));
+        }
+        if (!(ok = wait_or_abort(bar(kBarPReady + 1), n & 1, s_abort, p.err))) break;
+        tc_fence_after();
+        issue_pv(1, n);
+        mma_commit(bar(kBarKvFree + slot_of(iv)));
+        if (more) {
+          issue_s(1, n + 1);
+          mma_commit(bar(kBarSFull + 1));
+          mma_commit(bar(kBarKvFree + slot_of(2 * n + 2)));
+        }
+      }
+      mma_commit(bar(kBarOFinal));
+      if (!ok) {
+        // make sure no product is still writing TMEM before it is released
+        mma_commit(bar(kBarDrain));
+        mbar_wait(bar(kBarDrain), 0, p.err);
+      }
+    }
+    if (warp == 1) {
+      // TMEM is released after every softmax warp's last tensor-memory read
+      __syncwarp();
+      mbar_wait(bar(kBarStaged), 0, p.err);
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  } else if (warp >= kWidenWarp0) {
+    // =========================== K/V widening ===========================
+    regs_dec<88>();
+    const int kv_head = 2 * pair / (p.hq / p.hkv);
+    const int row0 = (warp - kWidenWarp0) * 32 + (lane >> 2);  // key of batch 0 within the tile; batch i: + 8 i
+    const int t = lane & 3;
+    const bool odd = (lane >> 2) & 1;
+    auto block_of = [&](int n) -> int {
+      return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + n * kBN / kBlockSize] : -1;
+    };
+    auto checked = [&](int blk) -> int {
+      if (blk >= 0 && blk < p.num_blocks) return blk;
+      flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
+      return -1;
+    };
+    uint4 codes[4], par[4];
+    // ring item i: K_{i/2} (even i) or V_{i/2} (odd i)
+    auto load_batch = [&](int i, int j, int blk) {
+      codes[j] = par[j] = make_uint4(0, 0, 0, 0);
+      const int row = row0 + 8 * j;
+      if (blk < 0 || (i >> 1) * kBN + row >= Lk) return;  // zeros: a scale and a minimum of 0
+      const uint8_t* base = ((i & 1) ? p.v_cache : p.k_cache) +
+                            (static_cast<int64_t>(blk) * p.hkv + kv_head) * kQ4RecordBytes +
+                            ((i >> 1) * kBN % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
+      const int tok = row % kQ4Tile;
+      codes[j] = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + t * 16));
+      par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
+    };
+    int blk = checked(block_of(0)), blk_next = -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_batch(0, j, blk);
+    for (int i = 0; i < 2 * n_tiles; ++i) {
+      const bool is_v = i & 1;
+      if (!is_v) blk_next = block_of((i >> 1) + 1);  // used one item later
+      else if (i + 1 < 2 * n_tiles) blk = checked(blk_next);
+      const int slot = i % kKvSlots;
+      if (i >= kKvSlots &&
+          !__all_sync(0xffffffffu, wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err)))
+        break;
+      const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = row0 + 8 * j;
+        uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
+        uint32_t sz[4] = {par[j].x, par[j].y, par[j].z, par[j].w};
+        int tt = t;
+        if (is_v) {
+          // two 8-byte chunks of V: per group, the 4 dims of the first and then of the second
+          const uint4 c = codes[j];
+          w[0] = __byte_perm(c.x, c.z, 0x5410);
+          w[1] = __byte_perm(c.x, c.z, 0x7632);
+          w[2] = __byte_perm(c.y, c.w, 0x5410);
+          w[3] = __byte_perm(c.y, c.w, 0x7632);
+          tt = t ^ ((row & 4) >> 1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((sz[k] & 0x7fffu) > 0x7c00u) {  // a NaN scale
+              atomicMin(s_nan + k, (i >> 1) * kBN + row);
+              sz[k] = 0u;
+            }
+        }
+        if (i + 1 < 2 * n_tiles) load_batch(i + 1, j, blk);
+        // odd rows take the groups in another order, so that the 8 lanes of a
+        // store phase (two rows, four chunks each) hit all banks
+        const uint32_t wa = odd ? w[1] : w[0], wb = odd ? w[0] : w[1], wc = odd ? w[3] : w[2], wd = odd ? w[2] : w[3];
+        const uint32_t pa = odd ? sz[1] : sz[0], pb = odd ? sz[0] : sz[1];
+        const uint32_t pc = odd ? sz[3] : sz[2], pd = odd ? sz[2] : sz[3];
+        const uint32_t at = dst + row * 128;
+        const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
+        auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
+          const uint4 v = dequantise8<E>(codes8, param);
+          sts128(at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+        };
+        put(wa, pa, 0, ca);
+        put(wb, pb, 0, cb);
+        put(wc, pc, 1, ca);
+        put(wd, pd, 1, cb);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarKvFull + slot));
+    }
+  } else {
+    // =========================== softmax groups ===========================
+    regs_inc<192>();
+    const int g = (warp - kSoftmaxWarp0) >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;  // query row within the tile == TMEM lane
+    const int pos = pos0 + row;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_base + g * 128;
+    const uint32_t tO = tmem + lane_base + 256 + g * 128;
+    const uint32_t prow = sbase + kOffP + g * kTileBytes + row * 128;
+    const int swz = row & 7;
+    const float sl2 = p.scale_log2;
+    float m = -INFINITY;  // running max, log2 units (scaled)
+    float l = 0.f;
+    bool ok = true;
+    for (int n = 0; n < n_tiles; ++n) {
+      ok = wait_or_abort(bar(kBarSFull + g), n & 1, s_abort, p.err);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float s[128];
+      {
+        uint32_t r0_[32], r1[32], r2[32], r3[32];
+        tmem_ld32(tS + 0, r0_);
+        tmem_ld32(tS + 32, r1);
+        tmem_ld32(tS + 64, r2);
+        tmem_ld32(tS + 96, r3);
+        tmem_wait_ld();
+        tmem_reg_fence(r0_);
+        tmem_reg_fence(r1);
+        tmem_reg_fence(r2);
+        tmem_reg_fence(r3);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          s[j] = __uint_as_float(r0_[j]);
+          s[32 + j] = __uint_as_float(r1[j]);
+          s[64 + j] = __uint_as_float(r2[j]);
+          s[96 + j] = __uint_as_float(r3[j]);
+        }
+      }
+      const int key0 = n * kBN;
+      if (key0 + kBN - 1 > pos0 || key0 + kBN > Lk) {
+        const int lim = min(pos, Lk - 1) - key0;  // keys j <= lim are visible
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+          if (j > lim) s[j] = -INFINITY;
+      }
+      float ma = s[0], mb = s[1];
+#pragma unroll
+      for (int j = 2; j < 126; j += 4) {
+        ma = fmax3(ma, s[j], s[j + 1]);
+        mb = fmax3(mb, s[j + 2], s[j + 3]);
+      }
+      float mx = fmaxf(fmax3(ma, s[126], s[127]), mb);
+      mx *= sl2;
+      float m_use = m;
+      if (mx > m + 8.0f) m_use = mx;  // move the max only when it grows by > 2^8
+      const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_use);
+      l *= alpha;
+      const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
+      const uint64_t negm2 = f32x2_pack(-m_use, -m_use);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+#pragma unroll
+        for (int j = c * 8; j < c * 8 + 8; j += 2) {
+          float a0, a1;
+          f32x2_unpack(f32x2_fma(f32x2_pack(s[j], s[j + 1]), sl2x2, negm2), a0, a1);
+          s[j] = ex2_approx(a0);
+          s[j + 1] = ex2_approx(a1);
+        }
+        const int half = c >> 3;
+        const uint32_t addr = prow + half * kHalfBytes + (((c & 7) ^ swz) << 4);
+        const float* e = s + c * 8;
+        sts128(addr, Ops::pack(e[0], e[1]), Ops::pack(e[2], e[3]), Ops::pack(e[4], e[5]), Ops::pack(e[6], e[7]));
+      }
+      m = m_use;
+      // rescale the running output (PV_g(n-1) is complete: S_g(n) was issued after it)
+      if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+        for (int c = 0; c < 16; ++c) {
+          uint32_t r[8];
+          tmem_ld8(tO + c * 8, r);
+          tmem_wait_ld();
+          tmem_reg_fence8(r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+          tmem_st8(tO + c * 8, r);
+        }
+        tmem_wait_st();
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarPReady + g));
+      // The row sum is not needed for P: add it up after P is handed over.
+      {
+        uint64_t acc[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) acc[a] = f32x2_pack(s[2 * a], s[2 * a + 1]);
+#pragma unroll
+        for (int j = 8; j < 128; j += 8)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) acc[a] = f32x2_add(acc[a], f32x2_pack(s[j + 2 * a], s[j + 2 * a + 1]));
+        float t0, t1, t2, t3, t4, t5, t6, t7;
+        f32x2_unpack(acc[0], t0, t1);
+        f32x2_unpack(acc[1], t2, t3);
+        f32x2_unpack(acc[2], t4, t5);
+        f32x2_unpack(acc[3], t6, t7);
+        l += ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
+      }
+    }
+    if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), 0, s_abort, p.err));
+    // Epilogue: O is staged in the two P buffers (both heads of a query row side
+    // by side, 512 B, 16-byte chunks rotated by the row), then leaves as whole rows.
+    const uint32_t stage = sbase + kOffP;
+    if (ok) {
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // group c of 32 dims
+        uint32_t r[32];
+        tmem_ld32(tO + c * 32, r);
+        tmem_wait_ld();
+        tmem_reg_fence(r);
+        if (pos >= s_nan[c]) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0x7fffffffu;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          const int q = g * 16 + c * 4 + j / 8;  // 16-byte chunk of the 512-byte row
+          sts128(stage + row * 512 + ((q ^ (row & 31)) << 4),
+                 Ops::pack(__uint_as_float(r[j + 0]) * inv, __uint_as_float(r[j + 1]) * inv),
+                 Ops::pack(__uint_as_float(r[j + 2]) * inv, __uint_as_float(r[j + 3]) * inv),
+                 Ops::pack(__uint_as_float(r[j + 4]) * inv, __uint_as_float(r[j + 5]) * inv),
+                 Ops::pack(__uint_as_float(r[j + 6]) * inv, __uint_as_float(r[j + 7]) * inv));
+        }
+      }
+    }
+    // all 8 softmax warps arrive, whatever happened, so the waits on it always end
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarStaged));
+    const bool staged = __all_sync(0xffffffffu, wait_or_abort(bar(kBarStaged), 0, s_abort, p.err));
+    if (ok && staged) {
+      uint16_t* obase = p.out + (static_cast<int64_t>(cq0 + r0) * p.hq + 2 * pair) * kHeadDim + lane * 8;
+      for (int rr = warp - kSoftmaxWarp0; rr < rows_valid; rr += 8) {
+        uint32_t a, b2, c2, d;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a), "=r"(b2), "=r"(c2), "=r"(d)
+                     : "r"(stage + rr * 512 + ((lane ^ (rr & 31)) << 4)));
+        *reinterpret_cast<uint4*>(obase + static_cast<int64_t>(rr) * p.hq * kHeadDim) = make_uint4(a, b2, c2, d);
+      }
+    }
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  }
+  return fn;
+}
+
+// [rows, heads, 128] view of q, rows row_stride elements apart; box = 128 rows x 1 head x 64 dims.
+bool encode_q(CUtensorMap* tm, const void* base, int64_t rows, int heads, int64_t row_stride, Elem elem) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim * 2), static_cast<cuuint64_t>(row_stride * 2)};
+  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = elem == Elem::kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(tm, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Elem E>
+cudaError_t launch_typed(const CUtensorMap& tq, const Q4PrefillParams& p, unsigned nblocks, cudaStream_t stream) {
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(prefill_q4_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  prefill_q4_kernel<E><<<nblocks, kThreads, kSmemBytes, stream>>>(tq, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_q4(const void* q, int64_t q_row_stride, int32_t total_q, const void* k_cache,
+                              const void* v_cache, int32_t num_blocks, const int32_t* cu_q, const int32_t* cu_k,
+                              int32_t max_seqlen_q, int32_t max_seqlen_k, const int32_t* block_tables,
+                              int32_t bt_stride, int32_t num_seqs, int32_t hq, int32_t hkv, float scale,
+                              const int32_t* items, int32_t num_items, void* out, unsigned int* err,
+                              cudaStream_t stream, Elem elem) {
+  CUtensorMap tq;
+  if (!encode_q(&tq, q, total_q, hq, q_row_stride, elem)) return cudaErrorInvalidValue;
+  Q4PrefillParams p;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.block_tables = block_tables;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.bt_stride = bt_stride;
+  p.num_blocks = num_blocks;
+  p.num_seqs = num_seqs;
+  p.max_q_tiles = (max_seqlen_q + kBM - 1) / kBM;
+  p.max_seqlen_q = max_seqlen_q;
+  p.max_seqlen_k = max_seqlen_k;
+  p.total_q = total_q;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.items = num_items > 0 ? items : nullptr;
+  p.out = static_cast<uint16_t*>(out);
+  p.err = err;
+  const int64_t pairs = hq / 2;
+  const int64_t nblocks = p.items ? num_items * pairs : static_cast<int64_t>(p.max_q_tiles) * num_seqs * pairs;
+  if (nblocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned nb = static_cast<unsigned>(nblocks);
+  return elem == Elem::kF16 ? launch_typed<Elem::kF16>(tq, p, nb, stream)
+                            : launch_typed<Elem::kBF16>(tq, p, nb, stream);
+}
+
+}  // namespace pkv

@@ -1,0 +1,190 @@
+"""Prefill over the 4-bit cache: against attention in 64 bits over the values read
+back, and bit for bit against loading the rows and running the 16-bit prefill."""
+import numpy as np
+import pytest
+import torch
+
+import q4_reference as R
+import workloads as W
+from test_gpu_q4_decode import Case
+
+pytestmark = pytest.mark.gpu
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_kv_cache_kvh_gb300 as m
+    m.pkv_device_error(clear=True)
+    return m
+
+
+class Prefill(Case):
+    """Sequences of lk tokens of which the last lq are queries."""
+
+    def __init__(self, pkv, lq, lk, hq, hkv, dtype, seed=0, extra_rows=0, rows=None):
+        super().__init__(pkv, lk, hq, hkv, dtype, seed, rows)
+        gen = W.make_generator(seed + 1000, "cuda")
+        self.lq, self.total = lq, sum(lq)
+        self.cq = np.concatenate(([0], np.cumsum(lq))).astype(np.int32)
+        self.ck = np.concatenate(([0], np.cumsum(lk))).astype(np.int32)
+        qkv = W.normal((self.total + extra_rows, (hq + 2 * hkv) * 128), gen, "cuda", dtype)
+        self.q = qkv[:, :hq * 128].unflatten(1, (hq, 128))
+        self.d_cq, self.d_ck = torch.from_numpy(self.cq).cuda(), torch.from_numpy(self.ck).cuda()
+
+    def prefill(self, **kw):
+        return self.f("pkv_prefill_varlen_q4")(self.q, self.d_cq, self.d_ck, max(self.lq), max(self.lens), self.scale,
+                                               self.kc, self.vc, self.tables, **kw)
+
+    def check(self, out, only=None):
+        assert self.pkv.pkv_device_error() == 0
+        half = torch.finfo(self.dtype).eps / 2
+        for b, n in enumerate(self.lens):
+            if self.lq[b] == 0 or (only is not None and b not in only):
+                continue
+            a, e = self.first[b], self.first[b + 1]
+            k, v = R.dequantised(self.k[a:e]).to(self.dtype), R.dequantised(self.v[a:e]).to(self.dtype)
+            q = self.q[self.cq[b]:self.cq[b + 1]]
+            ref = R.attention(q, k, v, n - self.lq[b], self.scale)
+            # k and v as the products read them; p is rounded to the type (half of it relative to each weight), the
+            # logits' fp32 sums are off by 2^-20 of their magnitude, the result is rounded once
+            big = float(v.double().abs().amax())
+            s = float((q.double().abs().amax((0, 1)) * k.double().abs().amax((0, 1))).sum()) * self.scale
+            tol = half * (ref.abs() + big) + big * 2.0 ** -20 * (2 + s)
+            err = (out[self.cq[b]:self.cq[b + 1]].double() - ref).abs()
+            assert bool((err <= tol).all()), f"sequence {b} ({self.lq[b]} of {n}): {float((err / tol).max()):.2f} of the bound"
+
+
+SHAPES = [
+    ([1], [1]), ([1], [129]), ([128], [128]), ([129, 1, 127], [129, 300, 383]), ([5, 200, 33], [5, 429, 256]),
+    ([255, 257, 1, 64], [255, 513, 1024, 64]), ([0, 40, 0], [0, 40, 700]), ([700], [3000])]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lq,lk", SHAPES)
+def test_against_64_bits(pkv, lq, lk, dtype):
+    c = Prefill(pkv, lq, lk, 16, 8, dtype, seed=sum(lk)).fill()
+    c.check(c.prefill())
+
+
+@pytest.mark.parametrize("hq,hkv,dtype", [(2, 1, BF16), (32, 8, BF16), (12, 3, F16), (6, 3, F16)])
+def test_head_layouts(pkv, hq, hkv, dtype):
+    c = Prefill(pkv, [200, 130], [450, 130], hq, hkv, dtype, seed=hq).fill()
+    c.check(c.prefill())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_bits_of_load_then_prefill(pkv, dtype):
+    """The same bits as pkv_load_kvcache_q4 followed by the contiguous 16-bit prefill; with a tile plan too."""
+    c = Prefill(pkv, [300, 1, 129, 513], [1324, 700, 129, 2048], 16, 8, dtype, seed=21).fill()
+    k, v = c.f("pkv_load_kvcache_q4")(c.kc, c.vc, c.slots)
+    want = c.f("pkv_prefill_varlen")(c.q, c.d_cq, c.d_ck, max(c.lq), max(c.lens), c.scale, k=k, v=v)
+    assert torch.equal(c.prefill(), want)
+    plan = pkv.pkv_prefill_plan(c.cq, c.ck)
+    assert torch.equal(c.prefill(plan=plan), want)
+
+
+def test_shared_prefix_blocks(pkv):
+    """Sequences that read the same physical blocks for their prefix."""
+    c = Prefill(pkv, [60, 100, 200], [572, 612, 712], 16, 8, BF16, seed=22)
+    c.tables[1:, :2] = c.tables[0, :2]
+    for b in (1, 2):
+        c.k[c.first[b]:c.first[b] + 512] = c.k[:512]
+        c.v[c.first[b]:c.first[b] + 512] = c.v[:512]
+    t = c.tables.cpu().numpy()
+    p = [np.arange(n) for n in c.lens]
+    slots = np.concatenate([t[b, x // 256] * 256 + x % 256 for b, x in enumerate(p)]).astype(np.int32)
+    for b in (1, 2):
+        slots[c.first[b]:c.first[b] + 512] = -1       # stored once, by the first sequence
+    c.slots = torch.from_numpy(slots).cuda()
+    c.fill()
+    c.check(c.prefill())
+
+
+def test_rows_behind_the_last_sequence_stay(pkv):
+    c = Prefill(pkv, [40, 100], [40, 300], 16, 8, BF16, seed=23, extra_rows=37).fill()
+    out = torch.full((c.total + 37, 16, 128), 5.0, dtype=BF16, device="cuda")
+    assert c.prefill(out=out) is out
+    c.check(out)
+    assert bool((out[c.total:] == 5).all())
+
+
+def test_nan_values_stay_behind_the_mask(pkv):
+    """A NaN in V or K at a position reaches the rows that may attend to it, and only its group (V)."""
+    c = Prefill(pkv, [200, 50], [330, 50], 16, 8, BF16, seed=24)
+    c.v[300, 2, 40] = float("nan")                     # query rows 170.. of sequence 0, kv head 2, group 1
+    c.k[310, 5, 0] = float("inf")                      # rows 180.., kv head 5: everything
+    out = c.fill().prefill()
+    assert c.pkv.pkv_device_error() == 0
+    want = torch.zeros((250, 16, 128), dtype=torch.bool, device="cuda")
+    want[170:200, 4:6, 32:64] = True
+    want[180:200, 10:12] = True
+    assert torch.equal(torch.isnan(out), want)
+    c.check(out, {1})
+
+
+def test_bad_blocks_and_lengths_are_reported(pkv):
+    c = Prefill(pkv, [100, 100], [400, 400], 16, 8, BF16, seed=25).fill()
+    good = c.tables.clone()
+    c.tables[0, 1] = -7
+    out = c.prefill()
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_BLOCK
+    c.tables.copy_(good)
+    c.check(out, {1})
+    c.d_ck[2] = 450                                    # sequence 1: 50 keys for 100 query rows
+    out = c.prefill()
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_SEQLEN
+    c.d_ck[2] = 800
+    c.check(c.prefill())
+    plan = torch.tensor([(0 << 16) | 9], dtype=torch.int32, device="cuda")      # a sequence that is not there
+    c.prefill(plan=plan)
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_SEQLEN
+
+
+def test_store_prefill_decode_run(pkv):
+    """The calls together as an engine makes them: two chunks of a prompt stored and attended to, then decode steps
+    in a captured graph, over one 4-bit cache; every output against 64 bits over the values it stands for."""
+    n0, n1, steps = 300, 229, 6
+    c = Prefill(pkv, [n0], [n0 + n1 + steps], 16, 8, BF16, seed=26)
+    total = n0 + n1
+    kv = lambda a, b: (c.k[a:b], c.v[a:b], c.kc, c.vc, c.slots[a:b])  # noqa: E731
+    q = W.normal_bf16((total + steps, 16, 128), W.make_generator(27, "cuda"), "cuda")
+    kd, vd = R.dequantised(c.k), R.dequantised(c.v)
+    half = torch.finfo(BF16).eps / 2
+
+    def near(out, rows, first, rounding):
+        ref = R.attention(q[rows], kd[:first + out.shape[0]], vd[:first + out.shape[0]], first, c.scale)
+        big = float(vd.abs().amax())
+        err = (out.double() - ref).abs()
+        assert bool((err <= half * ref.abs() + big * rounding).all()), float(err.max())
+
+    for a, b in ((0, n0), (n0, total)):
+        pkv.pkv_store_kvcache_q4(*kv(a, b))
+        cq, ck = torch.tensor([0, b - a], dtype=torch.int32), torch.tensor([0, b], dtype=torch.int32)
+        out = pkv.pkv_prefill_varlen_q4(q[a:b], cq.cuda(), ck.cuda(), b - a, b, c.scale, c.kc, c.vc, c.tables)
+        # k, v and p each rounded to bf16 (k moves a logit by half a step of the sum of its magnitudes, below 16 here)
+        near(out, slice(a, b), a, half * (2 + 2 * 16) + 2.0 ** -16)
+    qb, kb, vb = (torch.zeros((2, h, 128), dtype=BF16, device="cuda") for h in (16, 8, 8))
+    slot = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    ctx = torch.zeros(2, dtype=torch.int32, device="cuda")
+    tables = torch.cat((c.tables, torch.full_like(c.tables, -1)))
+    ws = pkv.decode_q4_workspace(2, 4096)
+    out = torch.empty((2, 16, 128), dtype=BF16, device="cuda")
+
+    def step():
+        pkv.pkv_store_decode_q4(qb, kb, vb, slot, c.kc, c.vc, tables, ctx, 4096, c.scale, ws, out=out)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(total, total + steps):
+        qb[0], kb[0], vb[0] = q[i], c.k[i], c.v[i]
+        slot[0], ctx[0] = c.slots[i], i + 1
+        g.replay()
+        near(out[:1], slice(i, i + 1), i, 2.0 ** -11 + 2.0 ** -14)
+        assert not bool(out[1].any())
+    assert pkv.pkv_device_error() == 0

@@ -71,6 +71,25 @@ def test_decode_refusals(lib, suffix):
     assert s(k=ODD) == s(v=ODD) == s(ks=1028) == s(vs=1028) == -4
 
 
+@pytest.mark.parametrize("suffix", ["", "_f16"])
+def test_prefill_refusals(lib, suffix):
+    pre = getattr(lib, "pkv_prefill_varlen_q4" + suffix)
+
+    def f(q=ONE, qs=2048, tq=10, kc=ONE, vc=ONE, nb=4, cq=ONE, ck=ONE, mq=10, mk=10, bt=ONE, bs=2, n=1, hq=16, hkv=8,
+          d=128, blk=256, sc=0.1, out=ONE, ws=None, wb=0):
+        return pre(q, qs, tq, kc, vc, nb, cq, ck, mq, mk, bt, bs, n, hq, hkv, d, blk, sc, out, ws, wb, None)
+
+    assert f(d=96) == f(blk=16) == f(hq=8) == f(hq=24, qs=4096) == f(hq=64, qs=8192) == f(hkv=0) == -2
+    assert f(tq=-1) == f(nb=-1) == f(mq=-1) == f(mk=-1) == f(bs=-1) == f(n=-1) == f(n=65536) == -6
+    assert f(sc=0.0) == f(sc=float("nan")) == f(nb=0) == f(bs=0) == -6
+    for name in ("q", "kc", "vc", "cq", "ck", "bt", "out"):
+        assert f(**{name: None}) == -1
+    assert f(qs=2047) == -3
+    assert f(q=ODD) == f(qs=2052) == f(kc=ODD) == f(vc=ODD) == f(out=ODD) == f(ws=ctypes.c_void_p(18), wb=4) == -4
+    assert f(ws=ONE, wb=6) == -6
+    assert f(n=0, q=None) == f(tq=0, q=None) == f(mq=0, q=None) == 0
+
+
 def test_workspace_sizes(lib):
     f = lib.pkv_decode_q4_workspace_bytes
     assert f(0, 16, 8, 4096) == f(4, 24, 8, 4096) == f(4, 16, 8, -1) == f(65536, 16, 8, 10) == f(1, 3, 2, 10) == 0
