@@ -145,34 +145,77 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 8 codes -> 8 values s * c + z, rounded once in fp32 and then to the element
-// type (fp16: saturated, since z + 15 s may pass 65504 by half a step of s).
-// A nibble becomes a float without a conversion: or-ed into 2^23 at its own
-// place it adds c * 2^(4p); 2^23 is taken off again exactly, and s * 2^(-4p)
-// (exact) undoes the shift.
-template <Elem E>
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// 8 codes -> 8 values s * c + z of the element type (dim p from bits 4p..4p+3).
+//
+// fp16: one fma.f16x2 per pair, so each value is s * c + z rounded once;
+// saturated, since z + 15 s may pass 65504 by half a step of s. A nibble
+// becomes a half by or-ing it into 1024, where it adds c (or 16 c).
+//
+// bf16: s * c + z in fp32, then rounded to bf16. kScaled values are 2^-64 times
+// those (exactly, in bf16): the nibbles, and-ed out in place, are then used as
+// they stand, as the fp32 subnormals c * 2^(4p - 149), with s * 2^(85 - 4p) as
+// the factor (s < 2^16). Unscaled, that factor would overflow, so there a nibble
+// is or-ed into 2^23 first and 2^23 taken off again.
+template <Elem E, bool kScaled = false>
 __device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t param) {
   using Ops = ElemOps<E>;
-  const float2 sz = h2_to_f2(param);
-  const uint32_t high = codes >> 16;
-  const uint64_t z2 = f32x2_pack(sz.y, sz.y), off2 = f32x2_pack(-8388608.f, -8388608.f);
-  float v[8];
-  float s = sz.x;
+  if constexpr (E == Elem::kF16) {
+    const uint32_t s2 = __byte_perm(param, param, 0x1010), z2 = __byte_perm(param, param, 0x3232);
+    const uint32_t high = codes >> 8;
+    uint32_t v[4];  // dims (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {  // dims i and i + 4
-    const uint32_t mask = 0xfu << (4 * i);
-    const uint64_t c2 = f32x2_add(f32x2_pack(__uint_as_float((codes & mask) | 0x4b000000u),
-                                             __uint_as_float((high & mask) | 0x4b000000u)), off2);
-    f32x2_unpack(f32x2_fma(c2, f32x2_pack(s, s), z2), v[i], v[i + 4]);
-    s *= 0.0625f;
-  }
-  uint32_t w[4];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? codes : high;
+      const uint32_t n = (i & 1) ? hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd400d400u)   // / 16 - 64
+                                 : hfma2(and_or(w, 0x000f000fu, 0x64006400u), 0x3c003c00u, 0xe400e400u);  // - 1024
+      v[i] = min2_nan<E>(hfma2(n, s2, z2), 0x7bff7bffu);
+    }
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                      __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+  } else {
+    const float2 sz = h2_to_f2(param);
+    const uint32_t high = codes >> 16;
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = Ops::pack(v[2 * i], v[2 * i + 1]);
-    if (E == Elem::kF16) w[i] = min2_nan<E>(w[i], 0x7bff7bffu);
+    for (int i = 0; i < 2; ++i) {  // dims 2i, 2i + 1 and 2i + 4, 2i + 5
+      const uint32_t m0 = 0xfu << (8 * i), m1 = 0xf0u << (8 * i);
+      uint64_t lo, hi, f2, z2;
+      if (kScaled) {
+        // 2^(85 - 4p) of p = 2i and 2i + 1; 2^-64
+        f2 = f32x2_pack(sz.x * __uint_as_float((127u + 85u - 8u * i) << 23),
+                        sz.x * __uint_as_float((127u + 81u - 8u * i) << 23));
+        const float z = sz.y * __uint_as_float((127u - 64u) << 23);
+        z2 = f32x2_pack(z, z);
+        lo = f32x2_pack(__uint_as_float(codes & m0), __uint_as_float(codes & m1));
+        hi = f32x2_pack(__uint_as_float(high & m0), __uint_as_float(high & m1));
+      } else {
+        f2 = f32x2_pack(sz.x * __uint_as_float((127u - 8u * i) << 23), sz.x * __uint_as_float((123u - 8u * i) << 23));
+        z2 = f32x2_pack(sz.y, sz.y);
+        const uint64_t off2 = f32x2_pack(-8388608.f, -8388608.f);
+        lo = f32x2_add(f32x2_pack(__uint_as_float(and_or(codes, m0, 0x4b000000u)),
+                                  __uint_as_float(and_or(codes, m1, 0x4b000000u))), off2);
+        hi = f32x2_add(f32x2_pack(__uint_as_float(and_or(high, m0, 0x4b000000u)),
+                                  __uint_as_float(and_or(high, m1, 0x4b000000u))), off2);
+      }
+      float a, b;
+      f32x2_unpack(f32x2_fma(lo, f2, z2), a, b);
+      w[i] = Ops::pack(a, b);
+      f32x2_unpack(f32x2_fma(hi, f2, z2), a, b);
+      w[2 + i] = Ops::pack(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace pkv

@@ -28,8 +28,8 @@
 // product it would reach every query row of the tile, masked or not (0 * NaN).
 // The first such position of each group is kept instead, and rows at or past it
 // get NaN in the epilogue.
-// Registers: 512 threads x 128 at launch; the softmax warpgroups take 192 each,
-// the widening one 88, the first 40 (128 * (192 + 192 + 88 + 40) = 65536).
+// Registers: 512 threads x 128 at launch, split over the warpgroups by what each
+// needs without spilling (shared memory leaves no L1 for local memory).
 // TMEM columns, issue order, the lazily moved maximum and the epilogue are as in
 // prefill.cu.
 #include <cuda.h>
@@ -46,13 +46,17 @@ constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kTileBytes = 128 * kHeadDim * 2;  // 32 KB
 constexpr int kHalfBytes = kTileBytes / 2;      // 16 KB: 128 rows x 64 dims
-constexpr int kKvSlots = 3;
-constexpr int kThreads = 512;
+constexpr int kKvSlots = 5;
+constexpr int kThreads = 640;
+constexpr int kWidenWarps = 8;
 constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
 
-constexpr int kOffQ = 0;                                 // 2 tiles
-constexpr int kOffP = 2 * kTileBytes;                    // 2 tiles
-constexpr int kOffKV = 4 * kTileBytes;                   // kKvSlots tiles
+// Registers per thread: 128 * (sum over the four warpgroups) is what the launch holds.
+constexpr int kRegsFirst = 48, kRegsSoftmax = 152, kRegsWiden = 64;
+static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
+
+constexpr int kOffQ = 0;                                 // 2 tiles (and O staging in the epilogue)
+constexpr int kOffKV = 2 * kTileBytes;                   // kKvSlots tiles
 constexpr int kOffBar = kOffKV + kKvSlots * kTileBytes;  // barriers
 constexpr int kBarQ = 0;
 constexpr int kBarKvFull = 1;                       // +slot, 4 warps
@@ -88,13 +92,26 @@ struct Q4PrefillParams {
   unsigned int* err;
 };
 
+// mbarrier test that may sleep for up to a microsecond: 18 warps poll here, and
+// their polls would take issue slots from the softmax and widening warps.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait that also gives up as soon as another role of the CTA has aborted.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                               unsigned int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait_long(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+      if (mbar_try_wait_long(bar, parity)) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       flag_error(err, PKV_DEVERR_TIMEOUT);
@@ -122,6 +139,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16: A's row i in TMEM lane i, two
+// 16-bit elements to a column.
+__device__ __forceinline__ void mma_f16kind_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
+      : "memory");
+}
+// Keeps what is computed from x where it stands: the issuing thread has few
+// registers, and every product's operand addresses would be kept in one otherwise.
+__device__ __forceinline__ void opaque(uint32_t& x) { asm volatile("" : "+r"(x)); }
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -183,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
-      if (i == kBarPReady || i == kBarPReady + 1 || (i >= kBarKvFull && i < kBarKvFull + kKvSlots)) count = 4;
+      if (i == kBarPReady || i == kBarPReady + 1 || (i >= kBarKvFull && i < kBarKvFull + kKvSlots)) count = i >= kBarKvFull && i < kBarKvFull + kKvSlots ? kWidenWarps : 4;
       if (i == kBarStaged) count = 8;
       mbar_init(bar(i), count);
     }
@@ -209,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s_tmem;
 
   if (warp < 4) {
-    regs_dec<40>();
+    regs_dec<kRegsFirst>();
     if (warp == 0 && lane == 0) mbar_wait(bar(kBarQ), 0, p.err);  // never leave a copy in flight
     if (warp == 1 && lane == 0) {
       // =========================== MMA issuer ===========================
@@ -220,8 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto par_of = [](int i) { return static_cast<uint32_t>((i / kKvSlots) & 1); };
       const uint32_t lo_kmaj = desc_lo(sbase, 16), lo_v = desc_lo(sbase, kHalfBytes);
       auto issue_s = [&](int g, int n) {
-        const uint32_t qa = lo_kmaj + ((kOffQ + g * kTileBytes) >> 4);
+        uint32_t qa = lo_kmaj + ((kOffQ + g * kTileBytes) >> 4);
         const uint32_t kbb = lo_kmaj + (kOffKV >> 4) + slot_of(2 * n) * (kTileBytes >> 4);
+        opaque(qa);
 #pragma unroll
         for (int ks = 0; ks < kHeadDim / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
@@ -229,14 +260,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto issue_pv = [&](int g, int n) {
-        const uint32_t pa = lo_kmaj + ((kOffP + g * kTileBytes) >> 4);
         const uint32_t vbb = lo_v + (kOffKV >> 4) + slot_of(2 * n + 1) * (kTileBytes >> 4);
+        uint32_t pa = tmem + g * 128;
+        opaque(pa);
 #pragma unroll
-        for (int ks = 0; ks < kBN / 16; ++ks) {
-          const uint32_t aoff = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-          mma_f16kind_lo(tmem + 256 + g * 128, pa + aoff, vbb + ((ks * 16 * 128) >> 4), idesc_pv,
+        for (int ks = 0; ks < kBN / 16; ++ks)
+          mma_f16kind_ts(tmem + 256 + g * 128, pa + ks * 8, vbb + ((ks * 16 * 128) >> 4), idesc_pv,
                          (n > 0 || ks > 0) ? 1u : 0u);
-        }
       };
       if (ok) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
       if (ok) {
@@ -286,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kWidenWarp0) {
     // =========================== K/V widening ===========================
-    regs_dec<88>();
+    regs_dec<kRegsWiden>();
     const int kv_head = 2 * pair / (p.hq / p.hkv);
-    const int row0 = (warp - kWidenWarp0) * 32 + (lane >> 2);  // key of batch 0 within the tile; batch i: + 8 i
+    const int row0 = (warp - kWidenWarp0) * 16 + (lane >> 2);  // key of batch 0 within the tile; batch i: + 8 i
     const int t = lane & 3;
     const bool odd = (lane >> 2) & 1;
     auto block_of = [&](int n) -> int {
@@ -299,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
       return -1;
     };
-    uint4 codes[4], par[4];
+    uint4 codes[2], par[2];
     // ring item i: K_{i/2} (even i) or V_{i/2} (odd i)
     auto load_batch = [&](int i, int j, int blk) {
       codes[j] = par[j] = make_uint4(0, 0, 0, 0);
@@ -314,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int blk = checked(block_of(0)), blk_next = -1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_batch(0, j, blk);
+    for (int j = 0; j < 2; ++j) load_batch(0, j, blk);
     for (int i = 0; i < 2 * n_tiles; ++i) {
       const bool is_v = i & 1;
       if (!is_v) blk_next = block_of((i >> 1) + 1);  // used one item later
@@ -325,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const int row = row0 + 8 * j;
         uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
         uint32_t sz[4] = {par[j].x, par[j].y, par[j].z, par[j].w};
@@ -354,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = dst + row * 128;
         const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
         auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
-          const uint4 v = dequantise8<E>(codes8, param);
+          const uint4 v = dequantise8<E, true>(codes8, param);
           sts128(at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
         };
         put(wa, pa, 0, ca);
@@ -368,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // =========================== softmax groups ===========================
-    regs_inc<192>();
+    regs_inc<kRegsSoftmax>();
     const int g = (warp - kSoftmaxWarp0) >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;  // query row within the tile == TMEM lane
@@ -376,9 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_base + g * 128;
     const uint32_t tO = tmem + lane_base + 256 + g * 128;
-    const uint32_t prow = sbase + kOffP + g * kTileBytes + row * 128;
-    const int swz = row & 7;
-    const float sl2 = p.scale_log2;
+    // bf16 K and V are held as 2^-64 of their values (dequantise8)
+    const float out_scale = E == Elem::kBF16 ? 18446744073709551616.f : 1.f;
+    const float sl2 = p.scale_log2 * out_scale;
     float m = -INFINITY;  // running max, log2 units (scaled)
     float l = 0.f;
     bool ok = true;
@@ -430,19 +460,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       l *= alpha;
       const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
       const uint64_t negm2 = f32x2_pack(-m_use, -m_use);
+      // P = 2^(s*sl2 - m_use), rounded to the element type, over the logits in TMEM
+      uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < 8; ++c) {
+        uint32_t pk[8];
 #pragma unroll
-        for (int j = c * 8; j < c * 8 + 8; j += 2) {
+        for (int i = 0; i < 8; ++i) {
+          const int j = c * 16 + 2 * i;
           float a0, a1;
           f32x2_unpack(f32x2_fma(f32x2_pack(s[j], s[j + 1]), sl2x2, negm2), a0, a1);
-          s[j] = ex2_approx(a0);
-          s[j + 1] = ex2_approx(a1);
+          a0 = ex2_approx(a0);
+          a1 = ex2_approx(a1);
+          sums[i & 3] = f32x2_add(sums[i & 3], f32x2_pack(a0, a1));
+          pk[i] = Ops::pack(a0, a1);
         }
-        const int half = c >> 3;
-        const uint32_t addr = prow + half * kHalfBytes + (((c & 7) ^ swz) << 4);
-        const float* e = s + c * 8;
-        sts128(addr, Ops::pack(e[0], e[1]), Ops::pack(e[2], e[3]), Ops::pack(e[4], e[5]), Ops::pack(e[6], e[7]));
+        tmem_st8(tS + c * 8, pk);
       }
       m = m_use;
       // rescale the running output (PV_g(n-1) is complete: S_g(n) was issued after it)
@@ -457,36 +490,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
           tmem_st8(tO + c * 8, r);
         }
-        tmem_wait_st();
       }
-      fence_proxy_async_smem();
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarPReady + g));
-      // The row sum is not needed for P: add it up after P is handed over.
       {
-        uint64_t acc[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) acc[a] = f32x2_pack(s[2 * a], s[2 * a + 1]);
-#pragma unroll
-        for (int j = 8; j < 128; j += 8)
-#pragma unroll
-          for (int a = 0; a < 4; ++a) acc[a] = f32x2_add(acc[a], f32x2_pack(s[j + 2 * a], s[j + 2 * a + 1]));
         float t0, t1, t2, t3, t4, t5, t6, t7;
-        f32x2_unpack(acc[0], t0, t1);
-        f32x2_unpack(acc[1], t2, t3);
-        f32x2_unpack(acc[2], t4, t5);
-        f32x2_unpack(acc[3], t6, t7);
+        f32x2_unpack(sums[0], t0, t1);
+        f32x2_unpack(sums[1], t2, t3);
+        f32x2_unpack(sums[2], t4, t5);
+        f32x2_unpack(sums[3], t6, t7);
         l += ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
       }
     }
     if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), 0, s_abort, p.err));
-    // Epilogue: O is staged in the two P buffers (both heads of a query row side
-    // by side, 512 B, 16-byte chunks rotated by the row), then leaves as whole rows.
-    const uint32_t stage = sbase + kOffP;
+    // Epilogue: every product is complete, so O is staged in the two Q tiles (both
+    // heads of a query row side by side, 512 B, 16-byte chunks rotated by the row)
+    // and leaves as whole rows.
+    const uint32_t stage = sbase + kOffQ;
     if (ok) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+      const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * out_scale;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // group c of 32 dims
         uint32_t r[32];
