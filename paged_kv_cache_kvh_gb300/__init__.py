@@ -380,38 +380,66 @@ def q4_cache(num_blocks: int, num_kv_heads: int = NUM_KV_HEADS, device="cuda") -
     return torch.empty((num_blocks, num_kv_heads, Q4_TILES, Q4_TILE_BYTES), dtype=torch.uint8, device=device)
 
 
-def _here(*tensors):
-    """All on the current CUDA device: the library launches there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        _need(t is None or t.get_device() == dev, "tensors must be on the current CUDA device")
+# The calls below are made once per layer and step, and a small one is over on the
+# GPU in a few microseconds: their checks read each tensor property once and build
+# no message unless one fails.
 
 
-def _q4_caches(k_cache, v_cache, hkv):
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _table(t, dev, name):
+    if t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor on the current device")
+
+
+def _rows_q4(t, dev, dtype, heads, name):
+    """Checks [N, heads, 128] rows and returns the elements between them (a single row may carry any stride)."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {_TYPE_NAME[dtype]} CUDA tensor on the current device")
+    if len(shape) != 3 or shape[1] != heads or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [N, {heads}, 128]")
+    if stride[2] != 1 or (stride[1] != HEAD_DIM and heads > 1):
+        raise ValueError(f"{name}: heads and dims must be contiguous within a row")
+    return stride[0] if shape[0] > 1 else heads * HEAD_DIM
+
+
+def _dense(t, dev, dtype, shape, name):
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {_TYPE_NAME[dtype]} {tuple(shape)} on the current CUDA device")
+
+
+def _q4_caches(k_cache, v_cache, dev):
+    """Checks the pair and returns (blocks, num_kv_heads)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != Q4_TILES or shape[3] != Q4_TILE_BYTES:
+        raise ValueError("k_cache must be uint8 [blocks, num_kv_heads, 16, 1280] (q4_cache)")
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t.dtype == torch.uint8 and t.is_cuda and t.is_contiguous() and t.dim() == 4
-              and tuple(t.shape[1:]) == (hkv, Q4_TILES, Q4_TILE_BYTES),
-              f"{name}: contiguous uint8 CUDA [blocks, {hkv}, 16, 1280] (q4_cache)")
-    _need(k_cache.shape[0] == v_cache.shape[0], "k_cache and v_cache must have the same number of blocks")
+        if t.dtype != torch.uint8 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous uint8 {tuple(shape)} on the current CUDA device (q4_cache)")
+    return shape[0], shape[1]
+
+
+def _call(entry, *args):
+    status = getattr(_lib, entry)(*args)
+    if status != PKV_OK:
+        raise PkvError(status, entry)
 
 
 def _store_q4(entry, dtype, k, v, k_cache, v_cache, slot_mapping, stream):
-    _need(k.dim() == 3 and v.shape == k.shape, "k, v must be [N, num_kv_heads, 128]")
-    N, hkv = k.shape[0], k.shape[1]
-    _rows(k, "k", hkv, dtype)
-    _rows(v, "v", hkv, dtype)
-    _q4_caches(k_cache, v_cache, hkv)
-    _dev_i32(slot_mapping, "slot_mapping")
-    _need(slot_mapping.numel() == N, "slot_mapping must have one entry per token")
-    _here(k, v, k_cache, v_cache, slot_mapping)
-    _check(getattr(_lib, entry)(_ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(k_cache), _ptr(v_cache),
-                                _ptr(slot_mapping), N, hkv, HEAD_DIM, BLOCK_SIZE, k_cache.shape[0], _stream(stream)),
-           entry)
-
-
-def _row_stride(t):
-    """Elements between rows; that of a single row is never used and may be anything."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    dev = torch.cuda.current_device()
+    blocks, hkv = _q4_caches(k_cache, v_cache, dev)
+    ks, vs = _rows_q4(k, dev, dtype, hkv, "k"), _rows_q4(v, dev, dtype, hkv, "v")
+    _table(slot_mapping, dev, "slot_mapping")
+    n = k.shape[0]
+    if v.shape[0] != n or slot_mapping.numel() != n:
+        raise ValueError("k, v and slot_mapping must have one entry per token")
+    _call(entry, k.data_ptr(), ks, v.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+          n, hkv, HEAD_DIM, BLOCK_SIZE, blocks, _raw_stream(stream, dev))
 
 
 def pkv_store_kvcache_q4(k, v, k_cache, v_cache, slot_mapping, stream=None):
@@ -426,21 +454,19 @@ def pkv_store_kvcache_q4_f16(k, v, k_cache, v_cache, slot_mapping, stream=None):
 
 
 def _load_q4(entry, dtype, k_cache, v_cache, slot_mapping, k, v, stream):
-    _need(k_cache.dim() == 4, "k_cache: uint8 [blocks, num_kv_heads, 16, 1280] (q4_cache)")
-    hkv = k_cache.shape[1]
-    _q4_caches(k_cache, v_cache, hkv)
-    _dev_i32(slot_mapping, "slot_mapping")
-    shape = (slot_mapping.numel(), hkv, HEAD_DIM)
+    dev = torch.cuda.current_device()
+    blocks, hkv = _q4_caches(k_cache, v_cache, dev)
+    _table(slot_mapping, dev, "slot_mapping")
+    n = slot_mapping.numel()
+    shape = (n, hkv, HEAD_DIM)
     if k is None:
         k = torch.zeros(shape, dtype=dtype, device=k_cache.device)
     if v is None:
         v = torch.zeros(shape, dtype=dtype, device=k_cache.device)
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t.dtype == dtype and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape,
-              f"{n} must be contiguous {_TYPE_NAME[dtype]} CUDA [N, {hkv}, 128]")
-    _here(k_cache, v_cache, slot_mapping, k, v)
-    _check(getattr(_lib, entry)(_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), shape[0], hkv, HEAD_DIM, BLOCK_SIZE,
-                                k_cache.shape[0], _ptr(k), _ptr(v), _stream(stream)), entry)
+    _dense(k, dev, dtype, shape, "k")
+    _dense(v, dev, dtype, shape, "v")
+    _call(entry, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hkv, HEAD_DIM, BLOCK_SIZE, blocks,
+          k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev))
     return k, v
 
 
@@ -471,33 +497,34 @@ def decode_q4_workspace(num_seqs: int, max_context_len: int, num_heads: int = NU
 
 def _decode_q4(entry, dtype, q, new, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale,
                workspace, out, stream):
-    _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [B, num_heads, 128], k_cache [blocks, num_kv_heads, 16, 1280]")
-    B, hq, hkv = q.shape[0], q.shape[1], k_cache.shape[1]
-    _rows(q, "q", hq, dtype)
-    _q4_caches(k_cache, v_cache, hkv)
-    _dev_i32(block_tables, "block_tables")
-    _dev_i32(context_lens, "context_lens")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] >= B and context_lens.numel() >= B, "table sizes")
+    dev = torch.cuda.current_device()
+    blocks, hkv = _q4_caches(k_cache, v_cache, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, num_heads, 128]")
+    B, hq = q.shape[0], q.shape[1]
+    qs = _rows_q4(q, dev, dtype, hq, "q")
+    _table(block_tables, dev, "block_tables")
+    _table(context_lens, dev, "context_lens")
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] < B or context_lens.numel() < B:
+        raise ValueError("block_tables must be [B, width] and context_lens [B]")
     if out is None:
-        out = torch.empty((B, hq, HEAD_DIM), dtype=dtype, device=q.device)
-    _need(out.is_cuda and out.is_contiguous() and out.shape == (B, hq, HEAD_DIM) and out.dtype == dtype,
-          f"out must be contiguous {_TYPE_NAME[dtype]} CUDA [B, {hq}, 128]")
-    _need(workspace.dtype == torch.uint8 and workspace.is_cuda and workspace.is_contiguous(),
-          "workspace must be a contiguous uint8 CUDA tensor")
-    _here(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+        out = q.new_empty((B, hq, HEAD_DIM))
+    else:
+        _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
+    if workspace.dtype != torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the current CUDA device")
     rows = ()
     if new is not None:
         k, v, slot_mapping = new
-        _rows(k, "k", hkv, dtype)
-        _rows(v, "v", hkv, dtype)
-        _dev_i32(slot_mapping, "slot_mapping")
-        _need(k.shape[0] >= B and v.shape[0] >= B and slot_mapping.numel() >= B, "one new row per sequence")
-        _here(k, v, slot_mapping)
-        rows = (_ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(slot_mapping))
-    _check(getattr(_lib, entry)(_ptr(q), _row_stride(q), *rows, _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
-                                _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, hq, hkv, HEAD_DIM,
-                                BLOCK_SIZE, int(max_context_len), float(softmax_scale), _ptr(out), _ptr(workspace),
-                                workspace.numel(), _stream(stream)), entry)
+        rows = (k.data_ptr(), _rows_q4(k, dev, dtype, hkv, "k"), v.data_ptr(), _rows_q4(v, dev, dtype, hkv, "v"),
+                slot_mapping.data_ptr())
+        _table(slot_mapping, dev, "slot_mapping")
+        if k.shape[0] < B or v.shape[0] < B or slot_mapping.numel() < B:
+            raise ValueError("k, v and slot_mapping must have one new row per sequence")
+    _call(entry, q.data_ptr(), qs, *rows, k_cache.data_ptr(), v_cache.data_ptr(), blocks, block_tables.data_ptr(),
+          tables[1], context_lens.data_ptr(), B, hq, hkv, HEAD_DIM, BLOCK_SIZE, int(max_context_len),
+          float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     return out
 
 
@@ -533,27 +560,31 @@ def pkv_store_decode_q4_f16(q, k, v, slot_mapping, k_cache, v_cache, block_table
 
 def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache,
                 v_cache, block_tables, out, plan, stream):
-    _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [total_q, num_heads, 128], k_cache [blocks, num_kv_heads, 16, 1280]")
-    total_q, hq, hkv = q.shape[0], q.shape[1], k_cache.shape[1]
-    _rows(q, "q", hq, dtype)
-    _q4_caches(k_cache, v_cache, hkv)
-    _dev_i32(cu_seqlens_q, "cu_seqlens_q")
-    _dev_i32(cu_seqlens_k, "cu_seqlens_k")
-    _dev_i32(block_tables, "block_tables")
+    dev = torch.cuda.current_device()
+    blocks, hkv = _q4_caches(k_cache, v_cache, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, num_heads, 128]")
+    total_q, hq = q.shape[0], q.shape[1]
+    qs = _rows_q4(q, dev, dtype, hq, "q")
+    _table(cu_seqlens_q, dev, "cu_seqlens_q")
+    _table(cu_seqlens_k, dev, "cu_seqlens_k")
+    _table(block_tables, dev, "block_tables")
     num_seqs = cu_seqlens_q.numel() - 1
-    _need(num_seqs >= 0 and cu_seqlens_k.numel() == num_seqs + 1, "cu_seqlens sizes")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] >= num_seqs, "block_tables [num_seqs, width]")
+    tables = block_tables.shape
+    if num_seqs < 0 or cu_seqlens_k.numel() != num_seqs + 1 or len(tables) != 2 or tables[0] < num_seqs:
+        raise ValueError("cu_seqlens must be [num_seqs + 1] and block_tables [num_seqs, width]")
     if out is None:
-        out = torch.empty((total_q, hq, HEAD_DIM), dtype=dtype, device=q.device)
-    _need(out.is_cuda and out.is_contiguous() and out.shape == (total_q, hq, HEAD_DIM) and out.dtype == dtype,
-          f"out must be contiguous {_TYPE_NAME[dtype]} CUDA [total_q, {hq}, 128]")
-    plan = _plan_arg(plan, None)
-    _here(q, cu_seqlens_q, cu_seqlens_k, k_cache, v_cache, block_tables, out, plan)
-    _check(getattr(_lib, entry)(
-        _ptr(q), _row_stride(q), total_q, _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(cu_seqlens_q),
-        _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], num_seqs,
-        hq, hkv, HEAD_DIM, BLOCK_SIZE, float(softmax_scale), _ptr(out), _ptr(plan),
-        0 if plan is None else plan.numel() * 4, _stream(stream)), entry)
+        out = q.new_empty((total_q, hq, HEAD_DIM))
+    else:
+        _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
+    items = n_items = 0
+    if plan is not None:
+        _table(plan, dev, "plan (pkv_prefill_plan)")
+        items, n_items = plan.data_ptr(), plan.numel()
+    _call(entry, q.data_ptr(), qs, total_q, k_cache.data_ptr(), v_cache.data_ptr(), blocks, cu_seqlens_q.data_ptr(),
+          cu_seqlens_k.data_ptr(), int(max_seqlen_q), int(max_seqlen_k), block_tables.data_ptr(), tables[1], num_seqs,
+          hq, hkv, HEAD_DIM, BLOCK_SIZE, float(softmax_scale), out.data_ptr(), items, 4 * n_items,
+          _raw_stream(stream, dev))
     return out
 
 

@@ -55,6 +55,10 @@ constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
 constexpr int kRegsFirst = 48, kRegsSoftmax = 152, kRegsWiden = 64;
 static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
 
+#ifndef PKV_Q4P_NAP
+#define PKV_Q4P_NAP 100
+#endif
+constexpr int kWidenNap = PKV_Q4P_NAP;
 constexpr int kOffQ = 0;                                 // 2 tiles (and O staging in the epilogue)
 constexpr int kOffKV = 2 * kTileBytes;                   // kKvSlots tiles
 constexpr int kOffBar = kOffKV + kKvSlots * kTileBytes;  // barriers
@@ -92,26 +96,18 @@ struct Q4PrefillParams {
   unsigned int* err;
 };
 
-// mbarrier test that may sleep for up to a microsecond: 18 warps poll here, and
-// their polls would take issue slots from the softmax and widening warps.
-__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000)
-      : "memory");
-  return ok != 0;
-}
-
 // Bounded wait that also gives up as soon as another role of the CTA has aborted.
+// kNap: nanoseconds slept between tests by a role that can afford to be late.
+template <int kNap = 0>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                               unsigned int* err) {
-  if (mbar_try_wait_long(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait_long(bar, parity)) return true;
+    for (int i = 0; i < 32; ++i) {
+      if (kNap > 0) __nanosleep(kNap);
+      if (mbar_try_wait(bar, parity)) return true;
+    }
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       flag_error(err, PKV_DEVERR_TIMEOUT);
@@ -351,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if (i + 1 < 2 * n_tiles) blk = checked(blk_next);
       const int slot = i % kKvSlots;
       if (i >= kKvSlots &&
-          !__all_sync(0xffffffffu, wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err)))
+          !__all_sync(0xffffffffu, wait_or_abort<kWidenNap>(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err)))
         break;
       const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
 #pragma unroll
