@@ -61,7 +61,7 @@ constexpr int kMaxChunk = 16;                                // units per chunk 
 constexpr int kMaxSeqs = 768;                                // sequences per launch (item table in shared memory)
 constexpr int kClasses = 8;                                  // sizes that short chunks are sorted into
 constexpr int kFan = 16;                                     // chunks merged at once
-constexpr int kFirst = 1 << 30, kLast = 1 << 29;             // stage header: an item's first and last unit
+constexpr int kFirst = 1 << 8, kLast = 1 << 9, kNew = 1 << 10;  // a unit's flags: first and last of its item, holds a new row
 constexpr uint32_t kTf32Mask = 0xffffe000u;                  // the bits that a tf32 operand keeps
 constexpr uint32_t kOne = 0x3f800000u;                       // 1.0f
 
@@ -72,11 +72,13 @@ constexpr uint32_t kOne = 0x3f800000u;                       // 1.0f
 __host__ __device__ constexpr int warps_of(int G) { return G <= 2 ? PKV_Q4_WARPS : 8; }
 
 // A warp's shared memory: two units of K, one of V, the query rows of two items
-// (they arrive with an item's first K), what is known of the two units, barriers.
-struct UnitHeader {
-  int32_t seq, head, tokens, chunks;  // head with kFirst / kLast; chunk | chunks of the sequence << 16
-  int64_t offset;                     // of the unit's first tile in the cache
-  int32_t bytes, pad;
+// (they arrive with an item's first K), and what its lanes share about them.
+struct WarpInfo {
+  int4 item[4];       // {sequence, head, chunk | chunks of the sequence << 16, -} of the items under way
+  int64_t place[2];   // per K slot: where the unit starts in the caches
+  int32_t unit[2];    // tokens, flags
+  uint32_t bytes[2];  // to fetch of K and of V each
+  uint64_t bars[3];   // K, K, V arrived
 };
 
 struct Q4DecodeParams {
@@ -133,27 +135,69 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&d)[4
                : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
                : "r"(addr));
 }
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
   return r;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1, const float (&c)[4]) {
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma1688_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1, const float (&c)[4]) {
+// the first of a chain: C = 0
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D = A B + C with C left as it is, and in place
+__device__ __forceinline__ void mma1688_tf32_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                  uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ void mma1688_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+#ifdef PKV_Q4_HI
+__device__ __forceinline__ uint32_t shift8(uint32_t x) { return __umulhi(x, 0x01000000u); }
+#else
+__device__ __forceinline__ uint32_t shift8(uint32_t x) { return x >> 8; }
+#endif
+
+// Whole-warp bounded wait, after a first test has failed.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+      flag_error(err, PKV_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -218,11 +262,12 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   constexpr int kWarps = warps_of(G), kThreads = kWarps * 32;
   constexpr int kNB = (G + 1) / 2;            // B operands: pairs of query heads
   constexpr int kQBytes = G * kHeadDim * 2;   // one item's query rows
-  constexpr int kWarpBytes = 3 * kUnitBytes + 2 * kQBytes;
+  // B fragments of q: in registers, or where those of two pairs of heads would not fit, in shared memory
+  constexpr bool kFragsInSmem = kNB > 1;
+  constexpr int kWarpBytes = 3 * kUnitBytes + 2 * kQBytes + (kFragsInSmem ? kNB * 2048 : 0);
   extern __shared__ __align__(128) uint8_t smem[];
-  UnitHeader* hdr_all = reinterpret_cast<UnitHeader*>(smem + kWarps * kWarpBytes);  // [warp][2]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(hdr_all + kWarps * 2);               // [warp][3]: K, K, V
-  int* sF = reinterpret_cast<int*>(bars + kWarps * 3);                              // [num_seqs + 1] whole chunks before b
+  WarpInfo* info_all = reinterpret_cast<WarpInfo*>(smem + kWarps * kWarpBytes);
+  int* sF = reinterpret_cast<int*>(info_all + kWarps);  // [num_seqs + 1] whole chunks before b
   int* sCtx = sF + kMaxSeqs + 1;                                                   // [num_seqs]
   int* plist = sCtx + kMaxSeqs;                                                    // sequences with a short last chunk
   int* red = plist + kMaxSeqs;                                                     // [2][kWarps], then [9][32]
@@ -236,7 +281,46 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   // sizes, longest first: the items that end the call are the shortest. A warp
   // holds sequences i * kThreads + tid, 32 consecutive ones (a group) at a time.
   int chunk, n_full, n_part = 0;
-  {
+  if (B <= 32) {
+    // One sequence per lane, every warp for itself (the sizes stay in registers,
+    // warp 0 writes the table). Short chunks follow in sequence order.
+    int ctx = 0;
+    if (lane < B) {
+      ctx = p.context_lens[lane];
+      if (ctx < 0 || ctx > p.max_ctx || ctx > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
+        if (cta == 0 && warp == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+        ctx = 0;
+      }
+    }
+    if (lane < 3) mbar_init(smem_u32(info_all[warp].bars + lane), 1);
+    mbar_fence_init();
+    int halves = (ctx + kHalfUnit - 1) / kHalfUnit, units = (ctx + kUnit - 1) / kUnit;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      halves += __shfl_xor_sync(0xffffffffu, halves, off);
+      units += __shfl_xor_sync(0xffffffffu, units, off);
+    }
+    chunk = chunk_tokens(static_cast<int64_t>(halves) * p.hkv, static_cast<int64_t>(units) * p.hkv, kWarps);
+    const int full = static_cast<int>(static_cast<unsigned>(ctx) / static_cast<unsigned>(chunk));
+    int scan = full;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, off);
+      if (lane >= off) scan += y;
+    }
+    n_full = __shfl_sync(0xffffffffu, scan, 31);
+    const uint32_t part = __ballot_sync(0xffffffffu, full * chunk < ctx);
+    n_part = __popc(part);
+    if (warp == 0) {
+      if (lane < B) {
+        sCtx[lane] = ctx;
+        sF[lane] = scan - full;
+        if (full * chunk < ctx) plist[__popc(part & ((1u << lane) - 1u))] = lane;
+      }
+      if (lane == 0) sF[B] = n_full;
+    }
+    __syncthreads();
+  } else {
     constexpr int kPer = (kMaxSeqs + kThreads - 1) / kThreads;
     static_assert(kPer * kWarps <= 32, "one lane per group below");
     int ctx[kPer];
@@ -266,7 +350,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       red[warp] = halves;
       red[kWarps + warp] = units;
     }
-    if (lane < 3) mbar_init(smem_u32(bars + warp * 3 + lane), 1);
+    if (lane < 3) mbar_init(smem_u32(info_all[warp].bars + lane), 1);
     mbar_fence_init();
     __syncthreads();
     int64_t all_halves = 0, all_units = 0;
@@ -280,7 +364,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
     int full[kPer], cls[kPer], scan[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      full[i] = ctx[i] / chunk;
+      full[i] = static_cast<int>(static_cast<unsigned>(ctx[i]) / static_cast<unsigned>(chunk));
       const int rest = ctx[i] - full[i] * chunk;
       cls[i] = rest > 0 ? kClasses - 1 - (rest * kClasses - 1) / chunk : -1;
       scan[i] = full[i];
@@ -349,9 +433,9 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   }
 
   const uint32_t k_buf = smem_u32(smem) + warp * kWarpBytes, v_buf = k_buf + 2 * kUnitBytes;
-  const uint32_t q_buf = v_buf + kUnitBytes;
-  const uint32_t k_full = smem_u32(bars + warp * 3), v_full = k_full + 16;
-  UnitHeader* hdr = hdr_all + warp * 2;
+  const uint32_t q_buf = v_buf + kUnitBytes, frags = q_buf + 2 * kQBytes + lane * 16;
+  WarpInfo* info = info_all + warp;
+  const uint32_t k_full = smem_u32(info->bars), v_full = k_full + 16;
   const int r = lane >> 2, t = lane & 3;
   const int W = n_ctas * kWarps;
   const bool dynamic = n_items > W;
@@ -360,16 +444,21 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   int64_t item = static_cast<int64_t>(warp) * n_ctas + cta;
   int next_raw = 0;  // lane 0: the counter's answer for the item after this one
   if (dynamic && lane == 0) next_raw = atomicAdd(p.work, 1);
-  int ib = 0, ihead = 0, ic = 0, inch = 0, itok = 0, iend = 0;  // sequence, head, chunk, chunks, next token, chunk's end
-  int ipb = -1;        // block of the unit to fetch; read one unit ahead of its use
-  bool fresh = false;  // ipb has not been checked yet
+  int ib = 0, ihead = 0, itok = 0;     // sequence, head, next token
+  int left = 0;                        // tokens of the chunk not asked for yet; 0: no more work
+  int items = 0;                       // items resolved
+  bool ifirst = false, itail = false;  // next unit is an item's first; the item is its sequence's last chunk
+  int ipb = -1;                        // block of the unit to fetch; read one unit ahead of its use
+  bool fresh = false;                  // ipb has not been checked and turned into ioff yet
+  int64_t ioff = -1;                   // where the next unit starts in the caches; -1: a bad block
   auto look_up = [&]() {
     ipb = p.block_tables[static_cast<int64_t>(ib) * p.bt_stride + itok / kBlockSize];
     fresh = true;
   };
   auto resolve = [&]() {  // item -> sequence, chunk, head (whole warp)
-    const int ci = static_cast<int>(item / p.hkv);
-    ihead = static_cast<int>(item - static_cast<int64_t>(ci) * p.hkv);
+    const int ci = static_cast<int>(static_cast<unsigned>(item) / static_cast<unsigned>(p.hkv));
+    ihead = static_cast<int>(item) - ci * p.hkv;
+    int c;
     if (ci < n_full) {
       // largest b with sF[b] <= ci, 32 probes at a time
       const int step = (B + 31) / 32;
@@ -378,99 +467,83 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       const int probe2 = hi * step + lane;
       const int cnt = __popc(__ballot_sync(0xffffffffu, lane < step && probe2 < B && sF[probe2] <= ci));
       ib = hi * step + cnt - 1;
-      ic = ci - sF[ib];
+      c = ci - sF[ib];
     } else {
       ib = plist[ci - n_full];
-      ic = sF[ib + 1] - sF[ib];
+      c = sF[ib + 1] - sF[ib];
     }
     const int ctx = sCtx[ib];
-    inch = sF[ib + 1] - sF[ib];
-    inch += inch * chunk < ctx ? 1 : 0;
-    itok = ic * chunk;
-    iend = min(itok + chunk, ctx);
+    int nch = sF[ib + 1] - sF[ib];
+    nch += nch * chunk < ctx ? 1 : 0;
+    itok = c * chunk;
+    left = min(chunk, ctx - itok);
+    ifirst = true;
+    itail = c == nch - 1;
+    if (lane == 0) info->item[items & 3] = make_int4(ib, ihead, c | (nch << 16), 0);
+    ++items;
     look_up();
   };
-  bool more = item < n_items;
-  if (more) resolve();
+  if (item < n_items) resolve();
   int issued = 0;  // units whose K has been asked for
   auto issue_k = [&]() {  // fetches the next unit's K (whole warp)
-    if (!more) return;
+    if (left <= 0) return;
     if (fresh) {
-      if (ipb < 0 || ipb >= p.num_blocks) {
-        if (lane == 0) flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
-        ipb = -1;
-      }
       fresh = false;
+      ioff = -1;
+      if (ipb >= 0 && ipb < p.num_blocks)
+        ioff = (static_cast<int64_t>(ipb) * p.hkv + ihead) * kQ4RecordBytes + (itok % kBlockSize) / kQ4Tile * kQ4TileBytes;
+      else if (lane == 0)
+        flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
     }
-    const int ntok = min(kUnit, iend - itok);
-    const int64_t rec = (static_cast<int64_t>(ipb) * p.hkv + ihead) * kQ4RecordBytes;
-    const bool first = itok == ic * chunk, last = itok + ntok == iend;
-    if (p.k_new != nullptr && last && ic == inch - 1) {
-      // this unit holds the newest position: its row is written before the unit is fetched
+    const int ntok = min(kUnit, left);
+    const bool last = left <= kUnit;
+    int flags = ntok | (ifirst ? kFirst : 0) | (last ? kLast : 0);
+    if (p.k_new != nullptr && last && itail) {
+      // the unit holds the newest position: the computing side puts its row in
       const int64_t slot = p.slot_mapping[ib];
       if (slot != -1) {
-        const int in_block = (iend - 1) % kBlockSize, tok = in_block % kQ4Tile;
-        if (ipb < 0 || slot != static_cast<int64_t>(ipb) * kBlockSize + in_block) {
-          if (lane == 0 && ihead == 0) flag_error(p.err, PKV_DEVERR_BAD_SLOT);
-        } else {
-          const int lane16 = lane & 15, j = lane16 >> 2, tt = lane16 & 3;
-          const bool is_v = lane >= 16;
-          const uint16_t* src = (is_v ? p.v_new + ib * p.v_new_stride : p.k_new + ib * p.k_new_stride) +
-                                ihead * kHeadDim + lane16 * 8;
-          uint32_t par;
-          uint32_t codes = quantise8<E>(*reinterpret_cast<const uint4*>(src), par);
-          const uint32_t vcodes = v_exchange(codes, j);
-          uint8_t* dst = (is_v ? p.v_cache_w : p.k_cache_w) + rec + in_block / kQ4Tile * kQ4TileBytes;
-          *reinterpret_cast<uint32_t*>(dst + (is_v ? q4_v_word(tok, j, tt) : q4_k_word(tok, j, tt))) =
-              is_v ? vcodes : codes;
-          if (tt == 0) *reinterpret_cast<uint32_t*>(dst + q4_param(tok, j)) = par;
-          // visible to the bulk copy (async proxy) that lane 0 issues below
-          asm volatile("fence.proxy.async.global;" ::: "memory");
-          __syncwarp();
-        }
+        if (ioff >= 0 && slot == static_cast<int64_t>(ipb) * kBlockSize + (itok + ntok - 1) % kBlockSize)
+          flags |= kNew;
+        else if (lane == 0 && ihead == 0)
+          flag_error(p.err, PKV_DEVERR_BAD_SLOT);
       }
     }
+    const uint32_t bytes = ioff < 0 ? 0u : static_cast<uint32_t>((ntok + kQ4Tile - 1) / kQ4Tile) * kQ4TileBytes;
     if (lane == 0) {
       const int s = issued & 1;
-      const uint32_t bytes = ipb < 0 ? 0u : static_cast<uint32_t>((ntok + kQ4Tile - 1) / kQ4Tile) * kQ4TileBytes;
-      const int64_t off = rec + (itok % kBlockSize) / kQ4Tile * kQ4TileBytes;
-      UnitHeader u;
-      u.seq = ib;
-      u.head = ihead | (first ? kFirst : 0) | (last ? kLast : 0);
-      u.tokens = ipb < 0 ? 0 : ntok;
-      u.chunks = ic | (inch << 16);
-      u.offset = off;
-      u.bytes = static_cast<int32_t>(bytes);
-      u.pad = 0;
-      hdr[s] = u;
-      mbar_arrive_expect_tx(k_full + 8 * s, bytes + (first ? kQBytes : 0));
-      if (bytes > 0) bulk_g2s(k_buf + s * kUnitBytes, p.k_cache + off, bytes, k_full + 8 * s);
-      if (first)
+      info->unit[s] = ioff < 0 ? flags & ~0xff : flags;
+      info->place[s] = ioff;
+      info->bytes[s] = bytes;
+      mbar_arrive_expect_tx(k_full + 8 * s, bytes + (ifirst ? kQBytes : 0));
+      if (bytes > 0) bulk_g2s(k_buf + s * kUnitBytes, p.k_cache + ioff, bytes, k_full + 8 * s);
+      if (ifirst)
         bulk_g2s(q_buf + s * kQBytes, p.q + static_cast<int64_t>(ib) * p.q_row_stride + ihead * G * kHeadDim, kQBytes,
                  k_full + 8 * s);
     }
+    ifirst = false;
     ++issued;
-    itok += ntok;
+    itok += kUnit;
+    left -= kUnit;
     if (last) {
-      more = false;
+      left = 0;
       if (dynamic) {
         item = static_cast<int64_t>(W) + __shfl_sync(0xffffffffu, next_raw, 0);
-        more = item < n_items;
-        if (more) {
+        if (item < n_items) {
           if (lane == 0) next_raw = atomicAdd(p.work, 1);
           resolve();
         }
       }
     } else if (itok % kBlockSize == 0) {
       look_up();
+    } else if (ioff >= 0) {
+      ioff += kUnitBytes;
     }
   };
   auto issue_v = [&](int n) {  // fetches V of unit n, whose K has been asked for
     if (n < issued && lane == 0) {
-      const int64_t off = hdr[n & 1].offset;
-      const uint32_t bytes = static_cast<uint32_t>(hdr[n & 1].bytes);
+      const uint32_t bytes = info->bytes[n & 1];
       mbar_arrive_expect_tx(v_full, bytes);
-      if (bytes > 0) bulk_g2s(v_buf, p.v_cache + off, bytes, v_full);
+      if (bytes > 0) bulk_g2s(v_buf, p.v_cache + info->place[n & 1], bytes, v_full);
     }
   };
   issue_k();
@@ -483,7 +556,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   // (r, t) then holds, of tokens 2t, 2t + 1, four dims of group r & 3 per chunk.
   const uint32_t par_off = kQ4TileParams + r * kQ4ParamBytes + t * 4;
   const uint32_t v_off = (lane & 7) * kQ4CodeBytes + (((lane >> 3) ^ ((lane & 4) >> 1)) << 4);
-  uint32_t qb[kNB][8][2];    // B fragments of q, one per 16 dims
+  uint32_t qb[kFragsInSmem ? 1 : kNB][8][2];  // B fragments of q, one per 16 dims
   uint32_t qs_b[G][2];       // B fragment of sum q over group t: high and low part
   float kc[kNB][2];          // per head: the power of two taken out of q and the codes, times scale * log2(e)
   float acc[kNB][8][4];
@@ -493,20 +566,44 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   float nu = 1.f;
 
   int done = 0;              // units worked through
+  int items_done = 0;
   bool pending = false;      // a partial result is written, its ticket not taken yet
   int pend_b = 0, pend_head = 0, pend_c = 0;  // pend_c: chunk | chunks << 16
   while (true) {
     const bool have = done < issued;
-    int seq = 0, head_flags = 0, chunks = 0;
+    int flags = 0;
     if (have) {
       const int s = done & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(k_full + 8 * s, (done >> 1) & 1, p.err))) break;
+      const uint32_t k_phase = (done >> 1) & 1;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(k_full + 8 * s, k_phase)) && !wait_warp(k_full + 8 * s, k_phase, p.err))
+        break;
       const uint32_t kst = k_buf + s * kUnitBytes;
-      seq = hdr[s].seq;
-      head_flags = hdr[s].head;
-      chunks = hdr[s].chunks;
-      const int ntok = hdr[s].tokens;
-      if (head_flags & kFirst) {
+      flags = info->unit[s];
+      const int ntok = flags & 0xff;
+      uint32_t new_codes = 0, new_par = 0;
+      if (flags & kNew) {
+        // The step's new row: lanes 0..15 quantise K's, lanes 16..31 V's, 8 dims
+        // each, and write it to the cache and over what was fetched of it.
+        const int4 it = info->item[items_done & 3];
+        const int lane16 = lane & 15, j = lane16 >> 2, tt = lane16 & 3, tok = (ntok - 1) % kQ4Tile;
+        const bool is_v = lane >= 16;
+        const uint16_t* src = (is_v ? p.v_new + it.x * p.v_new_stride : p.k_new + it.x * p.k_new_stride) +
+                              it.y * kHeadDim + lane16 * 8;
+        new_codes = quantise8<E>(*reinterpret_cast<const uint4*>(src), new_par);
+        const uint32_t vcodes = v_exchange(new_codes, j);
+        if (is_v) new_codes = vcodes;
+        const int word = is_v ? q4_v_word(tok, j, tt) : q4_k_word(tok, j, tt);
+        const int tile = (ntok - 1) / kQ4Tile * kQ4TileBytes;
+        uint8_t* dst = (is_v ? p.v_cache_w : p.k_cache_w) + info->place[s] + tile;
+        *reinterpret_cast<uint32_t*>(dst + word) = new_codes;
+        if (tt == 0) *reinterpret_cast<uint32_t*>(dst + q4_param(tok, j)) = new_par;
+        if (!is_v) {
+          sts32(kst + tile + word, new_codes);
+          if (tt == 0) sts32(kst + tile + q4_param(tok, j), new_par);
+        }
+        __syncwarp();
+      }
+      if (flags & kFirst) {
         // ---- a new item: query fragments ----
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) {
@@ -533,10 +630,14 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
           const uint32_t own[4] = {pack_f16(x[0] * f, x[4] * f), pack_f16(x[1] * f16, x[5] * f16),
                                    pack_f16(x[2] * f, x[6] * f), pack_f16(x[3] * f16, x[7] * f16)};
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const bool on = (ks >> 1) == (r >> 1);
-            qb[nb][ks][0] = on ? own[(ks & 1) * 2] : 0u;
-            qb[nb][ks][1] = on ? own[(ks & 1) * 2 + 1] : 0u;
+          for (int j = 0; j < 4; ++j) {  // group j's two fragments: 0 outside the column's own group
+            const bool on = j == (r >> 1);
+            if constexpr (kFragsInSmem) {
+              sts128(frags + nb * 2048 + j * 512, on ? own[0] : 0u, on ? own[1] : 0u, on ? own[2] : 0u, on ? own[3] : 0u);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) qb[nb][2 * j + i / 2][i & 1] = on ? own[i] : 0u;
+            }
           }
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
@@ -580,24 +681,35 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
           const uint32_t base = kst + (2 * pair + i) * kQ4TileBytes + lane * 16;
           w0[i] = lds128(base);
           w1[i] = lds128(base + 8 * kQ4CodeBytes);
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) c[i][nb][0] = c[i][nb][1] = c[i][nb][2] = c[i][nb][3] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
+          uint4 f[kNB];
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb) {
+            if constexpr (kFragsInSmem)
+              f[nb] = lds128(frags + nb * 2048 + j * 512);
+            else
+              f[nb] = make_uint4(qb[nb][2 * j][0], qb[nb][2 * j][1], qb[nb][2 * j + 1][0], qb[nb][2 * j + 1][1]);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t a = j == 0 ? w0[i].x : j == 1 ? w0[i].y : j == 2 ? w0[i].z : w0[i].w;
             const uint32_t b = j == 0 ? w1[i].x : j == 1 ? w1[i].y : j == 2 ? w1[i].z : w1[i].w;
-            const uint32_t ah = a >> 8, bh = b >> 8;
+            const uint32_t ah = shift8(a), bh = shift8(b);
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
-              mma16816(c[i][nb], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qb[nb][2 * j][0],
-                       qb[nb][2 * j][1], c[i][nb]);
+              if (j == 0)
+                mma16816_first(c[i][nb], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
+                               f[nb].x, f[nb].y);
+              else
+                mma16816(c[i][nb], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
+                         f[nb].x, f[nb].y);
               mma16816(c[i][nb], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u,
-                       qb[nb][2 * j + 1][0], qb[nb][2 * j + 1][1], c[i][nb]);
+                       f[nb].z, f[nb].w);
             }
           }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t base = kst + (2 * pair + i) * kQ4TileBytes + par_off;
@@ -616,10 +728,10 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
                 // the sum over the groups (the four lanes t) as a product with ones, plus z . sum q
                 float d[4];
                 const uint32_t h0 = __float_as_uint(x[h2]) & kTf32Mask, h1 = __float_as_uint(x[2 + h2]) & kTf32Mask;
-                mma1688_tf32(d, __float_as_uint(sz0.y), __float_as_uint(sz1.y), __float_as_uint(sz0.y),
+                mma1688_tf32_from(d, __float_as_uint(sz0.y), __float_as_uint(sz1.y), __float_as_uint(sz0.y),
                              __float_as_uint(sz1.y), qs_b[h][0], qs_b[h][1], from[h]);
                 mma1688_tf32(d, h0, h1, __float_as_uint(x[h2] - __uint_as_float(h0)),
-                             __float_as_uint(x[2 + h2] - __uint_as_float(h1)), kOne, kOne, d);
+                             __float_as_uint(x[2 + h2] - __uint_as_float(h1)), kOne, kOne);
                 lg[h][2 * pair + i][0] = d[0];
                 lg[h][2 * pair + i][1] = d[2];
               }
@@ -627,9 +739,18 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
           }
         }
       }
-      __syncwarp();  // every lane has read K and the header
+      __syncwarp();  // every lane has read K and its flags
       issue_k();
-      if (!__all_sync(0xffffffffu, mbar_wait(v_full, done & 1, p.err))) break;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(v_full, done & 1)) && !wait_warp(v_full, done & 1, p.err)) break;
+      if (flags & kNew) {
+        const int lane16 = lane & 15, j = lane16 >> 2, tt = lane16 & 3, tok = (ntok - 1) % kQ4Tile;
+        const uint32_t tile = v_buf + (ntok - 1) / kQ4Tile * kQ4TileBytes;
+        if (lane >= 16) {
+          sts32(tile + q4_v_word(tok, j, tt), new_codes);
+          if (tt == 0) sts32(tile + q4_param(tok, j), new_par);
+        }
+        __syncwarp();
+      }
 
       if (ntok > 0) {
         // V's scale and minimum of this lane's tokens and group
@@ -750,13 +871,13 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
           ldmatrix_x4_trans(base + 8 * kQ4CodeBytes, hi);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t lo8 = lo[q] >> 8, hi8 = hi[q] >> 8;
+            const uint32_t lo8 = shift8(lo[q]), hi8 = shift8(hi[q]);
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
               mma16816(acc[nb][2 * q], lo[q] & 0x000f000fu, lo[q] & 0x00f000f0u, hi[q] & 0x000f000fu,
-                       hi[q] & 0x00f000f0u, pb[nb][0], pb[nb][1], acc[nb][2 * q]);
+                       hi[q] & 0x00f000f0u, pb[nb][0], pb[nb][1]);
               mma16816(acc[nb][2 * q + 1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u,
-                       pb[nb][0], pb[nb][1], acc[nb][2 * q + 1]);
+                       pb[nb][0], pb[nb][1]);
             }
           }
         }
@@ -820,11 +941,13 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       }
     }
     if (!have) break;
-    if (!(head_flags & kLast)) continue;
+    if (!(flags & kLast)) continue;
 
     // ---- the item's end: lanes with t == (r & 3) hold dims 32 t + 8 q + 4 (r >> 2) .. + 3, q = 0..3 ----
-    const int b = seq, head = head_flags & 0xffff, nch = chunks >> 16;
-    const int64_t slot = static_cast<int64_t>(sF[b] + b + (chunks & 0xffff)) * p.hkv + head;
+    const int4 it = info->item[items_done & 3];
+    ++items_done;
+    const int b = it.x, head = it.y, nch = it.z >> 16;
+    const int64_t slot = static_cast<int64_t>(sF[b] + b + (it.z & 0xffff)) * p.hkv + head;
     const float back = __fdividef(16777216.f, nu);
     const int d0 = 32 * t + 4 * (r >> 2);
 #pragma unroll
@@ -862,7 +985,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
     pending = nch > 1;
     pend_b = b;
     pend_head = head;
-    pend_c = chunks;
+    pend_c = it.z;
   }
   // only after a wait that ran out: never leave a copy in flight into this CTA's shared memory
   if (done < issued) {
@@ -883,7 +1006,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
 template <int G>
 constexpr size_t smem_bytes() {
   return static_cast<size_t>(warps_of(G)) *
-             (3 * kUnitBytes + 2 * G * kHeadDim * 2 + 2 * sizeof(UnitHeader) + 3 * sizeof(uint64_t)) +
+             (3 * kUnitBytes + 2 * G * kHeadDim * 2 + (G > 2 ? 4096 : 0) + sizeof(WarpInfo)) +
          (3 * kMaxSeqs + 1 + (kClasses + 1) * 32) * sizeof(int);
 }
 static_assert(smem_bytes<2>() <= 227 * 1024 && smem_bytes<4>() <= 227 * 1024,
@@ -891,16 +1014,17 @@ static_assert(smem_bytes<2>() <= 227 * 1024 && smem_bytes<4>() <= 227 * 1024,
 
 template <Elem E, int G>
 cudaError_t launch_typed(const Q4DecodeParams& p, cudaStream_t stream) {
-  static bool attr_done[64] = {false};
+  static int sm_count[64] = {0};  // 0: this device's attributes are not set yet
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+  if (dev >= 0 && dev < 64) sms = sm_count[dev];
+  if (sms == 0) {
     const cudaError_t e = cudaFuncSetAttribute(q4_decode_kernel<E, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<G>()));
     if (e != cudaSuccess) return e;
-    attr_done[dev] = true;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
+    if (dev >= 0 && dev < 64) sm_count[dev] = sms;
   }
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
   q4_decode_kernel<E, G><<<sms, warps_of(G) * 32, smem_bytes<G>(), stream>>>(p);
   return cudaGetLastError();
 }
