@@ -35,6 +35,12 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t packed) {
   return __half22float2(*reinterpret_cast<const __half2*>(&packed));
 }
 
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Packed pair max / min that keep a NaN of either operand.
 template <Elem E>
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
@@ -55,81 +61,146 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The scale, the minimum and what the codes are computed with, of a group whose
+// packed (pairwise) maximum and minimum are given.
+struct Q4Group {
+  uint32_t param;  // s in the low half, z in the high half
+  float s, z;
+  float rs;        // 1 / s, off by 2^-22 of it at most; 0 where s is 0
+  bool plain;      // no quotient leaves [-0.5, 15.5], so none needs clamping
+  bool finite;
+};
+template <Elem E>
+__device__ __forceinline__ Q4Group q4_group(uint32_t mx2, uint32_t mn2) {
+  using Ops = ElemOps<E>;
+  mx2 = max2_nan<E>(mx2, __byte_perm(mx2, mx2, 0x1032));
+  mn2 = min2_nan<E>(mn2, __byte_perm(mn2, mn2, 0x1032));
+  const float mx = Ops::lo(mx2), mn = Ops::lo(mn2);
+  Q4Group g;
+  g.finite = fabsf(mx) < INFINITY && fabsf(mn) < INFINITY;  // false for NaN too
+  const float hi = fminf(fmaxf(mx, -kF16Max), kF16Max), lo = fminf(fmaxf(mn, -kF16Max), kF16Max);
+  const __half hs = __float2half_rn(__fdiv_rn(hi - lo, 15.f)), hz = __float2half_rn(lo);
+  g.param = g.finite ? static_cast<uint32_t>(__half_as_ushort(hs)) | (static_cast<uint32_t>(__half_as_ushort(hz)) << 16)
+                     : 0x7fff7fffu;
+  g.s = __half2float(hs);
+  g.z = __half2float(hz);
+  g.rs = g.s > 0.f ? __fdividef(1.f, g.s) : 0.f;
+  // A normal s is off by 2^-11 of itself, and z (exact in fp16 but below 2^-14,
+  // where it is off by 2^-25) by 2^-11 s at most: quotients stay below 15.02.
+  g.plain = g.finite && g.s >= 6.103515625e-5f && mx <= kF16Max && mn >= -kF16Max;
+  return g;
+}
+
+// Codes of 8 elements, element p in bits 4p..4p+3. They are those of the
+// definition exactly, also next to a border between two codes: the fp32 quotient
+// is off by less than 15.5 * 2^-21 < 2^-17, so only elements whose quotient lies
+// within 2^-16 of a border are decided again, from the sign of
+// x - z - (k + 1/2) s. There the fp32 difference t = x - z cancels against
+// (k + 1/2) s (16 bits) without rounding, and what t itself was rounded by is
+// added back.
+template <Elem E>
+__device__ __forceinline__ uint32_t q4_codes(const uint4 raw, const Q4Group& g) {
+  using Ops = ElemOps<E>;
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  constexpr float kNear = 0.5f - 1.52587890625e-5f;
+  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+  const uint64_t nz2 = f32x2_pack(-g.z, -g.z), rs2 = f32x2_pack(g.rs, g.rs);
+  const uint64_t round2 = f32x2_pack(kRound, kRound), nround2 = f32x2_pack(-kRound, -kRound);
+  float far = 0.f;
+  uint32_t v[8];  // the rounded quotients as floats 1.5 * 2^23 + code
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t y = f32x2_mul(f32x2_add(f32x2_pack(Ops::lo(in[i]), Ops::hi(in[i])), nz2), rs2);
+    const uint64_t r = f32x2_add(y, round2);
+    const uint64_t k = f32x2_add(r, nround2);
+    float y0, y1, k0, k1, r0, r1;
+    f32x2_unpack(y, y0, y1);
+    f32x2_unpack(k, k0, k1);
+    f32x2_unpack(r, r0, r1);
+    far = fmaxf(far, fabsf(y0 - k0));
+    far = fmaxf(far, fabsf(y1 - k1));
+    v[2 * i] = __float_as_uint(r0);
+    v[2 * i + 1] = __float_as_uint(r1);
+  }
+  if (!(g.plain && far <= kNear)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = (i & 1) ? Ops::hi(in[i / 2]) : Ops::lo(in[i / 2]);
+      const float t = x - g.z;
+      const float y = fminf(fmaxf(t * g.rs, 0.f), 15.f);
+      float k = (y + kRound) - kRound;
+      const float d = y - k;
+      if (fabsf(d) > kNear) {
+        const float lower = d > 0.f ? k : k - 1.f;
+        const float b = t - x;
+        const float lost = (x - (t - b)) + (-g.z - b);  // x - z == t + lost
+        const float side = fmaf(-(lower + 0.5f), g.s, t) + lost;
+        const bool odd = (static_cast<int>(lower) & 1) != 0;
+        k = (side > 0.f || (side == 0.f && odd)) ? lower + 1.f : lower;
+      }
+      v[i] = g.finite ? static_cast<uint32_t>(static_cast<int>(k)) : 0u;
+    }
+  }
+  // halves: codes 0..3 and 4..7; a code is the low 16 bits of v
+  uint32_t w = __byte_perm(v[0], v[4], 0x5410);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) w += __byte_perm(v[i], v[i + 4], 0x5410) << (4 * i);
+  return w;
+}
+
 // Quantises 8 consecutive dims per lane; the 4 lanes of an aligned lane quad
-// hold one group of 32 (all 32 lanes call this). Returns the 8 codes, dim p in
-// bits 4p..4p+3, and the group's parameters (s low half, z high half).
-//
-// The codes are those of the definition exactly, also next to a border between
-// two codes: the fp32 quotient is off by less than 15 * 2^-21 < 2^-17, so only
-// an element whose quotient lies within 2^-16 of a border is decided again,
-// from the sign of x - z - (k + 1/2) s. There the fp32 difference t = x - z
-// cancels against (k + 1/2) s (16 bits) without rounding, and what t itself
-// was rounded by is added back.
+// hold one group of 32 (all 32 lanes call this).
 template <Elem E>
 __device__ __forceinline__ uint32_t quantise8(const uint4 raw, uint32_t& param) {
-  using Ops = ElemOps<E>;
-  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t mx2 = max2_nan<E>(max2_nan<E>(in[0], in[1]), max2_nan<E>(in[2], in[3]));
-  uint32_t mn2 = min2_nan<E>(min2_nan<E>(in[0], in[1]), min2_nan<E>(in[2], in[3]));
+  uint32_t mx2 = max2_nan<E>(max2_nan<E>(raw.x, raw.y), max2_nan<E>(raw.z, raw.w));
+  uint32_t mn2 = min2_nan<E>(min2_nan<E>(raw.x, raw.y), min2_nan<E>(raw.z, raw.w));
 #pragma unroll
   for (int off = 1; off <= 2; off <<= 1) {
     mx2 = max2_nan<E>(mx2, __shfl_xor_sync(0xffffffffu, mx2, off));
     mn2 = min2_nan<E>(mn2, __shfl_xor_sync(0xffffffffu, mn2, off));
   }
-  mx2 = max2_nan<E>(mx2, __byte_perm(mx2, mx2, 0x1032));
-  mn2 = min2_nan<E>(mn2, __byte_perm(mn2, mn2, 0x1032));
-  float mx = Ops::lo(mx2), mn = Ops::lo(mn2);
-  if (!(fabsf(mx) < INFINITY && fabsf(mn) < INFINITY)) {
-    param = 0x7fff7fffu;
-    return 0u;
-  }
-  mx = fminf(fmaxf(mx, -kF16Max), kF16Max);
-  mn = fminf(fmaxf(mn, -kF16Max), kF16Max);
-  const __half hs = __float2half_rn(__fdiv_rn(mx - mn, 15.f)), hz = __float2half_rn(mn);
-  param = static_cast<uint32_t>(__half_as_ushort(hs)) | (static_cast<uint32_t>(__half_as_ushort(hz)) << 16);
-  const float s = __half2float(hs), z = __half2float(hz);
-  const float rs15 = s > 0.f ? __fdividef(1.f, 15.f * s) : 0.f;
-  float x[8], k[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = Ops::lo(in[i]);
-    x[2 * i + 1] = Ops::hi(in[i]);
-  }
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-  float far = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float u = __saturatef((x[i] - z) * rs15);  // (x - z) / (15 s), clamped to [0, 1]
-    k[i] = fmaf(u, 15.f, kRound) - kRound;
-    far = fmaxf(far, fabsf(fmaf(u, 15.f, -k[i])));
-  }
-  if (far > 0.5f - 1.52587890625e-5f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = x[i] - z;
-      const float d = fmaf(__saturatef(t * rs15), 15.f, -k[i]);
-      if (fabsf(d) > 0.5f - 1.52587890625e-5f) {
-        const float lower = d > 0.f ? k[i] : k[i] - 1.f;
-        const float b = t - x[i];
-        const float lost = (x[i] - (t - b)) + (-z - b);  // x - z == t + lost
-        const float side = fmaf(-(lower + 0.5f), s, t) + lost;
-        const bool odd = (static_cast<int>(lower) & 1) != 0;
-        k[i] = (side > 0.f || (side == 0.f && odd)) ? lower + 1.f : lower;
-      }
-    }
-  }
-  // four codes are one exact integer below 2^16 in fp32
-  const float lo = fmaf(4096.f, k[3], fmaf(256.f, k[2], fmaf(16.f, k[1], k[0])));
-  const float hi = fmaf(4096.f, k[7], fmaf(256.f, k[6], fmaf(16.f, k[5], k[4])));
-  return __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
+  const Q4Group g = q4_group<E>(mx2, mn2);
+  param = g.param;
+  return q4_codes<E>(raw, g);
+}
+
+// The same of 16 dims per lane, two lanes to a group: dims 8u.. (raw0) and
+// 16 + 8u.. (raw1) of the group for lane u of an aligned pair.
+template <Elem E>
+__device__ __forceinline__ void quantise16(const uint4 raw0, const uint4 raw1, uint32_t& param, uint32_t& codes0,
+                                           uint32_t& codes1) {
+  uint32_t mx2 = max2_nan<E>(max2_nan<E>(max2_nan<E>(raw0.x, raw0.y), max2_nan<E>(raw0.z, raw0.w)),
+                             max2_nan<E>(max2_nan<E>(raw1.x, raw1.y), max2_nan<E>(raw1.z, raw1.w)));
+  uint32_t mn2 = min2_nan<E>(min2_nan<E>(min2_nan<E>(raw0.x, raw0.y), min2_nan<E>(raw0.z, raw0.w)),
+                             min2_nan<E>(min2_nan<E>(raw1.x, raw1.y), min2_nan<E>(raw1.z, raw1.w)));
+  mx2 = max2_nan<E>(mx2, __shfl_xor_sync(0xffffffffu, mx2, 1));
+  mn2 = min2_nan<E>(mn2, __shfl_xor_sync(0xffffffffu, mn2, 1));
+  const Q4Group g = q4_group<E>(mx2, mn2);
+  param = g.param;
+  codes0 = q4_codes<E>(raw0, g);
+  codes1 = q4_codes<E>(raw1, g);
 }
 
 // The V word of lane (j, t) of a row's 16 lanes (lane 4 j + t): chunk
-// 2 t + (j & 1), fields j & ~1 and j | 1, from every lane's 8 dims 8 (4 j + t)...
-// The same exchange turns such words back into dims.
+// 2 t + (j & 1), fields j & ~1 and j | 1, from every lane's own 8 dims 8 (4 j + t)...
 __device__ __forceinline__ uint32_t v_exchange(uint32_t own, int j) {
   const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 4);
   return (j & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+}
+
+// The same where 8 lanes share a row, lane 2 j + u holding t = u (own0) and
+// t = u + 2 (own1): chunks 2 u + (j & 1) and 2 u + 4 + (j & 1). The exchange is
+// its own inverse, so it also turns such words back into dims.
+__device__ __forceinline__ void v_exchange2(uint32_t& own0, uint32_t& own1, int j) {
+  const uint32_t send = (j & 1) ? __byte_perm(own0, own1, 0x5410) : __byte_perm(own0, own1, 0x7632);
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, send, 2);
+  if (j & 1) {
+    own0 = __byte_perm(other, own0, 0x7610);
+    own1 = __byte_perm(other, own1, 0x7632);
+  } else {
+    own0 = __byte_perm(own0, other, 0x5410);
+    own1 = __byte_perm(own1, other, 0x7610);
+  }
 }
 
 // Byte offsets within a tile, for lane (j, t) of token `tok` of the tile.
@@ -138,12 +209,6 @@ __device__ __forceinline__ int q4_v_word(int tok, int j, int t) {
   return tok * kQ4CodeBytes + ((2 * t + (j & 1)) ^ (tok & 4)) * 8 + (j >> 1) * 4;
 }
 __device__ __forceinline__ int q4_param(int tok, int j) { return kQ4TileParams + tok * kQ4ParamBytes + 4 * j; }
-
-__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
   uint32_t r;

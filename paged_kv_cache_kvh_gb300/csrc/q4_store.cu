@@ -4,20 +4,23 @@
 // slot_mapping[i]; pkv_load_kvcache_q4 is its inverse, a gather of slots into
 // 16-bit rows. The format and the quantiser are in q4.cuh.
 //
-// Both move (512 + 160) bytes per (token, kv head) and are bound by HBM. A
-// 256-thread block takes 16 consecutive tokens of one kv head, 16 lanes to a
-// row and 8 dims (16 bytes) of K and of V to a lane: a row is read or written
-// as 256 contiguous bytes, and where the slots are consecutive (a prompt) the
-// block covers one whole 1280-byte tile of the cache. Heads vary fastest over
-// the grid, so the blocks that share the tokens' 2 KB rows run together.
+// Both move (512 + 160) bytes per (token, kv head) and are bound by HBM, the
+// store nearly as much by the instructions of the quantiser. Eight lanes share a
+// row, lane 2 j + u holding 16 of group j's 32 dims, in two 16-byte pieces
+// chosen so that each load or store of a warp covers whole 32-byte sectors; what
+// a group costs once (its scale) is then spread over twice the elements that
+// sixteen lanes to a row would give it. A 256-thread block takes 32 consecutive
+// tokens of one kv head: where the slots are consecutive (a prompt) it covers two
+// whole 1280-byte tiles of the cache. Heads vary fastest over the grid, so the
+// blocks that share the tokens' rows run together.
 #include "q4.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kRowsPerBlock = 16;
-constexpr int kThreads = kRowsPerBlock * 16;
+constexpr int kRowsPerBlock = 32;
+constexpr int kThreads = kRowsPerBlock * 8;
 
 struct Q4RowsParams {
   const uint16_t* k;  // rows in (store); strides in elements
@@ -69,55 +72,68 @@ __device__ __forceinline__ int64_t tile_offset(int64_t slot, int32_t hkv, int32_
 
 template <Elem E, bool kAligned>
 __global__ void __launch_bounds__(kThreads) store_q4_kernel(const Q4RowsParams p) {
-  const int lane16 = threadIdx.x & 15, j = lane16 >> 2, t = lane16 & 3;
+  const int lane8 = threadIdx.x & 7, j = lane8 >> 1, u = lane8 & 1;
   const int head = static_cast<int>(blockIdx.x);
   const int64_t token = (static_cast<int64_t>(blockIdx.z) * p.blocks_per_z + blockIdx.y) * kRowsPerBlock +
-                        (threadIdx.x >> 4);
-  const int64_t slot = row_slot(p, token, lane16 == 0 && head == 0);
-  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
+                        (threadIdx.x >> 3);
+  const int64_t slot = row_slot(p, token, lane8 == 0 && head == 0);
+  uint4 kr[2], vr[2];
+  kr[0] = kr[1] = vr[0] = vr[1] = make_uint4(0, 0, 0, 0);
   if (slot >= 0) {
-    const uint16_t* ks = p.k + token * p.k_stride + head * kHeadDim + lane16 * 8;
-    const uint16_t* vs = p.v + token * p.v_stride + head * kHeadDim + lane16 * 8;
-    kr = kAligned ? ld_rows_v4(ks) : ld_rows_u16(ks);
-    vr = kAligned ? ld_rows_v4(vs) : ld_rows_u16(vs);
+    const uint16_t* ks = p.k + token * p.k_stride + head * kHeadDim + 32 * j + 8 * u;
+    const uint16_t* vs = p.v + token * p.v_stride + head * kHeadDim + 32 * j + 8 * u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kr[i] = kAligned ? ld_rows_v4(ks + 16 * i) : ld_rows_u16(ks + 16 * i);
+      vr[i] = kAligned ? ld_rows_v4(vs + 16 * i) : ld_rows_u16(vs + 16 * i);
+    }
   }
-  uint32_t kp, vp;
-  const uint32_t kc = quantise8<E>(kr, kp);
-  const uint32_t vc = v_exchange(quantise8<E>(vr, vp), j);
+  uint32_t kp, vp, kc[2], vc[2];
+  quantise16<E>(kr[0], kr[1], kp, kc[0], kc[1]);
+  quantise16<E>(vr[0], vr[1], vp, vc[0], vc[1]);
+  v_exchange2(vc[0], vc[1], j);
   if (slot < 0) return;
   const int tok = static_cast<int>(slot % kQ4Tile);
   const int64_t off = tile_offset(slot, p.hkv, head);
   uint8_t* kd = p.k_cache + off;
   uint8_t* vd = p.v_cache + off;
-  *reinterpret_cast<uint32_t*>(kd + q4_k_word(tok, j, t)) = kc;
-  *reinterpret_cast<uint32_t*>(vd + q4_v_word(tok, j, t)) = vc;
-  if (t == 0) *reinterpret_cast<uint32_t*>(kd + q4_param(tok, j)) = kp;
-  if (t == 1) *reinterpret_cast<uint32_t*>(vd + q4_param(tok, j)) = vp;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<uint32_t*>(kd + q4_k_word(tok, j, u + 2 * i)) = kc[i];
+    *reinterpret_cast<uint32_t*>(vd + q4_v_word(tok, j, u + 2 * i)) = vc[i];
+  }
+  *reinterpret_cast<uint32_t*>((u == 0 ? kd : vd) + q4_param(tok, j)) = u == 0 ? kp : vp;
 }
 
 template <Elem E>
 __global__ void __launch_bounds__(kThreads) load_q4_kernel(const Q4RowsParams p) {
-  const int lane16 = threadIdx.x & 15, j = lane16 >> 2, t = lane16 & 3;
+  const int lane8 = threadIdx.x & 7, j = lane8 >> 1, u = lane8 & 1;
   const int head = static_cast<int>(blockIdx.x);
   const int64_t token = (static_cast<int64_t>(blockIdx.z) * p.blocks_per_z + blockIdx.y) * kRowsPerBlock +
-                        (threadIdx.x >> 4);
-  const int64_t slot = row_slot(p, token, lane16 == 0 && head == 0);
-  uint32_t kc = 0, vc = 0, kp = 0, vp = 0;
+                        (threadIdx.x >> 3);
+  const int64_t slot = row_slot(p, token, lane8 == 0 && head == 0);
+  uint32_t kc[2] = {0, 0}, vc[2] = {0, 0}, kp = 0, vp = 0;
   if (slot >= 0) {
     const int tok = static_cast<int>(slot % kQ4Tile);
     const int64_t off = tile_offset(slot, p.hkv, head);
     const uint8_t* ks = p.k_cache + off;
     const uint8_t* vs = p.v_cache + off;
-    kc = *reinterpret_cast<const uint32_t*>(ks + q4_k_word(tok, j, t));
-    vc = *reinterpret_cast<const uint32_t*>(vs + q4_v_word(tok, j, t));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kc[i] = *reinterpret_cast<const uint32_t*>(ks + q4_k_word(tok, j, u + 2 * i));
+      vc[i] = *reinterpret_cast<const uint32_t*>(vs + q4_v_word(tok, j, u + 2 * i));
+    }
     kp = *reinterpret_cast<const uint32_t*>(ks + q4_param(tok, j));
     vp = *reinterpret_cast<const uint32_t*>(vs + q4_param(tok, j));
   }
-  vc = v_exchange(vc, j);
+  v_exchange2(vc[0], vc[1], j);
   if (slot < 0) return;
-  const int64_t row = (token * p.hkv + head) * kHeadDim + lane16 * 8;
-  *reinterpret_cast<uint4*>(p.k_out + row) = dequantise8<E>(kc, kp);
-  *reinterpret_cast<uint4*>(p.v_out + row) = dequantise8<E>(vc, vp);
+  const int64_t row = (token * p.hkv + head) * kHeadDim + 32 * j + 8 * u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<uint4*>(p.k_out + row + 16 * i) = dequantise8<E>(kc[i], kp);
+    *reinterpret_cast<uint4*>(p.v_out + row + 16 * i) = dequantise8<E>(vc[i], vp);
+  }
 }
 
 dim3 rows_grid(Q4RowsParams& p) {
