@@ -105,40 +105,41 @@ __device__ __forceinline__ uint32_t q4_codes(const uint4 raw, const Q4Group& g) 
   constexpr float kNear = 0.5f - 1.52587890625e-5f;
   const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
   const uint64_t nz2 = f32x2_pack(-g.z, -g.z), rs2 = f32x2_pack(g.rs, g.rs);
-  const uint64_t round2 = f32x2_pack(kRound, kRound), nround2 = f32x2_pack(-kRound, -kRound);
+  const uint64_t round2 = f32x2_pack(kRound, kRound), minus2 = f32x2_pack(-1.f, -1.f);
   float far = 0.f;
   uint32_t v[8];  // the rounded quotients as floats 1.5 * 2^23 + code
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint64_t y = f32x2_mul(f32x2_add(f32x2_pack(Ops::lo(in[i]), Ops::hi(in[i])), nz2), rs2);
     const uint64_t r = f32x2_add(y, round2);
-    const uint64_t k = f32x2_add(r, nround2);
-    float y0, y1, k0, k1, r0, r1;
-    f32x2_unpack(y, y0, y1);
-    f32x2_unpack(k, k0, k1);
+    float d0, d1, r0, r1;
+    f32x2_unpack(f32x2_add(y, f32x2_fma(r, minus2, round2)), d0, d1);  // y - k, k = r - 1.5 * 2^23
     f32x2_unpack(r, r0, r1);
-    far = fmaxf(far, fabsf(y0 - k0));
-    far = fmaxf(far, fabsf(y1 - k1));
+    far = fmax3(far, fabsf(d0), fabsf(d1));
     v[2 * i] = __float_as_uint(r0);
     v[2 * i + 1] = __float_as_uint(r1);
   }
   if (!(g.plain && far <= kNear)) {
+    // (bf16 rows meet exact ties often enough for some lane of a warp to come
+    // here in every fifth call)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = (i & 1) ? Ops::hi(in[i / 2]) : Ops::lo(in[i / 2]);
       const float t = x - g.z;
-      const float y = fminf(fmaxf(t * g.rs, 0.f), 15.f);
-      float k = (y + kRound) - kRound;
+      float y = t * g.rs;
+      if (!g.plain) y = fminf(fmaxf(y, 0.f), 15.f);
+      const float r = y + kRound, k = r - kRound;
       const float d = y - k;
+      v[i] = __float_as_uint(r);
       if (fabsf(d) > kNear) {
         const float lower = d > 0.f ? k : k - 1.f;
         const float b = t - x;
         const float lost = (x - (t - b)) + (-g.z - b);  // x - z == t + lost
         const float side = fmaf(-(lower + 0.5f), g.s, t) + lost;
-        const bool odd = (static_cast<int>(lower) & 1) != 0;
-        k = (side > 0.f || (side == 0.f && odd)) ? lower + 1.f : lower;
+        const uint32_t lo = __float_as_uint(lower + kRound);
+        v[i] = lo + ((side > 0.f || (side == 0.f && (lo & 1u) != 0u)) ? 1u : 0u);
       }
-      v[i] = g.finite ? static_cast<uint32_t>(static_cast<int>(k)) : 0u;
+      if (!g.finite) v[i] = 0u;
     }
   }
   // halves: codes 0..3 and 4..7; a code is the low 16 bits of v

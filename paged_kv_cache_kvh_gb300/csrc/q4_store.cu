@@ -71,7 +71,7 @@ __device__ __forceinline__ int64_t tile_offset(int64_t slot, int32_t hkv, int32_
 }
 
 template <Elem E, bool kAligned>
-__global__ void __launch_bounds__(kThreads) store_q4_kernel(const Q4RowsParams p) {
+__global__ void __launch_bounds__(kThreads, 5) store_q4_kernel(const Q4RowsParams p) {
   const int lane8 = threadIdx.x & 7, j = lane8 >> 1, u = lane8 & 1;
   const int head = static_cast<int>(blockIdx.x);
   const int64_t token = (static_cast<int64_t>(blockIdx.z) * p.blocks_per_z + blockIdx.y) * kRowsPerBlock +
