@@ -212,46 +212,57 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 
-// Merges n partials (slots first, first + stride, ...) of one query head, 4 dims
-// per lane: o = sum 2^(m - M) o_i, l = sum 2^(m - M) l_i, M the largest m.
-__device__ __forceinline__ void merge_slots(const Q4DecodeParams& p, int64_t first, int64_t stride, int n, int G, int h,
-                                            int lane, float& M, float& den, float4& acc) {
-  constexpr int kAhead = 4;  // the partials sit in L2: loads of four slots in flight
-  M = -INFINITY;
-  den = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+// Merges n partials (slots first, first + stride, ...) of all G query heads, 4
+// dims per lane: o = sum 2^(m - M) o_i, l = sum 2^(m - M) l_i, M the largest m.
+// The partials sit in L2: the loads of kAhead slots and every head are in flight
+// together.
+template <int G>
+__device__ __forceinline__ void merge_slots(const Q4DecodeParams& p, int64_t first, int64_t stride, int n, int lane,
+                                            float (&M)[G], float (&den)[G], float4 (&acc)[G]) {
+  constexpr int kAhead = G == 1 ? 8 : G == 2 ? 4 : 2;
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    M[h] = -INFINITY;
+    den[h] = 0.f;
+    acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 1
   for (int c0 = 0; c0 < n; c0 += kAhead) {
-    float2 ml[kAhead];
-    float4 o[kAhead];
+    float2 ml[kAhead][G];
+    float4 o[kAhead][G];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c0 + i < n) {
-        const int64_t slot = (first + (c0 + i) * stride) * G + h;
-        ml[i] = __ldcg(p.ml + slot);
-        o[i] = __ldcg(reinterpret_cast<const float4*>(p.opart + slot * kHeadDim) + lane);
+      const int64_t slot = (first + min(c0 + i, n - 1) * stride) * G;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        ml[i][h] = __ldcg(p.ml + slot + h);
+        o[i][h] = __ldcg(reinterpret_cast<const float4*>(p.opart + (slot + h) * kHeadDim) + lane);
+        if (c0 + i >= n) ml[i][h].x = -INFINITY;  // the last one again: no weight
       }
     }
-    float Mg = M;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) Mg = fmaxf(Mg, ml[i].x);
-    const float Mu = (Mg == -INFINITY) ? 0.f : Mg;
-    const float sc = ex2_approx(M - Mu);
-    M = Mg;
-    den *= sc;
-    acc.x *= sc;
-    acc.y *= sc;
-    acc.z *= sc;
-    acc.w *= sc;
+    for (int h = 0; h < G; ++h) {
+      float Mg = M[h];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const float w = ex2_approx(ml[i].x - Mu);
-      den = fmaf(w, ml[i].y, den);
-      acc.x = fmaf(w, o[i].x, acc.x);
-      acc.y = fmaf(w, o[i].y, acc.y);
-      acc.z = fmaf(w, o[i].z, acc.z);
-      acc.w = fmaf(w, o[i].w, acc.w);
+      for (int i = 0; i < kAhead; ++i) Mg = fmaxf(Mg, ml[i][h].x);
+      const float Mu = (Mg == -INFINITY) ? 0.f : Mg;
+      const float sc = ex2_approx(M[h] - Mu);
+      M[h] = Mg;
+      den[h] *= sc;
+      acc[h].x *= sc;
+      acc[h].y *= sc;
+      acc[h].z *= sc;
+      acc[h].w *= sc;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const bool there = c0 + i < n;  // 0 * NaN must not be added
+        const float w = ex2_approx(ml[i][h].x - Mu);
+        den[h] = there ? fmaf(w, ml[i][h].y, den[h]) : den[h];
+        acc[h].x = there ? fmaf(w, o[i][h].x, acc[h].x) : acc[h].x;
+        acc[h].y = there ? fmaf(w, o[i][h].y, acc[h].y) : acc[h].y;
+        acc[h].z = there ? fmaf(w, o[i][h].z, acc[h].z) : acc[h].z;
+        acc[h].w = there ? fmaf(w, o[i][h].w, acc[h].w) : acc[h].w;
+      }
     }
   }
 }
@@ -911,14 +922,14 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       int n = in_group;
       if (merge && nch > kFan) {
         // merge the group into its first slot, then the groups
-#pragma unroll 1
+        float M[G], den[G];
+        float4 a[G];
+        merge_slots<G>(p, slot_g, p.hkv, in_group, lane, M, den, a);
+        __syncwarp();  // every lane has read the slot that is overwritten
+#pragma unroll
         for (int h = 0; h < G; ++h) {
-          float M, den;
-          float4 a;
-          merge_slots(p, slot_g, p.hkv, in_group, G, h, lane, M, den, a);
-          reinterpret_cast<float4*>(p.opart + (slot_g * G + h) * kHeadDim)[lane] = a;
-          __syncwarp();
-          if (lane == 0) p.ml[slot_g * G + h] = make_float2(M, den);
+          reinterpret_cast<float4*>(p.opart + (slot_g * G + h) * kHeadDim)[lane] = a[h];
+          if (lane == 0) p.ml[slot_g * G + h] = make_float2(M[h], den[h]);
         }
         at = static_cast<int64_t>(first_chunk) * p.hkv + pend_head;
         stride = static_cast<int64_t>(kFan) * p.hkv;
@@ -927,15 +938,15 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       }
       if (merge) {
         uint16_t* orow = p.out + (static_cast<int64_t>(pend_b) * p.hkv + pend_head) * G * kHeadDim;
-#pragma unroll 1
+        float M[G], den[G];
+        float4 a[G];
+        merge_slots<G>(p, at, stride, n, lane, M, den, a);
+#pragma unroll
         for (int h = 0; h < G; ++h) {
-          float M, den;
-          float4 a;
-          merge_slots(p, at, stride, n, G, h, lane, M, den, a);
-          const float inv = den == 0.f ? 0.f : 1.f / den;
+          const float inv = den[h] == 0.f ? 0.f : 1.f / den[h];
           uint2 v;
-          v.x = Ops::pack(a.x * inv, a.y * inv);
-          v.y = Ops::pack(a.z * inv, a.w * inv);
+          v.x = Ops::pack(a[h].x * inv, a[h].y * inv);
+          v.y = Ops::pack(a[h].z * inv, a[h].w * inv);
           reinterpret_cast<uint2*>(orow + h * kHeadDim)[lane] = v;
         }
       }
