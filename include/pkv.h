@@ -332,8 +332,9 @@ int pkv_decode_noalloc(const void* q, int64_t q_row_stride, const void* k_cache,
  * needs no initialisation: only stored tokens are read (bytes of others may be
  * fetched, but never reach a result).
  *
- * Supported: head_dim 128, block_size 256, any num_kv_heads up to 8192; for
- * attention 1, 2 or 4 query heads to a kv head (prefill: 2 or 4). The rows
+ * Supported: head_dim 128, block_size 256, any num_kv_heads; for attention one
+ * or an even number of query heads to a kv head (prefill: an even number), up
+ * to 8192 heads. The rows
  * (q, k, v, out) are bf16, or fp16 for the *_f16 names; the cache is the same
  * for both. Sizes of 0 are no-ops.
  */

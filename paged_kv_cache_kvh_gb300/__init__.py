@@ -530,8 +530,8 @@ def _decode_q4(entry, dtype, q, new, k_cache, v_cache, block_tables, context_len
 
 def pkv_decode_q4(q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace, *,
                   out=None, stream=None):
-    """pkv_decode over the 4-bit cache. q [B, num_heads, 128] bf16 with 1, 2 or 4 query heads
-    to a kv head of the caches. Returns out [B, num_heads, 128] bf16."""
+    """pkv_decode over the 4-bit cache. q [B, num_heads, 128] bf16 with one or an even number of
+    query heads to a kv head of the caches. Returns out [B, num_heads, 128] bf16."""
     return _decode_q4("pkv_decode_q4", torch.bfloat16, q, None, k_cache, v_cache, block_tables, context_lens,
                       max_context_len, softmax_scale, workspace, out, stream)
 
@@ -591,7 +591,7 @@ def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_s
 def pkv_prefill_varlen_q4(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache, v_cache,
                           block_tables, *, out=None, plan=None, stream=None):
     """pkv_prefill_varlen in prefix-cache mode over the 4-bit cache (new tokens stored first).
-    q [total_q, num_heads, 128] bf16, 2 or 4 query heads to a kv head; plan: optional tile plan
+    q [total_q, num_heads, 128] bf16, an even number of query heads to a kv head; plan: optional tile plan
     (pkv_prefill_plan). Returns out [total_q, num_heads, 128] bf16."""
     return _prefill_q4("pkv_prefill_varlen_q4", torch.bfloat16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                        max_seqlen_k, softmax_scale, k_cache, v_cache, block_tables, out, plan, stream)

@@ -1,8 +1,8 @@
 // q4_abi.cu -- extern "C" entry points of the 4-bit paged cache (declared in include/pkv.h).
 //
 // Arguments are checked on the host before anything is launched, like those of
-// the 16-bit entry points. These kernels take any number of kv heads, with 1, 2
-// or 4 query heads to each.
+// the 16-bit entry points. These kernels take any number of kv heads, with one or
+// an even number of query heads to each.
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -35,7 +35,7 @@ cudaError_t launch_prefill_q4(const void* q, int64_t q_row_stride, int32_t total
 
 namespace {
 
-constexpr int32_t kMaxKvHeads = 8192;  // as pkv_store_kvcache: rows of at most 2^20 elements
+constexpr int32_t kMaxHeads = 8192;  // as pkv_store_kvcache: rows of at most 2^20 elements
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -46,16 +46,17 @@ int launched(cudaError_t e) {
 }
 
 int check_cache_shape(int32_t num_kv_heads, int32_t head_dim, int32_t block_size) {
-  if (head_dim != pkv::kHeadDim || block_size != pkv::kBlockSize || num_kv_heads <= 0 || num_kv_heads > kMaxKvHeads)
+  if (head_dim != pkv::kHeadDim || block_size != pkv::kBlockSize || num_kv_heads <= 0 || num_kv_heads > kMaxHeads)
     return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
 
-// The query heads must be 1, 2 or 4 to a kv head.
+// Query heads come one to a kv head, or in pairs that share one.
 int check_heads(int32_t num_heads, int32_t num_kv_heads) {
-  if (num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads != 0) return PKV_ERR_UNSUPPORTED;
+  if (num_kv_heads <= 0 || num_heads <= 0 || num_heads > kMaxHeads || num_heads % num_kv_heads != 0)
+    return PKV_ERR_UNSUPPORTED;
   const int32_t g = num_heads / num_kv_heads;
-  return g == 1 || g == 2 || g == 4 ? PKV_OK : PKV_ERR_UNSUPPORTED;
+  return g == 1 || g % 2 == 0 ? PKV_OK : PKV_ERR_UNSUPPORTED;
 }
 
 int store_common(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride, void* k_cache,
@@ -215,7 +216,7 @@ int pkv_load_kvcache_q4_f16(const void* k_cache, const void* v_cache, const int3
 size_t pkv_decode_q4_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                      int32_t max_context_len) {
   if (num_seqs <= 0 || num_seqs > 65535 || max_context_len < 0 || max_context_len > (1 << 24) ||
-      num_kv_heads > kMaxKvHeads || check_heads(num_heads, num_kv_heads) != PKV_OK)
+      num_kv_heads > kMaxHeads || check_heads(num_heads, num_kv_heads) != PKV_OK)
     return 0;
   return pkv::decode_q4_workspace_bytes(num_seqs, num_kv_heads, num_heads / num_kv_heads, max_context_len);
 }

@@ -65,11 +65,8 @@ constexpr int kFirst = 1 << 8, kLast = 1 << 9, kNew = 1 << 10;  // a unit's flag
 constexpr uint32_t kTf32Mask = 0xffffe000u;                  // the bits that a tf32 operand keeps
 constexpr uint32_t kOne = 0x3f800000u;                       // 1.0f
 
-// Warps per CTA (one CTA per SM) for G query heads to a kv head.
-#ifndef PKV_Q4_WARPS
-#define PKV_Q4_WARPS 12
-#endif
-__host__ __device__ constexpr int warps_of(int G) { return G <= 2 ? PKV_Q4_WARPS : 8; }
+constexpr int kWarps = 12;                                   // per CTA; one CTA per SM
+constexpr int kThreads = kWarps * 32;
 
 // A warp's shared memory: two units of K, one of V, the query rows of two items
 // (they arrive with an item's first K), and what its lanes share about them.
@@ -88,6 +85,8 @@ struct Q4DecodeParams {
   const uint8_t* v_cache;
   int32_t num_blocks;
   int32_t hkv;
+  int32_t rows;   // items per (sequence, chunk): pairs of query heads that share a kv head, or single ones
+  int32_t share;  // rows per kv head
   const int32_t* block_tables;
   int32_t bt_stride;
   const int32_t* context_lens;
@@ -115,8 +114,8 @@ struct Q4DecodeParams {
 // 32 tokens (a short call is bound by the time of one chunk). Otherwise whole
 // units: x is the number that each warp would get; up to kMaxChunk, one chunk
 // each; beyond, as many rounds of equal chunks as keep a chunk within kMaxChunk.
-__host__ __device__ inline int chunk_tokens(int64_t half_units, int64_t units, int warps) {
-  const int64_t plan = int64_t{152} * warps;
+__host__ __device__ inline int chunk_tokens(int64_t half_units, int64_t units) {
+  constexpr int64_t plan = int64_t{152} * kWarps;
   if (half_units <= plan) return kHalfUnit;
   const int64_t x = (units + plan - 1) / plan;
   const int64_t rounds = (x + kMaxChunk - 1) / kMaxChunk;
@@ -134,9 +133,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&d)[4
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
                : "r"(addr));
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
@@ -219,7 +215,7 @@ __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((_
 template <int G>
 __device__ __forceinline__ void merge_slots(const Q4DecodeParams& p, int64_t first, int64_t stride, int n, int lane,
                                             float (&M)[G], float (&den)[G], float4 (&acc)[G]) {
-  constexpr int kAhead = G == 1 ? 8 : G == 2 ? 4 : 2;
+  constexpr int kAhead = G == 1 ? 8 : 4;
 #pragma unroll
   for (int h = 0; h < G; ++h) {
     M[h] = -INFINITY;
@@ -268,14 +264,10 @@ __device__ __forceinline__ void merge_slots(const Q4DecodeParams& p, int64_t fir
 }
 
 template <Elem E, int G>
-__global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodeParams p) {
   using Ops = ElemOps<E>;
-  constexpr int kWarps = warps_of(G), kThreads = kWarps * 32;
-  constexpr int kNB = (G + 1) / 2;            // B operands: pairs of query heads
   constexpr int kQBytes = G * kHeadDim * 2;   // one item's query rows
-  // B fragments of q: in registers, or where those of two pairs of heads would not fit, in shared memory
-  constexpr bool kFragsInSmem = kNB > 1;
-  constexpr int kWarpBytes = 3 * kUnitBytes + 2 * kQBytes + (kFragsInSmem ? kNB * 2048 : 0);
+  constexpr int kWarpBytes = 3 * kUnitBytes + 2 * kQBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   WarpInfo* info_all = reinterpret_cast<WarpInfo*>(smem + kWarps * kWarpBytes);
   int* sF = reinterpret_cast<int*>(info_all + kWarps);  // [num_seqs + 1] whole chunks before b
@@ -311,7 +303,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       halves += __shfl_xor_sync(0xffffffffu, halves, off);
       units += __shfl_xor_sync(0xffffffffu, units, off);
     }
-    chunk = chunk_tokens(static_cast<int64_t>(halves) * p.hkv, static_cast<int64_t>(units) * p.hkv, kWarps);
+    chunk = chunk_tokens(static_cast<int64_t>(halves) * p.rows, static_cast<int64_t>(units) * p.rows);
     const int full = static_cast<int>(static_cast<unsigned>(ctx) / static_cast<unsigned>(chunk));
     int scan = full;
 #pragma unroll
@@ -370,7 +362,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       all_halves += red[w];
       all_units += red[kWarps + w];
     }
-    chunk = chunk_tokens(all_halves * p.hkv, all_units * p.hkv, kWarps);
+    chunk = chunk_tokens(all_halves * p.rows, all_units * p.rows);
     __syncthreads();  // red is written again
     int full[kPer], cls[kPer], scan[kPer];
 #pragma unroll
@@ -429,8 +421,8 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
     if (tid == 0) sF[B] = n_full;
     __syncthreads();
   }
-  const int64_t n_items = static_cast<int64_t>(n_full + n_part) * p.hkv;
-  if (static_cast<int64_t>(n_full + B) * p.hkv > p.max_slots) {  // cannot happen: the workspace bound covers every table
+  const int64_t n_items = static_cast<int64_t>(n_full + n_part) * p.rows;
+  if (static_cast<int64_t>(n_full + B) * p.rows > p.max_slots) {  // cannot happen: the workspace bound covers every table
     if (tid == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
   }
@@ -438,13 +430,13 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   // rows without context: zeros
   for (int b = cta * kWarps + warp; b < B; b += n_ctas * kWarps) {
     if (sCtx[b] == 0) {
-      uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(b) * p.hkv * G * kHeadDim);
-      for (int i = lane; i < p.hkv * G * (kHeadDim / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+      uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(b) * p.rows * G * kHeadDim);
+      for (int i = lane; i < p.rows * G * (kHeadDim / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
     }
   }
 
   const uint32_t k_buf = smem_u32(smem) + warp * kWarpBytes, v_buf = k_buf + 2 * kUnitBytes;
-  const uint32_t q_buf = v_buf + kUnitBytes, frags = q_buf + 2 * kQBytes + lane * 16;
+  const uint32_t q_buf = v_buf + kUnitBytes;
   WarpInfo* info = info_all + warp;
   const uint32_t k_full = smem_u32(info->bars), v_full = k_full + 16;
   const int r = lane >> 2, t = lane & 3;
@@ -467,8 +459,8 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
     fresh = true;
   };
   auto resolve = [&]() {  // item -> sequence, chunk, head (whole warp)
-    const int ci = static_cast<int>(static_cast<unsigned>(item) / static_cast<unsigned>(p.hkv));
-    ihead = static_cast<int>(item) - ci * p.hkv;
+    const int ci = static_cast<int>(static_cast<unsigned>(item) / static_cast<unsigned>(p.rows));
+    ihead = static_cast<int>(item) - ci * p.rows;
     int c;
     if (ci < n_full) {
       // largest b with sF[b] <= ci, 32 probes at a time
@@ -502,7 +494,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       fresh = false;
       ioff = -1;
       if (ipb >= 0 && ipb < p.num_blocks)
-        ioff = (static_cast<int64_t>(ipb) * p.hkv + ihead) * kQ4RecordBytes + (itok % kBlockSize) / kQ4Tile * kQ4TileBytes;
+        ioff = (static_cast<int64_t>(ipb) * p.hkv + ihead / p.share) * kQ4RecordBytes + (itok % kBlockSize) / kQ4Tile * kQ4TileBytes;
       else if (lane == 0)
         flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
     }
@@ -567,10 +559,10 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
   // (r, t) then holds, of tokens 2t, 2t + 1, four dims of group r & 3 per chunk.
   const uint32_t par_off = kQ4TileParams + r * kQ4ParamBytes + t * 4;
   const uint32_t v_off = (lane & 7) * kQ4CodeBytes + (((lane >> 3) ^ ((lane & 4) >> 1)) << 4);
-  uint32_t qb[kFragsInSmem ? 1 : kNB][8][2];  // B fragments of q, one per 16 dims
+  uint32_t qb[8][2];         // B fragments of q, one per 16 dims
   uint32_t qs_b[G][2];       // B fragment of sum q over group t: high and low part
-  float kc[kNB][2];          // per head: the power of two taken out of q and the codes, times scale * log2(e)
-  float acc[kNB][8][4];
+  float kc[2];               // per head: the power of two taken out of q and the codes, times scale * log2(e)
+  float acc[8][4];
   uint64_t l2[G], z2[G];     // sums of p and of p z, tokens r and r + 8 apart
   float m[G];                // running maximum, -INFINITY before the first unit
   float from[G][4];          // minus the maximum that logits are taken relative to (a C fragment)
@@ -599,15 +591,17 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
         const int lane16 = lane & 15, j = lane16 >> 2, tt = lane16 & 3, tok = (ntok - 1) % kQ4Tile;
         const bool is_v = lane >= 16;
         const uint16_t* src = (is_v ? p.v_new + it.x * p.v_new_stride : p.k_new + it.x * p.k_new_stride) +
-                              it.y * kHeadDim + lane16 * 8;
+                              it.y / p.share * kHeadDim + lane16 * 8;
         new_codes = quantise8<E>(*reinterpret_cast<const uint4*>(src), new_par);
         const uint32_t vcodes = v_exchange(new_codes, j);
         if (is_v) new_codes = vcodes;
         const int word = is_v ? q4_v_word(tok, j, tt) : q4_k_word(tok, j, tt);
         const int tile = (ntok - 1) / kQ4Tile * kQ4TileBytes;
         uint8_t* dst = (is_v ? p.v_cache_w : p.k_cache_w) + info->place[s] + tile;
-        *reinterpret_cast<uint32_t*>(dst + word) = new_codes;
-        if (tt == 0) *reinterpret_cast<uint32_t*>(dst + q4_param(tok, j)) = new_par;
+        if (it.y % p.share == 0) {  // one of the items that share the kv head
+          *reinterpret_cast<uint32_t*>(dst + word) = new_codes;
+          if (tt == 0) *reinterpret_cast<uint32_t*>(dst + q4_param(tok, j)) = new_par;
+        }
         if (!is_v) {
           sts32(kst + tile + word, new_codes);
           if (tt == 0) sts32(kst + tile + q4_param(tok, j), new_par);
@@ -616,9 +610,8 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       }
       if (flags & kFirst) {
         // ---- a new item: query fragments ----
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) {
-          const int h = 2 * nb + (r & 1);  // the column's head; its group is r >> 1
+        {
+          const int h = r & 1;  // the column's head; its group is r >> 1
           uint4 raw = make_uint4(0, 0, 0, 0);
           if (h < G) raw = lds128(q_buf + s * kQBytes + h * kHeadDim * 2 + ((r >> 1) * 32 + t * 8) * 2);
           float x[8] = {Ops::lo(raw.x), Ops::hi(raw.x), Ops::lo(raw.y), Ops::hi(raw.y),
@@ -643,27 +636,23 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // group j's two fragments: 0 outside the column's own group
             const bool on = j == (r >> 1);
-            if constexpr (kFragsInSmem) {
-              sts128(frags + nb * 2048 + j * 512, on ? own[0] : 0u, on ? own[1] : 0u, on ? own[2] : 0u, on ? own[3] : 0u);
-            } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) qb[nb][2 * j + i / 2][i & 1] = on ? own[i] : 0u;
-            }
+            for (int i = 0; i < 4; ++i) qb[2 * j + i / 2][i & 1] = on ? own[i] : 0u;
           }
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const float fh = __shfl_sync(0xffffffffu, f, 4 * h2);
-            kc[nb][h2] = __fdividef(16777216.f, fh) * p.scale_log2;
+            kc[h2] = __fdividef(16777216.f, fh) * p.scale_log2;
             const float qs = __shfl_sync(0xffffffffu, sum, (2 * t + h2) * 4) * p.scale_log2;
-            if (2 * nb + h2 < G) {
-              qs_b[(2 * nb + h2) % G][0] = __float_as_uint(qs) & kTf32Mask;
-              qs_b[(2 * nb + h2) % G][1] = __float_as_uint(qs - __uint_as_float(__float_as_uint(qs) & kTf32Mask));
+            if (h2 < G) {
+              qs_b[h2 % G][0] = __float_as_uint(qs) & kTf32Mask;
+              qs_b[h2 % G][1] = __float_as_uint(qs - __uint_as_float(__float_as_uint(qs) & kTf32Mask));
             }
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[nb][i][c] = 0.f;
+            for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
         }
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -685,7 +674,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
             for (int i = 0; i < 4; ++i) lg[h][2 * pair + i / 2][i & 1] = -INFINITY;
           continue;
         }
-        float c[2][kNB][4];
+        float c[2][4];
         uint4 w0[2], w1[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -695,58 +684,39 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4 f[kNB];
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) {
-            if constexpr (kFragsInSmem)
-              f[nb] = lds128(frags + nb * 2048 + j * 512);
-            else
-              f[nb] = make_uint4(qb[nb][2 * j][0], qb[nb][2 * j][1], qb[nb][2 * j + 1][0], qb[nb][2 * j + 1][1]);
-          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t a = j == 0 ? w0[i].x : j == 1 ? w0[i].y : j == 2 ? w0[i].z : w0[i].w;
             const uint32_t b = j == 0 ? w1[i].x : j == 1 ? w1[i].y : j == 2 ? w1[i].z : w1[i].w;
             const uint32_t ah = shift8(a), bh = shift8(b);
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) {
-              if (j == 0)
-                mma16816_first(c[i][nb], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                               f[nb].x, f[nb].y);
-              else
-                mma16816(c[i][nb], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                         f[nb].x, f[nb].y);
-              mma16816(c[i][nb], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u,
-                       f[nb].z, f[nb].w);
-            }
+            if (j == 0)
+              mma16816_first(c[i], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qb[0][0],
+                             qb[0][1]);
+            else
+              mma16816(c[i], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qb[2 * j][0],
+                       qb[2 * j][1]);
+            mma16816(c[i], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, qb[2 * j + 1][0],
+                     qb[2 * j + 1][1]);
           }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t base = kst + (2 * pair + i) * kQ4TileBytes + par_off;
           const float2 sz0 = h2_to_f2(lds32(base)), sz1 = h2_to_f2(lds32(base + 8 * kQ4ParamBytes));
+          float x[4];  // s_g acc_g of [half][head]
+          f32x2_unpack(f32x2_mul(f32x2_pack(c[i][0], c[i][1]), f32x2_pack(sz0.x * kc[0], sz0.x * kc[1])), x[0], x[1]);
+          f32x2_unpack(f32x2_mul(f32x2_pack(c[i][2], c[i][3]), f32x2_pack(sz1.x * kc[0], sz1.x * kc[1])), x[2], x[3]);
 #pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) {
-            float x[4];  // s_g acc_g of [half][head]
-            f32x2_unpack(f32x2_mul(f32x2_pack(c[i][nb][0], c[i][nb][1]),
-                                   f32x2_pack(sz0.x * kc[nb][0], sz0.x * kc[nb][1])), x[0], x[1]);
-            f32x2_unpack(f32x2_mul(f32x2_pack(c[i][nb][2], c[i][nb][3]),
-                                   f32x2_pack(sz1.x * kc[nb][0], sz1.x * kc[nb][1])), x[2], x[3]);
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-              const int h = 2 * nb + h2;
-              if (h < G) {
-                // the sum over the groups (the four lanes t) as a product with ones, plus z . sum q
-                float d[4];
-                const uint32_t h0 = __float_as_uint(x[h2]) & kTf32Mask, h1 = __float_as_uint(x[2 + h2]) & kTf32Mask;
-                mma1688_tf32_from(d, __float_as_uint(sz0.y), __float_as_uint(sz1.y), __float_as_uint(sz0.y),
-                             __float_as_uint(sz1.y), qs_b[h][0], qs_b[h][1], from[h]);
-                mma1688_tf32(d, h0, h1, __float_as_uint(x[h2] - __uint_as_float(h0)),
-                             __float_as_uint(x[2 + h2] - __uint_as_float(h1)), kOne, kOne);
-                lg[h][2 * pair + i][0] = d[0];
-                lg[h][2 * pair + i][1] = d[2];
-              }
-            }
+          for (int h = 0; h < G; ++h) {
+            // the sum over the groups (the four lanes t) as a product with ones, plus z . sum q
+            float d[4];
+            const uint32_t h0 = __float_as_uint(x[h]) & kTf32Mask, h1 = __float_as_uint(x[2 + h]) & kTf32Mask;
+            mma1688_tf32_from(d, __float_as_uint(sz0.y), __float_as_uint(sz1.y), __float_as_uint(sz0.y),
+                              __float_as_uint(sz1.y), qs_b[h][0], qs_b[h][1], from[h]);
+            mma1688_tf32(d, h0, h1, __float_as_uint(x[h] - __uint_as_float(h0)),
+                         __float_as_uint(x[2 + h] - __uint_as_float(h1)), kOne, kOne);
+            lg[h][2 * pair + i][0] = d[0];
+            lg[h][2 * pair + i][1] = d[2];
           }
         }
       }
@@ -815,8 +785,8 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
             z2[h] = f32x2_mul(z2[h], f32x2_pack(sc, sc));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              acc[h / 2][i][h & 1] *= sc;
-              acc[h / 2][i][2 + (h & 1)] *= sc;
+              acc[i][h] *= sc;
+              acc[i][2 + h] *= sc;
             }
           }
         }
@@ -856,26 +826,19 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
           const float sc = __fdividef(nu2, nu);
           nu = nu2;
 #pragma unroll
-          for (int nb = 0; nb < kNB; ++nb)
+          for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[nb][i][c] *= sc;
+            for (int c = 0; c < 4; ++c) acc[i][c] *= sc;
         }
         // ---- o += (p s) . V codes ----
 #pragma unroll
         for (int tile = 0; tile < kUnitTiles; ++tile) {
           if (tile == 2 && ntok <= kHalfUnit) break;
           const uint64_t s2 = f32x2_pack(vsz[tile][0].x * nu, vsz[tile][1].x * nu);
-          uint32_t pb[kNB][2];
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) {
-            float a0, a1, b0 = 0.f, b1 = 0.f;
-            f32x2_unpack(f32x2_mul(pr[2 * nb][tile], s2), a0, a1);
-            if (2 * nb + 1 < G) f32x2_unpack(f32x2_mul(pr[(2 * nb + 1) % G][tile], s2), b0, b1);
-            pb[nb][0] = movmatrix(pack_f16(a0, b0));
-            pb[nb][1] = movmatrix(pack_f16(a1, b1));
-          }
+          float a0, a1, b0 = 0.f, b1 = 0.f;
+          f32x2_unpack(f32x2_mul(pr[0][tile], s2), a0, a1);
+          if (G > 1) f32x2_unpack(f32x2_mul(pr[G - 1][tile], s2), b0, b1);
+          const uint32_t p0 = movmatrix(pack_f16(a0, b0)), p1 = movmatrix(pack_f16(a1, b1));
           const uint32_t base = v_buf + tile * kQ4TileBytes + v_off;
           uint32_t lo[4], hi[4];
           ldmatrix_x4_trans(base, lo);
@@ -883,13 +846,9 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t lo8 = shift8(lo[q]), hi8 = shift8(hi[q]);
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) {
-              mma16816(acc[nb][2 * q], lo[q] & 0x000f000fu, lo[q] & 0x00f000f0u, hi[q] & 0x000f000fu,
-                       hi[q] & 0x00f000f0u, pb[nb][0], pb[nb][1]);
-              mma16816(acc[nb][2 * q + 1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u,
-                       pb[nb][0], pb[nb][1]);
-            }
+            mma16816(acc[2 * q], lo[q] & 0x000f000fu, lo[q] & 0x00f000f0u, hi[q] & 0x000f000fu, hi[q] & 0x00f000f0u, p0,
+                     p1);
+            mma16816(acc[2 * q + 1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, p0, p1);
           }
         }
       }
@@ -915,29 +874,29 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
         return is_last != 0;
       };
       const int g0 = c - c % kFan;  // this chunk's group of kFan
-      const int64_t slot_g = static_cast<int64_t>(first_chunk + g0) * p.hkv + pend_head;
+      const int64_t slot_g = static_cast<int64_t>(first_chunk + g0) * p.rows + pend_head;
       const int in_group = min(kFan, nch - g0);
       bool merge = arrive(slot_g, in_group);
-      int64_t at = slot_g, stride = p.hkv;
+      int64_t at = slot_g, stride = p.rows;
       int n = in_group;
       if (merge && nch > kFan) {
         // merge the group into its first slot, then the groups
         float M[G], den[G];
         float4 a[G];
-        merge_slots<G>(p, slot_g, p.hkv, in_group, lane, M, den, a);
+        merge_slots<G>(p, slot_g, p.rows, in_group, lane, M, den, a);
         __syncwarp();  // every lane has read the slot that is overwritten
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           reinterpret_cast<float4*>(p.opart + (slot_g * G + h) * kHeadDim)[lane] = a[h];
           if (lane == 0) p.ml[slot_g * G + h] = make_float2(M[h], den[h]);
         }
-        at = static_cast<int64_t>(first_chunk) * p.hkv + pend_head;
-        stride = static_cast<int64_t>(kFan) * p.hkv;
+        at = static_cast<int64_t>(first_chunk) * p.rows + pend_head;
+        stride = static_cast<int64_t>(kFan) * p.rows;
         n = (nch + kFan - 1) / kFan;
-        merge = arrive(at + p.hkv, n);  // the ticket of chunk 1, which no group uses
+        merge = arrive(at + p.rows, n);  // the ticket of chunk 1, which no group uses
       }
       if (merge) {
-        uint16_t* orow = p.out + (static_cast<int64_t>(pend_b) * p.hkv + pend_head) * G * kHeadDim;
+        uint16_t* orow = p.out + (static_cast<int64_t>(pend_b) * p.rows + pend_head) * G * kHeadDim;
         float M[G], den[G];
         float4 a[G];
         merge_slots<G>(p, at, stride, n, lane, M, den, a);
@@ -958,7 +917,7 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
     const int4 it = info->item[items_done & 3];
     ++items_done;
     const int b = it.x, head = it.y, nch = it.z >> 16;
-    const int64_t slot = static_cast<int64_t>(sF[b] + b + (it.z & 0xffff)) * p.hkv + head;
+    const int64_t slot = static_cast<int64_t>(sF[b] + b + (it.z & 0xffff)) * p.rows + head;
     const float back = __fdividef(16777216.f, nu);
     const int d0 = 32 * t + 4 * (r >> 2);
 #pragma unroll
@@ -978,12 +937,12 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
       if (t == (r & 3)) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float o0 = fmaf(acc[h / 2][2 * q][h & 1], ka, z), o1 = fmaf(acc[h / 2][2 * q][2 + (h & 1)], kb, z);
-          const float o2 = fmaf(acc[h / 2][2 * q + 1][h & 1], ka, z), o3 = fmaf(acc[h / 2][2 * q + 1][2 + (h & 1)], kb, z);
+          const float o0 = fmaf(acc[2 * q][h], ka, z), o1 = fmaf(acc[2 * q][2 + h], kb, z);
+          const float o2 = fmaf(acc[2 * q + 1][h], ka, z), o3 = fmaf(acc[2 * q + 1][2 + h], kb, z);
           if (nch > 1) {
             *reinterpret_cast<float4*>(p.opart + (slot * G + h) * kHeadDim + d0 + 8 * q) = make_float4(o0, o1, o2, o3);
           } else {
-            uint16_t* orow = p.out + ((static_cast<int64_t>(b) * p.hkv + head) * G + h) * kHeadDim;
+            uint16_t* orow = p.out + ((static_cast<int64_t>(b) * p.rows + head) * G + h) * kHeadDim;
             uint2 v;
             v.x = Ops::pack(o0, o1);
             v.y = Ops::pack(o2, o3);
@@ -1016,12 +975,11 @@ __global__ void __launch_bounds__(warps_of(G) * 32, 1) q4_decode_kernel(const Q4
 
 template <int G>
 constexpr size_t smem_bytes() {
-  return static_cast<size_t>(warps_of(G)) *
-             (3 * kUnitBytes + 2 * G * kHeadDim * 2 + (G > 2 ? 4096 : 0) + sizeof(WarpInfo)) +
+  return static_cast<size_t>(kWarps) *
+             (3 * kUnitBytes + 2 * G * kHeadDim * 2 + sizeof(WarpInfo)) +
          (3 * kMaxSeqs + 1 + (kClasses + 1) * 32) * sizeof(int);
 }
-static_assert(smem_bytes<2>() <= 227 * 1024 && smem_bytes<4>() <= 227 * 1024,
-              "shared memory above the 227 KB a CTA can opt into");
+static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
 template <Elem E, int G>
 cudaError_t launch_typed(const Q4DecodeParams& p, cudaStream_t stream) {
@@ -1036,7 +994,7 @@ cudaError_t launch_typed(const Q4DecodeParams& p, cudaStream_t stream) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
     if (dev >= 0 && dev < 64) sm_count[dev] = sms;
   }
-  q4_decode_kernel<E, G><<<sms, warps_of(G) * 32, smem_bytes<G>(), stream>>>(p);
+  q4_decode_kernel<E, G><<<sms, kWarps * 32, smem_bytes<G>(), stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1046,12 +1004,12 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // whole chunks, one short chunk per sequence, times heads. chunk_tokens makes at
 // most one whole chunk per warp up to x = kMaxChunk, chunks of 9 units or more
 // up to x = 128 and of 15 or more beyond; and none shorter than half a unit.
-int64_t max_slots(int64_t num_seqs, int64_t hkv, int64_t group, int64_t max_ctx) {
-  const int64_t units = num_seqs * ((max_ctx + kUnit - 1) / kUnit) * hkv;
-  const int64_t halves = num_seqs * (max_ctx / kHalfUnit) * hkv;
-  int64_t chunks = int64_t{128} * 152 * warps_of(static_cast<int>(group)) / 9 + 1;
+int64_t max_slots(int64_t num_seqs, int64_t rows, int64_t max_ctx) {
+  const int64_t units = num_seqs * ((max_ctx + kUnit - 1) / kUnit) * rows;
+  const int64_t halves = num_seqs * (max_ctx / kHalfUnit) * rows;
+  int64_t chunks = int64_t{128} * 152 * kWarps / 9 + 1;
   if (units / 15 + 1 > chunks) chunks = units / 15 + 1;
-  return (halves < chunks ? halves : chunks) + num_seqs * hkv;
+  return (halves < chunks ? halves : chunks) + num_seqs * rows;
 }
 
 }  // namespace
@@ -1065,8 +1023,9 @@ int64_t max_slots(int64_t num_seqs, int64_t hkv, int64_t group, int64_t max_ctx)
 size_t decode_q4_counter_bytes(size_t workspace_bytes) { return 256 + (workspace_bytes / 128 & ~size_t{255}); }
 
 size_t decode_q4_workspace_bytes(int32_t num_seqs, int32_t hkv, int32_t group, int32_t max_ctx) {
-  const int64_t n = max_slots(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv, group, max_ctx);
-  const size_t partials = static_cast<size_t>(n) * group * (kHeadDim * sizeof(float) + sizeof(float2));
+  const int heads = group > 1 ? 2 : 1;  // per item
+  const int64_t n = max_slots(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv * group / heads, max_ctx);
+  const size_t partials = static_cast<size_t>(n) * heads * (kHeadDim * sizeof(float) + sizeof(float2));
   return align_up((partials + 512) / 127 * 128 + 512, 256);
 }
 
@@ -1090,13 +1049,16 @@ cudaError_t launch_decode_q4(const void* q, int64_t q_row_stride, const void* k_
     p.max_ctx = max_ctx;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = static_cast<uint16_t*>(out) + static_cast<int64_t>(b0) * hkv * group * kHeadDim;
-    const int64_t n = max_slots(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, hkv, group, max_ctx);
+    const int heads = group > 1 ? 2 : 1;
+    p.rows = hkv * group / heads;
+    p.share = group / heads;
+    const int64_t n = max_slots(num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs, p.rows, max_ctx);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.work = reinterpret_cast<int32_t*>(ws);
     p.tickets = p.work + 2;
     ws += decode_q4_counter_bytes(workspace_bytes);
     p.opart = reinterpret_cast<float*>(ws);
-    p.ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(n) * group * kHeadDim * sizeof(float));
+    p.ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(n) * heads * kHeadDim * sizeof(float));
     p.max_slots = n;
     if (fused) {
       p.k_new = static_cast<const uint16_t*>(fused->k) + b0 * fused->k_row_stride;
@@ -1108,14 +1070,9 @@ cudaError_t launch_decode_q4(const void* q, int64_t q_row_stride, const void* k_
       p.v_cache_w = static_cast<uint8_t*>(const_cast<void*>(v_cache));
     }
     p.err = err;
-    cudaError_t e = cudaErrorInvalidValue;
     const bool f16 = elem == Elem::kF16;
-    if (group == 1)
-      e = f16 ? launch_typed<Elem::kF16, 1>(p, stream) : launch_typed<Elem::kBF16, 1>(p, stream);
-    else if (group == 2)
-      e = f16 ? launch_typed<Elem::kF16, 2>(p, stream) : launch_typed<Elem::kBF16, 2>(p, stream);
-    else if (group == 4)
-      e = f16 ? launch_typed<Elem::kF16, 4>(p, stream) : launch_typed<Elem::kBF16, 4>(p, stream);
+    const cudaError_t e = heads == 1 ? (f16 ? launch_typed<Elem::kF16, 1>(p, stream) : launch_typed<Elem::kBF16, 1>(p, stream))
+                                     : (f16 ? launch_typed<Elem::kF16, 2>(p, stream) : launch_typed<Elem::kBF16, 2>(p, stream));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -57,7 +57,7 @@ def test_decode_refusals(lib, suffix):
         return step(*a, k, ks, v, vs, sm, *b)
 
     for f in (d, s):
-        assert f(d=64) == f(blk=16) == f(hq=24, qs=4096) == f(hq=12) == f(hq=64, qs=8192) == f(hkv=0) == -2
+        assert f(d=64) == f(blk=16) == f(hq=24, qs=4096) == f(hq=12) == f(hq=40, qs=8192) == f(hkv=0) == -2
         assert f(n=-1) == f(n=65536) == f(nb=-1) == f(bs=-1) == f(mc=-1) == f(mc=(1 << 24) + 1) == -6
         assert f(sc=0.0) == f(sc=-1.0) == f(sc=float("nan")) == -6
         for name in ("q", "kc", "vc", "bt", "cl", "out"):
@@ -79,7 +79,7 @@ def test_prefill_refusals(lib, suffix):
           d=128, blk=256, sc=0.1, out=ONE, ws=None, wb=0):
         return pre(q, qs, tq, kc, vc, nb, cq, ck, mq, mk, bt, bs, n, hq, hkv, d, blk, sc, out, ws, wb, None)
 
-    assert f(d=96) == f(blk=16) == f(hq=8) == f(hq=24, qs=4096) == f(hq=64, qs=8192) == f(hkv=0) == -2
+    assert f(d=96) == f(blk=16) == f(hq=8) == f(hq=24, qs=4096) == f(hq=40, qs=8192) == f(hkv=0) == -2
     assert f(tq=-1) == f(nb=-1) == f(mq=-1) == f(mk=-1) == f(bs=-1) == f(n=-1) == f(n=65536) == -6
     assert f(sc=0.0) == f(sc=float("nan")) == f(nb=0) == f(bs=0) == -6
     for name in ("q", "kc", "vc", "cq", "ck", "bt", "out"):
@@ -111,9 +111,9 @@ def test_workspace_covers_every_slot():
         x = -(-units // plan)
         return 64 * -(-x // -(-x // 16))
 
-    def bound(n, hkv, ctx, plan):
-        units, halves = n * -(-ctx // 64) * hkv, n * (ctx // 32) * hkv
-        return min(halves, max(128 * plan // 9 + 1, units // 15 + 1)) + n * hkv
+    def bound(n, rows, ctx, plan):
+        units, halves = n * -(-ctx // 64) * rows, n * (ctx // 32) * rows
+        return min(halves, max(128 * plan // 9 + 1, units // 15 + 1)) + n * rows
 
     rng = random.Random(1)
     for _ in range(4000):
@@ -121,15 +121,15 @@ def test_workspace_covers_every_slot():
         ctx = int(2 ** rng.uniform(0, 17))
         lens = [rng.randint(0, ctx) if rng.random() < 0.8 else ctx for _ in range(n)]
         for group in (1, 2, 4):
-            plan = 152 * (12 if group <= 2 else 8)
-            c = chunk(sum(-(-x // 32) for x in lens) * hkv, sum(-(-x // 64) for x in lens) * hkv, plan)
+            plan, rows = 152 * 12, hkv * max(1, group // 2)
+            c = chunk(sum(-(-x // 32) for x in lens) * rows, sum(-(-x // 64) for x in lens) * rows, plan)
             assert c == 32 or (c % 64 == 0 and c <= 1024)
-            m = bound(n, hkv, ctx, plan)
-            assert sum(x // c for x in lens) * hkv + n * hkv <= m
+            m, heads = bound(n, rows, ctx, plan), min(group, 2)
+            assert sum(x // c for x in lens) * rows + n * rows <= m
             assert max(-(-x // c) for x in lens) < 2 ** 15
-            size = ((m * group * 520 + 512) // 127 * 128 + 512 + 255) // 256 * 256
+            size = ((m * heads * 520 + 512) // 127 * 128 + 512 + 255) // 256 * 256
             counters = 256 + (size // 128 & ~255)
-            assert 8 + 4 * m <= counters and counters + m * group * 520 <= size
+            assert 8 + 4 * m <= counters and counters + m * heads * 520 <= size
 
 
 def test_reference_places_are_a_permutation():
