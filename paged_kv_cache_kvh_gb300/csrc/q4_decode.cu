@@ -57,7 +57,7 @@ constexpr int kUnit = 64;                                    // tokens per stage
 constexpr int kHalfUnit = 32;                                // the shortest chunk
 constexpr int kUnitTiles = kUnit / kQ4Tile;
 constexpr int kUnitBytes = kUnitTiles * kQ4TileBytes;        // 5120, of K and of V each
-constexpr int kMaxChunk = 16;                                // units per chunk at most
+constexpr int kMaxChunk = 32;                                // units per chunk at most
 constexpr int kMaxSeqs = 768;                                // sequences per launch (item table in shared memory)
 constexpr int kClasses = 8;                                  // sizes that short chunks are sorted into
 constexpr int kFan = 16;                                     // chunks merged at once
@@ -177,12 +177,6 @@ __device__ __forceinline__ void mma1688_tf32(float (&c)[4], uint32_t a0, uint32_
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-#ifdef PKV_Q4_HI
-__device__ __forceinline__ uint32_t shift8(uint32_t x) { return __umulhi(x, 0x01000000u); }
-#else
-__device__ __forceinline__ uint32_t shift8(uint32_t x) { return x >> 8; }
-#endif
-
 // Whole-warp bounded wait, after a first test has failed.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned int* err) {
   const uint64_t t0 = globaltimer_ns();
@@ -445,8 +439,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
 
   // ---- the issuing side: which unit is fetched next ----
   int64_t item = static_cast<int64_t>(warp) * n_ctas + cta;
-  int next_raw = 0;  // lane 0: the counter's answer for the item after this one
-  if (dynamic && lane == 0) next_raw = atomicAdd(p.work, 1);
+  // Lane 0 asks the counter for the next item two units before this one ends: early
+  // enough to hide the answer's way, late enough to leave the last items to the
+  // warps that get to them first.
+  int next_raw = 0;
+  bool asked = false;
+  auto ask = [&]() {
+    if (lane == 0) next_raw = atomicAdd(p.work, 1);
+    asked = true;
+  };
   int ib = 0, ihead = 0, itok = 0;     // sequence, head, next token
   int left = 0;                        // tokens of the chunk not asked for yet; 0: no more work
   int items = 0;                       // items resolved
@@ -530,16 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
     if (last) {
       left = 0;
       if (dynamic) {
+        if (!asked) ask();
+        asked = false;
         item = static_cast<int64_t>(W) + __shfl_sync(0xffffffffu, next_raw, 0);
-        if (item < n_items) {
-          if (lane == 0) next_raw = atomicAdd(p.work, 1);
-          resolve();
-        }
+        if (item < n_items) resolve();
       }
-    } else if (itok % kBlockSize == 0) {
-      look_up();
-    } else if (ioff >= 0) {
-      ioff += kUnitBytes;
+    } else {
+      if (dynamic && !asked && left <= 2 * kUnit) ask();
+      if (itok % kBlockSize == 0)
+        look_up();
+      else if (ioff >= 0)
+        ioff += kUnitBytes;
     }
   };
   auto issue_v = [&](int n) {  // fetches V of unit n, whose K has been asked for
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           for (int i = 0; i < 2; ++i) {
             const uint32_t a = j == 0 ? w0[i].x : j == 1 ? w0[i].y : j == 2 ? w0[i].z : w0[i].w;
             const uint32_t b = j == 0 ? w1[i].x : j == 1 ? w1[i].y : j == 2 ? w1[i].z : w1[i].w;
-            const uint32_t ah = shift8(a), bh = shift8(b);
+            const uint32_t ah = a >> 8, bh = b >> 8;
             if (j == 0)
               mma16816_first(c[i], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qb[0][0],
                              qb[0][1]);
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           ldmatrix_x4_trans(base + 8 * kQ4CodeBytes, hi);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t lo8 = shift8(lo[q]), hi8 = shift8(hi[q]);
+            const uint32_t lo8 = lo[q] >> 8, hi8 = hi[q] >> 8;
             mma16816(acc[2 * q], lo[q] & 0x000f000fu, lo[q] & 0x00f000f0u, hi[q] & 0x000f000fu, hi[q] & 0x00f000f0u, p0,
                      p1);
             mma16816(acc[2 * q + 1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, p0, p1);
@@ -1002,13 +1004,13 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Most slots for partial results that a launch over these sizes can use: its
 // whole chunks, one short chunk per sequence, times heads. chunk_tokens makes at
-// most one whole chunk per warp up to x = kMaxChunk, chunks of 9 units or more
-// up to x = 128 and of 15 or more beyond; and none shorter than half a unit.
+// most one whole chunk per warp up to x = kMaxChunk, chunks of 17 units or more
+// up to x = 256 and of 29 or more beyond; and none shorter than half a unit.
 int64_t max_slots(int64_t num_seqs, int64_t rows, int64_t max_ctx) {
   const int64_t units = num_seqs * ((max_ctx + kUnit - 1) / kUnit) * rows;
   const int64_t halves = num_seqs * (max_ctx / kHalfUnit) * rows;
-  int64_t chunks = int64_t{128} * 152 * kWarps / 9 + 1;
-  if (units / 15 + 1 > chunks) chunks = units / 15 + 1;
+  int64_t chunks = int64_t{256} * 152 * kWarps / 17 + 1;
+  if (units / 29 + 1 > chunks) chunks = units / 29 + 1;
   return (halves < chunks ? halves : chunks) + num_seqs * rows;
 }
 
