@@ -509,7 +509,7 @@ def _decode_q4(entry, dtype, q, new, k_cache, v_cache, block_tables, context_len
     if len(tables) != 2 or tables[0] < B or context_lens.numel() < B:
         raise ValueError("block_tables must be [B, width] and context_lens [B]")
     if out is None:
-        out = q.new_empty((B, hq, HEAD_DIM))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
     if workspace.dtype != torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
@@ -574,7 +574,7 @@ def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_s
     if num_seqs < 0 or cu_seqlens_k.numel() != num_seqs + 1 or len(tables) != 2 or tables[0] < num_seqs:
         raise ValueError("cu_seqlens must be [num_seqs + 1] and block_tables [num_seqs, width]")
     if out is None:
-        out = q.new_empty((total_q, hq, HEAD_DIM))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
     items = n_items = 0
