@@ -14,9 +14,10 @@
 //      code p in bits 4p..4p+3.
 //   V: the 8-byte chunk r sits at chunk place r ^ (4 if token & 4 else 0); its
 //      16-bit field j holds dims 32 j + 4 r + p, p = 0..3.
-// Both orders are what a tensor-core operand fragment of the decode kernel
-// reads with one 16-byte (K) or 8-byte (V) shared-memory load without bank
-// conflicts; the swap of the V halves is for the latter.
+// Both orders are those of the decode kernel's tensor-core operands: a K row's
+// 16 bytes at 16 t are one lane's share of a fragment, and a 16-byte half chunk
+// pair of V, transposed by the load, is four dims of every group. The swap of the
+// V halves spreads 8 tokens' 16-byte pieces over more banks.
 #pragma once
 
 #include "pkv_common.cuh"

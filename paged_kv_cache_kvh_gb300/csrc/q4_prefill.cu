@@ -16,20 +16,37 @@
 //   warp 1        allocates TMEM, one lane issues every tcgen05.mma
 //   warps 4-7     softmax of the first head   (thread = TMEM lane = query row)
 //   warps 8-11    softmax of the second head
-//   warps 12-15   widen K_n, V_n (128 keys x 128 dims) into the 3-slot ring
-// (warps 2, 3 only make up the warpgroup for the register split.) A widening
-// warp takes 32 keys: four batches of 8 keys, 16 bytes of codes a lane, which
-// are 8 dims of each of the 4 groups. A batch's registers are loaded again for
-// the next tile as soon as it is widened, so a tile's loads are in flight while
-// the other batches are converted and the ring slot is waited for. 21
-// instructions widen 8 codes: about 2.7 k warp instructions per key tile beside
-// the 7 k or so of the softmax, in the two products' shadow. Rows past the
-// sequence are written as zeros. So is a group of V that reads back as NaN: in a
-// product it would reach every query row of the tile, masked or not (0 * NaN).
-// The first such position of each group is kept instead, and rows at or past it
-// get NaN in the epilogue.
-// Registers: 512 threads x 128 at launch, split over the warpgroups by what each
-// needs without spilling (shared memory leaves no L1 for local memory).
+//   warps 12-19   widen K_n, V_n (128 keys x 128 dims) into a ring of 5 tiles
+// (warps 2, 3 only make up the warpgroup for the register split.) P is written
+// over the logits in TMEM, as 16-bit pairs, and is the A operand of the second
+// product from there: the 64 KB of shared memory that two P tiles would take are
+// two more K/V tiles.
+//
+// A widening warp takes 16 keys of a tile: two batches of 8 keys, 16 bytes of
+// codes a lane, which are 8 dims of each of the 4 groups. A batch's registers are
+// loaded again for the next tile as soon as it is widened, so a tile's loads are
+// in flight while the other batch is converted and the ring slot is waited for.
+// A bf16 pair costs two ANDs, one packed multiply-add and one conversion (the
+// nibbles are used in place, as fp32 subnormals; see dequantise8), which is why
+// bf16 tiles hold 2^-64 of the values; the powers of two are taken out of the
+// logits and of the output. Rows past the sequence are written as zeros. So is a
+// group of V that reads back as NaN: in a product it would reach every query row
+// of the tile, masked or not (0 * NaN). The first such position of each group is
+// kept instead, and rows at or past it get NaN in the epilogue.
+//
+// Registers: 640 threads x 96 at launch, split over the warpgroups by what each
+// needs without spilling (shared memory leaves no L1 for local memory: the first
+// form, which spilled, took 904 us where this takes 491).
+//
+// What bounds it: issue slots. A key tile costs about 4.3 k warp instructions of
+// widening and 9 k of softmax a CTA, over four schedulers, against 1024 cycles of
+// tensor core. 128 prompts of 64..512 tokens on a shared prefix of 4096 (16 query
+// heads on 8): 491 us, 0.72 PFLOP/s; 5000 tokens after 7001: 457 us, 0.85. With
+// the tiles' widening left out the latter would take 367. Measured and not kept:
+// 4 widening warps (570 with register pressure solved; they are late), 6 (580:
+// the three schedulers that get two are uneven), P through shared memory (545),
+// logits in 64-key halves with two in flight for each head (630: 13 % more
+// instructions where they are what is short).
 // TMEM columns, issue order, the lazily moved maximum and the epilogue are as in
 // prefill.cu.
 #include <cuda.h>
@@ -55,15 +72,12 @@ constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
 constexpr int kRegsFirst = 48, kRegsSoftmax = 152, kRegsWiden = 64;
 static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
 
-#ifndef PKV_Q4P_NAP
-#define PKV_Q4P_NAP 100
-#endif
-constexpr int kWidenNap = PKV_Q4P_NAP;
+
 constexpr int kOffQ = 0;                                 // 2 tiles (and O staging in the epilogue)
 constexpr int kOffKV = 2 * kTileBytes;                   // kKvSlots tiles
 constexpr int kOffBar = kOffKV + kKvSlots * kTileBytes;  // barriers
 constexpr int kBarQ = 0;
-constexpr int kBarKvFull = 1;                       // +slot, 4 warps
+constexpr int kBarKvFull = 1;                       // +slot, the widening warps
 constexpr int kBarKvFree = kBarKvFull + kKvSlots;   // +slot
 constexpr int kBarSFull = kBarKvFree + kKvSlots;    // +g
 constexpr int kBarPReady = kBarSFull + 2;           // +g, 4 warps
@@ -97,15 +111,12 @@ struct Q4PrefillParams {
 };
 
 // Bounded wait that also gives up as soon as another role of the CTA has aborted.
-// kNap: nanoseconds slept between tests by a role that can afford to be late.
-template <int kNap = 0>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                               unsigned int* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     for (int i = 0; i < 32; ++i) {
-      if (kNap > 0) __nanosleep(kNap);
       if (mbar_try_wait(bar, parity)) return true;
     }
     if (*abort_flag) return false;
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1];
   const int Lq = cq1 - cq0, Lk = p.cu_k[b + 1] - p.cu_k[b];
-  if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || cq0 < 0 || cq1 > p.total_q ||
+  if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || Lk > INT_MAX - 2 * kBN || cq0 < 0 || cq1 > p.total_q ||
       Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
     if (threadIdx.x == 0 && qt == 0 && pair == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
@@ -209,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
-      if (i == kBarPReady || i == kBarPReady + 1 || (i >= kBarKvFull && i < kBarKvFull + kKvSlots)) count = i >= kBarKvFull && i < kBarKvFull + kKvSlots ? kWidenWarps : 4;
+      if (i >= kBarKvFull && i < kBarKvFull + kKvSlots) count = kWidenWarps;
+      if (i == kBarPReady || i == kBarPReady + 1) count = 4;
       if (i == kBarStaged) count = 8;
       mbar_init(bar(i), count);
     }
@@ -346,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!is_v) blk_next = block_of((i >> 1) + 1);  // used one item later
       else if (i + 1 < 2 * n_tiles) blk = checked(blk_next);
       const int slot = i % kKvSlots;
-      if (i >= kKvSlots &&
-          !__all_sync(0xffffffffu, wait_or_abort<kWidenNap>(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err)))
+      if (i >= kKvSlots && !__all_sync(0xffffffffu, wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1,
+                                                                  s_abort, p.err)))
         break;
       const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
 #pragma unroll
@@ -613,7 +625,7 @@ cudaError_t launch_prefill_q4(const void* q, int64_t q_row_stride, int32_t total
   p.bt_stride = bt_stride;
   p.num_blocks = num_blocks;
   p.num_seqs = num_seqs;
-  p.max_q_tiles = (max_seqlen_q + kBM - 1) / kBM;
+  p.max_q_tiles = (static_cast<int64_t>(max_seqlen_q < total_q ? max_seqlen_q : total_q) + kBM - 1) / kBM;
   p.max_seqlen_q = max_seqlen_q;
   p.max_seqlen_k = max_seqlen_k;
   p.total_q = total_q;

@@ -86,6 +86,24 @@ def test_bits_of_load_then_prefill(pkv, dtype):
     assert torch.equal(c.prefill(plan=plan), want)
 
 
+def test_growing_logits(pkv):
+    """The running maximum moves in every key tile."""
+    c = Prefill(pkv, [400], [1500], 16, 8, BF16, seed=28)
+    c.k = (c.k.float() + torch.linspace(-3, 3, 1500, device="cuda")[:, None, None]).to(BF16)
+    c.q = c.q.abs()
+    c.check(c.fill().prefill())
+
+
+@pytest.mark.parametrize("max_q", [400, 2 ** 31 - 1])
+def test_upper_bounds_of_the_lengths(pkv, max_q):
+    """max_seqlen_q and max_seqlen_k may be any upper bounds."""
+    c = Prefill(pkv, [200, 3], [300, 3], 4, 2, F16, seed=29).fill()
+    want = c.prefill()
+    c.check(want)
+    out = c.f("pkv_prefill_varlen_q4")(c.q, c.d_cq, c.d_ck, max_q, 2 ** 31 - 1, c.scale, c.kc, c.vc, c.tables)
+    assert torch.equal(out, want) and pkv.pkv_device_error() == 0
+
+
 def test_shared_prefix_blocks(pkv):
     """Sequences that read the same physical blocks for their prefix."""
     c = Prefill(pkv, [60, 100, 200], [572, 612, 712], 16, 8, BF16, seed=22)
