@@ -6,9 +6,9 @@
 //   out_d   = sum_t p_t (s_tg c_td + z_tg) / sum_t p_t,  p = softmax(logit)
 // The codes are used exactly as stored; no 16-bit K or V row is ever formed.
 //
-// What bounds it: 160 bytes per (token, kv head) from HBM, 47 codes a clock
-// and SM at the copy rate. Widening and multiplying them on the CUDA cores
-// (an unpack and two multiply-adds per code and query head) would need more
+// What bounds it: 160 bytes per (token, kv head) from HBM, which at the copy
+// rate are 47 codes a clock and SM. Widening and multiplying them on the CUDA
+// cores (an unpack and two multiply-adds per code and query head) would need more
 // issue slots than an SM has, so both products run on mma.sync m16n8k16:
 //  * A holds 16 tokens x 16 dims of codes (K) or 16 dims x 16 tokens (V) as
 //    fp16. A code in the low nibble of each 16-bit half, w & 0x000f000f, is
@@ -20,23 +20,44 @@
 //    accumulator ends with every group's own sum: lane (r, t) of the C fragment
 //    has tokens r, r + 8, group t, both heads. For V, column 2 g + h holds
 //    p_t s_tg: C columns of other groups than the row's dims are not used.
-//    G = 4 query heads take a second B; A is widened once.
-//  * p goes from C's layout to B's by movmatrix (8 x 8 transpose in registers).
+//  * The sum over the groups, four lanes, is a tf32 product with ones (each
+//    addend as a high and a low part, 2^-22 of it at most is lost), and
+//    z_tg . sum q is another, whose C starts at minus the running maximum:
+//    the logits come out relative to it. Shuffles instead took 184 us where
+//    these took 163.
+//  * V's 16-bit fields are transposed by the load from shared memory (ldmatrix),
+//    p goes from C's layout to B's by movmatrix (8 x 8 transposes in registers).
 //  * q is scaled by a power of two per head so that fp16 holds it exactly
 //    (elements below 2^-38 of the head's largest are rounded); p s is scaled by
 //    a running power of two and rounded to fp16 (relative 2^-11, as p is in any
-//    tensor-core product). Sums, maxima and the z terms stay in fp32.
+//    tensor-core product; kCentred below). Sums, maxima and the z terms stay in fp32.
 //
-// Work: an item is a chunk of up to 256 tokens of one (sequence, kv head), and
-// a warp works through items alone: it fetches 32 tokens a stage by two bulk
-// copies (K and V tiles of one (block, head) are contiguous) into its own ring
-// in shared memory and waits on its own barriers, so no warp ever waits for
-// another. One CTA of kWarps warps per SM. Every CTA derives the item table
-// from context_lens; warp w starts on item w and takes the next ones from a
-// counter in the workspace. Partial results (m, l, o) of sequences with several
-// chunks go to the workspace, and the warp that finishes last merges them
-// (ticket, no waiting): up to 16 chunks at once, groups of 16 and then the
-// groups beyond that.
+// Work: an item is a chunk of one sequence for a pair of query heads that share a
+// kv head (for a single head where each has its own; with four or more to a kv
+// head the pairs run next to one another and read the tiles from L2). A warp works
+// through items alone, 64 tokens a step: bulk copies (K and V tiles of one (block,
+// head) are contiguous) fetch K two steps ahead and V one step ahead into its own
+// 15 KB of shared memory, and it waits on its own barriers, so no warp ever waits
+// for another. One CTA of 12 warps per SM. Chunks: chunk_tokens. Every CTA derives
+// the item table from context_lens: whole chunks first, then the sequences' short
+// last chunks, longest first. Warp w starts on item w and takes the next ones from
+// a counter in the workspace, asked two steps before its item ends.
+// Partial results (m, l, o) of sequences with several chunks go to the workspace;
+// the ticket is taken a step later, when the writes have landed, and the warp that
+// takes the last one merges them (no waiting): up to 16 chunks at once, groups of
+// 16 and then the groups beyond that.
+// The fused step quantises a sequence's new row in the warps that read its last
+// tile, which put it over what was fetched; one of them writes it to the cache.
+//
+// Measured: 256 sequences of 512..4096 tokens, 16 query heads on 8: 141 us,
+// 5.4 TB/s (80 % of the copy rate); 512 of 800 on average, fp16: 101 us, 76 %; one of
+// 40007, 32 on 8: 31 us. With every block table folded onto a few blocks that
+// stay in L2 the first takes the same time: it is bound by execution, about 512
+// warp instructions per 32 tokens and pair of heads at 0.48 a clock and scheduler.
+// Measured and not kept: 16 warps of 32-token steps (165 us: more control per
+// token), 8 warps (163), one K buffer and 16 warps (141), accumulators rescaled
+// without a branch (154), other orders of the products (150 as they stood then),
+// shifts as multiplications (166).
 #include <type_traits>
 
 #include "q4.cuh"
@@ -260,6 +281,14 @@ __device__ __forceinline__ void merge_slots(const Q4DecodeParams& p, int64_t fir
 template <Elem E, int G>
 __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodeParams p) {
   using Ops = ElemOps<E>;
+  // What rounding p s to fp16 loses comes back multiplied by the code. With codes
+  // taken from their middle, c - 7.5, that is half as much: z + 7.5 s takes z's
+  // place, and 7.5 times the sum of the rounded p s (a product with ones) is taken
+  // off at the end. For bf16 the result's own rounding is 8 times larger than
+  // either, so only fp16 pays for it: 512 sequences of 800 tokens on average take
+  // 101 us instead of 98, at an error of 0.00025 instead of 0.00038 (the result's
+  // rounding alone: 0.0002).
+  constexpr bool kCentred = E == Elem::kF16;
   constexpr int kQBytes = G * kHeadDim * 2;   // one item's query rows
   constexpr int kWarpBytes = 3 * kUnitBytes + 2 * kQBytes;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -421,11 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
     return;
   }
 
-  // rows without context: zeros
+  // rows without context: zeros, and nothing to store
   for (int b = cta * kWarps + warp; b < B; b += n_ctas * kWarps) {
     if (sCtx[b] == 0) {
       uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(b) * p.rows * G * kHeadDim);
       for (int i = lane; i < p.rows * G * (kHeadDim / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+      if (p.k_new != nullptr && lane == 0 && p.slot_mapping[b] != -1) flag_error(p.err, PKV_DEVERR_BAD_SLOT);
     }
   }
 
@@ -565,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
   uint32_t qs_b[G][2];       // B fragment of sum q over group t: high and low part
   float kc[2];               // per head: the power of two taken out of q and the codes, times scale * log2(e)
   float acc[8][4];
-  uint64_t l2[G], z2[G];     // sums of p and of p z, tokens r and r + 8 apart
+  float ones[4];             // kCentred: sum of the rounded p s, group t
+  uint64_t l2[G], z2[G];     // sums of p and of p z (kCentred: p (z + 7.5 s)), tokens r and r + 8 apart
   float m[G];                // running maximum, -INFINITY before the first unit
   float from[G][4];          // minus the maximum that logits are taken relative to (a C fragment)
   float nu = 1.f;
@@ -620,18 +651,22 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
                         Ops::lo(raw.z), Ops::hi(raw.z), Ops::lo(raw.w), Ops::hi(raw.w)};
           float big = 0.f, sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            big = fmaxf(big, fabsf(x[i]));
-            sum += x[i];
-          }
+          for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+          const int e = big > 0.f ? 13 - exponent_of(big) : 0;  // the largest |q| goes to [2^13, 2^14)
+          const float f = pow2(min(e, 120));
+          // From |q| = 2^114 on, 2^24 / f would pass fp32: logits are then taken as
+          // if q were smaller. Their steps are still far above 1 (s >= 2^-24), so
+          // the largest one takes all the weight either way.
+          const float least = pow2(-100);
+          const float shrink = fminf(f * pow2(100), 1.f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(x[i], shrink, sum);
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const int e = big > 0.f ? max(-100, 13 - exponent_of(big)) : 0;  // the largest |q| goes to [2^13, 2^14)
-          const float f = pow2(min(e, 120));
           const float f16 = f * 0.0625f;  // for the codes that A holds 16 times too large
           const uint32_t own[4] = {pack_f16(x[0] * f, x[4] * f), pack_f16(x[1] * f16, x[5] * f16),
                                    pack_f16(x[2] * f, x[6] * f), pack_f16(x[3] * f16, x[7] * f16)};
@@ -644,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const float fh = __shfl_sync(0xffffffffu, f, 4 * h2);
-            kc[h2] = __fdividef(16777216.f, fh) * p.scale_log2;
+            kc[h2] = __fdividef(16777216.f, fmaxf(fh, least)) * p.scale_log2;
             const float qs = __shfl_sync(0xffffffffu, sum, (2 * t + h2) * 4) * p.scale_log2;
             if (h2 < G) {
               qs_b[h2 % G][0] = __float_as_uint(qs) & kTf32Mask;
@@ -655,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+          if (kCentred) ones[0] = ones[1] = ones[2] = ones[3] = 0.f;
         }
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -790,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
               acc[i][h] *= sc;
               acc[i][2 + h] *= sc;
             }
+            if (kCentred) ones[h] *= sc;
           }
         }
         // ---- p and its sums ----
@@ -801,14 +838,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           vsz[tile][1] = h2_to_f2(vp[tile][1]);
           smax = fmax3(smax, vsz[tile][0].x, vsz[tile][1].x);
         }
-        uint64_t pr[G][kUnitTiles];
+        uint64_t pr[G][kUnitTiles], mid[kUnitTiles];  // mid: z, or the value of the codes' middle
+#pragma unroll
+        for (int tile = 0; tile < kUnitTiles; ++tile) {
+          mid[tile] = f32x2_pack(vsz[tile][0].y, vsz[tile][1].y);
+          if (kCentred)
+            mid[tile] = f32x2_fma(f32x2_pack(vsz[tile][0].x, vsz[tile][1].x), f32x2_pack(7.5f, 7.5f), mid[tile]);
+        }
 #pragma unroll
         for (int h = 0; h < G; ++h)
 #pragma unroll
           for (int tile = 0; tile < kUnitTiles; ++tile) {
             pr[h][tile] = f32x2_pack(ex2_approx(lg[h][tile][0]), ex2_approx(lg[h][tile][1]));
             l2[h] = f32x2_add(l2[h], pr[h][tile]);
-            z2[h] = f32x2_fma(pr[h][tile], f32x2_pack(vsz[tile][0].y, vsz[tile][1].y), z2[h]);
+            z2[h] = f32x2_fma(pr[h][tile], mid[tile], z2[h]);
           }
         if (moved || __any_sync(0xffffffffu, smax * nu > 64.f)) {
           // p <= 2^8, so p s nu stays below 2^14 otherwise. nu: the power of two
@@ -831,6 +874,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][c] *= sc;
+          if (kCentred) {
+#pragma unroll
+            for (int h = 0; h < G; ++h) ones[h] *= sc;
+          }
         }
         // ---- o += (p s) . V codes ----
 #pragma unroll
@@ -842,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           if (G > 1) f32x2_unpack(f32x2_mul(pr[G - 1][tile], s2), b0, b1);
           const uint32_t p0 = movmatrix(pack_f16(a0, b0)), p1 = movmatrix(pack_f16(a1, b1));
           const uint32_t base = v_buf + tile * kQ4TileBytes + v_off;
+          if (kCentred) mma16816(ones, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, p0, p1);
           uint32_t lo[4], hi[4];
           ldmatrix_x4_trans(base, lo);
           ldmatrix_x4_trans(base + 8 * kQ4CodeBytes, hi);
@@ -933,6 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
         sum += __shfl_xor_sync(0xffffffffu, sum, off);
         z += __shfl_xor_sync(0xffffffffu, z, off);
       }
+      if (kCentred) z = fmaf(ones[h], -7.5f / nu, z);
       const float inv = nch > 1 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
       const float ka = back * inv, kb = ka * 0.0625f;
       z *= inv;

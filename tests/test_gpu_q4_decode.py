@@ -162,6 +162,29 @@ def test_query_sizes(pkv, factor):
     c.check(c.decode())
 
 
+@pytest.mark.parametrize("power", [100, 113, 114, 120, 126])
+def test_queries_near_the_end_of_bf16(pkv, power):
+    """Logits of up to 2^128 in fp32: the largest takes all the weight. The bound is the output's rounding and that of
+    p s to fp16 (p = 1): half a step each of the largest value, and fp32 terms far below them."""
+    c = Case(pkv, [5, 300, 1111], 4, 2, BF16, seed=5)
+    c.k *= 2.0 ** -4
+    c.fill()
+    c.q = c.q.sign() * 2.0 ** power
+    c.q[1] *= 1.5
+    out = c.decode().double()
+    assert pkv.pkv_device_error() == 0
+    for b in range(3):
+        a, e = c.first[b], c.first[b + 1]
+        k, v = (R.values(*R.quantise(x[a:e])) for x in (c.k, c.v))
+        for h in range(4):
+            logits = k[:, h // 2] @ c.q[b, h].double()
+            best = logits.topk(2).values
+            assert float(best[0] - best[1]) > 2.0 ** -16 * float(logits.abs().max()), "inputs: a clear largest logit"
+            want = v[int(logits.argmax()), h // 2]
+            tol = (2.0 ** -8 + 2.0 ** -10) * want.abs().max()
+            assert bool(((out[b, h] - want).abs() <= tol).all()), (b, h)
+
+
 def test_nan_rows_reach_only_their_sequence_and_group(pkv):
     c = Case(pkv, [100, 100, 100], 4, 2, BF16, seed=5)
     c.v[50, 0, 40] = float("nan")                   # sequence 0, kv head 0, group 1 of V
@@ -231,6 +254,24 @@ def test_step_wrong_slots_are_not_stored(pkv):
     assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_SLOT
     assert torch.equal(c.kc, kc)
     c.check(out)
+
+
+def test_step_slot_without_context(pkv):
+    """A padding row has no position that a slot could belong to: nothing is stored, and the slot is reported."""
+    for lens in ([40, 0], [40] + [0] * 40):         # either form of the item table
+        c = Case(pkv, lens, 4, 2, BF16, seed=17).fill()
+        kc = c.kc.clone()
+        B = len(lens)
+        rows = torch.zeros((B, 2, 128), dtype=BF16, device="cuda")
+        slot = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+        step = lambda: c.f("pkv_store_decode_q4")(c.q, rows, rows, slot, c.kc, c.vc, c.tables, c.ctx, c.max_ctx,
+                                                  c.scale, c.workspace())
+        c.check(step())
+        slot[1] = int(c.slots[3])
+        out = step()
+        assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_SLOT
+        assert torch.equal(c.kc, kc)
+        c.check(out)
 
 
 def test_bad_blocks_and_lengths_are_reported(pkv):
