@@ -423,7 +423,10 @@ int pkv_store_decode_q4_f16(const void* q, int64_t q_row_stride, const void* k, 
  * on the same stream) taken from the 4-bit cache. The values are rounded to the
  * element type as pkv_load_kvcache_q4 rounds them, and the arithmetic is
  * pkv_prefill_varlen's: the result is that of loading the rows and attending to
- * them contiguously, without the load. A group of V that reads back as NaN
+ * them contiguously, without the load. A call of few query tiles splits their
+ * keys over up to 8 CTAs, whose fp32 partial results are added in key order; how
+ * follows from the call's sizes alone (the bounds of the lengths and the block
+ * table's width among them), so equal calls give equal bits. A group of V that reads back as NaN
  * gives NaN in its 32 dims to the rows that may attend to it, and to no others.
  * Arguments, errors and the optional tile plan in `workspace` are as for
  * pkv_prefill_varlen. Rows of q and out that belong to no sequence are left

@@ -5,10 +5,10 @@
 // position Lk_b - Lq_b + i and attends to keys 0..that position. A key or value
 // element is s * c + z (q4.cuh) rounded to the element type, exactly what
 // pkv_load_kvcache_q4 returns, and the products, softmax and roundings are
-// those of prefill.cu in the same order: the output has the bits of loading the
-// rows and attending to them contiguously. What it saves is that round trip:
-// 512 bytes written and read again per (token, kv head), for every sequence
-// that shares a prefix.
+// those of prefill.cu in the same order: but for tiles whose keys are split (see
+// launch_typed), the output has the bits of loading the rows and attending to them
+// contiguously. What it saves is that round trip: 512 bytes written and read again
+// per (token, kv head), for every sequence that shares a prefix.
 //
 // One CTA computes a 128-row query tile of one sequence for two query heads of
 // one kv head, so a K or V tile is widened once for two products:
@@ -38,20 +38,23 @@
 // needs without spilling (shared memory leaves no L1 for local memory: the first
 // form, which spilled, took 904 us where this takes 491).
 //
-// What bounds it: issue slots. A key tile costs about 4.3 k warp instructions of
-// widening and 9 k of softmax a CTA, over four schedulers, against 1024 cycles of
-// tensor core. 128 prompts of 64..512 tokens on a shared prefix of 4096 (16 query
-// heads on 8): 491 us, 0.72 PFLOP/s; 5000 tokens after 7001: 457 us, 0.85. With
-// the tiles' widening left out the latter would take 367. Measured and not kept:
-// 4 widening warps (570 with register pressure solved; they are late), 6 (580:
-// the three schedulers that get two are uneven), P through shared memory (545),
-// logits in 64-key halves with two in flight for each head (630: 13 % more
-// instructions where they are what is short).
+// What bounds it: the softmax of one head's tile, which its next two products wait
+// for and which shares the schedulers with the widening. A key tile takes 2.1-2.6
+// us: about 4.5 k warp instructions of widening and 6 k of softmax over four
+// schedulers, against 2048 cycles (1.1 us) of tensor core; the tensor pipe is
+// active half of the time, instructions issue in 57 % of the cycles. 128 prompts of
+// 64..512 tokens on a shared prefix of 1024 (16 query heads on 8): 491 us, 0.72
+// PFLOP/s; 5000 tokens after 7001: 386 us, 1.0. Measured on the latter before keys
+// were split (then 457) and not kept: no widening at all, for comparison, 367; 4
+// widening warps (570; they are late), 6 (544: the schedulers have uneven loads),
+// P through shared memory (515), logits in 64-key halves with two in flight for
+// each head (630: more instructions), waits with a suspend hint or a sleep (same).
 // TMEM columns, issue order, the lazily moved maximum and the epilogue are as in
 // prefill.cu.
 #include <cuda.h>
 
 #include <climits>
+#include <mutex>
 
 #include "q4.cuh"
 
@@ -106,6 +109,7 @@ struct Q4PrefillParams {
   int32_t hkv;
   float scale_log2;
   const int32_t* items;  // optional tile plan: (qt << 16) | b per item; NULL: all pairs
+  int32_t first;         // the launch's first work item (query tiles x pairs of heads)
   uint16_t* out;
   unsigned int* err;
 };
@@ -168,7 +172,37 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <Elem E>
+// The cluster of CTAs that split the keys of one query tile (kSplit).
+__device__ __forceinline__ int cluster_parts() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ int cluster_part() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// this CTA's shared address -> the same place in another CTA of the cluster
+__device__ __forceinline__ uint32_t in_part(uint32_t addr, int part) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(part));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+
+template <Elem E, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_kernel(const __grid_constant__ CUtensorMap tm_q, const Q4PrefillParams p) {
   using Ops = ElemOps<E>;
@@ -187,9 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- work item: (query tile, sequence, pair of query heads), longest tiles first ----
   const int pairs = p.hq / 2;
+  const int parts = kSplit ? cluster_parts() : 1, part = kSplit ? cluster_part() : 0;
   int qt, b, pair;
   {
-    const int cta = static_cast<int>(blockIdx.x);
+    const int cta = p.first + static_cast<int>(blockIdx.x) / parts;
     pair = cta % pairs;
     if (p.items) {
       const int code = p.items[cta / pairs];
@@ -208,14 +243,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Lq = cq1 - cq0, Lk = p.cu_k[b + 1] - p.cu_k[b];
   if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || Lk > INT_MAX - 2 * kBN || cq0 < 0 || cq1 > p.total_q ||
       Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
-    if (threadIdx.x == 0 && qt == 0 && pair == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+    if (threadIdx.x == 0 && qt == 0 && pair == 0 && part == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
   }
   const int r0 = qt * kBM;
   if (r0 >= Lq) return;
   const int rows_valid = min(kBM, Lq - r0);
   const int pos0 = Lk - Lq + r0;  // position of the tile's first query row
-  const int n_tiles = (pos0 + rows_valid - 1) / kBN + 1;
+  const int n_all = (pos0 + rows_valid - 1) / kBN + 1;
+  const int tile0 = n_all * part / parts;                    // this CTA's key tiles: from tile0 on
+  const int n_tiles = n_all * (part + 1) / parts - tile0;    // (0 only where the keys are split)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
@@ -276,8 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_f16kind_ts(tmem + 256 + g * 128, pa + ks * 8, vbb + ((ks * 16 * 128) >> 4), idesc_pv,
                          (n > 0 || ks > 0) ? 1u : 0u);
       };
-      if (ok) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
-      if (ok) {
+      const bool any = n_tiles > 0;
+      if (ok && any) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
+      if (ok && any) {
         tc_fence_after();
         issue_s(0, 0);
         mma_commit(bar(kBarSFull + 0));
@@ -315,13 +353,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(kBarDrain), 0, p.err);
       }
     }
+    __syncwarp();
+    if (kSplit) cluster_sync();
     if (warp == 1) {
       // TMEM is released after every softmax warp's last tensor-memory read
-      __syncwarp();
       mbar_wait(bar(kBarStaged), 0, p.err);
       tc_fence_after();
       tmem_dealloc(tmem, 512);
     }
+    if (kSplit) cluster_sync();
   } else if (warp >= kWidenWarp0) {
     // =========================== K/V widening ===========================
     regs_dec<kRegsWiden>();
@@ -330,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = lane & 3;
     const bool odd = (lane >> 2) & 1;
     auto block_of = [&](int n) -> int {
-      return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + n * kBN / kBlockSize] : -1;
+      return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + (tile0 + n) * kBN / kBlockSize] : -1;
     };
     auto checked = [&](int blk) -> int {
       if (blk >= 0 && blk < p.num_blocks) return blk;
@@ -342,15 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_batch = [&](int i, int j, int blk) {
       codes[j] = par[j] = make_uint4(0, 0, 0, 0);
       const int row = row0 + 8 * j;
-      if (blk < 0 || (i >> 1) * kBN + row >= Lk) return;  // zeros: a scale and a minimum of 0
+      const int key0 = (tile0 + (i >> 1)) * kBN;
+      if (blk < 0 || key0 + row >= Lk) return;  // zeros: a scale and a minimum of 0
       const uint8_t* base = ((i & 1) ? p.v_cache : p.k_cache) +
                             (static_cast<int64_t>(blk) * p.hkv + kv_head) * kQ4RecordBytes +
-                            ((i >> 1) * kBN % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
+                            (key0 % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
       const int tok = row % kQ4Tile;
       codes[j] = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + t * 16));
       par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
     };
-    int blk = checked(block_of(0)), blk_next = -1;
+    int blk = n_tiles > 0 ? checked(block_of(0)) : -1, blk_next = -1;
 #pragma unroll
     for (int j = 0; j < 2; ++j) load_batch(0, j, blk);
     for (int i = 0; i < 2 * n_tiles; ++i) {
@@ -379,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if ((sz[k] & 0x7fffu) > 0x7c00u) {  // a NaN scale
-              atomicMin(s_nan + k, (i >> 1) * kBN + row);
+              atomicMin(s_nan + k, (tile0 + (i >> 1)) * kBN + row);
               sz[k] = 0u;
             }
         }
@@ -403,6 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarKvFull + slot));
+    }
+    __syncwarp();
+    if (kSplit) {
+      cluster_sync();
+      cluster_sync();
     }
   } else {
     // =========================== softmax groups ===========================
@@ -447,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s[96 + j] = __uint_as_float(r3[j]);
         }
       }
-      const int key0 = n * kBN;
+      const int key0 = (tile0 + n) * kBN;
       if (key0 + kBN - 1 > pos0 || key0 + kBN > Lk) {
         const int lim = min(pos, Lk - 1) - key0;  // keys j <= lim are visible
 #pragma unroll
@@ -467,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_use);
       l *= alpha;
       const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
-      const uint64_t negm2 = f32x2_pack(-m_use, -m_use);
+      const float neg_m = kSplit && m_use == -INFINITY ? 0.f : -m_use;  // a part may begin with keys that a row can't see
+      const uint64_t negm2 = f32x2_pack(neg_m, neg_m);
       // P = 2^(s*sl2 - m_use), rounded to the element type, over the logits in TMEM
       uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -513,10 +560,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), 0, s_abort, p.err));
+    const uint32_t stage = sbase + kOffQ;
+    if constexpr (kSplit) {
+      // Epilogue of a CTA that had some of the keys. The rows' maxima and sums are
+      // exchanged; then every row is scaled for the common maximum and sum and goes
+      // to the CTA that adds up its parts, in their order: rows_own of the 256 rows
+      // (both heads') each. The ring is idle in every CTA by then.
+      const int rows_own = 256 / parts;
+      const int ri = g * 128 + row;
+      const uint32_t ml = sbase + kOffKV + 4 * kTileBytes;  // behind the 128 KB that rows arrive in
+      if (!ok) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml + ri * 8), "f"(m), "f"(l) : "memory");
+      cluster_sync();
+      float M = -INFINITY, L = 0.f;
+      for (int i = 0; i < parts; ++i) M = fmaxf(M, ld_cluster_f2(in_part(ml + ri * 8, i)).x);
+      if (M == -INFINITY) M = 0.f;
+      for (int i = 0; i < parts; ++i) {
+        const float2 v = ld_cluster_f2(in_part(ml + ri * 8, i));
+        L = fmaf(ex2_approx(v.x - M), v.y, L);
+      }
+      const float inv = ex2_approx(m - M) * ((L > 0.f ? 1.f / L : L == L ? 0.f : L) * out_scale);
+      const uint32_t dst = in_part(stage + (part * rows_own + ri % rows_own) * 512, ri / rows_own);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // group c of 32 dims
+        uint32_t x[32];
+        if (ok && n_tiles > 0) {
+          tmem_ld32(tO + c * 32, x);
+          tmem_wait_ld();
+          tmem_reg_fence(x);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * inv);
+        if (pos >= s_nan[c]) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0x7fffffffu;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          st_cluster_f4(dst + (((c * 8 + j / 4) ^ (row & 31)) << 4), __uint_as_float(x[j]), __uint_as_float(x[j + 1]),
+                        __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarStaged));
+      cluster_sync();
+      for (int lr = warp - kSoftmaxWarp0; lr < rows_own; lr += 8) {
+        const int r2 = part * rows_own + lr, q_row = r2 & 127;
+        if (q_row >= rows_valid) continue;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < parts; ++i) {
+          float4 v;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "r"(stage + (i * rows_own + lr) * 512 + ((lane ^ (q_row & 31)) << 4))
+                       : "memory");
+          o.x += v.x;
+          o.y += v.y;
+          o.z += v.z;
+          o.w += v.w;
+        }
+        uint2 w;
+        w.x = Ops::pack(o.x, o.y);
+        w.y = Ops::pack(o.z, o.w);
+        *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(cq0 + r0 + q_row) * p.hq + 2 * pair + (r2 >> 7)) * kHeadDim +
+                                  lane * 4) = w;
+      }
+      return;
+    }
     // Epilogue: every product is complete, so O is staged in the two Q tiles (both
     // heads of a query row side by side, 512 B, 16-byte chunks rotated by the row)
     // and leaves as whole rows.
-    const uint32_t stage = sbase + kOffQ;
     if (ok) {
       tc_fence_after();
       const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * out_scale;
@@ -591,19 +711,108 @@ bool encode_q(CUtensorMap* tm, const void* base, int64_t rows, int heads, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMinPartTiles = 2;  // key tiles per CTA at least, where the keys of an item are split
+
+template <Elem E, bool kSplit>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(prefill_q4_kernel<E, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kSmemBytes));
+}
+
+struct DeviceLimits {
+  bool known;
+  int sms;
+  int clusters[4];  // clusters of 1, 2, 4 and 8 CTAs that run at once
+};
+
+cudaLaunchConfig_t launch_config(unsigned ctas, int parts, cudaLaunchAttribute* attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(parts);
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  return cfg;
+}
+
 template <Elem E>
-cudaError_t launch_typed(const CUtensorMap& tq, const Q4PrefillParams& p, unsigned nblocks, cudaStream_t stream) {
-  static bool attr_done[64] = {false};
+cudaError_t device_limits(DeviceLimits* out) {
+  static DeviceLimits all[64];
+  static std::mutex lock;
+  const std::lock_guard<std::mutex> hold(lock);
   int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(prefill_q4_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kSmemBytes));
-    if (e != cudaSuccess) return e;
-    attr_done[dev] = true;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && all[dev].known) {
+    *out = all[dev];
+    return cudaSuccess;
   }
-  prefill_q4_kernel<E><<<nblocks, kThreads, kSmemBytes, stream>>>(tq, p);
-  return cudaGetLastError();
+  DeviceLimits d{};
+  if ((e = allow_smem<E, false>()) != cudaSuccess || (e = allow_smem<E, true>()) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  d.clusters[0] = d.sms;
+  for (int i = 1; i < 4; ++i) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(d.sms) << i, 1 << i, &attr, nullptr);
+    if ((e = cudaOccupancyMaxActiveClusters(&d.clusters[i], prefill_q4_kernel<E, true>, &cfg)) != cudaSuccess) return e;
+  }
+  d.known = true;
+  if (dev >= 0 && dev < 64) all[dev] = d;
+  *out = d;
+  return cudaSuccess;
+}
+
+// The items run longest first, one CTA to an SM. What is left of them after whole
+// rounds would keep a few SMs busy for one more item, and a call of few items uses
+// few SMs from the start. Where all of that rest can run at once with each item's
+// keys split over a cluster of 2, 4 or 8 CTAs, it does, as a launch of its own,
+// the most parts first that leave a part kMinPartTiles key tiles. Times in key
+// tiles (about 2.1 us each): the rest takes `tiles` as it is, less what it fits
+// into the first round's uneven end (after an even number of rounds the long and
+// the short items have evened out), and tiles / parts when split, plus 2 for the
+// merge and 6 for the launch after others.
+//   16 query heads on 8   whole  2 parts  4 parts  8 parts   (us)
+//      16 tokens after 512   20.6    21.6     21.3     19.6   kept whole
+//     128 after 2048         45.2    34.9     28.8     24.7   8 parts
+//     512 after 1024         37.0    28.8     25.7     (59)   4: 32 clusters of 8 don't fit at once
+//    1024 after 4096         94.4    59.5      (73)    (128)  2
+//    2800 after 1024         74.9    99.5     95.4    112.5   whole: the rest fits into the uneven end
+//    3000 after 5000        208.0   203.9    218.2    226.5   whole
+//    5000 after 2000        215.2   207.7    200.8    216.2   4
+//    5000 after 7001        459.9   412.8    386.2    398.5   4
+template <Elem E>
+cudaError_t launch_typed(const CUtensorMap& tq, Q4PrefillParams& p, int64_t n_items, int32_t prefix_tiles,
+                         cudaStream_t stream) {
+  DeviceLimits d;
+  cudaError_t e = device_limits<E>(&d);
+  if (e != cudaSuccess) return e;
+  const int64_t rest = n_items % d.sms, rounds = n_items / d.sms;
+  int shift = 0;
+  if (rest > 0) {
+    const int64_t per_tile = (n_items + p.max_q_tiles - 1) / p.max_q_tiles;  // items as long as one another
+    const int64_t tiles = prefix_tiles + (rest + per_tile - 1) / per_tile;   // key tiles of the first of the rest
+    const int64_t uneven = rounds % 2 == 1 ? d.sms / per_tile : 0;
+    for (int i = 1; i < 4; ++i) {
+      const int64_t split = (tiles >> i) + (rounds > 0 ? 8 : 2);
+      if (rest <= d.clusters[i] && tiles >> i >= kMinPartTiles && tiles - uneven - split >= 2) shift = i;
+    }
+  }
+  const unsigned whole = static_cast<unsigned>(shift > 0 ? n_items - rest : n_items);
+  if (whole > 0) {
+    prefill_q4_kernel<E, false><<<whole, kThreads, kSmemBytes, stream>>>(tq, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (shift > 0) {
+    p.first = static_cast<int32_t>(whole);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(rest) << shift, 1 << shift, &attr, stream);
+    return cudaLaunchKernelEx(&cfg, prefill_q4_kernel<E, true>, tq, const_cast<const Q4PrefillParams&>(p));
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -638,9 +847,14 @@ cudaError_t launch_prefill_q4(const void* q, int64_t q_row_stride, int32_t total
   const int64_t pairs = hq / 2;
   const int64_t nblocks = p.items ? num_items * pairs : static_cast<int64_t>(p.max_q_tiles) * num_seqs * pairs;
   if (nblocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned nb = static_cast<unsigned>(nblocks);
-  return elem == Elem::kF16 ? launch_typed<Elem::kF16>(tq, p, nb, stream)
-                            : launch_typed<Elem::kBF16>(tq, p, nb, stream);
+  // tiles of keys before the queries, as far as the bounds of the lengths tell
+  const int64_t table_keys = static_cast<int64_t>(bt_stride) * kBlockSize;
+  const int64_t keys = max_seqlen_k < table_keys ? max_seqlen_k : table_keys;
+  const int64_t queries = max_seqlen_q < total_q ? max_seqlen_q : total_q;
+  const int32_t prefix_tiles = keys > queries ? static_cast<int32_t>((keys - queries) / kBN) : 0;
+  p.first = 0;
+  return elem == Elem::kF16 ? launch_typed<Elem::kF16>(tq, p, nblocks, prefix_tiles, stream)
+                            : launch_typed<Elem::kBF16>(tq, p, nblocks, prefix_tiles, stream);
 }
 
 }  // namespace pkv

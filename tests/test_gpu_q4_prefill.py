@@ -1,5 +1,6 @@
 """Prefill over the 4-bit cache: against attention in 64 bits over the values read
-back, and bit for bit against loading the rows and running the 16-bit prefill."""
+back and, where no keys are split over CTAs, bit for bit against loading the rows
+and running the 16-bit prefill."""
 import numpy as np
 import pytest
 import torch
@@ -77,13 +78,70 @@ def test_head_layouts(pkv, hq, hkv, dtype):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_bits_of_load_then_prefill(pkv, dtype):
-    """The same bits as pkv_load_kvcache_q4 followed by the contiguous 16-bit prefill; with a tile plan too."""
+    """The same bits as pkv_load_kvcache_q4 followed by the contiguous 16-bit prefill; with a tile plan too. (160 and 88
+    pairs of a tile and two heads, too many for their keys to be split.)"""
     c = Prefill(pkv, [300, 1, 129, 513], [1324, 700, 129, 2048], 16, 8, dtype, seed=21).fill()
     k, v = c.f("pkv_load_kvcache_q4")(c.kc, c.vc, c.slots)
     want = c.f("pkv_prefill_varlen")(c.q, c.d_cq, c.d_ck, max(c.lq), max(c.lens), c.scale, k=k, v=v)
     assert torch.equal(c.prefill(), want)
     plan = pkv.pkv_prefill_plan(c.cq, c.ck)
     assert torch.equal(c.prefill(plan=plan), want)
+
+
+# Few query tiles behind many keys: the keys of a tile are split over 2, 4 or 8 CTAs.
+SPLIT = [
+    ([100], [6000]), ([1], [2500]), ([1, 100, 0], [1, 6000, 40]),      # parts without keys
+    ([500, 3], [5000, 4990]),                                          # rows that see none of a part's keys
+    ([300, 300, 40], [2348, 2300, 2048]),                              # 2 CTAs
+    ([2560], [8560])]                                                  # whole rounds of tiles, then 8 split ones
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lq,lk", SPLIT)
+def test_keys_split_over_ctas(pkv, lq, lk, dtype):
+    c = Prefill(pkv, lq, lk, 16, 8, dtype, seed=31 + len(lq)).fill()
+    out = c.prefill()
+    c.check(out)
+    assert torch.equal(c.prefill(), out)
+    c.check(c.prefill(plan=pkv.pkv_prefill_plan(c.cq, c.ck)))
+
+
+def test_split_heads_growing_logits_and_graph(pkv):
+    """Other head layouts; maxima that differ from part to part; captured and replayed."""
+    for hq, hkv in ((8, 1), (4, 2), (32, 8)):
+        c = Prefill(pkv, [130, 7], [4400, 3000], hq, hkv, BF16, seed=40 + hq)
+        c.k = (c.k.float() + torch.linspace(-3, 3, c.k.shape[0], device="cuda")[:, None, None]).to(BF16)
+        c.q = c.q.abs()
+        want = c.fill().prefill()
+        c.check(want)
+        out = torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.prefill(out=out)
+        for _ in range(2):
+            out.fill_(9.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+def test_split_nan_values_and_bad_blocks(pkv):
+    lq, lk = [200, 50], [5000, 4000]
+    c = Prefill(pkv, lq, lk, 4, 2, BF16, seed=45).fill()
+    want = c.prefill()
+    c.v[4900, 1, 40] = float("nan")                 # sequence 0, group 1 of kv head 1: rows at or past key 4900
+    c.v[c.first[1] + 700, 0, 3] = float("inf")      # sequence 1, group 0 of kv head 0: every row
+    out = c.fill().prefill()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[4900 - 4800:200, 2:4, 32:64] = True
+    hit[200:250, 0:2, 0:32] = True
+    assert bool(out[hit].isnan().all())
+    assert torch.equal(out[~hit], want[~hit])
+    assert pkv.pkv_device_error() == 0
+    c.tables[1, 9] = 10 ** 6
+    out = c.prefill()
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_BLOCK
+    assert torch.equal(out[:200][~hit[:200]], want[:200][~hit[:200]])
 
 
 def test_growing_logits(pkv):
