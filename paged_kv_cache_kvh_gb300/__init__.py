@@ -381,92 +381,99 @@ def q4_cache(num_blocks: int, num_kv_heads: int = NUM_KV_HEADS, device="cuda") -
 
 
 # The calls below are made once per layer and step, and a small one is over on the
-# GPU in a few microseconds: their checks read each tensor property once and build
-# no message unless one fails.
+# GPU in a few microseconds, less than its checks can take here (and a launch that
+# finds the GPU idle costs the host twice as much): so each tensor property is read
+# once and no message is built unless a check fails.
+_U8, _I32 = torch.uint8, torch.int32
+_current_device, _current_raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _raw_stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_raw_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _table(t, dev, name):
-    if t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor on the current device")
 
 
-def _rows_q4(t, dev, dtype, heads, name):
-    """Checks [N, heads, 128] rows and returns the elements between them (a single row may carry any stride)."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != dtype or t.get_device() != dev:
+def _rows_q4(t, dev, dtype, name):
+    """Checks [N, heads, 128] rows and returns N, heads and the elements between rows (a single row may carry any
+    stride)."""
+    if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {_TYPE_NAME[dtype]} CUDA tensor on the current device")
-    if len(shape) != 3 or shape[1] != heads or shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must be [N, {heads}, 128]")
-    if stride[2] != 1 or (stride[1] != HEAD_DIM and heads > 1):
-        raise ValueError(f"{name}: heads and dims must be contiguous within a row")
-    return stride[0] if shape[0] > 1 else heads * HEAD_DIM
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N, heads, 128]")
+    n, heads, dims = t.shape
+    row, head, dim = t.stride()
+    if dims != HEAD_DIM or dim != 1 or (head != HEAD_DIM and heads > 1):
+        raise ValueError(f"{name} must be [N, heads, 128] with heads and dims contiguous within a row")
+    return n, heads, row if n > 1 else heads * HEAD_DIM
 
 
 def _dense(t, dev, dtype, shape, name):
-    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {_TYPE_NAME[dtype]} {tuple(shape)} on the current CUDA device")
 
 
 def _q4_caches(k_cache, v_cache, dev):
     """Checks the pair and returns (blocks, num_kv_heads)."""
     shape = k_cache.shape
-    if len(shape) != 4 or shape[2] != Q4_TILES or shape[3] != Q4_TILE_BYTES:
-        raise ValueError("k_cache must be uint8 [blocks, num_kv_heads, 16, 1280] (q4_cache)")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.uint8 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous uint8 {tuple(shape)} on the current CUDA device (q4_cache)")
+    if len(shape) != 4 or shape[2] != Q4_TILES or shape[3] != Q4_TILE_BYTES or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [blocks, num_kv_heads, 16, 1280] (q4_cache)")
+    if (k_cache.dtype is not _U8 or v_cache.dtype is not _U8 or k_cache.get_device() != dev
+            or v_cache.get_device() != dev or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous uint8 tensors on the current CUDA device (q4_cache)")
     return shape[0], shape[1]
 
 
-def _call(entry, *args):
-    status = getattr(_lib, entry)(*args)
-    if status != PKV_OK:
-        raise PkvError(status, entry)
-
-
 def _store_q4(entry, dtype, k, v, k_cache, v_cache, slot_mapping, stream):
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     blocks, hkv = _q4_caches(k_cache, v_cache, dev)
-    ks, vs = _rows_q4(k, dev, dtype, hkv, "k"), _rows_q4(v, dev, dtype, hkv, "v")
+    n, kh, ks = _rows_q4(k, dev, dtype, "k")
+    vn, vh, vs = _rows_q4(v, dev, dtype, "v")
     _table(slot_mapping, dev, "slot_mapping")
-    n = k.shape[0]
-    if v.shape[0] != n or slot_mapping.numel() != n:
+    if vn != n or slot_mapping.numel() != n:
         raise ValueError("k, v and slot_mapping must have one entry per token")
-    _call(entry, k.data_ptr(), ks, v.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
-          n, hkv, HEAD_DIM, BLOCK_SIZE, blocks, _raw_stream(stream, dev))
+    if kh != hkv or vh != hkv:
+        raise ValueError(f"k and v must have the caches' {hkv} heads")
+    status = entry(k.data_ptr(), ks, v.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+                   n, hkv, HEAD_DIM, BLOCK_SIZE, blocks, _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
 
 
 def pkv_store_kvcache_q4(k, v, k_cache, v_cache, slot_mapping, stream=None):
     """store_kvcache into the 4-bit cache: bf16 rows k[i], v[i] quantised into slot
     slot_mapping[i] (-1: skipped). k, v [N, num_kv_heads, 128], rows may be strided."""
-    _store_q4("pkv_store_kvcache_q4", torch.bfloat16, k, v, k_cache, v_cache, slot_mapping, stream)
+    _store_q4(_lib.pkv_store_kvcache_q4, torch.bfloat16, k, v, k_cache, v_cache, slot_mapping, stream)
 
 
 def pkv_store_kvcache_q4_f16(k, v, k_cache, v_cache, slot_mapping, stream=None):
     """pkv_store_kvcache_q4 of fp16 rows."""
-    _store_q4("pkv_store_kvcache_q4_f16", torch.float16, k, v, k_cache, v_cache, slot_mapping, stream)
+    _store_q4(_lib.pkv_store_kvcache_q4_f16, torch.float16, k, v, k_cache, v_cache, slot_mapping, stream)
 
 
 def _load_q4(entry, dtype, k_cache, v_cache, slot_mapping, k, v, stream):
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     blocks, hkv = _q4_caches(k_cache, v_cache, dev)
     _table(slot_mapping, dev, "slot_mapping")
     n = slot_mapping.numel()
     shape = (n, hkv, HEAD_DIM)
     if k is None:
         k = torch.zeros(shape, dtype=dtype, device=k_cache.device)
+    else:
+        _dense(k, dev, dtype, shape, "k")
     if v is None:
         v = torch.zeros(shape, dtype=dtype, device=k_cache.device)
-    _dense(k, dev, dtype, shape, "k")
-    _dense(v, dev, dtype, shape, "v")
-    _call(entry, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hkv, HEAD_DIM, BLOCK_SIZE, blocks,
-          k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev))
+    else:
+        _dense(v, dev, dtype, shape, "v")
+    status = entry(k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hkv, HEAD_DIM, BLOCK_SIZE,
+                   blocks, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
     return k, v
 
 
@@ -475,12 +482,12 @@ def pkv_load_kvcache_q4(k_cache, v_cache, slot_mapping, *, k=None, v=None, strea
     slot slot_mapping[i]. Rows of slot -1 are left as they were (zeros where the
     binding allocates k or v). Returns (k, v) [N, num_kv_heads, 128]; contiguous
     keys for pkv_prefill_varlen, for instance."""
-    return _load_q4("pkv_load_kvcache_q4", torch.bfloat16, k_cache, v_cache, slot_mapping, k, v, stream)
+    return _load_q4(_lib.pkv_load_kvcache_q4, torch.bfloat16, k_cache, v_cache, slot_mapping, k, v, stream)
 
 
 def pkv_load_kvcache_q4_f16(k_cache, v_cache, slot_mapping, *, k=None, v=None, stream=None):
     """pkv_load_kvcache_q4 into fp16 rows (saturated at 65504)."""
-    return _load_q4("pkv_load_kvcache_q4_f16", torch.float16, k_cache, v_cache, slot_mapping, k, v, stream)
+    return _load_q4(_lib.pkv_load_kvcache_q4_f16, torch.float16, k_cache, v_cache, slot_mapping, k, v, stream)
 
 
 def pkv_decode_q4_workspace_bytes(num_seqs: int, max_context_len: int, num_heads: int = NUM_HEADS,
@@ -497,34 +504,37 @@ def decode_q4_workspace(num_seqs: int, max_context_len: int, num_heads: int = NU
 
 def _decode_q4(entry, dtype, q, new, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale,
                workspace, out, stream):
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     blocks, hkv = _q4_caches(k_cache, v_cache, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be [B, num_heads, 128]")
-    B, hq = q.shape[0], q.shape[1]
-    qs = _rows_q4(q, dev, dtype, hq, "q")
+    B, hq, qs = _rows_q4(q, dev, dtype, "q")
     _table(block_tables, dev, "block_tables")
     _table(context_lens, dev, "context_lens")
     tables = block_tables.shape
     if len(tables) != 2 or tables[0] < B or context_lens.numel() < B:
         raise ValueError("block_tables must be [B, width] and context_lens [B]")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
-    if workspace.dtype != torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+    if workspace.dtype is not _U8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the current CUDA device")
     rows = ()
     if new is not None:
         k, v, slot_mapping = new
-        rows = (k.data_ptr(), _rows_q4(k, dev, dtype, hkv, "k"), v.data_ptr(), _rows_q4(v, dev, dtype, hkv, "v"),
-                slot_mapping.data_ptr())
+        kn, kh, ks = _rows_q4(k, dev, dtype, "k")
+        vn, vh, vs = _rows_q4(v, dev, dtype, "v")
         _table(slot_mapping, dev, "slot_mapping")
-        if k.shape[0] < B or v.shape[0] < B or slot_mapping.numel() < B:
+        if kn < B or vn < B or slot_mapping.numel() < B:
             raise ValueError("k, v and slot_mapping must have one new row per sequence")
-    _call(entry, q.data_ptr(), qs, *rows, k_cache.data_ptr(), v_cache.data_ptr(), blocks, block_tables.data_ptr(),
-          tables[1], context_lens.data_ptr(), B, hq, hkv, HEAD_DIM, BLOCK_SIZE, int(max_context_len),
-          float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+        if kh != hkv or vh != hkv:
+            raise ValueError(f"k and v must have the caches' {hkv} heads")
+        rows = (k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr())
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
+    status = entry(q.data_ptr(), qs, *rows, k_cache.data_ptr(), v_cache.data_ptr(), blocks, block_tables.data_ptr(),
+                   tables[1], context_lens.data_ptr(), B, hq, hkv, HEAD_DIM, BLOCK_SIZE, int(max_context_len),
+                   float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                   _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
     return out
 
 
@@ -532,14 +542,14 @@ def pkv_decode_q4(q, k_cache, v_cache, block_tables, context_lens, max_context_l
                   out=None, stream=None):
     """pkv_decode over the 4-bit cache. q [B, num_heads, 128] bf16 with one or an even number of
     query heads to a kv head of the caches. Returns out [B, num_heads, 128] bf16."""
-    return _decode_q4("pkv_decode_q4", torch.bfloat16, q, None, k_cache, v_cache, block_tables, context_lens,
+    return _decode_q4(_lib.pkv_decode_q4, torch.bfloat16, q, None, k_cache, v_cache, block_tables, context_lens,
                       max_context_len, softmax_scale, workspace, out, stream)
 
 
 def pkv_decode_q4_f16(q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace, *,
                       out=None, stream=None):
     """pkv_decode_q4 with fp16 q; returns fp16."""
-    return _decode_q4("pkv_decode_q4_f16", torch.float16, q, None, k_cache, v_cache, block_tables, context_lens,
+    return _decode_q4(_lib.pkv_decode_q4_f16, torch.float16, q, None, k_cache, v_cache, block_tables, context_lens,
                       max_context_len, softmax_scale, workspace, out, stream)
 
 
@@ -547,25 +557,22 @@ def pkv_store_decode_q4(q, k, v, slot_mapping, k_cache, v_cache, block_tables, c
                         softmax_scale, workspace, *, out=None, stream=None):
     """pkv_store_kvcache_q4 of the step's new K/V rows fused into the decode launch.
     slot_mapping[b] must be -1 or the slot of position context_lens[b]-1."""
-    return _decode_q4("pkv_store_decode_q4", torch.bfloat16, q, (k, v, slot_mapping), k_cache, v_cache, block_tables,
+    return _decode_q4(_lib.pkv_store_decode_q4, torch.bfloat16, q, (k, v, slot_mapping), k_cache, v_cache, block_tables,
                       context_lens, max_context_len, softmax_scale, workspace, out, stream)
 
 
 def pkv_store_decode_q4_f16(q, k, v, slot_mapping, k_cache, v_cache, block_tables, context_lens, max_context_len,
                             softmax_scale, workspace, *, out=None, stream=None):
     """pkv_store_decode_q4 on fp16 rows; returns fp16."""
-    return _decode_q4("pkv_store_decode_q4_f16", torch.float16, q, (k, v, slot_mapping), k_cache, v_cache,
+    return _decode_q4(_lib.pkv_store_decode_q4_f16, torch.float16, q, (k, v, slot_mapping), k_cache, v_cache,
                       block_tables, context_lens, max_context_len, softmax_scale, workspace, out, stream)
 
 
 def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache,
                 v_cache, block_tables, out, plan, stream):
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     blocks, hkv = _q4_caches(k_cache, v_cache, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be [total_q, num_heads, 128]")
-    total_q, hq = q.shape[0], q.shape[1]
-    qs = _rows_q4(q, dev, dtype, hq, "q")
+    total_q, hq, qs = _rows_q4(q, dev, dtype, "q")
     _table(cu_seqlens_q, dev, "cu_seqlens_q")
     _table(cu_seqlens_k, dev, "cu_seqlens_k")
     _table(block_tables, dev, "block_tables")
@@ -573,18 +580,20 @@ def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_s
     tables = block_tables.shape
     if num_seqs < 0 or cu_seqlens_k.numel() != num_seqs + 1 or len(tables) != 2 or tables[0] < num_seqs:
         raise ValueError("cu_seqlens must be [num_seqs + 1] and block_tables [num_seqs, width]")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
     items = n_items = 0
     if plan is not None:
         _table(plan, dev, "plan (pkv_prefill_plan)")
         items, n_items = plan.data_ptr(), plan.numel()
-    _call(entry, q.data_ptr(), qs, total_q, k_cache.data_ptr(), v_cache.data_ptr(), blocks, cu_seqlens_q.data_ptr(),
-          cu_seqlens_k.data_ptr(), int(max_seqlen_q), int(max_seqlen_k), block_tables.data_ptr(), tables[1], num_seqs,
-          hq, hkv, HEAD_DIM, BLOCK_SIZE, float(softmax_scale), out.data_ptr(), items, 4 * n_items,
-          _raw_stream(stream, dev))
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
+    status = entry(q.data_ptr(), qs, total_q, k_cache.data_ptr(), v_cache.data_ptr(), blocks, cu_seqlens_q.data_ptr(),
+                   cu_seqlens_k.data_ptr(), int(max_seqlen_q), int(max_seqlen_k), block_tables.data_ptr(), tables[1],
+                   num_seqs, hq, hkv, HEAD_DIM, BLOCK_SIZE, float(softmax_scale), out.data_ptr(), items, 4 * n_items,
+                   _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
     return out
 
 
@@ -593,14 +602,14 @@ def pkv_prefill_varlen_q4(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
     """pkv_prefill_varlen in prefix-cache mode over the 4-bit cache (new tokens stored first).
     q [total_q, num_heads, 128] bf16, an even number of query heads to a kv head; plan: optional tile plan
     (pkv_prefill_plan). Returns out [total_q, num_heads, 128] bf16."""
-    return _prefill_q4("pkv_prefill_varlen_q4", torch.bfloat16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+    return _prefill_q4(_lib.pkv_prefill_varlen_q4, torch.bfloat16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                        max_seqlen_k, softmax_scale, k_cache, v_cache, block_tables, out, plan, stream)
 
 
 def pkv_prefill_varlen_q4_f16(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k_cache,
                               v_cache, block_tables, *, out=None, plan=None, stream=None):
     """pkv_prefill_varlen_q4 with fp16 q; returns fp16."""
-    return _prefill_q4("pkv_prefill_varlen_q4_f16", torch.float16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+    return _prefill_q4(_lib.pkv_prefill_varlen_q4_f16, torch.float16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                        max_seqlen_k, softmax_scale, k_cache, v_cache, block_tables, out, plan, stream)
 
 
