@@ -13,7 +13,7 @@
 // One CTA computes a 128-row query tile of one sequence for two query heads of
 // one kv head, so a K or V tile is widened once for two products:
 //   warp 0        loads the Q tiles by TMA
-//   warp 1        allocates TMEM, one lane issues every tcgen05.mma
+//   warp 1        allocates TMEM and issues every tcgen05.mma
 //   warps 4-7     softmax of the first head   (thread = TMEM lane = query row)
 //   warps 8-11    softmax of the second head
 //   warps 12-19   widen K_n, V_n (128 keys x 128 dims) into a ring of 5 tiles
@@ -38,17 +38,27 @@
 // needs without spilling (shared memory leaves no L1 for local memory: the first
 // form, which spilled, took 904 us where this takes 491).
 //
-// What bounds it: the softmax of one head's tile, which its next two products wait
-// for and which shares the schedulers with the widening. A key tile takes 2.1-2.6
-// us: about 4.5 k warp instructions of widening and 6 k of softmax over four
-// schedulers, against 2048 cycles (1.1 us) of tensor core; the tensor pipe is
-// active half of the time, instructions issue in 57 % of the cycles. 128 prompts of
-// 64..512 tokens on a shared prefix of 1024 (16 query heads on 8): 491 us, 0.72
-// PFLOP/s; 5000 tokens after 7001: 386 us, 1.0. Measured on the latter before keys
-// were split (then 457) and not kept: no widening at all, for comparison, 367; 4
-// widening warps (570; they are late), 6 (544: the schedulers have uneven loads),
-// P through shared memory (515), logits in 64-key halves with two in flight for
-// each head (630: more instructions), waits with a suspend hint or a sleep (same).
+// The issuing warp runs its loop as a whole and elects a thread for each product:
+// operand addresses then stay in uniform registers, and with TMEM addresses as
+// constants an issue is a few instructions. One thread that computed them in its
+// own registers cost 4 % (496 -> 480 us): the issue order is the products' order,
+// and the warp competes with four busy ones for its scheduler.
+//
+// What bounds it: the products, whose operands come from shared memory at its full
+// rate (two 4 KB tiles in 64 cycles for the logits), the softmax of one head's tile
+// between them, and the widening, all on the same schedulers. A key tile takes
+// 2.0-2.4 us: about 4.5 k warp instructions of widening and 6 k of softmax, against
+// 2048 cycles (1.1 us) of tensor core at its peak; the tensor pipe is active half
+// of the time, instructions issue in 57 % of the cycles. 128 prompts of 64..512
+// tokens on a shared prefix of 1024 (16 query heads on 8): 480 us, 0.74 PFLOP/s;
+// 5000 tokens after 7001: 376 us, 1.02. Measured and not kept (the first as the
+// kernel now is, the others before, in its time): two issuing warps, one for each
+// head (528 and 427: the products of both mix); no maximum of a tile's logits
+// unless their sum is out of range (506 and 378: P then waits for the sum); 4
+// widening warps (581 and 461; they are late), 6 (580 and 545 when it was 491 and
+// 457: the schedulers have uneven loads), P through shared memory (545 and 515 when
+// it was 494 and 458), logits in 64-key halves with two in flight for each head
+// (630), waits with a suspend hint or a sleep (same).
 // TMEM columns, issue order, the lazily moved maximum and the epilogue are as in
 // prefill.cu.
 #include <cuda.h>
@@ -72,7 +82,7 @@ constexpr int kWidenWarps = 8;
 constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
 
 // Registers per thread: 128 * (sum over the four warpgroups) is what the launch holds.
-constexpr int kRegsFirst = 48, kRegsSoftmax = 152, kRegsWiden = 64;
+constexpr int kRegsFirst = 80, kRegsSoftmax = 144, kRegsWiden = 56;
 static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
 
 
@@ -150,19 +160,36 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16: A's row i in TMEM lane i, two
-// 16-bit elements to a column.
-__device__ __forceinline__ void mma_f16kind_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
-                                               uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem desc], kind::f16, issued by one elected thread; the whole
+// warp calls these, so that operand addresses are computed once for it, in uniform
+// registers. A from shared memory, or (ts) from TMEM: row i in lane i, two 16-bit
+// elements to a column.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
       : "memory");
 }
-// Keeps what is computed from x where it stands: the issuing thread has few
-// registers, and every product's operand addresses would be kept in one otherwise.
-__device__ __forceinline__ void opaque(uint32_t& x) { asm volatile("" : "+r"(x)); }
+// The issuing thread's products so far arrive on the barrier when they are complete.
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -281,75 +308,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at column 0
 
   if (warp < 4) {
     regs_dec<kRegsFirst>();
     if (warp == 0 && lane == 0) mbar_wait(bar(kBarQ), 0, p.err);  // never leave a copy in flight
-    if (warp == 1 && lane == 0) {
+    if (warp == 1) {
       // =========================== MMA issuer ===========================
       constexpr uint32_t idesc_s = idesc_f16kind_f32(kBM, kBN, false, false, Ops::kMmaFormat);
       constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kHeadDim, false, true, Ops::kMmaFormat);
-      bool ok = wait_or_abort(bar(kBarQ), 0, s_abort, p.err);
-      auto slot_of = [](int i) { return i % kKvSlots; };
-      auto par_of = [](int i) { return static_cast<uint32_t>((i / kKvSlots) & 1); };
-      const uint32_t lo_kmaj = desc_lo(sbase, 16), lo_v = desc_lo(sbase, kHalfBytes);
-      auto issue_s = [&](int g, int n) {
-        uint32_t qa = lo_kmaj + ((kOffQ + g * kTileBytes) >> 4);
-        const uint32_t kbb = lo_kmaj + (kOffKV >> 4) + slot_of(2 * n) * (kTileBytes >> 4);
-        opaque(qa);
+      const uint32_t q_lo = desc_lo(sbase + kOffQ, 16);
+      const uint32_t k_lo = desc_lo(sbase + kOffKV, 16), v_lo = desc_lo(sbase + kOffKV, kHalfBytes);
+      bool ok = all_ok(wait_or_abort(bar(kBarQ), 0, s_abort, p.err));
+      int slot = 0;          // of the ring's next tile: K_0, V_0, K_1, ...
+      uint32_t parity = 0;
+      auto landed = [&]() -> bool { return all_ok(wait_or_abort(bar(kBarKvFull + slot), parity, s_abort, p.err)); };
+      auto release = [&](int which) { commit_elected(bar(kBarKvFree + which)); };  // once its products are complete
+      auto advance = [&]() {
+        const bool wrap = slot == kKvSlots - 1;
+        slot = wrap ? 0 : slot + 1;
+        parity ^= wrap ? 1u : 0u;
+      };
+      auto issue_s = [&](int g, int at) {
+        const uint32_t q = q_lo + g * (kTileBytes >> 4), k = k_lo + at * (kTileBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kHeadDim / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-          mma_f16kind_lo(tmem + g * 128, qa + off, kbb + off, idesc_s, ks > 0 ? 1u : 0u);
+          mma_ss(tmem + g * 128, q + off, k + off, idesc_s, ks > 0 ? 1u : 0u);
         }
+        commit_elected(bar(kBarSFull + g));
       };
-      auto issue_pv = [&](int g, int n) {
-        const uint32_t vbb = lo_v + (kOffKV >> 4) + slot_of(2 * n + 1) * (kTileBytes >> 4);
-        uint32_t pa = tmem + g * 128;
-        opaque(pa);
+      auto issue_pv = [&](int g, int at, bool first) {
+        const uint32_t v = v_lo + at * (kTileBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-          mma_f16kind_ts(tmem + 256 + g * 128, pa + ks * 8, vbb + ((ks * 16 * 128) >> 4), idesc_pv,
-                         (n > 0 || ks > 0) ? 1u : 0u);
+          mma_ts(tmem + 256 + g * 128, tmem + g * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), idesc_pv,
+                 ks > 0 || !first ? 1u : 0u);
       };
-      const bool any = n_tiles > 0;
-      if (ok && any) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
-      if (ok && any) {
+      if (ok && n_tiles > 0 && (ok = landed())) {
         tc_fence_after();
-        issue_s(0, 0);
-        mma_commit(bar(kBarSFull + 0));
-        issue_s(1, 0);
-        mma_commit(bar(kBarSFull + 1));
-        mma_commit(bar(kBarKvFree + slot_of(0)));
+        issue_s(0, slot);
+        issue_s(1, slot);
+        release(slot);
+        advance();
       }
       for (int n = 0; ok && n < n_tiles; ++n) {
-        const int iv = 2 * n + 1;
-        if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(iv)), par_of(iv), s_abort, p.err))) break;
-        if (!(ok = wait_or_abort(bar(kBarPReady + 0), n & 1, s_abort, p.err))) break;
+        if (!(ok = landed())) break;
+        if (!(ok = all_ok(wait_or_abort(bar(kBarPReady + 0), n & 1, s_abort, p.err)))) break;
         tc_fence_after();
-        issue_pv(0, n);
+        const int at_v = slot;
+        advance();
         const bool more = n + 1 < n_tiles;
+        issue_pv(0, at_v, n == 0);
         if (more) {
-          if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(2 * n + 2)), par_of(2 * n + 2), s_abort, p.err))) break;
+          if (!(ok = landed())) break;
           tc_fence_after();
-          issue_s(0, n + 1);
-          mma_commit(bar(kBarSFull + 0));
+          issue_s(0, slot);
         }
-        if (!(ok = wait_or_abort(bar(kBarPReady + 1), n & 1, s_abort, p.err))) break;
+        if (!(ok = all_ok(wait_or_abort(bar(kBarPReady + 1), n & 1, s_abort, p.err)))) break;
         tc_fence_after();
-        issue_pv(1, n);
-        mma_commit(bar(kBarKvFree + slot_of(iv)));
+        issue_pv(1, at_v, n == 0);
+        release(at_v);
         if (more) {
-          issue_s(1, n + 1);
-          mma_commit(bar(kBarSFull + 1));
-          mma_commit(bar(kBarKvFree + slot_of(2 * n + 2)));
+          issue_s(1, slot);
+          release(slot);
+          advance();
         }
       }
-      mma_commit(bar(kBarOFinal));
+      commit_elected(bar(kBarOFinal));
       if (!ok) {
         // make sure no product is still writing TMEM before it is released
-        mma_commit(bar(kBarDrain));
+        commit_elected(bar(kBarDrain));
         mbar_wait(bar(kBarDrain), 0, p.err);
       }
     }
@@ -775,7 +804,7 @@ cudaError_t device_limits(DeviceLimits* out) {
 // into the first round's uneven end (after an even number of rounds the long and
 // the short items have evened out), and tiles / parts when split, plus 2 for the
 // merge and 6 for the launch after others.
-//   16 query heads on 8   whole  2 parts  4 parts  8 parts   (us)
+//   16 query heads on 8   whole  2 parts  4 parts  8 parts   (us, when this was chosen)
 //      16 tokens after 512   20.6    21.6     21.3     19.6   kept whole
 //     128 after 2048         45.2    34.9     28.8     24.7   8 parts
 //     512 after 1024         37.0    28.8     25.7     (59)   4: 32 clusters of 8 don't fit at once
