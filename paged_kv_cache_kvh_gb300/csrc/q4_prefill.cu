@@ -11,7 +11,9 @@
 // per (token, kv head), for every sequence that shares a prefix.
 //
 // One CTA computes a 128-row query tile of one sequence for two query heads of
-// one kv head, so a K or V tile is widened once for two products:
+// one kv head, so a K or V tile is widened once for two products; where sequences
+// have many query tiles, two CTAs take neighbouring ones and widen half of each
+// tile for both (Share):
 //   warp 0        loads the Q tiles by TMA
 //   warp 1        allocates TMEM and issues every tcgen05.mma
 //   warps 4-7     softmax of the first head   (thread = TMEM lane = query row)
@@ -44,21 +46,22 @@
 // own registers cost 4 % (496 -> 480 us): the issue order is the products' order,
 // and the warp competes with four busy ones for its scheduler.
 //
-// What bounds it: the products, whose operands come from shared memory at its full
-// rate (two 4 KB tiles in 64 cycles for the logits), the softmax of one head's tile
+// What bounds it: the products (the logits' operands come from shared memory at
+// its full rate, two 4 KB tiles in 64 cycles), the softmax of one head's tile
 // between them, and the widening, all on the same schedulers. A key tile takes
-// 2.0-2.4 us: about 4.5 k warp instructions of widening and 6 k of softmax, against
-// 2048 cycles (1.1 us) of tensor core at its peak; the tensor pipe is active half
-// of the time, instructions issue in 57 % of the cycles. 128 prompts of 64..512
-// tokens on a shared prefix of 1024 (16 query heads on 8): 480 us, 0.74 PFLOP/s;
-// 5000 tokens after 7001: 376 us, 1.02. Measured and not kept (the first as the
-// kernel now is, the others before, in its time): two issuing warps, one for each
-// head (528 and 427: the products of both mix); no maximum of a tile's logits
-// unless their sum is out of range (506 and 378: P then waits for the sum); 4
-// widening warps (581 and 461; they are late), 6 (580 and 545 when it was 491 and
-// 457: the schedulers have uneven loads), P through shared memory (545 and 515 when
-// it was 494 and 458), logits in 64-key halves with two in flight for each head
-// (630), waits with a suspend hint or a sleep (same).
+// 2.0-2.4 us, in pairs 1.7: about 4.5 k warp instructions of widening (a pair's
+// CTA: half) and 6 k of softmax, against 2048 cycles (1.1 us) of tensor core at its
+// peak. 128 prompts of 64..512 tokens on a shared prefix of 1024 (16 query heads on
+// 8): 480 us, 0.74 PFLOP/s, the tensor pipe active 42 % of the time, instructions
+// issued in 56 % of the cycles; 5000 tokens after 7001, in pairs: 329 us, 1.17.
+// Measured and not kept, on these two, each beside what the kernel then took: two
+// issuing warps, one for each head (528 and 427 beside 480 and 376: the products of
+// both mix); no maximum of a tile's logits unless their sum is out of range (506
+// and 378 beside 496 and 386: P then waits for the sum); 4 widening warps (581 and
+// 461 beside 495 and 386; they are late) and 6 (580 and 545 beside 491 and 457: the
+// schedulers have uneven loads); P through shared memory (545 and 515 beside 494
+// and 458); logits in 64-key halves with two in flight for each head (630 beside
+// 491); waits with a suspend hint or a sleep (same).
 // TMEM columns, issue order, the lazily moved maximum and the epilogue are as in
 // prefill.cu.
 #include <cuda.h>
@@ -84,7 +87,6 @@ constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
 // Registers per thread: 128 * (sum over the four warpgroups) is what the launch holds.
 constexpr int kRegsFirst = 80, kRegsSoftmax = 144, kRegsWiden = 56;
 static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
-
 
 constexpr int kOffQ = 0;                                 // 2 tiles (and O staging in the epilogue)
 constexpr int kOffKV = 2 * kTileBytes;                   // kKvSlots tiles
@@ -120,19 +122,33 @@ struct Q4PrefillParams {
   float scale_log2;
   const int32_t* items;  // optional tile plan: (qt << 16) | b per item; NULL: all pairs
   int32_t first;         // the launch's first work item (query tiles x pairs of heads)
+  int32_t by_twos;       // items in the order of pairs of neighbouring query tiles (no plan then)
   uint16_t* out;
   unsigned int* err;
 };
 
+// kCluster: what another CTA of the cluster did before it arrived is seen as well.
+template <bool kCluster>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  if (!kCluster) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait that also gives up as soon as another role of the CTA has aborted.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                               unsigned int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (try_wait<kCluster>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    for (int i = 0; i < 32; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-    }
+    for (int i = 0; i < 32; ++i)
+      if (try_wait<kCluster>(bar, parity)) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       flag_error(err, PKV_DEVERR_TIMEOUT);
@@ -189,6 +205,14 @@ __device__ __forceinline__ void commit_elected(uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
+// The same, on the barrier at this place in both CTAs of a pair.
+__device__ __forceinline__ void commit_elected_pair(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          bar)
+      : "memory");
+}
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
@@ -229,10 +253,29 @@ __device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, f
                : "memory");
 }
 
-template <Elem E, bool kSplit>
+// Copies within the cluster: dst and bar are in another CTA.
+__device__ __forceinline__ void bulk_s2s(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void min_cluster(uint32_t addr, int x) {
+  asm volatile("{\n\t.reg .s32 old;\n\tatom.shared::cluster.min.s32 old, [%0], %1;\n\t}" ::"r"(addr), "r"(x) : "memory");
+}
+// kWhole: a CTA has a query tile and all its keys. kSplitKeys: the CTAs of a
+// cluster have parts of one tile's keys. kPaired: two CTAs have neighbouring query
+// tiles of a sequence. Each widens 64 keys of every tile and copies them to the
+// other (1 KB bulk copies between their shared memories, which arrive on the
+// other's barriers; stores to the other one directly took 520 us where these take
+// 329). A slot is free when both have used it.
+enum class Share { kWhole, kSplitKeys, kPaired };
+
+template <Elem E, Share kShare>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_kernel(const __grid_constant__ CUtensorMap tm_q, const Q4PrefillParams p) {
   using Ops = ElemOps<E>;
+  constexpr bool kSplit = kShare == Share::kSplitKeys, kPair = kShare == Share::kPaired;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the 128-byte-swizzle atoms.
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -249,20 +292,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- work item: (query tile, sequence, pair of query heads), longest tiles first ----
   const int pairs = p.hq / 2;
   const int parts = kSplit ? cluster_parts() : 1, part = kSplit ? cluster_part() : 0;
+  const int rank = kPair ? cluster_part() : 0;
   int qt, b, pair;
   {
-    const int cta = p.first + static_cast<int>(blockIdx.x) / parts;
-    pair = cta % pairs;
+    const int item = p.first + static_cast<int>(blockIdx.x) / parts;
+    const int column = (p.by_twos ? item >> 1 : item) / pairs;
+    pair = (p.by_twos ? item >> 1 : item) % pairs;
     if (p.items) {
-      const int code = p.items[cta / pairs];
+      const int code = p.items[column];
       qt = code >> 16;
       b = code & 0xffff;
     } else {
-      qt = p.max_q_tiles - 1 - cta / pairs / p.num_seqs;
-      b = cta / pairs % p.num_seqs;
+      const int level = column / p.num_seqs;
+      qt = p.max_q_tiles - 1 - (p.by_twos ? 2 * level + (item & 1) : level);
+      b = column % p.num_seqs;
+      if (!kPair && qt < 0) return;  // the place beside an odd number of tiles
     }
   }
-  if (b >= p.num_seqs || qt < 0) {  // a plan for other cu_seqlens: skip the item
+  if (b >= p.num_seqs || (!kPair && qt < 0)) {  // a plan for other cu_seqlens: skip the item
     if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
   }
@@ -270,14 +317,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Lq = cq1 - cq0, Lk = p.cu_k[b + 1] - p.cu_k[b];
   if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || Lk > INT_MAX - 2 * kBN || cq0 < 0 || cq1 > p.total_q ||
       Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
-    if (threadIdx.x == 0 && qt == 0 && pair == 0 && part == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+    if (threadIdx.x == 0 && qt <= 0 && pair == 0 && part == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
   }
   const int r0 = qt * kBM;
-  if (r0 >= Lq) return;
-  const int rows_valid = min(kBM, Lq - r0);
+  // (a pair goes on if either of its tiles has a row: the earlier one may be the place
+  // beside an odd number of tiles, qt = -1)
+  if (max(0, r0 - (kPair ? rank ^ 1 : 0) * kBM) >= Lq) return;
+  const int rows_valid = qt < 0 ? 0 : min(kBM, Lq - r0);
   const int pos0 = Lk - Lq + r0;  // position of the tile's first query row
-  const int n_all = (pos0 + rows_valid - 1) / kBN + 1;
+  // key tiles; a pair goes through those of its later tile, as far as that has rows
+  const int n_all = (Lk - Lq + min(Lq, r0 + (kPair && rank == 1 ? 2 : 1) * kBM) - 1) / kBN + 1;
   const int tile0 = n_all * part / parts;                    // this CTA's key tiles: from tile0 on
   const int n_tiles = n_all * (part + 1) / parts - tile0;    // (0 only where the keys are split)
 
@@ -285,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
       if (i >= kBarKvFull && i < kBarKvFull + kKvSlots) count = kWidenWarps;
+      if (kPair && i >= kBarKvFree && i < kBarKvFree + kKvSlots) count = 2;
       if (i == kBarPReady || i == kBarPReady + 1) count = 4;
       if (i == kBarStaged) count = 8;
       mbar_init(bar(i), count);
@@ -307,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   __syncthreads();
+  if (kPair) cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at column 0
 
@@ -322,8 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = all_ok(wait_or_abort(bar(kBarQ), 0, s_abort, p.err));
       int slot = 0;          // of the ring's next tile: K_0, V_0, K_1, ...
       uint32_t parity = 0;
-      auto landed = [&]() -> bool { return all_ok(wait_or_abort(bar(kBarKvFull + slot), parity, s_abort, p.err)); };
-      auto release = [&](int which) { commit_elected(bar(kBarKvFree + which)); };  // once its products are complete
+      auto landed = [&]() -> bool {
+        return all_ok(wait_or_abort<kPair>(bar(kBarKvFull + slot), parity, s_abort, p.err));
+      };
+      auto release = [&](int which) {  // once its products are complete
+        if (kPair)
+          commit_elected_pair(bar(kBarKvFree + which));
+        else
+          commit_elected(bar(kBarKvFree + which));
+      };
       auto advance = [&]() {
         const bool wrap = slot == kKvSlots - 1;
         slot = wrap ? 0 : slot + 1;
@@ -383,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    if (kSplit) cluster_sync();
+    if (kSplit || kPair) cluster_sync();
     if (warp == 1) {
       // TMEM is released after every softmax warp's last tensor-memory read
       mbar_wait(bar(kBarStaged), 0, p.err);
@@ -395,9 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================== K/V widening ===========================
     regs_dec<kRegsWiden>();
     const int kv_head = 2 * pair / (p.hq / p.hkv);
-    const int row0 = (warp - kWidenWarp0) * 16 + (lane >> 2);  // key of batch 0 within the tile; batch i: + 8 i
+    // key of batch 0 within the tile; batch i: + 8 i
+    const int row0 = (kPair ? rank * 64 + (warp - kWidenWarp0) * 8 : (warp - kWidenWarp0) * 16) + (lane >> 2);
     const int t = lane & 3;
     const bool odd = (lane >> 2) & 1;
+    const uint32_t other = kPair ? in_part(sbase, rank ^ 1) : 0u;  // the pair's other CTA
     auto block_of = [&](int n) -> int {
       return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + (tile0 + n) * kBN / kBlockSize] : -1;
     };
@@ -407,10 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return -1;
     };
     uint4 codes[2], par[2];
-    // ring item i: K_{i/2} (even i) or V_{i/2} (odd i)
-    auto load_batch = [&](int i, int j, int blk) {
+    // key `row` of K_{i/2} (even i) or V_{i/2} (odd i), the ring's items, into registers j
+    auto load_row = [&](int i, int row, int j, int blk) {
       codes[j] = par[j] = make_uint4(0, 0, 0, 0);
-      const int row = row0 + 8 * j;
       const int key0 = (tile0 + (i >> 1)) * kBN;
       if (blk < 0 || key0 + row >= Lk) return;  // zeros: a scale and a minimum of 0
       const uint8_t* base = ((i & 1) ? p.v_cache : p.k_cache) +
@@ -420,65 +480,107 @@ __global__ void __launch_bounds__(kThreads, 1)
       codes[j] = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + t * 16));
       par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
     };
-    int blk = n_tiles > 0 ? checked(block_of(0)) : -1, blk_next = -1;
+    // registers j -> key `row` of the item's tile; `reload` fills them again meanwhile
+    auto widen_row = [&](int i, int row, int j, uint32_t slot_off, auto reload) {
+      uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
+      uint32_t sz[4] = {par[j].x, par[j].y, par[j].z, par[j].w};
+      int tt = t;
+      if (i & 1) {
+        // two 8-byte chunks of V: per group, the 4 dims of the first and then of the second
+        const uint4 c = codes[j];
+        w[0] = __byte_perm(c.x, c.z, 0x5410);
+        w[1] = __byte_perm(c.x, c.z, 0x7632);
+        w[2] = __byte_perm(c.y, c.w, 0x5410);
+        w[3] = __byte_perm(c.y, c.w, 0x7632);
+        tt = t ^ ((row & 4) >> 1);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) load_batch(0, j, blk);
-    for (int i = 0; i < 2 * n_tiles; ++i) {
-      const bool is_v = i & 1;
-      if (!is_v) blk_next = block_of((i >> 1) + 1);  // used one item later
-      else if (i + 1 < 2 * n_tiles) blk = checked(blk_next);
-      const int slot = i % kKvSlots;
-      if (i >= kKvSlots && !__all_sync(0xffffffffu, wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1,
-                                                                  s_abort, p.err)))
-        break;
-      const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = row0 + 8 * j;
-        uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
-        uint32_t sz[4] = {par[j].x, par[j].y, par[j].z, par[j].w};
-        int tt = t;
-        if (is_v) {
-          // two 8-byte chunks of V: per group, the 4 dims of the first and then of the second
-          const uint4 c = codes[j];
-          w[0] = __byte_perm(c.x, c.z, 0x5410);
-          w[1] = __byte_perm(c.x, c.z, 0x7632);
-          w[2] = __byte_perm(c.y, c.w, 0x5410);
-          w[3] = __byte_perm(c.y, c.w, 0x7632);
-          tt = t ^ ((row & 4) >> 1);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((sz[k] & 0x7fffu) > 0x7c00u) {  // a NaN scale
-              atomicMin(s_nan + k, (tile0 + (i >> 1)) * kBN + row);
-              sz[k] = 0u;
-            }
-        }
-        if (i + 1 < 2 * n_tiles) load_batch(i + 1, j, blk);
-        // odd rows take the groups in another order, so that the 8 lanes of a
-        // store phase (two rows, four chunks each) hit all banks
-        const uint32_t wa = odd ? w[1] : w[0], wb = odd ? w[0] : w[1], wc = odd ? w[3] : w[2], wd = odd ? w[2] : w[3];
-        const uint32_t pa = odd ? sz[1] : sz[0], pb = odd ? sz[0] : sz[1];
-        const uint32_t pc = odd ? sz[3] : sz[2], pd = odd ? sz[2] : sz[3];
-        const uint32_t at = dst + row * 128;
-        const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
-        auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
-          const uint4 v = dequantise8<E, true>(codes8, param);
-          sts128(at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
-        };
-        put(wa, pa, 0, ca);
-        put(wb, pb, 0, cb);
-        put(wc, pc, 1, ca);
-        put(wd, pd, 1, cb);
+        for (int k = 0; k < 4; ++k)
+          if ((sz[k] & 0x7fffu) > 0x7c00u) {  // a NaN scale
+            const int at = (tile0 + (i >> 1)) * kBN + row;
+            atomicMin(s_nan + k, at);
+            if (kPair) min_cluster(other + kOffMisc + 8 + 4 * k, at);
+            sz[k] = 0u;
+          }
       }
+      reload();
+      // odd rows take the groups in another order, so that the 8 lanes of a
+      // store phase (two rows, four chunks each) hit all banks
+      const uint32_t wa = odd ? w[1] : w[0], wb = odd ? w[0] : w[1], wc = odd ? w[3] : w[2], wd = odd ? w[2] : w[3];
+      const uint32_t pa = odd ? sz[1] : sz[0], pb = odd ? sz[0] : sz[1];
+      const uint32_t pc = odd ? sz[3] : sz[2], pd = odd ? sz[2] : sz[3];
+      const uint32_t at = kOffKV + slot_off + row * 128;
+      const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
+      auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
+        const uint4 v = dequantise8<E, true>(codes8, param);
+        const uint32_t off = at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4);
+        sts128(sbase + off, v.x, v.y, v.z, v.w);
+      };
+      put(wa, pa, 0, ca);
+      put(wb, pb, 0, cb);
+      put(wc, pc, 1, ca);
+      put(wd, pd, 1, cb);
+    };
+    // the item's slot, once the products (a pair's: of both CTAs) that used it before are complete
+    auto wait_slot = [&](int i) -> bool {
+      return i < kKvSlots || all_ok(wait_or_abort<kPair>(bar(kBarKvFree + i % kKvSlots), ((i / kKvSlots) - 1) & 1,
+                                                         s_abort, p.err));
+    };
+    auto written = [&](int i) {
+      const uint32_t full = bar(kBarKvFull + i % kKvSlots);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarKvFull + slot));
+      if (lane == 0) {
+        if (kPair) {
+          // the warp's 8 rows to the other CTA, which sends as many
+          mbar_arrive_expect_tx(full, 2048);
+          const uint32_t rows = sbase + kOffKV + i % kKvSlots * kTileBytes + row0 * 128;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t src = rows + half * kHalfBytes;
+            bulk_s2s(src - sbase + other, src, 1024, full - sbase + other);
+          }
+        } else {
+          mbar_arrive(full);
+        }
+      }
+    };
+    const int n_items = 2 * n_tiles;
+    int blk = n_tiles > 0 ? checked(block_of(0)) : -1, blk_next = -1;
+    if constexpr (kPair) {
+      // one batch of 8 keys a warp: K's in registers 0, V's in registers 1
+      load_row(0, row0, 0, blk);
+      load_row(1, row0, 1, blk);
+      for (int i = 0; i < n_items; i += 2) {
+        blk_next = block_of((i >> 1) + 1);
+        if (!wait_slot(i)) break;
+        if (i + 2 < n_items) blk = checked(blk_next);
+        widen_row(i, row0, 0, i % kKvSlots * kTileBytes, [&] { if (i + 2 < n_items) load_row(i + 2, row0, 0, blk); });
+        written(i);
+        if (!wait_slot(i + 1)) break;
+        widen_row(i + 1, row0, 1, (i + 1) % kKvSlots * kTileBytes,
+                  [&] { if (i + 2 < n_items) load_row(i + 3, row0, 1, blk); });
+        written(i + 1);
+      }
+      // the other CTA's last arrivals on this one's barriers
+      for (int i = max(0, n_items - kKvSlots); i < n_items; ++i)
+        if (!wait_slot(i + kKvSlots)) break;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_row(0, row0 + 8 * j, j, blk);
+      for (int i = 0; i < n_items; ++i) {
+        if (!(i & 1)) blk_next = block_of((i >> 1) + 1);  // used one item later
+        else if (i + 1 < n_items) blk = checked(blk_next);
+        if (!wait_slot(i)) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          widen_row(i, row0 + 8 * j, j, i % kKvSlots * kTileBytes,
+                    [&] { if (i + 1 < n_items) load_row(i + 1, row0 + 8 * j, j, blk); });
+        written(i);
+      }
     }
     __syncwarp();
-    if (kSplit) {
-      cluster_sync();
-      cluster_sync();
-    }
+    if (kSplit || kPair) cluster_sync();  // (a pair: nothing is on its way to this CTA or from it any more)
+    if (kSplit) cluster_sync();
   } else {
     // =========================== softmax groups ===========================
     regs_inc<kRegsSoftmax>();
@@ -663,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return;
     }
+    if (kPair) cluster_sync();  // NaN positions of both CTAs' keys are known
     // Epilogue: every product is complete, so O is staged in the two Q tiles (both
     // heads of a query row side by side, 512 B, 16-byte chunks rotated by the row)
     // and leaves as whole rows.
@@ -740,11 +843,12 @@ bool encode_q(CUtensorMap* tm, const void* base, int64_t rows, int heads, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kPairTiles = 4, kPairKeyTiles = 28;  // query tiles per sequence, and key tiles, from which on CTAs pair up
 constexpr int kMinPartTiles = 2;  // key tiles per CTA at least, where the keys of an item are split
 
-template <Elem E, bool kSplit>
+template <Elem E, Share kShare>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(prefill_q4_kernel<E, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(prefill_q4_kernel<E, kShare>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(kSmemBytes));
 }
 
@@ -781,13 +885,15 @@ cudaError_t device_limits(DeviceLimits* out) {
     return cudaSuccess;
   }
   DeviceLimits d{};
-  if ((e = allow_smem<E, false>()) != cudaSuccess || (e = allow_smem<E, true>()) != cudaSuccess) return e;
+  if ((e = allow_smem<E, Share::kWhole>()) != cudaSuccess || (e = allow_smem<E, Share::kSplitKeys>()) != cudaSuccess ||
+      (e = allow_smem<E, Share::kPaired>()) != cudaSuccess)
+    return e;
   if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   d.clusters[0] = d.sms;
   for (int i = 1; i < 4; ++i) {
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(d.sms) << i, 1 << i, &attr, nullptr);
-    if ((e = cudaOccupancyMaxActiveClusters(&d.clusters[i], prefill_q4_kernel<E, true>, &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&d.clusters[i], prefill_q4_kernel<E, Share::kSplitKeys>, &cfg)) != cudaSuccess) return e;
   }
   d.known = true;
   if (dev >= 0 && dev < 64) all[dev] = d;
@@ -813,12 +919,24 @@ cudaError_t device_limits(DeviceLimits* out) {
 //    3000 after 5000        208.0   203.9    218.2    226.5   whole
 //    5000 after 2000        215.2   207.7    200.8    216.2   4
 //    5000 after 7001        459.9   412.8    386.2    398.5   4
+//
+// Pairs of CTAs widen half as much each, 15 % of the time on long keys: one prompt
+// of 8192 259 -> 224 us, 16 of 1024 on 4096 589 -> 507, 5000 on 7001 382 -> 329.
+// On short ones setting two CTAs up together costs more (8 of 1024 on 1024 124 ->
+// 125, 16 of 1024 109 -> 126), and an odd number of tiles leaves one CTA idle
+// (32 of 300 on 8192 790 -> 862, 16 of 512..1024 on 2048 286 -> 302): so only where
+// sequences have kPairTiles query tiles on average and kPairKeyTiles key tiles.
 template <Elem E>
 cudaError_t launch_typed(const CUtensorMap& tq, Q4PrefillParams& p, int64_t n_items, int32_t prefix_tiles,
                          cudaStream_t stream) {
   DeviceLimits d;
   cudaError_t e = device_limits<E>(&d);
   if (e != cudaSuccess) return e;
+  // pairs: where sequences have query tiles enough that few are left single, and keys enough
+  const int64_t columns = p.items ? 1 : static_cast<int64_t>(p.num_seqs) * (p.hq / 2);
+  const bool paired = !p.items && p.total_q >= int64_t{kPairTiles} * kBM * p.num_seqs &&
+                      prefix_tiles + p.max_q_tiles >= kPairKeyTiles;
+  if (paired) n_items = (p.max_q_tiles + 1) / 2 * 2 * columns;
   const int64_t rest = n_items % d.sms, rounds = n_items / d.sms;
   int shift = 0;
   if (rest > 0) {
@@ -830,16 +948,22 @@ cudaError_t launch_typed(const CUtensorMap& tq, Q4PrefillParams& p, int64_t n_it
       if (rest <= d.clusters[i] && tiles >> i >= kMinPartTiles && tiles - uneven - split >= 2) shift = i;
     }
   }
-  const unsigned whole = static_cast<unsigned>(shift > 0 ? n_items - rest : n_items);
-  if (whole > 0) {
-    prefill_q4_kernel<E, false><<<whole, kThreads, kSmemBytes, stream>>>(tq, p);
+  const int64_t whole = shift > 0 ? n_items - rest : n_items;
+  cudaLaunchAttribute attr;
+  p.first = 0;
+  p.by_twos = paired;
+  if (whole > 0 && paired) {
+    const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(whole), 2, &attr, stream);
+    e = cudaLaunchKernelEx(&cfg, prefill_q4_kernel<E, Share::kPaired>, tq, const_cast<const Q4PrefillParams&>(p));
+    if (e != cudaSuccess) return e;
+  } else if (whole > 0) {
+    prefill_q4_kernel<E, Share::kWhole><<<static_cast<unsigned>(whole), kThreads, kSmemBytes, stream>>>(tq, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (shift > 0) {
     p.first = static_cast<int32_t>(whole);
-    cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(rest) << shift, 1 << shift, &attr, stream);
-    return cudaLaunchKernelEx(&cfg, prefill_q4_kernel<E, true>, tq, const_cast<const Q4PrefillParams&>(p));
+    return cudaLaunchKernelEx(&cfg, prefill_q4_kernel<E, Share::kSplitKeys>, tq, const_cast<const Q4PrefillParams&>(p));
   }
   return cudaSuccess;
 }

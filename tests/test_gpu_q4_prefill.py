@@ -106,6 +106,43 @@ def test_keys_split_over_ctas(pkv, lq, lk, dtype):
     c.check(c.prefill(plan=pkv.pkv_prefill_plan(c.cq, c.ck)))
 
 
+# 4 query tiles to a sequence on average and 28 key tiles: two CTAs widen each key tile for both.
+@pytest.mark.parametrize("lq,lk,hq,hkv,dtype", [
+    ([1100], [4000], 32, 8, BF16),                  # an odd number of tiles, the last of them not full
+    ([2400, 200], [4600, 900], 32, 8, F16),         # pairs whose later tile, or both, have no row
+    ([2100, 150], [2100, 4000], 32, 8, BF16),
+    ([1152, 1025, 1030], [1300, 1025, 5000], 24, 12, F16)])
+def test_pairs_of_query_tiles(pkv, lq, lk, hq, hkv, dtype):
+    c = Prefill(pkv, lq, lk, hq, hkv, dtype, seed=50 + hq).fill()
+    out = c.prefill()
+    c.check(out)
+    assert torch.equal(c.prefill(), out)
+    planned = c.prefill(plan=pkv.pkv_prefill_plan(c.cq, c.ck))                  # (a plan's tiles are not paired)
+    c.check(planned)
+    if lq == [2100, 150]:                                                       # (elsewhere some tiles' keys are split)
+        assert torch.equal(planned, out)
+
+
+def test_pairs_nan_values_and_bad_blocks(pkv):
+    c = Prefill(pkv, [2400, 300], [4500, 300], 32, 8, BF16, seed=56).fill()
+    want = c.prefill()
+    c.v[2100 + 2000, 1, 40] = float("nan")          # keys of either half of a tile: sequence 0, kv heads 1 and 2
+    c.v[2100 + 2080, 2, 70] = float("nan")
+    c.v[c.first[1] + 10, 0, 3] = float("inf")       # sequence 1, kv head 0
+    out = c.fill().prefill()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[2000:2400, 4:8, 32:64] = True
+    hit[2080:2400, 8:12, 64:96] = True
+    hit[2410:2700, 0:4, 0:32] = True
+    assert bool(out[hit].isnan().all())
+    assert torch.equal(out[~hit], want[~hit])
+    assert pkv.pkv_device_error() == 0
+    c.tables[1, 0] = 10 ** 6
+    out = c.prefill()
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_BLOCK
+    assert torch.equal(out[:2400][~hit[:2400]], want[:2400][~hit[:2400]])
+
+
 def test_split_heads_growing_logits_and_graph(pkv):
     """Other head layouts; maxima that differ from part to part; captured and replayed."""
     for hq, hkv in ((8, 1), (4, 2), (32, 8)):
