@@ -37,8 +37,13 @@
 // kept instead, and rows at or past it get NaN in the epilogue.
 //
 // Registers: 640 threads x 96 at launch, split over the warpgroups by what each
-// needs without spilling (shared memory leaves no L1 for local memory: the first
-// form, which spilled, took 904 us where this takes 491).
+// needs without spilling in its loop (shared memory leaves no L1 for local memory:
+// the first form, which spilled there, took 904 us where this takes 479).
+//
+// A tile's start is a chain of loads: lengths, block, codes, first widening, first
+// product, about 3 us in all beside 0.6 us between two CTAs and 1.8 us of epilogue.
+// So the first block is read with the lengths, and the first codes go out before
+// the CTA is set up (486 -> 479 and 328 -> 319 us on the two cases below).
 //
 // The issuing warp runs its loop as a whole and elects a thread for each product:
 // operand addresses then stay in uniform registers, and with TMEM addresses as
@@ -52,8 +57,8 @@
 // 2.0-2.4 us, in pairs 1.7: about 4.5 k warp instructions of widening (a pair's
 // CTA: half) and 6 k of softmax, against 2048 cycles (1.1 us) of tensor core at its
 // peak. 128 prompts of 64..512 tokens on a shared prefix of 1024 (16 query heads on
-// 8): 480 us, 0.74 PFLOP/s, the tensor pipe active 42 % of the time, instructions
-// issued in 56 % of the cycles; 5000 tokens after 7001, in pairs: 329 us, 1.17.
+// 8): 479 us, 0.74 PFLOP/s, the tensor pipe active 42 % of the time, instructions
+// issued in 56 % of the cycles; 5000 tokens after 7001, in pairs: 319 us, 1.21.
 // Measured and not kept, on these two, each beside what the kernel then took: two
 // issuing warps, one for each head (528 and 427 beside 480 and 376: the products of
 // both mix); no maximum of a tile's logits unless their sum is out of range (506
@@ -85,7 +90,7 @@ constexpr int kWidenWarps = 8;
 constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
 
 // Registers per thread: 128 * (sum over the four warpgroups) is what the launch holds.
-constexpr int kRegsFirst = 80, kRegsSoftmax = 144, kRegsWiden = 56;
+constexpr int kRegsFirst = 64, kRegsSoftmax = 144, kRegsWiden = 64;
 static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
 
 constexpr int kOffQ = 0;                                 // 2 tiles (and O staging in the epilogue)
@@ -313,8 +318,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
     return;
   }
-  const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1];
-  const int Lq = cq1 - cq0, Lk = p.cu_k[b + 1] - p.cu_k[b];
+  const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1], ck0 = p.cu_k[b], ck1 = p.cu_k[b + 1];
+  const int first_block = kSplit ? -1 : p.block_tables[static_cast<int64_t>(b) * p.bt_stride];
+  if (threadIdx.x == 0) {  // (while the lengths are on their way)
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i >= kBarKvFull && i < kBarKvFull + kKvSlots) count = kWidenWarps;
+      if (kPair && i >= kBarKvFree && i < kBarKvFree + kKvSlots) count = 2;
+      if (i == kBarPReady || i == kBarPReady + 1) count = 4;
+      if (i == kBarStaged) count = 8;
+      mbar_init(bar(i), count);
+    }
+    *s_abort = 0;
+    for (int i = 0; i < 4; ++i) s_nan[i] = INT_MAX;
+    mbar_fence_init();
+    prefetch_tmap(&tm_q);
+  }
+  const int Lq = cq1 - cq0, Lk = ck1 - ck0;
   if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || Lk > INT_MAX - 2 * kBN || cq0 < 0 || cq1 > p.total_q ||
       Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
     if (threadIdx.x == 0 && qt <= 0 && pair == 0 && part == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
@@ -331,19 +351,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile0 = n_all * part / parts;                    // this CTA's key tiles: from tile0 on
   const int n_tiles = n_all * (part + 1) / parts - tile0;    // (0 only where the keys are split)
 
+  // ---- widening: what a warp loads; the first loads go out before the CTA is set up ----
+  const int kv_head = 2 * pair / (p.hq / p.hkv);
+  // key of batch 0 within the tile; batch i: + 8 i
+  const int row0 = (kPair ? rank * 64 + (warp - kWidenWarp0) * 8 : (warp - kWidenWarp0) * 16) + (lane >> 2);
+  const int t = lane & 3;
+  const bool odd = (lane >> 2) & 1;
+  auto block_of = [&](int n) -> int {
+    return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + (tile0 + n) * kBN / kBlockSize] : -1;
+  };
+  auto checked = [&](int blk) -> int {
+    if (blk >= 0 && blk < p.num_blocks) return blk;
+    flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
+    return -1;
+  };
+  uint4 codes[2], par[2];
+  // key `row` of K_{i/2} (even i) or V_{i/2} (odd i), the ring's items, into registers j
+  auto load_row = [&](int i, int row, int j, int blk) {
+    codes[j] = par[j] = make_uint4(0, 0, 0, 0);
+    const int key0 = (tile0 + (i >> 1)) * kBN;
+    if (blk < 0 || key0 + row >= Lk) return;  // zeros: a scale and a minimum of 0
+    const uint8_t* base = ((i & 1) ? p.v_cache : p.k_cache) +
+                          (static_cast<int64_t>(blk) * p.hkv + kv_head) * kQ4RecordBytes +
+                          (key0 % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
+    const int tok = row % kQ4Tile;
+    codes[j] = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + t * 16));
+    par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
+  };
+  int blk = -1, blk_next = -1;
+  if (warp >= kWidenWarp0 && n_tiles > 0) {
+    blk = checked(kSplit ? block_of(0) : first_block);
+    // a pair's warp has one batch of 8 keys, K's in registers 0, V's in registers 1
+    load_row(0, row0, 0, blk);
+    load_row(kPair ? 1 : 0, kPair ? row0 : row0 + 8, 1, blk);
+  }
+
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      int count = 1;
-      if (i >= kBarKvFull && i < kBarKvFull + kKvSlots) count = kWidenWarps;
-      if (kPair && i >= kBarKvFree && i < kBarKvFree + kKvSlots) count = 2;
-      if (i == kBarPReady || i == kBarPReady + 1) count = 4;
-      if (i == kBarStaged) count = 8;
-      mbar_init(bar(i), count);
-    }
-    *s_abort = 0;
-    for (int i = 0; i < 4; ++i) s_nan[i] = INT_MAX;
-    mbar_fence_init();
-    prefetch_tmap(&tm_q);
     mbar_arrive_expect_tx(bar(kBarQ), 2 * kTileBytes);
     for (int g = 0; g < 2; ++g) {
       const uint32_t dst = sbase + kOffQ + g * kTileBytes;
@@ -453,33 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kWidenWarp0) {
     // =========================== K/V widening ===========================
     regs_dec<kRegsWiden>();
-    const int kv_head = 2 * pair / (p.hq / p.hkv);
-    // key of batch 0 within the tile; batch i: + 8 i
-    const int row0 = (kPair ? rank * 64 + (warp - kWidenWarp0) * 8 : (warp - kWidenWarp0) * 16) + (lane >> 2);
-    const int t = lane & 3;
-    const bool odd = (lane >> 2) & 1;
     const uint32_t other = kPair ? in_part(sbase, rank ^ 1) : 0u;  // the pair's other CTA
-    auto block_of = [&](int n) -> int {
-      return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + (tile0 + n) * kBN / kBlockSize] : -1;
-    };
-    auto checked = [&](int blk) -> int {
-      if (blk >= 0 && blk < p.num_blocks) return blk;
-      flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
-      return -1;
-    };
-    uint4 codes[2], par[2];
-    // key `row` of K_{i/2} (even i) or V_{i/2} (odd i), the ring's items, into registers j
-    auto load_row = [&](int i, int row, int j, int blk) {
-      codes[j] = par[j] = make_uint4(0, 0, 0, 0);
-      const int key0 = (tile0 + (i >> 1)) * kBN;
-      if (blk < 0 || key0 + row >= Lk) return;  // zeros: a scale and a minimum of 0
-      const uint8_t* base = ((i & 1) ? p.v_cache : p.k_cache) +
-                            (static_cast<int64_t>(blk) * p.hkv + kv_head) * kQ4RecordBytes +
-                            (key0 % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
-      const int tok = row % kQ4Tile;
-      codes[j] = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + t * 16));
-      par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
-    };
     // registers j -> key `row` of the item's tile; `reload` fills them again meanwhile
     auto widen_row = [&](int i, int row, int j, uint32_t slot_off, auto reload) {
       uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
@@ -545,11 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     const int n_items = 2 * n_tiles;
-    int blk = n_tiles > 0 ? checked(block_of(0)) : -1, blk_next = -1;
     if constexpr (kPair) {
-      // one batch of 8 keys a warp: K's in registers 0, V's in registers 1
-      load_row(0, row0, 0, blk);
-      load_row(1, row0, 1, blk);
       for (int i = 0; i < n_items; i += 2) {
         blk_next = block_of((i >> 1) + 1);
         if (!wait_slot(i)) break;
@@ -565,8 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, n_items - kKvSlots); i < n_items; ++i)
         if (!wait_slot(i + kKvSlots)) break;
     } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_row(0, row0 + 8 * j, j, blk);
       for (int i = 0; i < n_items; ++i) {
         if (!(i & 1)) blk_next = block_of((i >> 1) + 1);  // used one item later
         else if (i + 1 < n_items) blk = checked(blk_next);
