@@ -37,13 +37,15 @@
 // kept instead, and rows at or past it get NaN in the epilogue.
 //
 // Registers: 640 threads x 96 at launch, split over the warpgroups by what each
-// needs without spilling in its loop (shared memory leaves no L1 for local memory:
-// the first form, which spilled there, took 904 us where this takes 479).
+// needs without spilling (shared memory leaves no L1 for local memory: the first
+// form, which spilled, took 904 us where this takes 481).
 //
 // A tile's start is a chain of loads: lengths, block, codes, first widening, first
 // product, about 3 us in all beside 0.6 us between two CTAs and 1.8 us of epilogue.
-// So the first block is read with the lengths, and the first codes go out before
-// the CTA is set up (486 -> 479 and 328 -> 319 us on the two cases below).
+// So the first block is read with the lengths (486 -> 481 us on the first case
+// below), and a pair's first codes go out before it is set up, which waits for
+// both CTAs (328 -> 320 on the second; in the other forms the loop became slower
+// by more than that).
 //
 // The issuing warp runs its loop as a whole and elects a thread for each product:
 // operand addresses then stay in uniform registers, and with TMEM addresses as
@@ -57,8 +59,8 @@
 // 2.0-2.4 us, in pairs 1.7: about 4.5 k warp instructions of widening (a pair's
 // CTA: half) and 6 k of softmax, against 2048 cycles (1.1 us) of tensor core at its
 // peak. 128 prompts of 64..512 tokens on a shared prefix of 1024 (16 query heads on
-// 8): 479 us, 0.74 PFLOP/s, the tensor pipe active 42 % of the time, instructions
-// issued in 56 % of the cycles; 5000 tokens after 7001, in pairs: 319 us, 1.21.
+// 8): 481 us, 0.74 PFLOP/s, the tensor pipe active 42 % of the time, instructions
+// issued in 56 % of the cycles; 5000 tokens after 7001, in pairs: 320 us, 1.20.
 // Measured and not kept, on these two, each beside what the kernel then took: two
 // issuing warps, one for each head (528 and 427 beside 480 and 376: the products of
 // both mix); no maximum of a tile's logits unless their sum is out of range (506
@@ -88,10 +90,6 @@ constexpr int kKvSlots = 5;
 constexpr int kThreads = 640;
 constexpr int kWidenWarps = 8;
 constexpr int kWidenWarp0 = 12, kSoftmaxWarp0 = 4;
-
-// Registers per thread: 128 * (sum over the four warpgroups) is what the launch holds.
-constexpr int kRegsFirst = 64, kRegsSoftmax = 144, kRegsWiden = 64;
-static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
 
 constexpr int kOffQ = 0;                                 // 2 tiles (and O staging in the epilogue)
 constexpr int kOffKV = 2 * kTileBytes;                   // kKvSlots tiles
@@ -281,6 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_kernel(const __grid_constant__ CUtensorMap tm_q, const Q4PrefillParams p) {
   using Ops = ElemOps<E>;
   constexpr bool kSplit = kShare == Share::kSplitKeys, kPair = kShare == Share::kPaired;
+  // Registers per thread: 128 * (sum over the five warpgroups) is what the launch holds.
+  constexpr int kRegsFirst = kShare == Share::kWhole ? 48 : 80, kRegsSoftmax = kShare == Share::kWhole ? 152 : 144,
+                kRegsWiden = kShare == Share::kWhole ? 64 : 56;
+  static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the 128-byte-swizzle atoms.
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile0 = n_all * part / parts;                    // this CTA's key tiles: from tile0 on
   const int n_tiles = n_all * (part + 1) / parts - tile0;    // (0 only where the keys are split)
 
-  // ---- widening: what a warp loads; the first loads go out before the CTA is set up ----
+  // ---- widening: what a warp loads ----
   const int kv_head = 2 * pair / (p.hq / p.hkv);
   // key of batch 0 within the tile; batch i: + 8 i
   const int row0 = (kPair ? rank * 64 + (warp - kWidenWarp0) * 8 : (warp - kWidenWarp0) * 16) + (lane >> 2);
@@ -379,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
   };
   int blk = -1, blk_next = -1;
-  if (warp >= kWidenWarp0 && n_tiles > 0) {
-    blk = checked(kSplit ? block_of(0) : first_block);
-    // a pair's warp has one batch of 8 keys, K's in registers 0, V's in registers 1
+  if (kPair && warp >= kWidenWarp0) {
+    // a warp has one batch of 8 keys, K's in registers 0, V's in registers 1
+    blk = checked(first_block);
     load_row(0, row0, 0, blk);
-    load_row(kPair ? 1 : 0, kPair ? row0 : row0 + 8, 1, blk);
+    load_row(1, row0, 1, blk);
   }
 
   if (threadIdx.x == 0) {
@@ -578,6 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, n_items - kKvSlots); i < n_items; ++i)
         if (!wait_slot(i + kKvSlots)) break;
     } else {
+      blk = n_tiles > 0 ? checked(kSplit ? block_of(0) : first_block) : -1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_row(0, row0 + 8 * j, j, blk);
       for (int i = 0; i < n_items; ++i) {
         if (!(i & 1)) blk_next = block_of((i >> 1) + 1);  // used one item later
         else if (i + 1 < n_items) blk = checked(blk_next);
