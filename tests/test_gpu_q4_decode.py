@@ -348,6 +348,24 @@ def test_another_stream(pkv):
     c.check(out)
 
 
+def test_calls_at_once(pkv):
+    """Two streams, a workspace each."""
+    cases = [Case(pkv, [700, 40, 3000], 16, 8, BF16, seed=18).fill(), Case(pkv, [9000, 1], 32, 8, F16, seed=19).fill()]
+    spaces = [c.workspace() for c in cases]
+    want = [c.decode(w) for c, w in zip(cases, spaces)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for c, s, w in zip(cases, streams, spaces):
+            with torch.cuda.stream(s):
+                got.append(c.decode(w))
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    for c, w in zip(cases, want):
+        c.check(w)
+
+
 def test_cache_past_32_bit_offsets(pkv):
     """Block ids whose byte offsets pass 2^32, for K and V."""
     spare = 2 ** 32 // (8 * 20480) + 2

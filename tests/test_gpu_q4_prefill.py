@@ -181,6 +181,34 @@ def test_split_nan_values_and_bad_blocks(pkv):
     assert torch.equal(out[:200][~hit[:200]], want[:200][~hit[:200]])
 
 
+def test_calls_at_once_and_captured(pkv):
+    """Calls of all three kinds on several streams at once, and one captured graph of them."""
+    cases = [Prefill(pkv, lq, lk, 16, 8, BF16, seed=60 + i).fill()
+             for i, (lq, lk) in enumerate((([1400], [4000]), ([300], [5000]), ([200, 900, 77], [200, 950, 77])))]
+    want = [c.prefill() for c in cases]
+    for c, w in zip(cases, want):
+        c.check(w)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(c.prefill())
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    outs = [torch.empty_like(w) for w in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, o in zip(cases, outs):
+            c.prefill(out=o)
+    for o in outs:
+        o.fill_(5.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want)) and pkv.pkv_device_error() == 0
+
+
 def test_growing_logits(pkv):
     """The running maximum moves in every key tile."""
     c = Prefill(pkv, [400], [1500], 16, 8, BF16, seed=28)
