@@ -420,14 +420,16 @@ int pkv_store_decode_q4_f16(const void* q, int64_t q_row_stride, const void* k, 
 /*
  * pkv_prefill_varlen_q4 -- pkv_prefill_varlen in prefix-cache mode with every
  * key and value (cached prefix and new tokens, which the caller stores first
- * on the same stream) taken from the 4-bit cache. The values are rounded to the
- * element type as pkv_load_kvcache_q4 rounds them, and the arithmetic is
- * pkv_prefill_varlen's: the result is that of loading the rows and attending to
+ * on the same stream) taken from the 4-bit cache. Keys are rounded to the
+ * element type as pkv_load_kvcache_q4 rounds them, values and p to fp16 (more
+ * exact than bf16, whichever the element type is); sums and maxima are fp32. The
+ * result is, up to those roundings, that of loading the rows and attending to
  * them contiguously, without the load. A call of few query tiles splits their
  * keys over up to 8 CTAs, whose fp32 partial results are added in key order; how
  * follows from the call's sizes alone (the bounds of the lengths and the block
- * table's width among them), so equal calls give equal bits. A group of V that reads back as NaN
- * gives NaN in its 32 dims to the rows that may attend to it, and to no others.
+ * table's width among them), so equal calls give equal bits. A group of V that
+ * reads back as NaN gives NaN in its 32 dims to the rows that may attend to it,
+ * and to no others.
  * Arguments, errors and the optional tile plan in `workspace` are as for
  * pkv_prefill_varlen. Rows of q and out that belong to no sequence are left
  * as they were.

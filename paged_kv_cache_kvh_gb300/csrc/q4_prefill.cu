@@ -2,13 +2,15 @@
 // values all sit in the 4-bit paged cache.
 //
 // The operation is that of prefill.cu: query row i of sequence b sits at
-// position Lk_b - Lq_b + i and attends to keys 0..that position. A key or value
-// element is s * c + z (q4.cuh) rounded to the element type, exactly what
-// pkv_load_kvcache_q4 returns, and the products, softmax and roundings are
-// those of prefill.cu in the same order: but for tiles whose keys are split (see
-// launch_typed), the output has the bits of loading the rows and attending to them
-// contiguously. What it saves is that round trip: 512 bytes written and read again
-// per (token, kv head), for every sequence that shares a prefix.
+// position Lk_b - Lq_b + i and attends to keys 0..that position. A key's element is
+// s * c + z (q4.cuh) rounded to the rows' type, as pkv_load_kvcache_q4 returns it,
+// since Q K^T takes operands of one type. V and P are free of that, and fp16 holds
+// both (|V| <= 65504, P < 2^14) with 3 bits more than bf16: the second product is
+// fp16 for either type of rows (bf16 error against 64 bits 0.0030 -> 0.0022, the
+// result's own rounding being 0.0017; no difference in time). Maxima, sums and
+// accumulators are fp32. What the call saves is reading the rows back first: 512
+// bytes written and read again per (token, kv head), for every sequence that
+// shares a prefix.
 //
 // One CTA computes a 128-row query tile of one sequence for two query heads of
 // one kv head, so a K or V tile is widened once for two products; where sequences
@@ -28,10 +30,10 @@
 // codes a lane, which are 8 dims of each of the 4 groups. A batch's registers are
 // loaded again for the next tile as soon as it is widened, so a tile's loads are
 // in flight while the other batch is converted and the ring slot is waited for.
-// A bf16 pair costs two ANDs, one packed multiply-add and one conversion (the
-// nibbles are used in place, as fp32 subnormals; see dequantise8), which is why
-// bf16 tiles hold 2^-64 of the values; the powers of two are taken out of the
-// logits and of the output. Rows past the sequence are written as zeros. So is a
+// A pair of bf16 keys costs two ANDs, one packed multiply-add and one conversion
+// (the nibbles are used in place, as fp32 subnormals; see dequantise8), which is why
+// a bf16 K tile holds 2^-64 of the values; the powers of two are taken out of the
+// logits. Rows past the sequence are written as zeros. So is a
 // group of V that reads back as NaN: in a product it would reach every query row
 // of the tile, masked or not (0 * NaN). The first such position of each group is
 // kept instead, and rows at or past it get NaN in the epilogue.
@@ -75,6 +77,7 @@
 
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "q4.cuh"
 
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
       // =========================== MMA issuer ===========================
       constexpr uint32_t idesc_s = idesc_f16kind_f32(kBM, kBN, false, false, Ops::kMmaFormat);
-      constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kHeadDim, false, true, Ops::kMmaFormat);
+      constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kHeadDim, false, true, ElemOps<Elem::kF16>::kMmaFormat);
       const uint32_t q_lo = desc_lo(sbase + kOffQ, 16);
       const uint32_t k_lo = desc_lo(sbase + kOffKV, 16), v_lo = desc_lo(sbase + kOffKV, kHalfBytes);
       bool ok = all_ok(wait_or_abort(bar(kBarQ), 0, s_abort, p.err));
@@ -500,11 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegsWiden>();
     const uint32_t other = kPair ? in_part(sbase, rank ^ 1) : 0u;  // the pair's other CTA
     // registers j -> key `row` of the item's tile; `reload` fills them again meanwhile
-    auto widen_row = [&](int i, int row, int j, uint32_t slot_off, auto reload) {
+    auto widen_row = [&](auto of_v, int i, int row, int j, uint32_t slot_off, auto reload) {
+      constexpr bool kV = decltype(of_v)::value;
       uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
       uint32_t sz[4] = {par[j].x, par[j].y, par[j].z, par[j].w};
       int tt = t;
-      if (i & 1) {
+      if constexpr (kV) {
         // two 8-byte chunks of V: per group, the 4 dims of the first and then of the second
         const uint4 c = codes[j];
         w[0] = __byte_perm(c.x, c.z, 0x5410);
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t at = kOffKV + slot_off + row * 128;
       const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
       auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
-        const uint4 v = dequantise8<E, true>(codes8, param);
+        const uint4 v = kV ? dequantise8<Elem::kF16>(codes8, param) : dequantise8<E, true>(codes8, param);
         const uint32_t off = at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4);
         sts128(sbase + off, v.x, v.y, v.z, v.w);
       };
@@ -569,10 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         blk_next = block_of((i >> 1) + 1);
         if (!wait_slot(i)) break;
         if (i + 2 < n_items) blk = checked(blk_next);
-        widen_row(i, row0, 0, i % kKvSlots * kTileBytes, [&] { if (i + 2 < n_items) load_row(i + 2, row0, 0, blk); });
+        widen_row(std::false_type{}, i, row0, 0, i % kKvSlots * kTileBytes,
+                  [&] { if (i + 2 < n_items) load_row(i + 2, row0, 0, blk); });
         written(i);
         if (!wait_slot(i + 1)) break;
-        widen_row(i + 1, row0, 1, (i + 1) % kKvSlots * kTileBytes,
+        widen_row(std::true_type{}, i + 1, row0, 1, (i + 1) % kKvSlots * kTileBytes,
                   [&] { if (i + 2 < n_items) load_row(i + 3, row0, 1, blk); });
         written(i + 1);
       }
@@ -583,15 +588,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       blk = n_tiles > 0 ? checked(kSplit ? block_of(0) : first_block) : -1;
 #pragma unroll
       for (int j = 0; j < 2; ++j) load_row(0, row0 + 8 * j, j, blk);
-      for (int i = 0; i < n_items; ++i) {
-        if (!(i & 1)) blk_next = block_of((i >> 1) + 1);  // used one item later
-        else if (i + 1 < n_items) blk = checked(blk_next);
+      for (int i = 0; i < n_items; i += 2) {
+        blk_next = block_of((i >> 1) + 1);
         if (!wait_slot(i)) break;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          widen_row(i, row0 + 8 * j, j, i % kKvSlots * kTileBytes,
-                    [&] { if (i + 1 < n_items) load_row(i + 1, row0 + 8 * j, j, blk); });
+          widen_row(std::false_type{}, i, row0 + 8 * j, j, i % kKvSlots * kTileBytes,
+                    [&] { load_row(i + 1, row0 + 8 * j, j, blk); });
         written(i);
+        if (i + 2 < n_items) blk = checked(blk_next);
+        if (!wait_slot(i + 1)) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          widen_row(std::true_type{}, i + 1, row0 + 8 * j, j, (i + 1) % kKvSlots * kTileBytes,
+                    [&] { if (i + 2 < n_items) load_row(i + 2, row0 + 8 * j, j, blk); });
+        written(i + 1);
       }
     }
     __syncwarp();
@@ -607,10 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_base + g * 128;
     const uint32_t tO = tmem + lane_base + 256 + g * 128;
-    // bf16 K and V are held as 2^-64 of their values (dequantise8)
-    const float out_scale = E == Elem::kBF16 ? 18446744073709551616.f : 1.f;
-    const float sl2 = p.scale_log2 * out_scale;
-    float m = -INFINITY;  // running max, log2 units (scaled)
+    // a bf16 K is held as 2^-64 of its values (dequantise8)
+    const float sl2 = p.scale_log2 * (E == Elem::kBF16 ? 18446744073709551616.f : 1.f);
+    constexpr float kLift = 6.f;
+    float m = -INFINITY;  // running max less kLift, log2 units (scaled)
     float l = 0.f;
     bool ok = true;
     for (int n = 0; n < n_tiles; ++n) {
@@ -656,7 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = fmaxf(fmax3(ma, s[126], s[127]), mb);
       mx *= sl2;
       float m_use = m;
-      if (mx > m + 8.0f) m_use = mx;  // move the max only when it grows by > 2^8
+      // Move the maximum only when it grows by more than 2^8. m is kLift below it: P stays
+      // under 2^14, and is a normal fp16 number down to 2^-20 of the largest.
+      if (mx > m + (8.0f + kLift)) m_use = mx - kLift;
       const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_use);
       l *= alpha;
       const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
@@ -675,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           a0 = ex2_approx(a0);
           a1 = ex2_approx(a1);
           sums[i & 3] = f32x2_add(sums[i & 3], f32x2_pack(a0, a1));
-          pk[i] = Ops::pack(a0, a1);
+          pk[i] = ElemOps<Elem::kF16>::pack(a0, a1);
         }
         tmem_st8(tS + c * 8, pk);
       }
@@ -729,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 v = ld_cluster_f2(in_part(ml + ri * 8, i));
         L = fmaf(ex2_approx(v.x - M), v.y, L);
       }
-      const float inv = ex2_approx(m - M) * ((L > 0.f ? 1.f / L : L == L ? 0.f : L) * out_scale);
+      const float inv = ex2_approx(m - M) * ((L > 0.f ? 1.f / L : L == L ? 0.f : L));
       const uint32_t dst = in_part(stage + (part * rows_own + ri % rows_own) * 512, ri / rows_own);
       tc_fence_after();
 #pragma unroll
@@ -787,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // and leaves as whole rows.
     if (ok) {
       tc_fence_after();
-      const float inv = (l > 0.f ? 1.f / l : l == l ? 0.f : l) * out_scale;
+      const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // group c of 32 dims
         uint32_t r[32];
