@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Ops = ElemOps<E>;
   constexpr bool kSplit = kShare == Share::kSplitKeys, kPair = kShare == Share::kPaired;
   // Registers per thread: 128 * (sum over the five warpgroups) is what the launch holds.
-  constexpr int kRegsFirst = kShare == Share::kWhole ? 48 : 80, kRegsSoftmax = kShare == Share::kWhole ? 152 : 144,
-                kRegsWiden = kShare == Share::kWhole ? 64 : 56;
+  constexpr int kRegsFirst = kShare == Share::kWhole ? 64 : 80, kRegsSoftmax = 144;
+  constexpr int kRegsWiden = kShare == Share::kWhole ? 64 : 56;
   static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the 128-byte-swizzle atoms.
