@@ -57,7 +57,9 @@
 // Measured and not kept: 16 warps of 32-token steps (165 us: more control per
 // token), 8 warps (163), one K buffer and 16 warps (141), accumulators rescaled
 // without a branch (154), other orders of the products (150 as they stood then),
-// shifts as multiplications (166).
+// shifts as multiplications (166), bf16 queries as two e4m3 parts against codes that
+// are e4m3 numbers as they stand (183: fewer instructions, but spills and longer
+// chains).
 #include <type_traits>
 
 #include "q4.cuh"
