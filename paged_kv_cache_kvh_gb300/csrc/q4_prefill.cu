@@ -61,8 +61,8 @@
 // 2.0-2.4 us, in pairs 1.7: about 4.5 k warp instructions of widening (a pair's
 // CTA: half) and 6 k of softmax, against 2048 cycles (1.1 us) of tensor core at its
 // peak. 128 prompts of 64..512 tokens on a shared prefix of 1024 (16 query heads on
-// 8): 481 us, 0.74 PFLOP/s, the tensor pipe active 42 % of the time, instructions
-// issued in 56 % of the cycles; 5000 tokens after 7001, in pairs: 320 us, 1.20.
+// 8): 481 us a CTA to a tile (the tensor pipe active 42 % of the time, instructions
+// issued in 56 % of the cycles), 430 us, 0.82 PFLOP/s, with units; 5000 tokens after 7001, in pairs: 320 us, 1.20.
 // Measured and not kept, on these two, each beside what the kernel then took: two
 // issuing warps, one for each head (528 and 427 beside 480 and 376: the products of
 // both mix); no maximum of a tile's logits unless their sum is out of range (506
@@ -269,6 +269,183 @@ __device__ __forceinline__ void bulk_s2s(uint32_t dst, uint32_t src, uint32_t by
 __device__ __forceinline__ void min_cluster(uint32_t addr, int x) {
   asm volatile("{\n\t.reg .s32 old;\n\tatom.shared::cluster.min.s32 old, [%0], %1;\n\t}" ::"r"(addr), "r"(x) : "memory");
 }
+// A bf16 K is held as 2^-64 of its values (dequantise8).
+template <Elem E>
+constexpr float kKeyScale = E == Elem::kBF16 ? 18446744073709551616.f : 1.f;
+constexpr float kLift = 6.f;
+
+// One key tile of one query row (a thread's): logits from TMEM, P over them, the
+// running maximum m (less kLift, log2 units) and sum l. Where `masked`, keys
+// j <= lim are visible. kMayMiss: the first tiles may hold none.
+template <bool kMayMiss>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, bool masked, int lim, float sl2,
+                                             float& m, float& l, uint32_t p_ready, int lane) {
+  float s[128];
+  {
+    uint32_t r0_[32], r1[32], r2[32], r3[32];
+    tmem_ld32(tS + 0, r0_);
+    tmem_ld32(tS + 32, r1);
+    tmem_ld32(tS + 64, r2);
+    tmem_ld32(tS + 96, r3);
+    tmem_wait_ld();
+    tmem_reg_fence(r0_);
+    tmem_reg_fence(r1);
+    tmem_reg_fence(r2);
+    tmem_reg_fence(r3);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      s[j] = __uint_as_float(r0_[j]);
+      s[32 + j] = __uint_as_float(r1[j]);
+      s[64 + j] = __uint_as_float(r2[j]);
+      s[96 + j] = __uint_as_float(r3[j]);
+    }
+  }
+  if (masked) {
+#pragma unroll
+    for (int j = 0; j < 128; ++j)
+      if (j > lim) s[j] = -INFINITY;
+  }
+  float ma = s[0], mb = s[1];
+#pragma unroll
+  for (int j = 2; j < 126; j += 4) {
+    ma = fmax3(ma, s[j], s[j + 1]);
+    mb = fmax3(mb, s[j + 2], s[j + 3]);
+  }
+  float mx = fmaxf(fmax3(ma, s[126], s[127]), mb);
+  mx *= sl2;
+  float m_use = m;
+  // Move the maximum only when it grows by more than 2^8. m is kLift below it: P stays
+  // under 2^14, and is a normal fp16 number down to 2^-20 of the largest.
+  if (mx > m + (8.0f + kLift)) m_use = mx - kLift;
+  const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_use);
+  l *= alpha;
+  const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
+  const float neg_m = kMayMiss && m_use == -INFINITY ? 0.f : -m_use;  // a part may begin with keys that a row can't see
+  const uint64_t negm2 = f32x2_pack(neg_m, neg_m);
+  // P = 2^(s*sl2 - m_use), rounded to the element type, over the logits in TMEM
+  uint64_t sums[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = c * 16 + 2 * i;
+      float a0, a1;
+      f32x2_unpack(f32x2_fma(f32x2_pack(s[j], s[j + 1]), sl2x2, negm2), a0, a1);
+      a0 = ex2_approx(a0);
+      a1 = ex2_approx(a1);
+      sums[i & 3] = f32x2_add(sums[i & 3], f32x2_pack(a0, a1));
+      pk[i] = ElemOps<Elem::kF16>::pack(a0, a1);
+    }
+    tmem_st8(tS + c * 8, pk);
+  }
+  m = m_use;
+  // rescale the running output (PV_g(n-1) is complete: S_g(n) was issued after it)
+  if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+    for (int c = 0; c < 16; ++c) {
+      uint32_t r[8];
+      tmem_ld8(tO + c * 8, r);
+      tmem_wait_ld();
+      tmem_reg_fence8(r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+      tmem_st8(tO + c * 8, r);
+    }
+  }
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(p_ready);
+  {
+    float t0, t1, t2, t3, t4, t5, t6, t7;
+    f32x2_unpack(sums[0], t0, t1);
+    f32x2_unpack(sums[1], t2, t3);
+    f32x2_unpack(sums[2], t4, t5);
+    f32x2_unpack(sums[3], t6, t7);
+    l += ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
+  }
+}
+
+// A lane's share of one key: 16 bytes of codes (8 dims of each of the 4 groups) and
+// the 4 parameters.
+struct KeyShare {
+  uint4 codes, par;
+};
+__device__ __forceinline__ void load_key(const Q4PrefillParams& p, KeyShare& s, bool of_v, int blk, int kv_head, int key0,
+                                         int row, int lane, int Lk) {
+  s.codes = s.par = make_uint4(0, 0, 0, 0);
+  if (blk < 0 || key0 + row >= Lk) return;  // zeros: a scale and a minimum of 0
+  const uint8_t* base = (of_v ? p.v_cache : p.k_cache) +
+                        (static_cast<int64_t>(blk) * p.hkv + kv_head) * kQ4RecordBytes +
+                        (key0 % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
+  const int tok = row % kQ4Tile;
+  s.codes = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + (lane & 3) * 16));
+  s.par = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
+}
+__device__ __forceinline__ int checked_block(const Q4PrefillParams& p, int blk) {
+  if (blk >= 0 && blk < p.num_blocks) return blk;
+  flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
+  return -1;
+}
+// s -> key `row` of the K or V tile at `tile`; `reload` fills s again meanwhile,
+// on_nan(group) is called where a group of V is NaN (it is written as zeros).
+template <Elem E, bool kV, class Reload, class OnNan>
+__device__ __forceinline__ void widen_key(KeyShare& s, uint32_t tile, int row, int lane, Reload reload, OnNan on_nan) {
+  const bool odd = (lane >> 2) & 1;
+  uint32_t w[4] = {s.codes.x, s.codes.y, s.codes.z, s.codes.w};
+  uint32_t sz[4] = {s.par.x, s.par.y, s.par.z, s.par.w};
+  int tt = lane & 3;
+  if constexpr (kV) {
+    // two 8-byte chunks of V: per group, the 4 dims of the first and then of the second
+    const uint4 c = s.codes;
+    w[0] = __byte_perm(c.x, c.z, 0x5410);
+    w[1] = __byte_perm(c.x, c.z, 0x7632);
+    w[2] = __byte_perm(c.y, c.w, 0x5410);
+    w[3] = __byte_perm(c.y, c.w, 0x7632);
+    tt ^= (row & 4) >> 1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((sz[k] & 0x7fffu) > 0x7c00u) {  // a NaN scale
+        on_nan(k);
+        sz[k] = 0u;
+      }
+  }
+  reload();
+  // odd rows take the groups in another order, so that the 8 lanes of a
+  // store phase (two rows, four chunks each) hit all banks
+  const uint32_t wa = odd ? w[1] : w[0], wb = odd ? w[0] : w[1], wc = odd ? w[3] : w[2], wd = odd ? w[2] : w[3];
+  const uint32_t pa = odd ? sz[1] : sz[0], pb = odd ? sz[0] : sz[1];
+  const uint32_t pc = odd ? sz[3] : sz[2], pd = odd ? sz[2] : sz[3];
+  const uint32_t at = tile + row * 128;
+  const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
+  auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
+    const uint4 v = kV ? dequantise8<Elem::kF16>(codes8, param) : dequantise8<E, true>(codes8, param);
+    sts128(at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+  };
+  put(wa, pa, 0, ca);
+  put(wb, pb, 0, cb);
+  put(wc, pc, 1, ca);
+  put(wd, pd, 1, cb);
+}
+// The products of one key tile and head: logits from Q and K tiles (low halves of
+// their descriptors), output from P in TMEM and a V tile.
+template <Elem E>
+__device__ __forceinline__ void issue_logits(int g, uint32_t q_lo, uint32_t k_lo) {
+  constexpr uint32_t idesc = idesc_f16kind_f32(kBM, kBN, false, false, ElemOps<E>::kMmaFormat);
+#pragma unroll
+  for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+    const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+    mma_ss(g * 128, q_lo + g * (kTileBytes >> 4) + off, k_lo + off, idesc, ks > 0 ? 1u : 0u);
+  }
+}
+__device__ __forceinline__ void issue_output(int g, uint32_t v_lo, bool first) {
+  constexpr uint32_t idesc = idesc_f16kind_f32(kBM, kHeadDim, false, true, ElemOps<Elem::kF16>::kMmaFormat);
+#pragma unroll
+  for (int ks = 0; ks < kBN / 16; ++ks)
+    mma_ts(256 + g * 128, g * 128 + ks * 8, v_lo + ((ks * 16 * 128) >> 4), idesc, ks > 0 || !first ? 1u : 0u);
+}
+
 // kWhole: a CTA has a query tile and all its keys. kSplitKeys: the CTAs of a
 // cluster have parts of one tile's keys. kPaired: two CTAs have neighbouring query
 // tiles of a sequence. Each widens 64 keys of every tile and copies them to the
@@ -360,33 +537,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv_head = 2 * pair / (p.hq / p.hkv);
   // key of batch 0 within the tile; batch i: + 8 i
   const int row0 = (kPair ? rank * 64 + (warp - kWidenWarp0) * 8 : (warp - kWidenWarp0) * 16) + (lane >> 2);
-  const int t = lane & 3;
-  const bool odd = (lane >> 2) & 1;
   auto block_of = [&](int n) -> int {
     return n < n_tiles ? p.block_tables[static_cast<int64_t>(b) * p.bt_stride + (tile0 + n) * kBN / kBlockSize] : -1;
   };
-  auto checked = [&](int blk) -> int {
-    if (blk >= 0 && blk < p.num_blocks) return blk;
-    flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
-    return -1;
-  };
-  uint4 codes[2], par[2];
+  KeyShare share[2];
   // key `row` of K_{i/2} (even i) or V_{i/2} (odd i), the ring's items, into registers j
   auto load_row = [&](int i, int row, int j, int blk) {
-    codes[j] = par[j] = make_uint4(0, 0, 0, 0);
-    const int key0 = (tile0 + (i >> 1)) * kBN;
-    if (blk < 0 || key0 + row >= Lk) return;  // zeros: a scale and a minimum of 0
-    const uint8_t* base = ((i & 1) ? p.v_cache : p.k_cache) +
-                          (static_cast<int64_t>(blk) * p.hkv + kv_head) * kQ4RecordBytes +
-                          (key0 % kBlockSize + row) / kQ4Tile * kQ4TileBytes;
-    const int tok = row % kQ4Tile;
-    codes[j] = __ldg(reinterpret_cast<const uint4*>(base + tok * kQ4CodeBytes + t * 16));
-    par[j] = __ldg(reinterpret_cast<const uint4*>(base + kQ4TileParams + tok * kQ4ParamBytes));
+    load_key(p, share[j], i & 1, blk, kv_head, (tile0 + (i >> 1)) * kBN, row, lane, Lk);
   };
   int blk = -1, blk_next = -1;
   if (kPair && warp >= kWidenWarp0) {
     // a warp has one batch of 8 keys, K's in registers 0, V's in registers 1
-    blk = checked(first_block);
+    blk = checked_block(p, first_block);
     load_row(0, row0, 0, blk);
     load_row(1, row0, 1, blk);
   }
@@ -415,8 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) mbar_wait(bar(kBarQ), 0, p.err);  // never leave a copy in flight
     if (warp == 1) {
       // =========================== MMA issuer ===========================
-      constexpr uint32_t idesc_s = idesc_f16kind_f32(kBM, kBN, false, false, Ops::kMmaFormat);
-      constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kHeadDim, false, true, ElemOps<Elem::kF16>::kMmaFormat);
       const uint32_t q_lo = desc_lo(sbase + kOffQ, 16);
       const uint32_t k_lo = desc_lo(sbase + kOffKV, 16), v_lo = desc_lo(sbase + kOffKV, kHalfBytes);
       bool ok = all_ok(wait_or_abort(bar(kBarQ), 0, s_abort, p.err));
@@ -437,21 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         parity ^= wrap ? 1u : 0u;
       };
       auto issue_s = [&](int g, int at) {
-        const uint32_t q = q_lo + g * (kTileBytes >> 4), k = k_lo + at * (kTileBytes >> 4);
-#pragma unroll
-        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-          mma_ss(tmem + g * 128, q + off, k + off, idesc_s, ks > 0 ? 1u : 0u);
-        }
+        issue_logits<E>(g, q_lo, k_lo + at * (kTileBytes >> 4));
         commit_elected(bar(kBarSFull + g));
       };
-      auto issue_pv = [&](int g, int at, bool first) {
-        const uint32_t v = v_lo + at * (kTileBytes >> 4);
-#pragma unroll
-        for (int ks = 0; ks < kBN / 16; ++ks)
-          mma_ts(tmem + 256 + g * 128, tmem + g * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), idesc_pv,
-                 ks > 0 || !first ? 1u : 0u);
-      };
+      auto issue_pv = [&](int g, int at, bool first) { issue_output(g, v_lo + at * (kTileBytes >> 4), first); };
       if (ok && n_tiles > 0 && (ok = landed())) {
         tc_fence_after();
         issue_s(0, slot);
@@ -502,46 +651,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================== K/V widening ===========================
     regs_dec<kRegsWiden>();
     const uint32_t other = kPair ? in_part(sbase, rank ^ 1) : 0u;  // the pair's other CTA
-    // registers j -> key `row` of the item's tile; `reload` fills them again meanwhile
     auto widen_row = [&](auto of_v, int i, int row, int j, uint32_t slot_off, auto reload) {
-      constexpr bool kV = decltype(of_v)::value;
-      uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
-      uint32_t sz[4] = {par[j].x, par[j].y, par[j].z, par[j].w};
-      int tt = t;
-      if constexpr (kV) {
-        // two 8-byte chunks of V: per group, the 4 dims of the first and then of the second
-        const uint4 c = codes[j];
-        w[0] = __byte_perm(c.x, c.z, 0x5410);
-        w[1] = __byte_perm(c.x, c.z, 0x7632);
-        w[2] = __byte_perm(c.y, c.w, 0x5410);
-        w[3] = __byte_perm(c.y, c.w, 0x7632);
-        tt = t ^ ((row & 4) >> 1);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((sz[k] & 0x7fffu) > 0x7c00u) {  // a NaN scale
-            const int at = (tile0 + (i >> 1)) * kBN + row;
-            atomicMin(s_nan + k, at);
-            if (kPair) min_cluster(other + kOffMisc + 8 + 4 * k, at);
-            sz[k] = 0u;
-          }
-      }
-      reload();
-      // odd rows take the groups in another order, so that the 8 lanes of a
-      // store phase (two rows, four chunks each) hit all banks
-      const uint32_t wa = odd ? w[1] : w[0], wb = odd ? w[0] : w[1], wc = odd ? w[3] : w[2], wd = odd ? w[2] : w[3];
-      const uint32_t pa = odd ? sz[1] : sz[0], pb = odd ? sz[0] : sz[1];
-      const uint32_t pc = odd ? sz[3] : sz[2], pd = odd ? sz[2] : sz[3];
-      const uint32_t at = kOffKV + slot_off + row * 128;
-      const int ca = (odd ? 4 : 0) + tt, cb = (odd ? 0 : 4) + tt;  // 16-byte chunk within the half row
-      auto put = [&](uint32_t codes8, uint32_t param, int half, int chunk) {
-        const uint4 v = kV ? dequantise8<Elem::kF16>(codes8, param) : dequantise8<E, true>(codes8, param);
-        const uint32_t off = at + half * kHalfBytes + ((chunk ^ (row & 7)) << 4);
-        sts128(sbase + off, v.x, v.y, v.z, v.w);
-      };
-      put(wa, pa, 0, ca);
-      put(wb, pb, 0, cb);
-      put(wc, pc, 1, ca);
-      put(wd, pd, 1, cb);
+      widen_key<E, decltype(of_v)::value>(share[j], sbase + kOffKV + slot_off, row, lane, reload, [&](int k) {
+        const int at = (tile0 + (i >> 1)) * kBN + row;
+        atomicMin(s_nan + k, at);
+        if (kPair) min_cluster(other + kOffMisc + 8 + 4 * k, at);
+      });
     };
     // the item's slot, once the products (a pair's: of both CTAs) that used it before are complete
     auto wait_slot = [&](int i) -> bool {
@@ -572,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n_items; i += 2) {
         blk_next = block_of((i >> 1) + 1);
         if (!wait_slot(i)) break;
-        if (i + 2 < n_items) blk = checked(blk_next);
+        if (i + 2 < n_items) blk = checked_block(p, blk_next);
         widen_row(std::false_type{}, i, row0, 0, i % kKvSlots * kTileBytes,
                   [&] { if (i + 2 < n_items) load_row(i + 2, row0, 0, blk); });
         written(i);
@@ -585,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, n_items - kKvSlots); i < n_items; ++i)
         if (!wait_slot(i + kKvSlots)) break;
     } else {
-      blk = n_tiles > 0 ? checked(kSplit ? block_of(0) : first_block) : -1;
+      blk = n_tiles > 0 ? checked_block(p, kSplit ? block_of(0) : first_block) : -1;
 #pragma unroll
       for (int j = 0; j < 2; ++j) load_row(0, row0 + 8 * j, j, blk);
       for (int i = 0; i < n_items; i += 2) {
@@ -596,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           widen_row(std::false_type{}, i, row0 + 8 * j, j, i % kKvSlots * kTileBytes,
                     [&] { load_row(i + 1, row0 + 8 * j, j, blk); });
         written(i);
-        if (i + 2 < n_items) blk = checked(blk_next);
+        if (i + 2 < n_items) blk = checked_block(p, blk_next);
         if (!wait_slot(i + 1)) break;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -618,11 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_base + g * 128;
     const uint32_t tO = tmem + lane_base + 256 + g * 128;
-    // a bf16 K is held as 2^-64 of its values (dequantise8)
-    const float sl2 = p.scale_log2 * (E == Elem::kBF16 ? 18446744073709551616.f : 1.f);
-    constexpr float kLift = 6.f;
-    float m = -INFINITY;  // running max less kLift, log2 units (scaled)
-    float l = 0.f;
+    const float sl2 = p.scale_log2 * kKeyScale<E>;
+    float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int n = 0; n < n_tiles; ++n) {
       ok = wait_or_abort(bar(kBarSFull + g), n & 1, s_abort, p.err);
@@ -631,93 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      float s[128];
-      {
-        uint32_t r0_[32], r1[32], r2[32], r3[32];
-        tmem_ld32(tS + 0, r0_);
-        tmem_ld32(tS + 32, r1);
-        tmem_ld32(tS + 64, r2);
-        tmem_ld32(tS + 96, r3);
-        tmem_wait_ld();
-        tmem_reg_fence(r0_);
-        tmem_reg_fence(r1);
-        tmem_reg_fence(r2);
-        tmem_reg_fence(r3);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          s[j] = __uint_as_float(r0_[j]);
-          s[32 + j] = __uint_as_float(r1[j]);
-          s[64 + j] = __uint_as_float(r2[j]);
-          s[96 + j] = __uint_as_float(r3[j]);
-        }
-      }
       const int key0 = (tile0 + n) * kBN;
-      if (key0 + kBN - 1 > pos0 || key0 + kBN > Lk) {
-        const int lim = min(pos, Lk - 1) - key0;  // keys j <= lim are visible
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-          if (j > lim) s[j] = -INFINITY;
-      }
-      float ma = s[0], mb = s[1];
-#pragma unroll
-      for (int j = 2; j < 126; j += 4) {
-        ma = fmax3(ma, s[j], s[j + 1]);
-        mb = fmax3(mb, s[j + 2], s[j + 3]);
-      }
-      float mx = fmaxf(fmax3(ma, s[126], s[127]), mb);
-      mx *= sl2;
-      float m_use = m;
-      // Move the maximum only when it grows by more than 2^8. m is kLift below it: P stays
-      // under 2^14, and is a normal fp16 number down to 2^-20 of the largest.
-      if (mx > m + (8.0f + kLift)) m_use = mx - kLift;
-      const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_use);
-      l *= alpha;
-      const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
-      const float neg_m = kSplit && m_use == -INFINITY ? 0.f : -m_use;  // a part may begin with keys that a row can't see
-      const uint64_t negm2 = f32x2_pack(neg_m, neg_m);
-      // P = 2^(s*sl2 - m_use), rounded to the element type, over the logits in TMEM
-      uint64_t sums[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = c * 16 + 2 * i;
-          float a0, a1;
-          f32x2_unpack(f32x2_fma(f32x2_pack(s[j], s[j + 1]), sl2x2, negm2), a0, a1);
-          a0 = ex2_approx(a0);
-          a1 = ex2_approx(a1);
-          sums[i & 3] = f32x2_add(sums[i & 3], f32x2_pack(a0, a1));
-          pk[i] = ElemOps<Elem::kF16>::pack(a0, a1);
-        }
-        tmem_st8(tS + c * 8, pk);
-      }
-      m = m_use;
-      // rescale the running output (PV_g(n-1) is complete: S_g(n) was issued after it)
-      if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-        for (int c = 0; c < 16; ++c) {
-          uint32_t r[8];
-          tmem_ld8(tO + c * 8, r);
-          tmem_wait_ld();
-          tmem_reg_fence8(r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-          tmem_st8(tO + c * 8, r);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarPReady + g));
-      {
-        float t0, t1, t2, t3, t4, t5, t6, t7;
-        f32x2_unpack(sums[0], t0, t1);
-        f32x2_unpack(sums[1], t2, t3);
-        f32x2_unpack(sums[2], t4, t5);
-        f32x2_unpack(sums[3], t6, t7);
-        l += ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
-      }
+      softmax_tile<kSplit>(tS, tO, n == 0, key0 + kBN - 1 > pos0 || key0 + kBN > Lk, min(pos, Lk - 1) - key0, sl2, m, l,
+                           bar(kBarPReady + g), lane);
     }
     if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), 0, s_abort, p.err));
     const uint32_t stage = sbase + kOffQ;
@@ -840,6 +868,356 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---- the same for many short tiles: every CTA goes through several units ----
+//
+// One CTA to a tile spends about 5.4 us on each beside its key tiles: 3 us until the
+// first logits, 1.8 of epilogue, 0.6 between two CTAs. Here one CTA per SM goes
+// through units (a query tile and two heads) k * SMs + its index of a list, longest
+// tiles first, that every CTA builds from the lengths, and the roles run on from
+// one unit to the next:
+//   warp 0       describes the units (kDescs of them are under way at most) and
+//                loads a unit's queries as soon as the last one's logits are done
+//   warps 12-19  widen the next unit's first tiles while the last products run
+//   warp 1       issues the next unit's logits while the softmax warps still write
+//                the last output; its first product with V waits until they have
+//                read the accumulators
+// Outputs leave from registers, 32 bytes a store (the staging area is the queries').
+// 128 prompts of 64..512 tokens on a shared prefix of 1024: 480 -> 430 us; 64 of 384
+// on 1024 308 -> 290, 16 of 512..1024 on 2048 281 -> 275.
+constexpr int kMaxListSeqs = 256, kMaxList = 700, kMaxLevels = 32;  // sequences, tiles, tiles of a sequence
+constexpr int kDescs = 4;  // units under way between the loader and the last epilogue
+struct UnitInfo {
+  int n_tiles;  // < 0: no more
+  int b, pair, r0, rows_valid, pos0, Lk, cq0;
+};
+struct UnitsShared {
+  uint64_t bars[32];
+  UnitInfo unit[kDescs];
+  int nan[kDescs][4];
+  uint32_t tmem;
+  int abort_flag;
+  int list_len;
+  uint16_t list[kMaxList];
+};
+constexpr int kUBarQ = 0, kUBarKvFull = 1, kUBarKvFree = kUBarKvFull + kKvSlots, kUBarSFull = kUBarKvFree + kKvSlots,
+              kUBarPReady = kUBarSFull + 2, kUBarOFinal = kUBarPReady + 2, kUBarOFree = kUBarOFinal + 1,
+              kUBarQFree = kUBarOFree + 2, kUBarReady = kUBarQFree + 1, kUBarDone = kUBarReady + kDescs,
+              kUBarDrain = kUBarDone + kDescs, kUBarEnd = kUBarDrain + 1, kUNumBars = kUBarEnd + 1;
+static_assert(kUNumBars <= 32, "barriers");
+constexpr size_t kUnitsSmemBytes = kOffBar + sizeof(UnitsShared) + 1024;
+static_assert(kUnitsSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
+
+template <Elem E>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_q4_units_kernel(const __grid_constant__ CUtensorMap tm_q, const Q4PrefillParams p) {
+  using Ops = ElemOps<E>;
+  constexpr int kRegsFirst = 64, kRegsSoftmax = E == Elem::kBF16 ? 152 : 144, kRegsWiden = E == Elem::kBF16 ? 56 : 64;
+  static_assert(kRegsFirst + 2 * kRegsSoftmax + 2 * kRegsWiden == 5 * 96, "the split must sum up to the launch's registers");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
+  UnitsShared* sh = reinterpret_cast<UnitsShared*>(smem_raw + (sbase - raw_addr) + kOffBar);
+  const uint32_t bar0 = sbase + kOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  volatile int* s_abort = &sh->abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int pairs = p.hq / 2;
+
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < kUNumBars; ++i) {
+      int count = 1;
+      if (i >= kUBarKvFull && i < kUBarKvFull + kKvSlots) count = kWidenWarps;
+      if (i >= kUBarPReady && i < kUBarPReady + 2) count = 4;
+      if (i >= kUBarOFree && i < kUBarOFree + 2) count = 4;
+      if (i >= kUBarDone && i < kUBarDone + kDescs) count = 8;
+      if (i == kUBarEnd) count = 8;
+      mbar_init(bar(i), count);
+    }
+    sh->abort_flag = 0;
+    mbar_fence_init();
+    prefetch_tmap(&tm_q);
+  }
+  if (warp == 0) {
+    // the live query tiles, longest sequences' last ones first (every CTA builds the same list)
+    int tiles[kMaxListSeqs / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxListSeqs / 32; ++i) {
+      const int b = i * 32 + lane;
+      tiles[i] = 0;
+      if (b < p.num_seqs) {
+        const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1], Lq = cq1 - cq0, Lk = p.cu_k[b + 1] - p.cu_k[b];
+        if (Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || Lk > INT_MAX - 2 * kBN || cq0 < 0 ||
+            cq1 > p.total_q || Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
+          if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+        } else {
+          tiles[i] = (Lq + kBM - 1) / kBM;
+        }
+      }
+    }
+    int n = 0;
+    for (int qt = p.max_q_tiles - 1; qt >= 0; --qt) {
+#pragma unroll
+      for (int i = 0; i < kMaxListSeqs / 32; ++i) {
+        const uint32_t live = __ballot_sync(0xffffffffu, tiles[i] > qt);
+        const int at = n + __popc(live & ((1u << lane) - 1u));
+        if (tiles[i] > qt && at < kMaxList) sh->list[at] = static_cast<uint16_t>(qt * kMaxListSeqs + i * 32 + lane);
+        n += __popc(live);
+      }
+    }
+    if (lane == 0) {
+      if (n > kMaxList && blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);  // rows given to several sequences
+      sh->list_len = min(n, kMaxList);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at column 0
+  auto ready = [&](int j) -> bool {
+    return all_ok(wait_or_abort(bar(kUBarReady + (j % kDescs)), (j / kDescs) & 1, s_abort, p.err));
+  };
+
+  if (warp < 4) {
+    regs_dec<kRegsFirst>();
+    if (warp == 0 && lane == 0) {
+      // =========================== units and their queries ===========================
+      const int n_units = sh->list_len * pairs;
+      int loads = 0;
+      for (int j = 0;; ++j) {
+        const int d = j % kDescs;
+        if (j >= kDescs && !wait_or_abort(bar(kUBarDone + d), ((j / kDescs) - 1) & 1, s_abort, p.err)) break;
+        const int64_t unit = static_cast<int64_t>(j) * gridDim.x + blockIdx.x;
+        UnitInfo u{};
+        u.n_tiles = -1;
+        if (unit < n_units) {
+          const int code = sh->list[static_cast<int>(unit) / pairs];
+          u.b = code % kMaxListSeqs;
+          u.pair = static_cast<int>(unit) % pairs;
+          u.r0 = code / kMaxListSeqs * kBM;
+          u.cq0 = p.cu_q[u.b];
+          const int Lq = p.cu_q[u.b + 1] - u.cq0;
+          u.Lk = p.cu_k[u.b + 1] - p.cu_k[u.b];
+          u.rows_valid = min(kBM, Lq - u.r0);
+          u.pos0 = u.Lk - Lq + u.r0;
+          u.n_tiles = (u.pos0 + u.rows_valid - 1) / kBN + 1;
+        }
+        sh->unit[d] = u;
+        for (int i = 0; i < 4; ++i) sh->nan[d][i] = INT_MAX;
+        mbar_arrive(bar(kUBarReady + d));
+        if (u.n_tiles < 0) break;
+        if (j > 0 && !wait_or_abort(bar(kUBarQFree), (j - 1) & 1, s_abort, p.err)) break;
+        mbar_arrive_expect_tx(bar(kUBarQ), 2 * kTileBytes);
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t dst = sbase + kOffQ + g * kTileBytes;
+          tma_load_3d(dst, &tm_q, 0, 2 * u.pair + g, u.cq0 + u.r0, bar(kUBarQ));
+          tma_load_3d(dst + kHalfBytes, &tm_q, 64, 2 * u.pair + g, u.cq0 + u.r0, bar(kUBarQ));
+        }
+        ++loads;
+      }
+      if (loads > 0) mbar_wait(bar(kUBarQ), (loads - 1) & 1, p.err);  // never leave a copy in flight
+    }
+    if (warp == 1) {
+      // =========================== MMA issuer ===========================
+      const uint32_t q_lo = desc_lo(sbase + kOffQ, 16);
+      const uint32_t k_lo = desc_lo(sbase + kOffKV, 16), v_lo = desc_lo(sbase + kOffKV, kHalfBytes);
+      bool ok = true;
+      int slot = 0;
+      uint32_t parity = 0, tile_parity = 0;
+      auto landed = [&]() -> bool { return all_ok(wait_or_abort(bar(kUBarKvFull + slot), parity, s_abort, p.err)); };
+      auto release = [&](int which) { commit_elected(bar(kUBarKvFree + which)); };
+      auto advance = [&]() {
+        const bool wrap = slot == kKvSlots - 1;
+        slot = wrap ? 0 : slot + 1;
+        parity ^= wrap ? 1u : 0u;
+      };
+      auto issue_s = [&](int g, int at) {
+        issue_logits<E>(g, q_lo, k_lo + at * (kTileBytes >> 4));
+        commit_elected(bar(kUBarSFull + g));
+      };
+      auto issue_pv = [&](int g, int at, bool first) { issue_output(g, v_lo + at * (kTileBytes >> 4), first); };
+      for (int j = 0; ok; ++j) {
+        if (!(ok = ready(j))) break;
+        const int n_tiles = sh->unit[j % kDescs].n_tiles;
+        if (n_tiles < 0) break;
+        if (!(ok = all_ok(wait_or_abort(bar(kUBarQ), j & 1, s_abort, p.err)) && landed())) break;
+        tc_fence_after();
+        issue_s(0, slot);
+        issue_s(1, slot);
+        release(slot);
+        if (n_tiles == 1) commit_elected(bar(kUBarQFree));
+        advance();
+        for (int n = 0; n < n_tiles; ++n) {
+          const bool more = n + 1 < n_tiles;
+          if (!(ok = landed())) break;
+          if (!(ok = all_ok(wait_or_abort(bar(kUBarPReady + 0), tile_parity, s_abort, p.err)))) break;
+          if (n == 0 && j > 0 && !(ok = all_ok(wait_or_abort(bar(kUBarOFree + 0), (j - 1) & 1, s_abort, p.err)))) break;
+          tc_fence_after();
+          const int at_v = slot;
+          advance();
+          issue_pv(0, at_v, n == 0);
+          if (more) {
+            if (!(ok = landed())) break;
+            tc_fence_after();
+            issue_s(0, slot);
+          }
+          if (!(ok = all_ok(wait_or_abort(bar(kUBarPReady + 1), tile_parity, s_abort, p.err)))) break;
+          if (n == 0 && j > 0 && !(ok = all_ok(wait_or_abort(bar(kUBarOFree + 1), (j - 1) & 1, s_abort, p.err)))) break;
+          tc_fence_after();
+          issue_pv(1, at_v, n == 0);
+          release(at_v);
+          if (more) {
+            issue_s(1, slot);
+            release(slot);
+            if (n + 2 == n_tiles) commit_elected(bar(kUBarQFree));
+            advance();
+          }
+          tile_parity ^= 1;
+        }
+        commit_elected(bar(kUBarOFinal));
+      }
+      if (!ok) {
+        // make sure no product is still writing TMEM before it is released
+        commit_elected(bar(kUBarDrain));
+        mbar_wait(bar(kUBarDrain), 0, p.err);
+      }
+      __syncwarp();
+      mbar_wait(bar(kUBarEnd), 0, p.err);
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  } else if (warp >= kWidenWarp0) {
+    // =========================== K/V widening ===========================
+    regs_dec<kRegsWiden>();
+    const int row0 = (warp - kWidenWarp0) * 16 + (lane >> 2);
+    int slot = 0;
+    uint32_t parity = 1;  // of the slot's last use: nothing to wait for in the first round
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      if (!(ok = ready(j))) break;
+      const UnitInfo& u = sh->unit[j % kDescs];
+      const int n_tiles = u.n_tiles;
+      if (n_tiles < 0) break;
+      const int Lk = u.Lk;
+      const int64_t table = static_cast<int64_t>(u.b) * p.bt_stride;
+      const int kv_head = 2 * u.pair / (p.hq / p.hkv);
+      int* s_nan = sh->nan[j % kDescs];
+      auto block_of = [&](int n) -> int { return n < n_tiles ? p.block_tables[table + n * kBN / kBlockSize] : -1; };
+      KeyShare share[2];
+      auto load_row = [&](int i, int row, int jj, int blk) {
+        load_key(p, share[jj], i & 1, blk, kv_head, (i >> 1) * kBN, row, lane, Lk);
+      };
+      auto widen_row = [&](auto of_v, int i, int row, int jj, auto reload) {
+        widen_key<E, decltype(of_v)::value>(share[jj], sbase + kOffKV + slot * kTileBytes, row, lane, reload,
+                                            [&](int k) { atomicMin(s_nan + k, (i >> 1) * kBN + row); });
+      };
+      auto wait_slot = [&]() -> bool {
+        return all_ok(wait_or_abort(bar(kUBarKvFree + slot), parity, s_abort, p.err));
+      };
+      auto written = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kUBarKvFull + slot));
+        const bool wrap = slot == kKvSlots - 1;
+        slot = wrap ? 0 : slot + 1;
+        parity ^= wrap ? 1u : 0u;
+      };
+      const int n_items = 2 * n_tiles;
+      int blk = checked_block(p, block_of(0)), blk_next = -1;
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) load_row(0, row0 + 8 * jj, jj, blk);
+      for (int i = 0; i < n_items; i += 2) {
+        blk_next = block_of((i >> 1) + 1);
+        if (!(ok = wait_slot())) break;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+          widen_row(std::false_type{}, i, row0 + 8 * jj, jj, [&] { load_row(i + 1, row0 + 8 * jj, jj, blk); });
+        written();
+        if (i + 2 < n_items) blk = checked_block(p, blk_next);
+        if (!(ok = wait_slot())) break;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+          widen_row(std::true_type{}, i + 1, row0 + 8 * jj, jj,
+                    [&] { if (i + 2 < n_items) load_row(i + 2, row0 + 8 * jj, jj, blk); });
+        written();
+      }
+    }
+  } else {
+    // =========================== softmax groups ===========================
+    regs_inc<kRegsSoftmax>();
+    const int g = (warp - kSoftmaxWarp0) >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_base + g * 128;
+    const uint32_t tO = tmem + lane_base + 256 + g * 128;
+    const float sl2 = p.scale_log2 * kKeyScale<E>;
+    uint32_t tile_parity = 0;
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      if (!(ok = ready(j))) break;
+      const UnitInfo& u = sh->unit[j % kDescs];
+      const int n_tiles = u.n_tiles, pos0 = u.pos0, Lk = u.Lk;
+      if (n_tiles < 0) break;
+      const int pos = pos0 + row;
+      float m = -INFINITY, l = 0.f;
+      for (int n = 0; n < n_tiles; ++n) {
+        if (!(ok = all_ok(wait_or_abort(bar(kUBarSFull + g), tile_parity, s_abort, p.err)))) break;
+        tile_parity ^= 1;
+        tc_fence_after();
+        const int key0 = n * kBN;
+        softmax_tile<false>(tS, tO, n == 0, key0 + kBN - 1 > pos0 || key0 + kBN > Lk, min(pos, Lk - 1) - key0, sl2, m, l,
+                            bar(kUBarPReady + g), lane);
+      }
+      if (ok) ok = all_ok(wait_or_abort(bar(kUBarOFinal), j & 1, s_abort, p.err));
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+      const bool valid = row < u.rows_valid;
+      uint16_t* orow = p.out + (static_cast<int64_t>(u.cq0 + u.r0 + row) * p.hq + 2 * u.pair + g) * kHeadDim;
+      const int* s_nan = sh->nan[j % kDescs];
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {  // group c of 32 dims
+        uint32_t r[32];
+        tmem_ld32(tO + c * 32, r);
+        tmem_wait_ld();
+        tmem_reg_fence(r);
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kUBarOFree + g));
+        }
+        if (pos >= s_nan[c]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0x7fffffffu;
+        }
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          x[i] = Ops::pack(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
+        if (valid) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(orow + c * 32 + 2 * i), "r"(x[i]),
+                         "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]),
+                         "r"(x[i + 7])
+                         : "memory");
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kUBarDone + j % kDescs));
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kUBarEnd));
+  }
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -873,6 +1251,7 @@ bool encode_q(CUtensorMap* tm, const void* base, int64_t rows, int heads, int64_
 }
 
 constexpr int kPairTiles = 4, kPairKeyTiles = 28;  // query tiles per sequence, and key tiles, from which on CTAs pair up
+constexpr int kUnitRounds = 4;  // rounds of items from which on a CTA goes through several
 constexpr int kMinPartTiles = 2;  // key tiles per CTA at least, where the keys of an item are split
 
 template <Elem E, Share kShare>
@@ -915,7 +1294,9 @@ cudaError_t device_limits(DeviceLimits* out) {
   }
   DeviceLimits d{};
   if ((e = allow_smem<E, Share::kWhole>()) != cudaSuccess || (e = allow_smem<E, Share::kSplitKeys>()) != cudaSuccess ||
-      (e = allow_smem<E, Share::kPaired>()) != cudaSuccess)
+      (e = allow_smem<E, Share::kPaired>()) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(prefill_q4_units_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kUnitsSmemBytes))) != cudaSuccess)
     return e;
   if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   d.clusters[0] = d.sms;
@@ -949,6 +1330,9 @@ cudaError_t device_limits(DeviceLimits* out) {
 //    5000 after 2000        215.2   207.7    200.8    216.2   4
 //    5000 after 7001        459.9   412.8    386.2    398.5   4
 //
+// Many rounds of short tiles go to the kernel that takes them in units, if its list
+// holds them (its stores need 32-byte aligned rows).
+//
 // Pairs of CTAs widen half as much each, 15 % of the time on long keys: one prompt
 // of 8192 259 -> 224 us, 16 of 1024 on 4096 589 -> 507, 5000 on 7001 382 -> 329.
 // On short ones setting two CTAs up together costs more (8 of 1024 on 1024 124 ->
@@ -981,6 +1365,11 @@ cudaError_t launch_typed(const CUtensorMap& tq, Q4PrefillParams& p, int64_t n_it
   cudaLaunchAttribute attr;
   p.first = 0;
   p.by_twos = paired;
+  if (!paired && shift == 0 && rounds >= kUnitRounds && p.num_seqs <= kMaxListSeqs && p.max_q_tiles <= kMaxLevels &&
+      p.total_q / kBM + p.num_seqs <= kMaxList && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+    prefill_q4_units_kernel<E><<<d.sms, kThreads, kUnitsSmemBytes, stream>>>(tq, p);
+    return cudaGetLastError();
+  }
   if (whole > 0 && paired) {
     const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(whole), 2, &attr, stream);
     e = cudaLaunchKernelEx(&cfg, prefill_q4_kernel<E, Share::kPaired>, tq, const_cast<const Q4PrefillParams&>(p));

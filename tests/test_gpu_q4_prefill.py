@@ -212,6 +212,56 @@ def test_calls_at_once_and_captured(pkv):
     assert all(torch.equal(o, w) for o, w in zip(outs, want)) and pkv.pkv_device_error() == 0
 
 
+def many_short(seed, n, hq, hkv):
+    rng = np.random.default_rng(seed)
+    lq = [int(x) for x in rng.choice([0, 1, 5, 127, 128, 129, 200, 300], n)]
+    return lq, [max(1, a + int(b)) for a, b in zip(lq, rng.integers(0, 900, n))]
+
+
+@pytest.mark.parametrize("n,hq,hkv,dtype", [(40, 16, 8, BF16), (40, 32, 8, F16), (256, 4, 2, BF16), (70, 24, 4, F16)])
+def test_many_short_tiles(pkv, n, hq, hkv, dtype):
+    """Several units to a CTA (over 4 rounds of tiles), of one to ten key tiles; the same with an output that the
+    32-byte stores can't take, which goes to the kernel of one tile to a CTA: the same bits."""
+    c = Prefill(pkv, *many_short(n, n, hq, hkv), hq, hkv, dtype, seed=80 + n, extra_rows=3).fill()
+    flat = torch.full((c.q.shape[0] * hq * 128 + 8,), 3.0, dtype=dtype, device="cuda")
+    out, shifted = torch.full(c.q.shape, 3.0, dtype=dtype, device="cuda"), flat[8:].view(c.q.shape)
+    c.prefill(out=out)
+    c.check(out)
+    assert bool((out[c.total:] == 3.0).all())
+    c.prefill(out=shifted)
+    assert shifted.data_ptr() % 32 == 16 and torch.equal(shifted, out)
+    again = c.prefill(plan=pkv.pkv_prefill_plan(c.cq, c.ck))
+    assert torch.equal(again[:c.total], out[:c.total]) and pkv.pkv_device_error() == 0
+
+
+def test_many_short_tiles_nan_bad_blocks_and_lengths(pkv):
+    lq, lk = many_short(3, 60, 16, 8)
+    lq[7], lk[7] = 200, 700
+    lq[20], lk[20] = 300, 600
+    c = Prefill(pkv, lq, lk, 16, 8, BF16, seed=90).fill()
+    want = c.prefill()
+    c.v[c.first[7] + 650, 3, 100] = float("nan")
+    out = c.fill().prefill()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[c.cq[7] + 150:c.cq[8], 6:8, 96:128] = True
+    assert bool(out[hit].isnan().all()) and torch.equal(out[~hit], want[~hit])
+    assert pkv.pkv_device_error() == 0
+    c.tables[20, 1] = -7
+    out = c.prefill()
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_BLOCK
+    hit[c.cq[20]:c.cq[21]] = True
+    assert torch.equal(out[~hit], want[~hit])
+    c.tables[20, 1] = c.tables[20, 0]
+    mark = torch.full_like(want, 7.0)
+    c.f("pkv_prefill_varlen_q4")(c.q, c.d_cq, c.d_ck, 299, max(lk), c.scale, c.kc, c.vc, c.tables, out=mark)
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_SEQLEN   # the sequences of 300 are skipped
+    long = torch.zeros_like(hit)
+    for b, n in enumerate(lq):
+        if n == 300:
+            long[c.cq[b]:c.cq[b + 1]] = True
+    assert bool((mark[long] == 7.0).all()) and torch.equal(mark[~long & ~hit], want[~long & ~hit])
+
+
 def test_growing_logits(pkv):
     """The running maximum moves in every key tile."""
     c = Prefill(pkv, [400], [1500], 16, 8, BF16, seed=28)
