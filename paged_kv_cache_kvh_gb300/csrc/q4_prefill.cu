@@ -1263,7 +1263,7 @@ cudaError_t allow_smem() {
 struct DeviceLimits {
   bool known;
   int sms;
-  int clusters[4];  // clusters of 1, 2, 4 and 8 CTAs that run at once
+  int clusters[4];  // [i], i > 0: clusters of 2^i CTAs that run at once
 };
 
 cudaLaunchConfig_t launch_config(unsigned ctas, int parts, cudaLaunchAttribute* attr, cudaStream_t stream) {
@@ -1299,11 +1299,11 @@ cudaError_t device_limits(DeviceLimits* out) {
                                 static_cast<int>(kUnitsSmemBytes))) != cudaSuccess)
     return e;
   if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  d.clusters[0] = d.sms;
   for (int i = 1; i < 4; ++i) {
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = launch_config(static_cast<unsigned>(d.sms) << i, 1 << i, &attr, nullptr);
-    if ((e = cudaOccupancyMaxActiveClusters(&d.clusters[i], prefill_q4_kernel<E, Share::kSplitKeys>, &cfg)) != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveClusters(&d.clusters[i], prefill_q4_kernel<E, Share::kSplitKeys>, &cfg);
+    if (e != cudaSuccess) return e;
   }
   d.known = true;
   if (dev >= 0 && dev < 64) all[dev] = d;
@@ -1330,8 +1330,10 @@ cudaError_t device_limits(DeviceLimits* out) {
 //    5000 after 2000        215.2   207.7    200.8    216.2   4
 //    5000 after 7001        459.9   412.8    386.2    398.5   4
 //
-// Many rounds of short tiles go to the kernel that takes them in units, if its list
-// holds them (its stores need 32-byte aligned rows).
+// kUnitRounds rounds of items and more go to the kernel that takes them in units, if
+// its list holds them (its stores need 32-byte aligned rows): 29 of 100..1024 94 ->
+// 83 us, 200 of 64 on 300 135 -> 108, 40 of 1..400 on 500 96 -> 87; on fewer rounds
+// its fixed shares are uneven (4 of 2048 83 -> 97).
 //
 // Pairs of CTAs widen half as much each, 15 % of the time on long keys: one prompt
 // of 8192 259 -> 224 us, 16 of 1024 on 4096 589 -> 507, 5000 on 7001 382 -> 329.
