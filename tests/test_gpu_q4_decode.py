@@ -378,3 +378,15 @@ def test_cache_past_32_bit_offsets(pkv):
                                .astype(np.int32)).cuda()
     c.fill()
     c.check(c.decode())
+
+
+@pytest.mark.parametrize("hkv", [8192, 4])
+def test_most_heads(pkv, hkv):
+    c = Case(pkv, [10, 300 if hkv == 4 else 33], 8192, hkv, F16, seed=95, spare=1).fill()
+    c.check(c.decode())
+
+
+def test_most_sequences(pkv):
+    n = 65535
+    c = Case(pkv, [i % 3 for i in range(n)], 2, 1, BF16, seed=96).fill()
+    c.check(c.decode(), set(range(0, n, 1997)) | {n - 1, n - 2, n - 3})

@@ -382,3 +382,15 @@ def test_store_prefill_decode_run(pkv):
         near(out[:1], slice(i, i + 1), i, 2.0 ** -11 + 2.0 ** -14)
         assert not bool(out[1].any())
     assert pkv.pkv_device_error() == 0
+
+
+@pytest.mark.parametrize("hkv", [4096, 1])
+def test_most_heads(pkv, hkv):
+    c = Prefill(pkv, [3, 130], [10, 300], 8192, hkv, BF16, seed=95).fill()
+    c.check(c.prefill())
+
+
+def test_most_sequences(pkv):
+    n = 65535
+    c = Prefill(pkv, [1] * n, [1 + i % 3 for i in range(n)], 2, 1, BF16, seed=96).fill()
+    c.check(c.prefill(), set(range(0, n, 1997)) | {n - 1})
