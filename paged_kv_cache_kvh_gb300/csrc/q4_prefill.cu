@@ -33,14 +33,14 @@
 // A pair of bf16 keys costs two ANDs, one packed multiply-add and one conversion
 // (the nibbles are used in place, as fp32 subnormals; see dequantise8), which is why
 // a bf16 K tile holds 2^-64 of the values; the powers of two are taken out of the
-// logits. Rows past the sequence are written as zeros. So is a
-// group of V that reads back as NaN: in a product it would reach every query row
-// of the tile, masked or not (0 * NaN). The first such position of each group is
-// kept instead, and rows at or past it get NaN in the epilogue.
+// logits. Rows past the sequence are written as zeros. So is a group of V that
+// reads back as NaN: in a product it would reach every query row of the tile,
+// masked or not (0 * NaN). The first such position of each group is kept instead,
+// and rows at or past it get NaN in the epilogue.
 //
 // Registers: 640 threads x 96 at launch, split over the warpgroups by what each
-// needs without spilling (shared memory leaves no L1 for local memory: the first
-// form, which spilled, took 904 us where this takes 481).
+// needs without spilling in its loop (shared memory leaves no L1 for local memory:
+// the first form, which spilled there, took 904 us where this takes 481).
 //
 // A tile's start is a chain of loads: lengths, block, codes, first widening, first
 // product, about 3 us in all beside 0.6 us between two CTAs and 1.8 us of epilogue.
@@ -62,7 +62,8 @@
 // CTA: half) and 6 k of softmax, against 2048 cycles (1.1 us) of tensor core at its
 // peak. 128 prompts of 64..512 tokens on a shared prefix of 1024 (16 query heads on
 // 8): 481 us a CTA to a tile (the tensor pipe active 42 % of the time, instructions
-// issued in 56 % of the cycles), 430 us, 0.82 PFLOP/s, with units; 5000 tokens after 7001, in pairs: 320 us, 1.20.
+// issued in 56 % of the cycles), 427 us, 0.83 PFLOP/s, in units; 5000 tokens after
+// 7001, in pairs: 320 us, 1.20.
 // Measured and not kept, on these two, each beside what the kernel then took: two
 // issuing warps, one for each head (528 and 427 beside 480 and 376: the products of
 // both mix); no maximum of a tile's logits unless their sum is out of range (506
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 //                the last output; its first product with V waits until they have
 //                read the accumulators
 // Outputs leave from registers, 32 bytes a store (the staging area is the queries').
-// 128 prompts of 64..512 tokens on a shared prefix of 1024: 480 -> 430 us; 64 of 384
+// 128 prompts of 64..512 tokens on a shared prefix of 1024: 480 -> 427 us; 64 of 384
 // on 1024 308 -> 290, 16 of 512..1024 on 2048 281 -> 275.
 constexpr int kMaxListSeqs = 256, kMaxList = 700, kMaxLevels = 32;  // sequences, tiles, tiles of a sequence
 constexpr int kDescs = 4;  // units under way between the loader and the last epilogue
