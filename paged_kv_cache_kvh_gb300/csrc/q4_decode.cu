@@ -641,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           sts32(kst + tile + word, new_codes);
           if (tt == 0) sts32(kst + tile + q4_param(tok, j), new_par);
         }
+        fence_proxy_async_smem();  // the stage's next copy comes after these stores
         __syncwarp();
       }
       if (flags & kFirst) {
@@ -770,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
           sts32(tile + q4_v_word(tok, j, tt), new_codes);
           if (tt == 0) sts32(tile + q4_param(tok, j), new_par);
         }
+        fence_proxy_async_smem();
         __syncwarp();
       }
 
