@@ -381,7 +381,10 @@ int pkv_load_kvcache_q4_f16(const void* k_cache, const void* v_cache, const int3
  *         first use and used for these calls only, always with the same
  *         workspace_bytes; every call leaves it ready for the next one, of any
  *         sizes and head counts that it is large enough for. Calls that share
- *         it (two captured graphs, say) must not overlap in time.
+ *         it (two captured graphs, say) must not overlap in time. The exception
+ *         is a call that sets PKV_DEVERR_TIMEOUT: it leaves the workspace marked,
+ *         and later calls on it write nothing and set PKV_DEVERR_TIMEOUT again
+ *         until it has been zero-filled once more.
  * How a sequence is split over the GPU follows from the call's context lengths
  * alone, and the partial results are joined in chunk order, so equal calls give
  * equal bits.

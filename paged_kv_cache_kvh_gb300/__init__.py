@@ -511,7 +511,8 @@ def pkv_decode_q4_workspace_bytes(num_seqs: int, max_context_len: int, num_heads
 
 def decode_q4_workspace(num_seqs: int, max_context_len: int, num_heads: int = NUM_HEADS,
                         num_kv_heads: int = NUM_KV_HEADS, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace for pkv_decode_q4 (allocated by torch, outside the library)."""
+    """A zero-filled workspace for pkv_decode_q4 (allocated by torch, outside the library). After
+    PKV_DEVERR_TIMEOUT it has to be zero-filled again: until then calls on it write nothing and report that error."""
     n = pkv_decode_q4_workspace_bytes(num_seqs, max_context_len, num_heads, num_kv_heads)
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
 

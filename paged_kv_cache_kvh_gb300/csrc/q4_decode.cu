@@ -85,6 +85,7 @@ constexpr int kMaxSeqs = 768;                                // sequences per la
 constexpr int kClasses = 8;                                  // sizes that short chunks are sorted into
 constexpr int kFan = 16;                                     // chunks merged at once
 constexpr int kFirst = 1 << 8, kLast = 1 << 9, kNew = 1 << 10;  // a unit's flags: first and last of its item, holds a new row
+constexpr int kSpoilt = INT32_MIN;                           // see the end of the kernel
 constexpr uint32_t kTf32Mask = 0xffffe000u;                  // the bits that a tf32 operand keeps
 constexpr uint32_t kOne = 0x3f800000u;                       // 1.0f
 
@@ -117,7 +118,7 @@ struct Q4DecodeParams {
   int32_t num_seqs;
   float scale_log2;
   uint16_t* out;
-  int32_t* work;     // {next item, warps done}, zero between calls
+  int32_t* work;     // {next item, warps done}, zero between calls; kSpoilt in the latter after a wait that ran out
   int32_t* tickets;  // one per slot, zero between calls
   float2* ml;        // [slot][G] (max in log2 units, sum)
   float* opart;      // [slot][G][128], not normalised; slot (whole chunks before b + b + chunk) * hkv + head
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.num_seqs;
   const int n_ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const bool spoilt = __ldcg(p.work + 1) < 0;  // (on its way together with the lengths)
 
   // ---- item table (every CTA builds the same one) ----
   // Whole chunks first, in sequence order, then the short last chunks in kClasses
@@ -445,6 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
     }
     if (tid == 0) sF[B] = n_full;
     __syncthreads();
+  }
+  if (spoilt) {
+    if (tid == 0 && cta == 0) flag_error(p.err, PKV_DEVERR_TIMEOUT);
+    return;
   }
   const int64_t n_items = static_cast<int64_t>(n_full + n_part) * p.rows;
   if (static_cast<int64_t>(n_full + B) * p.rows > p.max_slots) {  // cannot happen: the workspace bound covers every table
@@ -1012,8 +1018,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const Q4DecodePa
     pend_head = head;
     pend_c = it.z;
   }
-  // only after a wait that ran out: never leave a copy in flight into this CTA's shared memory
+  // Only after a wait that ran out: never leave a copy in flight into this CTA's shared
+  // memory. Tickets that this warp should have taken are missing, so a later call would
+  // merge too early: the workspace is marked, and calls refuse it until it is zero-filled.
   if (done < issued) {
+    if (lane == 0) atomicOr(p.work + 1, kSpoilt);
     mbar_wait(v_full, done & 1, p.err);
     for (; done < issued; ++done) mbar_wait(k_full + 8 * (done & 1), (done >> 1) & 1, p.err);
   }
