@@ -395,10 +395,8 @@ def _raw_stream(stream, dev):
 
 
 def _made(make, shape, dtype, device, stream):
-    """A tensor that a call returns, made (and filled) on the stream that the call runs on: a fill on the current
-    stream could run after the call, and memory from its pool could still be in use there."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
+    """A tensor that a call with stream= returns, made (and filled) on that stream: a fill on the current one could run
+    after the call, and memory from its pool could still be in use there."""
     here = torch.cuda.current_stream()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_raw_stream(stream, None), device)
@@ -477,11 +475,13 @@ def _load_q4(entry, dtype, k_cache, v_cache, slot_mapping, k, v, stream):
     n = slot_mapping.numel()
     shape = (n, hkv, HEAD_DIM)
     if k is None:
-        k = _made(torch.zeros, shape, dtype, k_cache.device, stream)
+        k = (torch.zeros(shape, dtype=dtype, device=k_cache.device) if stream is None
+             else _made(torch.zeros, shape, dtype, k_cache.device, stream))
     else:
         _dense(k, dev, dtype, shape, "k")
     if v is None:
-        v = _made(torch.zeros, shape, dtype, k_cache.device, stream)
+        v = (torch.zeros(shape, dtype=dtype, device=k_cache.device) if stream is None
+             else _made(torch.zeros, shape, dtype, k_cache.device, stream))
     else:
         _dense(v, dev, dtype, shape, "v")
     status = entry(k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hkv, HEAD_DIM, BLOCK_SIZE,
@@ -541,7 +541,8 @@ def _decode_q4(entry, dtype, q, new, k_cache, v_cache, block_tables, context_len
             raise ValueError(f"k and v must have the caches' {hkv} heads")
         rows = (k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr())
     if out is None:
-        out = _made(torch.empty, q.shape, dtype, q.device, stream)
+        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+               else _made(torch.empty, q.shape, dtype, q.device, stream))
     else:
         _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
     status = entry(q.data_ptr(), qs, *rows, k_cache.data_ptr(), v_cache.data_ptr(), blocks, block_tables.data_ptr(),
@@ -600,7 +601,8 @@ def _prefill_q4(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_s
         _table(plan, dev, "plan (pkv_prefill_plan)")
         items, n_items = plan.data_ptr(), plan.numel()
     if out is None:
-        out = _made(torch.empty, q.shape, dtype, q.device, stream)
+        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+               else _made(torch.empty, q.shape, dtype, q.device, stream))
     else:
         _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
     status = entry(q.data_ptr(), qs, total_q, k_cache.data_ptr(), v_cache.data_ptr(), blocks, cu_seqlens_q.data_ptr(),

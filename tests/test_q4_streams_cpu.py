@@ -9,11 +9,11 @@ import torch
 class Recorder:
     def __init__(self, monkeypatch, m):
         self.steps, self.stream = [], "current"
-        real = {name: getattr(torch, name) for name in ("zeros", "empty")}
+        real = {name: getattr(torch, name) for name in ("zeros", "empty", "empty_like")}
 
         def maker(name):
             def make(*a, **kw):
-                self.steps.append((name, self.stream))
+                self.steps.append((name.removesuffix("_like"), self.stream))
                 return real[name](*a, **kw)
             return make
 
