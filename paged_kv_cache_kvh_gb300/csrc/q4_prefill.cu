@@ -128,6 +128,7 @@ struct Q4PrefillParams {
   int32_t hkv;
   float scale_log2;
   const int32_t* items;  // optional tile plan: (qt << 16) | b per item; NULL: all pairs
+  int32_t num_items;
   int32_t first;         // the launch's first work item (query tiles x pairs of heads)
   int32_t by_twos;       // items in the order of pairs of neighbouring query tiles (no plan then)
   uint16_t* out;
@@ -873,9 +874,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // One CTA to a tile spends about 5.4 us on each beside its key tiles: 3 us until the
 // first logits, 1.8 of epilogue, 0.6 between two CTAs. Here one CTA per SM goes
-// through units (a query tile and two heads) k * SMs + its index of a list, longest
-// tiles first, that every CTA builds from the lengths, and the roles run on from
-// one unit to the next:
+// through units (a query tile and two heads) k * SMs + its index of a list, a plan's
+// or else longest tiles first, that every CTA builds from the lengths, and the roles
+// run on from one unit to the next:
 //   warp 0       describes the units (kDescs of them are under way at most) and
 //                loads a unit's queries as soon as the last one's logits are done
 //   warps 12-19  widen the next unit's first tiles while the last products run
@@ -908,7 +909,9 @@ static_assert(kUNumBars <= 32, "barriers");
 constexpr size_t kUnitsSmemBytes = kOffBar + sizeof(UnitsShared) + 1024;
 static_assert(kUnitsSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
-template <Elem E>
+// kPlan: the list is a plan's (a form of its own: with both in one, calls without a
+// plan took 429 us where they take 424).
+template <Elem E, bool kPlan>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_units_kernel(const __grid_constant__ CUtensorMap tm_q, const Q4PrefillParams p) {
   using Ops = ElemOps<E>;
@@ -957,7 +960,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     int n = 0;
-    for (int qt = p.max_q_tiles - 1; qt >= 0; --qt) {
+    if constexpr (kPlan) {
+      // a plan's tiles, in its order; what it names beyond a sequence's end is left out
+      uint8_t* tiles_of = smem_raw + (sbase - raw_addr) + kOffKV;  // (the ring is not in use yet)
+#pragma unroll
+      for (int i = 0; i < kMaxListSeqs / 32; ++i) tiles_of[i * 32 + lane] = static_cast<uint8_t>(tiles[i]);
+      __syncwarp();
+      constexpr int kAhead = 8;
+      for (int i0 = 0; i0 < p.num_items; i0 += 32 * kAhead) {
+        int code[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) code[k] = p.items[min(i0 + 32 * k + lane, p.num_items - 1)];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int qt = code[k] >> 16, b = code[k] & 0xffff;
+          const bool strange = qt < 0 || b >= p.num_seqs;  // a plan for other cu_seqlens
+          if (strange && blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+          const bool take = i0 + 32 * k + lane < p.num_items && !strange && qt < tiles_of[b];
+          const uint32_t live = __ballot_sync(0xffffffffu, take);
+          if (take) sh->list[n + __popc(live & ((1u << lane) - 1u))] = static_cast<uint16_t>(qt * kMaxListSeqs + b);
+          n += __popc(live);
+        }
+      }
+    }
+    for (int qt = kPlan ? -1 : p.max_q_tiles - 1; qt >= 0; --qt) {
 #pragma unroll
       for (int i = 0; i < kMaxListSeqs / 32; ++i) {
         const uint32_t live = __ballot_sync(0xffffffffu, tiles[i] > qt);
@@ -1296,7 +1322,9 @@ cudaError_t device_limits(DeviceLimits* out) {
   DeviceLimits d{};
   if ((e = allow_smem<E, Share::kWhole>()) != cudaSuccess || (e = allow_smem<E, Share::kSplitKeys>()) != cudaSuccess ||
       (e = allow_smem<E, Share::kPaired>()) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(prefill_q4_units_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      (e = cudaFuncSetAttribute(prefill_q4_units_kernel<E, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kUnitsSmemBytes))) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(prefill_q4_units_kernel<E, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kUnitsSmemBytes))) != cudaSuccess)
     return e;
   if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -1369,8 +1397,11 @@ cudaError_t launch_typed(const CUtensorMap& tq, Q4PrefillParams& p, int64_t n_it
   p.first = 0;
   p.by_twos = paired;
   if (!paired && shift == 0 && rounds >= kUnitRounds && p.num_seqs <= kMaxListSeqs && p.max_q_tiles <= kMaxLevels &&
-      p.total_q / kBM + p.num_seqs <= kMaxList && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
-    prefill_q4_units_kernel<E><<<d.sms, kThreads, kUnitsSmemBytes, stream>>>(tq, p);
+      (p.items ? p.num_items : p.total_q / kBM + p.num_seqs) <= kMaxList && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+    if (p.items)
+      prefill_q4_units_kernel<E, true><<<d.sms, kThreads, kUnitsSmemBytes, stream>>>(tq, p);
+    else
+      prefill_q4_units_kernel<E, false><<<d.sms, kThreads, kUnitsSmemBytes, stream>>>(tq, p);
     return cudaGetLastError();
   }
   if (whole > 0 && paired) {
@@ -1416,6 +1447,7 @@ cudaError_t launch_prefill_q4(const void* q, int64_t q_row_stride, int32_t total
   p.hkv = hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.items = num_items > 0 ? items : nullptr;
+  p.num_items = num_items;
   p.out = static_cast<uint16_t*>(out);
   p.err = err;
   const int64_t pairs = hq / 2;
