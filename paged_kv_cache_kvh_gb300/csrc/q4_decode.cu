@@ -60,6 +60,7 @@
 // shifts as multiplications (166), bf16 queries as two e4m3 parts against codes that
 // are e4m3 numbers as they stand (183: fewer instructions, but spills and longer
 // chains).
+#include <atomic>
 #include <type_traits>
 
 #include "q4.cuh"
@@ -1047,16 +1048,16 @@ static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory above the 227 KB a C
 
 template <Elem E, int G>
 cudaError_t launch_typed(const Q4DecodeParams& p, cudaStream_t stream) {
-  static int sm_count[64] = {0};  // 0: this device's attributes are not set yet
+  static std::atomic<int> sm_count[64];  // 0: this device's attributes are not set yet
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64) sms = sm_count[dev];
+  if (dev >= 0 && dev < 64) sms = sm_count[dev].load(std::memory_order_acquire);
   if (sms == 0) {
     const cudaError_t e = cudaFuncSetAttribute(q4_decode_kernel<E, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<G>()));
     if (e != cudaSuccess) return e;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
-    if (dev >= 0 && dev < 64) sm_count[dev] = sms;
+    if (dev >= 0 && dev < 64) sm_count[dev].store(sms, std::memory_order_release);
   }
   q4_decode_kernel<E, G><<<sms, kWarps * 32, smem_bytes<G>(), stream>>>(p);
   return cudaGetLastError();

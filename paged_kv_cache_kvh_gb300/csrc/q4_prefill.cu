@@ -76,6 +76,7 @@
 // prefill.cu.
 #include <cuda.h>
 
+#include <atomic>
 #include <climits>
 #include <mutex>
 #include <type_traits>
@@ -1250,14 +1251,15 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
+  static std::atomic<EncodeTiledFn> known;
+  EncodeTiledFn fn = known.load(std::memory_order_acquire);
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
             cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+      known.store(fn = reinterpret_cast<EncodeTiledFn>(ptr), std::memory_order_release);
   }
   return fn;
 }
