@@ -618,7 +618,8 @@ def pkv_prefill_varlen_q4(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
                           block_tables, *, out=None, plan=None, stream=None):
     """pkv_prefill_varlen in prefix-cache mode over the 4-bit cache (new tokens stored first).
     q [total_q, num_heads, 128] bf16, an even number of query heads to a kv head; plan: optional tile plan
-    (pkv_prefill_plan). Returns out [total_q, num_heads, 128] bf16."""
+    (pkv_prefill_plan), for batches of widely different lengths: long prompts of like lengths are faster without.
+    Returns out [total_q, num_heads, 128] bf16."""
     return _prefill_q4(_lib.pkv_prefill_varlen_q4, torch.bfloat16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                        max_seqlen_k, softmax_scale, k_cache, v_cache, block_tables, out, plan, stream)
 

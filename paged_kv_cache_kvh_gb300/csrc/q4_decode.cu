@@ -49,8 +49,8 @@
 // The fused step quantises a sequence's new row in the warps that read its last
 // tile, which put it over what was fetched; one of them writes it to the cache.
 //
-// Measured: 256 sequences of 512..4096 tokens, 16 query heads on 8: 141 us,
-// 5.4 TB/s (80 % of the copy rate); 512 of 800 on average, fp16: 101 us, 76 %; one of
+// Measured: 256 sequences of 512..4096 tokens, 16 query heads on 8: 139 us,
+// 5.5 TB/s (81 % of the copy rate); 512 of 800 on average, fp16: 101 us, 76 %; one of
 // 40007, 32 on 8: 31 us. With every block table folded onto a few blocks that
 // stay in L2 the first takes the same time: it is bound by execution, about 512
 // warp instructions per 32 tokens and pair of heads at 0.48 a clock and scheduler.

@@ -38,9 +38,13 @@
 // masked or not (0 * NaN). The first such position of each group is kept instead,
 // and rows at or past it get NaN in the epilogue.
 //
-// Registers: 640 threads x 96 at launch, split over the warpgroups by what each
-// needs without spilling in its loop (shared memory leaves no L1 for local memory:
-// the first form, which spilled there, took 904 us where this takes 481).
+// Registers: 640 threads x 96 at launch, split over the warpgroups so that as little
+// as possible spills (shared memory leaves no L1 for local memory: the first form,
+// which spilled in its loops, took 904 us where this takes 481). What the compiler
+// still spills: 20 bytes in the bf16 form whose keys are split, 8 in the fp16 form of
+// many short tiles, nothing in the others. Other splits of those two were no better:
+// 152 registers for the softmax, as bf16 has, in the latter (36 bytes; 128 prompts on
+// a prefix 474 -> 512 us) and in the former (28 bytes; 512 on 16384 85 -> 86 us).
 //
 // A tile's start is a chain of loads: lengths, block, codes, first widening, first
 // product, about 3 us in all beside 0.6 us between two CTAs and 1.8 us of epilogue.
@@ -63,7 +67,7 @@
 // peak. 128 prompts of 64..512 tokens on a shared prefix of 1024 (16 query heads on
 // 8): 481 us a CTA to a tile (the tensor pipe active 42 % of the time, instructions
 // issued in 56 % of the cycles), 427 us, 0.83 PFLOP/s, in units; 5000 tokens after
-// 7001, in pairs: 320 us, 1.20.
+// 7001, in pairs, replayed from a graph: 321 us, 1.21 PFLOP/s (fp16 315).
 // Measured and not kept, on these two, each beside what the kernel then took: two
 // issuing warps, one for each head (528 and 427 beside 480 and 376: the products of
 // both mix); no maximum of a tile's logits unless their sum is out of range (506
@@ -325,7 +329,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool firs
   const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
   const float neg_m = kMayMiss && m_use == -INFINITY ? 0.f : -m_use;  // a part may begin with keys that a row can't see
   const uint64_t negm2 = f32x2_pack(neg_m, neg_m);
-  // P = 2^(s*sl2 - m_use), rounded to the element type, over the logits in TMEM
+  // P = 2^(s*sl2 - m_use), rounded to fp16 (for either type of rows), over the logits in TMEM
   uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -1364,14 +1368,24 @@ cudaError_t device_limits(DeviceLimits* out) {
 // kUnitRounds rounds of items and more go to the kernel that takes them in units, if
 // its list holds them (its stores need 32-byte aligned rows): 29 of 100..1024 94 ->
 // 83 us, 200 of 64 on 300 135 -> 108, 40 of 1..400 on 500 96 -> 87; on fewer rounds
-// its fixed shares are uneven (4 of 2048 83 -> 97).
+// its fixed shares are uneven (4 of 2048 83 -> 97). Without a plan the items are all
+// places up to the longest sequence, empty ones among them, of which each costs the
+// other forms a CTA: one of 4096 beside 20 of 10 120 -> 112 us (of 1 on 2000: 178 ->
+// 145), one of 1024 beside 255 of 1, all on 1000, 433 -> 304. Full rounds behind long
+// keys gain nothing (48 of 400 on 2000 494 in either form, 200 of 100 on 2000 470 ->
+// 477) or lose (64 of 200 on 4096 549 -> 578, 100 of 300 on 4096 1269 -> 1322); what
+// is left over after them, if its keys are split, keeps them from units (128 of 300 on
+// 4096 1644, in units 1695).
 //
 // Pairs of CTAs widen half as much each, 15 % of the time on long keys: one prompt
 // of 8192 259 -> 224 us, 16 of 1024 on 4096 589 -> 507, 5000 on 7001 382 -> 329.
 // On short ones setting two CTAs up together costs more (8 of 1024 on 1024 124 ->
 // 125, 16 of 1024 109 -> 126), and an odd number of tiles leaves one CTA idle
 // (32 of 300 on 8192 790 -> 862, 16 of 512..1024 on 2048 286 -> 302): so only where
-// sequences have kPairTiles query tiles on average and kPairKeyTiles key tiles.
+// sequences have kPairTiles query tiles on average and kPairKeyTiles key tiles. A
+// plan's items are not paired (5000 on 7001 321 us without a plan, 356 with one), but it
+// leaves out the empty places (one of 4096 beside 20 of 10 112 -> 77 us, one of 8192
+// beside 31 of 1 on 2000 437 -> 312).
 template <Elem E>
 cudaError_t launch_typed(const CUtensorMap& tq, Q4PrefillParams& p, int64_t n_items, int32_t prefix_tiles,
                          cudaStream_t stream) {
