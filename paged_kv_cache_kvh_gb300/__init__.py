@@ -399,7 +399,8 @@ def _made(make, shape, dtype, device, stream):
     after the call, and memory from its pool could still be in use there."""
     here = torch.cuda.current_stream()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_raw_stream(stream, None), device)
+        handle = _raw_stream(stream, None)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device)  # cudaStreamLegacy: torch's default
     with torch.cuda.stream(stream):
         t = make(shape, dtype=dtype, device=device)
     t.record_stream(here)

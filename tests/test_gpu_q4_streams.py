@@ -106,3 +106,18 @@ def test_load_in_a_graph_forked_to_another_stream(pkv):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_raw_handles_of_the_default_streams(pkv):
+    """0 and cudaStreamLegacy (1) are torch's default stream, 2 is the thread's own; tensors made by the call."""
+    k = W.normal_bf16((300, 8, 128), W.make_generator(35, "cuda"), "cuda")
+    kc, vc = pkv.q4_cache(2), pkv.q4_cache(2)
+    slots = torch.arange(300, dtype=torch.int32, device="cuda")
+    pkv.pkv_store_kvcache_q4(k, k, kc, vc, slots)
+    want = pkv.pkv_load_kvcache_q4(kc, vc, slots)
+    torch.cuda.synchronize()
+    for handle in (0, 1, 2, torch.cuda.current_stream()):
+        got = pkv.pkv_load_kvcache_q4(kc, vc, slots, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert pkv.pkv_device_error() == 0

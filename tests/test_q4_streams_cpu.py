@@ -75,10 +75,11 @@ def prefill(m, rec, **kw):
 def test_returned_tensors_are_made_on_the_calls_stream(monkeypatch, m, call):
     rec = Recorder(monkeypatch, m)
     made = ["zeros", "zeros"] if call is load else ["empty"]
-    for stream in (rec.Stream(77), 77):                             # a torch stream, a raw handle
+    # a torch stream, a raw handle, the default stream by either of its handles
+    for stream, on, launched in ((rec.Stream(77), 77, 77), (77, 77, 77), (0, 0, 0), (1, 0, 1)):
         call(m, rec, stream=stream)
-        want = [x for name in made for x in ((name, 77), ("kept for", "here"))]
-        assert rec.steps == want + [("launch", 77)]
+        want = [x for name in made for x in ((name, on), ("kept for", "here"))]
+        assert rec.steps == want + [("launch", launched)]
     call(m, rec, stream=None)
     assert rec.steps == [(name, "current") for name in made] + [("launch", "current")]
 
