@@ -464,6 +464,85 @@ size_t pkv_decode_q4_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_
                                      int32_t max_context_len);
 
 /*
+ * ---- Rotary positions ----
+ *
+ * The pages rotate q and k by their positions before the attention block
+ * (get_rope in layers/rotary_embedding.py, theta 1e6). These calls do that step,
+ * alone or together with store_kvcache of the same rows.
+ *
+ * pkv_rope_frequencies -- host-side, once per model: the angle that each of the
+ * rotary_dim/2 pairs of a head turns per position, f_i = theta^(-2i/rotary_dim)
+ * radians and what a scaling makes of it for longer contexts:
+ *   PKV_ROPE_NONE    f_i
+ *   PKV_ROPE_LINEAR  f_i / factor
+ *   PKV_ROPE_NTK     theta * factor^(r/(r-2)) in theta's place (r = rotary_dim; r = 2: as PKV_ROPE_NONE)
+ *   PKV_ROPE_BANDS   g f_i + (1 - g) f_i / factor, with g = (turns over
+ *                    original_max_position - a) / (b - a) clamped to 0..1
+ *                    (a, b: the low and high frequency factors, 1 and 4 for instance)
+ *   PKV_ROPE_YARN    (1 - g) f_i + g f_i / factor, g rising from 0 to 1 between the pairs that turn a and b times over
+ *                    original_max_position (a = 32, b = 1 for instance; the pairs' numbers rounded down and up and
+ *                    clamped to 0..r-1), and *h_magnitude = 0.1 ln(factor) + 1
+ * h_freqs: [rotary_dim/2] int64 on the host, f_i in units of 2^-64 full turns per
+ * position (rounded towards zero): position * f_i modulo 2^64 is the exact
+ * fraction of a turn. *h_magnitude: what turned values are multiplied by (1 but for
+ * PKV_ROPE_YARN). Arguments that a scaling does not use are ignored. Returns PKV_OK, PKV_ERR_NULL_POINTER,
+ * PKV_ERR_UNSUPPORTED (rotary_dim odd, below 2 or above 1024; no such scaling) or
+ * PKV_ERR_BAD_SIZE (theta <= 1, factor < 1, original_max_position < 1, a >= b (BANDS) or a <= b or b <= 0 (YARN), or
+ * values that are not finite).
+ */
+#define PKV_ROPE_NONE 0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_NTK 2
+#define PKV_ROPE_BANDS 3
+#define PKV_ROPE_YARN 4
+int pkv_rope_frequencies(int32_t rotary_dim, double theta, int32_t scaling, double factor,
+                         double original_max_position, double a, double b, int64_t* h_freqs, float* h_magnitude);
+
+/*
+ * pkv_rope -- turns the first rotary_dim elements of every head of q and k by the
+ * row's position; the others are copied. Pair i is elements i and i + rotary_dim/2,
+ * or, interleaved, 2i and 2i + 1:
+ *   a' = (a cos - b sin) * magnitude,  b' = (b cos + a sin) * magnitude
+ * in fp32, rounded once.
+ *   q, k          [num_tokens, num_heads | num_kv_heads, head_dim], heads and dims
+ *                 contiguous, rows *_row_stride elements apart (views of a fused qkv
+ *                 are fine). One of the two head counts may be 0.
+ *   positions     [num_tokens] int64, any values (negative ones turn backwards).
+ *   freqs         [rotary_dim/2] int64 on the device (pkv_rope_frequencies).
+ *   q_out, k_out  as q and k; may be the same rows (in place), else must not overlap them.
+ * head_dim up to 1024, rotary_dim even and at most head_dim. 16-byte vectors where
+ * pointers are 16-byte aligned, strides multiples of 8 and head_dim and rotary_dim
+ * multiples of 16; any 2-byte alignment otherwise.
+ */
+int pkv_rope(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const int64_t* positions,
+             const int64_t* freqs, int32_t rotary_dim, float magnitude, int32_t interleaved, int32_t num_tokens,
+             int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_row_stride,
+             void* k_out, int64_t k_out_row_stride, cudaStream_t stream);
+int pkv_rope_f16(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const int64_t* positions,
+                 const int64_t* freqs, int32_t rotary_dim, float magnitude, int32_t interleaved, int32_t num_tokens,
+                 int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_row_stride,
+                 void* k_out, int64_t k_out_row_stride, cudaStream_t stream);
+
+/*
+ * pkv_rope_store_kvcache -- pkv_rope of q and k, then pkv_store_kvcache of the
+ * turned k and of v, in one launch and with the same results: k is turned on its
+ * way to its slot and not written anywhere else. Slots, caches and their errors
+ * are as for pkv_store_kvcache (a row with slot -1 only has its q turned).
+ *   v  [num_tokens, num_kv_heads, head_dim], rows v_row_stride elements apart.
+ */
+int pkv_rope_store_kvcache(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                           int64_t v_row_stride, const int64_t* positions, const int64_t* freqs, int32_t rotary_dim,
+                           float magnitude, int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                           int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int64_t num_slots, void* q_out,
+                           int64_t q_out_row_stride, void* k_cache, void* v_cache, cudaStream_t stream);
+int pkv_rope_store_kvcache_f16(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                               int64_t v_row_stride, const int64_t* positions, const int64_t* freqs,
+                               int32_t rotary_dim, float magnitude, int32_t interleaved, const int32_t* slot_mapping,
+                               int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int64_t num_slots, void* q_out, int64_t q_out_row_stride, void* k_cache, void* v_cache,
+                               cudaStream_t stream);
+
+/*
  * pkv_build_prefill_metadata / pkv_build_decode_metadata -- the per-step index
  * preparation of engine/model_runner.py (prepare_prefill, prepare_decode in
  * "vLLM 学习笔记 02：nano-vllm 源码逐段精读"; worked example in

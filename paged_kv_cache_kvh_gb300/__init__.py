@@ -43,8 +43,8 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libpkv.so is not built ({LIB_PATH}); run python paged_kv_cache_kvh_gb300/build_lib.py")
 
 _lib = ctypes.CDLL(LIB_PATH)
-_i32, _i64, _u64, _vp, _f32, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p,
-                                     ctypes.c_float, ctypes.c_size_t)
+_i32, _i64, _u64, _vp, _f32, _f64, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p,
+                                           ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
 _SIGNATURES = {
     "pkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "pkv_version": (ctypes.c_int, []),
@@ -75,7 +75,14 @@ _SIGNATURES = {
     "pkv_selftest_wait_timeout": (ctypes.c_int, [_u64, _vp]),
     "pkv_decode_q4_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
 }
+_SIGNATURES["pkv_rope_frequencies"] = (ctypes.c_int, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp])
 for _suffix in ("", "_f16"):
+    _SIGNATURES["pkv_rope" + _suffix] = (
+        ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _f32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
+                       _vp])
+    _SIGNATURES["pkv_rope_store_kvcache" + _suffix] = (
+        ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _f32, _i32, _vp, _i32, _i32, _i32, _i32, _i64,
+                       _vp, _i64, _vp, _vp, _vp])
     _SIGNATURES["pkv_store_kvcache_q4" + _suffix] = (
         ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp])
     _SIGNATURES["pkv_load_kvcache_q4" + _suffix] = (
@@ -669,6 +676,141 @@ def pkv_build_decode_metadata(num_tokens, block_tables, num_blocks, stream=None)
                                           int(num_blocks), B, _ptr(out["slot_mapping"]), _ptr(out["context_lens"]),
                                           _ptr(out["positions"]), _stream(stream)), "pkv_build_decode_metadata")
     return out
+
+
+# ---- rotary positions ----------------------------------------------------------------
+
+ROPE_SCALINGS = ("none", "linear", "ntk", "bands", "yarn")  # the PKV_ROPE_* codes in order
+
+
+def rope_frequencies(rotary_dim: int = HEAD_DIM, theta: float = 1e6, scaling: str = "none", *, factor: float = 1.0,
+                     original_max_position: float = 0.0, ramp=None, device="cuda"):
+    """What pkv_rope needs once per model: (freqs, magnitude), freqs an int64 tensor [rotary_dim/2] on `device` (numpy
+    if None) of turns per position in units of 2^-64, magnitude the factor of the turned values. `scaling` stretches the
+    frequencies for longer contexts by `factor`: "linear" all of them, "ntk" through theta, "bands" and "yarn" by how
+    often a pair turns over original_max_position, between the two values of `ramp` (by default (1, 4) and (32, 1)).
+    The formulas are in include/pkv.h."""
+    _need(scaling in ROPE_SCALINGS, f"scaling must be one of {ROPE_SCALINGS}")
+    _need(rotary_dim >= 2, "rotary_dim must be an even number of at least 2")
+    a, b = ramp if ramp is not None else ((32.0, 1.0) if scaling == "yarn" else (1.0, 4.0))
+    freqs, magnitude = np.empty(rotary_dim // 2, dtype=np.int64), ctypes.c_float()
+    _check(_lib.pkv_rope_frequencies(int(rotary_dim), float(theta), ROPE_SCALINGS.index(scaling), float(factor),
+                                     float(original_max_position), float(a), float(b), freqs.ctypes.data,
+                                     ctypes.addressof(magnitude)), "pkv_rope_frequencies")
+    return (freqs if device is None else torch.from_numpy(freqs).to(device)), magnitude.value
+
+
+def _head_rows(t, dev, dtype, name):
+    """Checks [N, heads, dims] rows and returns the three and the elements between rows (a single row may carry any
+    stride)."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {_TYPE_NAME[dtype]} CUDA tensor on the current device")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N, heads, dims]")
+    n, heads, dims = t.shape
+    row, head, dim = t.stride()
+    if (dim != 1 and dims > 1) or (head != dims and heads > 1):
+        raise ValueError(f"{name} must be [N, heads, dims] with heads and dims contiguous within a row")
+    return n, heads, dims, row if n > 1 else heads * dims
+
+
+def _i64_array(t, dev, name):
+    if t.dtype is not torch.int64 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int64 CUDA tensor on the current device")
+
+
+def _turned(t, out, dtype, dev, shape, name, stream):
+    """The rows that a turned tensor goes to, and the elements between them."""
+    if out is None:
+        out = (torch.empty_like(t, memory_format=torch.contiguous_format) if stream is None
+               else _made(torch.empty, t.shape, dtype, t.device, stream))
+        return out, shape[1] * shape[2]
+    n, heads, dims, row = _head_rows(out, dev, dtype, name)
+    if (n, heads, dims) != shape:
+        raise ValueError(f"{name} must have the shape of its input")
+    return out, row
+
+
+def _rope(entry, dtype, q, k, positions, freqs, magnitude, interleaved, q_out, k_out, stream):
+    dev = _current_device()
+    n, hq, dims, qs = _head_rows(q, dev, dtype, "q")
+    _i64_array(positions, dev, "positions")
+    _i64_array(freqs, dev, "freqs")
+    if positions.numel() != n:
+        raise ValueError("positions must have one entry per token")
+    hkv = ks = kos = 0
+    if k is not None:
+        kn, hkv, kd, ks = _head_rows(k, dev, dtype, "k")
+        if kn != n or kd != dims:
+            raise ValueError("q and k must have the same rows and dims")
+        k_out, kos = _turned(k, k_out, dtype, dev, (n, hkv, dims), "k_out", stream)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    q_out, qos = _turned(q, q_out, dtype, dev, (n, hq, dims), "q_out", stream)
+    status = entry(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, positions.data_ptr(), freqs.data_ptr(),
+                   2 * freqs.numel(), magnitude, interleaved, n, hq, hkv, dims, q_out.data_ptr(), qos,
+                   None if k is None else k_out.data_ptr(), kos, _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
+    return q_out, k_out
+
+
+def pkv_rope(q, k, positions, freqs, *, magnitude=1.0, interleaved=False, q_out=None, k_out=None, stream=None):
+    """Turns the first 2 * freqs.numel() dims of every head of bf16 q [N, heads, dims] and k (None: q alone) by the rows'
+    positions (int64 [N]): pairs (i, i + r/2), or (2i, 2i + 1) if interleaved. freqs, magnitude: rope_frequencies. Rows
+    may be strided; q_out and k_out may be q and k themselves. Returns (q_out, k_out)."""
+    return _rope(_lib.pkv_rope, torch.bfloat16, q, k, positions, freqs, magnitude, interleaved, q_out, k_out, stream)
+
+
+def pkv_rope_f16(q, k, positions, freqs, *, magnitude=1.0, interleaved=False, q_out=None, k_out=None, stream=None):
+    """pkv_rope of fp16 rows."""
+    return _rope(_lib.pkv_rope_f16, torch.float16, q, k, positions, freqs, magnitude, interleaved, q_out, k_out, stream)
+
+
+def _rope_store(entry, dtype, q, k, v, positions, freqs, k_cache, v_cache, slot_mapping, magnitude, interleaved, q_out,
+                stream):
+    dev = _current_device()
+    n, hq, dims, qs = _head_rows(q, dev, dtype, "q")
+    kn, hkv, kd, ks = _head_rows(k, dev, dtype, "k")
+    vn, vh, vd, vs = _head_rows(v, dev, dtype, "v")
+    if kn != n or vn != n or vh != hkv or kd != dims or vd != dims:
+        raise ValueError("q, k and v must have the same rows and dims, k and v the same heads")
+    _i64_array(positions, dev, "positions")
+    _i64_array(freqs, dev, "freqs")
+    _table(slot_mapping, dev, "slot_mapping")
+    if positions.numel() != n or slot_mapping.numel() != n:
+        raise ValueError("positions and slot_mapping must have one entry per token")
+    shape = k_cache.shape
+    if (k_cache.dtype is not dtype or v_cache.dtype is not dtype or v_cache.shape != shape
+            or k_cache.get_device() != dev or v_cache.get_device() != dev or shape[-2:] != (hkv, dims)
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError(f"k_cache and v_cache must be contiguous {_TYPE_NAME[dtype]} [..., {hkv}, {dims}] on the current "
+                         "CUDA device")
+    q_out, qos = _turned(q, q_out, dtype, dev, (n, hq, dims), "q_out", stream)
+    row = hkv * dims
+    status = entry(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), freqs.data_ptr(),
+                   2 * freqs.numel(), magnitude, interleaved, slot_mapping.data_ptr(), n, hq, hkv, dims,
+                   k_cache.numel() // row if row else 0, q_out.data_ptr(), qos, k_cache.data_ptr(), v_cache.data_ptr(),
+                   _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
+    return q_out
+
+
+def pkv_rope_store_kvcache(q, k, v, positions, freqs, k_cache, v_cache, slot_mapping, *, magnitude=1.0,
+                           interleaved=False, q_out=None, stream=None):
+    """pkv_rope of q and k with pkv_store_kvcache of the turned k and of v in the same launch; k itself is left as it is.
+    Returns q_out (q itself where q_out=q)."""
+    return _rope_store(_lib.pkv_rope_store_kvcache, torch.bfloat16, q, k, v, positions, freqs, k_cache, v_cache,
+                       slot_mapping, magnitude, interleaved, q_out, stream)
+
+
+def pkv_rope_store_kvcache_f16(q, k, v, positions, freqs, k_cache, v_cache, slot_mapping, *, magnitude=1.0,
+                               interleaved=False, q_out=None, stream=None):
+    """pkv_rope_store_kvcache of fp16 rows."""
+    return _rope_store(_lib.pkv_rope_store_kvcache_f16, torch.float16, q, k, v, positions, freqs, k_cache, v_cache,
+                       slot_mapping, magnitude, interleaved, q_out, stream)
+
 
 
 def pkv_device_error(clear: bool = True, stream=None) -> int:
