@@ -543,6 +543,58 @@ int pkv_rope_store_kvcache_f16(const void* q, int64_t q_row_stride, const void* 
                                cudaStream_t stream);
 
 /*
+ * ---- Attention with modified scores and masks ----
+ *
+ * The attention calls above take softmax(scale * q.k) over all keys up to the
+ * query's position. These take other scores and other sets of visible keys, for
+ * models that need them, over the same cache, for any head counts (num_heads a
+ * multiple of num_kv_heads, at most 8192). For a query at position p and a key at
+ * position t, in this order:
+ *   x = softmax_scale * q . k
+ *   x = softcap * tanh(x / softcap)          where softcap > 0 (0: no cap)
+ *   x = x - slopes[head] * |p - t|           where slopes != NULL ([num_heads] fp32, any values)
+ * and the key takes part where all of these hold:
+ *   t <= p, or t < prefix_lens[sequence]     (prefill, where prefix_lens != NULL: keys that every row sees)
+ *   t < length of the sequence
+ *   t >= key_starts[row]                     where key_starts != NULL (the first position of the row's document, say)
+ *   p - t < window                           where window > 0
+ * A row that sees no key gets zeros. Values at keys that take no part, infinities
+ * and NaN among them, reach no result. Arithmetic is fp32; products take the 16-bit rows as they are.
+ */
+
+/*
+ * pkv_decode_mod -- pkv_decode with the scores and masks above: one query row per
+ * sequence, at position context_lens[b] - 1. Arguments and errors as for pkv_decode but for
+ *   num_blocks  at most 2^23 - 1 (and not 0)
+ *   key_starts  [num_seqs] int32, or NULL
+ *   weights     NULL, or fp32 [num_blocks, num_kv_heads, 256]: each token's attention added up over the calls, beside
+ *         the cache. For every key that takes part, weights[slot / 256][kv head][slot % 256] += the sum over the kv
+ *         head's query heads of its softmax probability; the newest token's (position context_lens[b] - 1) starts
+ *         from 0 in this call, whatever was there. What a prompt's tokens start from is the caller's to fill in.
+ *         Sequences of one call must not share blocks then (their additions would race).
+ *   workspace  >= pkv_decode_mod_workspace_bytes(...) bytes, 16-byte aligned. It holds nothing between calls and needs
+ *         no initialisation; calls that share it must not overlap in time.
+ * How sequences are split over the GPU follows from the call's lengths alone, and partial results are joined in order,
+ * so equal calls give equal bits.
+ */
+int pkv_decode_mod(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                   const int32_t* block_tables, int32_t block_table_stride, const int32_t* context_lens,
+                   int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int32_t max_context_len, float softmax_scale, float softcap, const float* slopes, int32_t window,
+                   const int32_t* key_starts, float* weights, void* out, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+int pkv_decode_mod_f16(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
+                       int32_t num_blocks, const int32_t* block_tables, int32_t block_table_stride,
+                       const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale,
+                       float softcap, const float* slopes, int32_t window, const int32_t* key_starts, float* weights,
+                       void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes pkv_decode_mod(_f16) needs for these sizes, with weights (1) or without (0); 0 for sizes it refuses. */
+size_t pkv_decode_mod_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                      int32_t max_context_len, int32_t weights);
+
+/*
  * pkv_build_prefill_metadata / pkv_build_decode_metadata -- the per-step index
  * preparation of engine/model_runner.py (prepare_prefill, prepare_decode in
  * "vLLM 学习笔记 02：nano-vllm 源码逐段精读"; worked example in

@@ -76,7 +76,11 @@ _SIGNATURES = {
     "pkv_decode_q4_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
 }
 _SIGNATURES["pkv_rope_frequencies"] = (ctypes.c_int, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp])
+_SIGNATURES["pkv_decode_mod_workspace_bytes"] = (_sz, [_i32, _i32, _i32, _i32, _i32])
 for _suffix in ("", "_f16"):
+    _SIGNATURES["pkv_decode_mod" + _suffix] = (
+        ctypes.c_int, [_vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _vp,
+                       _i32, _vp, _vp, _vp, _vp, _sz, _vp])
     _SIGNATURES["pkv_rope" + _suffix] = (
         ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _f32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
                        _vp])
@@ -810,6 +814,114 @@ def pkv_rope_store_kvcache_f16(q, k, v, positions, freqs, k_cache, v_cache, slot
     """pkv_rope_store_kvcache of fp16 rows."""
     return _rope_store(_lib.pkv_rope_store_kvcache_f16, torch.float16, q, k, v, positions, freqs, k_cache, v_cache,
                        slot_mapping, magnitude, interleaved, q_out, stream)
+
+
+
+# ---- attention with modified scores and masks ------------------------------------------
+
+
+def _f32_array(t, dev, count, name):
+    """The pointer of an optional fp32 [count]."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of {count} on the current device")
+    return t.data_ptr()
+
+
+def _i32_optional(t, dev, count, name):
+    """The pointer of an optional int32 [count]."""
+    if t is None:
+        return None
+    _table(t, dev, name)
+    if t.numel() < count:
+        raise ValueError(f"{name} must have {count} entries")
+    return t.data_ptr()
+
+
+def _caches(k_cache, v_cache, dev, dtype):
+    """Checks the pair and returns (blocks, num_kv_heads)."""
+    shape = k_cache.shape
+    if (len(shape) != 4 or shape[1] != BLOCK_SIZE or shape[3] != HEAD_DIM or v_cache.shape != shape
+            or k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != dev
+            or v_cache.get_device() != dev or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError(f"k_cache and v_cache must be contiguous {_TYPE_NAME[dtype]} [blocks, 256, num_kv_heads, 128] on "
+                         "the current CUDA device")
+    return shape[0], shape[2]
+
+
+def _weight_pool(weights, dev, blocks, hkv):
+    if (weights.dtype is not torch.float32 or weights.get_device() != dev or weights.shape != (blocks, hkv, BLOCK_SIZE)
+            or not weights.is_contiguous()):
+        raise ValueError(f"weights must be contiguous fp32 [{blocks}, {hkv}, 256] on the current CUDA device")
+    return weights.data_ptr()
+
+
+def attention_weights(num_blocks: int, num_kv_heads: int = NUM_KV_HEADS, device="cuda") -> torch.Tensor:
+    """Zeros beside a cache of num_blocks blocks, fp32 [num_blocks, num_kv_heads, 256]: what pkv_decode_mod adds each
+    token's attention to and pkv_evict_kvcache goes by."""
+    return torch.zeros((num_blocks, num_kv_heads, BLOCK_SIZE), dtype=torch.float32, device=device)
+
+
+def pkv_decode_mod_workspace_bytes(num_seqs: int, max_context_len: int, num_heads: int = NUM_HEADS,
+                                   num_kv_heads: int = NUM_KV_HEADS, weights: bool = False) -> int:
+    return int(_lib.pkv_decode_mod_workspace_bytes(num_seqs, num_heads, num_kv_heads, max_context_len, int(weights)))
+
+
+def decode_mod_workspace(num_seqs: int, max_context_len: int, num_heads: int = NUM_HEADS,
+                         num_kv_heads: int = NUM_KV_HEADS, weights: bool = False, device="cuda") -> torch.Tensor:
+    """A workspace for pkv_decode_mod of up to these sizes (of these head counts; it holds nothing between calls).
+    weights: calls add attention up."""
+    n = pkv_decode_mod_workspace_bytes(num_seqs, max_context_len, num_heads, num_kv_heads, weights)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _decode_mod(entry, dtype, q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace,
+                softcap, slopes, window, key_starts, weights, out, stream):
+    dev = _current_device()
+    blocks, hkv = _caches(k_cache, v_cache, dev, dtype)
+    B, hq, qs = _rows_q4(q, dev, dtype, "q")
+    _table(block_tables, dev, "block_tables")
+    _table(context_lens, dev, "context_lens")
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] < B or context_lens.numel() < B:
+        raise ValueError("block_tables must be [B, width] and context_lens [B]")
+    if workspace.dtype is not _U8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the current CUDA device")
+    slopes = None if slopes is None else _f32_array(slopes, dev, hq, "slopes")
+    key_starts = None if key_starts is None else _i32_optional(key_starts, dev, B, "key_starts")
+    weights = None if weights is None else _weight_pool(weights, dev, blocks, hkv)
+    if out is None:
+        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+               else _made(torch.empty, q.shape, dtype, q.device, stream))
+    else:
+        _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
+    status = entry(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), blocks, block_tables.data_ptr(), tables[1],
+                   context_lens.data_ptr(), B, hq, hkv, HEAD_DIM, BLOCK_SIZE, int(max_context_len),
+                   float(softmax_scale), float(softcap), slopes, int(window), key_starts, weights, out.data_ptr(),
+                   workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
+    return out
+
+
+def pkv_decode_mod(q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace, *,
+                   softcap=0.0, slopes=None, window=0, key_starts=None, weights=None, out=None, stream=None):
+    """pkv_decode with modified scores and masks, for any head counts (caches [blocks, 256, num_kv_heads, 128]): scores
+    softcap * tanh(x / softcap) if softcap, then - slopes[head] * (p - t) for slopes fp32 [num_heads]; keys from
+    key_starts[b] (int32 [B]) on and, if window, the newest `window` of them. weights (attention_weights): each key's
+    probability is added up there. workspace: decode_mod_workspace. Returns out [B, num_heads, 128]."""
+    return _decode_mod(_lib.pkv_decode_mod, torch.bfloat16, q, k_cache, v_cache, block_tables, context_lens,
+                       max_context_len, softmax_scale, workspace, softcap, slopes, window, key_starts, weights, out,
+                       stream)
+
+
+def pkv_decode_mod_f16(q, k_cache, v_cache, block_tables, context_lens, max_context_len, softmax_scale, workspace, *,
+                       softcap=0.0, slopes=None, window=0, key_starts=None, weights=None, out=None, stream=None):
+    """pkv_decode_mod on fp16 tensors; returns fp16."""
+    return _decode_mod(_lib.pkv_decode_mod_f16, torch.float16, q, k_cache, v_cache, block_tables, context_lens,
+                       max_context_len, softmax_scale, workspace, softcap, slopes, window, key_starts, weights, out,
+                       stream)
 
 
 

@@ -1,0 +1,914 @@
+// decode_mod.cu -- single-query attention over the paged cache whose scores are capped, biased by distance or see a part
+// of the keys, for any head counts; and each key's attention added up beside it.
+//
+// For sequence b with p = context_lens[b] - 1, query head h, kv head h / G and every visible t (start_b <= t <= p and
+// p - t < window):
+//   x_t = scale * q . k_t;   s_t = cap * tanh(x_t / cap) (or x_t);   z_t = s_t - slope_h * (p - t)
+//   out = sum_t e^(z_t - m) v_t / sum_t e^(z_t - m),    weights[t] += sum over the G heads of a kv head of their share.
+//
+// What bounds it: 512 bytes of K and V per (token, kv head) from HBM. The products run on mma.sync m16n8k16 with the
+// tokens as rows: S^T = K Q^T for up to 8 query heads of a kv head at a time (their number changes nothing but the
+// columns in use), O^T += V^T P. tcgen05 would work on 128 rows of which a kv head has 1 to 16; as it is, the two
+// products of 16 tokens and one kv head are 24 instructions where HBM takes 380 clocks for their 8 KB. That leaves time
+// for exact arithmetic: p goes to the second product as two 16-bit parts (p and what its rounding lost), tanhf is CUDA's.
+//
+// Work: a warp is a worker of its own. Each (kv head, part of its query heads) is a stream; a stream's units, 16 tokens
+// of a sequence each, are laid end to end and cut into R equal ranges, so that every worker gets the same number of
+// bytes, whatever the lengths. Workers of one CTA take the same range of neighbouring heads: their rows lie side by
+// side. Every CTA derives the ranges from context_lens; nothing is kept from one call for the next. A worker's 16-token
+// units of K and of V come by TMA (two 128-byte halves of each row, 128-byte swizzle) into a ring of kStages of its
+// own, and it waits on its own barriers. The running maximum only moves when a score passes it by 2^8, so a step
+// needs one vote and no shuffles.
+// A sequence that ends inside the range in which it began is written out at once. For the others the workers leave
+// (max, sum, o) in the workspace and a second kernel joins them in order; with weights a third one turns the scores,
+// which the first left in the workspace, into shares. Equal calls give equal bits.
+#include <atomic>
+#include <cmath>
+#include <type_traits>
+
+#include <cuda.h>
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+struct DecodeModArgs {
+  const void* q;
+  int64_t q_row_stride;
+  const void* k_cache;
+  const void* v_cache;
+  int32_t num_blocks;
+  const int32_t* block_tables;
+  int32_t bt_stride;
+  const int32_t* context_lens;
+  int32_t num_seqs, hq, hkv, max_ctx;
+  float scale, softcap;
+  const float* slopes;
+  int32_t window;
+  const int32_t* key_starts;
+  float* weights;
+  void* out;
+  void* workspace;
+};
+
+namespace {
+
+constexpr int kUnit = 16;                           // tokens
+constexpr int kUnitBytes = kUnit * kHeadDim * 2;    // 4 KB, of K and of V each
+constexpr int kStages = 3;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCtas = 152;                          // one to an SM
+constexpr int kWorkers = kCtas * kWarps;
+constexpr int kMinUnits = 2;                        // units to a range at least
+constexpr int kOffBars = kWarps * kStages * 2 * kUnitBytes;
+constexpr int kOffScan = kOffBars + kWarps * kStages * 8;
+constexpr size_t kSmemBytes = kOffScan + (kThreads + kWarps + 1) * 8 + 1024;  // + alignment slack
+constexpr int kMergeWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// How a call's heads are cut into streams: parts of up to 8 or 16 query heads of one kv head.
+struct Streams {
+  int32_t group, per, parts, count, ranges;
+};
+Streams streams_of(int32_t hq, int32_t hkv) {
+  Streams s;
+  s.group = hq / hkv;
+  s.per = s.group <= 8 ? 8 : 16;
+  s.parts = (s.group + s.per - 1) / s.per;
+  s.count = hkv * s.parts;
+  s.ranges = s.count < kWorkers ? kWorkers / s.count : 1;
+  return s;
+}
+
+// Workspace: RangeInfo[1 + ranges] (the first holds the call's totals), (max, 1 / sum) per (sequence, query head),
+// partial (max, sum) and o per (range, stream, first or last sequence of the range, head of the part), and with weights
+// the scores per (sequence, unit, stream, head of the part, token).
+struct RangeInfo {
+  int64_t first_unit;  // of the sequence that begins in this range and goes on behind it
+  int64_t units;
+  int32_t seq;         // -1: none
+  int32_t ranges;      // entry 0: ranges in use
+};
+struct Layout {
+  size_t info, final_ml, ml, o, scores, total;
+};
+Layout layout_of(const Streams& s, int32_t num_seqs, int32_t hq, int32_t max_ctx, bool weights) {
+  Layout l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 127) / 128 * 128;
+    return here;
+  };
+  const size_t slots = static_cast<size_t>(s.ranges) * s.count * 2 * s.per;
+  l.info = take(sizeof(RangeInfo) * (1 + static_cast<size_t>(s.ranges)));
+  l.final_ml = take(weights ? sizeof(float2) * num_seqs * hq : 0);
+  l.ml = take(sizeof(float2) * slots);
+  l.o = take(sizeof(float) * kHeadDim * slots);
+  const size_t units = (static_cast<size_t>(max_ctx) + kUnit - 1) / kUnit;
+  l.scores = take(weights ? sizeof(float) * num_seqs * units * s.count * s.per * kUnit : 0);
+  l.total = at;
+  return l;
+}
+
+struct DecodeModParams {
+  const uint16_t* q;
+  int64_t q_row_stride;
+  const int32_t* block_tables;
+  int32_t bt_stride, num_blocks;
+  const int32_t* context_lens;
+  int32_t num_seqs, hq, hkv, max_ctx;
+  Streams st;
+  float scale_log2, cap_log2, scale_by_cap;  // cap_log2 == 0: no cap
+  const float* slopes;
+  int32_t window;
+  const int32_t* key_starts;
+  float* weights;
+  uint16_t* out;
+  RangeInfo* info;
+  float2* final_ml;
+  float2* ml;
+  float* o;
+  float* scores;
+  int64_t seq_units;  // units that `scores` holds per sequence
+  unsigned int* err;
+};
+
+// The visible tokens [lo, ctx) of a sequence; empty (0, 0) where there are none or the length is bad.
+__device__ __forceinline__ int2 visible(const DecodeModParams& p, int b, bool report) {
+  int ctx = p.context_lens[b];
+  int lo = p.key_starts ? max(p.key_starts[b], 0) : 0;
+  if (ctx < 0 || ctx > p.max_ctx || ctx > static_cast<int64_t>(p.bt_stride) * kBlockSize) {
+    if (report) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+    ctx = 0;
+  }
+  if (p.window > 0) lo = max(lo, ctx - p.window);
+  return lo < ctx ? make_int2(lo, ctx) : make_int2(0, 0);
+}
+__device__ __forceinline__ int units_of(int2 v) {
+  return v.y == 0 ? 0 : (v.y + kUnit - 1) / kUnit - v.x / kUnit;
+}
+__device__ __forceinline__ int64_t range_start(int64_t r, int64_t units, int32_t ranges) { return r * units / ranges; }
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst_smem, const void* tmap, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst_smem),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&d)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&d)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <Elem E>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (E == Elem::kBF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void sts128_zero(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
+// Walks a worker's range: the sequence and the unit within it, and the block that holds it.
+struct Walk {
+  int b;          // sequence
+  int2 seen;      // its visible tokens
+  int unit;       // absolute unit (token / kUnit) of the sequence
+  int last;       // the sequence's last unit
+};
+
+// NT: eights of query heads that a worker takes.
+template <Elem E, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const DecodeModParams p) {
+  using Ops = ElemOps<E>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + kOffScan);  // units before each thread's sequences
+  int64_t* warp_units = scan + kThreads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = sbase + warp * kStages * 2 * kUnitBytes;
+  const uint32_t bars = sbase + kOffBars + warp * kStages * 8;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    mbar_fence_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+
+  // ---- the units of all sequences, laid end to end ----
+  const int B = p.num_seqs;
+  const int per = (B + kThreads - 1) / kThreads;  // consecutive sequences per thread
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    const int n = b < B ? units_of(visible(p, b, blockIdx.x == 0)) : 0;
+    mine += n;
+    // sequences that see no key: zeros
+    uint32_t empty = __ballot_sync(0xffffffffu, n == 0 && b < B && b % gridDim.x == blockIdx.x);
+    for (; empty; empty &= empty - 1) {
+      const int64_t row = (warp * 32 + __ffs(empty) - 1) * per + i;
+      uint4* o = reinterpret_cast<uint4*>(p.out + row * p.hq * kHeadDim);
+      for (int j = lane; j < p.hq * (kHeadDim / 8); j += 32) o[j] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  int64_t sum = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, sum, off);
+    if (lane >= off) sum += y;
+  }
+  if (lane == 31) warp_units[warp] = sum;
+  __syncthreads();
+  int64_t before = 0, units = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_units[w];
+    units += warp_units[w];
+  }
+  scan[tid] = before + sum - mine;
+  __syncthreads();
+  const int64_t fill = (units + kMinUnits - 1) / kMinUnits;
+  const int ranges = static_cast<int>(fill < p.st.ranges ? fill : p.st.ranges);
+  if (blockIdx.x == 0 && tid == 0) {
+    p.info[0].units = units;
+    p.info[0].ranges = ranges;
+  }
+  const int worker = static_cast<int>(blockIdx.x) * kWarps + warp;
+  const int workers = static_cast<int>(gridDim.x) * kWarps;
+  // A stream has all its ranges, or (more streams than workers) one range and a worker several streams.
+  const bool split = p.st.ranges > 1;
+  const int range = split ? worker / p.st.count : 0;
+  if (range >= ranges) return;
+  const int64_t start = range_start(range, units, ranges), end = range_start(range + 1, units, ranges);
+
+  // the sequence that holds unit `start`
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < kThreads / 32; ++j) at += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= start));
+  Walk begin;
+  int64_t begin_first = scan[at - 1];  // first unit of begin.b
+  begin.b = (at - 1) * per;
+  while (true) {
+    begin.seen = visible(p, begin.b, false);
+    const int n = units_of(begin.seen);
+    if (begin_first + n > start) break;
+    begin_first += n;
+    ++begin.b;
+  }
+  begin.last = (begin.seen.y - 1) / kUnit;
+  begin.unit = begin.seen.x / kUnit + static_cast<int>(start - begin_first);
+
+  const int row16 = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: this lane's row of K
+  const int rowv = (lane & 7) + (lane >> 4) * 8;         // and of V
+  const int r = lane >> 2, c = lane & 3;                 // fragment row and column pair
+  uint32_t phase = 0;                                    // bit i: parity of the next wait on stage i
+  int stage = 0;
+  bool ok = true;
+
+  for (int stream = split ? worker % p.st.count : worker; stream < p.st.count && ok; stream += workers) {
+    const int hk = stream / p.st.parts, part = stream - hk * p.st.parts;
+    const int head0 = hk * p.st.group + part * p.st.per;
+    const int heads = min(p.st.per, p.st.group - part * p.st.per);
+
+    // ---- fetching, kStages units ahead ----
+    Walk ahead = begin;
+    int64_t to_fetch = end - start;
+    int under_way = 0;                               // copies not waited for
+    int block = -1, next_block = -1, block_at = -1;  // table entries; block_at: table place of `block`
+    auto fetch = [&](int slot) {
+      if (ahead.unit > ahead.last) {  // the next sequence with units
+        do {
+          ++ahead.b;
+          ahead.seen = visible(p, ahead.b, false);
+        } while (ahead.seen.y == 0);
+        ahead.unit = ahead.seen.x / kUnit;
+        ahead.last = (ahead.seen.y - 1) / kUnit;
+        block_at = -1;
+      }
+      const int place = ahead.unit / (kBlockSize / kUnit);
+      if (place != block_at) {
+        const int32_t* table = p.block_tables + static_cast<int64_t>(ahead.b) * p.bt_stride;
+        block = block_at >= 0 ? next_block : table[place];
+        block_at = place;
+        next_block = place < (ahead.seen.y - 1) / kBlockSize ? table[place + 1] : 0;
+        if (block < 0 || block >= p.num_blocks) {
+          if (lane == 0) flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
+          block = 0;
+        }
+      }
+      if (lane == 0) {
+        const int row = block * kBlockSize + (ahead.unit % (kBlockSize / kUnit)) * kUnit;
+        const uint32_t bar = bars + 8 * slot, dst = ring + slot * 2 * kUnitBytes;
+        mbar_arrive_expect_tx(bar, 2 * kUnitBytes);
+        tma_load_4d(dst, &tm_k, 0, row, hk, 0, bar);
+        tma_load_4d(dst + kUnitBytes, &tm_v, 0, row, hk, 0, bar);
+      }
+      ++ahead.unit;
+      --to_fetch;
+      ++under_way;
+    };
+    {
+      int slot = stage;
+      for (int i = 0; i < kStages && to_fetch > 0; ++i) {
+        fetch(slot);
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+      }
+    }
+
+    Walk now = begin;
+    int64_t first_unit = begin_first;  // of the sequence under way
+    int64_t left = end - start;
+    while (left > 0 && ok) {
+      // ---- one sequence's units in this range ----
+      const int n = static_cast<int>(min(left, static_cast<int64_t>(now.last - now.unit + 1)));
+      const int seq_first = now.unit;
+      // Q as the second operand: lane (r, c) holds head r, dims 16 i + 2 c, + 1 and + 8, + 9
+      uint32_t qf[NT][8][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int h = 8 * t + r;
+        const uint16_t* row = p.q + now.b * p.q_row_stride + static_cast<int64_t>(head0 + h) * kHeadDim + 2 * c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            qf[t][i][j] = h < heads ? *reinterpret_cast<const uint32_t*>(row + 16 * i + 8 * j) : 0u;
+      }
+      float slope[NT][2], m[NT][2], l[NT][2], acc[NT][8][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int h = 8 * t + 2 * c + j;
+          slope[t][j] = p.slopes && h < heads ? p.slopes[head0 + h] * kLog2e : 0.f;
+          m[t][j] = -INFINITY;
+          l[t][j] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[t][i][j] = 0.f;
+      }
+
+      for (int u = 0; u < n; ++u) {
+        const int token0 = (seq_first + u) * kUnit;
+        const uint32_t bar = bars + 8 * stage;
+        const uint32_t ks = ring + stage * 2 * kUnitBytes, vs = ks + kUnitBytes;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar, (phase >> stage) & 1u, p.err))) {
+          ok = false;
+          break;
+        }
+        phase ^= 1u << stage;
+        --under_way;
+        const bool edge = token0 < now.seen.x || token0 + kUnit > now.seen.y;
+        if (edge) {  // rows of V that are not visible may hold anything: 0 * NaN must not be added
+          const int token = token0 + (lane >> 1);
+          if (token < now.seen.x || token >= now.seen.y) {
+            const uint32_t row = vs + (lane & 1) * (kUnitBytes / 2) + (lane >> 1) * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts128_zero(row + 16 * i);
+          }
+          fence_proxy_async_smem();  // before a later copy into the same place
+          __syncwarp();
+        }
+
+        // S^T = K Q^T; two chains to halve the latency
+        float s[NT][2][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[t][j >> 2][j & 3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t a[4];
+          const int chunk = 2 * i + (lane >> 4);
+          ldmatrix_x4(ks + (chunk >> 3) * (kUnitBytes / 2) + row16 * 128 + (((chunk & 7) ^ (row16 & 7)) << 4), a);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816<E>(s[t][i & 1], a, qf[t][i][0], qf[t][i][1]);
+        }
+
+        // scores in log2 units; lane (r, c): tokens r, r + 8 of heads 2 c, 2 c + 1
+        float z[NT][4];
+        bool rise = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = s[t][0][j] + s[t][1][j];
+            z[t][j] = p.cap_log2 > 0.f ? p.cap_log2 * tanhf(x * p.scale_by_cap) : x * p.scale_log2;
+            const int token = token0 + r + (j >> 1) * 8;
+            if (p.slopes) z[t][j] = fmaf(-slope[t][j & 1], static_cast<float>(now.seen.y - 1 - token), z[t][j]);
+            if (edge && (token < now.seen.x || token >= now.seen.y)) z[t][j] = -INFINITY;
+            rise = rise || z[t][j] > m[t][j & 1] + 8.f;
+          }
+        if (p.weights) {
+          float* to = p.scores + ((now.b * p.seq_units + (seq_first + u)) * p.st.count + stream) * (p.st.per * kUnit);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int h = 8 * t + 2 * c + (j & 1);
+              if (h < heads) to[h * kUnit + r + (j >> 1) * 8] = z[t][j];
+            }
+        }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float top = fmaxf(fmaxf(z[t][j], z[t][j + 2]), m[t][j]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              const float alpha = m[t][j] == -INFINITY ? 0.f : ex2_approx(m[t][j] - top);
+              m[t][j] = top;
+              l[t][j] *= alpha;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[t][i][j] *= alpha;
+                acc[t][i][j + 2] *= alpha;
+              }
+            }
+        }
+        // p, and what rounding it to 16 bits loses, as the second operand of the product with V
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[j] = ex2_approx(z[t][j] - (m[t][j & 1] == -INFINITY ? 0.f : m[t][j & 1]));
+            l[t][j & 1] += e[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t hi = Ops::pack(e[2 * j], e[2 * j + 1]);
+            ph[t][j] = movmatrix(hi);
+            pl[t][j] = movmatrix(Ops::pack(e[2 * j] - Ops::lo(hi), e[2 * j + 1] - Ops::hi(hi)));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t a[4];
+          const int chunk = 2 * i + ((lane >> 3) & 1);
+          ldmatrix_x4_trans(vs + (chunk >> 3) * (kUnitBytes / 2) + rowv * 128 + (((chunk & 7) ^ (rowv & 7)) << 4), a);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816<E>(acc[t][i], a, ph[t][0], ph[t][1]);
+            mma16816<E>(acc[t][i], a, pl[t][0], pl[t][1]);
+          }
+        }
+        __syncwarp();
+        if (to_fetch > 0) fetch(stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+      }
+      if (!ok) break;
+
+      // ---- the end of a sequence, or of the range inside one ----
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], off);
+      const bool begins = first_unit >= start;              // this range holds its first unit
+      const bool ends = now.unit + n > now.last;            // and its last
+      if (begins && ends) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float inv0 = l[t][0] == 0.f ? 0.f : 1.f / l[t][0], inv1 = l[t][1] == 0.f ? 0.f : 1.f / l[t][1];
+          uint16_t* row = p.out + (static_cast<int64_t>(now.b) * p.hq + head0 + 8 * t + r) * kHeadDim + 2 * c;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t x = movmatrix(Ops::pack(acc[t][i][0] * inv0, acc[t][i][1] * inv1));
+            const uint32_t y = movmatrix(Ops::pack(acc[t][i][2] * inv0, acc[t][i][3] * inv1));
+            if (8 * t + r < heads) {
+              *reinterpret_cast<uint32_t*>(row + 16 * i) = x;
+              *reinterpret_cast<uint32_t*>(row + 16 * i + 8) = y;
+            }
+          }
+          if (p.weights && r == 0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int h = 8 * t + 2 * c + j;
+              if (h < heads)
+                p.final_ml[static_cast<int64_t>(now.b) * p.hq + head0 + h] = make_float2(m[t][j], j ? inv1 : inv0);
+            }
+          }
+        }
+      } else {
+        const int64_t slot =
+            ((static_cast<int64_t>(range) * p.st.count + stream) * 2 + (first_unit <= start ? 0 : 1)) * p.st.per;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int h = 8 * t + 2 * c + j;
+            if (h < heads) {
+              float* o = p.o + (slot + h) * kHeadDim + r;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                o[16 * i] = acc[t][i][j];
+                o[16 * i + 8] = acc[t][i][j + 2];
+              }
+              if (r == 0) p.ml[slot + h] = make_float2(m[t][j], l[t][j]);
+            }
+          }
+      }
+      left -= n;
+      if (left == 0) {
+        if (stream == 0 && lane == 0) {
+          RangeInfo* info = p.info + 1 + range;
+          info->seq = begins && !ends ? now.b : -1;
+          info->first_unit = first_unit;
+          info->units = now.last - now.seen.x / kUnit + 1;
+        }
+      } else {
+        first_unit += now.last - now.seen.x / kUnit + 1;
+        do {
+          ++now.b;
+          now.seen = visible(p, now.b, false);
+        } while (now.seen.y == 0);
+        now.unit = now.seen.x / kUnit;
+        now.last = (now.seen.y - 1) / kUnit;
+      }
+    }
+    if (!ok) {  // leave no copy in flight
+      for (int i = 0; i < under_way; ++i)
+        mbar_wait(bars + 8 * ((stage + i) % kStages), (phase >> ((stage + i) % kStages)) & 1u, p.err);
+    }
+  }
+}
+
+// Joins the partial results of one query head of the sequence that begins in a range and goes on behind it.
+template <Elem E>
+__global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(const DecodeModParams p) {
+  using Ops = ElemOps<E>;
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t units = p.info[0].units;
+  const int ranges = p.info[0].ranges;
+  const int range = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
+  if (range >= ranges) return;
+  const RangeInfo info = p.info[1 + range];
+  if (info.seq < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = h / p.st.group, in_group = h - hk * p.st.group, part = in_group / p.st.per;
+  const int stream = hk * p.st.parts + part, in_part = in_group - part * p.st.per;
+  // the range that holds the sequence's last unit
+  const int last = static_cast<int>(((info.first_unit + info.units) * ranges - 1) / units);
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kAhead = 4;
+  for (int r0 = range + warp; r0 <= last; r0 += kMergeWarps * kAhead) {
+    float2 ml[kAhead];
+    float4 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = min(r0 + i * kMergeWarps, last);
+      const int64_t slot =
+          ((static_cast<int64_t>(r) * p.st.count + stream) * 2 +
+           (info.first_unit <= range_start(r, units, ranges) ? 0 : 1)) * p.st.per + in_part;
+      ml[i] = p.ml[slot];
+      x[i] = *(reinterpret_cast<const float4*>(p.o + slot * kHeadDim) + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (r0 + i * kMergeWarps > last) break;
+      const float top = fmaxf(M, ml[i].x), use = top == -INFINITY ? 0.f : top;
+      const float a = ex2_approx(M - use), b = ex2_approx(ml[i].x - use);
+      M = top;
+      L = L * a + ml[i].y * b;
+      o.x = o.x * a + x[i].x * b;
+      o.y = o.y * a + x[i].y * b;
+      o.z = o.z * a + x[i].z * b;
+      o.w = o.w * a + x[i].w * b;
+    }
+  }
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
+  }
+  s_o[warp][lane] = o;
+  __syncthreads();
+  if (warp != 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_m[w]);
+  const float use = top == -INFINITY ? 0.f : top;
+  L = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float a = ex2_approx(s_m[w] - use);
+    const float4 y = s_o[w][lane];
+    L += s_l[w] * a;
+    o.x += y.x * a;
+    o.y += y.y * a;
+    o.z += y.z * a;
+    o.w += y.w * a;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t row = static_cast<int64_t>(info.seq) * p.hq + h;
+  *(reinterpret_cast<uint2*>(p.out + row * kHeadDim) + lane) =
+      make_uint2(Ops::pack(o.x * inv, o.y * inv), Ops::pack(o.z * inv, o.w * inv));
+  if (p.weights && lane == 0) p.final_ml[row] = make_float2(top, inv);
+}
+
+// weights[t] += the share of t among its sequence's scores, summed over the query heads of a kv head; the newest token's
+// starts from 0. One block per (256-token block of a sequence), one thread per token.
+__global__ void __launch_bounds__(kBlockSize) decode_mod_weights_kernel(const DecodeModParams p) {
+  const int b = static_cast<int>(blockIdx.y), token = static_cast<int>(blockIdx.x) * kBlockSize + threadIdx.x;
+  const int2 seen = visible(p, b, false);
+  const int ctx = p.context_lens[b];
+  const bool good = ctx > 0 && ctx <= p.max_ctx && ctx <= static_cast<int64_t>(p.bt_stride) * kBlockSize;
+  if (!good || static_cast<int>(blockIdx.x) > (ctx - 1) / kBlockSize ||
+      (static_cast<int>(blockIdx.x) + 1) * kBlockSize <= min(seen.x, ctx - 1)) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const int block = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + blockIdx.x];
+  const bool shown = token >= seen.x && token < seen.y, newest = token == ctx - 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (block < 0 || block >= p.num_blocks || !(shown || newest)) return;  // a bad block has been reported
+  float* w = p.weights + static_cast<int64_t>(block) * p.hkv * kBlockSize + threadIdx.x;
+  const float* z0 = p.scores + (b * p.seq_units + token / kUnit) * p.st.count * (p.st.per * kUnit) + token % kUnit;
+  const float2* ml0 = p.final_ml + static_cast<int64_t>(b) * p.hq;
+#pragma unroll 4
+  for (int hk = 0; hk < p.hkv; ++hk) {
+    float share = 0.f;
+    if (shown) {
+      for (int g = 0; g < p.st.group; ++g) {
+        const int part = g / p.st.per;
+        const float2 ml = ml0[hk * p.st.group + g];
+        const float z = z0[((hk * p.st.parts + part) * p.st.per + g - part * p.st.per) * kUnit];
+        share += ml.y == 0.f ? 0.f : ex2_approx(z - ml.x) * ml.y;
+      }
+    }
+    float* to = w + static_cast<int64_t>(hk) * kBlockSize;
+    *to = (newest ? 0.f : *to) + share;
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                                        &q) == cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return found ? reinterpret_cast<EncodeTiledFn>(ptr) : nullptr;
+  }();
+  return fn;
+}
+
+// A cache as [half of the dims][head][slot][64 dims], so that one copy brings both 128-byte halves of kUnit rows.
+bool encode_cache(CUtensorMap* tm, const void* base, int64_t slots, int heads, Elem elem) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(slots), static_cast<cuuint64_t>(heads), 2};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(heads) * kHeadDim * 2, kHeadDim * 2, kHeadDim};
+  const cuuint32_t box[4] = {64, kUnit, 1, 2};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType dt = elem == Elem::kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(tm, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch whose blocks may be set up while the kernel before it ends (each waits for that one's results itself).
+template <typename... Args>
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <Elem E, int NT>
+cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeModParams& p, int ctas,
+                         cudaStream_t stream) {
+  static std::atomic<bool> attr_done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool known = dev >= 0 && dev < 64;
+  if (!known || !attr_done[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(decode_mod_kernel<E, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    if (known) attr_done[dev].store(true, std::memory_order_release);
+  }
+  decode_mod_kernel<E, NT><<<ctas, kThreads, kSmemBytes, stream>>>(tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_mod_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t max_ctx, bool weights) {
+  return layout_of(streams_of(hq, hkv), num_seqs, hq, max_ctx, weights).total;
+}
+
+cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStream_t stream, Elem elem) {
+  const Streams st = streams_of(a.hq, a.hkv);
+  const bool weights = a.weights != nullptr;
+  const Layout lay = layout_of(st, a.num_seqs, a.hq, a.max_ctx, weights);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  DecodeModParams p{};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.q_row_stride = a.q_row_stride;
+  p.block_tables = a.block_tables;
+  p.bt_stride = a.bt_stride;
+  p.num_blocks = a.num_blocks;
+  p.context_lens = a.context_lens;
+  p.num_seqs = a.num_seqs;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.max_ctx = a.max_ctx;
+  p.st = st;
+  p.scale_log2 = a.scale * kLog2e;
+  p.cap_log2 = a.softcap * kLog2e;
+  p.scale_by_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  p.slopes = a.slopes;
+  p.window = a.window;
+  p.key_starts = a.key_starts;
+  p.weights = a.weights;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.info = reinterpret_cast<RangeInfo*>(ws + lay.info);
+  p.final_ml = reinterpret_cast<float2*>(ws + lay.final_ml);
+  p.ml = reinterpret_cast<float2*>(ws + lay.ml);
+  p.o = reinterpret_cast<float*>(ws + lay.o);
+  p.scores = reinterpret_cast<float*>(ws + lay.scores);
+  p.seq_units = (static_cast<int64_t>(a.max_ctx) + kUnit - 1) / kUnit;
+  p.err = err;
+  CUtensorMap tk, tv;
+  const int64_t slots = static_cast<int64_t>(a.num_blocks) * kBlockSize;
+  if (!encode_cache(&tk, a.k_cache, slots, a.hkv, elem) || !encode_cache(&tv, a.v_cache, slots, a.hkv, elem))
+    return cudaErrorInvalidValue;
+  // no more workers than the longest lengths could keep busy
+  const int64_t most = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits * st.count;
+  const int64_t want = (most + kWarps - 1) / kWarps;
+  const int ctas = static_cast<int>(want < 1 ? 1 : (want < kCtas ? want : kCtas));
+  const bool f16 = elem == Elem::kF16;
+  cudaError_t e;
+  if (st.per == 8)
+    e = f16 ? launch_typed<Elem::kF16, 1>(tk, tv, p, ctas, stream) : launch_typed<Elem::kBF16, 1>(tk, tv, p, ctas, stream);
+  else
+    e = f16 ? launch_typed<Elem::kF16, 2>(tk, tv, p, ctas, stream) : launch_typed<Elem::kBF16, 2>(tk, tv, p, ctas, stream);
+  if (e != cudaSuccess) return e;
+  if (st.ranges > 1) {
+    const int64_t half_most = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits;
+    const unsigned ranges = static_cast<unsigned>(half_most < st.ranges ? (half_most < 1 ? 1 : half_most) : st.ranges);
+    const dim3 grid(ranges, static_cast<unsigned>(a.hq));
+    e = launch_behind(f16 ? decode_mod_merge_kernel<Elem::kF16> : decode_mod_merge_kernel<Elem::kBF16>, grid,
+                      kMergeWarps * 32, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  if (weights && a.max_ctx > 0) {
+    const dim3 grid(static_cast<unsigned>((a.max_ctx + kBlockSize - 1) / kBlockSize), static_cast<unsigned>(a.num_seqs));
+    e = launch_behind(decode_mod_weights_kernel, grid, kBlockSize, stream, p);
+  }
+  return e;
+}
+
+}  // namespace pkv
+
+namespace {
+
+constexpr int32_t kMaxHeads = 8192;
+constexpr int32_t kMaxBlocks = (1 << 23) - 1;  // slots are 32-bit coordinates of the copies
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool heads_fit(int32_t hq, int32_t hkv) { return hkv > 0 && hq > 0 && hq <= kMaxHeads && hq % hkv == 0; }
+
+int decode_mod_common(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
+                      int32_t num_blocks, const int32_t* block_tables, int32_t block_table_stride,
+                      const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale,
+                      float softcap, const float* slopes, int32_t window, const int32_t* key_starts, float* weights,
+                      void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream, pkv::Elem elem) {
+  if (head_dim != pkv::kHeadDim || block_size != pkv::kBlockSize || !heads_fit(num_heads, num_kv_heads))
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs < 0 || num_seqs > 65535 || num_blocks < 0 || num_blocks > kMaxBlocks || block_table_stride < 0 ||
+      max_context_len < 0 || max_context_len > (1 << 24) || window < 0)
+    return PKV_ERR_BAD_SIZE;
+  if (num_seqs == 0) return PKV_OK;
+  if (!(softmax_scale > 0.f) || std::isinf(softmax_scale) || !(softcap >= 0.f) || std::isinf(softcap))
+    return PKV_ERR_BAD_SIZE;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PKV_ERR_NULL_POINTER;
+  if (num_blocks == 0) return PKV_ERR_BAD_SIZE;
+  if (q_row_stride < static_cast<int64_t>(num_heads) * head_dim) return PKV_ERR_BAD_STRIDE;
+  if (!aligned(q, 16) || q_row_stride % 8 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(out, 16) || !aligned(slopes, 4) || !aligned(key_starts, 4) || !aligned(weights, 4))
+    return PKV_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < pkv::decode_mod_workspace_bytes(num_seqs, num_heads, num_kv_heads,
+                                                                      max_context_len, weights != nullptr))
+    return PKV_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return PKV_ERR_ALIGNMENT;
+  unsigned int* err = nullptr;
+  const int st = pkv::device_error_word(&err);
+  if (st != PKV_OK) return st;
+  pkv::DecodeModArgs a{};
+  a.q = q;
+  a.q_row_stride = q_row_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.num_blocks = num_blocks;
+  a.block_tables = block_tables;
+  a.bt_stride = block_table_stride;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.hq = num_heads;
+  a.hkv = num_kv_heads;
+  a.max_ctx = max_context_len;
+  a.scale = softmax_scale;
+  a.softcap = softcap;
+  a.slopes = slopes;
+  a.window = window;
+  a.key_starts = key_starts;
+  a.weights = weights;
+  a.out = out;
+  a.workspace = workspace;
+  if (pkv::launch_decode_mod(a, err, stream, elem) == cudaSuccess) return PKV_OK;
+  (void)cudaGetLastError();
+  return PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_decode_mod_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                      int32_t max_context_len, int32_t weights) {
+  if (num_seqs <= 0 || num_seqs > 65535 || max_context_len < 0 || max_context_len > (1 << 24) ||
+      !heads_fit(num_heads, num_kv_heads))
+    return 0;
+  return pkv::decode_mod_workspace_bytes(num_seqs, num_heads, num_kv_heads, max_context_len, weights != 0);
+}
+
+// The bf16 and fp16 entry points share one body; only the elements' type differs.
+
+int pkv_decode_mod(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                   const int32_t* block_tables, int32_t block_table_stride, const int32_t* context_lens,
+                   int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int32_t max_context_len, float softmax_scale, float softcap, const float* slopes, int32_t window,
+                   const int32_t* key_starts, float* weights, void* out, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+  return decode_mod_common(q, q_row_stride, k_cache, v_cache, num_blocks, block_tables, block_table_stride,
+                           context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                           softmax_scale, softcap, slopes, window, key_starts, weights, out, workspace,
+                           workspace_bytes, stream, pkv::Elem::kBF16);
+}
+
+int pkv_decode_mod_f16(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
+                       int32_t num_blocks, const int32_t* block_tables, int32_t block_table_stride,
+                       const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t block_size, int32_t max_context_len, float softmax_scale,
+                       float softcap, const float* slopes, int32_t window, const int32_t* key_starts, float* weights,
+                       void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return decode_mod_common(q, q_row_stride, k_cache, v_cache, num_blocks, block_tables, block_table_stride,
+                           context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                           softmax_scale, softcap, slopes, window, key_starts, weights, out, workspace,
+                           workspace_bytes, stream, pkv::Elem::kF16);
+}
+
+}  // extern "C"

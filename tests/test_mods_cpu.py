@@ -1,0 +1,46 @@
+"""CPU checks of attention with modified scores: arguments refused on the host, workspace sizes."""
+import ctypes
+
+import pytest
+
+ONE = ctypes.c_void_p(16)
+ODD = ctypes.c_void_p(24)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import paged_kv_cache_kvh_gb300 as m
+    return m._lib
+
+
+@pytest.mark.parametrize("suffix", ["", "_f16"])
+def test_decode_refusals(lib, suffix):
+    dec = getattr(lib, "pkv_decode_mod" + suffix)
+    need = lib.pkv_decode_mod_workspace_bytes(4, 16, 8, 4096, 0)
+    more = lib.pkv_decode_mod_workspace_bytes(4, 16, 8, 4096, 1)
+    assert more > need > 0
+
+    def f(q=ONE, qs=2048, kc=ONE, vc=ONE, nb=16, bt=ONE, bs=16, cl=ONE, n=4, hq=16, hkv=8, d=128, blk=256, mc=4096, sc=0.1,
+          cap=0.0, sl=None, win=0, st=None, w=None, out=ONE, ws=ONE, wb=need):
+        return dec(q, qs, kc, vc, nb, bt, bs, cl, n, hq, hkv, d, blk, mc, sc, cap, sl, win, st, w, out, ws, wb, None)
+
+    assert f(d=64) == f(blk=16) == f(hq=12) == f(hkv=0) == f(hq=0) == f(hq=-8) == f(hq=8200, qs=1 << 21) == -2
+    assert f(n=-1) == f(n=65536) == f(nb=-1) == f(nb=0) == f(nb=1 << 23) == f(bs=-1) == f(mc=-1) == f(mc=(1 << 24) + 1) == -6
+    assert f(sc=0.0) == f(sc=float("nan")) == f(sc=float("inf")) == f(cap=-1.0) == f(cap=float("nan")) == -6
+    assert f(cap=float("inf")) == f(win=-1) == -6
+    for name in ("q", "kc", "vc", "bt", "cl", "out"):
+        assert f(**{name: None}) == -1
+    assert f(qs=2047) == -3
+    assert f(q=ODD) == f(qs=2052) == f(kc=ODD) == f(vc=ODD) == f(out=ODD) == f(ws=ODD) == -4
+    for name in ("sl", "st", "w"):
+        assert f(**{name: ctypes.c_void_p(18), "wb": more}) == -4
+    assert f(ws=None) == f(wb=need - 1) == f(w=ONE, wb=more - 1) == -5
+    assert f(n=0, q=None) == 0
+
+
+def test_decode_workspace_sizes(lib):
+    size = lib.pkv_decode_mod_workspace_bytes
+    assert size(0, 16, 8, 4096, 0) == size(65536, 16, 8, 4096, 0) == size(4, 12, 8, 4096, 0) == size(4, 16, 8, -1, 0) == 0
+    # partial results: bounded by the GPU's workers, whatever the batch; scores: one per (sequence, token, head)
+    assert size(65535, 16, 8, 1 << 24, 0) == size(1, 16, 8, 16, 0) < 1 << 26
+    assert size(256, 16, 8, 4096, 1) >= 256 * 16 * 4096 * 4
