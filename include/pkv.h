@@ -595,6 +595,34 @@ size_t pkv_decode_mod_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32
                                       int32_t max_context_len, int32_t weights);
 
 /*
+ * pkv_evict_kvcache -- cuts every sequence of more than `budget` tokens down to
+ * `budget`: of each kv head the tokens at the first `first` positions, the newest
+ * `recent` ones, and of the others those with the largest weights (as pkv_decode_mod
+ * adds them up beside the cache), equal weights in order of position. The pages keep
+ * every token of a sequence; this call has no counterpart there. Kept tokens keep
+ * their order and move up: token kept[b][h][j] of head h becomes token j, its K and V
+ * rows and its weight with it. Each head chooses for itself, so a slot may then hold
+ * different tokens of different heads. Shorter sequences keep all their tokens.
+ *   k_cache, v_cache  [num_blocks, 256, num_kv_heads, 128], 16-bit elements of either type, 16-byte aligned
+ *   weights           fp32 [num_blocks, num_kv_heads, 256]; a NaN counts as larger than any number
+ *   max_context_len   upper bound on context_lens[b] (<= 2^24)
+ *   new_block_tables  [num_seqs, new_block_table_stride] int32: the blocks that the kept tokens are copied to (of
+ *                     shorter sequences all tokens), none of them in a block_tables row of the call; the old blocks
+ *                     are only read, so sequences may share them. Its rows have room for min(budget, max_context_len)
+ *                     tokens. NULL: in place, within the sequence's own blocks, which no other sequence may share then.
+ *                     Blocks behind the new length are free afterwards.
+ *   kept              int32 [num_seqs, num_kv_heads, budget] out: old positions in rising order, -1 behind the last
+ *   new_context_lens  int32 [num_seqs] out, min(context_lens[b], budget); not context_lens itself
+ * 1 <= budget <= 2^24, first + recent <= budget. Slots behind the new length are left as they were. Bad lengths
+ * (taken as 0) and blocks (their tokens are not moved) set PKV_DEVERR_BAD_SEQLEN and PKV_DEVERR_BAD_BLOCK.
+ */
+int pkv_evict_kvcache(void* k_cache, void* v_cache, float* weights, int32_t num_blocks, const int32_t* block_tables,
+                      int32_t block_table_stride, const int32_t* context_lens, int32_t num_seqs, int32_t num_kv_heads,
+                      int32_t head_dim, int32_t block_size, int32_t max_context_len, int32_t budget, int32_t first,
+                      int32_t recent, const int32_t* new_block_tables, int32_t new_block_table_stride, int32_t* kept,
+                      int32_t* new_context_lens, cudaStream_t stream);
+
+/*
  * pkv_build_prefill_metadata / pkv_build_decode_metadata -- the per-step index
  * preparation of engine/model_runner.py (prepare_prefill, prepare_decode in
  * "vLLM 学习笔记 02：nano-vllm 源码逐段精读"; worked example in

@@ -76,6 +76,9 @@ _SIGNATURES = {
     "pkv_decode_q4_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
 }
 _SIGNATURES["pkv_rope_frequencies"] = (ctypes.c_int, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp])
+_SIGNATURES["pkv_evict_kvcache"] = (
+    ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
+                   _vp, _vp])
 _SIGNATURES["pkv_decode_mod_workspace_bytes"] = (_sz, [_i32, _i32, _i32, _i32, _i32])
 for _suffix in ("", "_f16"):
     _SIGNATURES["pkv_decode_mod" + _suffix] = (
@@ -922,6 +925,52 @@ def pkv_decode_mod_f16(q, k_cache, v_cache, block_tables, context_lens, max_cont
     return _decode_mod(_lib.pkv_decode_mod_f16, torch.float16, q, k_cache, v_cache, block_tables, context_lens,
                        max_context_len, softmax_scale, workspace, softcap, slopes, window, key_starts, weights, out,
                        stream)
+
+
+
+def pkv_evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, max_context_len, budget, *, first=0,
+                      recent=0, new_block_tables=None, kept=None, new_context_lens=None, stream=None):
+    """Cuts each sequence of more than `budget` tokens down to it: per kv head the first `first`, the newest `recent` and
+    of the others those with the largest weights (attention_weights, added up by pkv_decode_mod) stay, in order. Rows and
+    weights go to the blocks of new_block_tables [B, width], or, without, move up within the sequence's own blocks.
+    Caches of either 16-bit type. Returns (kept int32 [B, num_kv_heads, budget]: old positions, -1 behind the last;
+    new_context_lens int32 [B])."""
+    dev = _current_device()
+    dtype = k_cache.dtype
+    if dtype not in _TYPE_NAME:
+        raise ValueError("k_cache and v_cache must be bf16 or fp16")
+    blocks, hkv = _caches(k_cache, v_cache, dev, dtype)
+    weights_at = _weight_pool(weights, dev, blocks, hkv)
+    _table(block_tables, dev, "block_tables")
+    _table(context_lens, dev, "context_lens")
+    tables, B, budget = block_tables.shape, context_lens.numel(), int(budget)
+    if len(tables) != 2 or tables[0] < B or budget < 1:
+        raise ValueError("block_tables must be [B, width], context_lens [B] and budget at least 1")
+    new_at, new_width = None, 0
+    if new_block_tables is not None:
+        _table(new_block_tables, dev, "new_block_tables")
+        if new_block_tables.dim() != 2 or new_block_tables.shape[0] < B:
+            raise ValueError("new_block_tables must be [B, width]")
+        new_at, new_width = new_block_tables.data_ptr(), new_block_tables.shape[1]
+    made = []
+    for t, shape, name in ((kept, (B, hkv, budget), "kept"), (new_context_lens, (B,), "new_context_lens")):
+        if t is None:
+            t = (torch.empty(shape, dtype=_I32, device=k_cache.device) if stream is None
+                 else _made(torch.empty, shape, _I32, k_cache.device, stream))
+        else:
+            _table(t, dev, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {shape}")
+        made.append(t)
+    if made[1].data_ptr() == context_lens.data_ptr() and B > 0:
+        raise ValueError("new_context_lens must not be context_lens")
+    status = _lib.pkv_evict_kvcache(
+        k_cache.data_ptr(), v_cache.data_ptr(), weights_at, blocks, block_tables.data_ptr(), tables[1],
+        context_lens.data_ptr(), B, hkv, HEAD_DIM, BLOCK_SIZE, int(max_context_len), budget, int(first), int(recent),
+        new_at, new_width, made[0].data_ptr(), made[1].data_ptr(), _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, "pkv_evict_kvcache")
+    return made[0], made[1]
 
 
 

@@ -81,3 +81,16 @@ def cache_rows(cache, table, length):
     """The first `length` rows [length, hkv, d] that a block table names."""
     blocks = torch.as_tensor(table[:-(-length // 256)], dtype=torch.long, device=cache.device)
     return cache[blocks].flatten(0, 1)[:length]
+
+
+def evict_choice(weights, first, recent, budget):
+    """The positions of `weights` [n] that stay: plain Python, the largest by (weight, lower position first)."""
+    n = len(weights)
+    if n <= budget:
+        return list(range(n))
+    middle = range(first, n - recent)
+
+    def size(t):
+        return (1, 0.0) if math.isnan(weights[t]) else (0, weights[t])
+    best = sorted(middle, key=size, reverse=True)[:budget - first - recent]   # a stable sort
+    return sorted(list(range(first)) + best + list(range(n - recent, n)))

@@ -44,3 +44,21 @@ def test_decode_workspace_sizes(lib):
     # partial results: bounded by the GPU's workers, whatever the batch; scores: one per (sequence, token, head)
     assert size(65535, 16, 8, 1 << 24, 0) == size(1, 16, 8, 16, 0) < 1 << 26
     assert size(256, 16, 8, 4096, 1) >= 256 * 16 * 4096 * 4
+
+
+def test_evict_refusals(lib):
+    def f(kc=ONE, vc=ONE, w=ONE, nb=16, bt=ONE, bs=16, cl=ONE, n=4, h=8, d=128, blk=256, mc=4096, budget=300, first=4,
+          recent=32, nt=ONE, ns=2, kept=ONE, nl=ONE):
+        return lib.pkv_evict_kvcache(kc, vc, w, nb, bt, bs, cl, n, h, d, blk, mc, budget, first, recent, nt, ns, kept, nl,
+                                     None)
+
+    assert f(d=64) == f(blk=16) == f(h=0) == f(h=8193) == -2
+    assert f(n=-1) == f(n=65536) == f(nb=-1) == f(bs=-1) == f(mc=-1) == f(mc=(1 << 24) + 1) == -6
+    assert f(budget=0) == f(budget=(1 << 24) + 1) == f(first=-1) == f(recent=-1) == f(first=301) == f(recent=297) == -6
+    assert f(first=(1 << 31) - 1, recent=(1 << 31) - 1) == f(ns=1) == f(ns=-1) == -6
+    for name in ("kc", "vc", "w", "bt", "cl", "kept", "nl"):
+        assert f(**{name: None}) == -1
+    assert f(kc=ODD) == f(vc=ODD) == -4
+    for name in ("w", "bt", "cl", "nt", "kept", "nl"):
+        assert f(**{name: ctypes.c_void_p(18)}) == -4
+    assert f(n=0, kc=None) == 0
