@@ -595,6 +595,34 @@ size_t pkv_decode_mod_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32
                                       int32_t max_context_len, int32_t weights);
 
 /*
+ * pkv_prefill_varlen_mod -- pkv_prefill_varlen with the scores and masks above, for any head counts. Query row i of
+ * sequence b sits at position Lk_b - Lq_b + i, as there; keys come from contiguous k/v (block_tables == NULL) or from
+ * the paged cache. Arguments and errors as for pkv_prefill_varlen but for
+ *   num_blocks   at most 2^23 - 1
+ *   key_starts   [total_q] int32, one per query row, or NULL: with documents packed into a sequence, the position at
+ *                which the row's document starts
+ *   prefix_lens  [num_seqs] int32, or NULL: keys at positions below are seen by every row, also by rows before them
+ * There is no tile plan. Rows of q and out that belong to no sequence are left as they were. A NaN or an infinity in V
+ * reaches the rows that its key takes part in, and no others.
+ */
+int pkv_prefill_varlen_mod(const void* q, int64_t q_row_stride, int32_t total_q, const void* k, const void* v,
+                           int64_t kv_row_stride, int32_t total_k, const void* k_cache, const void* v_cache,
+                           int32_t num_blocks, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                           int32_t max_seqlen_q, int32_t max_seqlen_k, const int32_t* block_tables,
+                           int32_t block_table_stride, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t block_size, float softmax_scale, float softcap,
+                           const float* slopes, int32_t window, const int32_t* key_starts, const int32_t* prefix_lens,
+                           void* out, cudaStream_t stream);
+int pkv_prefill_varlen_mod_f16(const void* q, int64_t q_row_stride, int32_t total_q, const void* k, const void* v,
+                               int64_t kv_row_stride, int32_t total_k, const void* k_cache, const void* v_cache,
+                               int32_t num_blocks, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                               int32_t max_seqlen_q, int32_t max_seqlen_k, const int32_t* block_tables,
+                               int32_t block_table_stride, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, float softmax_scale, float softcap,
+                               const float* slopes, int32_t window, const int32_t* key_starts,
+                               const int32_t* prefix_lens, void* out, cudaStream_t stream);
+
+/*
  * pkv_evict_kvcache -- cuts every sequence of more than `budget` tokens down to
  * `budget`: of each kv head the tokens at the first `first` positions, the newest
  * `recent` ones, and of the others those with the largest weights (as pkv_decode_mod

@@ -81,6 +81,9 @@ _SIGNATURES["pkv_evict_kvcache"] = (
                    _vp, _vp])
 _SIGNATURES["pkv_decode_mod_workspace_bytes"] = (_sz, [_i32, _i32, _i32, _i32, _i32])
 for _suffix in ("", "_f16"):
+    _SIGNATURES["pkv_prefill_varlen_mod" + _suffix] = (
+        ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _i32,
+                       _i32, _i32, _i32, _i32, _f32, _f32, _vp, _i32, _vp, _vp, _vp, _vp])
     _SIGNATURES["pkv_decode_mod" + _suffix] = (
         ctypes.c_int, [_vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _vp,
                        _i32, _vp, _vp, _vp, _vp, _sz, _vp])
@@ -926,6 +929,70 @@ def pkv_decode_mod_f16(q, k_cache, v_cache, block_tables, context_lens, max_cont
                        max_context_len, softmax_scale, workspace, softcap, slopes, window, key_starts, weights, out,
                        stream)
 
+
+
+def _prefill_mod(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, k, v, k_cache,
+                 v_cache, block_tables, softcap, slopes, window, key_starts, prefix_lens, out, stream):
+    dev = _current_device()
+    total_q, hq, qs = _rows_q4(q, dev, dtype, "q")
+    _table(cu_seqlens_q, dev, "cu_seqlens_q")
+    _table(cu_seqlens_k, dev, "cu_seqlens_k")
+    num_seqs = cu_seqlens_q.numel() - 1
+    if num_seqs < 0 or cu_seqlens_k.numel() != num_seqs + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have one entry per sequence and one more")
+    if block_tables is not None:
+        if k is not None or v is not None:
+            raise ValueError("pass either k and v, or caches and block_tables")
+        blocks, hkv = _caches(k_cache, v_cache, dev, dtype)
+        _table(block_tables, dev, "block_tables")
+        if block_tables.dim() != 2 or block_tables.shape[0] < num_seqs:
+            raise ValueError("block_tables must be [num_seqs, width]")
+        keys = (None, None, 0, 0, k_cache.data_ptr(), v_cache.data_ptr(), blocks)
+        table = (block_tables.data_ptr(), block_tables.shape[1])
+    else:
+        if k is None or v is None:
+            raise ValueError("k and v, or block_tables with caches, must be given")
+        n, hkv, ks = _rows_q4(k, dev, dtype, "k")
+        vn, vh, vs = _rows_q4(v, dev, dtype, "v")
+        if vn != n or vh != hkv or vs != ks:
+            raise ValueError("k and v must share shape and row stride")
+        keys, table = (k.data_ptr(), v.data_ptr(), ks, n, None, None, 0), (None, 0)
+    slopes = None if slopes is None else _f32_array(slopes, dev, hq, "slopes")
+    key_starts = None if key_starts is None else _i32_optional(key_starts, dev, total_q, "key_starts")
+    prefix_lens = None if prefix_lens is None else _i32_optional(prefix_lens, dev, num_seqs, "prefix_lens")
+    if out is None:
+        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+               else _made(torch.empty, q.shape, dtype, q.device, stream))
+    else:
+        _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
+    status = entry(q.data_ptr(), qs, total_q, *keys, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+                   int(max_seqlen_q), int(max_seqlen_k), *table, num_seqs, hq, hkv, HEAD_DIM, BLOCK_SIZE,
+                   float(softmax_scale), float(softcap), slopes, int(window), key_starts, prefix_lens, out.data_ptr(),
+                   _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(status, entry.__name__)
+    return out
+
+
+def pkv_prefill_varlen_mod(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, *, k=None, v=None,
+                           k_cache=None, v_cache=None, block_tables=None, softcap=0.0, slopes=None, window=0,
+                           key_starts=None, prefix_lens=None, out=None, stream=None):
+    """pkv_prefill_varlen with modified scores and masks, for any head counts: scores softcap * tanh(x / softcap) if
+    softcap, then - slopes[head] * |p - t| for slopes fp32 [num_heads]; a row at position p sees the keys t <= p and, of
+    sequence b, those below prefix_lens[b] (int32 [num_seqs]); of these, key_starts[row] (int32 [total_q]) and later
+    ones, and, if window, those with p - t < window. Rows that see none get zeros. Returns out [total_q, num_heads, 128]."""
+    return _prefill_mod(_lib.pkv_prefill_varlen_mod, torch.bfloat16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                        max_seqlen_k, softmax_scale, k, v, k_cache, v_cache, block_tables, softcap, slopes, window,
+                        key_starts, prefix_lens, out, stream)
+
+
+def pkv_prefill_varlen_mod_f16(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale, *, k=None,
+                               v=None, k_cache=None, v_cache=None, block_tables=None, softcap=0.0, slopes=None,
+                               window=0, key_starts=None, prefix_lens=None, out=None, stream=None):
+    """pkv_prefill_varlen_mod on fp16 tensors; returns fp16."""
+    return _prefill_mod(_lib.pkv_prefill_varlen_mod_f16, torch.float16, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                        max_seqlen_k, softmax_scale, k, v, k_cache, v_cache, block_tables, softcap, slopes, window,
+                        key_starts, prefix_lens, out, stream)
 
 
 def pkv_evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, max_context_len, budget, *, first=0,

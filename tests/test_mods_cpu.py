@@ -62,3 +62,28 @@ def test_evict_refusals(lib):
     for name in ("w", "bt", "cl", "nt", "kept", "nl"):
         assert f(**{name: ctypes.c_void_p(18)}) == -4
     assert f(n=0, kc=None) == 0
+
+
+@pytest.mark.parametrize("suffix", ["", "_f16"])
+def test_prefill_refusals(lib, suffix):
+    pre = getattr(lib, "pkv_prefill_varlen_mod" + suffix)
+
+    def f(q=ONE, qs=2048, tq=10, k=None, v=None, ks=0, tk=0, kc=ONE, vc=ONE, nb=4, cq=ONE, ck=ONE, mq=10, mk=10, bt=ONE,
+          bs=2, n=1, hq=16, hkv=8, d=128, blk=256, sc=0.1, cap=0.0, sl=None, win=0, st=None, pl=None, out=ONE):
+        return pre(q, qs, tq, k, v, ks, tk, kc, vc, nb, cq, ck, mq, mk, bt, bs, n, hq, hkv, d, blk, sc, cap, sl, win, st, pl,
+                   out, None)
+
+    flat = dict(bt=None, kc=None, vc=None, k=ONE, v=ONE, ks=1024, tk=10)
+    assert f(d=64) == f(blk=16) == f(hq=12) == f(hkv=0) == f(hq=8200, hkv=8200) == -2
+    for name in ("n", "tq", "tk", "mq", "mk", "win"):
+        assert f(**{name: -1}) == -6
+    assert f(n=65536) == f(mq=(1 << 24) + 1) == f(mk=(1 << 24) + 1) == f(nb=0) == f(nb=1 << 23) == f(bs=0) == -6
+    assert f(**{**flat, "tk": 0}) == f(sc=0.0) == f(sc=float("inf")) == f(cap=-1.0) == f(cap=float("nan")) == -6
+    for name in ("q", "out", "cq", "ck", "kc", "vc"):
+        assert f(**{name: None}) == -1
+    assert f(**{**flat, "k": None}) == f(**{**flat, "v": None}) == -1
+    assert f(qs=2047) == f(**{**flat, "ks": 1023}) == -3
+    assert f(q=ODD) == f(qs=2052) == f(out=ODD) == f(kc=ODD) == f(vc=ODD) == f(**{**flat, "ks": 1028}) == -4
+    for name in ("sl", "st", "pl"):
+        assert f(**{name: ctypes.c_void_p(18)}) == -4
+    assert f(n=0, q=None) == f(tq=0, q=None) == f(mq=0, q=None) == 0
