@@ -9,16 +9,21 @@
 // between its rows' smallest lo and largest hi and nothing else; a warp (32 rows) masks single scores only in tiles that
 // one of its rows' ranges ends in, and writes zeros without any arithmetic for tiles that none of its rows sees.
 //
-// The machine is that of the causal kernel without modifications: two softmax groups of four warps, 128 query rows each,
-// one issuing thread, one TMA warp, a ring of three 32 KB tiles. The two groups are two query heads of one kv head at the
+// The machine is that of the causal kernel without modifications: two softmax groups, 128 query rows each, one issuing
+// thread, one TMA warp, a ring of three 32 KB tiles; but eight warps to a group, two threads to a row. The two groups are two query heads of one kv head at the
 // same rows, or, where a kv head has an odd number of query heads, one head at two neighbouring tiles of rows: either
 // way one K and one V tile serves both.
 //
-// tanh: the softmax is issue-limited, and tanh through exponential and reciprocal would triple its 16-a-clock special
-// function work (128 x 128 scores a group: 2 us a tile of 1.6). An odd polynomial on packed pairs costs 5 instructions a
-// pair where all of a warp's |x| <= 0.5 cap (4 terms), 7 up to the cap (6 terms); only a tile with scores beyond goes
-// through 1 - 2 / (1 + e^2x). All three are off by at most 6.1e-7 of the score, 2^-15 at a score of 50: far below what
-// rounding p to 16 bits loses (fp16 keeps 2^-11). The coefficients are least-maximum fits of tanh(x) / x on those ranges.
+// tanh: the softmax is issue-limited, and tanh through exponential and reciprocal would triple its special function
+// work (128 x 128 scores a group: 2 us a tile of 1.6). An odd polynomial on packed pairs costs 4 instructions a pair for
+// bf16 where all of a warp's |x| <= 0.4 cap, 6 up to the cap (fp16: one more each); only a tile with scores beyond goes
+// through 1 - 2 / (1 + e^2x). A score is off by at most 7e-6 of itself for bf16 (p by 2^-12 at a score of 32, where its
+// rounding to 16 bits loses 2^-9) and 6e-7 for fp16 (2^-15; 2^-12).
+//
+// The maximum: rows go by a reference that is moved when a score passes it by 2^8 and subtracted where the scores are
+// scaled, so a tile needs one pass for the largest value and nothing else. Scores of bf16 rows capped at 52 or less
+// need none at all: 2^z lies within 2^-75 .. 2^75, sums of it times v within fp32 (|v| up to 2^52; beyond, the row is
+// computed again, see below), and bf16 keeps the same relative precision there as near 1.
 //
 // Values of V at keys that a row does not see are multiplied by p = 0; where they are not finite the sum is spoilt
 // (0 * NaN). The rows of V behind the sequence's end, which may hold anything, are zeroed in shared memory. Elsewhere
@@ -63,7 +68,9 @@ constexpr int kBN = 128;
 constexpr int kTileBytes = 128 * kHeadDim * 2;  // 32 KB
 constexpr int kHalfBytes = kTileBytes / 2;      // 16 KB: 128 rows x 64 dims
 constexpr int kKvSlots = 3;
-constexpr int kThreads = 320;
+constexpr int kSoftmaxWarps = 16;                // 8 to a group: two threads share a row, 64 of its keys (and dims) each
+constexpr int kThreads = (4 + kSoftmaxWarps) * 32;
+constexpr int kCols = kBN / 2;                   // scores to a thread
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kOffQ = 0;                                // 2 tiles
@@ -78,18 +85,36 @@ constexpr int kBarPReady = kBarSFull + 2;         // +group
 constexpr int kBarOFinal = kBarPReady + 2;
 constexpr int kBarVTail = kBarOFinal + 1;
 constexpr int kBarDrain = kBarVTail + 1;
-constexpr int kBarStaged = kBarDrain + 1;         // the 8 softmax warps have staged their O rows
+constexpr int kBarStaged = kBarDrain + 1;         // the softmax warps have staged their O rows
 constexpr int kNumBars = kBarStaged + 1;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag, smallest lo and largest hi per softmax warp,
+constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag, smallest lo and largest hi of 32 rows,
 constexpr int kMiscBytes = 8 + 16 * 4 + 8 * 4;    // rows to be computed once more
-constexpr size_t kSmemBytes = kOffMisc + kMiscBytes + 1024;  // + alignment slack
+constexpr int kOffMax = kOffMisc + kMiscBytes;    // [group][half][row] bf16: the halves' largest scores
+constexpr size_t kSmemBytes = kOffMax + 4 * kBM * 2 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
-// tanh x = x (c0 + c1 x^2 + ...): relative error 5.6e-7 for |x| <= 0.5, 6.1e-7 for |x| <= 1
-constexpr double kTanh4[4] = {0.9999994557571216, -0.33326317896947046, 0.13190296288204925, -0.044402218547957305};
-constexpr double kTanh6[6] = {0.9999994135741078,    -0.3332904232451419,  0.13281433250603616,
-                              -0.051605653809187996, 0.016743090747062123, -0.0030670504021806768};
-constexpr double kTop4 = 0.5, kTop6 = 1.0;
+// tanh x = x (c0 + c1 x^2 + ...), least-maximum fits of tanh(x) / x: for bf16 off by 6.3e-6 of the result for |x| <= 0.4
+// and 6.9e-6 for |x| <= 1, for fp16 by 5.6e-7 for |x| <= 0.5 and 6.1e-7 for |x| <= 1.
+template <Elem E>
+struct TanhFit;
+template <>
+struct TanhFit<Elem::kBF16> {
+  static constexpr int kNear = 3, kFar = 5;
+  static constexpr double kNearTop = 0.4, kFarTop = 1.0;
+  static constexpr double kNearC[6] = {0.9999937530753578, -0.33262579162588246, 0.12127784712702376};
+  static constexpr double kFarC[6] = {0.9999930890836747, -0.3329806490410056, 0.13036809964236198,
+                                      -0.04481753658422978, 0.009036415875549408};
+};
+template <>
+struct TanhFit<Elem::kF16> {
+  static constexpr int kNear = 4, kFar = 6;
+  static constexpr double kNearTop = 0.5, kFarTop = 1.0;
+  static constexpr double kNearC[6] = {0.9999994557571216, -0.33326317896947046, 0.13190296288204925,
+                                       -0.044402218547957305};
+  static constexpr double kFarC[6] = {0.9999994135741078,    -0.3332904232451419,  0.13281433250603616,
+                                      -0.051605653809187996, 0.016743090747062123, -0.0030670504021806768};
+};
+constexpr float kFixedCap = 52.f;  // bf16: scores capped here and below need no running maximum
 
 struct PrefillModParams {
   const int32_t* cu_q;
@@ -104,9 +129,11 @@ struct PrefillModParams {
   int32_t units;          // head pairs, or heads
   float scale, scale_log2;
   float softcap;
-  float cap_log2, scale_by_cap, top4, top6;  // largest |q.k| that the polynomials take (0: none but zeros)
-  float c4[4], c6[6];                        // of z in log2 units, by powers of q.k
-  float tanh6[6];
+  float cap_log2, scale_by_cap;
+  float near_top, far_top;      // largest |q.k| that the polynomials take (0: none but zeros)
+  float near_c[6], far_c[6];    // of z in log2 units, by powers of q.k
+  float tanh_c[6];              // kFarC
+  int32_t fixed;                // no running maximum
   const float* slopes;
   int32_t window;
   const int32_t* key_starts;
@@ -165,11 +192,6 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -177,46 +199,47 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // cap * tanh(x / cap) in log2 units, for any x = q.k; the polynomial where the difference from 1 would lose bits
+template <int N>
 __device__ __forceinline__ float capped(float x, const PrefillModParams& p) {
   const float t = x * p.scale_by_cap, v = t * t;
-  float r = p.tanh6[5];
+  float r = p.tanh_c[N - 1];
 #pragma unroll
-  for (int i = 4; i >= 0; --i) r = fmaf(r, v, p.tanh6[i]);
+  for (int i = N - 2; i >= 0; --i) r = fmaf(r, v, p.tanh_c[i]);
   const float far = fmaf(-2.f, rcp_approx(1.f + ex2_approx(t * (2.f * kLog2e))), 1.f);
-  return p.cap_log2 * (fabsf(t) <= static_cast<float>(kTop6) ? t * r : far);
+  return p.cap_log2 * (fabsf(t) <= 1.f ? t * r : far);
 }
 template <int N>
-__device__ __forceinline__ void cap_all(float (&s)[128], const float (&coef)[N]) {
+struct Poly2 {  // the polynomial of a pair, plus `add`
   uint64_t c[N];
+  __device__ __forceinline__ explicit Poly2(const float* coef) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) c[i] = f32x2_pack(coef[i], coef[i]);
-#pragma unroll
-  for (int j = 0; j < 128; j += 2) {
-    const uint64_t x = f32x2_pack(s[j], s[j + 1]);
+    for (int i = 0; i < N; ++i) c[i] = f32x2_pack(coef[i], coef[i]);
+  }
+  __device__ __forceinline__ uint64_t operator()(uint64_t x, uint64_t add) const {
     const uint64_t v = f32x2_mul(x, x);
     uint64_t r = c[N - 1];
 #pragma unroll
     for (int i = N - 2; i >= 0; --i) r = f32x2_fma(r, v, c[i]);
-    f32x2_unpack(f32x2_mul(x, r), s[j], s[j + 1]);
+    return f32x2_fma(x, r, add);
   }
-}
-__device__ __forceinline__ float max_all(const float (&s)[128]) {
+};
+__device__ __forceinline__ float max_all(const float (&s)[kCols]) {
   float a = s[0], b = s[1];
 #pragma unroll
-  for (int j = 2; j < 126; j += 4) {
+  for (int j = 2; j < kCols - 2; j += 4) {
     a = fmax3(a, s[j], s[j + 1]);
     b = fmax3(b, s[j + 2], s[j + 3]);
   }
-  return fmaxf(fmax3(a, s[126], s[127]), b);
+  return fmaxf(fmax3(a, s[kCols - 2], s[kCols - 1]), b);
 }
-__device__ __forceinline__ float min_all(const float (&s)[128]) {
-  float a = s[0], b = s[1];
+__device__ __forceinline__ float size_all(const float (&s)[kCols]) {  // the largest |s|
+  float a = fabsf(s[0]), b = fabsf(s[1]);
 #pragma unroll
-  for (int j = 2; j < 126; j += 4) {
-    a = fmin3(a, s[j], s[j + 1]);
-    b = fmin3(b, s[j + 2], s[j + 3]);
+  for (int j = 2; j < kCols - 2; j += 4) {
+    a = fmax3(a, fabsf(s[j]), fabsf(s[j + 1]));
+    b = fmax3(b, fabsf(s[j + 2]), fabsf(s[j + 3]));
   }
-  return fminf(fmin3(a, s[126], s[127]), b);
+  return fmaxf(fmax3(a, fabsf(s[kCols - 2]), fabsf(s[kCols - 1])), b);
 }
 
 // One (row, query head) by a whole warp from the rows in memory: a key to a lane, then four dims to a lane.
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* s_lo = reinterpret_cast<int*>(smem + kOffMisc + 8);               // [8] smallest lo of a softmax warp's rows
+  int* s_lo = reinterpret_cast<int*>(smem + kOffMisc + 8);               // [8] smallest lo of 32 rows
   int* s_hi = s_lo + 8;                                                  // [8] largest hi
   uint32_t* s_again = reinterpret_cast<uint32_t*>(s_hi + 8);             // [2][4] rows to be computed once more
 
@@ -317,29 +340,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (r0 >= Lq) return;
 
   // The softmax thread of a row: its position and the keys it sees. Rows behind the last one take its place.
-  const int g = (warp - 2) >> 2;
+  const int g = (warp - 4) >> 3, half = (warp >> 2) & 1 ? 0 : 1;  // warps 4..7 and 12..15 take the first keys of a tile
+  const int rows32 = 4 * g + (warp & 3);                           // the warp's 32 rows, of 8 times 32
   const int row = (warp & 3) * 32 + lane;  // within the group's tile == TMEM lane
   const int g_row0 = r0 + (p.neighbours && g > 0 ? kBM : 0);
   const int pos = Lk - Lq + min(g_row0 + row, Lq - 1);
-  int lo = 0, hi = 0;
-  if (warp >= 2) {
+  int lo = 0, hi = 0, any_lo = 0, any_hi = 0;  // seen by the row; by any of the warp's rows
+  if (warp >= 4) {
     lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
     if (p.key_starts) lo = max(lo, p.key_starts[cq0 + min(g_row0 + row, Lq - 1)]);
     hi = min(Lk, max(pos + 1, p.prefix_lens ? p.prefix_lens[b] : 0));
     // a row without keys widens nothing
-    const int warp_lo = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX);
-    const int warp_hi = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
-    if (lane == 0) {
-      s_lo[warp - 2] = warp_lo;
-      s_hi[warp - 2] = warp_hi;
-      s_again[warp - 2] = 0;
+    any_lo = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX);
+    any_hi = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
+    if (lane == 0 && half == 0) {
+      s_lo[rows32] = any_lo;
+      s_hi[rows32] = any_hi;
+      s_again[rows32] = 0;
     }
   }
 
   // Thread 0 is the TMA warp's issuing lane: the queries are on their way before anything else is set up.
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), (i == kBarPReady || i == kBarPReady + 1) ? 4 : (i == kBarStaged ? 8 : 1));
+      mbar_init(bar(i), i == kBarStaged ? kSoftmaxWarps : (i == kBarPReady || i == kBarPReady + 1 ? 8 : 1));
     *s_abort = 0;
     mbar_fence_init();
     prefetch_tmap(&tm_q);
@@ -511,166 +535,166 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(kBarDrain), 0, p.err);
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // =========================== softmax groups ===========================
-    const int quad = warp & 3;
     const int head = head0 + (p.neighbours ? 0 : g);
-    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_base + g * 128;
-    const uint32_t tO = tmem + lane_base + 256 + g * 128;
-    const uint32_t prow = sbase + kOffP + g * kTileBytes + row * 128;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + g * 128 + half * kCols;
+    const uint32_t tO = tmem + lane_base + 256 + g * 128 + half * kCols;
+    const uint32_t prow = sbase + kOffP + g * kTileBytes + half * kHalfBytes + row * 128;
     const int swz = row & 7;
     const float sl2 = p.scale_log2;
     const float slope = kBias ? p.slopes[head] * kLog2e : 0.f;
-    // what the warp's rows have in common
-    const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);  // seen by all
-    const int any_lo = s_lo[warp - 2], any_hi = s_hi[warp - 2];                                         // by any
+    const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);  // seen by all rows
     const int min_pos = __reduce_min_sync(0xffffffffu, pos);
-    float m = -INFINITY;  // running max, log2 units
-    float l = 0.f;
+    __nv_bfloat16* s_max = reinterpret_cast<__nv_bfloat16*>(smem + kOffMax) + 2 * g * kBM + row;  // [half][row]
+    // Named barrier of the two warps. Both come to it once per tile and once at the end, whatever happens, so it needs no
+    // time limit.
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + rows32) : "memory"); };
+    const bool by_maximum = !kCap || kBias || !p.fixed;
+    float m = -INFINITY;  // the row's reference, log2 units; within 8 of its running maximum from below, or fixed at 0
+    float l = 0.f;        // of this thread's keys
     bool ok = true;
     for (int n = 0; n < n_tiles; ++n) {
       // every lane waits (each needs the acquire); the warp then agrees, so
       // the warp-collective tensor-memory loads below run on all 32 lanes
-      ok = wait_or_abort(bar(kBarSFull + g), n & 1, s_abort, p.err);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int key0 = (tile0 + n) * kBN;
-      if (key0 + kBN <= any_lo || key0 >= any_hi) {  // no row sees any of these keys
-#pragma unroll
-        for (int c = 0; c < 16; ++c) sts128(prow + (c >> 3) * kHalfBytes + (((c & 7) ^ swz) << 4), 0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPReady + g));
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarSFull + g), n & 1, s_abort, p.err));
+      if (!ok) {  // the other warp of these rows may still come to the pair's barrier
+        if (by_maximum) pair_sync();
         continue;
       }
-      float s[128];
-      {
-        uint32_t r0_[32], r1[32], r2[32], r3[32];
-        tmem_ld32(tS + 0, r0_);
-        tmem_ld32(tS + 32, r1);
-        tmem_ld32(tS + 64, r2);
-        tmem_ld32(tS + 96, r3);
-        tmem_wait_ld();
-        tmem_reg_fence(r0_);
-        tmem_reg_fence(r1);
-        tmem_reg_fence(r2);
-        tmem_reg_fence(r3);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          s[j] = __uint_as_float(r0_[j]);
-          s[32 + j] = __uint_as_float(r1[j]);
-          s[64 + j] = __uint_as_float(r2[j]);
-          s[96 + j] = __uint_as_float(r3[j]);
-        }
-      }
-      const bool edge = key0 < all_lo || key0 + kBN > all_hi;
-      float mx = 0.f;
-      if (kCap) {
-        mx = max_all(s);
-        const float top = fmaxf(mx, -min_all(s));
-        if (__all_sync(0xffffffffu, top <= p.top4)) {
-          cap_all<4>(s, p.c4);
-        } else if (__all_sync(0xffffffffu, top <= p.top6)) {
-          cap_all<6>(s, p.c6);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 128; ++j) s[j] = capped(s[j], p);
-        }
-        mx = capped(mx, p);
-      }
-      if (kBias) {
-        const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
-        if (key0 + kBN - 1 <= min_pos) {  // all keys at or before all rows: - slope (pos - t) grows by slope a key
-          const float base = -slope * static_cast<float>(pos - key0);
-          const uint64_t step = f32x2_pack(8.f * slope, 8.f * slope);
-          uint64_t at[4];
-#pragma unroll
-          for (int a = 0; a < 4; ++a) at[a] = f32x2_pack(fmaf(slope, 2.f * a, base), fmaf(slope, 2.f * a + 1.f, base));
-#pragma unroll
-          for (int j = 0; j < 128; j += 2) {
-            uint64_t& t = at[(j >> 1) & 3];
-            const uint64_t x = f32x2_pack(s[j], s[j + 1]);
-            f32x2_unpack(kCap ? f32x2_add(x, t) : f32x2_fma(x, sl2x2, t), s[j], s[j + 1]);
-            t = f32x2_add(t, step);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            s[j] = fmaf(-slope, fabsf(static_cast<float>(pos - key0 - j)), kCap ? s[j] : s[j] * sl2);
-        }
-      }
-      if (edge) {
-        const int jlo = lo - key0, jhi = hi - key0;  // keys j with jlo <= j < jhi are visible
-        if (key0 < all_lo) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (j < jlo) s[j] = -INFINITY;
-        }
-        if (key0 + kBN > all_hi) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (j >= jhi) s[j] = -INFINITY;
-        }
-      }
-      // Row max, row sum and the exponent arguments use the 3-input max and the
-      // packed fp32x2 instructions: the tile's softmax is issue-limited.
-      if (edge || kBias || !kCap) {
-        mx = max_all(s);
-        if (!kCap && !kBias) mx *= sl2;
-      }
-      float m_use = m;
-      if (mx > m + 8.0f) m_use = mx;  // move the max only when it grows by > 2^8
-      const float alpha = m_use == m ? 1.f : ex2_approx(m - m_use);
-      l *= alpha;
-      // P = 2^(z - m_use), rounded to the element type, into the swizzled K-major A tile
-      const float m_sub = m_use == -INFINITY ? 0.f : m_use;  // no key seen yet: all of P is 2^-inf
-      const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
-      const uint64_t negm2 = f32x2_pack(-m_sub, -m_sub);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-#pragma unroll
-        for (int j = c * 8; j < c * 8 + 8; j += 2) {
-          float a0, a1;
-          const uint64_t x = f32x2_pack(s[j], s[j + 1]);
-          f32x2_unpack(kCap || kBias ? f32x2_add(x, negm2) : f32x2_fma(x, sl2x2, negm2), a0, a1);
-          s[j] = ex2_approx(a0);
-          s[j + 1] = ex2_approx(a1);
-        }
-        const uint32_t addr = prow + (c >> 3) * kHalfBytes + (((c & 7) ^ swz) << 4);
-        const float* e = s + c * 8;
-        sts128(addr, Ops::pack(e[0], e[1]), Ops::pack(e[2], e[3]), Ops::pack(e[4], e[5]), Ops::pack(e[6], e[7]));
-      }
-      m = m_use;
-      // rescale the running output (PV of tile n - 1 is complete: S of tile n was issued after it)
-      if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-        for (int c = 0; c < 16; ++c) {
-          uint32_t r[8];
-          tmem_ld8(tO + c * 8, r);
+      tc_fence_after();
+      const int key0 = (tile0 + n) * kBN + half * kCols;
+      const bool none = key0 + kCols <= any_lo || key0 >= any_hi;  // no row sees any of these keys
+      float s[kCols], mx = -INFINITY;
+      const float base = m == -INFINITY ? 0.f : m;
+      if (!none) {
+        {
+          uint32_t x0[32], x1[32];
+          tmem_ld32(tS + 0, x0);
+          tmem_ld32(tS + 32, x1);
           tmem_wait_ld();
-          tmem_reg_fence8(r);
+          tmem_reg_fence(x0);
+          tmem_reg_fence(x1);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-          tmem_st8(tO + c * 8, r);
+          for (int j = 0; j < 32; ++j) {
+            s[j] = __uint_as_float(x0[j]);
+            s[32 + j] = __uint_as_float(x1[j]);
+          }
         }
-        tmem_wait_st();
+        auto each = [&](auto arg) {
+#pragma unroll
+          for (int j = 0; j < kCols; j += 2) f32x2_unpack(arg(j, f32x2_pack(s[j], s[j + 1])), s[j], s[j + 1]);
+        };
+        // ---- s = z - base, base the row's reference so far (0 as long as it has seen no key) ----
+        const uint64_t neg = f32x2_pack(-base, -base);
+        if (kCap) {
+          using Fit = TanhFit<E>;
+          const float size = size_all(s);
+          if (__all_sync(0xffffffffu, size <= p.near_top)) {
+            const Poly2<Fit::kNear> poly(p.near_c);
+            each([&](int, uint64_t x) { return poly(x, neg); });
+          } else if (__all_sync(0xffffffffu, size <= p.far_top)) {
+            const Poly2<Fit::kFar> poly(p.far_c);
+            each([&](int, uint64_t x) { return poly(x, neg); });
+          } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) s[j] = capped<Fit::kFar>(s[j], p) - base;
+          }
+        }
+        if (kBias) {
+          const float less = kCap ? 0.f : base;
+          if (key0 + kCols - 1 <= min_pos) {  // all keys at or before all rows: - slope (pos - t) grows by slope a key
+            const float first = -slope * static_cast<float>(pos - key0) - less;
+            const uint64_t sl2x2 = f32x2_pack(sl2, sl2), step = f32x2_pack(8.f * slope, 8.f * slope);
+            uint64_t at[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) at[a] = f32x2_pack(fmaf(slope, 2.f * a, first), fmaf(slope, 2.f * a + 1.f, first));
+            each([&](int j, uint64_t x) {
+              uint64_t& t = at[(j >> 1) & 3];
+              const uint64_t y = kCap ? f32x2_add(x, t) : f32x2_fma(x, sl2x2, t);
+              t = f32x2_add(t, step);
+              return y;
+            });
+          } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+              s[j] = fmaf(-slope, fabsf(static_cast<float>(pos - key0 - j)), kCap ? s[j] : fmaf(s[j], sl2, -less));
+          }
+        }
+        if (!kCap && !kBias) {
+          const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
+          each([&](int, uint64_t x) { return f32x2_fma(x, sl2x2, neg); });
+        }
+        if (key0 < all_lo || key0 + kCols > all_hi) {  // some row does not see all of the keys
+          const int jlo = lo - key0, jhi = hi - key0;  // this one sees keys j with jlo <= j < jhi
+#pragma unroll
+          for (int w = 0; w < kCols / 32; ++w) {
+            const int a = min(max(jlo - 32 * w, 0), 32), z = min(max(jhi - 32 * w, 0), 32);
+            const uint32_t seen = a < z ? (0xffffffffu << a) & (0xffffffffu >> (32 - z)) : 0u;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[32 * w + j] = (seen >> j) & 1u ? s[32 * w + j] : -INFINITY;
+          }
+        }
+        if (by_maximum) mx = max_all(s) + base;
+      }
+      if (by_maximum) {
+        // The reference moves to the row's largest score when that is above it by more than 8 (2^8 of headroom), and to
+        // the first tile's in which the row sees a key. Its two threads tell one another theirs (rounded: any value near
+        // will do); the place is free again, since the tile's scores are only there once both were done with the last.
+        const __nv_bfloat16 mine = __float2bfloat16_rn(mx);
+        s_max[half * kBM] = mine;
+        pair_sync();
+        const float to = fmaxf(__bfloat162float(mine), __bfloat162float(s_max[(half ^ 1) * kBM]));
+        const bool move = to > (m == -INFINITY ? m : m + 8.f);
+        if (__any_sync(0xffffffffu, move)) {
+          const float delta = move ? base - to : 0.f;
+          const uint64_t less = f32x2_pack(delta, delta);
+#pragma unroll
+          for (int j = 0; j < kCols; j += 2) f32x2_unpack(f32x2_add(f32x2_pack(s[j], s[j + 1]), less), s[j], s[j + 1]);
+          const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - to));
+          if (move) m = to;
+          l *= alpha;
+          if (n > 0) {  // the running output too (PV of tile n - 1 is complete: S of tile n was issued after it)
+#pragma unroll 1
+            for (int c = 0; c < kCols / 8; ++c) {
+              uint32_t r[8];
+              tmem_ld8(tO + c * 8, r);
+              tmem_wait_ld();
+              tmem_reg_fence8(r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+              tmem_st8(tO + c * 8, r);
+            }
+            tmem_wait_st();
+          }
+        }
+      }
+      // P = 2^s, rounded to the element type, into the swizzled K-major A tile
+      if (!none) {
+#pragma unroll
+        for (int c = 0; c < kCols / 8; ++c) {
+#pragma unroll
+          for (int j = c * 8; j < c * 8 + 8; ++j) s[j] = ex2_approx(s[j]);
+          const float* e = s + c * 8;
+          sts128(prow + ((c ^ swz) << 4), Ops::pack(e[0], e[1]), Ops::pack(e[2], e[3]), Ops::pack(e[4], e[5]),
+                 Ops::pack(e[6], e[7]));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols / 8; ++c) sts128(prow + ((c ^ swz) << 4), 0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarPReady + g));
       // The row sum is not needed for P: add it up after P is handed over.
-      {
+      if (!none) {
         uint64_t acc[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) acc[a] = f32x2_pack(s[2 * a], s[2 * a + 1]);
 #pragma unroll
-        for (int j = 8; j < 128; j += 8)
+        for (int j = 8; j < kCols; j += 8)
 #pragma unroll
           for (int a = 0; a < 4; ++a) acc[a] = f32x2_add(acc[a], f32x2_pack(s[j + 2 * a], s[j + 2 * a + 1]));
         float t0, t1, t2, t3, t4, t5, t6, t7;
@@ -682,25 +706,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), 0, s_abort, p.err));
-    // Epilogue. Every product is complete, so the two P buffers (64 KB) are
-    // free: each thread stages its normalised O row there (the rows of the two
-    // groups side by side, 512 B, 16-byte chunks rotated by the row to spread
-    // the banks), then each warp stores whole rows.
+    // Epilogue. Every product is complete, so the K/V ring and the two P buffers are free: a row's two threads add up
+    // their sums through the one, each stages its half of the normalised O row in the other (the rows of the two groups
+    // side by side, 512 B, 16-byte chunks rotated by the row to spread the banks), then each warp stores whole rows.
     const uint32_t stage = sbase + kOffP;
-    uint32_t again = 0;
+    float* s_sum = reinterpret_cast<float*>(smem + kOffKV) + 2 * g * kBM + row;  // [half][row]
+    if (ok) s_sum[half * kBM] = l;
+    pair_sync();
+    if (ok) l += s_sum[(half ^ 1) * kBM];
     if (ok) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float spoilt = 0.f;  // NaN once any element is not finite
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kCols / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(tO + c * 32, r);
         tmem_wait_ld();
         tmem_reg_fence(r);
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
-          const int q = g * 16 + c * 4 + j / 8;  // 16-byte chunk of the 512-byte row
+          const int q = g * 16 + half * 8 + c * 4 + j / 8;  // 16-byte chunk of the 512-byte row
           sts128(stage + row * 512 + ((q ^ (row & 31)) << 4),
                  Ops::pack(__uint_as_float(r[j + 0]) * inv, __uint_as_float(r[j + 1]) * inv),
                  Ops::pack(__uint_as_float(r[j + 2]) * inv, __uint_as_float(r[j + 3]) * inv),
@@ -710,10 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) spoilt = fmaf(__uint_as_float(r[j]), 0.f, spoilt);
       }
-      again = __ballot_sync(0xffffffffu, isnan(spoilt) && g_row0 + row < Lq);
-      if (lane == 0 && again) s_again[4 * g + quad] = again;
+      const uint32_t again = __ballot_sync(0xffffffffu, isnan(spoilt) && g_row0 + row < Lq);
+      if (lane == 0 && again) atomicOr(s_again + rows32, again);
     }
-    // all 8 softmax warps arrive, whatever happened, so the wait below (and
+    // all softmax warps arrive, whatever happened, so the wait below (and
     // warp 1's before releasing TMEM) always ends; every tensor-memory read of
     // this warp is complete here
     tc_fence_before();
@@ -726,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* obase = p.out + (static_cast<int64_t>(cq0 + to_row0) * p.hq + head0 + (p.neighbours ? 0 : to_g)) * kHeadDim +
                         (lane & 15) * 8;
       const uint32_t* skip = s_again + 4 * to_g;
-      for (int rr = warp - 2; rr < min(kBM, Lq - r0); rr += 8) {
+      for (int rr = warp - 4; rr < min(kBM, Lq - r0); rr += kSoftmaxWarps) {
         uint32_t a, b2, c2, d;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(a), "=r"(b2), "=r"(c2), "=r"(d)
@@ -734,10 +760,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (to_row0 + rr < Lq && !((skip[rr >> 5] >> (rr & 31)) & 1u))
           *reinterpret_cast<uint4*>(obase + static_cast<int64_t>(rr) * p.hq * kHeadDim) = make_uint4(a, b2, c2, d);
       }
-      for (; again; again &= again - 1) {
+      for (uint32_t again = half == 0 ? s_again[rows32] : 0; again; again &= again - 1) {
         const int src = __ffs(again) - 1;
-        row_again<E>(p, b, ck0, static_cast<int64_t>(cq0) + g_row0 + quad * 32 + src, head,
-                     __shfl_sync(0xffffffffu, pos, src), max(0, __shfl_sync(0xffffffffu, lo, src)),
+        row_again<E>(p, b, ck0, static_cast<int64_t>(cq0) + g_row0 + (warp & 3) * 32 + src, head,
+                     __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, lo, src),
                      __shfl_sync(0xffffffffu, hi, src), lane);
       }
     }
@@ -815,6 +841,22 @@ cudaError_t launch_elem(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
                   : launch_typed<E, false, false>(tq, tk, tv, p, blocks, stream);
 }
 
+// z = sum over i of scale_log2 c_i c^2i (q.k)^(2i + 1), c = scale / cap. Where the powers of c leave fp32's range (odd
+// scales, far from any use) the first polynomial is kept to |x| <= 0.02 cap, where its last terms are nothing, and the
+// second is not used.
+template <Elem E>
+void fit_tanh(PrefillModParams& p) {
+  using Fit = TanhFit<E>;
+  const double c = static_cast<double>(p.scale) / p.softcap, s = static_cast<double>(p.scale) * 1.4426950408889634;
+  for (int i = 0; i < 6; ++i) {
+    p.near_c[i] = static_cast<float>(s * Fit::kNearC[i] * std::pow(c, 2 * i));
+    p.far_c[i] = static_cast<float>(s * Fit::kFarC[i] * std::pow(c, 2 * i));
+    p.tanh_c[i] = static_cast<float>(Fit::kFarC[i]);
+  }
+  p.near_top = c < 100 ? static_cast<float>(std::fmin((c > 1e-5 ? Fit::kNearTop : 0.02) / c, 1e18)) : 0.f;
+  p.far_top = c < 100 && c > 1e-3 ? static_cast<float>(Fit::kFarTop / c) : 0.f;
+}
+
 cudaError_t launch_prefill_mod(const PrefillModArgs& a, unsigned int* err, cudaStream_t stream, Elem elem) {
   const bool paged = a.block_tables != nullptr;
   const int64_t kv_rows = paged ? static_cast<int64_t>(a.num_blocks) * kBlockSize : a.total_k;
@@ -848,15 +890,8 @@ cudaError_t launch_prefill_mod(const PrefillModArgs& a, unsigned int* err, cudaS
   if (a.softcap > 0.f) {
     p.cap_log2 = a.softcap * kLog2e;
     p.scale_by_cap = a.scale / a.softcap;
-    // z = sum over i of scale_log2 c_i c^2i (q.k)^(2i + 1), c = scale / cap. Where the powers of c leave fp32's range
-    // (odd scales, far from any use) the first polynomial is kept to |x| <= 0.02 cap, where its last terms are nothing,
-    // and the second is not used.
-    const double c = static_cast<double>(a.scale) / a.softcap, s = static_cast<double>(a.scale) * 1.4426950408889634;
-    for (int i = 0; i < 4; ++i) p.c4[i] = static_cast<float>(s * kTanh4[i] * std::pow(c, 2 * i));
-    for (int i = 0; i < 6; ++i) p.c6[i] = static_cast<float>(s * kTanh6[i] * std::pow(c, 2 * i));
-    for (int i = 0; i < 6; ++i) p.tanh6[i] = static_cast<float>(kTanh6[i]);
-    p.top4 = c < 100 ? static_cast<float>(std::fmin((c > 1e-5 ? kTop4 : 0.02) / c, 1e18)) : 0.f;
-    p.top6 = c < 100 && c > 1e-3 ? static_cast<float>(kTop6 / c) : 0.f;
+    elem == Elem::kF16 ? fit_tanh<Elem::kF16>(p) : fit_tanh<Elem::kBF16>(p);
+    p.fixed = elem == Elem::kBF16 && a.softcap <= kFixedCap;
   }
   p.slopes = a.slopes;
   p.window = a.window;
