@@ -64,7 +64,7 @@ constexpr int kMinUnits = 2;                        // units to a range at least
 constexpr int kOffBars = kWarps * kStages * 2 * kUnitBytes;
 constexpr int kOffScan = kOffBars + kWarps * kStages * 8;
 constexpr size_t kSmemBytes = kOffScan + (kThreads + kWarps + 1) * 8 + 1024;  // + alignment slack
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // How a call's heads are cut into streams: parts of up to 8 or 16 query heads of one kv head.
@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = sbase + warp * kStages * 2 * kUnitBytes;
   const uint32_t bars = sbase + kOffBars + warp * kStages * 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be set up beside this one
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
     mbar_fence_init();
@@ -569,33 +570,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partial results of one query head of the sequence that begins in a range and goes on behind it.
-template <Elem E>
-__global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(const DecodeModParams p) {
-  using Ops = ElemOps<E>;
-  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
-  __shared__ float4 s_o[kMergeWarps][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t units = p.info[0].units;
-  const int ranges = p.info[0].ranges;
-  const int range = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
-  if (range >= ranges) return;
-  const RangeInfo info = p.info[1 + range];
-  if (info.seq < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = h / p.st.group, in_group = h - hk * p.st.group, part = in_group / p.st.per;
-  const int stream = hk * p.st.parts + part, in_part = in_group - part * p.st.per;
-  // the range that holds the sequence's last unit
-  const int last = static_cast<int>(((info.first_unit + info.units) * ranges - 1) / units);
-  float M = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 4;
-  for (int r0 = range + warp; r0 <= last; r0 += kMergeWarps * kAhead) {
+// Partial results r = first, first + step, ... up to last of one query head, joined: (max, sum) and four dims to a lane.
+__device__ __forceinline__ void join(const DecodeModParams& p, const RangeInfo& info, int64_t units, int ranges, int stream,
+                                     int in_part, int first, int last, int step, int lane, float& M, float& L, float4& o) {
+  constexpr int kAhead = 5;
+  M = -INFINITY;
+  L = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = first; r0 <= last; r0 += step * kAhead) {
     float2 ml[kAhead];
     float4 x[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int r = min(r0 + i * kMergeWarps, last);
+      const int r = min(r0 + i * step, last);
       const int64_t slot =
           ((static_cast<int64_t>(r) * p.st.count + stream) * 2 +
            (info.first_unit <= range_start(r, units, ranges) ? 0 : 1)) * p.st.per + in_part;
@@ -604,7 +591,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(cons
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (r0 + i * kMergeWarps > last) break;
+      if (r0 + i * step > last) break;
       const float top = fmaxf(M, ml[i].x), use = top == -INFINITY ? 0.f : top;
       const float a = ex2_approx(M - use), b = ex2_approx(ml[i].x - use);
       M = top;
@@ -615,34 +602,79 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(cons
       o.w = o.w * a + x[i].w * b;
     }
   }
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = L;
-  }
-  s_o[warp][lane] = o;
-  __syncthreads();
-  if (warp != 0) return;
-  float top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_m[w]);
-  const float use = top == -INFINITY ? 0.f : top;
-  L = 0.f;
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float a = ex2_approx(s_m[w] - use);
-    const float4 y = s_o[w][lane];
-    L += s_l[w] * a;
-    o.x += y.x * a;
-    o.y += y.y * a;
-    o.z += y.z * a;
-    o.w += y.w * a;
-  }
+}
+
+template <Elem E>
+__device__ __forceinline__ void write_joined(const DecodeModParams& p, int seq, int h, int lane, float M, float L, float4 o) {
+  using Ops = ElemOps<E>;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int64_t row = static_cast<int64_t>(info.seq) * p.hq + h;
+  const int64_t row = static_cast<int64_t>(seq) * p.hq + h;
   *(reinterpret_cast<uint2*>(p.out + row * kHeadDim) + lane) =
       make_uint2(Ops::pack(o.x * inv, o.y * inv), Ops::pack(o.z * inv, o.w * inv));
-  if (p.weights && lane == 0) p.final_ml[row] = make_float2(top, inv);
+  if (p.weights && lane == 0) p.final_ml[row] = make_float2(M, inv);
+}
+
+// A block joins what one query head of the sequences left that begin in its kMergeWarps ranges and go on behind them:
+// a warp each those of few pieces, all warps together those of many.
+template <Elem E>
+__global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(const DecodeModParams p) {
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = static_cast<int>(blockIdx.y);
+  const int hk = h / p.st.group, in_group = h - hk * p.st.group, part = in_group / p.st.per;
+  const int stream = hk * p.st.parts + part, in_part = in_group - part * p.st.per;
+  const int first = static_cast<int>(blockIdx.x) * kMergeWarps;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t units = p.info[0].units;
+  const int ranges = p.info[0].ranges;
+  float M, L;
+  float4 o;
+  // the last range of each sequence is the one that holds its last unit
+  auto last_of = [&](const RangeInfo& i) { return static_cast<int>(((i.first_unit + i.units) * ranges - 1) / units); };
+  if (first + warp < ranges) {
+    const RangeInfo info = p.info[1 + first + warp];
+    if (info.seq >= 0) {
+      const int last = last_of(info);
+      if (last - (first + warp) < kMergeWarps) {
+        join(p, info, units, ranges, stream, in_part, first + warp, last, 1, lane, M, L, o);
+        write_joined<E>(p, info.seq, h, lane, M, L, o);
+      }
+    }
+  }
+  for (int range = first; range < min(first + kMergeWarps, ranges); ++range) {
+    const RangeInfo info = p.info[1 + range];
+    if (info.seq < 0) continue;
+    const int last = last_of(info);
+    if (last - range < kMergeWarps) continue;
+    join(p, info, units, ranges, stream, in_part, range + warp, last, kMergeWarps, lane, M, L, o);
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
+    s_o[warp][lane] = o;
+    __syncthreads();
+    if (warp == 0) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_m[w]);
+      const float use = top == -INFINITY ? 0.f : top;
+      L = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float a = ex2_approx(s_m[w] - use);
+        const float4 y = s_o[w][lane];
+        L += s_l[w] * a;
+        o.x += y.x * a;
+        o.y += y.y * a;
+        o.z += y.z * a;
+        o.w += y.w * a;
+      }
+      write_joined<E>(p, info.seq, h, lane, top, L, o);
+    }
+    __syncthreads();
+  }
 }
 
 // weights[t] += the share of t among its sequence's scores, summed over the query heads of a kv head; the newest token's
@@ -664,19 +696,32 @@ __global__ void __launch_bounds__(kBlockSize) decode_mod_weights_kernel(const De
   float* w = p.weights + static_cast<int64_t>(block) * p.hkv * kBlockSize + threadIdx.x;
   const float* z0 = p.scores + (b * p.seq_units + token / kUnit) * p.st.count * (p.st.per * kUnit) + token % kUnit;
   const float2* ml0 = p.final_ml + static_cast<int64_t>(b) * p.hq;
-#pragma unroll 4
-  for (int hk = 0; hk < p.hkv; ++hk) {
-    float share = 0.f;
+  constexpr int kHeads = 8;  // kv heads whose loads are on the way together
+  for (int h0 = 0; h0 < p.hkv; h0 += kHeads) {
+    float old[kHeads], share[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      share[i] = 0.f;
+      old[i] = newest || h0 + i >= p.hkv ? 0.f : w[static_cast<int64_t>(h0 + i) * kBlockSize];
+    }
     if (shown) {
       for (int g = 0; g < p.st.group; ++g) {
-        const int part = g / p.st.per;
-        const float2 ml = ml0[hk * p.st.group + g];
-        const float z = z0[((hk * p.st.parts + part) * p.st.per + g - part * p.st.per) * kUnit];
-        share += ml.y == 0.f ? 0.f : ex2_approx(z - ml.x) * ml.y;
+        const int part = g / p.st.per, in_part = g - part * p.st.per;
+        float z[kHeads];
+        float2 ml[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+          const int hk = min(h0 + i, p.hkv - 1);
+          z[i] = z0[((hk * p.st.parts + part) * p.st.per + in_part) * kUnit];
+          ml[i] = ml0[hk * p.st.group + g];
+        }
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) share[i] += ml[i].y == 0.f ? 0.f : ex2_approx(z[i] - ml[i].x) * ml[i].y;
       }
     }
-    float* to = w + static_cast<int64_t>(hk) * kBlockSize;
-    *to = (newest ? 0.f : *to) + share;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      if (h0 + i < p.hkv) w[static_cast<int64_t>(h0 + i) * kBlockSize] = old[i] + share[i];
   }
 }
 
@@ -797,7 +842,7 @@ cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStr
   if (st.ranges > 1) {
     const int64_t half_most = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits;
     const unsigned ranges = static_cast<unsigned>(half_most < st.ranges ? (half_most < 1 ? 1 : half_most) : st.ranges);
-    const dim3 grid(ranges, static_cast<unsigned>(a.hq));
+    const dim3 grid((ranges + kMergeWarps - 1) / kMergeWarps, static_cast<unsigned>(a.hq));
     e = launch_behind(f16 ? decode_mod_merge_kernel<Elem::kF16> : decode_mod_merge_kernel<Elem::kBF16>, grid,
                       kMergeWarps * 32, stream, p);
     if (e != cudaSuccess) return e;

@@ -4,15 +4,17 @@
 // others those with the largest weights (attention added up beside the cache by the decode), equal ones in order of
 // position, budget in all. What stays moves up, in order: token kept[j] becomes token j.
 //
-// Select: one block per (sequence, kv head). Weights become unsigned numbers of the same order, held in shared memory
-// (those past kCached are read again each time); three histograms of 11, 11 and 10 bits, each within the bin that the
-// one before it found, give the value of the last token that stays and how many of its equals do. Then every warp counts
-// what it keeps in its own stretch of positions, a scan over the warps gives each its place, and a second sweep writes
-// kept[] in order. Counts are integers, so the order of the atomics changes nothing.
+// Select: one block per (sequence, kv head), or a cluster of up to 8 where there are few. Weights become unsigned numbers
+// of the same order, held in shared memory (those past kCached are read again each time); three histograms of 11, 11 and
+// 10 bits, each within the bin that the one before it found, summed over the cluster, give the value of the last token
+// that stays and how many of its equals do. Then every warp counts what it keeps in its own stretch of positions, a scan
+// over the warps (and blocks) gives each its place, and a second sweep writes kept[] in order. Counts are integers, so
+// the order of the atomics changes nothing.
 // Move: 512 bytes of K and V and a weight per kept token, from wherever it is to its new place; a gather bound by HBM.
-// To other blocks every row is on its own: four rows of a half-warp are on the way at once. In place, the rows of one
-// (kv head, K or V, some of the 16-byte columns) belong to one block, which takes them in order: rows only move towards
-// the front, so a chunk may be written once it has been read, and chunks behind it are still where they were.
+// To other blocks every row is on its own. In place, the rows of one (kv head, K or V, some of the 16-byte columns) belong
+// to one block, which takes them in order: rows only move towards the front, so a chunk may be written once it has been
+// read, and chunks behind it are still where they were. Measured and not kept: rows copied by the block that has chosen
+// them, beside the choices of others (96 sequences 229 us instead of 227, one of 40007 45 instead of 40: 64 SMs copy).
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -34,15 +36,20 @@ struct EvictArgs {
 
 namespace {
 
-constexpr int kCached = 48 * 1024;  // tokens whose weights a block holds
+constexpr int kCached = 48 * 1024;  // tokens whose weights a block holds at most
 constexpr int kBins = 2048;
+constexpr int kMaxRanks = 8;        // blocks that may share a selection (a portable cluster)
 constexpr int kMoveThreads = 256;
 constexpr int kHalfWarps = kMoveThreads / 16;
-constexpr int kAhead = 4;           // rows that a half-warp has on the way
+// Rows that a half-warp has on the way, and how many times that a block copies (96 sequences cut to 1500: 1 x 8 202 us,
+// 2 x 4 199, 4 x 4 214, 8 x 2 299: more rows take registers, and with them warps).
+constexpr int kAhead = 2;
+constexpr int kRounds = 4;
 
 struct EvictParams {
   EvictArgs a;
-  int32_t cached;  // tokens that fit in the block's shared memory
+  int32_t ranks;   // blocks that share a (sequence, kv head) in the selection, a cluster
+  int32_t cached;  // tokens that fit in a block's shared memory
   int32_t parts;   // in place: blocks that share a row
   unsigned int* err;
 };
@@ -73,28 +80,72 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Everything that any block of the cluster wrote to shared memory before is there for all of them behind it.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Words of the same shared array in another block of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(const int* mine, int rank) {
+  uint32_t addr;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
+  return addr;
+}
+__device__ __forceinline__ int cluster_load(const int* mine, int rank) {
+  int x;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(cluster_address(mine, rank)) : "memory");
+  return x;
+}
+__device__ __forceinline__ int4 cluster_load4(const int* mine, int rank) {
+  int4 x;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(cluster_address(mine, rank))
+               : "memory");
+  return x;
+}
+// Sum of what the warps before this one have in x.
+__device__ __forceinline__ int before_warp(const int* x, int warp, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < warp ? x[lane] : 0);
+}
+__device__ __forceinline__ uint4 ld_row(const uint16_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins];
+  extern __shared__ __align__(16) int hist[];  // one of kBins, in a cluster one to a pass; then the weights
   __shared__ int s_warp[2][kWarps];
-  __shared__ int s_bin, s_left;
-  const int hk = static_cast<int>(blockIdx.x), b = static_cast<int>(blockIdx.y);
+  __shared__ int s_bin, s_left, s_total[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int hists = p.ranks > 1 ? 3 : 1;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(hist + hists * kBins);
+  const int ranks = p.ranks, rank = static_cast<int>(blockIdx.x) % ranks;
+  const int hk = static_cast<int>(blockIdx.x) / ranks, b = static_cast<int>(blockIdx.y);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = length_of(p, b, hk == 0 && tid == 0);
+  const int n = length_of(p, b, blockIdx.x == 0 && tid == 0);
   const int budget = p.a.budget;
   int32_t* kept = p.a.kept + (static_cast<int64_t>(b) * p.a.hkv + hk) * budget;
-  if (hk == 0 && tid == 0) p.a.new_lens[b] = min(n, budget);
+  if (blockIdx.x == 0 && tid == 0) p.a.new_lens[b] = min(n, budget);
+  const int all_tid = rank * kThreads + tid, all_threads = ranks * kThreads;
   if (n <= budget) {
-    for (int j = tid; j < budget; j += kThreads) kept[j] = j < n ? j : -1;
+    for (int j = all_tid; j < budget; j += all_threads) kept[j] = j < n ? j : -1;
     return;
   }
-  const int lo = p.a.first, hi = n - p.a.recent;  // the tokens to choose from
-  for (int j = tid; j < lo; j += kThreads) kept[j] = j;
-  for (int j = tid; j < p.a.recent; j += kThreads) kept[budget - p.a.recent + j] = hi + j;
-  int want = budget - lo - p.a.recent;            // of them
+  const int all_hi = n - p.a.recent;              // the tokens to choose from: [first, all_hi)
+  for (int j = all_tid; j < p.a.first; j += all_threads) kept[j] = j;
+  for (int j = all_tid; j < p.a.recent; j += all_threads) kept[budget - p.a.recent + j] = all_hi + j;
+  int want = budget - p.a.first - p.a.recent;     // of them
   if (want == 0) return;
+  // this block's share of them
+  const int share = (all_hi - p.a.first + ranks - 1) / ranks;
+  const int lo = min(p.a.first + rank * share, all_hi), hi = min(lo + share, all_hi);
 
   const int32_t* table = p.a.block_tables + static_cast<int64_t>(b) * p.a.bt_stride;
   auto load = [&](int t) -> uint32_t {
@@ -110,14 +161,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
   for (int t = lo + tid; t < in_smem; t += kThreads) keys[t - lo] = load(t);
   auto key = [&](int t) -> uint32_t { return t < in_smem ? keys[t - lo] : load(t); };
 
+  for (int i = tid; i < hists * kBins; i += kThreads) hist[i] = 0;
+  __syncthreads();
+
   // ---- the value of the last token that stays ----
   uint32_t prefix = 0, known = 0;  // the bits found so far, and their mask
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t bins = pass == 2 ? 1024u : 2048u;
-    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-    __syncthreads();
+    int* mine = hist + (ranks > 1 ? pass * kBins : 0);
     for (int t0 = lo + warp * 32; t0 < hi; t0 += kThreads) {
       const int t = t0 + lane;
       const uint32_t k = t < hi ? key(t) : 0u;
@@ -130,18 +183,45 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         const uint32_t first_bin = __shfl_sync(0xffffffffu, bin, leader);
         const uint32_t same = __ballot_sync(0xffffffffu, in && bin == first_bin);
         if (lane == leader)
-          atomicAdd(&hist[bin], __popc(same));
+          atomicAdd(mine + bin, __popc(same));
         else if (in && !((same >> lane) & 1u))
-          atomicAdd(&hist[bin], 1);
+          atomicAdd(mine + bin, 1);
       }
     }
-    __syncthreads();
-    // bins from the top down: thread i has kBins / kThreads of them
-    constexpr int kPer = kBins / kThreads;
-    int mine = 0;
+    if (ranks > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    // bins from the top down, of all blocks: thread i has kBins / kThreads of them
+    constexpr int kPer = kBins / kThreads < 4 ? 4 : kBins / kThreads;
+    int count[kPer], total = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += hist[kBins - 1 - (tid * kPer + i)];
-    int scan = mine;
+    for (int i = 0; i < kPer; i += 4) {  // bins of four, the last first
+      int4 c = make_int4(0, 0, 0, 0);
+      const int* four = mine + kBins - 4 - (tid * kPer + i);
+      if (tid * kPer < kBins) {
+        if (ranks == 1) {
+          c = *reinterpret_cast<const int4*>(four);
+        } else {
+          int4 there[kMaxRanks];  // all on the way together
+#pragma unroll
+          for (int r = 0; r < kMaxRanks; ++r) there[r] = r < ranks ? cluster_load4(four, r) : c;
+#pragma unroll
+          for (int r = 0; r < kMaxRanks; ++r) {
+            c.x += there[r].x;
+            c.y += there[r].y;
+            c.z += there[r].z;
+            c.w += there[r].w;
+          }
+        }
+      }
+      count[i] = c.w;
+      count[i + 1] = c.z;
+      count[i + 2] = c.y;
+      count[i + 3] = c.x;
+      total += (c.x + c.y) + (c.z + c.w);
+    }
+    int scan = total;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, scan, off);
@@ -149,24 +229,24 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     }
     if (lane == 31) s_warp[0][warp] = scan;
     __syncthreads();
-    int above = scan - mine;
-    for (int w = 0; w < warp; ++w) above += s_warp[0][w];
-    if (above < want && above + mine >= want) {
+    const int above = scan - total + before_warp(s_warp[0], warp, lane);
+    if (above < want && above + total >= want) {
       int left = want - above;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int bin = kBins - 1 - (tid * kPer + i), c = hist[bin];
-        if (left > 0 && left <= c) {
-          s_bin = bin;
+        if (left > 0 && left <= count[i]) {
+          s_bin = kBins - 1 - (tid * kPer + i);
           s_left = left;
         }
-        left -= c;
+        left -= count[i];
       }
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(s_bin) << shift;
     known |= (bins - 1) << shift;
     want = s_left;
+    if (ranks == 1 && pass < 2)
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
   }
 
@@ -185,12 +265,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     s_warp[1][warp] = equal;
   }
   __syncthreads();
-  int greater_before = 0, equal_before = 0;
-  for (int w = 0; w < warp; ++w) {
-    greater_before += s_warp[0][w];
-    equal_before += s_warp[1][w];
+  int greater_before = before_warp(s_warp[0], warp, lane), equal_before = before_warp(s_warp[1], warp, lane);
+  if (warp == kWarps - 1 && lane == 0) {
+    s_total[0] = greater_before + s_warp[0][warp];
+    s_total[1] = equal_before + s_warp[1][warp];
   }
-  int at = lo + greater_before + min(equal_before, want);
+  int greater_there = 0, equal_there = 0;  // in the blocks before this one
+  if (ranks > 1) {
+    cluster_sync();
+    greater_there = __reduce_add_sync(0xffffffffu, lane < rank ? cluster_load(s_total, lane) : 0);
+    equal_there = __reduce_add_sync(0xffffffffu, lane < rank ? cluster_load(s_total + 1, lane) : 0);
+  }
+  equal_before += equal_there;
+  int at = p.a.first + greater_there + greater_before + min(equal_before, want);
   const uint32_t below = (1u << lane) - 1u;
   for (int t0 = begin; t0 < end; t0 += 32) {
     const bool in = t0 + lane < end;
@@ -203,54 +290,62 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     at += __popc(keeps);
     equal_before += __popc(sames);
   }
+  if (ranks > 1) cluster_sync();  // no block's shared memory goes while another may read it
 }
 
-__device__ __forceinline__ uint4 ld_row(const uint16_t* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
-}
-
-// To other blocks: an item is (kept token, kv head), heads fastest; a half-warp moves its K and V rows.
+// To other blocks: an item is (kept token, kv head), heads fastest; a half-warp moves its K and V rows. The next items'
+// tokens are asked for while a round's rows are on the way.
 __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictParams p) {
   const int b = static_cast<int>(blockIdx.y), hkv = p.a.hkv;
   const int lane = threadIdx.x & 15;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t items = static_cast<int64_t>(min(length_of(p, b, false), p.a.budget)) * hkv;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kHalfWarps * kAhead) + (threadIdx.x >> 4);
-  const uint16_t* kc = static_cast<const uint16_t*>(p.a.k_cache);
-  const uint16_t* vc = static_cast<const uint16_t*>(p.a.v_cache);
-  int64_t to[kAhead], w_to[kAhead];
-  uint4 k[kAhead], v[kAhead];
-  float w[kAhead];
+  int64_t item = static_cast<int64_t>(blockIdx.x) * (kHalfWarps * kAhead * kRounds) + (threadIdx.x >> 4);
+  const int64_t end = min(items, static_cast<int64_t>(blockIdx.x + 1) * (kHalfWarps * kAhead * kRounds));
+  uint16_t* kc = static_cast<uint16_t*>(p.a.k_cache);
+  uint16_t* vc = static_cast<uint16_t*>(p.a.v_cache);
+  const int32_t* kept = p.a.kept + static_cast<int64_t>(b) * hkv * p.a.budget;
+  int t[kAhead], j[kAhead], hk[kAhead];
+  auto ask = [&](int64_t first) {
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int64_t item = first + i * kHalfWarps;
-    to[i] = -1;
-    if (item < items) {
-      const int j = static_cast<int>(item / hkv), hk = static_cast<int>(item - static_cast<int64_t>(j) * hkv);
-      const int t = p.a.kept[(static_cast<int64_t>(b) * hkv + hk) * p.a.budget + j];
-      const int from = block_of(p, p.a.block_tables, p.a.bt_stride, b, t);
-      const int dest = block_of(p, p.a.new_tables, p.a.new_stride, b, j);
-      if (from >= 0 && dest >= 0) {
-        const int64_t src = ((static_cast<int64_t>(from) * kBlockSize + t % kBlockSize) * hkv + hk) * kHeadDim + lane * 8;
-        k[i] = ld_row(kc + src);
-        v[i] = ld_row(vc + src);
-        w[i] = p.a.weights[weight_place(p, from, hk, t)];
-        to[i] = ((static_cast<int64_t>(dest) * kBlockSize + j % kBlockSize) * hkv + hk) * kHeadDim + lane * 8;
-        w_to[i] = weight_place(p, dest, hk, j);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t x = first + i * kHalfWarps;
+      t[i] = -1;
+      if (x < end) {
+        j[i] = static_cast<int>(x / hkv);
+        hk[i] = static_cast<int>(x - static_cast<int64_t>(j[i]) * hkv);
+        t[i] = kept[static_cast<int64_t>(hk[i]) * p.a.budget + j[i]];
       }
     }
-  }
+  };
+  ask(item);
+  while (item < end) {
+    int64_t to[kAhead], w_to[kAhead];
+    uint4 k[kAhead], v[kAhead];
+    float w[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    if (to[i] < 0) continue;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.k_cache) + to[i]) = k[i];
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.v_cache) + to[i]) = v[i];
-    if (lane == 0) p.a.weights[w_to[i]] = w[i];
+    for (int i = 0; i < kAhead; ++i) {
+      to[i] = -1;
+      if (t[i] < 0) continue;
+      const int from = block_of(p, p.a.block_tables, p.a.bt_stride, b, t[i]);
+      const int dest = block_of(p, p.a.new_tables, p.a.new_stride, b, j[i]);
+      if (from < 0 || dest < 0) continue;
+      const int64_t src = ((static_cast<int64_t>(from) * kBlockSize + t[i] % kBlockSize) * hkv + hk[i]) * kHeadDim + lane * 8;
+      k[i] = ld_row(kc + src);
+      v[i] = ld_row(vc + src);
+      w[i] = p.a.weights[weight_place(p, from, hk[i], t[i])];
+      to[i] = ((static_cast<int64_t>(dest) * kBlockSize + j[i] % kBlockSize) * hkv + hk[i]) * kHeadDim + lane * 8;
+      w_to[i] = weight_place(p, dest, hk[i], j[i]);
+    }
+    item += kHalfWarps * kAhead;
+    ask(item);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (to[i] < 0) continue;
+      *reinterpret_cast<uint4*>(kc + to[i]) = k[i];
+      *reinterpret_cast<uint4*>(vc + to[i]) = v[i];
+      if (lane == 0) p.a.weights[w_to[i]] = w[i];
+    }
   }
 }
 
@@ -329,28 +424,41 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaS
 
 template <int kThreads>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
-  const int smem = p.cached * 4;
   // the attribute holds for the current device; setting it again costs the host less than a launch
-  const cudaError_t e =
-      cudaFuncSetAttribute(evict_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (3 * kBins + kCached) * 4);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.a.hkv), static_cast<unsigned>(p.a.num_seqs));
-  evict_select_kernel<kThreads><<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.a.hkv * p.ranks), static_cast<unsigned>(p.a.num_seqs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>((p.ranks > 1 ? 3 : 1) * kBins + p.cached) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(p.ranks);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads>, p);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, unsigned int* err, cudaStream_t stream) {
   EvictParams p{};
   p.a = a;
   p.err = err;
-  p.cached = a.max_ctx < kCached ? a.max_ctx : kCached;
-  // Few or long sequences: as many threads as a block can have; else several blocks to an SM hide one another's waits.
+  // Few (sequence, kv head) pairs with many tokens each: up to 8 blocks share one, of 1024 threads. Many pairs: smaller
+  // blocks, several to an SM, hide one another's waits.
   const int64_t blocks = static_cast<int64_t>(a.num_seqs) * a.hkv;
-  cudaError_t e = blocks < 2 * 152 || a.max_ctx > 16384 ? launch_select<1024>(p, stream) : launch_select<256>(p, stream);
+  p.ranks = 1;
+  while (p.ranks < kMaxRanks && blocks * p.ranks * 2 <= 2 * 152 && a.max_ctx >= 2048 * p.ranks) p.ranks *= 2;
+  const int share = (a.max_ctx + p.ranks - 1) / p.ranks;
+  p.cached = share < kCached ? share : kCached;
+  const cudaError_t e =
+      blocks * p.ranks <= 2 * 152 || share > 16384 ? launch_select<1024>(p, stream) : launch_select<256>(p, stream);
   if (e != cudaSuccess) return e;
   if (a.new_tables) {
     const int64_t most = static_cast<int64_t>(a.budget < a.max_ctx ? a.budget : a.max_ctx) * a.hkv;
-    const int64_t per = kHalfWarps * kAhead;
+    const int64_t per = kHalfWarps * kAhead * kRounds;
     const dim3 grid(static_cast<unsigned>((most + per - 1) / per), static_cast<unsigned>(a.num_seqs));
     return most > 0 ? launch_behind(evict_copy_kernel, grid, kMoveThreads, stream, p) : cudaSuccess;
   }
