@@ -567,8 +567,8 @@ int pkv_rope_store_kvcache_f16(const void* q, int64_t q_row_stride, const void* 
  * sequence, at position context_lens[b] - 1. Arguments and errors as for pkv_decode but for
  *   num_blocks  at most 2^23 - 1 (and not 0)
  *   key_starts  [num_seqs] int32, or NULL
- *   weights     NULL, or fp32 [num_blocks, num_kv_heads, 256]: each token's attention added up over the calls, beside
- *         the cache. For every key that takes part, weights[slot / 256][kv head][slot % 256] += the sum over the kv
+ *   weights     NULL, or fp32 [num_blocks, num_kv_heads, 256], 16-byte aligned: each token's attention added up over the
+ *         calls, beside the cache. For every key that takes part, weights[slot / 256][kv head][slot % 256] += the sum over the kv
  *         head's query heads of its softmax probability; the newest token's (position context_lens[b] - 1) starts
  *         from 0 in this call, whatever was there. What a prompt's tokens start from is the caller's to fill in.
  *         Sequences of one call must not share blocks then (their additions would race).

@@ -69,26 +69,27 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // How a call's heads are cut into streams: parts of up to 8 or 16 query heads of one kv head.
 struct Streams {
-  int32_t group, per, parts, count, ranges;
+  int32_t group, per, heads, parts, count, ranges;  // heads: of the largest part
 };
 Streams streams_of(int32_t hq, int32_t hkv) {
   Streams s;
   s.group = hq / hkv;
   s.per = s.group <= 8 ? 8 : 16;
+  s.heads = s.group < s.per ? s.group : s.per;
   s.parts = (s.group + s.per - 1) / s.per;
   s.count = hkv * s.parts;
   s.ranges = s.count < kWorkers ? kWorkers / s.count : 1;
   return s;
 }
 
-// Workspace: RangeInfo[1 + ranges] (the first holds the call's totals), (max, 1 / sum) per (sequence, query head),
-// partial (max, sum) and o per (range, stream, first or last sequence of the range, head of the part), and with weights
-// the scores per (sequence, unit, stream, head of the part, token).
-struct RangeInfo {
-  int64_t first_unit;  // of the sequence that begins in this range and goes on behind it
-  int64_t units;
+// Workspace: RangeInfo per range, (max, 1 / sum) per (sequence, query head), partial (max, sum) and o per (range, stream,
+// first or last sequence of the range, head of the part), and with weights the scores per (sequence, unit, stream, head
+// of the part, token).
+struct alignas(16) RangeInfo {  // the sequence that begins in this range and goes on behind it
   int32_t seq;         // -1: none
-  int32_t ranges;      // entry 0: ranges in use
+  int32_t last;        // the range that holds its last unit
+  int32_t place;       // its partial results are this range's first (0) or last (1); in later ranges they are the first
+  int32_t pad;
 };
 struct Layout {
   size_t info, final_ml, ml, o, scores, total;
@@ -101,13 +102,13 @@ Layout layout_of(const Streams& s, int32_t num_seqs, int32_t hq, int32_t max_ctx
     at += (bytes + 127) / 128 * 128;
     return here;
   };
-  const size_t slots = static_cast<size_t>(s.ranges) * s.count * 2 * s.per;
-  l.info = take(sizeof(RangeInfo) * (1 + static_cast<size_t>(s.ranges)));
+  const size_t slots = static_cast<size_t>(s.ranges) * s.count * 2 * s.heads;
+  l.info = take(sizeof(RangeInfo) * s.ranges);
   l.final_ml = take(weights ? sizeof(float2) * num_seqs * hq : 0);
   l.ml = take(sizeof(float2) * slots);
   l.o = take(sizeof(float) * kHeadDim * slots);
   const size_t units = (static_cast<size_t>(max_ctx) + kUnit - 1) / kUnit;
-  l.scores = take(weights ? sizeof(float) * num_seqs * units * s.count * s.per * kUnit : 0);
+  l.scores = take(weights ? sizeof(float) * num_seqs * units * s.count * s.heads * kUnit : 0);
   l.total = at;
   return l;
 }
@@ -132,6 +133,7 @@ struct DecodeModParams {
   float* o;
   float* scores;
   int64_t seq_units;  // units that `scores` holds per sequence
+  int32_t used_ranges;  // ranges that the longest lengths could fill
   unsigned int* err;
 };
 
@@ -260,16 +262,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int64_t fill = (units + kMinUnits - 1) / kMinUnits;
   const int ranges = static_cast<int>(fill < p.st.ranges ? fill : p.st.ranges);
-  if (blockIdx.x == 0 && tid == 0) {
-    p.info[0].units = units;
-    p.info[0].ranges = ranges;
-  }
   const int worker = static_cast<int>(blockIdx.x) * kWarps + warp;
   const int workers = static_cast<int>(gridDim.x) * kWarps;
   // A stream has all its ranges, or (more streams than workers) one range and a worker several streams.
   const bool split = p.st.ranges > 1;
   const int range = split ? worker / p.st.count : 0;
-  if (range >= ranges) return;
+  if (range >= ranges) {
+    if (split && lane == 0 && worker % p.st.count == 0 && range < p.used_ranges) p.info[range].seq = -1;
+    return;
+  }
   const int64_t start = range_start(range, units, ranges), end = range_start(range + 1, units, ranges);
 
   // the sequence that holds unit `start`
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rise = rise || z[t][j] > m[t][j & 1] + 8.f;
           }
         if (p.weights) {
-          float* to = p.scores + ((now.b * p.seq_units + (seq_first + u)) * p.st.count + stream) * (p.st.per * kUnit);
+          float* to = p.scores + ((now.b * p.seq_units + (seq_first + u)) * p.st.count + stream) * (p.st.heads * kUnit);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const int64_t slot =
-            ((static_cast<int64_t>(range) * p.st.count + stream) * 2 + (first_unit <= start ? 0 : 1)) * p.st.per;
+            ((static_cast<int64_t>(range) * p.st.count + stream) * 2 + (first_unit <= start ? 0 : 1)) * p.st.heads;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -548,10 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       left -= n;
       if (left == 0) {
         if (stream == 0 && lane == 0) {
-          RangeInfo* info = p.info + 1 + range;
-          info->seq = begins && !ends ? now.b : -1;
-          info->first_unit = first_unit;
-          info->units = now.last - now.seen.x / kUnit + 1;
+          const int64_t last_unit = first_unit + (now.last - now.seen.x / kUnit);
+          RangeInfo info;
+          info.seq = begins && !ends ? now.b : -1;
+          info.last = static_cast<int>(((last_unit + 1) * ranges - 1) / units);
+          info.place = first_unit <= start ? 0 : 1;
+          info.pad = 0;
+          *reinterpret_cast<int4*>(p.info + range) = *reinterpret_cast<const int4*>(&info);
         }
       } else {
         first_unit += now.last - now.seen.x / kUnit + 1;
@@ -571,9 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Partial results r = first, first + step, ... up to last of one query head, joined: (max, sum) and four dims to a lane.
-__device__ __forceinline__ void join(const DecodeModParams& p, const RangeInfo& info, int64_t units, int ranges, int stream,
-                                     int in_part, int first, int last, int step, int lane, float& M, float& L, float4& o) {
-  constexpr int kAhead = 5;
+__device__ __forceinline__ void join(const DecodeModParams& p, int range, int place, int stream, int in_part, int first,
+                                     int last, int step, int lane, float& M, float& L, float4& o) {
+  constexpr int kAhead = 10;
   M = -INFINITY;
   L = 0.f;
   o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -583,9 +587,7 @@ __device__ __forceinline__ void join(const DecodeModParams& p, const RangeInfo& 
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int r = min(r0 + i * step, last);
-      const int64_t slot =
-          ((static_cast<int64_t>(r) * p.st.count + stream) * 2 +
-           (info.first_unit <= range_start(r, units, ranges) ? 0 : 1)) * p.st.per + in_part;
+      const int64_t slot = ((static_cast<int64_t>(r) * p.st.count + stream) * 2 + (r == range ? place : 0)) * p.st.heads + in_part;
       ml[i] = p.ml[slot];
       x[i] = *(reinterpret_cast<const float4*>(p.o + slot * kHeadDim) + lane);
     }
@@ -619,6 +621,7 @@ __device__ __forceinline__ void write_joined(const DecodeModParams& p, int seq, 
 template <Elem E>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(const DecodeModParams p) {
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ int s_info[kMergeWarps][3];
   __shared__ float4 s_o[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = static_cast<int>(blockIdx.y);
   const int hk = h / p.st.group, in_group = h - hk * p.st.group, part = in_group / p.st.per;
@@ -626,28 +629,24 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(cons
   const int first = static_cast<int>(blockIdx.x) * kMergeWarps;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t units = p.info[0].units;
-  const int ranges = p.info[0].ranges;
   float M, L;
   float4 o;
-  // the last range of each sequence is the one that holds its last unit
-  auto last_of = [&](const RangeInfo& i) { return static_cast<int>(((i.first_unit + i.units) * ranges - 1) / units); };
+  const int ranges = p.used_ranges;
   if (first + warp < ranges) {
-    const RangeInfo info = p.info[1 + first + warp];
-    if (info.seq >= 0) {
-      const int last = last_of(info);
-      if (last - (first + warp) < kMergeWarps) {
-        join(p, info, units, ranges, stream, in_part, first + warp, last, 1, lane, M, L, o);
-        write_joined<E>(p, info.seq, h, lane, M, L, o);
-      }
+    const int4 info = *reinterpret_cast<const int4*>(p.info + first + warp);  // {seq, last, place}
+    s_info[warp][0] = info.x;
+    s_info[warp][1] = info.y;
+    s_info[warp][2] = info.z;
+    if (info.x >= 0 && info.y - (first + warp) < kMergeWarps) {
+      join(p, first + warp, info.z, stream, in_part, first + warp, info.y, 1, lane, M, L, o);
+      write_joined<E>(p, info.x, h, lane, M, L, o);
     }
   }
-  for (int range = first; range < min(first + kMergeWarps, ranges); ++range) {
-    const RangeInfo info = p.info[1 + range];
-    if (info.seq < 0) continue;
-    const int last = last_of(info);
-    if (last - range < kMergeWarps) continue;
-    join(p, info, units, ranges, stream, in_part, range + warp, last, kMergeWarps, lane, M, L, o);
+  __syncthreads();
+  for (int i = 0; i < min(kMergeWarps, ranges - first); ++i) {
+    const int range = first + i, seq = s_info[i][0], last = s_info[i][1];
+    if (seq < 0 || last - range < kMergeWarps) continue;
+    join(p, range, s_info[i][2], stream, in_part, range + warp, last, kMergeWarps, lane, M, L, o);
     if (lane == 0) {
       s_m[warp] = M;
       s_l[warp] = L;
@@ -671,57 +670,72 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(cons
         o.z += y.z * a;
         o.w += y.w * a;
       }
-      write_joined<E>(p, info.seq, h, lane, top, L, o);
+      write_joined<E>(p, seq, h, lane, top, L, o);
     }
     __syncthreads();
   }
 }
 
 // weights[t] += the share of t among its sequence's scores, summed over the query heads of a kv head; the newest token's
-// starts from 0. One block per (256-token block of a sequence), one thread per token.
+// starts from 0. One block per (256-token block of a sequence); a thread takes four tokens of every fourth kv head.
 __global__ void __launch_bounds__(kBlockSize) decode_mod_weights_kernel(const DecodeModParams p) {
-  const int b = static_cast<int>(blockIdx.y), token = static_cast<int>(blockIdx.x) * kBlockSize + threadIdx.x;
+  const int b = static_cast<int>(blockIdx.y), place = static_cast<int>(blockIdx.x);
+  const int quad = static_cast<int>(threadIdx.x) & 63, token = place * kBlockSize + 4 * quad;
   const int2 seen = visible(p, b, false);
   const int ctx = p.context_lens[b];
   const bool good = ctx > 0 && ctx <= p.max_ctx && ctx <= static_cast<int64_t>(p.bt_stride) * kBlockSize;
-  if (!good || static_cast<int>(blockIdx.x) > (ctx - 1) / kBlockSize ||
-      (static_cast<int>(blockIdx.x) + 1) * kBlockSize <= min(seen.x, ctx - 1)) {
+  if (!good || place > (ctx - 1) / kBlockSize || (place + 1) * kBlockSize <= min(seen.x, ctx - 1)) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  const int block = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + blockIdx.x];
-  const bool shown = token >= seen.x && token < seen.y, newest = token == ctx - 1;
+  const int block = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + place];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (block < 0 || block >= p.num_blocks || !(shown || newest)) return;  // a bad block has been reported
-  float* w = p.weights + static_cast<int64_t>(block) * p.hkv * kBlockSize + threadIdx.x;
-  const float* z0 = p.scores + (b * p.seq_units + token / kUnit) * p.st.count * (p.st.per * kUnit) + token % kUnit;
+  if (block < 0 || block >= p.num_blocks) return;  // reported where it was fetched
+  bool shown[4], any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    shown[i] = token + i >= seen.x && token + i < seen.y;
+    any = any || shown[i] || token + i == ctx - 1;
+  }
+  if (!any) return;
+  const int newest = ctx - 1 - token;  // 0..3: one of these
+  float4* w = reinterpret_cast<float4*>(p.weights + static_cast<int64_t>(block) * p.hkv * kBlockSize) + quad;
+  const int z_stride = p.st.heads * (kUnit / 4);  // float4 per stream
+  const float4* z0 = reinterpret_cast<const float4*>(p.scores) +
+                     (b * p.seq_units + token / kUnit) * p.st.count * z_stride + (quad & (kUnit / 4 - 1));
   const float2* ml0 = p.final_ml + static_cast<int64_t>(b) * p.hq;
-  constexpr int kHeads = 8;  // kv heads whose loads are on the way together
-  for (int h0 = 0; h0 < p.hkv; h0 += kHeads) {
-    float old[kHeads], share[kHeads];
+  constexpr int kHeads = 2;  // kv heads whose loads are on the way together
+  for (int h0 = static_cast<int>(threadIdx.x) >> 6; h0 < p.hkv; h0 += 4 * kHeads) {
+    float4 old[kHeads];
+    float share[kHeads][4];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      share[i] = 0.f;
-      old[i] = newest || h0 + i >= p.hkv ? 0.f : w[static_cast<int64_t>(h0 + i) * kBlockSize];
+      const int hk = min(h0 + 4 * i, p.hkv - 1);
+      old[i] = w[static_cast<int64_t>(hk) * (kBlockSize / 4)];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) share[i][j] = 0.f;
     }
-    if (shown) {
-      for (int g = 0; g < p.st.group; ++g) {
-        const int part = g / p.st.per, in_part = g - part * p.st.per;
-        float z[kHeads];
-        float2 ml[kHeads];
+#pragma unroll 2
+    for (int g = 0; g < p.st.group; ++g) {
+      const int part = g / p.st.per, in_part = g - part * p.st.per;
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          const int hk = min(h0 + i, p.hkv - 1);
-          z[i] = z0[((hk * p.st.parts + part) * p.st.per + in_part) * kUnit];
-          ml[i] = ml0[hk * p.st.group + g];
-        }
+      for (int i = 0; i < kHeads; ++i) {
+        const int hk = min(h0 + 4 * i, p.hkv - 1);
+        const float4 z = z0[(hk * p.st.parts + part) * z_stride + in_part * (kUnit / 4)];
+        const float2 ml = ml0[hk * p.st.group + g];
+        const float zs[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) share[i] += ml[i].y == 0.f ? 0.f : ex2_approx(z[i] - ml[i].x) * ml[i].y;
+        for (int j = 0; j < 4; ++j)
+          share[i][j] += shown[j] && ml.y != 0.f ? ex2_approx(zs[j] - ml.x) * ml.y : 0.f;
       }
     }
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-      if (h0 + i < p.hkv) w[static_cast<int64_t>(h0 + i) * kBlockSize] = old[i] + share[i];
+    for (int i = 0; i < kHeads; ++i) {
+      if (h0 + 4 * i >= p.hkv) break;
+      auto added = [&](int j, float before) { return newest == j ? share[i][j] : (shown[j] ? before + share[i][j] : before); };
+      w[static_cast<int64_t>(h0 + 4 * i) * (kBlockSize / 4)] =
+          make_float4(added(0, old[i].x), added(1, old[i].y), added(2, old[i].z), added(3, old[i].w));
+    }
   }
 }
 
@@ -829,7 +843,9 @@ cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStr
   if (!encode_cache(&tk, a.k_cache, slots, a.hkv, elem) || !encode_cache(&tv, a.v_cache, slots, a.hkv, elem))
     return cudaErrorInvalidValue;
   // no more workers than the longest lengths could keep busy
-  const int64_t most = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits * st.count;
+  const int64_t fill = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits;
+  p.used_ranges = static_cast<int32_t>(fill < st.ranges ? fill : st.ranges);
+  const int64_t most = fill * st.count;
   const int64_t want = (most + kWarps - 1) / kWarps;
   const int ctas = static_cast<int>(want < 1 ? 1 : (want < kCtas ? want : kCtas));
   const bool f16 = elem == Elem::kF16;
@@ -839,10 +855,8 @@ cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStr
   else
     e = f16 ? launch_typed<Elem::kF16, 2>(tk, tv, p, ctas, stream) : launch_typed<Elem::kBF16, 2>(tk, tv, p, ctas, stream);
   if (e != cudaSuccess) return e;
-  if (st.ranges > 1) {
-    const int64_t half_most = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits;
-    const unsigned ranges = static_cast<unsigned>(half_most < st.ranges ? (half_most < 1 ? 1 : half_most) : st.ranges);
-    const dim3 grid((ranges + kMergeWarps - 1) / kMergeWarps, static_cast<unsigned>(a.hq));
+  if (st.ranges > 1 && p.used_ranges > 0) {
+    const dim3 grid(static_cast<unsigned>((p.used_ranges + kMergeWarps - 1) / kMergeWarps), static_cast<unsigned>(a.hq));
     e = launch_behind(f16 ? decode_mod_merge_kernel<Elem::kF16> : decode_mod_merge_kernel<Elem::kBF16>, grid,
                       kMergeWarps * 32, stream, p);
     if (e != cudaSuccess) return e;
@@ -883,7 +897,7 @@ int decode_mod_common(const void* q, int64_t q_row_stride, const void* k_cache, 
   if (num_blocks == 0) return PKV_ERR_BAD_SIZE;
   if (q_row_stride < static_cast<int64_t>(num_heads) * head_dim) return PKV_ERR_BAD_STRIDE;
   if (!aligned(q, 16) || q_row_stride % 8 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(out, 16) || !aligned(slopes, 4) || !aligned(key_starts, 4) || !aligned(weights, 4))
+      !aligned(out, 16) || !aligned(slopes, 4) || !aligned(key_starts, 4) || !aligned(weights, 16))
     return PKV_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < pkv::decode_mod_workspace_bytes(num_seqs, num_heads, num_kv_heads,
                                                                       max_context_len, weights != nullptr))
