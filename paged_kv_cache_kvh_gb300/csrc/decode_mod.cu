@@ -63,15 +63,27 @@ constexpr int kWorkers = kCtas * kWarps;
 constexpr int kMinUnits = 2;                        // units to a range at least
 constexpr int kOffBars = kWarps * kStages * 2 * kUnitBytes;
 constexpr int kOffScan = kOffBars + kWarps * kStages * 8;
-constexpr size_t kSmemBytes = kOffScan + (kThreads + kWarps + 1) * 8 + 1024;  // + alignment slack
+constexpr int kOffPieces = kOffScan + (kThreads + kWarps) * 8;
+// What a worker has of a sequence that is not all in its range, for the other workers of the CTA.
+struct Piece {
+  int32_t seq;         // -1: none
+  int32_t ends;        // its last unit is here
+  int64_t first_unit;  // the sequence's first unit, and the one behind its last
+  int64_t end_unit;
+  const float2* ml;    // (max, sum) and o per head: in the worker's ring, or in the workspace if that was still in use
+  const float* o;
+};
+constexpr int kPieces = 2 * kWarps;
+constexpr size_t kSmemBytes = kOffPieces + kPieces * sizeof(Piece) + 1024;  // + alignment slack
 constexpr int kMergeWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // How a call's heads are cut into streams: parts of up to 8 or 16 query heads of one kv head.
 struct Streams {
   int32_t group, per, heads, parts, count, ranges;  // heads: of the largest part
+  int32_t by_cta;  // a CTA's workers share a stream, and their partial results are joined before they leave the CTA
 };
-Streams streams_of(int32_t hq, int32_t hkv) {
+Streams streams_of(int32_t hq, int32_t hkv, int32_t num_seqs, int32_t max_ctx) {
   Streams s;
   s.group = hq / hkv;
   s.per = s.group <= 8 ? 8 : 16;
@@ -79,6 +91,15 @@ Streams streams_of(int32_t hq, int32_t hkv) {
   s.parts = (s.group + s.per - 1) / s.per;
   s.count = hkv * s.parts;
   s.ranges = s.count < kWorkers ? kWorkers / s.count : 1;
+  // Two ways to share the streams out. Workers take them in turn: neighbouring heads' rows, which lie side by side, are
+  // read at the same time, but each of a long sequence's pieces goes through memory (256 sequences: 409 us, the other way
+  // 418). Or a CTA takes eight neighbouring ranges of one stream and joins its workers' pieces (one sequence of 40007,
+  // 32 on 8 heads: 37.0 us instead of 38.2; 14 of up to 1000, 12 heads: 23.6, 24.4): for short ranges, and where the
+  // streams leave at most one CTA in 16 over.
+  const int32_t ctas = kCtas / s.count;
+  const int64_t units = (static_cast<int64_t>(max_ctx) + kUnit - 1) / kUnit * num_seqs;
+  s.by_cta = ctas * s.count * 16 >= kCtas * 15 && units <= 128 * s.ranges;
+  if (s.by_cta) s.ranges = ctas * kWarps;
   return s;
 }
 
@@ -133,7 +154,8 @@ struct DecodeModParams {
   float* o;
   float* scores;
   int64_t seq_units;  // units that `scores` holds per sequence
-  int32_t used_ranges;  // ranges that the longest lengths could fill
+  int32_t used_ranges;  // ranges (by_cta: eights of them) that the longest lengths could fill
+  int32_t range_step;   // by_cta: 8
   unsigned int* err;
 };
 
@@ -151,7 +173,10 @@ __device__ __forceinline__ int2 visible(const DecodeModParams& p, int b, bool re
 __device__ __forceinline__ int units_of(int2 v) {
   return v.y == 0 ? 0 : (v.y + kUnit - 1) / kUnit - v.x / kUnit;
 }
-__device__ __forceinline__ int64_t range_start(int64_t r, int64_t units, int32_t ranges) { return r * units / ranges; }
+__device__ __forceinline__ int64_t range_start(int r, int64_t units, int32_t ranges) {
+  if (units < (1 << 20)) return static_cast<uint32_t>(r) * static_cast<uint32_t>(units) / static_cast<uint32_t>(ranges);
+  return r * units / ranges;  // a 64-bit division takes some 0.3 us
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst_smem, const void* tmap, int c0, int c1, int c2, int c3,
                                             uint32_t bar) {
@@ -204,6 +229,26 @@ struct Walk {
   int unit;       // absolute unit (token / kUnit) of the sequence
   int last;       // the sequence's last unit
 };
+
+__device__ __forceinline__ void add_piece(float& M, float& L, float4& o, float2 ml, float4 x) {
+  const float top = fmaxf(M, ml.x), use = top == -INFINITY ? 0.f : top;
+  const float a = ex2_approx(M - use), b = ex2_approx(ml.x - use);
+  M = top;
+  L = L * a + ml.y * b;
+  o.x = o.x * a + x.x * b;
+  o.y = o.y * a + x.y * b;
+  o.z = o.z * a + x.z * b;
+  o.w = o.w * a + x.w * b;
+}
+template <Elem E>
+__device__ __forceinline__ void write_joined(const DecodeModParams& p, int seq, int h, int lane, float M, float L, float4 o) {
+  using Ops = ElemOps<E>;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t row = static_cast<int64_t>(seq) * p.hq + h;
+  *(reinterpret_cast<uint2*>(p.out + row * kHeadDim) + lane) =
+      make_uint2(Ops::pack(o.x * inv, o.y * inv), Ops::pack(o.z * inv, o.w * inv));
+  if (p.weights && lane == 0) p.final_ml[row] = make_float2(M, inv);
+}
 
 // NT: eights of query heads that a worker takes.
 template <Elem E, int NT>
@@ -265,30 +310,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int worker = static_cast<int>(blockIdx.x) * kWarps + warp;
   const int workers = static_cast<int>(gridDim.x) * kWarps;
   // A stream has all its ranges, or (more streams than workers) one range and a worker several streams.
-  const bool split = p.st.ranges > 1;
-  const int range = split ? worker / p.st.count : 0;
-  if (range >= ranges) {
+  const bool split = p.st.ranges > 1, by_cta = p.st.by_cta != 0;
+  const int cta_range = static_cast<int>(blockIdx.x) / p.st.count;  // by_cta: which eight ranges
+  const int range = by_cta ? cta_range * kWarps + warp : (split ? worker / p.st.count : 0);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + kOffPieces);
+  if (lane < 2) pieces[2 * warp + lane].seq = -1;
+  __syncwarp();
+  const bool idle = range >= ranges;
+  if (idle && !by_cta) {
     if (split && lane == 0 && worker % p.st.count == 0 && range < p.used_ranges) p.info[range].seq = -1;
     return;
   }
-  const int64_t start = range_start(range, units, ranges), end = range_start(range + 1, units, ranges);
+  const int64_t start = idle ? 0 : range_start(range, units, ranges);
+  const int64_t end = idle ? 0 : range_start(range + 1, units, ranges);
 
   // the sequence that holds unit `start`
-  int at = 0;
+  Walk begin{};
+  int64_t begin_first = 0;  // first unit of begin.b
+  if (!idle) {
+    int at = 0;
 #pragma unroll
-  for (int j = 0; j < kThreads / 32; ++j) at += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= start));
-  Walk begin;
-  int64_t begin_first = scan[at - 1];  // first unit of begin.b
-  begin.b = (at - 1) * per;
-  while (true) {
-    begin.seen = visible(p, begin.b, false);
-    const int n = units_of(begin.seen);
-    if (begin_first + n > start) break;
-    begin_first += n;
-    ++begin.b;
+    for (int j = 0; j < kThreads / 32; ++j) at += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= start));
+    begin_first = scan[at - 1];
+    begin.b = (at - 1) * per;
+    while (true) {
+      begin.seen = visible(p, begin.b, false);
+      const int n = units_of(begin.seen);
+      if (begin_first + n > start) break;
+      begin_first += n;
+      ++begin.b;
+    }
+    begin.last = (begin.seen.y - 1) / kUnit;
+    begin.unit = begin.seen.x / kUnit + static_cast<int>(start - begin_first);
   }
-  begin.last = (begin.seen.y - 1) / kUnit;
-  begin.unit = begin.seen.x / kUnit + static_cast<int>(start - begin_first);
 
   const int row16 = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: this lane's row of K
   const int rowv = (lane & 7) + (lane >> 4) * 8;         // and of V
@@ -297,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int stage = 0;
   bool ok = true;
 
-  for (int stream = split ? worker % p.st.count : worker; stream < p.st.count && ok; stream += workers) {
+  const int first_stream = by_cta ? static_cast<int>(blockIdx.x) % p.st.count : (split ? worker % p.st.count : worker);
+  for (int stream = first_stream; !idle && stream < p.st.count && ok; stream += workers) {
     const int hk = stream / p.st.parts, part = stream - hk * p.st.parts;
     const int head0 = hk * p.st.group + part * p.st.per;
     const int heads = min(p.st.per, p.st.group - part * p.st.per);
@@ -528,27 +583,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        const int64_t slot =
-            ((static_cast<int64_t>(range) * p.st.count + stream) * 2 + (first_unit <= start ? 0 : 1)) * p.st.heads;
+        const int place = first_unit <= start ? 0 : 1;
+        const int64_t slot = ((static_cast<int64_t>(range) * p.st.count + stream) * 2 + place) * p.st.heads;
+        float* o_to = p.o + slot * kHeadDim;
+        float2* ml_to = p.ml + slot;
+        if (by_cta) {
+          if (left == n) {  // no copies under way
+            o_to = reinterpret_cast<float*>(smem + warp * kStages * 2 * kUnitBytes);
+            ml_to = reinterpret_cast<float2*>(o_to + p.st.heads * kHeadDim);
+          }
+          if (lane == 0) {
+            Piece& piece = pieces[2 * warp + place];
+            piece.seq = now.b;
+            piece.ends = ends;
+            piece.first_unit = first_unit;
+            piece.end_unit = first_unit + (now.last - now.seen.x / kUnit + 1);
+            piece.ml = ml_to;
+            piece.o = o_to;
+          }
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int h = 8 * t + 2 * c + j;
             if (h < heads) {
-              float* o = p.o + (slot + h) * kHeadDim + r;
+              float* o = o_to + h * kHeadDim + r;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 o[16 * i] = acc[t][i][j];
                 o[16 * i + 8] = acc[t][i][j + 2];
               }
-              if (r == 0) p.ml[slot + h] = make_float2(m[t][j], l[t][j]);
+              if (r == 0) ml_to[h] = make_float2(m[t][j], l[t][j]);
             }
           }
       }
       left -= n;
       if (left == 0) {
-        if (stream == 0 && lane == 0) {
+        if (!by_cta && stream == 0 && lane == 0) {
           const int64_t last_unit = first_unit + (now.last - now.seen.x / kUnit);
           RangeInfo info;
           info.seq = begins && !ends ? now.b : -1;
@@ -572,6 +644,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bars + 8 * ((stage + i) % kStages), (phase >> ((stage + i) % kStages)) & 1u, p.err);
     }
   }
+  if (!by_cta) return;
+
+  // ---- the CTA's pieces, joined in order: pieces of one sequence lie side by side ----
+  __syncthreads();
+  const int stream = first_stream, hk = stream / p.st.parts, part = stream - hk * p.st.parts;
+  const int head0 = hk * p.st.group + part * p.st.per;
+  const int heads = min(p.st.per, p.st.group - part * p.st.per);
+  const int64_t cta_start = cta_range * kWarps < ranges ? range_start(cta_range * kWarps, units, ranges) : 0;
+  RangeInfo goes_on;
+  goes_on.seq = -1;
+  goes_on.last = goes_on.place = goes_on.pad = 0;
+  for (int i = 0, group = 0; i < kPieces; ++group) {
+    const Piece first = pieces[i];
+    if (first.seq < 0) {
+      ++i;
+      --group;
+      continue;
+    }
+    int n = i + 1;       // one behind the sequence's last piece here
+    bool ends = first.ends != 0;
+    for (int k = i + 1; k < kPieces; ++k) {
+      if (pieces[k].seq < 0) continue;
+      if (pieces[k].seq != first.seq) break;
+      ends = pieces[k].ends != 0;
+      n = k + 1;
+    }
+    const bool begins = first.first_unit >= cta_start;
+    const int place = first.first_unit <= cta_start ? 0 : 1;
+    for (int h = (warp - group) & (kWarps - 1); h < heads; h += kWarps) {
+      float M = -INFINITY, L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = i; k < n; ++k) {
+        if (pieces[k].seq < 0) continue;
+        const float2 ml = pieces[k].ml[h];
+        const float4 x = *(reinterpret_cast<const float4*>(pieces[k].o + h * kHeadDim) + lane);
+        add_piece(M, L, o, ml, x);
+      }
+      if (begins && ends) {
+        write_joined<E>(p, first.seq, head0 + h, lane, M, L, o);
+      } else {
+        const int64_t slot = ((static_cast<int64_t>(cta_range) * kWarps * p.st.count + stream) * 2 + place) * p.st.heads + h;
+        *(reinterpret_cast<float4*>(p.o + slot * kHeadDim) + lane) = o;
+        if (lane == 0) p.ml[slot] = make_float2(M, L);
+      }
+    }
+    if (begins && !ends) {
+      goes_on.seq = first.seq;
+      goes_on.last = static_cast<int>((first.end_unit * ranges - 1) / units) / kWarps;
+      goes_on.place = place;
+    }
+    i = n;
+  }
+  if (stream == 0 && tid == 0 && cta_range < p.used_ranges)
+    *reinterpret_cast<int4*>(p.info + cta_range) = *reinterpret_cast<const int4*>(&goes_on);
 }
 
 // Partial results r = first, first + step, ... up to last of one query head, joined: (max, sum) and four dims to a lane.
@@ -587,33 +713,17 @@ __device__ __forceinline__ void join(const DecodeModParams& p, int range, int pl
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int r = min(r0 + i * step, last);
-      const int64_t slot = ((static_cast<int64_t>(r) * p.st.count + stream) * 2 + (r == range ? place : 0)) * p.st.heads + in_part;
+      const int64_t slot =
+          ((static_cast<int64_t>(r) * p.range_step * p.st.count + stream) * 2 + (r == range ? place : 0)) * p.st.heads + in_part;
       ml[i] = p.ml[slot];
       x[i] = *(reinterpret_cast<const float4*>(p.o + slot * kHeadDim) + lane);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (r0 + i * step > last) break;
-      const float top = fmaxf(M, ml[i].x), use = top == -INFINITY ? 0.f : top;
-      const float a = ex2_approx(M - use), b = ex2_approx(ml[i].x - use);
-      M = top;
-      L = L * a + ml[i].y * b;
-      o.x = o.x * a + x[i].x * b;
-      o.y = o.y * a + x[i].y * b;
-      o.z = o.z * a + x[i].z * b;
-      o.w = o.w * a + x[i].w * b;
+      add_piece(M, L, o, ml[i], x[i]);
     }
   }
-}
-
-template <Elem E>
-__device__ __forceinline__ void write_joined(const DecodeModParams& p, int seq, int h, int lane, float M, float L, float4 o) {
-  using Ops = ElemOps<E>;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int64_t row = static_cast<int64_t>(seq) * p.hq + h;
-  *(reinterpret_cast<uint2*>(p.out + row * kHeadDim) + lane) =
-      make_uint2(Ops::pack(o.x * inv, o.y * inv), Ops::pack(o.z * inv, o.w * inv));
-  if (p.weights && lane == 0) p.final_ml[row] = make_float2(M, inv);
 }
 
 // A block joins what one query head of the sequences left that begin in its kMergeWarps ranges and go on behind them:
@@ -803,11 +913,11 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
 }  // namespace
 
 size_t decode_mod_workspace_bytes(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t max_ctx, bool weights) {
-  return layout_of(streams_of(hq, hkv), num_seqs, hq, max_ctx, weights).total;
+  return layout_of(streams_of(hq, hkv, num_seqs, max_ctx), num_seqs, hq, max_ctx, weights).total;
 }
 
 cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStream_t stream, Elem elem) {
-  const Streams st = streams_of(a.hq, a.hkv);
+  const Streams st = streams_of(a.hq, a.hkv, a.num_seqs, a.max_ctx);
   const bool weights = a.weights != nullptr;
   const Layout lay = layout_of(st, a.num_seqs, a.hq, a.max_ctx, weights);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -844,9 +954,11 @@ cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStr
     return cudaErrorInvalidValue;
   // no more workers than the longest lengths could keep busy
   const int64_t fill = (p.seq_units * a.num_seqs + kMinUnits - 1) / kMinUnits;
-  p.used_ranges = static_cast<int32_t>(fill < st.ranges ? fill : st.ranges);
-  const int64_t most = fill * st.count;
-  const int64_t want = (most + kWarps - 1) / kWarps;
+  const int32_t used = static_cast<int32_t>(fill < st.ranges ? fill : st.ranges);
+  p.range_step = st.by_cta ? kWarps : 1;
+  p.used_ranges = (used + p.range_step - 1) / p.range_step;
+  const int64_t want = st.by_cta ? static_cast<int64_t>(p.used_ranges) * st.count
+                                 : (fill * st.count + kWarps - 1) / kWarps;
   const int ctas = static_cast<int>(want < 1 ? 1 : (want < kCtas ? want : kCtas));
   const bool f16 = elem == Elem::kF16;
   cudaError_t e;
