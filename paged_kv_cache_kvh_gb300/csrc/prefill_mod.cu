@@ -29,8 +29,9 @@
 // (0 * NaN). The rows of V behind the sequence's end, which may hold anything, are zeroed in shared memory. Elsewhere
 // such values are rare, so they are found in the result: a row whose sum is not finite is computed once more by its
 // warp from the rows in memory, one key to a lane, with the keys that it does not see left out.
-#include <atomic>
+#include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include <cuda.h>
 
@@ -127,6 +128,7 @@ struct PrefillModParams {
   int32_t hq, group;      // query heads; per kv head
   int32_t neighbours;     // the two softmax groups are neighbouring tiles of one head, not two heads
   int32_t units;          // head pairs, or heads
+  int32_t first;          // this launch's first item
   float scale, scale_log2;
   float softcap;
   float cap_log2, scale_by_cap;
@@ -298,7 +300,41 @@ __device__ __noinline__ void row_again(const PrefillModParams& p, int b, int64_t
       make_uint2(Ops::pack(acc[0] * inv, acc[1] * inv), Ops::pack(acc[2] * inv, acc[3] * inv));
 }
 
-template <Elem E, bool kCap, bool kBias>
+// The cluster of CTAs that split the keys of one item (kSplit).
+__device__ __forceinline__ int cluster_parts() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ int cluster_part() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// this CTA's shared address -> the same place in another CTA of the cluster
+__device__ __forceinline__ uint32_t in_part(uint32_t addr, int part) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(part));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+
+// The launch of split items may begin while the one before it still runs, and must not be over before that is.
+__device__ __forceinline__ void wait_for_others() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// kSplit: the CTAs of a cluster have parts of one item's keys.
+template <Elem E, bool kCap, bool kBias, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefillModParams p) {
@@ -320,10 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   // ---- work item: (query tile, sequence, heads), the last query tiles (the longest key ranges) first ----
-  const int cta = static_cast<int>(blockIdx.x);
+  if (!kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // items split over clusters fill the end
+  const int parts = kSplit ? cluster_parts() : 1, part = kSplit ? cluster_part() : 0;
+  const int item = p.first + static_cast<int>(blockIdx.x) / parts;
   const int per_tile = p.num_seqs * p.units;
-  const int qt = p.q_tiles - 1 - cta / per_tile;
-  const int b = (cta % per_tile) / p.units, unit = cta % p.units;
+  const int qt = p.q_tiles - 1 - item / per_tile;
+  const int b = (item % per_tile) / p.units, unit = item % p.units;
   const int head0 = p.neighbours ? unit : 2 * unit;
   const int hk = head0 / p.group;
 
@@ -334,22 +372,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                    (p.paged ? Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize : (ck0 < 0 || ck1 > p.total_k));
   if (bad) {
     if (threadIdx.x == 0 && qt == 0 && unit == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+    if (kSplit) wait_for_others();
     return;
   }
   const int r0 = qt * (p.neighbours ? 2 * kBM : kBM);
-  if (r0 >= Lq) return;
+  if (r0 >= Lq) {
+    if (kSplit) wait_for_others();
+    return;
+  }
 
   // The softmax thread of a row: its position and the keys it sees. Rows behind the last one take its place.
   const int g = (warp - 4) >> 3, half = (warp >> 2) & 1 ? 0 : 1;  // warps 4..7 and 12..15 take the first keys of a tile
   const int rows32 = 4 * g + (warp & 3);                           // the warp's 32 rows, of 8 times 32
   const int row = (warp & 3) * 32 + lane;  // within the group's tile == TMEM lane
   const int g_row0 = r0 + (p.neighbours && g > 0 ? kBM : 0);
-  const int pos = Lk - Lq + min(g_row0 + row, Lq - 1);
-  int lo = 0, hi = 0, any_lo = 0, any_hi = 0;  // seen by the row; by any of the warp's rows
+  auto seen_from = [&](int r, int& pos_, int& lo_, int& hi_) {  // r: row of the sequence
+    r = min(r, Lq - 1);
+    pos_ = Lk - Lq + r;
+    lo_ = p.window > 0 ? max(0, pos_ - p.window + 1) : 0;
+    if (p.key_starts) lo_ = max(lo_, p.key_starts[cq0 + r]);
+    hi_ = min(Lk, max(pos_ + 1, p.prefix_lens ? p.prefix_lens[b] : 0));
+  };
+  int pos = 0, lo = 0, hi = 0, any_lo = 0, any_hi = 0;  // seen by the row; by any of the warp's rows
   if (warp >= 4) {
-    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    if (p.key_starts) lo = max(lo, p.key_starts[cq0 + min(g_row0 + row, Lq - 1)]);
-    hi = min(Lk, max(pos + 1, p.prefix_lens ? p.prefix_lens[b] : 0));
+    seen_from(g_row0 + row, pos, lo, hi);
     // a row without keys widens nothing
     any_lo = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX);
     any_hi = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
@@ -395,10 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     end_key = max(end_key, s_hi[i]);
   }
   // rows that see nothing at all: one tile, all masked
-  const int tile0 = first_key < end_key ? first_key / kBN : 0;
-  const int n_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - tile0 : 1;
+  const int all_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - first_key / kBN : 1;
+  const int tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
+  const int n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;  // 0 at times
   const int tail_keys = Lk - (tile0 + n_tiles - 1) * kBN;  // keys that the last tile has
-  const bool v_tail = tail_keys < kBN;
+  const bool v_tail = tail_keys < kBN && n_tiles > 0;
 
   auto k_row = [&](int n) -> int {  // where tile tile0 + n begins
     const int key0 = (tile0 + n) * kBN;
@@ -491,8 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (n > 0 || ks > 0) ? 1u : 0u);
         }
       };
-      if (ok) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
-      if (ok) {
+      const bool any = !kSplit || n_tiles > 0;
+      if (ok && any) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
+      if (ok && any) {
         tc_fence_after();
         issue_s(0, 0);
         mma_commit(bar(kBarSFull + 0));
@@ -714,6 +762,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) s_sum[half * kBM] = l;
     pair_sync();
     if (ok) l += s_sum[(half ^ 1) * kBM];
+    if constexpr (kSplit) {
+      // The parts' references and sums are exchanged; then every row is scaled for the common ones and goes to the CTA
+      // that adds up its parts, in their order: rows_own of the 256 rows each. Q, P and the ring are idle in every CTA
+      // by then, and the rows arrive where Q and P were.
+      const int rows_own = 2 * kBM / parts, ri = g * kBM + row;
+      const uint32_t ml = sbase + kOffKV + 8 * kBM;  // behind the pair's sums
+      float ref = by_maximum ? m : 0.f;
+      if (!ok || n_tiles == 0) {
+        ref = -INFINITY;
+        l = 0.f;
+      }
+      if (half == 0) asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml + ri * 8), "f"(ref), "f"(l) : "memory");
+      cluster_sync();
+      float M = -INFINITY, L = 0.f;
+      for (int i = 0; i < parts; ++i) M = fmaxf(M, ld_cluster_f2(in_part(ml + ri * 8, i)).x);
+      if (M == -INFINITY) M = 0.f;
+      for (int i = 0; i < parts; ++i) {
+        const float2 v = ld_cluster_f2(in_part(ml + ri * 8, i));
+        L = fmaf(ex2_approx(v.x - M), v.y, L);
+      }
+      const float inv = ex2_approx(ref - M) * (L == 0.f ? 0.f : 1.f / L);
+      const uint32_t dst = in_part(sbase + kOffQ + (part * rows_own + ri % rows_own) * 512, ri / rows_own);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c) {
+        uint32_t x[32];
+        if (ok && n_tiles > 0) {
+          tmem_ld32(tO + c * 32, x);
+          tmem_wait_ld();
+          tmem_reg_fence(x);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          st_cluster_f4(dst + (((half * 16 + c * 8 + j / 4) ^ (row & 31)) << 4), __uint_as_float(x[j]) * inv,
+                        __uint_as_float(x[j + 1]) * inv, __uint_as_float(x[j + 2]) * inv, __uint_as_float(x[j + 3]) * inv);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarStaged));
+      cluster_sync();
+      for (int lr = warp - 4; lr < rows_own; lr += kSoftmaxWarps) {
+        const int r2 = part * rows_own + lr, g2 = r2 / kBM, q_row = r2 % kBM;
+        const int seq_row = r0 + q_row + (p.neighbours ? g2 * kBM : 0), to_head = head0 + (p.neighbours ? 0 : g2);
+        if (seq_row >= Lq) continue;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < parts; ++i) {
+          float4 v;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "r"(sbase + kOffQ + (i * rows_own + lr) * 512 + ((lane ^ (q_row & 31)) << 4))
+                       : "memory");
+          o.x += v.x;
+          o.y += v.y;
+          o.z += v.z;
+          o.w += v.w;
+        }
+        const int64_t out_row = static_cast<int64_t>(cq0) + seq_row;
+        if (__any_sync(0xffffffffu, isnan(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)))))) {
+          int row_pos, row_lo, row_hi;
+          seen_from(seq_row, row_pos, row_lo, row_hi);
+          row_again<E>(p, b, ck0, out_row, to_head, row_pos, row_lo, row_hi, lane);
+        } else {
+          *(reinterpret_cast<uint2*>(p.out + (out_row * p.hq + to_head) * kHeadDim) + lane) =
+              make_uint2(Ops::pack(o.x, o.y), Ops::pack(o.z, o.w));
+        }
+      }
+      wait_for_others();
+      return;
+    }
     if (ok) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -769,6 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (kSplit) {  // (warps 0 to 3 here) every thread of a cluster comes to both of its barriers
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     // TMEM is released after every softmax warp's last tensor-memory read
     // (they all arrive on kBarStaged once O is staged); no CTA-wide barrier,
@@ -778,6 +902,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(bar(kBarStaged), 0, p.err);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (kSplit) {
+    cluster_sync();
+    wait_for_others();
   }
 }
 
@@ -814,31 +942,110 @@ bool encode_rows_heads_dims(CUtensorMap* tm, const void* base, int64_t rows, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct DeviceLimits {
+  bool known;
+  int sms;
+  int clusters[4];  // [i], i > 0: clusters of 2^i CTAs that run at once
+};
+
 template <Elem E, bool kCap, bool kBias>
-cudaError_t launch_typed(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillModParams& p,
-                         unsigned blocks, cudaStream_t stream) {
-  static std::atomic<bool> attr_done[64];
+cudaError_t device_limits(DeviceLimits* out) {
+  static DeviceLimits all[64];
+  static std::mutex lock;
+  const std::lock_guard<std::mutex> hold(lock);
   int dev = 0;
-  cudaGetDevice(&dev);
-  const bool known = dev >= 0 && dev < 64;
-  if (!known || !attr_done[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<E, kCap, kBias>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-    if (e != cudaSuccess) return e;
-    if (known) attr_done[dev].store(true, std::memory_order_release);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && all[dev].known) {
+    *out = all[dev];
+    return cudaSuccess;
   }
-  prefill_mod_kernel<E, kCap, kBias><<<blocks, kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  DeviceLimits d{};
+  e = cudaFuncSetAttribute(prefill_mod_kernel<E, kCap, kBias, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prefill_mod_kernel<E, kCap, kBias, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes));
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+  for (int i = 1; i < 4 && e == cudaSuccess; ++i) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(d.sms) << i);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1u << i;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&d.clusters[i], prefill_mod_kernel<E, kCap, kBias, true>, &cfg);
+  }
+  if (e != cudaSuccess) return e;
+  d.known = true;
+  if (dev >= 0 && dev < 64) all[dev] = d;
+  *out = d;
+  return cudaSuccess;
+}
+
+// The items run longest first, one CTA to an SM. What is left of them after whole rounds would keep a few SMs busy for one
+// more item, and a call of few items uses few SMs from the start. Where all of that rest can run at once with each item's
+// keys split over a cluster of 2, 4 or 8 CTAs, it does, as a launch of its own that fills SMs as the first one leaves
+// them, the most parts first that leave a part kMinPartTiles key tiles. Times in key tiles (about 1.9 us each), as far as
+// the bounds of the lengths tell them: the rest takes `tiles` as it is, less what it fits into the first round's uneven
+// end (after an even number of rounds the long and the short items have evened out), and tiles / parts when split, plus
+// 2 for the join and 2 for the launch beside others.
+constexpr int kMinPartTiles = 2;
+template <Elem E, bool kCap, bool kBias>
+cudaError_t launch_typed(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, PrefillModParams& p,
+                         int64_t n_items, int64_t max_tiles, int64_t seen_tiles, cudaStream_t stream) {
+  DeviceLimits d;
+  cudaError_t e = device_limits<E, kCap, kBias>(&d);
+  if (e != cudaSuccess) return e;
+  const int64_t rest = n_items % d.sms, rounds = n_items / d.sms;
+  int shift = 0;
+  if (rest > 0) {
+    const int64_t per_tile = static_cast<int64_t>(p.num_seqs) * p.units;  // items as long as one another
+    const int64_t shorter = (n_items - rest) / per_tile * (p.neighbours ? 2 : 1);
+    const int64_t tiles = std::min(max_tiles - shorter, seen_tiles);  // key tiles of the first of the rest
+    const int64_t uneven = rounds % 2 == 1 ? d.sms / per_tile : 0;
+    for (int i = 1; i < 4; ++i) {
+      const int64_t split = (tiles >> i) + (rounds > 0 ? 4 : 2);
+      if (rest <= d.clusters[i] && tiles >> i >= kMinPartTiles && tiles - uneven - split >= 2) shift = i;
+    }
+  }
+  const int64_t whole = shift > 0 ? n_items - rest : n_items;
+  p.first = 0;
+  if (whole > 0) {
+    prefill_mod_kernel<E, kCap, kBias, false><<<static_cast<unsigned>(whole), kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (shift == 0) return cudaSuccess;
+  p.first = static_cast<int32_t>(whole);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rest) << shift);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1u << shift;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = whole > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, prefill_mod_kernel<E, kCap, kBias, true>, tq, tk, tv,
+                            const_cast<const PrefillModParams&>(p));
 }
 
 template <Elem E>
-cudaError_t launch_elem(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillModParams& p,
-                        unsigned blocks, cudaStream_t stream) {
+cudaError_t launch_elem(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, PrefillModParams& p,
+                        int64_t n_items, int64_t max_tiles, int64_t seen_tiles, cudaStream_t stream) {
   if (p.softcap > 0.f)
-    return p.slopes ? launch_typed<E, true, true>(tq, tk, tv, p, blocks, stream)
-                    : launch_typed<E, true, false>(tq, tk, tv, p, blocks, stream);
-  return p.slopes ? launch_typed<E, false, true>(tq, tk, tv, p, blocks, stream)
-                  : launch_typed<E, false, false>(tq, tk, tv, p, blocks, stream);
+    return p.slopes ? launch_typed<E, true, true>(tq, tk, tv, p, n_items, max_tiles, seen_tiles, stream)
+                    : launch_typed<E, true, false>(tq, tk, tv, p, n_items, max_tiles, seen_tiles, stream);
+  return p.slopes ? launch_typed<E, false, true>(tq, tk, tv, p, n_items, max_tiles, seen_tiles, stream)
+                  : launch_typed<E, false, false>(tq, tk, tv, p, n_items, max_tiles, seen_tiles, stream);
 }
 
 // z = sum over i of scale_log2 c_i c^2i (q.k)^(2i + 1), c = scale / cap. Where the powers of c leave fp32's range (odd
@@ -878,7 +1085,7 @@ cudaError_t launch_prefill_mod(const PrefillModArgs& a, unsigned int* err, cudaS
   p.neighbours = p.group % 2;
   p.units = p.neighbours ? a.hq : a.hq / 2;
   const int rows = p.neighbours ? 2 * kBM : kBM;
-  p.q_tiles = static_cast<int32_t>((static_cast<int64_t>(a.max_seqlen_q) + rows - 1) / rows);
+  p.q_tiles = static_cast<int32_t>((static_cast<int64_t>(std::min(a.max_seqlen_q, a.total_q)) + rows - 1) / rows);
   p.max_seqlen_q = a.max_seqlen_q;
   p.max_seqlen_k = a.max_seqlen_k;
   p.total_q = a.total_q;
@@ -904,10 +1111,15 @@ cudaError_t launch_prefill_mod(const PrefillModArgs& a, unsigned int* err, cudaS
   p.kv_stride = kv_stride;
   p.out = static_cast<uint16_t*>(a.out);
   p.err = err;
-  const int64_t blocks = static_cast<int64_t>(p.q_tiles) * a.num_seqs * p.units;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return elem == Elem::kF16 ? launch_elem<Elem::kF16>(tq, tk, tv, p, static_cast<unsigned>(blocks), stream)
-                            : launch_elem<Elem::kBF16>(tq, tk, tv, p, static_cast<unsigned>(blocks), stream);
+  const int64_t n_items = static_cast<int64_t>(p.q_tiles) * a.num_seqs * p.units;
+  if (n_items > 0x7fffffff) return cudaErrorInvalidValue;
+  // key tiles of the last query tile at most
+  int64_t keys = a.max_seqlen_k;
+  if (paged) keys = std::min(keys, static_cast<int64_t>(a.bt_stride) * kBlockSize);
+  const int64_t max_tiles = (keys + kBN - 1) / kBN;
+  const int64_t seen_tiles = a.window > 0 && !a.prefix_lens ? (static_cast<int64_t>(a.window) + rows) / kBN + 1 : max_tiles;
+  return elem == Elem::kF16 ? launch_elem<Elem::kF16>(tq, tk, tv, p, n_items, max_tiles, seen_tiles, stream)
+                            : launch_elem<Elem::kBF16>(tq, tk, tv, p, n_items, max_tiles, seen_tiles, stream);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -295,3 +295,62 @@ def test_binding_refusals(pkv):
             call(**kw)
         assert e.value.status == -6
     assert call(q=c.q[:0]).shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("mods", list(MODS))
+@pytest.mark.parametrize("seqs,hq,hkv", [
+    ([(2500, 200)], 16, 8), ([(3000, 1)], 4, 1), ([(1000, 130), (0, 5), (2000, 64)], 3, 1), ([(900, 300), (0, 0)], 12, 12),
+    ([(7, 2600)], 16, 8),           # full rounds of tiles and a rest
+    ([(1500, 129), (20, 3)], 2, 1),
+])
+def test_split_keys(pkv, seqs, hq, hkv, dtype, mods):
+    """Few query tiles, or few beyond whole rounds of them: their keys are split over clusters of CTAs."""
+    c = Case(seqs, hq, hkv, dtype, seed=hq + len(seqs))
+    m = _mods(MODS[mods], c)
+    out = torch.full((c.q.shape[0], hq, D), 7.0, dtype=dtype, device="cuda")
+    c.run(pkv, out=out, **m)
+    c.check(out, **m)
+    assert bool((out[c.cu_q[-1]:] == 7).all())
+    assert torch.equal(c.run(pkv, **m)[:c.cu_q[-1]], out[:c.cu_q[-1]])
+    assert pkv.pkv_device_error() == 0
+
+
+def test_split_keys_values_behind_the_mask(pkv):
+    c = Case([(2000, 100)], 4, 2, torch.bfloat16)
+    clean = c.run(pkv)
+    c.set_v(0, 2050, 0, 9, float("nan"))
+    c.set_v(0, 60, 1, 100, float("inf"))
+    out = c.run(pkv)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[50:100, :2, 9] = True
+    bad[:100, 2:, 100] = True
+    assert torch.equal(~torch.isfinite(out[:100]), bad[:100])
+    room = 2.0 ** -7 * (clean[:100].float().abs() + 8)
+    assert bool(((out[:100].float() - clean[:100].float()).abs() <= room)[~bad[:100]].all())
+
+
+def test_split_keys_in_a_graph_and_bad_blocks(pkv):
+    """The launch of split items runs beside the one before it: what follows on the stream sees all of both."""
+    c = Case([(7, 2600)], 16, 8, torch.bfloat16)
+    want = c.run(pkv, softcap=20.0)
+    out, seen = torch.zeros_like(want), torch.zeros_like(want)
+    cu = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (c.cu_q, c.cu_k)]
+    tables = c.tables.cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out.zero_()
+        pkv.pkv_prefill_varlen_mod(c.q, *cu, c.max_q, c.max_k, D ** -0.5, k_cache=c.kc, v_cache=c.vc, block_tables=tables,
+                                   softcap=20.0, out=out)
+        seen.copy_(out)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(seen[:2600], want[:2600])
+    c.tables[0, 3] = -1
+    c.run(pkv)
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_BLOCK
+    c.tables[0, 3] = int(tables[0, 3])
+    c.cu_q[1] = 2700          # more rows than q has
+    c.run(pkv)
+    assert pkv.pkv_device_error() == pkv.PKV_DEVERR_BAD_SEQLEN
