@@ -62,9 +62,10 @@ class Case:
         return fn(self.q, *cu, self.max_q, self.max_k, scale, out=out, stream=stream, **keys, **mods)
 
     def check(self, out, scale=D ** -0.5, prefix_lens=None, key_starts=None, **mods):
-        """p is rounded to 16 bits for the product with V, up to 2^8 above the running maximum's scale: half a step of
-        each p; the polynomials for tanh are off by 6.9e-6 (bf16) or 6.1e-7 (fp16) of a score, which the cap bounds; then the
-        result's own rounding."""
+        """p is rounded to 16 bits for the product with V: q = p (1 + e) with |e| at most half a step, eps. The result is
+        sum q v / sum p or, where few keys are seen, sum q v / sum q. The first is off by sum p e v, at most eps sum p |v|;
+        the second by sum p e (v - result), at most eps (sum p |v| + |result|). The polynomials for tanh are off by 6.9e-6
+        (bf16) or 6.1e-7 (fp16) of a score, which the cap bounds; then the result's own rounding, eps |result|."""
         worst = 0.0
         eps = torch.finfo(self.dtype).eps / 2
         for b, (c, n) in enumerate(self.seqs):
@@ -80,7 +81,7 @@ class Case:
                 cap = (6.9e-6 if self.dtype == torch.bfloat16 else 6.1e-7) * mods.get("softcap", 0.0)
                 size = torch.einsum("hnt,thd->nhd", p, self.v[k0:k0 + total].double().abs().nan_to_num(0, 0, 0)
                                     .repeat_interleave(self.hq // self.hkv, 1))
-                room = ref.abs() * eps + size * (eps + 2 * cap + 2.0 ** -18) + bound + 2.0 ** -25
+                room = ref.abs() * 2 * eps + size * (eps + 2 * cap + 2.0 ** -18) + bound + 2.0 ** -25
                 got = out[q0 + a:q0 + z].double()
                 err = (got - ref).abs()
                 assert bool((err <= room).all()), (b, a, float((err / room).max()))
