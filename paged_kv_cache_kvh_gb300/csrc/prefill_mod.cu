@@ -406,47 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  // Thread 0 is the TMA warp's issuing lane: the queries are on their way before anything else is set up.
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i == kBarStaged ? kSoftmaxWarps : (i == kBarPReady || i == kBarPReady + 1 ? 8 : 1));
-    *s_abort = 0;
-    mbar_fence_init();
-    prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-    mbar_arrive_expect_tx(bar(kBarQ), 2 * kTileBytes);
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t dst = sbase + kOffQ + i * kTileBytes;
-      const int head = head0 + (p.neighbours ? 0 : i), first = cq0 + r0 + (p.neighbours ? i * kBM : 0);
-      tma_load_3d(dst, &tm_q, 0, head, first, bar(kBarQ));
-      tma_load_3d(dst + kHalfBytes, &tm_q, 64, head, first, bar(kBarQ));
-    }
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(s_tmem), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncwarp();  // warp 0 arrives converged, after thread 0 has initialised the barriers
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *s_tmem;
-
   // ---- the key tiles ----
-  int first_key = INT32_MAX, end_key = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    first_key = min(first_key, s_lo[i]);
-    end_key = max(end_key, s_hi[i]);
-  }
-  // rows that see nothing at all: one tile, all masked
-  const int all_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - first_key / kBN : 1;
-  const int tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
-  const int n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;  // 0 at times
-  const int tail_keys = Lk - (tile0 + n_tiles - 1) * kBN;  // keys that the last tile has
-  const bool v_tail = tail_keys < kBN && n_tiles > 0;
-
+  int tile0 = 0, n_tiles = 0;  // a split item's part may have none
+  auto set_tiles = [&](int first_key, int end_key) {
+    // rows that see nothing at all: one tile, all masked
+    const int all_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - first_key / kBN : 1;
+    tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
+    n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;
+  };
   auto k_row = [&](int n) -> int {  // where tile tile0 + n begins
     const int key0 = (tile0 + n) * kBN;
     if (!p.paged) return ck0 + key0;
@@ -467,12 +434,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_load_3d(dst, tm, 0, hk, at, bar(kBarKvFull + slot));
     tma_load_3d(dst + kHalfBytes, tm, 64, hk, at, bar(kBarKvFull + slot));
   };
+  // Without first keys of single rows every row sees at least itself, and the range follows from the first and last row.
+  if (!p.key_starts) {
+    const int pos0 = Lk - Lq + r0, last = Lk - Lq + min(r0 + (p.neighbours ? 2 * kBM : kBM), Lq);
+    set_tiles(p.window > 0 ? max(0, pos0 - p.window + 1) : 0, min(Lk, max(last, p.prefix_lens ? p.prefix_lens[b] : 0)));
+  }
+
+  // Thread 0 is the TMA warp's issuing lane: the queries and, where their place is known, the first keys and values are on
+  // their way before anything else is set up.
+  int issued = 0;  // ring items (thread 0)
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bar(i), i == kBarStaged ? kSoftmaxWarps : (i == kBarPReady || i == kBarPReady + 1 ? 8 : 1));
+    *s_abort = 0;
+    mbar_fence_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    mbar_arrive_expect_tx(bar(kBarQ), 2 * kTileBytes);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t dst = sbase + kOffQ + i * kTileBytes;
+      const int head = head0 + (p.neighbours ? 0 : i), first = cq0 + r0 + (p.neighbours ? i * kBM : 0);
+      tma_load_3d(dst, &tm_q, 0, head, first, bar(kBarQ));
+      tma_load_3d(dst + kHalfBytes, &tm_q, 64, head, first, bar(kBarQ));
+    }
+    for (; issued < kKvSlots && issued < 2 * n_tiles; ++issued) load_kv(issued);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncwarp();  // warp 0 arrives converged, after thread 0 has initialised the barriers
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (p.key_starts) {
+    int first_key = INT32_MAX, end_key = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      first_key = min(first_key, s_lo[i]);
+      end_key = max(end_key, s_hi[i]);
+    }
+    set_tiles(first_key, end_key);
+  }
+  const int tail_keys = Lk - (tile0 + n_tiles - 1) * kBN;  // keys that the last tile has
+  const bool v_tail = tail_keys < kBN && n_tiles > 0;
 
   if (warp == 0) {
     // =========================== TMA producer ===========================
-    int issued = 0;
     if (lane == 0) {
-      for (int i = 0; i < 2 * n_tiles; ++i) {
+      for (int i = issued; i < 2 * n_tiles; ++i) {
         const int slot = i % kKvSlots;
         if (i >= kKvSlots && !wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err))
           break;
