@@ -414,8 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
     n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;
   };
-  auto k_row = [&](int n) -> int {  // where tile tile0 + n begins
-    const int key0 = (tile0 + n) * kBN;
+  // Tile n of this CTA's. A bias favours the nearest keys: from the last tile to the first, the reference is found in the
+  // first one and stays (5000 on 7001: 404 us from the first on, 331 from the last; without a bias 308 and 326).
+  constexpr bool kBack = kBias;
+  auto first_key_of = [&](int n) { return (tile0 + (kBack ? n_tiles - 1 - n : n)) * kBN; };
+  auto k_row = [&](int n) -> int {  // where tile n begins
+    const int key0 = first_key_of(n);
     if (!p.paged) return ck0 + key0;
     int blk = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + key0 / kBlockSize];
     if (blk < 0 || blk >= p.num_blocks) {
@@ -481,24 +485,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int tail_keys = Lk - (tile0 + n_tiles - 1) * kBN;  // keys that the last tile has
   const bool v_tail = tail_keys < kBN && n_tiles > 0;
+  const int tail_item = kBack ? 1 : 2 * n_tiles - 1;       // the ring item of its values
 
   if (warp == 0) {
     // =========================== TMA producer ===========================
-    if (lane == 0) {
-      for (int i = issued; i < 2 * n_tiles; ++i) {
-        const int slot = i % kKvSlots;
-        if (i >= kKvSlots && !wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err))
-          break;
-        load_kv(i);
-        ++issued;
+    auto issue_up_to = [&](int end) {
+      if (lane == 0) {
+        for (int i = issued; i < end; ++i) {
+          const int slot = i % kKvSlots;
+          if (i >= kKvSlots && !wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err))
+            break;
+          load_kv(i);
+          ++issued;
+        }
       }
-    }
-    issued = __shfl_sync(0xffffffffu, issued, 0);
-    if (v_tail && issued == 2 * n_tiles) {
-      // Zero the rows of the last V tile that lie past the sequence end.
-      const int i = 2 * n_tiles - 1;
-      const int slot = i % kKvSlots;
-      const bool ok = wait_or_abort(bar(kBarKvFull + slot), (i / kKvSlots) & 1, s_abort, p.err);
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+    };
+    issue_up_to(kBack ? min(kKvSlots, 2 * n_tiles) : 2 * n_tiles);
+    if (v_tail && issued > tail_item) {
+      // Zero the rows of the sequence's last V tile that lie past its end.
+      const int slot = tail_item % kKvSlots;
+      const bool ok = wait_or_abort(bar(kBarKvFull + slot), (tail_item / kKvSlots) & 1, s_abort, p.err);
       if (ok) {
         const uint32_t base = sbase + kOffKV + slot * kTileBytes;
         // rows tail_keys..127 of both 64-dim halves: 128-byte rows, swizzle
@@ -506,15 +513,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nz = (kBN - tail_keys) * 2 * 8;  // 16-byte chunks
         for (int c = lane; c < nz; c += 32) {
           const int at = tail_keys + (c >> 4);
-          const int half = (c >> 3) & 1;
+          const int half_ = (c >> 3) & 1;
           const int chunk = c & 7;
-          sts128(base + half * kHalfBytes + at * 128 + chunk * 16, 0u, 0u, 0u, 0u);
+          sts128(base + half_ * kHalfBytes + at * 128 + chunk * 16, 0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarVTail));
     }
+    issue_up_to(2 * n_tiles);
     if (lane == 0) {
       // Never leave a copy in flight into this CTA's shared memory.
       mbar_wait(bar(kBarQ), 0, p.err);
@@ -563,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int n = 0; ok && n < n_tiles; ++n) {
         const int iv = 2 * n + 1;
-        if (n == n_tiles - 1 && v_tail)
+        if (iv == tail_item && v_tail)
           ok = wait_or_abort(bar(kBarVTail), 0, s_abort, p.err);
         else
           ok = wait_or_abort(bar(kBarKvFull + slot_of(iv)), par_of(iv), s_abort, p.err);
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       tc_fence_after();
-      const int key0 = (tile0 + n) * kBN + half * kCols;
+      const int key0 = first_key_of(n) + half * kCols;
       const bool none = key0 + kCols <= any_lo || key0 >= any_hi;  // no row sees any of these keys
       float s[kCols], mx = -INFINITY;
       const float base = m == -INFINITY ? 0.f : m;
