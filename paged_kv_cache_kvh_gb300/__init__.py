@@ -690,6 +690,10 @@ def pkv_build_decode_metadata(num_tokens, block_tables, num_blocks, stream=None)
 
 # ---- rotary positions ----------------------------------------------------------------
 
+# Outputs on the current device and stream without the dispatcher and its device guard: 2 us less a call, and the launch
+# behind it is cheaper too.
+_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+
 ROPE_SCALINGS = ("none", "linear", "ntk", "bands", "yarn")  # the PKV_ROPE_* codes in order
 
 
@@ -732,9 +736,10 @@ def _i64_array(t, dev, name):
 def _turned(t, out, dtype, dev, shape, name, stream):
     """The rows that a turned tensor goes to, and the elements between them."""
     if out is None:
-        out = (torch.empty_like(t, memory_format=torch.contiguous_format) if stream is None
-               else _made(torch.empty, t.shape, dtype, t.device, stream))
-        return out, shape[1] * shape[2]
+        row = shape[1] * shape[2]
+        out = (_empty_cuda(shape, (row, shape[2], 1), dtype) if stream is None
+               else _made(torch.empty, shape, dtype, t.device, stream))
+        return out, row
     n, heads, dims, row = _head_rows(out, dev, dtype, name)
     if (n, heads, dims) != shape:
         raise ValueError(f"{name} must have the shape of its input")
@@ -898,7 +903,7 @@ def _decode_mod(entry, dtype, q, k_cache, v_cache, block_tables, context_lens, m
     key_starts = None if key_starts is None else _i32_optional(key_starts, dev, B, "key_starts")
     weights = None if weights is None else _weight_pool(weights, dev, blocks, hkv)
     if out is None:
-        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+        out = (_empty_cuda((B, hq, HEAD_DIM), (hq * HEAD_DIM, HEAD_DIM, 1), dtype) if stream is None
                else _made(torch.empty, q.shape, dtype, q.device, stream))
     else:
         _dense(out, dev, dtype, (B, hq, HEAD_DIM), "out")
@@ -961,7 +966,7 @@ def _prefill_mod(entry, dtype, q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_
     key_starts = None if key_starts is None else _i32_optional(key_starts, dev, total_q, "key_starts")
     prefix_lens = None if prefix_lens is None else _i32_optional(prefix_lens, dev, num_seqs, "prefix_lens")
     if out is None:
-        out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+        out = (_empty_cuda((total_q, hq, HEAD_DIM), (hq * HEAD_DIM, HEAD_DIM, 1), dtype) if stream is None
                else _made(torch.empty, q.shape, dtype, q.device, stream))
     else:
         _dense(out, dev, dtype, (total_q, hq, HEAD_DIM), "out")
@@ -1020,9 +1025,10 @@ def pkv_evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, max
             raise ValueError("new_block_tables must be [B, width]")
         new_at, new_width = new_block_tables.data_ptr(), new_block_tables.shape[1]
     made = []
-    for t, shape, name in ((kept, (B, hkv, budget), "kept"), (new_context_lens, (B,), "new_context_lens")):
+    for t, shape, strides, name in ((kept, (B, hkv, budget), (hkv * budget, budget, 1), "kept"),
+                                    (new_context_lens, (B,), (1,), "new_context_lens")):
         if t is None:
-            t = (torch.empty(shape, dtype=_I32, device=k_cache.device) if stream is None
+            t = (_empty_cuda(shape, strides, _I32) if stream is None
                  else _made(torch.empty, shape, _I32, k_cache.device, stream))
         else:
             _table(t, dev, name)
