@@ -41,7 +41,7 @@ def _check(got, x, positions, freqs, interleaved, magnitude):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("n,hq,hkv,dims,rot,pad,offset", [
     (1, 16, 8, 128, 128, 0, 0),
-    (7, 16, 8, 128, 128, 2048, 0),
+    (7, 16, 8, 128, 128, 2056, 0),
     (5, 32, 8, 128, 64, 8, 8),
     (9, 3, 1, 128, 96, 0, 0),       # six of eight pieces turned
     (6, 5, 2, 96, 32, 16, 0),       # six pieces to a head: some threads of a block idle
@@ -108,7 +108,7 @@ def test_special_values_stay_in_their_pair(pkv):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("n,hq,hkv,dims,rot,pad", [(37, 16, 8, 128, 128, 2048), (3, 12, 12, 128, 64, 0),
+@pytest.mark.parametrize("n,hq,hkv,dims,rot,pad", [(37, 16, 8, 128, 128, 2056), (3, 12, 12, 128, 64, 0),
                                                   (2600, 4, 1, 128, 128, 0), (5, 2, 1, 80, 10, 3), (4, 0, 2, 128, 128, 0)])
 def test_rope_store_is_rope_then_store(pkv, dtype, interleaved, n, hq, hkv, dims, rot, pad):
     rope, rope_store = _names(pkv, dtype)
