@@ -23,6 +23,7 @@
 // (max, sum, o) in the workspace and a second kernel joins them in order; with weights a third one turns the scores,
 // which the first left in the workspace, into shares. Equal calls give equal bits.
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -77,6 +78,7 @@ constexpr int kPieces = 2 * kWarps;
 constexpr size_t kSmemBytes = kOffPieces + kPieces * sizeof(Piece) + 1024;  // + alignment slack
 constexpr int kMergeWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoCap = 1e30f;  // from here on a cap changes no score that fp32 tells from its neighbours below 1e26
 
 // How a call's heads are cut into streams: parts of up to 8 or 16 query heads of one kv head.
 struct Streams {
@@ -934,8 +936,9 @@ cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStr
   p.max_ctx = a.max_ctx;
   p.st = st;
   p.scale_log2 = a.scale * kLog2e;
-  p.cap_log2 = a.softcap * kLog2e;
-  p.scale_by_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  const float cap = a.softcap < kNoCap ? a.softcap : 0.f;
+  p.cap_log2 = cap * kLog2e;
+  p.scale_by_cap = cap > 0.f ? fminf(a.scale / cap, FLT_MAX) : 0.f;  // not infinity: a score of 0 stays 0
   p.slopes = a.slopes;
   p.window = a.window;
   p.key_starts = a.key_starts;

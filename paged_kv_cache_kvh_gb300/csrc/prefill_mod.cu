@@ -30,6 +30,7 @@
 // such values are rare, so they are found in the result: a row whose sum is not finite is computed once more by its
 // warp from the rows in memory, one key to a lane, with the keys that it does not see left out.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -115,6 +116,7 @@ struct TanhFit<Elem::kF16> {
   static constexpr double kFarC[6] = {0.9999994135741078,    -0.3332904232451419,  0.13281433250603616,
                                       -0.051605653809187996, 0.016743090747062123, -0.0030670504021806768};
 };
+constexpr float kNoCap = 1e30f;     // from here on a cap changes no score that fp32 tells from its neighbours below 1e26
 constexpr float kFixedCap = 52.f;  // bf16: scores capped here and below need no running maximum
 
 struct PrefillModParams {
@@ -1087,8 +1089,9 @@ void fit_tanh(PrefillModParams& p) {
   using Fit = TanhFit<E>;
   const double c = static_cast<double>(p.scale) / p.softcap, s = static_cast<double>(p.scale) * 1.4426950408889634;
   for (int i = 0; i < 6; ++i) {
-    p.near_c[i] = static_cast<float>(s * Fit::kNearC[i] * std::pow(c, 2 * i));
-    p.far_c[i] = static_cast<float>(s * Fit::kFarC[i] * std::pow(c, 2 * i));
+    // (c >= 100: nothing but zeros goes through them, and stays zero)
+    p.near_c[i] = c < 100 || i == 0 ? static_cast<float>(s * Fit::kNearC[i] * std::pow(c, 2 * i)) : 0.f;
+    p.far_c[i] = c < 100 || i == 0 ? static_cast<float>(s * Fit::kFarC[i] * std::pow(c, 2 * i)) : 0.f;
     p.tanh_c[i] = static_cast<float>(Fit::kFarC[i]);
   }
   p.near_top = c < 100 ? static_cast<float>(std::fmin((c > 1e-5 ? Fit::kNearTop : 0.02) / c, 1e18)) : 0.f;
@@ -1124,12 +1127,12 @@ cudaError_t launch_prefill_mod(const PrefillModArgs& a, unsigned int* err, cudaS
   p.paged = paged ? 1 : 0;
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
-  p.softcap = a.softcap;
-  if (a.softcap > 0.f) {
-    p.cap_log2 = a.softcap * kLog2e;
-    p.scale_by_cap = a.scale / a.softcap;
+  p.softcap = a.softcap < kNoCap ? a.softcap : 0.f;
+  if (p.softcap > 0.f) {
+    p.cap_log2 = p.softcap * kLog2e;
+    p.scale_by_cap = fminf(a.scale / p.softcap, FLT_MAX);  // not infinity: a score of 0 stays 0
     elem == Elem::kF16 ? fit_tanh<Elem::kF16>(p) : fit_tanh<Elem::kBF16>(p);
-    p.fixed = elem == Elem::kBF16 && a.softcap <= kFixedCap;
+    p.fixed = elem == Elem::kBF16 && p.softcap <= kFixedCap;
   }
   p.slopes = a.slopes;
   p.window = a.window;

@@ -168,6 +168,18 @@ def test_extreme_scores(pkv):
         _compare(out, q, kc, vc, tables, lens, 1.0, torch.float16, softcap=cap)
 
 
+@pytest.mark.parametrize("cap", [1e-40, 1e-20, 1e-9, 1e-3, 1e12, 1e31, 3e38])
+def test_caps_of_any_size(pkv, cap):
+    """Scores of 0 among them, which stay 0 under any cap."""
+    lens = [300, 64, 40]
+    for dtype in (torch.bfloat16, torch.float16):
+        q, kc, vc, tables, ctx = _case(lens, 4, 2, dtype)
+        q[1] = 0
+        kc[tables[2, 0], :7] = 0
+        out = _decode(pkv, dtype)(q, kc, vc, tables, ctx, 512, D ** -0.5, pkv.decode_mod_workspace(3, 512, 4, 2), softcap=cap)
+        _compare(out, q, kc, vc, tables, lens, D ** -0.5, dtype, softcap=cap)
+
+
 def test_bad_blocks_and_lengths_are_reported(pkv):
     lens = [300, 40]
     q, kc, vc, tables, ctx = _case(lens, 4, 2, torch.bfloat16)

@@ -163,6 +163,16 @@ def test_cap_over_its_whole_range(pkv, sharp, scale, cap):
         c.check(c.run(pkv, scale=scale, softcap=cap), scale=scale, softcap=cap)
 
 
+@pytest.mark.parametrize("cap", [1e-40, 1e-20, 1e-9, 1e12, 1e31, 3e38])
+def test_caps_of_any_size(pkv, cap):
+    """Scores of 0 among them, which stay 0 under any cap."""
+    for dtype in (torch.bfloat16, torch.float16):
+        c = Case([(130, 200), (0, 140)], 4, 2, dtype)
+        c.q[200:] = 0
+        c.q[7] = 0
+        c.check(c.run(pkv, softcap=cap), softcap=cap)
+
+
 def test_matches_pkv_prefill(pkv):
     c = Case([(300, 400), (0, 77)], 16, 8, torch.bfloat16)
     cu = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (c.cu_q, c.cu_k)]

@@ -130,6 +130,30 @@ def test_rope_store_is_rope_then_store(pkv, dtype, interleaved, n, hq, hkv, dims
     assert pkv.pkv_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n", [1300, 2500, 4999, 9000])
+def test_many_tokens_are_as_few(pkv, dtype, interleaved, n):
+    """Two, four and eight tokens to a block, the last one with fewer, against calls with one token to a block."""
+    rope, rope_store = _names(pkv, dtype)
+    q, k, v = (_rows(n, h, 128, dtype, s, 40) for s, h in ((1, 5), (2, 3), (3, 3)))
+    positions = torch.randint(-9, 1 << 20, (n,), generator=torch.Generator().manual_seed(5)).cuda()
+    freqs, _ = pkv.rope_frequencies(96)
+    slots = torch.randperm(n + 300, generator=torch.Generator().manual_seed(6))[:n].int().cuda()
+    slots[3] = -1
+    caches = [torch.full((n + 300, 3, 128), 3.0, dtype=dtype, device="cuda") for _ in range(4)]
+    qo, ko = rope(q, k, positions, freqs, interleaved=interleaved)
+    q2 = rope_store(q, k, v, positions, freqs, *caches[:2], slots, interleaved=interleaved)
+    for a in range(0, n, 700):
+        cut = slice(a, min(n, a + 700))
+        qw, kw = rope(q[cut], k[cut], positions[cut], freqs, interleaved=interleaved)
+        assert torch.equal(qo[cut], qw) and torch.equal(ko[cut], kw) and torch.equal(q2[cut], qw)
+        rope_store(q[cut], k[cut], v[cut], positions[cut], freqs, *caches[2:], slots[cut], interleaved=interleaved)
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    kept = slots >= 0
+    assert torch.equal(caches[0][slots[kept].long()], ko[kept]) and torch.equal(caches[1][slots[kept].long()], v[kept])
+
+
 def test_bad_slots_are_reported_and_skipped(pkv):
     q, k = _rows(3, 2, 128, torch.bfloat16, 1), _rows(3, 1, 128, torch.bfloat16, 2)
     kc = torch.zeros((1, 256, 1, 128), dtype=torch.bfloat16, device="cuda")
