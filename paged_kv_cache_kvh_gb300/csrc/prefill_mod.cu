@@ -661,6 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t neg = f32x2_pack(-base, -base);
         if (kCap) {
           using Fit = TanhFit<E>;
+          if (key0 + kCols > Lk) {  // whatever lies behind the sequence has no say in how its scores are worked out
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) s[j] = j < Lk - key0 ? s[j] : 0.f;
+          }
           const float size = size_all(s);
           if (__all_sync(0xffffffffu, size <= p.near_top)) {
             const Poly2<Fit::kNear> poly(p.near_c);

@@ -128,3 +128,42 @@ def test_prompts_steps_eviction_steps(pkv, dtype, in_place):
         got = weights[_dev(tables[b], torch.long)].transpose(0, 1).flatten(1)[:, :n].double()
         assert bool(((got - want_w[b]).abs() <= want_w[b] * 2.0 ** -15 + 2.0 ** -19).all())
     assert pkv.pkv_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_blocks_far_into_a_large_cache(pkv, dtype):
+    """Blocks whose elements lie beyond 2^32 give what the same rows at the start of a small cache give, bit for bit."""
+    f16 = dtype == torch.float16
+    rope_store = pkv.pkv_rope_store_kvcache_f16 if f16 else pkv.pkv_rope_store_kvcache
+    prefill = pkv.pkv_prefill_varlen_mod_f16 if f16 else pkv.pkv_prefill_varlen_mod
+    decode = pkv.pkv_decode_mod_f16 if f16 else pkv.pkv_decode_mod
+    hq, hkv, n, scale = 16, 8, 700, D ** -0.5
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v = (torch.randn((n, h, D), generator=g, device="cuda").to(dtype) for h in (hq, hkv, hkv))
+    positions = torch.arange(n, device="cuda")
+    freqs, _ = pkv.rope_frequencies(D)
+    results = []
+    for blocks, used in ((8, [3, 0, 7, 5]), (16500, [16499, 2, 16390, 16450])):
+        kc, vc = (torch.empty((blocks, BS, hkv, D), dtype=dtype, device="cuda") for _ in range(2))
+        weights = pkv.attention_weights(blocks, hkv)
+        table = _dev([used[:3]])
+        slots = _dev([used[i // BS] * BS + i % BS for i in range(n)])
+        qt = rope_store(q, k, v, positions, freqs, kc, vc, slots)
+        cu = _dev([0, n])
+        out = prefill(qt, cu, cu, n, n, scale, k_cache=kc, v_cache=vc, block_tables=table, softcap=20.0, window=300)
+        ws = pkv.decode_mod_workspace(1, n, hq, hkv, weights=True)
+        step = decode(qt[-1:], kc, vc, table, _dev([n]), n, scale, ws, softcap=20.0, weights=weights)
+        kept, _ = pkv.pkv_evict_kvcache(kc, vc, weights, table, _dev([n]), n, 200, first=2, recent=30,
+                                        new_block_tables=_dev([used[3:]]))
+        results.append((qt, out, step, kept, kc[used], vc[used][3, :200], weights[used][:3]))
+        kc_kept, vc_kept = kc[used[3], :200], vc[used[3], :200]
+        for h in range(hkv):
+            at = slots[kept[0, h].long()].long()
+            assert torch.equal(kc_kept[:, h], kc.flatten(0, 1)[at, h]) and torch.equal(vc_kept[:, h], vc.flatten(0, 1)[at, h])
+    for name, a, b in zip(("q", "prefill", "decode", "kept"), *results):
+        assert torch.equal(a, b), name
+    a, b = results[0][4], results[1][4]
+    assert torch.equal(a[:2], b[:2]) and torch.equal(a[2, :n - 2 * BS], b[2, :n - 2 * BS])
+    assert torch.equal(a[3, :200], b[3, :200])
+    assert torch.equal(results[0][5], results[1][5]) and torch.equal(results[0][6], results[1][6])
+    assert pkv.pkv_device_error() == 0

@@ -227,6 +227,29 @@ def test_values_behind_the_mask(pkv, paged, hq, hkv):
     assert pkv.pkv_device_error() == 0
 
 
+@pytest.mark.parametrize("mods", list(MODS))
+@pytest.mark.parametrize("seqs", [[(0, 130), (300, 77), (0, 3)], [(2100, 140)]])
+def test_what_lies_behind_a_sequence_changes_no_bit(pkv, seqs, mods):
+    for dtype in (torch.bfloat16, torch.float16):
+        for paged in (False, True):
+            c = Case(seqs, 4, 2, dtype, paged=paged)
+            m = _mods(MODS[mods], c)
+            outs = []
+            for value in (float("nan"), 0.0, 30000.0):
+                if paged:
+                    for b, (cached, new) in enumerate(seqs):
+                        last = int(c.tables[b, (cached + new - 1) // BS])
+                        for cache in (c.kc, c.vc):
+                            cache[last, (cached + new - 1) % BS + 1:] = value
+                outs.append(c.run(pkv, **m)[:c.cu_q[-1]])
+            if not paged:  # the keys of the sequences behind the first one
+                first = outs[0][:c.cu_q[1]].clone()
+                for x in (c.k, c.v):
+                    x[c.cu_k[1]:] *= 1000
+                outs = [first, c.run(pkv, **m)[:c.cu_q[1]]]
+            assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
 def test_nan_keys_and_queries(pkv):
     c = Case([(0, 200)], 4, 2, torch.float16, paged=False)
     c.k[150, 1, 3] = float("nan")
