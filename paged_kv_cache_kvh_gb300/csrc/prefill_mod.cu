@@ -15,13 +15,16 @@
 // groups are two query heads of one kv head at the same rows, or, where a kv head has an odd number of query heads, one
 // head at two neighbouring tiles of rows: either way one K and one V tile serves both.
 //
+// A CTA goes from item to item, taking the next from the launch's CTAs that have not begun (cluster launch control) when
+// the last loads of its item are under way: whoever is done first gets the longest of what is left, and the next item's
+// queries, keys and first products run under the last tile and the end of this one (16 k rows of 100..1024-token prompts
+// with a cap and a window 77 us with a CTA to an item, 69 now; 5000 on 7001 without a cap 311 and 322, see Place).
+//
 // What bounds it: a key tile of both groups takes about 2 us, its products 1.1 of that; the rest is the chain of each
 // group (product, softmax, barrier, product) with two groups to overlap and the softmax's issue slots, 54 % in use as
-// the tensor pipe is. 16 on 8 heads, 5000 on 7001 in the cache: 350 us capped at 50 and 311 without a cap, of 207 at
-// cuBLAS' rate (0.59 and 0.67 of it); 16 k rows of 100..1024-token prompts with a cap and a window: 77 us, 3.5 us fixed
-// per CTA among it. Measured and not kept: 384 threads with registers shared out by role (427 us where 404 was), scores
-// fetched a tile ahead (430: three slots of the ring are too few for it), a CTA going from item to item with the next
-// one's first products under the last one's end (538: the loop over items around the softmax makes the compiler spill).
+// the tensor pipe is. 16 on 8 heads, 5000 on 7001 in the cache: 351 us capped at 50 and 322 without a cap, of 207 at
+// cuBLAS' rate (0.59 and 0.64 of it). Measured and not kept: 384 threads with registers shared out by role (427 us where
+// 404 was), scores fetched a tile ahead (430: three slots of the ring are too few for it).
 //
 // tanh: the softmax is issue-limited, and tanh through exponential and reciprocal would triple its special function
 // work (128 x 128 scores a group: 2 us a tile of 1.6). An odd polynomial on packed pairs costs 4 instructions a pair for
@@ -36,8 +39,9 @@
 //
 // Values of V at keys that a row does not see are multiplied by p = 0; where they are not finite the sum is spoilt
 // (0 * NaN). The rows of V behind the sequence's end, which may hold anything, are zeroed in shared memory. Elsewhere
-// such values are rare, so they are found in the result: a row whose sum is not finite is computed once more by its
-// warp from the rows in memory, one key to a lane, with the keys that it does not see left out.
+// such values are rare, so they are found in the result: a row whose sum is not finite is computed once more by a
+// warp that has nothing else to do, from the rows in memory, one key to a lane, with the keys that it does not see left
+// out.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -94,13 +98,29 @@ constexpr int kBarKvFree = kBarKvFull + kKvSlots;
 constexpr int kBarSFull = kBarKvFree + kKvSlots;  // +group
 constexpr int kBarPReady = kBarSFull + 2;         // +group
 constexpr int kBarOFinal = kBarPReady + 2;
-constexpr int kBarVTail = kBarOFinal + 1;
-constexpr int kBarDrain = kBarVTail + 1;
-constexpr int kBarStaged = kBarDrain + 1;         // the softmax warps have staged their O rows
-constexpr int kNumBars = kBarStaged + 1;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag, smallest lo and largest hi of 32 rows,
-constexpr int kMiscBytes = 8 + 16 * 4 + 8 * 4;    // rows to be computed once more
-constexpr int kOffMax = kOffMisc + kMiscBytes;    // [group][half][row] bf16: the halves' largest scores
+constexpr int kBarVTail = kBarOFinal + 1;         // +item % 2: zeros are behind the last value
+constexpr int kBarDrain = kBarVTail + 2;
+constexpr int kBarDone = kBarDrain + 1;           // the softmax warps have read tensor memory for the last time
+constexpr int kBarItemFull = kBarDone + 1;        // +item % 2: it is described
+constexpr int kBarItemFree = kBarItemFull + 2;    // +item % 2: everyone has read its description
+constexpr int kBarQFree = kBarItemFree + 2;       // an item's last product with Q is complete
+constexpr int kBarOFree = kBarQFree + 1;          // +group: its O has been read
+constexpr int kBarNext = kBarOFree + 2;           // the next item's number has arrived
+constexpr int kBarRows = kBarNext + 1;            // an item's rows have been written
+constexpr int kNumBars = kBarRows + 1;
+constexpr int kOffNext = kOffBar + (kNumBars * 8 + 15) / 16 * 16;  // where the hardware writes it, 16 bytes
+constexpr int kOffItems = kOffNext + 16;
+
+// What the roles of a CTA have to know of an item.
+struct Item {
+  int32_t b, head0, cq0, ck0, Lq, Lk;
+  int32_t r0;              // first query row
+  int32_t tile0, n_tiles;  // key tiles; n_tiles < 0: no more items
+};
+constexpr int kOffAgain = kOffItems + 2 * sizeof(Item);  // [item % 2][32 rows][half] rows to be computed again
+constexpr int kOffSeen = (kOffAgain + 2 * kSoftmaxWarps * 4 + 15) / 16 * 16;  // [warp] the keys that any and that all of its rows see
+constexpr int kOffMisc = kOffSeen + kSoftmaxWarps * 16;  // tmem address, abort flag
+constexpr int kOffMax = kOffMisc + 8;                   // [group][half][row] bf16: the halves' largest scores
 constexpr size_t kSmemBytes = kOffMax + 4 * kBM * 2 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
@@ -344,7 +364,31 @@ __device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, f
 // The launch of split items may begin while the one before it still runs, and must not be over before that is.
 __device__ __forceinline__ void wait_for_others() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// kSplit: the CTAs of a cluster have parts of one item's keys.
+// The next item, from the CTAs of the launch that have not begun yet: asks the hardware to cancel one of them and to write
+// its place to `addr` (16 bytes, counted by the barrier). After an answer that there are none it must not be asked again.
+__device__ __forceinline__ void ask_next(uint32_t addr, uint32_t bar) {
+  fence_proxy_async_smem();  // the last answer has been read
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(addr),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool next_cta(uint32_t addr, int& cta) {
+  uint32_t there, x = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 answer;\n\tld.shared.b128 answer, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, answer;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, answer;\n\t}"
+      : "=r"(there), "=r"(x)
+      : "r"(addr)
+      : "memory");
+  cta = static_cast<int>(x);
+  return there != 0;
+}
+
+// A CTA goes from item to item, its roles one behind another: while the softmax warps finish an item, the next one's
+// queries, keys and first products are under way. kSplit: the CTAs of a cluster have parts of one item's keys, and only
+// that item.
 template <Elem E, bool kCap, bool kBias, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -357,123 +401,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (sbase - raw_addr);
   const uint32_t bar0 = sbase + kOffBar;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  Item* items = reinterpret_cast<Item*>(smem + kOffItems);
+  volatile uint32_t* s_again = reinterpret_cast<volatile uint32_t*>(smem + kOffAgain);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* s_lo = reinterpret_cast<int*>(smem + kOffMisc + 8);               // [8] smallest lo of 32 rows
-  int* s_hi = s_lo + 8;                                                  // [8] largest hi
-  uint32_t* s_again = reinterpret_cast<uint32_t*>(s_hi + 8);             // [2][4] rows to be computed once more
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-
-  // ---- work item: (query tile, sequence, heads), the last query tiles (the longest key ranges) first ----
   if (!kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // items split over clusters fill the end
   const int parts = kSplit ? cluster_parts() : 1, part = kSplit ? cluster_part() : 0;
-  const int item = p.first + static_cast<int>(blockIdx.x) / parts;
-  const int per_tile = p.num_seqs * p.units;
-  const int qt = p.q_tiles - 1 - item / per_tile;
-  const int b = (item % per_tile) / p.units, unit = item % p.units;
-  const int head0 = p.neighbours ? unit : 2 * unit;
-  const int hk = head0 / p.group;
 
-  const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1];
-  const int ck0 = p.cu_k[b], ck1 = p.cu_k[b + 1];
-  const int Lq = cq1 - cq0, Lk = ck1 - ck0;
-  const bool bad = Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || cq0 < 0 || cq1 > p.total_q ||
-                   (p.paged ? Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize : (ck0 < 0 || ck1 > p.total_k));
-  if (bad) {
-    if (threadIdx.x == 0 && qt == 0 && unit == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
-    if (kSplit) wait_for_others();
-    return;
-  }
-  const int r0 = qt * (p.neighbours ? 2 * kBM : kBM);
-  if (r0 >= Lq) {
-    if (kSplit) wait_for_others();
-    return;
-  }
-
-  // The softmax thread of a row: its position and the keys it sees. Rows behind the last one take its place.
-  const int g = (warp - 4) >> 3, half = (warp >> 2) & 1 ? 0 : 1;  // warps 4..7 and 12..15 take the first keys of a tile
-  const int rows32 = 4 * g + (warp & 3);                           // the warp's 32 rows, of 8 times 32
-  const int row = (warp & 3) * 32 + lane;  // within the group's tile == TMEM lane
-  const int g_row0 = r0 + (p.neighbours && g > 0 ? kBM : 0);
-  auto seen_from = [&](int r, int& pos_, int& lo_, int& hi_) {  // r: row of the sequence
-    r = min(r, Lq - 1);
-    pos_ = Lk - Lq + r;
-    lo_ = p.window > 0 ? max(0, pos_ - p.window + 1) : 0;
-    if (p.key_starts) lo_ = max(lo_, p.key_starts[cq0 + r]);
-    hi_ = min(Lk, max(pos_ + 1, p.prefix_lens ? p.prefix_lens[b] : 0));
-  };
-  int pos = 0, lo = 0, hi = 0, any_lo = 0, any_hi = 0;  // seen by the row; by any of the warp's rows
-  if (warp >= 4) {
-    seen_from(g_row0 + row, pos, lo, hi);
-    // a row without keys widens nothing
-    any_lo = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX);
-    any_hi = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
-    if (lane == 0 && half == 0) {
-      s_lo[rows32] = any_lo;
-      s_hi[rows32] = any_hi;
-      s_again[rows32] = 0;
-    }
-  }
-
-  // ---- the key tiles ----
-  int tile0 = 0, n_tiles = 0;  // a split item's part may have none
-  auto set_tiles = [&](int first_key, int end_key) {
-    // rows that see nothing at all: one tile, all masked
-    const int all_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - first_key / kBN : 1;
-    tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
-    n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;
-  };
-  // Tile n of this CTA's. A bias favours the nearest keys: from the last tile to the first, the reference is found in the
-  // first one and stays (5000 on 7001: 404 us from the first on, 331 from the last; without a bias 308 and 326).
-  constexpr bool kBack = kBias;
-  auto first_key_of = [&](int n) { return (tile0 + (kBack ? n_tiles - 1 - n : n)) * kBN; };
-  auto k_row = [&](int n) -> int {  // where tile n begins
-    const int key0 = first_key_of(n);
-    if (!p.paged) return ck0 + key0;
-    int blk = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + key0 / kBlockSize];
-    if (blk < 0 || blk >= p.num_blocks) {
-      flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
-      blk = 0;
-    }
-    return blk * kBlockSize + key0 % kBlockSize;
-  };
-  // ring item i: K of tile i / 2 (even i) or V (odd i), into slot i % kKvSlots
-  auto load_kv = [&](int i) {
-    const int slot = i % kKvSlots;
-    const CUtensorMap* tm = (i & 1) ? &tm_v : &tm_k;
-    const int at = k_row(i >> 1);
-    const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
-    mbar_arrive_expect_tx(bar(kBarKvFull + slot), kTileBytes);
-    tma_load_3d(dst, tm, 0, hk, at, bar(kBarKvFull + slot));
-    tma_load_3d(dst + kHalfBytes, tm, 64, hk, at, bar(kBarKvFull + slot));
-  };
-  // Without first keys of single rows every row sees at least itself, and the range follows from the first and last row.
-  if (!p.key_starts) {
-    const int pos0 = Lk - Lq + r0, last = Lk - Lq + min(r0 + (p.neighbours ? 2 * kBM : kBM), Lq);
-    set_tiles(p.window > 0 ? max(0, pos0 - p.window + 1) : 0, min(Lk, max(last, p.prefix_lens ? p.prefix_lens[b] : 0)));
-  }
-
-  // Thread 0 is the TMA warp's issuing lane: the queries and, where their place is known, the first keys and values are on
-  // their way before anything else is set up.
-  int issued = 0;  // ring items (thread 0)
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i == kBarStaged ? kSoftmaxWarps : (i == kBarPReady || i == kBarPReady + 1 ? 8 : 1));
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i == kBarPReady || i == kBarPReady + 1 || i == kBarOFree || i == kBarOFree + 1) count = kSoftmaxWarps / 2;
+      if (i == kBarDone || i == kBarRows) count = kSoftmaxWarps;
+      if (i == kBarItemFree || i == kBarItemFree + 1) count = kSoftmaxWarps + 2;
+      mbar_init(bar(i), count);
+    }
     *s_abort = 0;
     mbar_fence_init();
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
-    mbar_arrive_expect_tx(bar(kBarQ), 2 * kTileBytes);
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t dst = sbase + kOffQ + i * kTileBytes;
-      const int head = head0 + (p.neighbours ? 0 : i), first = cq0 + r0 + (p.neighbours ? i * kBM : 0);
-      tma_load_3d(dst, &tm_q, 0, head, first, bar(kBarQ));
-      tma_load_3d(dst + kHalfBytes, &tm_q, 64, head, first, bar(kBarQ));
-    }
-    for (; issued < kKvSlots && issued < 2 * n_tiles; ++issued) load_kv(issued);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), 512);
@@ -485,472 +435,691 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (p.key_starts) {
-    int first_key = INT32_MAX, end_key = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      first_key = min(first_key, s_lo[i]);
-      end_key = max(end_key, s_hi[i]);
-    }
-    set_tiles(first_key, end_key);
-  }
-  const int tail_keys = Lk - (tile0 + n_tiles - 1) * kBN;  // keys that the last tile has
-  const bool v_tail = tail_keys < kBN && n_tiles > 0;
-  const int tail_item = kBack ? 1 : 2 * n_tiles - 1;       // the ring item of its values
+  // Row r of an item's sequence: its position and the keys it sees. Rows behind the last one take its place.
+  auto seen_from = [&](const Item& it, int r, int& pos_, int& lo_, int& hi_) {
+    r = min(r, it.Lq - 1);
+    pos_ = it.Lk - it.Lq + r;
+    lo_ = p.window > 0 ? max(0, pos_ - p.window + 1) : 0;
+    if (p.key_starts) lo_ = max(lo_, p.key_starts[it.cq0 + r]);
+    hi_ = min(it.Lk, max(pos_ + 1, p.prefix_lens ? p.prefix_lens[it.b] : 0));
+  };
+  // Tile n of an item's: a bias favours the nearest keys: from the last tile to the first, the reference is found in the
+  // first one and stays (5000 on 7001: 404 us from the first on, 331 from the last; without a bias 308 and 326).
+  constexpr bool kBack = kBias;
+  auto first_key_of = [&](const Item& it, int n) { return (it.tile0 + (kBack ? it.n_tiles - 1 - n : n)) * kBN; };
+  // keys that the last of the tiles has, and the item's load of its values (the first load is 0)
+  auto tail_of = [&](const Item& it) { return it.Lk - (it.tile0 + it.n_tiles - 1) * kBN; };
+  auto tail_load = [&](const Item& it) { return kBack ? 1 : 2 * it.n_tiles - 1; };
 
+  bool had_item = false;  // (kSplit, warps 0 to 3)
   if (warp == 0) {
-    // =========================== TMA producer ===========================
-    auto issue_up_to = [&](int end) {
-      if (lane == 0) {
-        for (int i = issued; i < end; ++i) {
-          const int slot = i % kKvSlots;
-          if (i >= kKvSlots && !wait_or_abort(bar(kBarKvFree + slot), ((i / kKvSlots) - 1) & 1, s_abort, p.err))
-            break;
-          load_kv(i);
-          ++issued;
+    // =========================== items and their loads ===========================
+    // Loads of all items are counted through: load x goes into slot x % kKvSlots.
+    int ring = 0, k = 0;
+    bool ok = true, waiting = false;  // for the next item's number, after an abort
+    uint32_t next_parity = 0;
+    int cta = static_cast<int>(blockIdx.x);
+    const int per_tile = p.num_seqs * p.units;
+    while (ok) {
+      // ---- the last query tiles (the longest key ranges) first ----
+      const int item = p.first + cta / parts;
+      const int qt = p.q_tiles - 1 - item / per_tile, unit = item % p.units;
+      Item it;
+      it.b = (item % per_tile) / p.units;
+      it.head0 = p.neighbours ? unit : 2 * unit;
+      it.r0 = qt * (p.neighbours ? 2 * kBM : kBM);
+      it.cq0 = p.cu_q[it.b];
+      it.ck0 = p.cu_k[it.b];
+      const int cq1 = p.cu_q[it.b + 1], ck1 = p.cu_k[it.b + 1];
+      it.Lq = cq1 - it.cq0;
+      it.Lk = ck1 - it.ck0;
+      const bool bad = it.Lq < 0 || it.Lk < it.Lq || it.Lq > p.max_seqlen_q || it.Lk > p.max_seqlen_k || it.cq0 < 0 ||
+                       cq1 > p.total_q || (p.paged ? it.Lk > static_cast<int64_t>(p.bt_stride) * kBlockSize
+                                                   : (it.ck0 < 0 || ck1 > p.total_k));
+      if (bad && lane == 0 && qt == 0 && unit == 0) flag_error(p.err, PKV_DEVERR_BAD_SEQLEN);
+      if (!bad && it.r0 < it.Lq) {
+        // the keys that any of the rows sees; a row that sees none widens nothing
+        const int rows = p.neighbours ? 2 * kBM : kBM;
+        int first_key = INT32_MAX, end_key = 0;
+        for (int r = lane; r < (p.key_starts ? rows : 2); r += 32) {
+          int pos, lo, hi;  // without first keys of single rows the first and the last row tell
+          seen_from(it, p.key_starts ? it.r0 + r : (r == 0 ? it.r0 : it.r0 + rows - 1), pos, lo, hi);
+          if (lo < hi) {
+            first_key = min(first_key, lo);
+            end_key = max(end_key, hi);
+          }
         }
-      }
-      issued = __shfl_sync(0xffffffffu, issued, 0);
-    };
-    issue_up_to(kBack ? min(kKvSlots, 2 * n_tiles) : 2 * n_tiles);
-    if (v_tail && issued > tail_item) {
-      // Zero the rows of the sequence's last V tile that lie past its end.
-      const int slot = tail_item % kKvSlots;
-      const bool ok = wait_or_abort(bar(kBarKvFull + slot), (tail_item / kKvSlots) & 1, s_abort, p.err);
-      if (ok) {
-        const uint32_t base = sbase + kOffKV + slot * kTileBytes;
-        // rows tail_keys..127 of both 64-dim halves: 128-byte rows, swizzle
-        // only permutes 16-byte chunks within a row.
-        const int nz = (kBN - tail_keys) * 2 * 8;  // 16-byte chunks
-        for (int c = lane; c < nz; c += 32) {
-          const int at = tail_keys + (c >> 4);
-          const int half_ = (c >> 3) & 1;
-          const int chunk = c & 7;
-          sts128(base + half_ * kHalfBytes + at * 128 + chunk * 16, 0u, 0u, 0u, 0u);
+        first_key = __reduce_min_sync(0xffffffffu, first_key);
+        end_key = __reduce_max_sync(0xffffffffu, end_key);
+        // rows that see nothing at all: one tile, all masked
+        const int all_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - first_key / kBN : 1;
+        it.tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
+        it.n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;  // 0 at times
+        if (k >= 2) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) - 1) & 1, s_abort, p.err));
+        if (!ok) break;
+        if (lane == 0) {
+          items[k & 1] = it;
+          mbar_arrive(bar(kBarItemFull + (k & 1)));
         }
-        fence_proxy_async_smem();
+        had_item = true;
+        if (k >= 1) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarQFree), (k - 1) & 1, s_abort, p.err));
+        if (!ok) break;
+        const int hk = it.head0 / p.group;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kBarQ), 2 * kTileBytes);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t dst = sbase + kOffQ + i * kTileBytes;
+            const int head = it.head0 + (p.neighbours ? 0 : i), first = it.cq0 + it.r0 + (p.neighbours ? i * kBM : 0);
+            tma_load_3d(dst, &tm_q, 0, head, first, bar(kBarQ));
+            tma_load_3d(dst + kHalfBytes, &tm_q, 64, head, first, bar(kBarQ));
+          }
+        }
+        int issued = 0;  // of the item's loads: K of tile i / 2 (even i) or V (odd i)
+        auto issue_up_to = [&](int end) {
+          if (lane == 0) {
+            for (int i = issued; i < end; ++i) {
+              const int x = ring + i, slot = x % kKvSlots;
+              if (x >= kKvSlots && !wait_or_abort(bar(kBarKvFree + slot), ((x / kKvSlots) - 1) & 1, s_abort, p.err)) break;
+              int at = first_key_of(it, i >> 1);
+              if (p.paged) {
+                int blk = p.block_tables[static_cast<int64_t>(it.b) * p.bt_stride + at / kBlockSize];
+                if (blk < 0 || blk >= p.num_blocks) {
+                  flag_error(p.err, PKV_DEVERR_BAD_BLOCK);
+                  blk = 0;
+                }
+                at = blk * kBlockSize + at % kBlockSize;
+              } else {
+                at += it.ck0;
+              }
+              const CUtensorMap* tm = (i & 1) ? &tm_v : &tm_k;
+              const uint32_t dst = sbase + kOffKV + slot * kTileBytes;
+              mbar_arrive_expect_tx(bar(kBarKvFull + slot), kTileBytes);
+              tma_load_3d(dst, tm, 0, hk, at, bar(kBarKvFull + slot));
+              tma_load_3d(dst + kHalfBytes, tm, 64, hk, at, bar(kBarKvFull + slot));
+              ++issued;
+            }
+          }
+          issued = __shfl_sync(0xffffffffu, issued, 0);
+        };
+        const int tail_keys = tail_of(it), tail = tail_load(it);
+        issue_up_to(kBack ? min(kKvSlots, 2 * it.n_tiles) : 2 * it.n_tiles);
+        if (tail_keys < kBN && it.n_tiles > 0 && issued > tail) {
+          // Zero the rows of the sequence's last V tile that lie past its end.
+          const int slot = (ring + tail) % kKvSlots;
+          if (wait_or_abort(bar(kBarKvFull + slot), ((ring + tail) / kKvSlots) & 1, s_abort, p.err)) {
+            const uint32_t base = sbase + kOffKV + slot * kTileBytes;
+            // rows tail_keys..127 of both 64-dim halves: 128-byte rows, swizzle
+            // only permutes 16-byte chunks within a row.
+            const int nz = (kBN - tail_keys) * 2 * 8;  // 16-byte chunks
+            for (int c = lane; c < nz; c += 32) {
+              const int at = tail_keys + (c >> 4), half = (c >> 3) & 1, chunk = c & 7;
+              sts128(base + half * kHalfBytes + at * 128 + chunk * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(bar(kBarVTail + (k & 1)));  // of every item
+        issue_up_to(2 * it.n_tiles);
+        ring += issued;
+        ++k;
+        ok = issued == 2 * it.n_tiles;
       }
+      if (kSplit || !ok) break;
+      // asked for when this item's last loads are under way, not before: whoever is done first has the longest of the rest
+      if (lane == 0) ask_next(sbase + kOffNext, bar(kBarNext));
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarNext), next_parity, s_abort, p.err))) {
+        waiting = true;
+        break;
+      }
+      next_parity ^= 1;
+      const bool there = next_cta(sbase + kOffNext, cta);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarVTail));
+      if (!there) break;
     }
-    issue_up_to(2 * n_tiles);
+    // no more items
+    if (ok && k >= 2) ok = wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) - 1) & 1, s_abort, p.err);
+    ok = __all_sync(0xffffffffu, ok);
     if (lane == 0) {
+      if (ok) {
+        items[k & 1].n_tiles = -1;
+        mbar_arrive(bar(kBarItemFull + (k & 1)));
+      }
       // Never leave a copy in flight into this CTA's shared memory.
-      mbar_wait(bar(kBarQ), 0, p.err);
-      for (int i = max(0, issued - kKvSlots); i < issued; ++i)
-        mbar_wait(bar(kBarKvFull + i % kKvSlots), (i / kKvSlots) & 1, p.err);
+      if (k > 0) mbar_wait(bar(kBarQ), (k - 1) & 1, p.err);
+      for (int x = max(0, ring - kKvSlots); x < ring; ++x)
+        mbar_wait(bar(kBarKvFull + x % kKvSlots), (x / kKvSlots) & 1, p.err);
+      if (waiting) mbar_wait(bar(kBarNext), next_parity, p.err);
     }
   } else if (warp == 1) {
     // =========================== MMA issuer ===========================
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_f16kind_f32(kBM, kBN, false, false, Ops::kMmaFormat);
       constexpr uint32_t idesc_pv = idesc_f16kind_f32(kBM, kHeadDim, false, true, Ops::kMmaFormat);
-      bool ok = wait_or_abort(bar(kBarQ), 0, s_abort, p.err);
-      auto slot_of = [](int i) { return i % kKvSlots; };
-      auto par_of = [](int i) { return static_cast<uint32_t>((i / kKvSlots) & 1); };
+      auto slot_of = [](int x) { return x % kKvSlots; };
+      auto par_of = [](int x) { return static_cast<uint32_t>((x / kKvSlots) & 1); };
       // Descriptor low halves: each product below costs two 32-bit adds and
       // the tcgen05.mma (this one thread issues every product of the CTA).
       const uint32_t lo_kmaj = desc_lo(sbase, 16), lo_v = desc_lo(sbase, kHalfBytes);
-      auto issue_s = [&](int i, int n) {
+      auto issue_s = [&](int i, int slot) {
         const uint32_t qa = lo_kmaj + ((kOffQ + i * kTileBytes) >> 4);
-        const uint32_t kbb = lo_kmaj + (kOffKV >> 4) + slot_of(2 * n) * (kTileBytes >> 4);
+        const uint32_t kbb = lo_kmaj + (kOffKV >> 4) + slot * (kTileBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kHeadDim / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
           mma_f16kind_lo(tmem + i * 128, qa + off, kbb + off, idesc_s, ks > 0 ? 1u : 0u);
         }
+        mma_commit(bar(kBarSFull + i));
       };
-      auto issue_pv = [&](int i, int n) {
+      auto issue_pv = [&](int i, int slot, bool first) {
         const uint32_t pa = lo_kmaj + ((kOffP + i * kTileBytes) >> 4);
-        const uint32_t vbb = lo_v + (kOffKV >> 4) + slot_of(2 * n + 1) * (kTileBytes >> 4);
+        const uint32_t vbb = lo_v + (kOffKV >> 4) + slot * (kTileBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks) {
           const uint32_t aoff = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
           mma_f16kind_lo(tmem + 256 + i * 128, pa + aoff, vbb + ((ks * 16 * 128) >> 4), idesc_pv,
-                         (n > 0 || ks > 0) ? 1u : 0u);
+                         (!first || ks > 0) ? 1u : 0u);
         }
       };
-      const bool any = !kSplit || n_tiles > 0;
-      if (ok && any) ok = wait_or_abort(bar(kBarKvFull + slot_of(0)), par_of(0), s_abort, p.err);
-      if (ok && any) {
-        tc_fence_after();
-        issue_s(0, 0);
-        mma_commit(bar(kBarSFull + 0));
-        issue_s(1, 0);
-        mma_commit(bar(kBarSFull + 1));
-        mma_commit(bar(kBarKvFree + slot_of(0)));
-      }
-      for (int n = 0; ok && n < n_tiles; ++n) {
-        const int iv = 2 * n + 1;
-        if (iv == tail_item && v_tail)
-          ok = wait_or_abort(bar(kBarVTail), 0, s_abort, p.err);
-        else
-          ok = wait_or_abort(bar(kBarKvFull + slot_of(iv)), par_of(iv), s_abort, p.err);
-        if (!ok) break;
-        if (!(ok = wait_or_abort(bar(kBarPReady + 0), n & 1, s_abort, p.err))) break;
-        tc_fence_after();
-        issue_pv(0, n);
-        const bool more = n + 1 < n_tiles;
-        if (more) {
-          if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(2 * n + 2)), par_of(2 * n + 2), s_abort, p.err)))
-            break;
+      int ring = 0, t = 0;  // loads and tiles of the items before
+      bool ok = true;
+      for (int k = 0;; ++k) {
+        if (!(ok = wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
+        const Item it = items[k & 1];
+        if (it.n_tiles < 0) break;
+        had_item = true;
+        mbar_arrive(bar(kBarItemFree + (k & 1)));
+        if (!(ok = wait_or_abort(bar(kBarQ), k & 1, s_abort, p.err))) break;
+        const bool v_tail = tail_of(it) < kBN && it.n_tiles > 0;
+        if (it.n_tiles > 0) {
+          if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(ring)), par_of(ring), s_abort, p.err))) break;
           tc_fence_after();
-          issue_s(0, n + 1);
-          mma_commit(bar(kBarSFull + 0));
+          issue_s(0, slot_of(ring));
+          issue_s(1, slot_of(ring));
+          mma_commit(bar(kBarKvFree + slot_of(ring)));
+          if (it.n_tiles == 1) mma_commit(bar(kBarQFree));
         }
-        if (!(ok = wait_or_abort(bar(kBarPReady + 1), n & 1, s_abort, p.err))) break;
-        tc_fence_after();
-        issue_pv(1, n);
-        mma_commit(bar(kBarKvFree + slot_of(iv)));
-        if (more) {
-          issue_s(1, n + 1);
-          mma_commit(bar(kBarSFull + 1));
-          mma_commit(bar(kBarKvFree + slot_of(2 * n + 2)));
+        for (int n = 0; n < it.n_tiles; ++n) {
+          const int xv = ring + 2 * n + 1, xk = xv + 1;
+          if (v_tail && 2 * n + 1 == tail_load(it))
+            ok = wait_or_abort(bar(kBarVTail + (k & 1)), (k >> 1) & 1, s_abort, p.err);
+          else
+            ok = wait_or_abort(bar(kBarKvFull + slot_of(xv)), par_of(xv), s_abort, p.err);
+          if (!ok) break;
+          const bool more = n + 1 < it.n_tiles;
+          for (int i = 0; ok && i < 2; ++i) {
+            if (!(ok = wait_or_abort(bar(kBarPReady + i), (t + n) & 1, s_abort, p.err))) break;
+            if (n == 0 && k > 0 && !(ok = wait_or_abort(bar(kBarOFree + i), (k - 1) & 1, s_abort, p.err))) break;
+            tc_fence_after();
+            issue_pv(i, slot_of(xv), n == 0);
+            if (i == 1) mma_commit(bar(kBarKvFree + slot_of(xv)));
+            if (!more) continue;
+            if (i == 0) {
+              if (!(ok = wait_or_abort(bar(kBarKvFull + slot_of(xk)), par_of(xk), s_abort, p.err))) break;
+              tc_fence_after();
+            }
+            issue_s(i, slot_of(xk));
+            if (i == 1) {
+              mma_commit(bar(kBarKvFree + slot_of(xk)));
+              if (n + 2 == it.n_tiles) mma_commit(bar(kBarQFree));
+            }
+          }
+          if (!ok) break;
         }
+        mma_commit(bar(kBarOFinal));
+        if (!ok) break;
+        ring += 2 * it.n_tiles;
+        t += it.n_tiles;
       }
-      mma_commit(bar(kBarOFinal));
       if (!ok) {
         // make sure no product is still writing TMEM before it is released
         mma_commit(bar(kBarDrain));
         mbar_wait(bar(kBarDrain), 0, p.err);
       }
     }
+    had_item = __shfl_sync(0xffffffffu, had_item ? 1 : 0, 0) != 0;
+  } else if (kSplit && warp < 4) {
+    had_item = __all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull), 0, s_abort, p.err)) && items[0].n_tiles >= 0;
+  } else if (warp == 2) {
+    // =========================== rows that are computed again ===========================
+    for (int k = 0;; ++k) {
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
+      const Item it = items[k & 1];
+      if (it.n_tiles < 0) break;
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarRows), k & 1, s_abort, p.err))) break;
+      for (int i = 0; i < 8; ++i) {  // of 32 rows
+        const volatile uint32_t* masks = s_again + (k & 1) * kSoftmaxWarps + (i >> 2) * 8 + (i & 3);  // of the two halves
+        const int first = it.r0 + (i & 3) * 32 + (p.neighbours && i >= 4 ? kBM : 0);
+        for (uint32_t again = masks[0] | masks[4]; again; again &= again - 1) {
+          const int r = first + __ffs(again) - 1;
+          int pos, lo, hi;
+          seen_from(it, r, pos, lo, hi);
+          row_again<E>(p, it.b, it.ck0, static_cast<int64_t>(it.cq0) + r, it.head0 + (p.neighbours ? 0 : i >> 2), pos, lo, hi,
+                       lane);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemFree + (k & 1)));
+    }
   } else if (warp >= 4) {
     // =========================== softmax groups ===========================
-    const int head = head0 + (p.neighbours ? 0 : g);
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + g * 128 + half * kCols;
-    const uint32_t tO = tmem + lane_base + 256 + g * 128 + half * kCols;
-    const uint32_t prow = sbase + kOffP + g * kTileBytes + half * kHalfBytes + row * 128;
-    const int swz = row & 7;
+    // Where a thread works follows from its number u among the softmax threads: 256 to a group, of these 128 to a half of
+    // a tile's keys, of these 32 to a warp. It is taken apart anew in each part of the item: kept over the loop over the
+    // tiles it would cost the registers that the scores need (chunk of 5000 on 7001 with a bias 405 us kept, 338 anew).
+    // P, the largest scores and the ranges lie in its order.
+    struct Place {
+      int u;
+      __device__ int lane() const { return u & 31; }
+      __device__ int g() const { return u >> 8; }
+      __device__ int half() const { return (u >> 7) & 1; }
+      __device__ int warp() const { return u >> 5; }
+      __device__ int quarter() const { return (u >> 5) & 3; }
+      __device__ int row() const { return u & 127; }                // within the group's tile == TMEM lane
+      __device__ int barrier() const { return ((u >> 5) & 11) | 4; }  // of the two warps of 32 rows
+    };
+    auto place = [&]() {
+      int t;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+      return Place{t - 128};
+    };
+    auto tmem_at = [&](const Place& w, int first) {
+      return tmem + (static_cast<uint32_t>(w.u & 96) << 16) + first + ((w.u & 384) >> 1);
+    };
+    auto seen_at = [&](const Place& w) { return sbase + kOffSeen + w.warp() * 16; };
+    auto p_row = [&](const Place& w) { return sbase + kOffP + w.u * 128; };
+    auto max_at = [&](int u) { return sbase + kOffMax + u * 2; };
     const float sl2 = p.scale_log2;
-    const float slope = kBias ? p.slopes[head] * kLog2e : 0.f;
-    const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);  // seen by all rows
-    const int min_pos = __reduce_min_sync(0xffffffffu, pos);
-    __nv_bfloat16* s_max = reinterpret_cast<__nv_bfloat16*>(smem + kOffMax) + 2 * g * kBM + row;  // [half][row]
-    // Named barrier of the two warps. Both come to it once per tile and once at the end, whatever happens, so it needs no
-    // time limit.
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + rows32) : "memory"); };
+    // Named barrier of the two warps of 32 rows. Both come to it equally often whatever happens, so it needs no time
+    // limit: they agree on whether to go on before every item, and then come to it once per tile and twice at the end.
+    auto pair_sync = [](const Place& w) { asm volatile("bar.sync %0, 64;" ::"r"(w.barrier()) : "memory"); };
+    auto pair_agree = [](const Place& w, bool yes) {
+      uint32_t all;
+      asm volatile(
+          "{\n\t.reg .pred q, r;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.and.pred r, %2, 64, q;\n\tselp.u32 %0, 1, 0, r;\n\t}"
+          : "=r"(all)
+          : "r"(yes ? 1u : 0u), "r"(w.barrier())
+          : "memory");
+      return all != 0;
+    };
     const bool by_maximum = !kCap || kBias || !p.fixed;
-    float m = -INFINITY;  // the row's reference, log2 units; within 8 of its running maximum from below, or fixed at 0
-    float l = 0.f;        // of this thread's keys
+    uint32_t parity = 0;  // of the scores' barrier
     bool ok = true;
-    for (int n = 0; n < n_tiles; ++n) {
-      // every lane waits (each needs the acquire); the warp then agrees, so
-      // the warp-collective tensor-memory loads below run on all 32 lanes
-      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarSFull + g), n & 1, s_abort, p.err));
-      if (!ok) {  // the other warp of these rows may still come to the pair's barrier
-        if (by_maximum) pair_sync();
-        continue;
-      }
-      tc_fence_after();
-      const int key0 = first_key_of(n) + half * kCols;
-      const bool none = key0 + kCols <= any_lo || key0 >= any_hi;  // no row sees any of these keys
-      float s[kCols], mx = -INFINITY;
-      const float base = m == -INFINITY ? 0.f : m;
-      if (!none) {
-        {
-          uint32_t x0[32], x1[32];
-          tmem_ld32(tS + 0, x0);
-          tmem_ld32(tS + 32, x1);
-          tmem_wait_ld();
-          tmem_reg_fence(x0);
-          tmem_reg_fence(x1);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            s[j] = __uint_as_float(x0[j]);
-            s[32 + j] = __uint_as_float(x1[j]);
-          }
-        }
-        auto each = [&](auto arg) {
-#pragma unroll
-          for (int j = 0; j < kCols; j += 2) f32x2_unpack(arg(j, f32x2_pack(s[j], s[j + 1])), s[j], s[j + 1]);
-        };
-        // ---- s = z - base, base the row's reference so far (0 as long as it has seen no key) ----
-        const uint64_t neg = f32x2_pack(-base, -base);
-        if (kCap) {
-          using Fit = TanhFit<E>;
-          if (key0 + kCols > Lk) {  // whatever lies behind the sequence has no say in how its scores are worked out
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) s[j] = j < Lk - key0 ? s[j] : 0.f;
-          }
-          const float size = size_all(s);
-          if (__all_sync(0xffffffffu, size <= p.near_top)) {
-            const Poly2<Fit::kNear> poly(p.near_c);
-            each([&](int, uint64_t x) { return poly(x, neg); });
-          } else if (__all_sync(0xffffffffu, size <= p.far_top)) {
-            const Poly2<Fit::kFar> poly(p.far_c);
-            each([&](int, uint64_t x) { return poly(x, neg); });
-          } else {
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) s[j] = capped<Fit::kFar>(s[j], p) - base;
-          }
-        }
-        if (kBias) {
-          const float less = kCap ? 0.f : base;
-          if (key0 + kCols - 1 <= min_pos) {  // all keys at or before all rows: - slope (pos - t) grows by slope a key
-            const float first = -slope * static_cast<float>(pos - key0) - less;
-            const uint64_t sl2x2 = f32x2_pack(sl2, sl2), step = f32x2_pack(8.f * slope, 8.f * slope);
-            uint64_t at[4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) at[a] = f32x2_pack(fmaf(slope, 2.f * a, first), fmaf(slope, 2.f * a + 1.f, first));
-            each([&](int j, uint64_t x) {
-              uint64_t& t = at[(j >> 1) & 3];
-              const uint64_t y = kCap ? f32x2_add(x, t) : f32x2_fma(x, sl2x2, t);
-              t = f32x2_add(t, step);
-              return y;
-            });
-          } else {
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-              s[j] = fmaf(-slope, fabsf(static_cast<float>(pos - key0 - j)), kCap ? s[j] : fmaf(s[j], sl2, -less));
-          }
-        }
-        if (!kCap && !kBias) {
-          const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
-          each([&](int, uint64_t x) { return f32x2_fma(x, sl2x2, neg); });
-        }
-        if (key0 < all_lo || key0 + kCols > all_hi) {  // some row does not see all of the keys
-          const int jlo = lo - key0, jhi = hi - key0;  // this one sees keys j with jlo <= j < jhi
-#pragma unroll
-          for (int w = 0; w < kCols / 32; ++w) {
-            const int a = min(max(jlo - 32 * w, 0), 32), z = min(max(jhi - 32 * w, 0), 32);
-            const uint32_t seen = a < z ? (0xffffffffu << a) & (0xffffffffu >> (32 - z)) : 0u;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[32 * w + j] = (seen >> j) & 1u ? s[32 * w + j] : -INFINITY;
-          }
-        }
-        if (by_maximum) mx = max_all(s) + base;
-      }
-      if (by_maximum) {
-        // The reference moves to the row's largest score when that is above it by more than 8 (2^8 of headroom), and to
-        // the first tile's in which the row sees a key. Its two threads tell one another theirs (rounded: any value near
-        // will do); the place is free again, since the tile's scores are only there once both were done with the last.
-        const __nv_bfloat16 mine = __float2bfloat16_rn(mx);
-        s_max[half * kBM] = mine;
-        pair_sync();
-        const float to = fmaxf(__bfloat162float(mine), __bfloat162float(s_max[(half ^ 1) * kBM]));
-        const bool move = to > (m == -INFINITY ? m : m + 8.f);
-        if (__any_sync(0xffffffffu, move)) {
-          const float delta = move ? base - to : 0.f;
-          const uint64_t less = f32x2_pack(delta, delta);
-#pragma unroll
-          for (int j = 0; j < kCols; j += 2) f32x2_unpack(f32x2_add(f32x2_pack(s[j], s[j + 1]), less), s[j], s[j + 1]);
-          const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - to));
-          if (move) m = to;
-          l *= alpha;
-          if (n > 0) {  // the running output too (PV of tile n - 1 is complete: S of tile n was issued after it)
-#pragma unroll 1
-            for (int c = 0; c < kCols / 8; ++c) {
-              uint32_t r[8];
-              tmem_ld8(tO + c * 8, r);
-              tmem_wait_ld();
-              tmem_reg_fence8(r);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-              tmem_st8(tO + c * 8, r);
-            }
-            tmem_wait_st();
-          }
-        }
-      }
-      // P = 2^s, rounded to the element type, into the swizzled K-major A tile
-      if (!none) {
-#pragma unroll
-        for (int c = 0; c < kCols / 8; ++c) {
-#pragma unroll
-          for (int j = c * 8; j < c * 8 + 8; ++j) s[j] = ex2_approx(s[j]);
-          const float* e = s + c * 8;
-          sts128(prow + ((c ^ swz) << 4), Ops::pack(e[0], e[1]), Ops::pack(e[2], e[3]), Ops::pack(e[4], e[5]),
-                 Ops::pack(e[6], e[7]));
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < kCols / 8; ++c) sts128(prow + ((c ^ swz) << 4), 0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarPReady + g));
-      // The row sum is not needed for P: add it up after P is handed over. Where rows may see few keys, of the rounded p,
-      // which is what V is multiplied by, so that their shares add up to 1 exactly (a row that sees one key gets its
-      // value as it is); in sums over many keys the roundings do not add up (everywhere it would cost 5 to 9 %).
-      if (!none) {
-        if (key0 < all_lo || key0 + kCols > all_hi) {
-#pragma unroll
-          for (int j = 0; j < kCols; j += 2) {
-            const uint32_t w = Ops::pack(s[j], s[j + 1]);
-            s[j] = Ops::lo(w);
-            s[j + 1] = Ops::hi(w);
-          }
-        }
-        uint64_t acc[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) acc[a] = f32x2_pack(s[2 * a], s[2 * a + 1]);
-#pragma unroll
-        for (int j = 8; j < kCols; j += 8)
-#pragma unroll
-          for (int a = 0; a < 4; ++a) acc[a] = f32x2_add(acc[a], f32x2_pack(s[j + 2 * a], s[j + 2 * a + 1]));
-        float t0, t1, t2, t3, t4, t5, t6, t7;
-        f32x2_unpack(acc[0], t0, t1);
-        f32x2_unpack(acc[1], t2, t3);
-        f32x2_unpack(acc[2], t4, t5);
-        f32x2_unpack(acc[3], t6, t7);
-        l += ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
-      }
-    }
-    if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), 0, s_abort, p.err));
-    // Epilogue. Every product is complete, so the K/V ring and the two P buffers are free: a row's two threads add up
-    // their sums through the one, each stages its half of the normalised O row in the other (the rows of the two groups
-    // side by side, 512 B, 16-byte chunks rotated by the row to spread the banks), then each warp stores whole rows.
-    const uint32_t stage = sbase + kOffP;
-    float* s_sum = reinterpret_cast<float*>(smem + kOffKV) + 2 * g * kBM + row;  // [half][row]
-    if (ok) s_sum[half * kBM] = l;
-    pair_sync();
-    if (ok) l += s_sum[(half ^ 1) * kBM];
-    if constexpr (kSplit) {
-      // The parts' references and sums are exchanged; then every row is scaled for the common ones and goes to the CTA
-      // that adds up its parts, in their order: rows_own of the 256 rows each. Q, P and the ring are idle in every CTA
-      // by then, and the rows arrive where Q and P were.
-      const int rows_own = 2 * kBM / parts, ri = g * kBM + row;
-      const uint32_t ml = sbase + kOffKV + 4 * kBM * 4;  // behind the halves' sums of 256 rows
-      float ref = by_maximum ? m : 0.f;
-      if (!ok || n_tiles == 0) {
-        ref = -INFINITY;
-        l = 0.f;
-      }
-      if (half == 0) asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml + ri * 8), "f"(ref), "f"(l) : "memory");
-      cluster_sync();
-      float M = -INFINITY, L = 0.f;
-      for (int i = 0; i < parts; ++i) M = fmaxf(M, ld_cluster_f2(in_part(ml + ri * 8, i)).x);
-      if (M == -INFINITY) M = 0.f;
-      for (int i = 0; i < parts; ++i) {
-        const float2 v = ld_cluster_f2(in_part(ml + ri * 8, i));
-        L = fmaf(ex2_approx(v.x - M), v.y, L);
-      }
-      const float inv = ex2_approx(ref - M) * (L == 0.f ? 0.f : 1.f / L);
-      const uint32_t dst = in_part(sbase + kOffQ + (part * rows_own + ri % rows_own) * 512, ri / rows_own);
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < kCols / 32; ++c) {
-        uint32_t x[32];
-        if (ok && n_tiles > 0) {
-          tmem_ld32(tO + c * 32, x);
-          tmem_wait_ld();
-          tmem_reg_fence(x);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          st_cluster_f4(dst + (((half * 16 + c * 8 + j / 4) ^ (row & 31)) << 4), __uint_as_float(x[j]) * inv,
-                        __uint_as_float(x[j + 1]) * inv, __uint_as_float(x[j + 2]) * inv, __uint_as_float(x[j + 3]) * inv);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarStaged));
-      cluster_sync();
-      for (int lr = warp - 4; lr < rows_own; lr += kSoftmaxWarps) {
-        const int r2 = part * rows_own + lr, g2 = r2 / kBM, q_row = r2 % kBM;
-        const int seq_row = r0 + q_row + (p.neighbours ? g2 * kBM : 0), to_head = head0 + (p.neighbours ? 0 : g2);
-        if (seq_row >= Lq) continue;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < parts; ++i) {
-          float4 v;
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                       : "r"(sbase + kOffQ + (i * rows_own + lr) * 512 + ((lane ^ (q_row & 31)) << 4))
+    for (int k = 0;; ++k) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err));
+      const Place w0 = place();
+      ok = pair_agree(w0, ok);
+      if (!ok) break;
+      const Item& it = items[k & 1];
+      if (it.n_tiles < 0) break;
+      int pos, lo, hi;
+      seen_from(it, it.r0 + (p.neighbours && w0.g() > 0 ? kBM : 0) + w0.row(), pos, lo, hi);
+      // seen by any and by all of the warp's rows
+      {
+        const int any_lo = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX);
+        const int any_hi = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
+        const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+        if (w0.lane() == 0)
+          asm volatile("st.shared.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(seen_at(w0)), "r"(any_lo), "r"(any_hi), "r"(all_lo),
+                       "r"(all_hi)
                        : "memory");
-          o.x += v.x;
-          o.y += v.y;
-          o.z += v.z;
-          o.w += v.w;
+        __syncwarp();
+      }
+      const int min_pos = __reduce_min_sync(0xffffffffu, pos);
+      const float slope = kBias ? p.slopes[it.head0 + (p.neighbours ? 0 : w0.g())] * kLog2e : 0.f;
+      float m = -INFINITY;  // the row's reference, log2 units; within 8 of its running maximum from below, or fixed at 0
+      float l = 0.f;        // of this thread's keys
+      constexpr int kStep = kBack ? -kBN : kBN;
+      int key0 = first_key_of(it, 0) + w0.half() * kCols - kStep;
+      for (int left = it.n_tiles; left > 0; --left) {
+        key0 += kStep;
+        const Place w = place();
+        int any_lo, any_hi, all_lo, all_hi;
+        asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(any_lo), "=r"(any_hi), "=r"(all_lo), "=r"(all_hi)
+                     : "r"(seen_at(w))
+                     : "memory");
+        // every lane waits (each needs the acquire); the warp then agrees, so
+        // the warp-collective tensor-memory loads below run on all 32 lanes
+        if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarSFull + w.g()), parity, s_abort, p.err));
+        if (!ok) {  // the other warp of these rows may still come to the pair's barrier
+          if (by_maximum) pair_sync(w);
+          continue;
         }
-        const int64_t out_row = static_cast<int64_t>(cq0) + seq_row;
-        if (__any_sync(0xffffffffu, isnan(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)))))) {
-          int row_pos, row_lo, row_hi;
-          seen_from(seq_row, row_pos, row_lo, row_hi);
-          row_again<E>(p, b, ck0, out_row, to_head, row_pos, row_lo, row_hi, lane);
+        parity ^= 1;
+        tc_fence_after();
+        const bool none = key0 + kCols <= any_lo || key0 >= any_hi;  // no row sees any of these keys
+        const bool edge = key0 < all_lo || key0 + kCols > all_hi;  // some row does not see all of them
+        float s[kCols], mx = -INFINITY;
+        const float base = m == -INFINITY ? 0.f : m;
+        if (!none) {
+          {
+            uint32_t x0[32], x1[32];
+            const uint32_t tS = tmem_at(w, 0);
+            tmem_ld32(tS + 0, x0);
+            tmem_ld32(tS + 32, x1);
+            tmem_wait_ld();
+            tmem_reg_fence(x0);
+            tmem_reg_fence(x1);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              s[j] = __uint_as_float(x0[j]);
+              s[32 + j] = __uint_as_float(x1[j]);
+            }
+          }
+          auto each = [&](auto arg) {
+#pragma unroll
+            for (int j = 0; j < kCols; j += 2) f32x2_unpack(arg(j, f32x2_pack(s[j], s[j + 1])), s[j], s[j + 1]);
+          };
+          // ---- s = z - base, base the row's reference so far (0 as long as it has seen no key) ----
+          const uint64_t neg = f32x2_pack(-base, -base);
+          if (kCap) {
+            using Fit = TanhFit<E>;
+            if (key0 + kCols > any_hi) {  // what lies behind the rows' keys has no say in how their scores are worked out
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) s[j] = j < any_hi - key0 ? s[j] : 0.f;
+            }
+            const float size = size_all(s);
+            if (__all_sync(0xffffffffu, size <= p.near_top)) {
+              const Poly2<Fit::kNear> poly(p.near_c);
+              each([&](int, uint64_t x) { return poly(x, neg); });
+            } else if (__all_sync(0xffffffffu, size <= p.far_top)) {
+              const Poly2<Fit::kFar> poly(p.far_c);
+              each([&](int, uint64_t x) { return poly(x, neg); });
+            } else {
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) s[j] = capped<Fit::kFar>(s[j], p) - base;
+            }
+          }
+          if (kBias) {
+            const float less = kCap ? 0.f : base;
+            if (key0 + kCols - 1 <= min_pos) {  // all keys at or before all rows: - slope (pos - t) grows by slope a key
+              const float first = -slope * static_cast<float>(pos - key0) - less;
+              const uint64_t sl2x2 = f32x2_pack(sl2, sl2), step = f32x2_pack(8.f * slope, 8.f * slope);
+              uint64_t at[4];
+#pragma unroll
+              for (int a = 0; a < 4; ++a) at[a] = f32x2_pack(fmaf(slope, 2.f * a, first), fmaf(slope, 2.f * a + 1.f, first));
+              each([&](int j, uint64_t x) {
+                uint64_t& t = at[(j >> 1) & 3];
+                const uint64_t y = kCap ? f32x2_add(x, t) : f32x2_fma(x, sl2x2, t);
+                t = f32x2_add(t, step);
+                return y;
+              });
+            } else {
+#pragma unroll
+              for (int j = 0; j < kCols; ++j)
+                s[j] = fmaf(-slope, fabsf(static_cast<float>(pos - key0 - j)), kCap ? s[j] : fmaf(s[j], sl2, -less));
+            }
+          }
+          if (!kCap && !kBias) {
+            const uint64_t sl2x2 = f32x2_pack(sl2, sl2);
+            each([&](int, uint64_t x) { return f32x2_fma(x, sl2x2, neg); });
+          }
+          if (edge) {  // some row does not see all of the keys
+            const int jlo = lo - key0, jhi = hi - key0;  // this one sees keys j with jlo <= j < jhi
+#pragma unroll
+            for (int w = 0; w < kCols / 32; ++w) {
+              const int a = min(max(jlo - 32 * w, 0), 32), z = min(max(jhi - 32 * w, 0), 32);
+              const uint32_t seen = a < z ? (0xffffffffu << a) & (0xffffffffu >> (32 - z)) : 0u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[32 * w + j] = (seen >> j) & 1u ? s[32 * w + j] : -INFINITY;
+            }
+          }
+          if (by_maximum) mx = max_all(s) + base;
+        }
+        if (by_maximum) {
+          // The reference moves to the row's largest score when that is above it by more than 8 (2^8 of headroom), and to
+          // the first tile's in which the row sees a key. Its two threads tell one another theirs (rounded: any value near
+          // will do); the place is free again, since the tile's scores are only there once both were done with the last.
+          const Place wm = place();
+          const __nv_bfloat16 mine = __float2bfloat16_rn(mx);
+          uint16_t others;
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(max_at(wm.u)), "h"(__bfloat16_as_ushort(mine)) : "memory");
+          pair_sync(wm);
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(others) : "r"(max_at(wm.u ^ 128)) : "memory");
+          const float to = fmaxf(__bfloat162float(mine), __bfloat162float(__ushort_as_bfloat16(others)));
+          const bool move = to > (m == -INFINITY ? m : m + 8.f);
+          if (__any_sync(0xffffffffu, move)) {
+            const float delta = move ? base - to : 0.f;
+            const uint64_t less = f32x2_pack(delta, delta);
+#pragma unroll
+            for (int j = 0; j < kCols; j += 2) f32x2_unpack(f32x2_add(f32x2_pack(s[j], s[j + 1]), less), s[j], s[j + 1]);
+            const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - to));
+            const bool rescale = move && m != -INFINITY;
+            if (move) m = to;
+            l *= alpha;
+            if (__any_sync(0xffffffffu, rescale)) {
+              // the running output too (PV of the tile before is complete: S of this one was issued after it)
+              const uint32_t tO = tmem_at(wm, 256);
+#pragma unroll 1
+              for (int c = 0; c < kCols / 8; ++c) {
+                uint32_t r[8];
+                tmem_ld8(tO + c * 8, r);
+                tmem_wait_ld();
+                tmem_reg_fence8(r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+                tmem_st8(tO + c * 8, r);
+              }
+              tmem_wait_st();
+            }
+          }
+        }
+        // P = 2^s, rounded to the element type, into the swizzled K-major A tile (eight addresses, made here: kept over the
+        // loop they would cost the registers that the scores need)
+        const Place wp = place();
+        const uint32_t to_p = p_row(wp) | (wp.u & 7) << 4;
+        if (!none) {
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c) {
+#pragma unroll
+            for (int j = c * 8; j < c * 8 + 8; ++j) s[j] = ex2_approx(s[j]);
+            const float* e = s + c * 8;
+            sts128(to_p ^ (c << 4), Ops::pack(e[0], e[1]), Ops::pack(e[2], e[3]), Ops::pack(e[4], e[5]),
+                   Ops::pack(e[6], e[7]));
+          }
         } else {
-          *(reinterpret_cast<uint2*>(p.out + (out_row * p.hq + to_head) * kHeadDim) + lane) =
-              make_uint2(Ops::pack(o.x, o.y), Ops::pack(o.z, o.w));
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c) sts128(to_p ^ (c << 4), 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (wp.lane() == 0) mbar_arrive(bar(kBarPReady + wp.g()));
+        // The row sum is not needed for P: add it up after P is handed over. Where rows may see few keys, of the rounded p,
+        // which is what V is multiplied by, so that their shares add up to 1 exactly (a row that sees one key gets its
+        // value as it is); in sums over many keys the roundings do not add up (everywhere it would cost 5 to 9 %).
+        if (!none) {
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < kCols; j += 2) {
+              const uint32_t w = Ops::pack(s[j], s[j + 1]);
+              s[j] = Ops::lo(w);
+              s[j + 1] = Ops::hi(w);
+            }
+          }
+          uint64_t acc[4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) acc[a] = f32x2_pack(s[2 * a], s[2 * a + 1]);
+#pragma unroll
+          for (int j = 8; j < kCols; j += 8)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) acc[a] = f32x2_add(acc[a], f32x2_pack(s[j + 2 * a], s[j + 2 * a + 1]));
+          float t0, t1, t2, t3, t4, t5, t6, t7;
+          f32x2_unpack(acc[0], t0, t1);
+          f32x2_unpack(acc[1], t2, t3);
+          f32x2_unpack(acc[2], t4, t5);
+          f32x2_unpack(acc[3], t6, t7);
+          l += ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
         }
       }
-      wait_for_others();
-      return;
-    }
-    if (ok) {
-      tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      float spoilt = 0.f;  // NaN once any element is not finite
-#pragma unroll
-      for (int c = 0; c < kCols / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tO + c * 32, r);
-        tmem_wait_ld();
-        tmem_reg_fence(r);
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          const int q = g * 16 + half * 8 + c * 4 + j / 8;  // 16-byte chunk of the 512-byte row
-          sts128(stage + row * 512 + ((q ^ (row & 31)) << 4),
-                 Ops::pack(__uint_as_float(r[j + 0]) * inv, __uint_as_float(r[j + 1]) * inv),
-                 Ops::pack(__uint_as_float(r[j + 2]) * inv, __uint_as_float(r[j + 3]) * inv),
-                 Ops::pack(__uint_as_float(r[j + 4]) * inv, __uint_as_float(r[j + 5]) * inv),
-                 Ops::pack(__uint_as_float(r[j + 6]) * inv, __uint_as_float(r[j + 7]) * inv));
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) spoilt = fmaf(__uint_as_float(r[j]), 0.f, spoilt);
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarOFinal), k & 1, s_abort, p.err));
+      // Epilogue, with the item's description read again. Every product is complete, so the warp's part of P is free: a
+      // row's two threads add up their sums through it.
+      const Item* described = items + (k & 1);
+      asm volatile("" : "+l"(described)::"memory");
+      const int Lq = described->Lq, cq0 = described->cq0;
+      const Place w1 = place();
+      const int g = w1.g(), half = w1.half(), row = w1.row(), lane = w1.lane();
+      const uint32_t prow = p_row(w1), tO = tmem_at(w1, 256);
+      const uint32_t other = half ? prow - kHalfBytes : prow + kHalfBytes;
+      if (ok) asm volatile("st.shared.f32 [%0], %1;" ::"r"(prow), "f"(l) : "memory");
+      pair_sync(w1);
+      if (ok) {
+        float more;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(more) : "r"(other) : "memory");
+        l += more;
       }
-      const uint32_t again = __ballot_sync(0xffffffffu, isnan(spoilt) && g_row0 + row < Lq);
-      if (lane == 0 && again) atomicOr(s_again + rows32, again);
+      pair_sync(w1);
+      if constexpr (kSplit) {
+        // The parts' references and sums are exchanged; then every row is scaled for the common ones and goes to the CTA
+        // that adds up its parts, in their order: rows_own of the 256 rows each. Q, P and the ring are idle in every CTA
+        // by then; the rows arrive where Q and P were.
+        const int rows_own = 2 * kBM / parts, ri = g * kBM + row;
+        const uint32_t ml = sbase + kOffKV;
+        float ref = by_maximum ? m : 0.f;
+        if (!ok || described->n_tiles == 0) {
+          ref = -INFINITY;
+          l = 0.f;
+        }
+        if (half == 0) asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml + ri * 8), "f"(ref), "f"(l) : "memory");
+        cluster_sync();
+        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < parts; ++i) M = fmaxf(M, ld_cluster_f2(in_part(ml + ri * 8, i)).x);
+        if (M == -INFINITY) M = 0.f;
+        for (int i = 0; i < parts; ++i) {
+          const float2 v = ld_cluster_f2(in_part(ml + ri * 8, i));
+          L = fmaf(ex2_approx(v.x - M), v.y, L);
+        }
+        const float inv = ex2_approx(ref - M) * (L == 0.f ? 0.f : 1.f / L);
+        const uint32_t dst = in_part(sbase + kOffQ + (part * rows_own + ri % rows_own) * 512, ri / rows_own);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t x[32];
+          if (ok && described->n_tiles > 0) {
+            tmem_ld32(tO + c * 32, x);
+            tmem_wait_ld();
+            tmem_reg_fence(x);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            st_cluster_f4(dst + (((half * 16 + c * 8 + j / 4) ^ (row & 31)) << 4), __uint_as_float(x[j]) * inv,
+                          __uint_as_float(x[j + 1]) * inv, __uint_as_float(x[j + 2]) * inv, __uint_as_float(x[j + 3]) * inv);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarDone));
+        cluster_sync();
+        for (int lr = warp - 4; lr < rows_own; lr += kSoftmaxWarps) {
+          const int r2 = part * rows_own + lr, g2 = r2 / kBM, q_row = r2 % kBM;
+          const int seq_row = it.r0 + q_row + (p.neighbours ? g2 * kBM : 0), to_head = it.head0 + (p.neighbours ? 0 : g2);
+          if (seq_row >= Lq) continue;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < parts; ++i) {
+            float4 v;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                         : "r"(sbase + kOffQ + (i * rows_own + lr) * 512 + ((lane ^ (q_row & 31)) << 4))
+                         : "memory");
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+          }
+          const int64_t out_row = static_cast<int64_t>(cq0) + seq_row;
+          if (__any_sync(0xffffffffu, isnan(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)))))) {
+            int row_pos, row_lo, row_hi;
+            seen_from(it, seq_row, row_pos, row_lo, row_hi);
+            row_again<E>(p, it.b, it.ck0, out_row, to_head, row_pos, row_lo, row_hi, lane);
+          } else {
+            *(reinterpret_cast<uint2*>(p.out + (out_row * p.hq + to_head) * kHeadDim) + lane) =
+                make_uint2(Ops::pack(o.x, o.y), Ops::pack(o.z, o.w));
+          }
+        }
+        wait_for_others();
+        return;
+      }
+      // The warp stages its 64 dims of its normalised rows there (128 B a row, 16-byte chunks rotated by the row) and stores
+      // them, four rows at once. Rows that are to be computed again are left to warp 2.
+      const uint32_t to_p = prow | (lane & 7) << 4;
+      const int row0 = described->r0 + (p.neighbours && g > 0 ? kBM : 0) + w1.quarter() * 32;  // of the sequence
+      uint32_t again = 0;
+      if (ok) {
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float spoilt = 0.f;  // NaN once any element is not finite
+        // sixteen columns at once: 32 made the compiler spill scores in the loop over the tiles (351 us became 590)
+#pragma unroll 1
+        for (int c = 0; c < kCols / 8; c += 2) {
+          uint32_t r[2][8];
+#pragma unroll
+          for (int a = 0; a < 2; ++a) tmem_ld8(tO + (c + a) * 8, r[a]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            tmem_reg_fence8(r[a]);
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              x[j] = __uint_as_float(r[a][j]);
+              spoilt = fmaf(x[j], 0.f, spoilt);
+            }
+            sts128(to_p ^ ((c + a) << 4), Ops::pack(x[0] * inv, x[1] * inv), Ops::pack(x[2] * inv, x[3] * inv),
+                   Ops::pack(x[4] * inv, x[5] * inv), Ops::pack(x[6] * inv, x[7] * inv));
+          }
+        }
+        again = __ballot_sync(0xffffffffu, isnan(spoilt) && row0 + lane < Lq);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarOFree + g));
+      if (ok) {
+        const uint32_t stage = prow - lane * 128;
+        const int64_t step = static_cast<int64_t>(p.hq) * kHeadDim;
+        uint16_t* to = p.out + (static_cast<int64_t>(cq0 + row0) * p.hq + described->head0 + (p.neighbours ? 0 : g)) * kHeadDim +
+                       half * kCols + (lane & 7) * 8 + (lane >> 3) * step;
+#pragma unroll 4
+        for (int rr = lane >> 3; rr < 32; rr += 4, to += 4 * step) {
+          uint32_t x0, x1, x2, x3;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                       : "r"(stage + rr * 128 + (((lane ^ rr) & 7) << 4))
+                       : "memory");
+          if (row0 + rr < Lq) *reinterpret_cast<uint4*>(to) = make_uint4(x0, x1, x2, x3);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        s_again[(k & 1) * kSoftmaxWarps + w1.warp()] = again;
+        mbar_arrive(bar(kBarRows));
+        mbar_arrive(bar(kBarItemFree + (k & 1)));
+      }
     }
-    // all softmax warps arrive, whatever happened, so the wait below (and
-    // warp 1's before releasing TMEM) always ends; every tensor-memory read of
-    // this warp is complete here
+    // every softmax warp comes here, whatever happened (a split item's leave above): its last tensor-memory read is complete
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kBarStaged));
-    const bool staged = __all_sync(0xffffffffu, wait_or_abort(bar(kBarStaged), 0, s_abort, p.err));
-    if (ok && staged) {
-      const int to_g = lane >> 4;  // this lane's half of the 512 bytes
-      const int to_row0 = r0 + (p.neighbours ? to_g * kBM : 0);
-      uint16_t* obase = p.out + (static_cast<int64_t>(cq0 + to_row0) * p.hq + head0 + (p.neighbours ? 0 : to_g)) * kHeadDim +
-                        (lane & 15) * 8;
-      const uint32_t* skip = s_again + 4 * to_g;
-      for (int rr = warp - 4; rr < min(kBM, Lq - r0); rr += kSoftmaxWarps) {
-        uint32_t a, b2, c2, d;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(a), "=r"(b2), "=r"(c2), "=r"(d)
-                     : "r"(stage + rr * 512 + ((lane ^ (rr & 31)) << 4)));
-        if (to_row0 + rr < Lq && !((skip[rr >> 5] >> (rr & 31)) & 1u))
-          *reinterpret_cast<uint4*>(obase + static_cast<int64_t>(rr) * p.hq * kHeadDim) = make_uint4(a, b2, c2, d);
-      }
-      for (uint32_t again = half == 0 ? s_again[rows32] : 0; again; again &= again - 1) {
-        const int src = __ffs(again) - 1;
-        row_again<E>(p, b, ck0, static_cast<int64_t>(cq0) + g_row0 + (warp & 3) * 32 + src, head,
-                     __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, lo, src),
-                     __shfl_sync(0xffffffffu, hi, src), lane);
-      }
-    }
+    if (lane == 0) mbar_arrive(bar(kBarDone));
+    if (kSplit) wait_for_others();
+    return;
   }
 
-  if (kSplit) {  // (warps 0 to 3 here) every thread of a cluster comes to both of its barriers
+  if (kSplit && had_item) {  // (warps 0 to 3 here) every thread of a cluster comes to both of its barriers
     __syncwarp();
     cluster_sync();
   }
   if (warp == 1) {
-    // TMEM is released after every softmax warp's last tensor-memory read
-    // (they all arrive on kBarStaged once O is staged); no CTA-wide barrier,
-    // so no role waits at one with some of its lanes still busy. The wait is
-    // time-bounded but ignores the abort flag: the softmax warps always arrive.
+    // TMEM is released after every softmax warp's last tensor-memory read. The wait is time-bounded but ignores the abort
+    // flag: the softmax warps always arrive.
     __syncwarp();
-    mbar_wait(bar(kBarStaged), 0, p.err);
+    mbar_wait(bar(kBarDone), 0, p.err);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
   if (kSplit) {
-    cluster_sync();
+    if (had_item) cluster_sync();
     wait_for_others();
   }
 }
