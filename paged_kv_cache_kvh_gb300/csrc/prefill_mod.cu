@@ -21,8 +21,8 @@
 // with a cap and a window 77 us with a CTA to an item, 69 now; 5000 on 7001 without a cap 311 and 322, see Place).
 //
 // What bounds it: a key tile of both groups takes about 2 us, its products 1.1 of that; the rest is the chain of each
-// group (product, softmax, barrier, product) with two groups to overlap and the softmax's issue slots, 54 % in use as
-// the tensor pipe is. 16 on 8 heads, 5000 on 7001 in the cache: 351 us capped at 50 and 322 without a cap, of 207 at
+// group (product, softmax, barrier, product) with two groups to overlap: the tensor pipe is 53 % in use and the issue
+// slots 48 %. 16 on 8 heads, 5000 on 7001 in the cache: 351 us capped at 50 and 322 without a cap, of 207 at
 // cuBLAS' rate (0.59 and 0.64 of it). Measured and not kept: 384 threads with registers shared out by role (427 us where
 // 404 was), scores fetched a tile ahead (430: three slots of the ring are too few for it).
 //
