@@ -511,8 +511,8 @@ int pkv_rope_frequencies(int32_t rotary_dim, double theta, int32_t scaling, doub
  *   freqs         [rotary_dim/2] int64 on the device (pkv_rope_frequencies).
  *   q_out, k_out  as q and k; may be the same rows (in place), else must not overlap them.
  * head_dim up to 1024, rotary_dim even and at most head_dim. 16-byte vectors where
- * pointers are 16-byte aligned, strides multiples of 8 and head_dim and rotary_dim
- * multiples of 16; any 2-byte alignment otherwise.
+ * pointers are 16-byte aligned and strides and head_dim multiples of 8 (fastest with
+ * head_dim and rotary_dim multiples of 16); any 2-byte alignment otherwise.
  */
 int pkv_rope(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const int64_t* positions,
              const int64_t* freqs, int32_t rotary_dim, float magnitude, int32_t interleaved, int32_t num_tokens,

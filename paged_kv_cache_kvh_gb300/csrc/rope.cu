@@ -217,6 +217,106 @@ __global__ void __launch_bounds__(kThreads, 4) rope_v16_kernel(const RopeParams 
   }
 }
 
+// Any turned part: a thread moves 16-byte pieces, and finds the partners of the turned elements in one in what the others
+// have read (in the half layout they lie anywhere in the row; in one piece if a half is a whole number of them). Since
+// rows may be turned in place, a batch of whole rows is read before any of it is written. Needs 16-byte alignment
+// throughout and d in multiples of 8. 5.5 k tokens of 32 heads on 8, 6 of 128 dims, with the store: 49 us (interleaved 31);
+// partners fetched from the rows once more 60, a pair at a time 183; one piece a thread at once 47 (33), four 63 (34).
+constexpr int kBatch8 = 2;
+template <Elem E, bool kInterleaved, bool kStore>
+__global__ void __launch_bounds__(kThreads, 5) rope_v8_kernel(const RopeParams p) {
+  using Ops = ElemOps<E>;
+  extern __shared__ __align__(16) float angles[];
+  __shared__ uint4 read[2][kBatch8][kThreads];  // what the threads have read, in turns: the pieces of a row lie side by side
+  __shared__ int64_t slots[kMaxTokens];
+  const int first = static_cast<int>(blockIdx.x) * p.tokens;
+  const int n = min(p.tokens, p.num_tokens - first);
+  float* cosines = angles;
+  float* sines = angles + p.tokens * p.half;
+  block_angles<kStore>(p, first, n, cosines, sines, slots);
+  __syncthreads();
+  const int pieces = p.d >> 3;
+  const int rows = p.hq + p.hkv + (kStore ? p.hkv : 0);
+  const int step = kThreads / pieces;  // rows a block moves at once
+  const int e0 = 8 * (static_cast<int>(threadIdx.x) % pieces);
+  const int at = static_cast<int>(threadIdx.x) / pieces;
+  const int end = at < step ? n * rows : 0;  // (threads left over)
+  const bool whole = p.half % 8 == 0;
+  int turn = 0;
+  for (int r0 = 0; r0 < n * rows; r0 += step * kBatch8) {
+    uint4 x[kBatch8];
+    uint16_t* to[kBatch8];
+    int token[kBatch8];  // of the block, where this piece is turned; else -1
+#pragma unroll
+    for (int i = 0; i < kBatch8; ++i) {
+      const int r = r0 + i * step + at;
+      to[i] = nullptr;
+      token[i] = -1;
+      if (r >= end) continue;
+      const int t = r / rows, row = r - t * rows;
+      const int part = row < p.hq ? 0 : (row < p.hq + p.hkv ? 1 : 2);
+      const int head = row - (part > 0 ? p.hq : 0) - (part > 1 ? p.hkv : 0);
+      int64_t line = first + t;
+      if (kStore && part > 0) {
+        line = slots[t];
+        if (line < 0) continue;
+      }
+      const uint16_t* s = p.src[part] + (first + t) * p.src_stride[part] + head * p.d;
+      to[i] = p.dst[part] + line * p.dst_stride[part] + head * p.d + e0;
+      x[i] = ld_row16(s + e0);
+      if (!kInterleaved) read[turn][i][threadIdx.x] = x[i];
+      if (part < 2 && e0 < 2 * p.half) token[i] = t;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBatch8; ++i) {
+      if (token[i] < 0) continue;
+      const uint16_t* s = reinterpret_cast<const uint16_t*>(&read[turn][i][at * pieces]);  // the row
+      uint32_t* w = &x[i].x;
+      const float* cs = cosines + token[i] * p.half;
+      const float* sn = sines + token[i] * p.half;
+      if (kInterleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int pair = (e0 >> 1) + j;
+          if (pair < p.half) turn_pair<E>(w[j], cs[pair], sn[pair]);
+        }
+      } else if (whole) {
+        const bool second = e0 >= p.half;
+        const int pair = second ? e0 - p.half : e0;
+        uint4 y = *reinterpret_cast<const uint4*>(s + (second ? pair : pair + p.half));
+        uint32_t* v = &y.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (second)
+            turn_word<E>(v[j], w[j], cs[pair + 2 * j], sn[pair + 2 * j], cs[pair + 2 * j + 1], sn[pair + 2 * j + 1]);
+          else
+            turn_word<E>(w[j], v[j], cs[pair + 2 * j], sn[pair + 2 * j], cs[pair + 2 * j + 1], sn[pair + 2 * j + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float r2[2] = {Ops::lo(w[j]), Ops::hi(w[j])};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int e = e0 + 2 * j + h;
+            if (e >= 2 * p.half) continue;
+            const bool second = e >= p.half;
+            const int pair = second ? e - p.half : e;
+            const float y = Ops::lo(s[second ? pair : pair + p.half]);
+            r2[h] = second ? fmaf(r2[h], cs[pair], y * sn[pair]) : fmaf(r2[h], cs[pair], -y * sn[pair]);
+          }
+          w[j] = Ops::pack(r2[0], r2[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch8; ++i)
+      if (to[i]) *reinterpret_cast<uint4*>(to[i]) = x[i];
+    turn ^= 1;
+  }
+}
+
 // Any sizes and alignment: one pair, or one element that is copied, at a time.
 template <Elem E, bool kInterleaved, bool kStore>
 __global__ void __launch_bounds__(kThreads) rope_u16_kernel(const RopeParams p) {
@@ -265,8 +365,10 @@ bool vec16(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(
 template <Elem E, bool kInterleaved, bool kStore>
 void launch_typed(const RopeParams& p, bool vector, unsigned blocks, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(p.tokens) * p.half * 8;
-  if (vector)
+  if (vector && p.d % 16 == 0 && p.half % 8 == 0)
     rope_v16_kernel<E, kInterleaved, kStore><<<blocks, kThreads, smem, stream>>>(p);
+  else if (vector)
+    rope_v8_kernel<E, kInterleaved, kStore><<<blocks, kThreads, smem, stream>>>(p);
   else
     rope_u16_kernel<E, kInterleaved, kStore><<<blocks, kThreads, smem, stream>>>(p);
 }
@@ -301,7 +403,7 @@ cudaError_t launch_rope(const RopeArgs& a, bool interleaved, unsigned int* err, 
   // Several tokens to a block spread the wait for the angles over more rows; with few tokens every SM should have some.
   p.tokens = 1;
   while (p.tokens < kMaxTokens && a.num_tokens >= 2 * p.tokens * 4 * 152) p.tokens *= 2;
-  bool vector = a.d % 16 == 0 && a.rot % 16 == 0 && a.d <= 16 * kThreads;
+  bool vector = a.d % 8 == 0 && a.d <= 8 * kThreads;
   if (a.hq > 0) vector = vector && vec16(a.q, a.q_stride) && vec16(a.q_out, a.q_out_stride);
   if (a.hkv > 0) vector = vector && vec16(a.k, a.k_stride) && vec16(a.k_out, a.k_out_stride);
   if (a.hkv > 0 && store) vector = vector && vec16(a.v, a.v_stride) && vec16(a.v_out, a.k_out_stride);

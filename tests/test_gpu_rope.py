@@ -45,7 +45,7 @@ def _check(got, x, positions, freqs, interleaved, magnitude):
     (5, 32, 8, 128, 64, 8, 8),
     (9, 3, 1, 128, 96, 0, 0),       # six of eight pieces turned
     (6, 5, 2, 96, 32, 16, 0),       # six pieces to a head: some threads of a block idle
-    (4, 2, 2, 64, 6, 0, 0),         # 3 pairs: one at a time
+    (4, 2, 2, 64, 6, 0, 0),         # 3 pairs
     (3, 4, 1, 20, 20, 0, 0),
     (3, 2, 1, 128, 128, 1, 0),      # odd row stride
     (3, 2, 1, 128, 128, 0, 1),      # rows 2 bytes off
@@ -75,6 +75,41 @@ def test_rope(pkv, dtype, interleaved, n, hq, hkv, dims, rot, pad, offset):
     a, b = rope(q, k, positions, freqs, interleaved=interleaved, magnitude=1.25, q_out=q, k_out=k)
     assert a is q and torch.equal(q, qo) and q.storage_offset() == around and not torch.equal(q, q0)
     assert k is None or (b is k and torch.equal(k, ko))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n,hq,hkv,dims,rot", [(5, 4, 2, 128, 6), (1300, 3, 1, 128, 120), (3, 5, 2, 72, 72), (7, 3, 3, 40, 24),
+                                               (4, 2, 1, 96, 90), (2, 40, 8, 1000, 998), (6, 1, 1, 8, 2), (2, 3, 1, 24, 16),
+                                               (5000, 1, 1, 1024, 1022)])
+def test_any_turned_part_and_in_place(pkv, dtype, interleaved, n, hq, hkv, dims, rot):
+    """16-byte pieces that hold turned elements and copied ones, partners in other pieces; in place and to the cache."""
+    rope, rope_store = _names(pkv, dtype)
+    q, k, v = (_rows(n, h, dims, dtype, s, 8) for s, h in ((1, hq), (2, hkv), (3, hkv)))
+    positions = torch.randint(0, 1 << 17, (n,), generator=torch.Generator().manual_seed(5)).cuda()
+    freqs, _ = pkv.rope_frequencies(rot)
+    qo, ko = rope(q, k, positions, freqs, magnitude=1.25, interleaved=interleaved)
+    few = min(n, 9)
+    _check(qo[:few], q[:few], positions[:few], freqs, interleaved, 1.25)
+    _check(ko[:few], k[:few], positions[:few], freqs, interleaved, 1.25)
+    # the same rows a pair at a time: 2 bytes off
+    q1, k1 = (torch.empty((n, h * dims + 9), dtype=dtype, device="cuda")[:, 1:1 + h * dims].unflatten(1, (h, dims))
+              for h in (hq, hkv))
+    q1.copy_(q)
+    k1.copy_(k)
+    qs, ks = rope(q1, k1, positions, freqs, magnitude=1.25, interleaved=interleaved)
+    assert torch.equal(qo, qs) and torch.equal(ko, ks)
+    slots = torch.randperm(n + 5, generator=torch.Generator().manual_seed(6))[:n].int().cuda()
+    slots[n // 2] = -1
+    kc, vc = (torch.full((n + 5, hkv, dims), 3.0, dtype=dtype, device="cuda") for _ in range(2))
+    q2 = rope_store(q, k, v, positions, freqs, kc, vc, slots, magnitude=1.25, interleaved=interleaved)
+    kept = slots >= 0
+    assert torch.equal(q2, qo)
+    assert torch.equal(kc[slots[kept].long()], ko[kept]) and torch.equal(vc[slots[kept].long()], v[kept])
+    assert int((kc == 3).all(-1).all(-1).sum()) == 5 + 1
+    back = rope(q, k, positions, freqs, magnitude=1.25, interleaved=interleaved, q_out=q, k_out=k)
+    assert back[0] is q and torch.equal(q, qo) and torch.equal(k, ko)
+    assert pkv.pkv_device_error() == 0
 
 
 def test_padding_between_rows_is_left(pkv):
