@@ -167,3 +167,54 @@ def test_blocks_far_into_a_large_cache(pkv, dtype):
     assert torch.equal(a[3, :200], b[3, :200])
     assert torch.equal(results[0][5], results[1][5]) and torch.equal(results[0][6], results[1][6])
     assert pkv.pkv_device_error() == 0
+
+
+def test_two_threads_on_their_own_streams(pkv):
+    """Calls of two threads at once, each on a stream of its own, give what they give one after another."""
+    import threading
+    hq, hkv, scale = 12, 4, D ** -0.5
+    lens = [[900, 33, 1400, 257], [2100, 5, 640]]
+    freqs, _ = pkv.rope_frequencies(D)
+    work = []
+    for seed, ls in enumerate(lens):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        per = [-(-n // BS) for n in ls]
+        ids = iter(range(sum(per)))
+        table = [[next(ids) for _ in range(k)] + [-1] * (max(per) - k) for k in per]
+        rows = lambda h: torch.randn((sum(ls), h, D), generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        work.append(dict(q=rows(hq), k=rows(hkv), v=rows(hkv), blocks=sum(per), table=_dev(table), lens=_dev(ls),
+                         most=max(ls), cu=_dev([0] + torch.tensor(ls).cumsum(0).tolist()),
+                         positions=torch.cat([torch.arange(n, device="cuda") for n in ls]),
+                         slots=_dev([t[i // BS] * BS + i % BS for t, n in zip(table, ls) for i in range(n)]),
+                         ws=pkv.decode_mod_workspace(len(ls), max(ls), hq, hkv, weights=True)))
+
+    def run(w):
+        kc, vc = (torch.zeros((w["blocks"], BS, hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        weights = pkv.attention_weights(w["blocks"], hkv)
+        qt = pkv.pkv_rope_store_kvcache(w["q"], w["k"], w["v"], w["positions"], freqs, kc, vc, w["slots"])
+        out = pkv.pkv_prefill_varlen_mod(qt, w["cu"], w["cu"], w["most"], w["most"], scale, k_cache=kc, v_cache=vc,
+                                         block_tables=w["table"], softcap=30.0, window=500)
+        step = pkv.pkv_decode_mod(qt[w["cu"][1:].long() - 1], kc, vc, w["table"], w["lens"], w["most"], scale, w["ws"],
+                                  softcap=30.0, weights=weights)
+        kept, _ = pkv.pkv_evict_kvcache(kc, vc, weights, w["table"], w["lens"], w["most"], 300, first=4, recent=50)
+        return [qt, out, step, kept, kc, vc]
+
+    want = [run(w) for w in work]
+    torch.cuda.synchronize()
+    failures = []
+
+    def thread(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = run(work[i])
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    failures.append(i)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures and pkv.pkv_device_error() == 0
