@@ -120,8 +120,7 @@ struct Item {
 constexpr int kOffAgain = kOffItems + 2 * sizeof(Item);  // [item % 2][32 rows][half] rows to be computed again
 constexpr int kOffSeen = (kOffAgain + 2 * kSoftmaxWarps * 4 + 15) / 16 * 16;  // [warp] the keys that any and that all of its rows see
 constexpr int kOffMisc = kOffSeen + kSoftmaxWarps * 16;  // tmem address, abort flag
-constexpr int kOffMax = kOffMisc + 8;                   // [group][half][row] bf16: the halves' largest scores
-constexpr size_t kSmemBytes = kOffMax + 4 * kBM * 2 + 1024;  // + alignment slack
+constexpr size_t kSmemBytes = kOffMisc + 8 + 1024;       // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
 // tanh x = x (c0 + c1 x^2 + ...), least-maximum fits of tanh(x) / x: for bf16 off by 6.3e-6 of the result for |x| <= 0.4
@@ -706,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Where a thread works follows from its number u among the softmax threads: 256 to a group, of these 128 to a half of
     // a tile's keys, of these 32 to a warp. It is taken apart anew in each part of the item: kept over the loop over the
     // tiles it would cost the registers that the scores need (chunk of 5000 on 7001 with a bias 405 us kept, 338 anew).
-    // P, the largest scores and the ranges lie in its order.
+    // P and the ranges lie in its order.
     struct Place {
       int u;
       __device__ int lane() const { return u & 31; }
@@ -727,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto seen_at = [&](const Place& w) { return sbase + kOffSeen + w.warp() * 16; };
     auto p_row = [&](const Place& w) { return sbase + kOffP + w.u * 128; };
-    auto max_at = [&](int u) { return sbase + kOffMax + u * 2; };
+    auto max_for = [&](int u) { return sbase + kOffP + u * 128 + (u & 31) * 4; };
     const float sl2 = p.scale_log2;
     // Named barrier of the two warps of 32 rows. Both come to it equally often whatever happens, so it needs no time
     // limit: they agree on whether to go on before every item, and then come to it once per tile and twice at the end.
@@ -868,15 +867,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (by_maximum) {
           // The reference moves to the row's largest score when that is above it by more than 8 (2^8 of headroom), and to
-          // the first tile's in which the row sees a key. Its two threads tell one another theirs (rounded: any value near
-          // will do); the place is free again, since the tile's scores are only there once both were done with the last.
+          // the first tile's in which the row sees a key. Its two threads tell one another theirs as they are: rounded to
+          // 16 bits, a largest score of 8192 could lie 32 below the reference, and all of the row's p below fp16's range.
+          // Either writes it into the other's row of P, a word to a lane, which the other reads before it writes P there:
+          // the row's last product is complete once the tile's scores are there, and its threads have met since they last
+          // used it (for P, or for the item before).
           const Place wm = place();
-          const __nv_bfloat16 mine = __float2bfloat16_rn(mx);
-          uint16_t others;
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(max_at(wm.u)), "h"(__bfloat16_as_ushort(mine)) : "memory");
+          float others;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(max_for(wm.u ^ 128)), "f"(mx) : "memory");
           pair_sync(wm);
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(others) : "r"(max_at(wm.u ^ 128)) : "memory");
-          const float to = fmaxf(__bfloat162float(mine), __bfloat162float(__ushort_as_bfloat16(others)));
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(others) : "r"(max_for(wm.u)) : "memory");
+          const float to = fmaxf(mx, others);
           const bool move = to > (m == -INFINITY ? m : m + 8.f);
           if (__any_sync(0xffffffffu, move)) {
             const float delta = move ? base - to : 0.f;
