@@ -106,8 +106,8 @@ constexpr int kBarItemFree = kBarItemFull + 2;    // +item % 2: everyone has rea
 constexpr int kBarQFree = kBarItemFree + 2;       // an item's last product with Q is complete
 constexpr int kBarOFree = kBarQFree + 1;          // +group: its O has been read
 constexpr int kBarNext = kBarOFree + 2;           // the next item's number has arrived
-constexpr int kBarRows = kBarNext + 1;            // an item's rows have been written
-constexpr int kNumBars = kBarRows + 1;
+constexpr int kBarRows = kBarNext + 1;            // +item % 2: its rows have been written
+constexpr int kNumBars = kBarRows + 2;
 constexpr int kOffNext = kOffBar + (kNumBars * 8 + 15) / 16 * 16;  // where the hardware writes it, 16 bytes
 constexpr int kOffItems = kOffNext + 16;
 
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
       if (i == kBarPReady || i == kBarPReady + 1 || i == kBarOFree || i == kBarOFree + 1) count = kSoftmaxWarps / 2;
-      if (i == kBarDone || i == kBarRows) count = kSoftmaxWarps;
+      if (i == kBarDone || i == kBarRows || i == kBarRows + 1) count = kSoftmaxWarps;
       if (i == kBarItemFree || i == kBarItemFree + 1) count = kSoftmaxWarps + 2;
       mbar_init(bar(i), count);
     }
@@ -685,7 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
       const Item it = items[k & 1];
       if (it.n_tiles < 0) break;
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarRows), k & 1, s_abort, p.err))) break;
+      // one barrier to each of two items: the softmax warps cannot be done with item k + 2 before this warp has let go of
+      // item k, but with k + 1 they can
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarRows + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
       for (int i = 0; i < 8; ++i) {  // of 32 rows
         const volatile uint32_t* masks = s_again + (k & 1) * kSoftmaxWarps + (i >> 2) * 8 + (i & 3);  // of the two halves
         const int first = it.r0 + (i & 3) * 32 + (p.neighbours && i >= 4 ? kBM : 0);
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         s_again[(k & 1) * kSoftmaxWarps + w1.warp()] = again;
-        mbar_arrive(bar(kBarRows));
+        mbar_arrive(bar(kBarRows + (k & 1)));
         mbar_arrive(bar(kBarItemFree + (k & 1)));
       }
     }
