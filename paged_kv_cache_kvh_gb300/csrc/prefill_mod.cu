@@ -119,8 +119,8 @@ struct Item {
 };
 constexpr int kOffAgain = kOffItems + 2 * sizeof(Item);  // [item % 2][32 rows][half] rows to be computed again
 constexpr int kOffSeen = (kOffAgain + 2 * kSoftmaxWarps * 4 + 15) / 16 * 16;  // [warp] the keys that any and that all of its rows see
-constexpr int kOffMisc = kOffSeen + kSoftmaxWarps * 16;  // tmem address, abort flag
-constexpr size_t kSmemBytes = kOffMisc + 8 + 1024;       // + alignment slack
+constexpr int kOffMisc = kOffSeen + kSoftmaxWarps * 16;  // tmem address, abort flag, when rows last were computed again
+constexpr size_t kSmemBytes = kOffMisc + 16 + 1024;      // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
 // tanh x = x (c0 + c1 x^2 + ...), least-maximum fits of tanh(x) / x: for bf16 off by 6.3e-6 of the result for |x| <= 0.4
@@ -180,6 +180,14 @@ struct PrefillModParams {
 
 // Bounded wait that also gives up as soon as another role of the CTA has
 // aborted (so one lost arrival costs one time-out, not one per wait).
+//
+// Rows that are computed again may take longer than the limit (one value that is not finite, before long ranges of keys),
+// and the waits for an item's description, and for the last reader of an older one, wait for them in the end. There
+// (kBehindRows) the limit counts from when those rows last went on, if that is later than the wait's begin.
+__device__ __forceinline__ volatile uint64_t* rows_went_on(volatile int* abort_flag) {
+  return reinterpret_cast<volatile uint64_t*>(abort_flag + 1);
+}
+template <bool kBehindRows = false>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                               unsigned int* err) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -189,11 +197,18 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (kBehindRows) {
+        const uint64_t went_on = *rows_went_on(abort_flag);  // read before the time that it is taken from
+        if (globaltimer_ns() - went_on <= kWaitLimitNs) continue;
+      }
       flag_error(err, PKV_DEVERR_TIMEOUT);
       *abort_flag = 1;
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_for_item(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  return wait_or_abort<true>(bar, parity, abort_flag, err);
 }
 
 // 8-column TMEM load / store (32 lanes x 8 x 32 bit), for the rare O rescale
@@ -272,6 +287,15 @@ __device__ __forceinline__ float size_all(const float (&s)[kCols]) {  // the lar
     b = fmax3(b, fabsf(s[j + 2]), fabsf(s[j + 3]));
   }
   return fmaxf(fmax3(a, fabsf(s[kCols - 2]), fabsf(s[kCols - 1])), b);
+}
+
+// Row r of an item's sequence: its position and the keys it sees. Rows behind the last one take its place.
+__device__ __forceinline__ void seen_from(const PrefillModParams& p, const Item& it, int r, int& pos, int& lo, int& hi) {
+  r = min(r, it.Lq - 1);
+  pos = it.Lk - it.Lq + r;
+  lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  if (p.key_starts) lo = max(lo, p.key_starts[it.cq0 + r]);
+  hi = min(it.Lk, max(pos + 1, p.prefix_lens ? p.prefix_lens[it.b] : 0));
 }
 
 // One (row, query head) by a whole warp from the rows in memory: a key to a lane, then four dims to a lane.
@@ -419,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(i), count);
     }
     *s_abort = 0;
+    *rows_went_on(s_abort) = 0;
     mbar_fence_init();
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -434,14 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  // Row r of an item's sequence: its position and the keys it sees. Rows behind the last one take its place.
-  auto seen_from = [&](const Item& it, int r, int& pos_, int& lo_, int& hi_) {
-    r = min(r, it.Lq - 1);
-    pos_ = it.Lk - it.Lq + r;
-    lo_ = p.window > 0 ? max(0, pos_ - p.window + 1) : 0;
-    if (p.key_starts) lo_ = max(lo_, p.key_starts[it.cq0 + r]);
-    hi_ = min(it.Lk, max(pos_ + 1, p.prefix_lens ? p.prefix_lens[it.b] : 0));
-  };
   // Tile n of an item's: a bias favours the nearest keys: from the last tile to the first, the reference is found in the
   // first one and stays (5000 on 7001: 404 us from the first on, 331 from the last; without a bias 308 and 326).
   constexpr bool kBack = kBias;
@@ -482,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int first_key = INT32_MAX, end_key = 0;
         for (int r = lane; r < (p.key_starts ? rows : 2); r += 32) {
           int pos, lo, hi;  // without first keys of single rows the first and the last row tell
-          seen_from(it, p.key_starts ? it.r0 + r : (r == 0 ? it.r0 : it.r0 + rows - 1), pos, lo, hi);
+          seen_from(p, it, p.key_starts ? it.r0 + r : (r == 0 ? it.r0 : it.r0 + rows - 1), pos, lo, hi);
           if (lo < hi) {
             first_key = min(first_key, lo);
             end_key = max(end_key, hi);
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_tiles = first_key < end_key ? (end_key + kBN - 1) / kBN - first_key / kBN : 1;
         it.tile0 = (first_key < end_key ? first_key / kBN : 0) + (kSplit ? all_tiles * part / parts : 0);
         it.n_tiles = kSplit ? all_tiles * (part + 1) / parts - all_tiles * part / parts : all_tiles;  // 0 at times
-        if (k >= 2) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) - 1) & 1, s_abort, p.err));
+        if (k >= 2) ok = __all_sync(0xffffffffu, wait_for_item(bar(kBarItemFree + (k & 1)), ((k >> 1) - 1) & 1, s_abort, p.err));
         if (!ok) break;
         if (lane == 0) {
           items[k & 1] = it;
@@ -577,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!there) break;
     }
     // no more items
-    if (ok && k >= 2) ok = wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) - 1) & 1, s_abort, p.err);
+    if (ok && k >= 2) ok = wait_for_item(bar(kBarItemFree + (k & 1)), ((k >> 1) - 1) & 1, s_abort, p.err);
     ok = __all_sync(0xffffffffu, ok);
     if (lane == 0) {
       if (ok) {
@@ -623,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ring = 0, t = 0;  // loads and tiles of the items before
       bool ok = true;
       for (int k = 0;; ++k) {
-        if (!(ok = wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
+        if (!(ok = wait_for_item(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
         const Item it = items[k & 1];
         if (it.n_tiles < 0) break;
         had_item = true;
@@ -678,11 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     had_item = __shfl_sync(0xffffffffu, had_item ? 1 : 0, 0) != 0;
   } else if (kSplit && warp < 4) {
-    had_item = __all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull), 0, s_abort, p.err)) && items[0].n_tiles >= 0;
+    had_item = __all_sync(0xffffffffu, wait_for_item(bar(kBarItemFull), 0, s_abort, p.err)) && items[0].n_tiles >= 0;
   } else if (warp == 2) {
     // =========================== rows that are computed again ===========================
     for (int k = 0;; ++k) {
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
+      if (!__all_sync(0xffffffffu, wait_for_item(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
       const Item it = items[k & 1];
       if (it.n_tiles < 0) break;
       // one barrier to each of two items: the softmax warps cannot be done with item k + 2 before this warp has let go of
@@ -692,9 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const volatile uint32_t* masks = s_again + (k & 1) * kSoftmaxWarps + (i >> 2) * 8 + (i & 3);  // of the two halves
         const int first = it.r0 + (i & 3) * 32 + (p.neighbours && i >= 4 ? kBM : 0);
         for (uint32_t again = masks[0] | masks[4]; again; again &= again - 1) {
+          if (lane == 0) *rows_went_on(s_abort) = globaltimer_ns();
           const int r = first + __ffs(again) - 1;
           int pos, lo, hi;
-          seen_from(it, r, pos, lo, hi);
+          seen_from(p, it, r, pos, lo, hi);
           row_again<E>(p, it.b, it.ck0, static_cast<int64_t>(it.cq0) + r, it.head0 + (p.neighbours ? 0 : i >> 2), pos, lo, hi,
                        lane);
         }
@@ -746,14 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t parity = 0;  // of the scores' barrier
     bool ok = true;
     for (int k = 0;; ++k) {
-      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err));
+      if (ok) ok = __all_sync(0xffffffffu, wait_for_item(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err));
       const Place w0 = place();
       ok = pair_agree(w0, ok);
       if (!ok) break;
       const Item& it = items[k & 1];
       if (it.n_tiles < 0) break;
       int pos, lo, hi;
-      seen_from(it, it.r0 + (p.neighbours && w0.g() > 0 ? kBM : 0) + w0.row(), pos, lo, hi);
+      seen_from(p, it, it.r0 + (p.neighbours && w0.g() > 0 ? kBM : 0) + w0.row(), pos, lo, hi);
       // seen by any and by all of the warp's rows
       {
         const int any_lo = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX);
@@ -1035,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t out_row = static_cast<int64_t>(cq0) + seq_row;
           if (__any_sync(0xffffffffu, isnan(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)))))) {
             int row_pos, row_lo, row_hi;
-            seen_from(it, seq_row, row_pos, row_lo, row_hi);
+            seen_from(p, it, seq_row, row_pos, row_lo, row_hi);
             row_again<E>(p, it.b, it.ck0, out_row, to_head, row_pos, row_lo, row_hi, lane);
           } else {
             *(reinterpret_cast<uint2*>(p.out + (out_row * p.hq + to_head) * kHeadDim) + lane) =

@@ -14,7 +14,7 @@ def _source():
 
 def _uses(text, name):
     """(barrier, parity) of the wait for, and the barrier of the arrival at, the one named, as expressions of k."""
-    waits = re.findall(r"wait_or_abort\(bar\((%s[^,]*)\), ([^,]*), s_abort" % name, text)
+    waits = re.findall(r"wait_\w+\(bar\((%s[^,]*)\), ([^,]*), s_abort" % name, text)
     arrivals = re.findall(r"mbar_arrive\(bar\((%s[^;]*)\)\);" % name, text)
     return waits, arrivals
 
