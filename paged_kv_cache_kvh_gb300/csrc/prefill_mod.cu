@@ -39,9 +39,10 @@
 //
 // Values of V at keys that a row does not see are multiplied by p = 0; where they are not finite the sum is spoilt
 // (0 * NaN). The rows of V behind the sequence's end, which may hold anything, are zeroed in shared memory. Elsewhere
-// such values are rare, so they are found in the result: a row whose sum is not finite is computed once more by a
-// warp that has nothing else to do, from the rows in memory, one key to a lane, with the keys that it does not see left
-// out.
+// such values are rare, so they are found in the result: a row whose sum is not finite, and whose visible keys do not
+// account for that, is computed once more by a warp that has nothing else to do, from the rows in memory, one key to a lane,
+// with the keys that it does not see left out (one NaN behind 5000 cached keys, 12,800 rows of 2 heads: 1.1 ms where all
+// rows but a tile's see it, 130 where 254 of one tile do not, 0.3 without it).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -298,29 +299,39 @@ __device__ __forceinline__ void seen_from(const PrefillModParams& p, const Item&
   hi = min(it.Lk, max(pos + 1, p.prefix_lens ? p.prefix_lens[it.b] : 0));
 }
 
-// One (row, query head) by a whole warp from the rows in memory: a key to a lane, then four dims to a lane.
+// The elements of a key's row of K or V, from the first of kv head hk's.
+__device__ __forceinline__ int64_t key_place(const PrefillModParams& p, int b, int64_t k0, int hk, int t) {
+  if (!p.paged) return (k0 + t) * p.kv_stride + hk * kHeadDim;
+  int blk = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + t / kBlockSize];
+  if (blk < 0 || blk >= p.num_blocks) blk = 0;  // reported where the tile was fetched
+  return (static_cast<int64_t>(blk) * kBlockSize + t % kBlockSize) * p.kv_stride + hk * kHeadDim;
+}
+
+// One (row of the item's sequence, query head) by a whole warp from the rows in memory: a key to a lane, then four dims to a
+// lane; eight rows of V on the way (32 keys 3.2 us; one row of V at a time 26).
 template <Elem E>
-__device__ __noinline__ void row_again(const PrefillModParams& p, int b, int64_t k0, int64_t row, int head, int pos,
-                                       int lo, int hi, int lane) {
+__device__ __forceinline__ void row_again(const PrefillModParams& p, const Item& it, int head, int row,
+                                          volatile uint64_t* went_on) {
   using Ops = ElemOps<E>;
-  const int hk = head / p.group;
-  const uint16_t* q = p.q + row * p.q_stride + head * kHeadDim;
+  const int lane = threadIdx.x & 31, hk = head / p.group;
+  const int64_t at = static_cast<int64_t>(it.cq0) + row;
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + at * p.q_stride + head * kHeadDim);
   const float slope = p.slopes ? p.slopes[head] * kLog2e : 0.f;
-  auto key_row = [&](int t) -> int64_t {
-    if (!p.paged) return (k0 + t) * p.kv_stride + hk * kHeadDim;
-    int blk = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + t / kBlockSize];
-    if (blk < 0 || blk >= p.num_blocks) blk = 0;  // reported where the tile was fetched
-    return (static_cast<int64_t>(blk) * kBlockSize + t % kBlockSize) * p.kv_stride + hk * kHeadDim;
-  };
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t0 = lo; t0 < hi; t0 += 32) {
+  int pos, lo, hi;
+  seen_from(p, it, row, pos, lo, hi);
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};  // l: of this lane's keys
+  for (int t0 = lo < hi ? lo & ~31 : hi; t0 < hi; t0 += 32) {
+    if (lane == 0 && (t0 & 1023) == 0) *went_on = globaltimer_ns();
+    const int64_t place = key_place(p, it.b, it.ck0, hk, t0);  // 32 keys lie in one block
     const int t = t0 + lane;
+    const bool seen = t >= lo && t < hi;
     float z = -INFINITY;
-    if (t < hi) {
-      const uint4* kr = reinterpret_cast<const uint4*>(p.k + key_row(t));
+    if (seen) {
+      const uint4* kr = reinterpret_cast<const uint4*>(p.k + place + lane * p.kv_stride);
       float x = 0.f;
+#pragma unroll 4
       for (int i = 0; i < kHeadDim / 8; ++i) {
-        const uint4 a = kr[i], c = reinterpret_cast<const uint4*>(q)[i];
+        const uint4 a = kr[i], c = q[i];
         x = fmaf(Ops::lo(a.x), Ops::lo(c.x), fmaf(Ops::hi(a.x), Ops::hi(c.x), x));
         x = fmaf(Ops::lo(a.y), Ops::lo(c.y), fmaf(Ops::hi(a.y), Ops::hi(c.y), x));
         x = fmaf(Ops::lo(a.z), Ops::lo(c.z), fmaf(Ops::hi(a.z), Ops::hi(c.z), x));
@@ -330,28 +341,138 @@ __device__ __noinline__ void row_again(const PrefillModParams& p, int b, int64_t
       z = fmaf(-slope, fabsf(static_cast<float>(pos - t)), z);
     }
     float top = fmaxf(m, z);
+#pragma unroll
     for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float use = top == -INFINITY ? 0.f : top;
     const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - use);
-    const float e = t < hi ? ex2_approx(z - use) : 0.f;
-    float sum = e;
-    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float e = seen ? ex2_approx(z - use) : 0.f;
     m = top;
-    l = l * alpha + sum;
+    l = l * alpha + e;
+#pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] *= alpha;
-    const int n = min(32, hi - t0);
-    for (int i = 0; i < n; ++i) {
+    const uint16_t* vr = p.v + place + lane * 4;
+    const int end = min(32, hi - t0);  // 0 times what is not finite must not be added: keys that are seen, and no others
+#pragma unroll 8
+    for (int i = max(0, lo - t0); i < end; ++i) {
       const float pi = __shfl_sync(0xffffffffu, e, i);
-      const uint2 x = *(reinterpret_cast<const uint2*>(p.v + key_row(t0 + i)) + lane);
+      const uint2 x = *reinterpret_cast<const uint2*>(vr + i * p.kv_stride);
       acc[0] = fmaf(pi, Ops::lo(x.x), acc[0]);
       acc[1] = fmaf(pi, Ops::hi(x.x), acc[1]);
       acc[2] = fmaf(pi, Ops::lo(x.y), acc[2]);
       acc[3] = fmaf(pi, Ops::hi(x.y), acc[3]);
     }
   }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  *(reinterpret_cast<uint2*>(p.out + (row * p.hq + head) * kHeadDim) + lane) =
+  *(reinterpret_cast<uint2*>(p.out + (at * p.hq + head) * kHeadDim) + lane) =
       make_uint2(Ops::pack(acc[0] * inv, acc[1] * inv), Ops::pack(acc[2] * inv, acc[3] * inv));
+}
+
+// An item's marked rows, [group][half][32 rows]: those whose sums are not finite, though their shares are. That may come
+// from keys that they see, and is right then: NaN where one of these is NaN; infinity where one is infinite, since any key
+// that is not seen would have made it NaN. Such rows' marks are taken off; the others (values that a tile's products took in
+// without being seen, sums beyond fp32) are to be computed again. What is known of the item's values, per dim, four to a
+// lane: the first and the last key with NaN (infinity), and in which of up to 32 stretches of keys there is one.
+template <Elem E>
+__device__ __forceinline__ void settle_marks(const PrefillModParams& p, const Item& it, volatile uint32_t* marks,
+                                             volatile uint64_t* went_on) {
+  constexpr uint32_t kInf = E == Elem::kBF16 ? 0x7f80u : 0x7c00u;
+  constexpr uint32_t kAdd = (0x8000u - kInf) * 0x10001u;  // carries into the sign's place from an exponent of ones
+  const int lane = threadIdx.x & 31, hk = it.head0 / p.group;
+  const int from = it.tile0 * kBN, to = min(it.Lk, from + it.n_tiles * kBN);
+  const int stretch = ((to - from + 511) / 512) * 16;
+  int first[2][4], last[2][4];  // [infinity][dim]
+  uint32_t has[2][4];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    first[d >> 2][d & 3] = INT32_MAX;
+    last[d >> 2][d & 3] = -1;
+    has[d >> 2][d & 3] = 0u;
+  }
+  for (int t0 = from; t0 < to; t0 += 16) {
+    if (lane == 0 && (t0 & 1023) == 0) *went_on = globaltimer_ns();
+    const uint16_t* vr = p.v + key_place(p, it.b, it.ck0, hk, t0) + lane * 4;
+    uint2 x[16];
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      x[j] = t0 + j < to ? *reinterpret_cast<const uint2*>(vr + j * p.kv_stride) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) any |= ((x[j].x & 0x7fff7fffu) + kAdd) | ((x[j].y & 0x7fff7fffu) + kAdd);
+    if (!__any_sync(0xffffffffu, (any & 0x80008000u) != 0)) continue;
+    const uint32_t bit = 1u << ((t0 - from) / stretch);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t size = ((d < 2 ? x[j].x : x[j].y) >> (16 * (d & 1))) & 0x7fffu;
+#pragma unroll
+        for (int inf = 0; inf < 2; ++inf)
+          if (inf ? size == kInf : size > kInf) {
+            first[inf][d] = min(first[inf][d], t0 + j);
+            last[inf][d] = t0 + j;
+            has[inf][d] |= bit;
+          }
+      }
+  }
+  for (int i = 0; i < 8; ++i) {  // of 32 rows
+    const int row0 = it.r0 + (i & 3) * 32 + (p.neighbours && i >= 4 ? kBM : 0);
+    const int head = it.head0 + (p.neighbours ? 0 : i >> 2);
+    volatile uint32_t* halves = marks + (i >> 2) * 8 + (i & 3);
+    uint32_t again = halves[0] | halves[4];
+    for (uint32_t left = again; left; left &= left - 1) {
+      const int r = row0 + __ffs(left) - 1;
+      int pos, lo, hi;
+      seen_from(p, it, r, pos, lo, hi);
+      // stretches that the row sees all of
+      const int a = (max(lo - from, 0) + stretch - 1) / stretch, z = hi >= to ? 32 : (hi - from) / stretch;
+      const uint32_t seen = a < z ? (0xffffffffu << a) & (0xffffffffu >> (32 - z)) : 0u;
+      const uint2 o = *(reinterpret_cast<const uint2*>(p.out + ((static_cast<int64_t>(it.cq0) + r) * p.hq + head) * kHeadDim) +
+                        lane);
+      bool settled = true;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t size = ((d < 2 ? o.x : o.y) >> (16 * (d & 1))) & 0x7fffu;
+#pragma unroll
+        for (int inf = 0; inf < 2; ++inf)
+          if (inf ? size == kInf : size > kInf)
+            settled = settled && ((first[inf][d] >= lo && first[inf][d] < hi) || (last[inf][d] >= lo && last[inf][d] < hi) ||
+                                  (has[inf][d] & seen) != 0);
+      }
+      if (__all_sync(0xffffffffu, settled)) again &= ~(left & -left);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      halves[0] = again;
+      halves[4] = 0;
+    }
+  }
+  __syncwarp();
+}
+
+// What is left of an item's marked rows, by one warp. A function that finds its place in shared memory itself, one row at a
+// time: other forms took registers from the kernel's loop over the tiles (four rows at once 93 instead of 142 ms for 254 rows
+// of 5,100 keys, but any chunk of 5000 on 7001, capped, 367 us instead of 349).
+template <Elem E>
+__device__ __noinline__ void item_again(const PrefillModParams& p, int parity) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const Item& it = reinterpret_cast<const Item*>(smem + kOffItems)[parity];
+  volatile uint32_t* marks = reinterpret_cast<volatile uint32_t*>(smem + kOffAgain) + parity * kSoftmaxWarps;
+  volatile uint64_t* went_on = rows_went_on(reinterpret_cast<volatile int*>(smem + kOffMisc + 4));
+  settle_marks<E>(p, it, marks, went_on);
+  for (int i = 0; i < 8; ++i) {  // of 32 rows
+    const int row0 = it.r0 + (i & 3) * 32 + (p.neighbours && i >= 4 ? kBM : 0);
+    for (uint32_t again = marks[(i >> 2) * 8 + (i & 3)]; again; again &= again - 1)
+      row_again<E>(p, it, it.head0 + (p.neighbours ? 0 : i >> 2), row0 + __ffs(again) - 1, went_on);
+  }
+}
+template <Elem E>
+__device__ __noinline__ void split_row_again(const PrefillModParams& p, const Item& it, int head, int row,
+                                             volatile uint64_t* went_on) {
+  row_again<E>(p, it, head, row, went_on);
 }
 
 // The cluster of CTAs that split the keys of one item (kSplit).
@@ -700,23 +821,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================== rows that are computed again ===========================
     for (int k = 0;; ++k) {
       if (!__all_sync(0xffffffffu, wait_for_item(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
-      const Item it = items[k & 1];
-      if (it.n_tiles < 0) break;
+      if (items[k & 1].n_tiles < 0) break;
       // one barrier to each of two items: the softmax warps cannot be done with item k + 2 before this warp has let go of
       // item k, but with k + 1 they can
       if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarRows + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
-      for (int i = 0; i < 8; ++i) {  // of 32 rows
-        const volatile uint32_t* masks = s_again + (k & 1) * kSoftmaxWarps + (i >> 2) * 8 + (i & 3);  // of the two halves
-        const int first = it.r0 + (i & 3) * 32 + (p.neighbours && i >= 4 ? kBM : 0);
-        for (uint32_t again = masks[0] | masks[4]; again; again &= again - 1) {
-          if (lane == 0) *rows_went_on(s_abort) = globaltimer_ns();
-          const int r = first + __ffs(again) - 1;
-          int pos, lo, hi;
-          seen_from(p, it, r, pos, lo, hi);
-          row_again<E>(p, it.b, it.ck0, static_cast<int64_t>(it.cq0) + r, it.head0 + (p.neighbours ? 0 : i >> 2), pos, lo, hi,
-                       lane);
-        }
-      }
+      if (__any_sync(0xffffffffu, s_again[(k & 1) * kSoftmaxWarps + (lane & (kSoftmaxWarps - 1))] != 0)) item_again<E>(p, k & 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarItemFree + (k & 1)));
     }
@@ -1012,6 +1121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           L = fmaf(ex2_approx(v.x - M), v.y, L);
         }
         const float inv = ex2_approx(ref - M) * (L == 0.f ? 0.f : 1.f / L);
+        const uint32_t sums = ml + 2 * kBM * 8;  // for this CTA's own rows
+        if (half == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + ri * 4), "f"(L) : "memory");
         const uint32_t dst = in_part(sbase + kOffQ + (part * rows_own + ri % rows_own) * 512, ri / rows_own);
         tc_fence_after();
 #pragma unroll
@@ -1051,10 +1162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             o.w += v.w;
           }
           const int64_t out_row = static_cast<int64_t>(cq0) + seq_row;
-          if (__any_sync(0xffffffffu, isnan(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)))))) {
-            int row_pos, row_lo, row_hi;
-            seen_from(p, it, seq_row, row_pos, row_lo, row_hi);
-            row_again<E>(p, it.b, it.ck0, out_row, to_head, row_pos, row_lo, row_hi, lane);
+          float sum;  // NaN where a score is: so is the row, then
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sum) : "r"(sums + r2 * 4) : "memory");
+          if (!isnan(sum) && __any_sync(0xffffffffu, isnan(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)))))) {
+            split_row_again<E>(p, it, to_head, seq_row, rows_went_on(s_abort));
           } else {
             *(reinterpret_cast<uint2*>(p.out + (out_row * p.hq + to_head) * kHeadDim) + lane) =
                 make_uint2(Ops::pack(o.x, o.y), Ops::pack(o.z, o.w));
@@ -1092,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    Ops::pack(x[4] * inv, x[5] * inv), Ops::pack(x[6] * inv, x[7] * inv));
           }
         }
-        again = __ballot_sync(0xffffffffu, isnan(spoilt) && row0 + lane < Lq);
+        again = __ballot_sync(0xffffffffu, isnan(spoilt) && !isnan(inv) && row0 + lane < Lq);
       }
       tc_fence_before();
       __syncwarp();
