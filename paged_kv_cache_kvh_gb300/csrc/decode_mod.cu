@@ -407,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
+    // A worker whose wait runs out leaves before it can say what goes on behind its range: nothing, then.
+    const bool tells = !by_cta && stream == 0 && lane == 0;
+    if (tells) p.info[range].seq = -1;
     Walk now = begin;
     int64_t first_unit = begin_first;  // of the sequence under way
     int64_t left = end - start;
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       left -= n;
       if (left == 0) {
-        if (!by_cta && stream == 0 && lane == 0) {
+        if (tells) {
           const int64_t last_unit = first_unit + (now.last - now.seen.x / kUnit);
           RangeInfo info;
           info.seq = begins && !ends ? now.b : -1;
@@ -731,6 +734,12 @@ __device__ __forceinline__ void join(const DecodeModParams& p, int range, int pl
   }
 }
 
+// Whether {seq, last, place} can be what a range's worker has left: workspaces need no initialisation, so nothing else is
+// followed, not even where a wait that ran out has kept a worker from writing it.
+__device__ __forceinline__ bool fits(const DecodeModParams& p, int range, int seq, int last, int place) {
+  return seq >= 0 && seq < p.num_seqs && last >= range && last < p.used_ranges && place >= 0 && place <= 1;
+}
+
 // A block joins what one query head of the sequences left that begin in its kMergeWarps ranges and go on behind them:
 // a warp each those of few pieces, all warps together those of many.
 template <Elem E>
@@ -748,7 +757,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_mod_merge_kernel(cons
   float4 o;
   const int ranges = p.used_ranges;
   if (first + warp < ranges) {
-    const int4 info = *reinterpret_cast<const int4*>(p.info + first + warp);  // {seq, last, place}
+    int4 info = *reinterpret_cast<const int4*>(p.info + first + warp);  // {seq, last, place}
+    if (!fits(p, first + warp, info.x, info.y, info.z)) info.x = -1;
     s_info[warp][0] = info.x;
     s_info[warp][1] = info.y;
     s_info[warp][2] = info.z;
