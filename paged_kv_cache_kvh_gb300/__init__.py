@@ -690,9 +690,13 @@ def pkv_build_decode_metadata(num_tokens, block_tables, num_blocks, stream=None)
 
 # ---- rotary positions ----------------------------------------------------------------
 
+def _empty_on_cuda(shape, strides, dtype):
+    return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
 # Outputs on the current device and stream without the dispatcher and its device guard: 2 us less a call, and the launch
-# behind it is cheaper too.
-_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+# behind it is cheaper too. The name is not one that every torch has to offer.
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", _empty_on_cuda)
 
 ROPE_SCALINGS = ("none", "linear", "ntk", "bands", "yarn")  # the PKV_ROPE_* codes in order
 
