@@ -552,14 +552,20 @@ int pkv_rope_store_kvcache_f16(const void* q, int64_t q_row_stride, const void* 
  * position t, in this order:
  *   x = softmax_scale * q . k
  *   x = softcap * tanh(x / softcap)          where softcap > 0 (0: no cap)
- *   x = x - slopes[head] * |p - t|           where slopes != NULL ([num_heads] fp32, any values)
+ *   x = x - slopes[head] * |p - t|           where slopes != NULL ([num_heads] fp32, any finite values)
  * and the key takes part where all of these hold:
  *   t <= p, or t < prefix_lens[sequence]     (prefill, where prefix_lens != NULL: keys that every row sees)
  *   t < length of the sequence
  *   t >= key_starts[row]                     where key_starts != NULL (the first position of the row's document, say)
  *   p - t < window                           where window > 0
- * A row that sees no key gets zeros. Values at keys that take no part, infinities
- * and NaN among them, reach no result. Arithmetic is fp32; products take the 16-bit rows as they are.
+ * A key's position t is its place in the sequence: the place in its blocks, over the cache. After pkv_evict_kvcache,
+ * which moves tokens up, each head for itself, that is no longer the token's position in the text: window, slopes,
+ * key_starts and prefix_lens then count places in the cache, and a model that means positions cannot use them there. Scale
+ * and cap take no positions, and rotary ones stay in the rows.
+ *
+ * A row that sees no key gets zeros. Values at keys that take no part, infinities and NaN among them, reach no result
+ * (but for the choice between two forms of tanh in the prefill, see there). Products take the 16-bit rows as they are and
+ * add up in fp32; scores, maxima, sums and the decode's shares are fp32.
  */
 
 /*
@@ -603,7 +609,11 @@ size_t pkv_decode_mod_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32
  *                which the row's document starts
  *   prefix_lens  [num_seqs] int32, or NULL: keys at positions below are seen by every row, also by rows before them
  * There is no tile plan. Rows of q and out that belong to no sequence are left as they were. A NaN or an infinity in V
- * reaches the rows that its key takes part in, and no others.
+ * reaches the rows that its key takes part in, and no others; rows of a tile beside it that do not see it are computed
+ * one by one, at some 0.1 us for each key that they see.
+ * The shares of keys are rounded to the rows' 16 bits for the product with V (half a step of each). tanh is a polynomial
+ * off by at most 7e-6 of a score for bf16 rows and 6e-7 for fp16, or, where a tile holds scores beyond the cap, taken from
+ * the exponential: keys of the tile that take no part have a say in that, so they may change a result by as much.
  */
 int pkv_prefill_varlen_mod(const void* q, int64_t q_row_stride, int32_t total_q, const void* k, const void* v,
                            int64_t kv_row_stride, int32_t total_k, const void* k_cache, const void* v_cache,
@@ -630,7 +640,8 @@ int pkv_prefill_varlen_mod_f16(const void* q, int64_t q_row_stride, int32_t tota
  * every token of a sequence; this call has no counterpart there. Kept tokens keep
  * their order and move up: token kept[b][h][j] of head h becomes token j, its K and V
  * rows and its weight with it. Each head chooses for itself, so a slot may then hold
- * different tokens of different heads. Shorter sequences keep all their tokens.
+ * different tokens of different heads, and what counts positions in the attention calls above counts places from then
+ * on. Shorter sequences keep all their tokens.
  *   k_cache, v_cache  [num_blocks, 256, num_kv_heads, 128], 16-bit elements of either type, 16-byte aligned
  *   weights           fp32 [num_blocks, num_kv_heads, 256]; a NaN counts as larger than any number
  *   max_context_len   upper bound on context_lens[b] (<= 2^24)

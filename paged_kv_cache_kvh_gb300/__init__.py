@@ -924,7 +924,8 @@ def pkv_decode_mod(q, k_cache, v_cache, block_tables, context_lens, max_context_
                    softcap=0.0, slopes=None, window=0, key_starts=None, weights=None, out=None, stream=None):
     """pkv_decode with modified scores and masks, for any head counts (caches [blocks, 256, num_kv_heads, 128]): scores
     softcap * tanh(x / softcap) if softcap, then - slopes[head] * (p - t) for slopes fp32 [num_heads]; keys from
-    key_starts[b] (int32 [B]) on and, if window, the newest `window` of them. weights (attention_weights): each key's
+    key_starts[b] (int32 [B]) on and, if window, the newest `window` of them. Positions are places in the cache, which after
+    pkv_evict_kvcache are not those in the text: softcap alone holds there. weights (attention_weights): each key's
     probability is added up there. workspace: decode_mod_workspace. Returns out [B, num_heads, 128]."""
     return _decode_mod(_lib.pkv_decode_mod, torch.bfloat16, q, k_cache, v_cache, block_tables, context_lens,
                        max_context_len, softmax_scale, workspace, softcap, slopes, window, key_starts, weights, out,
@@ -1008,7 +1009,8 @@ def pkv_evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, max
                       recent=0, new_block_tables=None, kept=None, new_context_lens=None, stream=None):
     """Cuts each sequence of more than `budget` tokens down to it: per kv head the first `first`, the newest `recent` and
     of the others those with the largest weights (attention_weights, added up by pkv_decode_mod) stay, in order. Rows and
-    weights go to the blocks of new_block_tables [B, width], or, without, move up within the sequence's own blocks.
+    weights go to the blocks of new_block_tables [B, width], or, without, move up within the sequence's own blocks; window,
+    slopes, key_starts and prefix_lens of the attention calls count the new places from then on.
     Caches of either 16-bit type. Returns (kept int32 [B, num_kv_heads, budget]: old positions, -1 behind the last;
     new_context_lens int32 [B])."""
     dev = _current_device()
