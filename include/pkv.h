@@ -651,7 +651,7 @@ int pkv_prefill_varlen_mod_f16(const void* q, int64_t q_row_stride, int32_t tota
  *                     tokens. NULL: in place, within the sequence's own blocks, which no other sequence may share then.
  *                     Blocks behind the new length are free afterwards.
  *   kept              int32 [num_seqs, num_kv_heads, budget] out: old positions in rising order, -1 behind the last
- *   new_context_lens  int32 [num_seqs] out, min(context_lens[b], budget); not context_lens itself
+ *   new_context_lens  int32 [num_seqs] out, min(context_lens[b], budget); must not overlap context_lens (PKV_ERR_BAD_SIZE)
  * 1 <= budget <= 2^24, first + recent <= budget. Slots behind the new length are left as they were. Bad lengths
  * (taken as 0) and blocks (their tokens are not moved) set PKV_DEVERR_BAD_SEQLEN and PKV_DEVERR_BAD_BLOCK.
  */

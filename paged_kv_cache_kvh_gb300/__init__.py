@@ -1041,8 +1041,8 @@ def pkv_evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, max
             if t.shape != shape:
                 raise ValueError(f"{name} must be {shape}")
         made.append(t)
-    if made[1].data_ptr() == context_lens.data_ptr() and B > 0:
-        raise ValueError("new_context_lens must not be context_lens")
+    if abs(made[1].data_ptr() - context_lens.data_ptr()) < 4 * B:
+        raise ValueError("new_context_lens must not overlap context_lens")
     status = _lib.pkv_evict_kvcache(
         k_cache.data_ptr(), v_cache.data_ptr(), weights_at, blocks, block_tables.data_ptr(), tables[1],
         context_lens.data_ptr(), B, hkv, HEAD_DIM, BLOCK_SIZE, int(max_context_len), budget, int(first), int(recent),

@@ -499,6 +499,9 @@ extern "C" int pkv_evict_kvcache(void* k_cache, void* v_cache, float* weights, i
                         static_cast<const void*>(context_lens), static_cast<const void*>(new_block_tables),
                         static_cast<const void*>(kept), static_cast<const void*>(new_context_lens)})
     if (!pkv::aligned(p, 4)) return PKV_ERR_ALIGNMENT;
+  // the new lengths are written while the old ones are still read
+  const intptr_t apart = reinterpret_cast<intptr_t>(new_context_lens) - reinterpret_cast<intptr_t>(context_lens);
+  if (apart < 4 * static_cast<intptr_t>(num_seqs) && -apart < 4 * static_cast<intptr_t>(num_seqs)) return PKV_ERR_BAD_SIZE;
   unsigned int* err = nullptr;
   const int st = pkv::device_error_word(&err);
   if (st != PKV_OK) return st;

@@ -59,3 +59,20 @@ def test_places_count_after_an_eviction(pkv, kind, dtype):
         room = eps * ref.abs() + bound + 2.0 ** -25
     assert bool(((out.double() - ref).abs() <= room).all())
     assert pkv.pkv_device_error() == 0
+
+
+def test_lengths_side_by_side_and_overlapping(pkv):
+    hkv, n = 2, 400
+    kc, vc = (torch.randn((6, BS, hkv, D), device="cuda").to(torch.bfloat16) for _ in range(2))
+    weights = pkv.attention_weights(6, hkv)
+    tables = torch.tensor([[0, 1], [2, 3], [4, 5]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n, n - 1, 7, 0, 0, 0], dtype=torch.int32, device="cuda")
+    before = kc.clone()
+    for at in (0, 1, 2):
+        with pytest.raises(ValueError):
+            pkv.pkv_evict_kvcache(kc, vc, weights, tables, lens[:3], n, 100, new_context_lens=lens[at:at + 3])
+    with pytest.raises(ValueError):
+        pkv.pkv_evict_kvcache(kc, vc, weights, tables, lens[2:5], n, 100, new_context_lens=lens[:3])
+    assert torch.equal(kc, before) and lens.tolist() == [n, n - 1, 7, 0, 0, 0]
+    pkv.pkv_evict_kvcache(kc, vc, weights, tables, lens[:3], n, 100, new_context_lens=lens[3:])
+    assert lens.tolist() == [n, n - 1, 7, 100, 100, 7] and pkv.pkv_device_error() == 0
