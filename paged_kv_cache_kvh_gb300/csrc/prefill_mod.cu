@@ -18,11 +18,11 @@
 // A CTA goes from item to item, taking the next from the launch's CTAs that have not begun (cluster launch control) when
 // the last loads of its item are under way: whoever is done first gets the longest of what is left, and the next item's
 // queries, keys and first products run under the last tile and the end of this one (16 k rows of 100..1024-token prompts
-// with a cap and a window 77 us with a CTA to an item, 69 now; 5000 on 7001 without a cap 311 and 322, see Place).
+// with a cap and a window 77 us with a CTA to an item, 68 now; 5000 on 7001 without a cap 311 and 322, see Place).
 //
 // What bounds it: a key tile of both groups takes about 2 us, its products 1.1 of that; the rest is the chain of each
-// group (product, softmax, barrier, product) with two groups to overlap: the tensor pipe is 53 % in use and the issue
-// slots 48 %. 16 on 8 heads, 5000 on 7001 in the cache: 351 us capped at 50 and 322 without a cap, of 207 at
+// group (product, softmax, barrier, product) with two groups to overlap: the tensor pipe is 54 % in use and the issue
+// slots 49 %. 16 on 8 heads, 5000 on 7001 in the cache: 350 us capped at 50 and 322 without a cap, of 207 at
 // cuBLAS' rate (0.59 and 0.64 of it). Measured and not kept: 384 threads with registers shared out by role (427 us where
 // 404 was), scores fetched a tile ahead (430: three slots of the ring are too few for it).
 //
@@ -120,7 +120,7 @@ struct Item {
 };
 constexpr int kOffAgain = kOffItems + 2 * sizeof(Item);  // [item % 2][32 rows][half] rows to be computed again
 constexpr int kOffSeen = (kOffAgain + 2 * kSoftmaxWarps * 4 + 15) / 16 * 16;  // [warp] the keys that any and that all of its rows see
-constexpr int kOffMisc = kOffSeen + kSoftmaxWarps * 16;  // tmem address, abort flag, when rows last were computed again
+constexpr int kOffMisc = kOffSeen + kSoftmaxWarps * 16;  // tmem address, abort flag, when rows were last computed again
 constexpr size_t kSmemBytes = kOffMisc + 16 + 1024;      // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory above the 227 KB a CTA can opt into");
 
@@ -428,8 +428,8 @@ __device__ __forceinline__ void settle_marks(const PrefillModParams& p, const It
       // stretches that the row sees all of
       const int a = (max(lo - from, 0) + stretch - 1) / stretch, z = hi >= to ? 32 : (hi - from) / stretch;
       const uint32_t seen = a < z ? (0xffffffffu << a) & (0xffffffffu >> (32 - z)) : 0u;
-      const uint2 o = *(reinterpret_cast<const uint2*>(p.out + ((static_cast<int64_t>(it.cq0) + r) * p.hq + head) * kHeadDim) +
-                        lane);
+      const int64_t at = (static_cast<int64_t>(it.cq0) + r) * p.hq + head;
+      const uint2 o = *(reinterpret_cast<const uint2*>(p.out + at * kHeadDim) + lane);
       bool settled = true;
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
@@ -825,7 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one barrier to each of two items: the softmax warps cannot be done with item k + 2 before this warp has let go of
       // item k, but with k + 1 they can
       if (!__all_sync(0xffffffffu, wait_or_abort(bar(kBarRows + (k & 1)), (k >> 1) & 1, s_abort, p.err))) break;
-      if (__any_sync(0xffffffffu, s_again[(k & 1) * kSoftmaxWarps + (lane & (kSoftmaxWarps - 1))] != 0)) item_again<E>(p, k & 1);
+      if (__any_sync(0xffffffffu, s_again[(k & 1) * kSoftmaxWarps + (lane & (kSoftmaxWarps - 1))] != 0))
+        item_again<E>(p, k & 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarItemFree + (k & 1)));
     }

@@ -14,8 +14,9 @@
 // r/2 cosines and sines once, for all heads, into shared memory while their first rows are on the way; then a thread
 // moves 32 bytes at a time (eight pairs). The fused form writes turned keys and values to their slots, which saves the
 // keys' way through memory (2 x 2 KB of the 16 KB a token of 16 heads on 8 costs in two calls) and a launch. Measured:
-// 15 k tokens of 16 heads on 8 25.9 us, with the store 35.1 (6.0 and 5.9 TB/s, 0.87 to 0.89 of a plain copy's rate);
-// 5 tokens take 2.0 us, 256 with the store 2.6, on the device; their calls from Python 11.6 and 14.9.
+// 15 k tokens of 16 heads on 8 29.1 us, with the store 37.0 (0.79 and 0.83 of a plain copy's rate) with the L2 full of other
+// data, 25.9 and 35.1 again and again on the same rows, of which a part is in the L2 then; 5 tokens take 2.0 us, 256 with
+// the store 2.6, on the device; their calls from Python 11.6 and 14.9.
 #include <cmath>
 #include <type_traits>
 
