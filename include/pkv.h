@@ -564,8 +564,10 @@ int pkv_rope_store_kvcache_f16(const void* q, int64_t q_row_stride, const void* 
  * and cap take no positions, and rotary ones stay in the rows.
  *
  * A row that sees no key gets zeros. Values at keys that take no part, infinities and NaN among them, reach no result
- * (but for the choice between two forms of tanh in the prefill, see there). Products take the 16-bit rows as they are and
- * add up in fp32; scores, maxima, sums and the decode's shares are fp32.
+ * (but for the choice between two forms of tanh in the prefill, see there); in V of keys that take part they come out as
+ * the sums have them. Products take the 16-bit rows as they are and add up in fp32; scores, maxima and sums are fp32. For
+ * the product with V shares are rounded to the rows' 16 bits, in the decode with what that lost as a second 16-bit number;
+ * of fp16 rows shares below 2^-25 of the row's largest are lost.
  */
 
 /*
@@ -611,9 +613,9 @@ size_t pkv_decode_mod_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32
  * There is no tile plan. Rows of q and out that belong to no sequence are left as they were. A NaN or an infinity in V
  * reaches the rows that its key takes part in, and no others; rows of a tile beside it that do not see it are computed
  * one by one, at some 0.1 us for each key that they see.
- * The shares of keys are rounded to the rows' 16 bits for the product with V (half a step of each). tanh is a polynomial
- * off by at most 7e-6 of a score for bf16 rows and 6e-7 for fp16, or, where a tile holds scores beyond the cap, taken from
- * the exponential: keys of the tile that take no part have a say in that, so they may change a result by as much.
+ * tanh is a polynomial off by at most 7e-6 of a score for bf16 rows and 6e-7 for fp16, or, where a tile holds scores
+ * beyond the cap, taken from the exponential: keys of the tile that take no part have a say in that, so they may change a
+ * result by as much.
  */
 int pkv_prefill_varlen_mod(const void* q, int64_t q_row_stride, int32_t total_q, const void* k, const void* v,
                            int64_t kv_row_stride, int32_t total_k, const void* k_cache, const void* v_cache,

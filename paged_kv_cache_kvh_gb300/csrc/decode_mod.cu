@@ -142,6 +142,7 @@ Layout layout_of(const Streams& s, int32_t num_seqs, int32_t hq, int32_t max_ctx
 struct DecodeModParams {
   const uint16_t* q;
   int64_t q_row_stride;
+  const uint16_t* v;  // the cache once more, for values that are not finite
   const int32_t* block_tables;
   int32_t bt_stride, num_blocks;
   const int32_t* context_lens;
@@ -253,6 +254,42 @@ __device__ __forceinline__ void write_joined(const DecodeModParams& p, int seq, 
   *(reinterpret_cast<uint2*>(p.out + row * kHeadDim) + lane) =
       make_uint2(Ops::pack(o.x * inv, o.y * inv), Ops::pack(o.z * inv, o.w * inv));
   if (p.weights && lane == 0) p.final_ml[row] = make_float2(M, inv);
+}
+
+// Which of a lane's 16 dims (2 i: 16 i + lane / 4, 2 i + 1: 8 more) hold +infinity (bits 0 to 15 of the result), -infinity
+// (16 to 31) and NaN (32 to 47) among the values of tokens from..to - 1 of sequence b.
+template <Elem E>
+__device__ __noinline__ uint64_t odd_values(const DecodeModParams& p, int b, int hk, int from, int to) {
+  constexpr uint32_t kInf = E == Elem::kBF16 ? 0x7f80u : 0x7c00u;
+  const int lane = threadIdx.x & 31;
+  uint32_t odd = 0;  // of dims 4 lane .. 4 lane + 3: bits 0 to 3, 4 to 7 and 8 to 11
+  for (int t0 = from & ~15; t0 < to; t0 += 16) {
+    int block = p.block_tables[static_cast<int64_t>(b) * p.bt_stride + t0 / kBlockSize];
+    if (block < 0 || block >= p.num_blocks) block = 0;  // reported where it was fetched
+    const int64_t row = (static_cast<int64_t>(block) * kBlockSize + t0 % kBlockSize) * p.hkv + hk;
+    const uint16_t* rows = p.v + row * kHeadDim + 4 * lane;
+    uint2 x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      x[j] = t0 + j >= from && t0 + j < to
+                 ? *reinterpret_cast<const uint2*>(rows + static_cast<int64_t>(j) * p.hkv * kHeadDim) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t e = ((d < 2 ? x[j].x : x[j].y) >> (16 * (d & 1))) & 0xffffu, size = e & 0x7fffu;
+        if (size >= kInf) odd |= 1u << (d + (size > kInf ? 8 : (e >> 15 ? 4 : 0)));
+      }
+  }
+  uint64_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int dim = 8 * i + lane / 4;
+    const uint32_t there = __shfl_sync(0xffffffffu, odd, dim >> 2) >> (dim & 3);
+    mine |= static_cast<uint64_t>(there & 1u) << i | static_cast<uint64_t>((there >> 4) & 1u) << (16 + i) |
+            static_cast<uint64_t>((there >> 8) & 1u) << (32 + i);
+  }
+  return mine;
 }
 
 // NT: eights of query heads that a worker takes.
@@ -557,6 +594,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         stage = stage + 1 == kStages ? 0 : stage + 1;
       }
       if (!ok) break;
+
+      // A value that is infinite makes NaN with the second part of p, which may be 0 or of the other sign. Where a sum is
+      // NaN the values are looked through: those of one infinity alone make that.
+      {
+        float spoilt = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) spoilt = fmaf(acc[t][i][j], 0.f, spoilt);
+        if (__any_sync(0xffffffffu, isnan(spoilt))) {
+          const uint64_t odd = odd_values<E>(p, now.b, hk, max(seq_first * kUnit, now.seen.x),
+                                             min((seq_first + n) * kUnit, now.seen.y));
+          const uint32_t nan = static_cast<uint32_t>(odd >> 32), up = static_cast<uint32_t>(odd) & 0xffffu;
+          const uint32_t down = static_cast<uint32_t>(odd) >> 16;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t bit = 1u << (2 * i + (j >> 1));
+                if (isnan(acc[t][i][j]) && !(nan & bit) && ((up ^ down) & bit))
+                  acc[t][i][j] = up & bit ? INFINITY : -INFINITY;
+              }
+        }
+      }
 
       // ---- the end of a sequence, or of the range inside one ----
 #pragma unroll
@@ -939,6 +1004,7 @@ cudaError_t launch_decode_mod(const DecodeModArgs& a, unsigned int* err, cudaStr
   DecodeModParams p{};
   p.q = static_cast<const uint16_t*>(a.q);
   p.q_row_stride = a.q_row_stride;
+  p.v = static_cast<const uint16_t*>(a.v_cache);
   p.block_tables = a.block_tables;
   p.bt_stride = a.bt_stride;
   p.num_blocks = a.num_blocks;
