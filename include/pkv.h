@@ -567,7 +567,7 @@ int pkv_rope_store_kvcache_f16(const void* q, int64_t q_row_stride, const void* 
  * (but for the choice between two forms of tanh in the prefill, see there); in V of keys that take part they come out as
  * the sums have them. Products take the 16-bit rows as they are and add up in fp32; scores, maxima and sums are fp32. For
  * the product with V shares are rounded to the rows' 16 bits, in the decode with what that lost as a second 16-bit number;
- * of fp16 rows shares below 2^-25 of the row's largest are lost.
+ * of fp16 rows shares below 2^-32 of the row's largest are lost.
  */
 
 /*

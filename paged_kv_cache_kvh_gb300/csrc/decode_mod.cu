@@ -81,6 +81,10 @@ constexpr int kPieces = 2 * kWarps;
 constexpr size_t kSmemBytes = kOffPieces + kPieces * sizeof(Piece) + 1024;  // + alignment slack
 constexpr int kMergeWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+// A row's largest share before it is divided by their sum, log2: fp16 shares go down to 2^-24 in steps of as much, two parts
+// together too, so this much more of the small ones is kept (and 2^7 with 2^8 of headroom stays below fp16's largest number).
+template <Elem E>
+constexpr float kLift = E == Elem::kF16 ? 7.f : 0.f;
 constexpr float kNoCap = 1e30f;  // from here on a cap changes no score that fp32 tells from its neighbours below 1e26
 
 // How a call's heads are cut into streams: parts of up to 8 or 16 query heads of one kv head.
@@ -531,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int token = token0 + r + (j >> 1) * 8;
             if (p.slopes) z[t][j] = fmaf(-slope[t][j & 1], static_cast<float>(now.seen.y - 1 - token), z[t][j]);
             if (edge && (token < now.seen.x || token >= now.seen.y)) z[t][j] = -INFINITY;
-            rise = rise || z[t][j] > m[t][j & 1] + 8.f;
+            rise = rise || z[t][j] > m[t][j & 1] + (8.f + kLift<E>);
           }
         if (p.weights) {
           float* to = p.scores + ((now.b * p.seq_units + (seq_first + u)) * p.st.count + stream) * (p.st.heads * kUnit);
@@ -548,9 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(fmaxf(z[t][j], z[t][j + 2]), m[t][j]);
+              float top = fmaxf(z[t][j], z[t][j + 2]);
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              top = fmaxf(top - kLift<E>, m[t][j]);
               const float alpha = m[t][j] == -INFINITY ? 0.f : ex2_approx(m[t][j] - top);
               m[t][j] = top;
               l[t][j] *= alpha;

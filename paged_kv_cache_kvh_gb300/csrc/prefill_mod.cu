@@ -146,6 +146,10 @@ struct TanhFit<Elem::kF16> {
                                       -0.051605653809187996, 0.016743090747062123, -0.0030670504021806768};
 };
 constexpr float kNoCap = 1e30f;     // from here on a cap changes no score that fp32 tells from its neighbours below 1e26
+// A row's largest share before it is divided by their sum, log2: fp16 shares go down to 2^-24 in steps of as much, so those
+// from 2^-21 of the largest on keep 11 bits (and 2^7 with 2^8 of headroom stays below fp16's largest number).
+template <Elem E>
+constexpr float kLift = E == Elem::kF16 ? 7.f : 0.f;
 constexpr float kFixedCap = 52.f;  // bf16: scores capped here and below need no running maximum
 
 struct PrefillModParams {
@@ -895,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int min_pos = __reduce_min_sync(0xffffffffu, pos);
       const float slope = kBias ? p.slopes[it.head0 + (p.neighbours ? 0 : w0.g())] * kLog2e : 0.f;
-      float m = -INFINITY;  // the row's reference, log2 units; within 8 of its running maximum from below, or fixed at 0
+      float m = -INFINITY;  // the row's reference, log2 units; within 8 (and kLift) of its running maximum from below, or 0
       float l = 0.f;        // of this thread's keys
       constexpr int kStep = kBack ? -kBN : kBN;
       int key0 = first_key_of(it, 0) + w0.half() * kCols - kStep;
@@ -996,8 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (by_maximum) mx = max_all(s) + base;
         }
         if (by_maximum) {
-          // The reference moves to the row's largest score when that is above it by more than 8 (2^8 of headroom), and to
-          // the first tile's in which the row sees a key. Its two threads tell one another theirs as they are: rounded to
+          // The reference moves to the row's largest score (less kLift) when that is above it by more than 8 (2^8 of
+          // headroom), and to the first tile's in which the row sees a key. Its two threads tell one another theirs as they are: rounded to
           // 16 bits, a largest score of 8192 could lie 32 below the reference, and all of the row's p below fp16's range.
           // Either writes it into the other's row of P, a word to a lane, which the other reads before it writes P there:
           // the row's last product is complete once the tile's scores are there, and its threads have met since they last
@@ -1007,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(max_for(wm.u ^ 128)), "f"(mx) : "memory");
           pair_sync(wm);
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(others) : "r"(max_for(wm.u)) : "memory");
-          const float to = fmaxf(mx, others);
+          const float to = fmaxf(mx, others) - kLift<E>;
           const bool move = to > (m == -INFINITY ? m : m + 8.f);
           if (__any_sync(0xffffffffu, move)) {
             const float delta = move ? base - to : 0.f;

@@ -73,3 +73,26 @@ def test_what_is_not_finite(pkv, dtype, lens, hq, hkv, mods):
             largest = float(torch.where(torch.isfinite(v), v, torch.zeros_like(v)).double().abs().max())
             # the result's rounding, and 2^-15 of sum p |v|: p in two parts, scores of a few units in 32 bits
             assert bool(((got - ref).abs() <= eps * ref.abs() + 2.0 ** -15 * largest)[fine].all())
+
+
+@pytest.mark.parametrize("gap", [9.0, 12.0, 14.0])
+@pytest.mark.parametrize("hq,hkv,n", [(16, 8, 700), (12, 1, 5000), (2, 1, 40)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_shares_far_below_the_largest(pkv, dtype, hq, hkv, n, gap):
+    """A first key that takes nearly all of the weight and whose value is nothing: the result is the others' small shares."""
+    g = torch.Generator().manual_seed(3)
+    blocks = -(-n // BS)
+    q, kc, vc = torch.zeros((1, hq, D)), torch.zeros((blocks, BS, hkv, D)), torch.rand((blocks, BS, hkv, D), generator=g) + 0.5
+    q[..., 0] = 1.0
+    kc[..., 0] = torch.randint(0, 3, (blocks, BS, hkv), generator=g) / 4.0
+    kc[0, 0, :, 0] = gap
+    vc[0, 0] = 0
+    q, kc, vc = (x.to(dtype).cuda() for x in (q, kc, vc))
+    call = pkv.pkv_decode_mod_f16 if dtype == torch.float16 else pkv.pkv_decode_mod
+    out = call(q, kc, vc, torch.arange(blocks, dtype=torch.int32, device="cuda")[None],
+               torch.tensor([n], dtype=torch.int32, device="cuda"), n, 1.0, pkv.decode_mod_workspace(1, n, hq, hkv))
+    k, v = (c.flatten(0, 1)[:n].cpu() for c in (kc, vc))
+    ref = _by_definition(q[0].cpu(), k.double() * D ** 0.5, v, 0, 0, 0.0)
+    # the result's rounding; p in two parts (2^-15), scores of 14 units in 32 bits (2^-18)
+    room = ref.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -14) + 2.0 ** -25
+    assert bool(((out[0].double().cpu() - ref).abs() <= room).all())

@@ -131,3 +131,23 @@ def test_bias_far_from_the_keys(pkv, dtype, cached):
         err = (out[a:a + 16].double() - ref).abs()
         assert bool((err <= room).all()), float((err / room).max())
     assert pkv.pkv_device_error() == 0
+
+
+@pytest.mark.parametrize("cached,new,hq,hkv", [(300, 150, 4, 2), (0, 300, 3, 1), (3000, 100, 4, 2)])
+@pytest.mark.parametrize("gap", [9.0, 12.0, 14.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_shares_far_below_the_largest(pkv, dtype, gap, cached, new, hq, hkv):
+    """A first key that takes nearly all of the weight and has nothing to say: the result is the others' small shares, from
+    2^-13 to 2^-21 of the largest, each of which is rounded by half a step of 16 bits."""
+    total = cached + new
+    g = torch.Generator().manual_seed(3)
+    q, k = torch.zeros((new, hq, D)), torch.zeros((total, hkv, D))
+    q[:, :, 0] = 1.0
+    k[:, :, 0] = torch.randint(0, 3, (total, hkv), generator=g) / 4.0
+    k[0, :, 0] = gap
+    v = torch.rand((total, hkv, D), generator=g) + 0.5
+    v[0] = 0
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    _check(_run(pkv, q, k, v, cached), q, k, v, cached, dtype)
+    slopes = torch.full((hq,), 2.0 ** -12, device="cuda")
+    _check(_run(pkv, q, k, v, cached, slopes=slopes), q, k, v, cached, dtype, slopes=slopes)
