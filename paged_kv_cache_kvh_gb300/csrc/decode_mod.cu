@@ -20,8 +20,8 @@
 // bytes, whatever the lengths. Workers of one CTA take the same range of neighbouring heads: their rows lie side by
 // side. Every CTA derives the ranges from context_lens; nothing is kept from one call for the next. A worker's 16-token
 // units of K and of V come by TMA (two 128-byte halves of each row, 128-byte swizzle) into a ring of kStages of its
-// own, and it waits on its own barriers. The running maximum only moves when a score passes it by 2^8, so a step
-// needs one vote and no shuffles.
+// own, and it waits on its own barriers. The reference (the running maximum; of fp16 rows 2^7 below it, see kLift) only
+// moves when a score passes it by 2^8, so a step needs one vote and no shuffles.
 // A sequence that ends inside the range in which it began is written out at once. For the others the workers leave
 // (max, sum, o) in the workspace and a second kernel joins them in order; with weights a third one turns the scores,
 // which the first left in the workspace, into shares. Equal calls give equal bits.
@@ -81,8 +81,9 @@ constexpr int kPieces = 2 * kWarps;
 constexpr size_t kSmemBytes = kOffPieces + kPieces * sizeof(Piece) + 1024;  // + alignment slack
 constexpr int kMergeWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
-// A row's largest share before it is divided by their sum, log2: fp16 shares go down to 2^-24 in steps of as much, two parts
-// together too, so this much more of the small ones is kept (and 2^7 with 2^8 of headroom stays below fp16's largest number).
+// A row's largest share before it is divided by their sum, log2: fp16 shares go down to 2^-24 in steps of as much, two
+// parts together too, so this much more of the small ones is kept (and 2^7 with 2^8 of headroom stays below fp16's largest
+// number).
 template <Elem E>
 constexpr float kLift = E == Elem::kF16 ? 7.f : 0.f;
 constexpr float kNoCap = 1e30f;  // from here on a cap changes no score that fp32 tells from its neighbours below 1e26

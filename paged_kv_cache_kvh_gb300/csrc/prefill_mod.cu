@@ -32,10 +32,11 @@
 // through 1 - 2 / (1 + e^2x). A score is off by at most 7e-6 of itself for bf16 (p by 2^-12 at a score of 32, where its
 // rounding to 16 bits loses 2^-9) and 6e-7 for fp16 (2^-15; 2^-12).
 //
-// The maximum: rows go by a reference that is moved when a score passes it by 2^8 and subtracted where the scores are
-// scaled, so a tile needs one pass for the largest value and nothing else. Scores of bf16 rows capped at 52 or less
-// need none at all: 2^z lies within 2^-75 .. 2^75, sums of it times v within fp32 (|v| up to 2^52; beyond, the row is
-// computed again, see below), and bf16 keeps the same relative precision there as near 1.
+// The maximum: rows go by a reference (of fp16 rows 2^7 below the largest score, see kLift) that is moved when a score
+// passes it by 2^8 and subtracted where the scores are scaled, so a tile needs one pass for the largest value and nothing
+// else. Scores of bf16 rows capped at 52 or less need none at all: 2^z lies within 2^-75 .. 2^75, sums of it times v within
+// fp32 (|v| up to 2^52; beyond, the row is computed again, see below), and bf16 keeps the same relative precision there as
+// near 1.
 //
 // Values of V at keys that a row does not see are multiplied by p = 0; where they are not finite the sum is spoilt
 // (0 * NaN). The rows of V behind the sequence's end, which may hold anything, are zeroed in shared memory. Elsewhere
